@@ -25,7 +25,8 @@ STATUS_NAMES = {0: "EP_OK", 1: "EP_ERR_INVALID_ARG", 2: "EP_ERR_STATE", 3: "EP_E
 # Access sites of the checked build (enum CheckSite in csrc/ep_internal.h).
 CHECK_SITES = ("src_hidden", "src_ids", "src_scale", "src_weights", "recv_hidden", "recv_ids",
                "recv_scale", "recv_weights", "route_write", "eplb_src", "eplb_dst", "route_read",
-               "combine_in", "combine_out", "noalloc_ids", "noalloc_route", "dev_counts", "live_counts")
+               "combine_in", "combine_out", "noalloc_ids", "noalloc_route", "dev_counts", "live_counts",
+               "moe_ids", "moe_weights", "moe_out")
 
 EP_DTYPE_BF16 = 0
 EP_DTYPE_FP8_E4M3 = 1
@@ -45,6 +46,13 @@ EXPORTS = ("ep_is_supported", "ep_workspace_size", "ep_create", "ep_create_with_
            "ep_rank_mask", "ep_last_error", "ep_combine_noalloc", "ep_workspace_size_ex",
            "ep_create_ex", "ep_dispatch_ex", "ep_binary_version", "ep_partition_describe",
            "ep_partition_check", "ep_partition_connect", "ep_partition_info_of")
+# Every symbol include/ep_moe.h declares.
+MOE_EXPORTS = ("ep_router_create", "ep_router_workspace_size", "ep_router_run", "ep_router_destroy",
+               "ep_experts_workspace_size", "ep_experts_create", "ep_experts_run", "ep_experts_destroy")
+EP_MOE_MAX_TOKENS = 64
+EP_MOE_MAX_EXPERTS = 512
+EP_SCORE_SOFTMAX = 0
+EP_SCORE_SIGMOID = 1
 EP_NOALLOC_MAX_SLOTS = 65536
 
 
@@ -84,6 +92,23 @@ class EpDispatchArgsC(ctypes.Structure):
                 ("num_tokens", ctypes.c_void_p), ("runtime_max_tokens_per_rank", ctypes.c_int),
                 ("active_rank_mask", ctypes.c_uint64), ("eplb_local_stats", ctypes.c_void_p),
                 ("eplb_stats_bytes", ctypes.c_int), ("num_tokens_device", ctypes.c_void_p)]
+
+
+class EpRouterConfigC(ctypes.Structure):
+    _fields_ = [("num_experts", ctypes.c_int), ("top_k", ctypes.c_int), ("hidden", ctypes.c_int),
+                ("dtype", ctypes.c_int), ("scoring", ctypes.c_int), ("num_groups", ctypes.c_int),
+                ("top_groups", ctypes.c_int), ("renormalize", ctypes.c_int), ("scale", ctypes.c_float),
+                ("weight", ctypes.c_void_p), ("bias", ctypes.c_void_p)]
+
+
+class EpWeightC(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("group", ctypes.c_int)]
+
+
+class EpExpertsConfigC(ctypes.Structure):
+    _fields_ = [("num_experts", ctypes.c_int), ("first_expert", ctypes.c_int), ("top_k", ctypes.c_int),
+                ("hidden", ctypes.c_int), ("intermediate", ctypes.c_int), ("max_tokens", ctypes.c_int),
+                ("gate_up", EpWeightC), ("down", EpWeightC)]
 
 
 class EpError(RuntimeError):
@@ -162,6 +187,17 @@ def load(build_if_missing: bool = True) -> ctypes.CDLL:
         L.ep_partition_connect.restype = i32
         L.ep_last_error.argtypes = []
         L.ep_last_error.restype = ctypes.c_char_p
+        ll = ctypes.c_longlong
+        L.ep_router_create.argtypes = [ctypes.POINTER(EpRouterConfigC), PP]
+        L.ep_router_workspace_size.argtypes = [P, i32, ctypes.POINTER(sz)]
+        L.ep_router_run.argtypes = [P, P, ll, i32, P, P, P, sz, P]
+        L.ep_router_destroy.argtypes = [P]
+        L.ep_experts_workspace_size.argtypes = [ctypes.POINTER(EpExpertsConfigC), ctypes.POINTER(sz)]
+        L.ep_experts_create.argtypes = [ctypes.POINTER(EpExpertsConfigC), P, sz, PP]
+        L.ep_experts_run.argtypes = [P, P, ll, P, P, i32, P, ll, P]
+        L.ep_experts_destroy.argtypes = [P]
+        for name in MOE_EXPORTS:
+            getattr(L, name).restype = i32
         if checked():
             L.ep_checked_trim_extent.argtypes = [i32, ctypes.c_longlong]
             L.ep_checked_trim_extent.restype = i32

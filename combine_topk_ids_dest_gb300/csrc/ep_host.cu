@@ -39,6 +39,7 @@
 #include <nvtx3/nvToolsExt.h>
 
 #include "ep_internal.h"
+#include "moe_internal.h"
 
 struct ep_handle {
     int ep, num_experts, top_k, hidden, capacity, experts_per_rank;
@@ -390,7 +391,8 @@ const char *epk::check_site_name(int site)
         "dispatch: receive scale row", "dispatch: receive weight row", "dispatch: routing state",
         "dispatch: eplb_local_stats", "dispatch: gathered eplb stats", "combine: routing state",
         "combine: expert output row", "combine: output row", "ep_combine_noalloc: id row",
-        "ep_combine_noalloc: routing scratch", "dispatch: device token counts", "live token counts"};
+        "ep_combine_noalloc: routing scratch", "dispatch: device token counts", "live token counts",
+        "moe: ids", "moe: routing weights", "moe: output row"};
     return (site >= 0 && site < kNumSites) ? names[site] : "unknown site";
 }
 
@@ -948,10 +950,15 @@ ep_status ep_binary_version(int *version)
     if (!version)
         return fail(EP_ERR_INVALID_ARG, "version is NULL");
     *version = 0;
-    int v[16], n = 0;
+    int v[24], n = 0;
     cudaError_t ce = epk::kernel_binary_versions(v, 15, &n);
     if (ce == cudaSuccess && n < 16)
         ce = epk::noalloc_binary_version(&v[n++]);
+    if (ce == cudaSuccess) {
+        int more = 0;
+        ce = moe::kernel_binary_versions(v + n, 24 - n, &more);
+        n += more;
+    }
     if (ce != cudaSuccess) {
         cudaGetLastError();
         return fail(EP_ERR_CUDA, "cudaFuncGetAttributes: %s", cudaGetErrorString(ce));

@@ -29,6 +29,7 @@ enum CheckSite {
     kSiteRouteWrite, kSiteEplbSrc, kSiteEplbDst,
     kSiteRouteRead, kSiteCombineIn, kSiteCombineOut,
     kSiteNoallocIds, kSiteNoallocRoute, kSiteDevCounts, kSiteLiveCounts,
+    kSiteMoeIds, kSiteMoeWeights, kSiteMoeOut,
     kNumSites
 };
 

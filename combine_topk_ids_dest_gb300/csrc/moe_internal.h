@@ -1,0 +1,88 @@
+// moe_internal.h -- argument blocks and launchers shared by the C ABI of the
+// MoE operators (moe_host.cu) and their kernels. Not installed.
+#pragma once
+
+#include <cstddef>
+#include <cstdint>
+
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include "ep_internal.h"
+#include "ep_moe.h"
+
+namespace moe {
+
+constexpr int kMaxTokens = EP_MOE_MAX_TOKENS;    // rows of one experts or linear call
+constexpr int kMaxLocal = EP_MOE_MAX_EXPERTS;    // experts of one handle
+
+// A contiguous share of `total` units for block b of G.
+static __host__ __device__ inline int share_begin(int total, int b, int G)
+{
+    return static_cast<int>(static_cast<long long>(total) * b / G);
+}
+
+// The block whose share holds unit u: the largest b with share_begin(b) <= u.
+static __host__ __device__ inline int share_owner(int total, int u, int G)
+{
+    return static_cast<int>(((static_cast<long long>(u) + 1) * G - 1) / total);
+}
+
+// ---- router (moe_router.cu) -------------------------------------------------------
+
+struct RouterArgs {
+    const void *x, *weight;
+    const float *bias;
+    long long x_stride;
+    int32_t *ids;
+    float *weights;
+    float *logits;  // workspace [T, E]
+    int T, H, E, K, bf16, scoring, groups, top_groups, renormalize;
+    float scale;
+    epk::CheckCtx chk;
+};
+
+size_t router_workspace(const RouterArgs &a);
+cudaError_t launch_router(const RouterArgs &a, cudaStream_t stream);
+cudaError_t router_binary_version(int *v);
+
+// ---- experts with dense bf16 weights (moe_experts.cu) ---------------------------
+
+constexpr int kTileRows = 128;              // weight rows of a tile: the MMA's M
+constexpr int kChunk = 64;                  // inputs of a bf16 chunk: one 128-byte swizzled row
+constexpr int kStageA = kTileRows * kChunk * 2;
+
+struct ExpertsArgs {
+    CUtensorMap mx;   // x [T, H], one-row boxes of 64 columns
+    CUtensorMap mw1;  // w_gate_up [2 E, I, H], boxes 64 x 128
+    CUtensorMap mw2;  // w_down [E, H, I], boxes 64 x 128
+    CUtensorMap mh;   // h [2 P, I] (high parts, then low parts), boxes 64 x 8
+    const int32_t *ids;
+    const float *weights;
+    __nv_bfloat16 *out;
+    long long out_stride;
+    __nv_bfloat16 *h;
+    float *part;
+    int *done;     // finished tiles of the first product
+    int *leaving;  // blocks that are done with the counters
+    int *tiles;    // per tile: parts that have been written
+    unsigned int *err;  // host memory: set when a wait ran out
+    int T, K, P, H, I, E, first;
+    int mt1, kc1, mt2, kc2;  // row tiles and chunks of the two products
+    int h_stride;
+    int stages, bytes_b, part_floats;
+    epk::CheckCtx chk;
+};
+
+cudaError_t launch_experts(const ExpertsArgs &a, int grid, size_t smem, cudaStream_t stream);
+cudaError_t experts_binary_version(int *v);
+// Dynamic shared memory of a launch for T tokens; sets stages, bytes_b and part_floats.
+size_t experts_smem(ExpertsArgs *a);
+// Floats of one block's part (two per block) for up to T tokens.
+size_t experts_part_floats(int T);
+
+// Binary versions of this library's MoE kernels, as epk::kernel_binary_versions.
+cudaError_t kernel_binary_versions(int *out, int max, int *n);
+
+}  // namespace moe

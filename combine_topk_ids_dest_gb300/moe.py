@@ -1,0 +1,211 @@
+"""PyTorch binding of the MoE operators (include/ep_moe.h): argument marshalling only.
+
+:class:`EpRouter` makes the ``topk_ids`` and ``topk_weights`` that
+``EpComm.dispatch`` takes; :class:`EpExperts` computes the experts for a few
+tokens, on all experts or on the rows one rank received; :class:`EpMoeLayer`
+is both, a whole layer on one GPU. All work runs in the CUDA library on
+torch's current stream of the tensors' device; torch supplies device memory
+and streams only. Weights are kept by reference, not copied.
+
+Calls on one object must be ordered on the device (one stream, or streams
+with events between them): it holds one call's intermediate results. Create
+objects outside CUDA graph captures; calls can be captured.
+"""
+from __future__ import annotations
+
+import ctypes
+from typing import Optional, Tuple
+
+import torch
+
+from . import _lib
+from ._lib import EpError, check
+
+_DTYPES = {torch.bfloat16: _lib.EP_DTYPE_BF16, torch.float16: _lib.EP_DTYPE_FP16}
+_SCORING = {"softmax": _lib.EP_SCORE_SOFTMAX, "sigmoid": _lib.EP_SCORE_SIGMOID}
+
+
+def _device_of(t: torch.Tensor, name: str) -> torch.device:
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    return t.device
+
+
+def _weight(name, t, dtype, shape, device):
+    """A weight operand: contiguous `shape` of dtype on the device."""
+    if not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.device != device \
+            or tuple(t.shape) != tuple(shape) or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor {tuple(shape)} on {device}")
+    return t
+
+
+class _Handle:
+    """A handle of the C ABI and the device it lives on."""
+
+    _destroy = ""
+
+    def _open(self, device: torch.device):
+        self._L = _lib.load()
+        self.device = device
+        self._index = device.index
+        self._h = None
+
+    def destroy(self) -> None:
+        """Free the handle; repeated calls do nothing."""
+        h, self._h = getattr(self, "_h", None), None
+        if h is not None:
+            check(getattr(self._L, self._destroy)(h))
+
+    def __del__(self):
+        try:
+            self.destroy()
+        except Exception:  # interpreter shutdown
+            pass
+
+    def _live(self):
+        if self._h is None:
+            raise EpError(_lib.EP_ERR_STATE, f"the {type(self).__name__} was destroyed")
+        return self._h
+
+    def _rows(self, x, cols, dtype, name="x"):
+        """Row count and stride of an operand [rows, cols] whose rows are contiguous."""
+        if x.dtype is not dtype or x.get_device() != self._index:
+            raise ValueError(f"{name} is {x.dtype} on {x.device}, expected {dtype} on {self.device}")
+        if x.dim() != 2 or x.shape[1] != cols or (x.stride(1) != 1 and cols != 1):
+            raise ValueError(f"{name} must be a [tokens, {cols}] tensor with contiguous rows, got {tuple(x.shape)}")
+        n = x.shape[0]
+        return n, (x.stride(0) if n > 1 else cols)
+
+    def _call(self, fn, *args):
+        """fn(handle, *args, stream) on the handle's device."""
+        if torch.cuda.current_device() != self._index:
+            with torch.cuda.device(self._index):
+                return check(fn(self._live(), *args, torch.cuda.current_stream().cuda_stream))
+        status = fn(self._live(), *args, torch._C._cuda_getCurrentRawStream(self._index))
+        if status:
+            check(status)
+
+
+class EpRouter(_Handle):
+    """A token's top-k experts and their weights from its hidden row.
+
+    ``weight`` [num_experts, hidden] (bf16 or fp16) gives logits
+    ``x @ weight.T`` in fp32. ``scoring`` "softmax" or "sigmoid" turns them
+    into scores; ``bias`` (fp32 [num_experts], optional) is added for the
+    choice only, -inf masks an expert. With ``num_groups`` > 1 the choice is
+    limited to the ``top_groups`` groups of experts whose two best experts add
+    up highest. The chosen scores, divided by their sum if ``renormalize``,
+    times ``scale``, are the weights. Choices come in descending order, ties
+    go to the lowest index; slots without an expert hold id -1, weight 0.
+    """
+
+    _destroy = "ep_router_destroy"
+
+    def __init__(self, weight: torch.Tensor, top_k: int, scoring: str = "softmax",
+                 bias: Optional[torch.Tensor] = None, num_groups: int = 1, top_groups: int = 1,
+                 renormalize: bool = True, scale: float = 1.0):
+        device = _device_of(weight, "weight")
+        if weight.dtype not in _DTYPES or weight.dim() != 2:
+            raise ValueError("weight must be a bfloat16 or float16 tensor [num_experts, hidden]")
+        if scoring not in _SCORING:
+            raise ValueError(f"scoring {scoring!r}: use one of {sorted(_SCORING)}")
+        self.num_experts, self.hidden = (int(n) for n in weight.shape)
+        self.top_k, self.dtype = int(top_k), weight.dtype
+        self._weight = _weight("weight", weight, weight.dtype, weight.shape, device)
+        self._bias = None if bias is None else _weight("bias", bias, torch.float32, (self.num_experts,), device)
+        self._open(device)
+        cfg = _lib.EpRouterConfigC(self.num_experts, self.top_k, self.hidden, _DTYPES[weight.dtype],
+                                   _SCORING[scoring], int(num_groups), int(top_groups), int(bool(renormalize)),
+                                   float(scale), weight.data_ptr(), 0 if bias is None else bias.data_ptr())
+        h = ctypes.c_void_p()
+        with torch.cuda.device(device):
+            check(self._L.ep_router_create(ctypes.byref(cfg), ctypes.byref(h)))
+        self._h = h.value
+        self._need = {}  # workspace bytes by row count
+
+    def _workspace(self, n: int) -> Tuple[Optional[torch.Tensor], int]:
+        need = self._need.get(n)
+        if need is None:
+            size = ctypes.c_size_t(0)
+            check(self._L.ep_router_workspace_size(self._live(), n, ctypes.byref(size)))
+            need = self._need[n] = size.value
+        return (torch.empty(need, dtype=torch.uint8, device=self.device) if need else None), need
+
+    def __call__(self, x: torch.Tensor) -> Tuple[torch.Tensor, torch.Tensor]:
+        """``x`` [tokens, hidden] -> ids int32 and weights fp32, both [tokens, top_k]."""
+        n, stride = self._rows(x, self.hidden, self.dtype)
+        ids = torch.empty((n, self.top_k), dtype=torch.int32, device=x.device)
+        weights = torch.empty((n, self.top_k), dtype=torch.float32, device=x.device)
+        ws, need = self._workspace(n)
+        self._call(self._L.ep_router_run, x.data_ptr(), stride, n, ids.data_ptr(), weights.data_ptr(),
+                   ws.data_ptr() if need else 0, need)
+        return ids, weights
+
+
+class EpExperts(_Handle):
+    """The experts of an MoE layer for up to ``max_tokens`` (at most 64) tokens.
+
+    ``gate_up`` [experts, 2*intermediate, hidden] (gate rows, then up rows) and
+    ``down`` [experts, hidden, intermediate] are bf16 tensors. The experts are
+    the global ids ``first_expert ..``; ids outside them are skipped, so one
+    rank's experts run on the rows ``EpComm.dispatch`` delivered and write the
+    rows ``EpComm.combine`` adds up.
+    """
+
+    _destroy = "ep_experts_destroy"
+
+    def __init__(self, gate_up, down, top_k: int, max_tokens: int = 64, first_expert: int = 0):
+        device = _device_of(gate_up, "gate_up")
+        if gate_up.dim() != 3 or gate_up.shape[1] % 2:
+            raise ValueError("gate_up must be [experts, 2*intermediate, hidden]")
+        E, I2, H = (int(n) for n in gate_up.shape)
+        self.num_experts, self.intermediate, self.hidden = E, I2 // 2, H
+        self.top_k, self.max_tokens, self.first_expert = int(top_k), int(max_tokens), int(first_expert)
+        self.dtype = torch.bfloat16
+        self._w = (_weight("gate_up", gate_up, torch.bfloat16, (E, I2, H), device),
+                   _weight("down", down, torch.bfloat16, (E, H, I2 // 2), device))
+        self._open(device)
+        cfg = _lib.EpExpertsConfigC(E, self.first_expert, self.top_k, H, I2 // 2, self.max_tokens,
+                                    _lib.EpWeightC(gate_up.data_ptr(), 0), _lib.EpWeightC(down.data_ptr(), 0))
+        need = ctypes.c_size_t(0)
+        check(self._L.ep_experts_workspace_size(ctypes.byref(cfg), ctypes.byref(need)))
+        h = ctypes.c_void_p()
+        with torch.cuda.device(device):
+            self._ws = torch.empty(need.value, dtype=torch.uint8, device=device)
+            torch.cuda.current_stream().synchronize()  # the memory may still be in use on this stream
+            check(self._L.ep_experts_create(ctypes.byref(cfg), self._ws.data_ptr(), need.value, ctypes.byref(h)))
+        self._h = h.value
+
+    def __call__(self, x: torch.Tensor, topk_ids: torch.Tensor, topk_weights: torch.Tensor,
+                 out: Optional[torch.Tensor] = None) -> torch.Tensor:
+        """``x`` bf16 [tokens, hidden], ``topk_ids`` int32 and ``topk_weights`` fp32 [tokens, top_k] ->
+        the weighted sum of each token's experts, bf16 [tokens, hidden] (``out`` if given)."""
+        n, stride = self._rows(x, self.hidden, self.dtype)
+        for name, t, dtype in (("topk_ids", topk_ids, torch.int32), ("topk_weights", topk_weights, torch.float32)):
+            if t.dtype is not dtype or t.get_device() != self._index or tuple(t.shape) != (n, self.top_k) \
+                    or not t.is_contiguous():
+                raise ValueError(f"{name} must be a contiguous {dtype} tensor [{n}, {self.top_k}] on {self.device}")
+        if out is None:
+            out = torch.empty((n, self.hidden), dtype=self.dtype, device=x.device)
+            out_stride = self.hidden
+        else:
+            m, out_stride = self._rows(out, self.hidden, self.dtype, "out")
+            if m != n:
+                raise ValueError(f"out must have {n} rows, got {m}")
+        self._call(self._L.ep_experts_run, x.data_ptr(), stride, topk_ids.data_ptr(), topk_weights.data_ptr(), n,
+                   out.data_ptr(), out_stride)
+        return out
+
+
+class EpMoeLayer:
+    """A whole MoE layer for a few tokens on one GPU: router, then experts."""
+
+    def __init__(self, router: EpRouter, experts: EpExperts):
+        if router.hidden != experts.hidden or router.top_k != experts.top_k or router.dtype is not experts.dtype:
+            raise ValueError("router and experts must have the same hidden size, top_k and dtype")
+        self.router, self.experts = router, experts
+
+    def __call__(self, x: torch.Tensor, out: Optional[torch.Tensor] = None):
+        """``x`` [tokens, hidden] -> (y [tokens, hidden], ids, weights)."""
+        ids, weights = self.router(x)
+        return self.experts(x, ids, weights, out), ids, weights
