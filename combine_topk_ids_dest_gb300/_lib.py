@@ -48,7 +48,9 @@ EXPORTS = ("ep_is_supported", "ep_workspace_size", "ep_create", "ep_create_with_
            "ep_partition_check", "ep_partition_connect", "ep_partition_info_of")
 # Every symbol include/ep_moe.h declares.
 MOE_EXPORTS = ("ep_router_create", "ep_router_workspace_size", "ep_router_run", "ep_router_destroy",
-               "ep_experts_workspace_size", "ep_experts_create", "ep_experts_run", "ep_experts_destroy")
+               "ep_experts_workspace_size", "ep_experts_create", "ep_experts_run", "ep_experts_destroy",
+               "ep_weight_packed_size", "ep_weight_pack", "ep_linear_workspace_size", "ep_linear_create",
+               "ep_linear_run", "ep_linear_destroy")
 EP_MOE_MAX_TOKENS = 64
 EP_MOE_MAX_EXPERTS = 512
 EP_SCORE_SOFTMAX = 0
@@ -102,7 +104,19 @@ class EpRouterConfigC(ctypes.Structure):
 
 
 class EpWeightC(ctypes.Structure):
-    _fields_ = [("data", ctypes.c_void_p), ("group", ctypes.c_int)]
+    _fields_ = [("data", ctypes.c_void_p), ("group", ctypes.c_int), ("has_zeros", ctypes.c_int),
+                ("scale_dtype", ctypes.c_int)]
+
+
+class EpIntWeightC(ctypes.Structure):
+    _fields_ = [("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p), ("zeros", ctypes.c_void_p),
+                ("scale_dtype", ctypes.c_int), ("mats", ctypes.c_int), ("rows", ctypes.c_int),
+                ("cols", ctypes.c_int), ("group", ctypes.c_int)]
+
+
+class EpLinearConfigC(ctypes.Structure):
+    _fields_ = [("inputs", ctypes.c_int), ("outputs", ctypes.c_int), ("max_tokens", ctypes.c_int),
+                ("weight", EpWeightC)]
 
 
 class EpExpertsConfigC(ctypes.Structure):
@@ -196,6 +210,12 @@ def load(build_if_missing: bool = True) -> ctypes.CDLL:
         L.ep_experts_create.argtypes = [ctypes.POINTER(EpExpertsConfigC), P, sz, PP]
         L.ep_experts_run.argtypes = [P, P, ll, P, P, i32, P, ll, P]
         L.ep_experts_destroy.argtypes = [P]
+        L.ep_weight_packed_size.argtypes = [ctypes.POINTER(EpIntWeightC), ctypes.POINTER(sz)]
+        L.ep_weight_pack.argtypes = [ctypes.POINTER(EpIntWeightC), P, sz, P]
+        L.ep_linear_workspace_size.argtypes = [ctypes.POINTER(EpLinearConfigC), ctypes.POINTER(sz)]
+        L.ep_linear_create.argtypes = [ctypes.POINTER(EpLinearConfigC), P, sz, PP]
+        L.ep_linear_run.argtypes = [P, i32, P, ll, i32, P, ll, P]
+        L.ep_linear_destroy.argtypes = [P]
         for name in MOE_EXPORTS:
             getattr(L, name).restype = i32
         if checked():

@@ -524,7 +524,7 @@ size_t experts_smem(ExpertsArgs *a)
                    static_cast<size_t>(a->E) * 2 + static_cast<size_t>(a->E + 1) * 2 + static_cast<size_t>(a->P);
     a->bytes_b = T8 <= 8 ? 24 * 1024 : 48 * 1024;  // at least 12 and 3 stages of the largest token tile
     a->part_floats = static_cast<int>(experts_part_floats(a->T));
-    const size_t room = 227 * 1024 - sizeof(Shared) - 1024 - lists - a->bytes_b - 64;
+    const size_t room = kSmemMax - sizeof(Shared) - 1024 - lists - a->bytes_b - 64;
     a->stages = static_cast<int>(room / kStageA);
     if (a->stages > kMaxStagesA)
         a->stages = kMaxStagesA;
@@ -534,7 +534,8 @@ size_t experts_smem(ExpertsArgs *a)
 cudaError_t launch_experts(const ExpertsArgs &a, int grid, size_t smem, cudaStream_t stream)
 {
     static const cudaError_t attr =
-        cudaFuncSetAttribute(experts_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 226 * 1024);
+        cudaFuncSetAttribute(experts_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             kSmemMax - 64 - static_cast<int>(sizeof(Shared)));
     if (attr != cudaSuccess)
         return attr;
     cudaLaunchConfig_t cfg = {};

@@ -284,22 +284,296 @@ ep_status ep_router_destroy(ep_router *r)
 
 }  // extern "C"
 
+// ---- 4-bit weights ------------------------------------------------------------------------
+
+namespace {
+
+bool is_group(int g) { return g == 32 || g == 64 || g == 128; }
+
+int div_up(int a, int b) { return (a + b - 1) / b; }
+
+ep_status check_int_weight(const ep_int_weight *w)
+{
+    if (!w)
+        MOE_FAIL("weight is NULL");
+    if (!is_group(w->group))
+        MOE_FAIL("group=%d: use 32, 64 or 128", w->group);
+    if (w->mats < 1 || w->rows < 1 || w->cols < 1 || w->cols % w->group)
+        MOE_FAIL("mats=%d, rows=%d, cols=%d: positive, cols a multiple of group=%d", w->mats, w->rows, w->cols, w->group);
+    if (w->cols > EP_MOE_MAX_DIM || w->rows > 16 * EP_MOE_MAX_DIM || w->mats > 2 * EP_MOE_MAX_EXPERTS)
+        MOE_FAIL("mats=%d, rows=%d, cols=%d are limited to %d, %d, %d", w->mats, w->rows, w->cols,
+                 2 * EP_MOE_MAX_EXPERTS, 16 * EP_MOE_MAX_DIM, EP_MOE_MAX_DIM);
+    if (w->scale_dtype != EP_DTYPE_BF16 && w->scale_dtype != EP_DTYPE_FP16)
+        MOE_FAIL("scale_dtype %d: use bf16 or fp16", static_cast<int>(w->scale_dtype));
+    return EP_OK;
+}
+
+size_t packed_size(const ep_int_weight &w)
+{
+    return size_t(w.mats) * div_up(w.rows, 128) * div_up(w.cols, 128) *
+           moe::int4_tile_bytes(w.group, w.zeros != nullptr);
+}
+
+// The parts that experts and linear handles share: the device, the workspace and the host flag.
+struct Base {
+    int device = 0, sms = 0;
+    uint8_t *ws = nullptr;
+    bool owns_ws = false;
+    Flags flags;
+
+    ep_status open(void *workspace, size_t bytes, size_t need, size_t off_words, size_t words)
+    {
+        if (workspace && (!aligned(workspace, 256) || bytes < need))
+            MOE_FAIL("workspace has %zu bytes, needs %zu, 256-byte aligned", bytes, need);
+        ep_status st = current_device(&device, &sms);
+        if (st != EP_OK)
+            return st;
+        sms = sms < kMaxBlocks ? sms : kMaxBlocks;
+        st = flags.make();
+        if (st != EP_OK)
+            return st;
+        ws = static_cast<uint8_t *>(workspace);
+        if (!ws) {
+            const cudaError_t ce = cudaMalloc(reinterpret_cast<void **>(&ws), need);
+            if (ce != cudaSuccess) {
+                ws = nullptr;
+                return cuda_error(ce, "cudaMalloc");
+            }
+            owns_ws = true;
+        }
+        cudaError_t ce = cudaMemset(ws + off_words, 0, words * 4);
+        if (ce == cudaSuccess)
+            ce = cudaStreamSynchronize(nullptr);
+        return ce == cudaSuccess ? EP_OK : cuda_error(ce, "clearing the counters");
+    }
+    void close()
+    {
+        if (owns_ws && ws)
+            cudaFree(ws);  // waits for work that uses it
+        ws = nullptr;
+        flags.free();
+    }
+    static constexpr int kMaxBlocks = 256;
+};
+
+constexpr size_t kWords = 64;  // done at 0, leaving at 32, then the tiles' counters
+
+template <class Args> void set_words(Args &a, uint8_t *words)
+{
+    int *const w = reinterpret_cast<int *>(words);
+    a.done = w;
+    a.leaving = w + 32;
+    a.tiles = w + kWords;
+}
+
+ep_status check_rows(const char *name, const void *p, long long stride, int cols, int align, int step)
+{
+    if (!p || !aligned(p, align))
+        MOE_FAIL("%s is NULL or not %d-byte aligned", name, align);
+    if (stride < cols || stride % step)
+        MOE_FAIL("%s: stride %lld must be a multiple of %d and at least %d", name, stride, step, cols);
+    return EP_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+ep_status ep_weight_packed_size(const ep_int_weight *w, size_t *bytes)
+{
+    if (!bytes)
+        MOE_FAIL("bytes is NULL");
+    const ep_status st = check_int_weight(w);
+    if (st != EP_OK)
+        return st;
+    *bytes = packed_size(*w);
+    return set_error(EP_OK, "");
+}
+
+ep_status ep_weight_pack(const ep_int_weight *w, void *packed, size_t bytes, void *stream)
+{
+    Range range("ep_weight_pack");
+    ep_status st = check_int_weight(w);
+    if (st != EP_OK)
+        return st;
+    if (!w->codes || !w->scales || !aligned(w->scales, 2))
+        MOE_FAIL("codes or scales is NULL or scales is not 2-byte aligned");
+    if (!packed || !aligned(packed, 128) || bytes < packed_size(*w))
+        MOE_FAIL("packed has %zu bytes, needs %zu, 128-byte aligned", bytes, packed_size(*w));
+    int dev = 0;
+    st = current_device(&dev, nullptr);
+    if (st != EP_OK)
+        return st;
+    moe::PackArgs a = {};
+    a.codes = w->codes;
+    a.scales = static_cast<const uint16_t *>(w->scales);
+    a.zeros = w->zeros;
+    a.dst = static_cast<uint8_t *>(packed);
+    a.mats = w->mats;
+    a.rows = w->rows;
+    a.cols = w->cols;
+    a.group = w->group;
+    a.mt = div_up(w->rows, 128);
+    a.kc = div_up(w->cols, 128);
+    a.tile_bytes = moe::int4_tile_bytes(w->group, w->zeros != nullptr);
+    const cudaStream_t s = static_cast<cudaStream_t>(stream);
+    const cudaError_t ce = moe::launch_pack(a, s);
+    return ce == cudaSuccess ? set_error(EP_OK, "") : cuda_error(ce, "ep_weight_pack");
+}
+
+}  // extern "C"
+
+// ---- linear -------------------------------------------------------------------------------
+
+struct ep_linear {
+    ep_linear_config cfg;
+    Base base;
+};
+
+namespace {
+
+struct LinearLayout {
+    size_t off_words, words, total;
+};
+
+ep_status plan_linear(const ep_linear_config *c, LinearLayout *l)
+{
+    if (!c)
+        MOE_FAIL("config is NULL");
+    if (!is_group(c->weight.group))
+        MOE_FAIL("weight: group=%d: use 32, 64 or 128", c->weight.group);
+    if (c->inputs < 1 || c->inputs > EP_MOE_MAX_DIM || c->inputs % c->weight.group)
+        MOE_FAIL("inputs=%d must be a multiple of group=%d in [1, %d]", c->inputs, c->weight.group, EP_MOE_MAX_DIM);
+    if (c->outputs < 1 || c->outputs > 16 * EP_MOE_MAX_DIM)
+        MOE_FAIL("outputs=%d outside [1, %d]", c->outputs, 16 * EP_MOE_MAX_DIM);
+    if (c->max_tokens < 1 || c->max_tokens > EP_MOE_MAX_TOKENS)
+        MOE_FAIL("max_tokens=%d outside [1, %d]", c->max_tokens, EP_MOE_MAX_TOKENS);
+    if (c->weight.scale_dtype != EP_DTYPE_BF16 && c->weight.scale_dtype != EP_DTYPE_FP16)
+        MOE_FAIL("weight: scale_dtype %d: use bf16 or fp16", static_cast<int>(c->weight.scale_dtype));
+    if (!c->weight.data || !aligned(c->weight.data, 128))
+        MOE_FAIL("weight: data is NULL or not 128-byte aligned");
+    size_t off = align256(moe::int4_part_floats(c->max_tokens, true) * 4 * 2 * Base::kMaxBlocks);
+    l->off_words = off;
+    l->words = kWords + div_up(c->outputs, 128);
+    l->total = off + align256(l->words * 4);
+    return EP_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+ep_status ep_linear_workspace_size(const ep_linear_config *cfg, size_t *bytes)
+{
+    if (!bytes)
+        MOE_FAIL("bytes is NULL");
+    LinearLayout l{};
+    const ep_status st = plan_linear(cfg, &l);
+    if (st != EP_OK)
+        return st;
+    *bytes = l.total;
+    return set_error(EP_OK, "");
+}
+
+ep_status ep_linear_create(const ep_linear_config *cfg, void *workspace, size_t bytes, ep_linear **out)
+{
+    if (!out)
+        MOE_FAIL("out is NULL");
+    *out = nullptr;
+    LinearLayout l{};
+    ep_status st = plan_linear(cfg, &l);
+    if (st != EP_OK)
+        return st;
+    ep_linear *h = new (std::nothrow) ep_linear();
+    if (!h)
+        return set_error(EP_ERR_OOM, "host allocation of the handle failed");
+    h->cfg = *cfg;
+    st = h->base.open(workspace, bytes, l.total, l.off_words, l.words);
+    if (st != EP_OK) {
+        h->base.close();
+        delete h;
+        return st;
+    }
+    *out = h;
+    return set_error(EP_OK, "");
+}
+
+ep_status ep_linear_run(ep_linear *h, ep_dtype dtype, const void *x, long long x_stride, int num_tokens, void *y,
+                        long long y_stride, void *stream)
+{
+    Range range("ep_linear_run");
+    if (!h)
+        MOE_FAIL("handle is NULL");
+    const ep_linear_config &c = h->cfg;
+    if (num_tokens < 0 || num_tokens > c.max_tokens)
+        MOE_FAIL("num_tokens=%d outside [0, max_tokens=%d]", num_tokens, c.max_tokens);
+    ep_status st = same_device(h->base.device);
+    if (st != EP_OK)
+        return st;
+    if (num_tokens == 0)
+        return set_error(EP_OK, "");
+    if (dtype != EP_DTYPE_BF16 && dtype != EP_DTYPE_FP16)
+        MOE_FAIL("dtype %d: use bf16 or fp16", static_cast<int>(dtype));
+    st = check_rows("x", x, x_stride, c.inputs, 16, 8);
+    if (st == EP_OK)
+        st = check_rows("y", y, y_stride, c.outputs, 2, 1);
+    if (st == EP_OK)
+        st = h->base.flags.take();
+    if (st != EP_OK)
+        return st;
+    LinearLayout l{};
+    plan_linear(&c, &l);
+    moe::Int4Args a = {};
+    a.T = num_tokens;
+    a.E = 1;
+    a.H = c.inputs;
+    a.I = c.outputs;
+    st = encode_map(&a.mx, "x", dtype == EP_DTYPE_FP16, x, a.H, a.T, 0, x_stride, 0, moe::kChunk, 8);
+    if (st != EP_OK)
+        return st;
+    a.w1 = static_cast<const uint8_t *>(c.weight.data);
+    a.out = y;
+    a.out_stride = y_stride;
+    a.part = reinterpret_cast<float *>(h->base.ws);
+    set_words(a, h->base.ws + l.off_words);
+    a.err = h->base.flags.err;
+    a.mt1 = div_up(c.outputs, 128);
+    a.kc1 = div_up(c.inputs, 128);
+    a.group1 = a.group2 = c.weight.group;
+    a.zeros1 = a.zeros2 = c.weight.has_zeros != 0;
+    a.tile1 = a.tile2 = moe::int4_tile_bytes(c.weight.group, a.zeros1);
+    a.scale_fp16 = c.weight.scale_dtype == EP_DTYPE_FP16;
+    const size_t smem = moe::int4_smem(&a, true);
+    unsigned long long *rec = epk::check_record();
+    a.chk = epk::check_ctx(rec);
+    const cudaStream_t s = static_cast<cudaStream_t>(stream);
+    return finish(moe::launch_int4(a, true, dtype == EP_DTYPE_BF16, h->base.sms, smem, s), "ep_linear_run", rec, s);
+}
+
+ep_status ep_linear_destroy(ep_linear *h)
+{
+    if (h) {
+        h->base.close();
+        delete h;
+    }
+    return set_error(EP_OK, "");
+}
+
+}  // extern "C"
+
 // ---- experts ----------------------------------------------------------------------------
 
 struct ep_experts {
     ep_experts_config cfg;
-    int device, sms;
-    uint8_t *ws;
-    bool owns_ws;
-    Flags flags;
-    CUtensorMap mw1, mw2;
+    Base base;
+    CUtensorMap mw1, mw2;  // of bf16 weights
 };
 
 namespace {
 
 struct ExpertsLayout {
     size_t off_h, off_part, off_words, words, total;
-    int h_stride, pairs;
+    int h_stride;
 };
 
 // Workspace for the largest call: h [2][pairs][intermediate] bf16, two fp32
@@ -314,34 +588,71 @@ ep_status plan_experts(const ep_experts_config *c, ExpertsLayout *l)
         MOE_FAIL("first_expert=%d < 0", c->first_expert);
     if (c->top_k < 1 || c->top_k > EP_MAX_TOP_K)
         MOE_FAIL("top_k=%d outside [1, %d]", c->top_k, EP_MAX_TOP_K);
-    const int hi[2] = {c->hidden, c->intermediate};
-    const char *const names[2] = {"hidden", "intermediate"};
-    for (int i = 0; i < 2; ++i)
-        if (hi[i] < 8 || hi[i] > EP_MOE_MAX_DIM || hi[i] % 8)
-            MOE_FAIL("%s=%d must be a multiple of 8 in [8, %d]", names[i], hi[i], EP_MOE_MAX_DIM);
     if (c->max_tokens < 1 || c->max_tokens > EP_MOE_MAX_TOKENS)
         MOE_FAIL("max_tokens=%d outside [1, %d]", c->max_tokens, EP_MOE_MAX_TOKENS);
     const ep_weight *const w[2] = {&c->gate_up, &c->down};
+    const char *const names[2] = {"gate_up", "down"};
+    const int inputs[2] = {c->hidden, c->intermediate};
+    const char *const of[2] = {"hidden", "intermediate"};
+    if ((w[0]->group == 0) != (w[1]->group == 0))
+        MOE_FAIL("gate_up and down must both be bf16 or both packed");
     for (int i = 0; i < 2; ++i) {
-        if (!w[i]->data || !aligned(w[i]->data, 16))
-            MOE_FAIL("%s: data is NULL or not 16-byte aligned", i ? "down" : "gate_up");
-        if (w[i]->group != 0)
-            MOE_FAIL("%s: unknown group %d", i ? "down" : "gate_up", w[i]->group);
+        if (w[i]->group != 0 && !is_group(w[i]->group))
+            MOE_FAIL("%s: group=%d: use 0 (bf16), 32, 64 or 128", names[i], w[i]->group);
+        const int step = w[i]->group ? w[i]->group : 8;
+        if (inputs[i] < step || inputs[i] > EP_MOE_MAX_DIM || inputs[i] % step)
+            MOE_FAIL("%s=%d must be a multiple of %d in [%d, %d]", of[i], inputs[i], step, step, EP_MOE_MAX_DIM);
+        if (!w[i]->data || !aligned(w[i]->data, w[i]->group ? 128 : 16))
+            MOE_FAIL("%s: data is NULL or not %d-byte aligned", names[i], w[i]->group ? 128 : 16);
+        if (w[i]->group && (w[i]->scale_dtype != EP_DTYPE_BF16 && w[i]->scale_dtype != EP_DTYPE_FP16))
+            MOE_FAIL("%s: scale_dtype %d: use bf16 or fp16", names[i], static_cast<int>(w[i]->scale_dtype));
     }
-    l->pairs = c->max_tokens * c->top_k;
-    l->h_stride = (c->intermediate + 63) / 64 * 64;
+    if (w[0]->group && w[0]->scale_dtype != w[1]->scale_dtype)
+        MOE_FAIL("gate_up and down must have the same scale_dtype");
+    const int pairs = c->max_tokens * c->top_k;
+    const size_t part = w[0]->group ? moe::int4_part_floats(c->max_tokens, false) : moe::experts_part_floats(c->max_tokens);
+    l->h_stride = div_up(c->intermediate, 64) * 64;
     size_t off = 0;
     l->off_h = off;
-    off += align256(size_t(2) * l->pairs * l->h_stride * 2);
+    off += align256(size_t(2) * pairs * l->h_stride * 2);
     l->off_part = off;
-    off += align256(moe::experts_part_floats(c->max_tokens) * 4 * 2 * 256);  // up to 256 blocks
+    off += align256(part * 4 * 2 * Base::kMaxBlocks);
     l->off_words = off;
-    const size_t mt1 = (c->intermediate + moe::kTileRows - 1) / moe::kTileRows;
-    const size_t mt2 = (c->hidden + moe::kTileRows - 1) / moe::kTileRows;
-    l->words = 64 + c->num_experts * mt1 + mt2;
+    l->words = kWords + size_t(c->num_experts) * div_up(c->intermediate, 128) + div_up(c->hidden, 128);
     off += align256(l->words * 4);
     l->total = off;
     return EP_OK;
+}
+
+// What both kernels' argument blocks have in common.
+template <class Args>
+ep_status experts_args(const ep_experts *h, Args &a, const ExpertsLayout &l, const void *x, long long x_stride,
+                       int num_tokens, const int32_t *ids, const float *weights, long long out_stride, int chunk)
+{
+    const ep_experts_config &c = h->cfg;
+    a.T = num_tokens;
+    a.K = c.top_k;
+    a.P = num_tokens * c.top_k;
+    a.H = c.hidden;
+    a.I = c.intermediate;
+    a.E = c.num_experts;
+    a.first = c.first_expert;
+    a.h = reinterpret_cast<__nv_bfloat16 *>(h->base.ws + l.off_h);
+    a.h_stride = l.h_stride;
+    a.ids = ids;
+    a.weights = weights;
+    a.out_stride = out_stride;
+    a.part = reinterpret_cast<float *>(h->base.ws + l.off_part);
+    set_words(a, h->base.ws + l.off_words);
+    a.err = h->base.flags.err;
+    a.mt1 = div_up(a.I, moe::kTileRows);
+    a.kc1 = div_up(a.H, chunk);
+    a.mt2 = div_up(a.H, moe::kTileRows);
+    a.kc2 = div_up(a.I, chunk);
+    ep_status st = encode_map(&a.mx, "x", 0, x, a.H, a.T, 0, x_stride, 0, moe::kChunk, 1);
+    if (st == EP_OK)
+        st = encode_map(&a.mh, "h", 0, a.h, a.I, 2LL * a.P, 0, a.h_stride, 0, moe::kChunk, 8);
+    return st;
 }
 
 }  // namespace
@@ -369,44 +680,18 @@ ep_status ep_experts_create(const ep_experts_config *cfg, void *workspace, size_
     ep_status st = plan_experts(cfg, &l);
     if (st != EP_OK)
         return st;
-    if (workspace && (!aligned(workspace, 256) || bytes < l.total))
-        MOE_FAIL("workspace has %zu bytes, needs %zu, 256-byte aligned", bytes, l.total);
-    int dev = 0, sms = 0;
-    st = current_device(&dev, &sms);
-    if (st != EP_OK)
-        return st;
     ep_experts *h = new (std::nothrow) ep_experts();
     if (!h)
         return set_error(EP_ERR_OOM, "host allocation of the handle failed");
     h->cfg = *cfg;
-    h->device = dev;
-    h->sms = sms < 256 ? sms : 256;
-    h->ws = static_cast<uint8_t *>(workspace);
-    h->owns_ws = workspace == nullptr;
     const long long E = cfg->num_experts, H = cfg->hidden, I = cfg->intermediate;
-    st = encode_map(&h->mw1, "gate_up", 0, cfg->gate_up.data, H, I, 2 * E, H, I * H, moe::kChunk, moe::kTileRows);
-    if (st == EP_OK)
+    st = h->base.open(workspace, bytes, l.total, l.off_words, l.words);
+    if (st == EP_OK && cfg->gate_up.group == 0)
+        st = encode_map(&h->mw1, "gate_up", 0, cfg->gate_up.data, H, I, 2 * E, H, I * H, moe::kChunk, moe::kTileRows);
+    if (st == EP_OK && cfg->gate_up.group == 0)
         st = encode_map(&h->mw2, "down", 0, cfg->down.data, I, H, E, I, H * I, moe::kChunk, moe::kTileRows);
-    if (st == EP_OK)
-        st = h->flags.make();
-    if (st == EP_OK && h->owns_ws) {
-        const cudaError_t ce = cudaMalloc(reinterpret_cast<void **>(&h->ws), l.total);
-        if (ce != cudaSuccess) {
-            h->ws = nullptr;
-            st = cuda_error(ce, "cudaMalloc");
-        }
-    }
-    if (st == EP_OK) {
-        cudaError_t ce = cudaMemset(h->ws + l.off_words, 0, l.words * 4);
-        if (ce == cudaSuccess)
-            ce = cudaStreamSynchronize(nullptr);
-        if (ce != cudaSuccess)
-            st = cuda_error(ce, "clearing the counters");
-    }
     if (st != EP_OK) {
-        h->flags.free();
-        if (h->owns_ws && h->ws)
-            cudaFree(h->ws);
+        h->base.close();
         delete h;
         return st;
     }
@@ -423,70 +708,63 @@ ep_status ep_experts_run(ep_experts *h, const void *x, long long x_stride, const
     const ep_experts_config &c = h->cfg;
     if (num_tokens < 0 || num_tokens > c.max_tokens)
         MOE_FAIL("num_tokens=%d outside [0, max_tokens=%d]", num_tokens, c.max_tokens);
-    ep_status st = same_device(h->device);
+    ep_status st = same_device(h->base.device);
     if (st != EP_OK)
         return st;
     if (num_tokens == 0)
         return set_error(EP_OK, "");
-    if (!x || !aligned(x, 16))
-        MOE_FAIL("x is NULL or not 16-byte aligned");
-    if (x_stride < c.hidden || x_stride % 8)
-        MOE_FAIL("x_stride=%lld must be a multiple of 8 and at least hidden=%d", x_stride, c.hidden);
+    st = check_rows("x", x, x_stride, c.hidden, 16, 8);
+    if (st == EP_OK)
+        st = check_rows("out", out, out_stride, c.hidden, 2, 1);
+    if (st != EP_OK)
+        return st;
     if (!ids || !weights || !aligned(ids, 4) || !aligned(weights, 4))
         MOE_FAIL("ids or weights is NULL or not 4-byte aligned");
-    if (!out || !aligned(out, 2) || out_stride < c.hidden)
-        MOE_FAIL("out is NULL, not 2-byte aligned, or out_stride=%lld < hidden=%d", out_stride, c.hidden);
-    st = h->flags.take();
+    st = h->base.flags.take();
     if (st != EP_OK)
         return st;
     ExpertsLayout l{};
-    st = plan_experts(&c, &l);
-    if (st != EP_OK)
-        return st;
-    moe::ExpertsArgs a = {};
-    a.mw1 = h->mw1;
-    a.mw2 = h->mw2;
-    a.T = num_tokens;
-    a.K = c.top_k;
-    a.P = num_tokens * c.top_k;
-    a.H = c.hidden;
-    a.I = c.intermediate;
-    a.E = c.num_experts;
-    a.first = c.first_expert;
-    a.h = reinterpret_cast<__nv_bfloat16 *>(h->ws + l.off_h);
-    a.h_stride = l.h_stride;
-    st = encode_map(&a.mx, "x", 0, x, a.H, a.T, 0, x_stride, 0, moe::kChunk, 1);
-    if (st == EP_OK)
-        st = encode_map(&a.mh, "h", 0, a.h, a.I, 2LL * a.P, 0, a.h_stride, 0, moe::kChunk, 8);
-    if (st != EP_OK)
-        return st;
-    a.ids = ids;
-    a.weights = weights;
-    a.out = static_cast<__nv_bfloat16 *>(out);
-    a.out_stride = out_stride;
-    a.part = reinterpret_cast<float *>(h->ws + l.off_part);
-    int *const words = reinterpret_cast<int *>(h->ws + l.off_words);
-    a.done = words;
-    a.leaving = words + 32;
-    a.tiles = words + 64;
-    a.err = h->flags.err;
-    a.mt1 = (a.I + moe::kTileRows - 1) / moe::kTileRows;
-    a.kc1 = (a.H + moe::kChunk - 1) / moe::kChunk;
-    a.mt2 = (a.H + moe::kTileRows - 1) / moe::kTileRows;
-    a.kc2 = (a.I + moe::kChunk - 1) / moe::kChunk;
-    const size_t smem = moe::experts_smem(&a);
+    plan_experts(&c, &l);
     unsigned long long *rec = epk::check_record();
-    a.chk = epk::check_ctx(rec);
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
-    return finish(moe::launch_experts(a, h->sms, smem, s), "ep_experts_run", rec, s);
+    cudaError_t ce;
+    if (c.gate_up.group == 0) {
+        moe::ExpertsArgs a = {};
+        st = experts_args(h, a, l, x, x_stride, num_tokens, ids, weights, out_stride, moe::kChunk);
+        if (st != EP_OK)
+            return st;
+        a.mw1 = h->mw1;
+        a.mw2 = h->mw2;
+        a.out = static_cast<__nv_bfloat16 *>(out);
+        a.chk = epk::check_ctx(rec);
+        const size_t smem = moe::experts_smem(&a);
+        ce = moe::launch_experts(a, h->base.sms, smem, s);
+    } else {
+        moe::Int4Args a = {};
+        st = experts_args(h, a, l, x, x_stride, num_tokens, ids, weights, out_stride, 128);
+        if (st != EP_OK)
+            return st;
+        a.w1 = static_cast<const uint8_t *>(c.gate_up.data);
+        a.w2 = static_cast<const uint8_t *>(c.down.data);
+        a.group1 = c.gate_up.group;
+        a.group2 = c.down.group;
+        a.zeros1 = c.gate_up.has_zeros != 0;
+        a.zeros2 = c.down.has_zeros != 0;
+        a.tile1 = moe::int4_tile_bytes(a.group1, a.zeros1);
+        a.tile2 = moe::int4_tile_bytes(a.group2, a.zeros2);
+        a.scale_fp16 = c.gate_up.scale_dtype == EP_DTYPE_FP16;
+        a.out = out;
+        a.chk = epk::check_ctx(rec);
+        const size_t smem = moe::int4_smem(&a, false);
+        ce = moe::launch_int4(a, false, true, h->base.sms, smem, s);
+    }
+    return finish(ce, "ep_experts_run", rec, s);
 }
 
 ep_status ep_experts_destroy(ep_experts *h)
 {
     if (h) {
-        if (h->owns_ws && h->ws)
-            cudaFree(h->ws);  // waits for work that uses it
-        h->flags.free();
+        h->base.close();
         delete h;
     }
     return set_error(EP_OK, "");
@@ -496,7 +774,8 @@ ep_status ep_experts_destroy(ep_experts *h)
 
 cudaError_t moe::kernel_binary_versions(int *out, int max, int *n)
 {
-    cudaError_t (*const fns[])(int *) = {moe::router_binary_version, moe::experts_binary_version};
+    cudaError_t (*const fns[])(int *) = {moe::router_binary_version, moe::experts_binary_version,
+                                          moe::int4_binary_version};
     *n = 0;
     for (auto *f : fns) {
         int v = 0;

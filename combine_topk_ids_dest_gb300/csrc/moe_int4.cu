@@ -1,0 +1,761 @@
+// moe_int4.cu -- products of a few tokens with 4-bit weights and group scales:
+// a linear layer, and the experts of an MoE layer.
+//
+//   w = s (q - z):  q 0..15, one scale s and zero point z (8 without) per `group` inputs
+//   linear:   y = x W^T
+//   experts:  as in moe_experts.cu
+//
+// The kernel is that of moe_experts.cu, with the weights' way to the MMA
+// lengthened by one step. A stage of the ring is a tile of 128 rows x 128
+// inputs, repacked once when the weight was taken: 8 KB of codes, its scales
+// and zero points. Two warpgroups (a thread is a weight row) turn codes into
+// q - z, whole numbers that 16 bits hold exactly, and store them to tensor
+// memory as the MMA's A operand: shared memory could not carry the 16-bit
+// tile's write and read at this rate. Scales are applied to sums, not to
+// weights: each group's sum is an accumulator of its own, and two more
+// warpgroups add s times it to fp32 registers. So no weight is rounded.
+#include "moe_device.h"
+#include "moe_internal.h"
+
+namespace moe {
+
+namespace {
+
+constexpr int kThreads = 640;      // warps: weights, MMA, tokens, -, 8 x codes, 8 x results
+constexpr int kMaxStagesA = 24;
+constexpr int kMaxStagesB = 16;
+constexpr int kTmemA = 4;          // 16-bit weight tiles in tensor memory, 64 columns each
+constexpr int kMaxSums = 16;       // accumulators in tensor memory, in the other 256 columns
+constexpr int kResults = 256;      // threads of the result warps
+
+struct Shared {
+    uint64_t full_a[kMaxStagesA], empty_a[kMaxStagesA];
+    uint64_t full_b[kMaxStagesB], empty_b[kMaxStagesB];
+    uint64_t full_t[kTmemA], empty_t[kTmemA];
+    uint64_t full_d[kMaxSums], empty_d[kMaxSums];
+    uint64_t drain;
+    uint32_t tmem;
+    int abort;
+    int active, nmax;
+    int issued_a, issued_b;
+    int last, reset;
+};
+
+struct Lists {
+    unsigned long long *mask;
+    float *weight;
+    unsigned short *expert, *offset;
+    unsigned char *token;
+};
+
+static __device__ __forceinline__ int div_up(int a, int b) { return (a + b - 1) / b; }
+
+static __device__ __forceinline__ void split(float v, __nv_bfloat16 &hi, __nv_bfloat16 &lo)
+{
+    hi = __float2bfloat16_rn(v);
+    const float r = v - __bfloat162float(hi);
+    lo = __float2bfloat16_rn(isfinite(r) ? r : 0.0f);
+}
+
+static __device__ __forceinline__ float swiglu(float gate, float up) { return gate / (1.0f + expf(-gate)) * up; }
+
+static __device__ __forceinline__ int part_slot(int total, int b, int G, int begin)
+{
+    return 2 * b + (begin <= share_begin(total, b, G) ? 0 : 1);
+}
+
+// Eight codes to four pairs q - z. Code 2p is at bits 4p, code 2p + 1 at bits
+// 4p + 16, so a shift and a mask leave a pair; or-ing the exponent of 128
+// (bf16; 1024 in fp16) makes them 128 + q, and `zz` holds 128 + z twice.
+template <bool BF16> static __device__ __forceinline__ void decode(uint32_t w, uint32_t zz, uint32_t *out)
+{
+#pragma unroll
+    for (int p = 0; p < 4; ++p) {
+        const uint32_t v = ((w >> (4 * p)) & 0x000F000Fu) | (BF16 ? 0x43004300u : 0x64006400u);
+        if (BF16)
+            asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(out[p]) : "r"(v), "r"(zz));
+        else
+            asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(out[p]) : "r"(v), "r"(zz));
+    }
+}
+
+static __device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t *r)
+{
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, "
+                 "%13, %14, %15, %16};" ::"r"(addr),
+                 "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
+                 "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+                 : "memory");
+}
+
+template <bool LINEAR, bool BF16>
+__global__ void __launch_bounds__(kThreads, 1) int4_kernel(const __grid_constant__ Int4Args a)
+{
+    extern __shared__ uint8_t dyn[];
+    __shared__ Shared sh;
+    const uint32_t dyn0 = smem_u32(dyn);
+    const uint32_t ring_b = (dyn0 + 1023u) & ~1023u;
+    const uint32_t ring_a = ring_b + a.bytes_b;
+    uint8_t *const ring_a_p = dyn + (ring_a - dyn0);
+    const int T8 = (a.T + 7) & ~7;
+    float *const acc = reinterpret_cast<float *>(ring_a_p + a.stages * a.stage_a);
+    Lists li;
+    li.mask = reinterpret_cast<unsigned long long *>(acc + (LINEAR ? 0 : T8 * kTileRows));
+    li.weight = reinterpret_cast<float *>(li.mask + a.E);
+    li.expert = reinterpret_cast<unsigned short *>(li.weight + a.P);
+    li.offset = li.expert + a.E;
+    li.token = reinterpret_cast<unsigned char *>(li.offset + a.E + 1);
+
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int G = gridDim.x, blk = blockIdx.x;
+    volatile int *const abort = &sh.abort;
+
+    if (tid == 0) {
+        sh.abort = sh.reset = sh.issued_a = sh.issued_b = 0;
+        for (int i = 0; i < kMaxStagesA; ++i) {
+            mbar_init(smem_u32(&sh.full_a[i]), 1);
+            mbar_init(smem_u32(&sh.empty_a[i]), 4 + 8);  // the warps that read codes, then scales
+        }
+        for (int i = 0; i < kMaxStagesB; ++i) {
+            mbar_init(smem_u32(&sh.full_b[i]), 1);
+            mbar_init(smem_u32(&sh.empty_b[i]), 1);
+        }
+        for (int i = 0; i < kTmemA; ++i) {
+            mbar_init(smem_u32(&sh.full_t[i]), 4);
+            mbar_init(smem_u32(&sh.empty_t[i]), 1);
+        }
+        for (int i = 0; i < kMaxSums; ++i) {
+            mbar_init(smem_u32(&sh.full_d[i]), 1);
+            mbar_init(smem_u32(&sh.empty_d[i]), 8);
+        }
+        mbar_init(smem_u32(&sh.drain), 1);
+        mbar_init_fence();
+        tma_prefetch_map(&a.mx);
+        if (!LINEAR)
+            tma_prefetch_map(&a.mh);
+    }
+    if (warp == 1)
+        tmem_alloc(smem_u32(&sh.tmem), 512);
+
+    if (LINEAR) {  // one "expert" whose tokens are the rows of x
+        if (tid == 0) {
+            li.expert[0] = 0;
+            li.offset[0] = 0;
+            li.offset[1] = static_cast<unsigned short>(a.T);
+            sh.active = 1;
+            sh.nmax = a.T;
+        }
+    } else {
+        for (int e = tid; e < a.E; e += kThreads)
+            li.mask[e] = 0;
+        __syncthreads();
+        for (int i = tid; i < a.P; i += kThreads) {
+            if (!EP_IN_BOUNDS(a.chk, epk::kSiteMoeIds, a.ids + i, 4, a.ids, 4LL * a.P))
+                continue;
+            const int e = a.ids[i] - a.first;
+            if (e >= 0 && e < a.E)
+                atomicOr(&li.mask[e], 1ULL << (i / a.K));
+        }
+        __syncthreads();
+        if (warp == 0) {
+            int n_active = 0, n_pairs = 0, nmax = 0;
+            for (int e0 = 0; e0 < a.E; e0 += 32) {
+                const int e = e0 + lane;
+                const int n = e < a.E ? __popcll(li.mask[e]) : 0;
+                const unsigned live = __ballot_sync(~0u, n > 0);
+                int sum = n;
+                for (int d = 1; d < 32; d <<= 1) {
+                    const int v = __shfl_up_sync(~0u, sum, d);
+                    if (lane >= d)
+                        sum += v;
+                }
+                if (n > 0) {
+                    const int at = n_active + __popc(live & ((1u << lane) - 1));
+                    li.expert[at] = static_cast<unsigned short>(e);
+                    li.offset[at] = static_cast<unsigned short>(n_pairs + sum - n);
+                }
+                n_active += __popc(live);
+                n_pairs += __shfl_sync(~0u, sum, 31);
+                nmax = max(nmax, __reduce_max_sync(~0u, n));
+            }
+            if (lane == 0) {
+                li.offset[n_active] = static_cast<unsigned short>(n_pairs);
+                sh.active = n_active;
+                sh.nmax = nmax;
+            }
+        }
+        __syncthreads();
+        for (int i = tid; i < sh.active; i += kThreads) {
+            const int e = li.expert[i];
+            int at = li.offset[i];
+            for (unsigned long long m = li.mask[e]; m; m &= m - 1, ++at) {
+                const int t = __ffsll(static_cast<long long>(m)) - 1;
+                float w = 0.0f;
+                for (int k = 0; k < a.K; ++k)
+                    if (a.ids[t * a.K + k] - a.first == e &&
+                        EP_IN_BOUNDS(a.chk, epk::kSiteMoeWeights, a.weights + t * a.K + k, 4, a.weights, 4LL * a.P))
+                        w += a.weights[t * a.K + k];
+                li.token[at] = static_cast<unsigned char>(t);
+                li.weight[at] = w;
+            }
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = sh.tmem;
+    const int A = sh.active;
+
+    if (A == 0) {
+        for (long long i = static_cast<long long>(blk) * kThreads + tid; i < static_cast<long long>(a.T) * a.H;
+             i += static_cast<long long>(G) * kThreads) {
+            const long long t = i / a.H;
+            uint16_t *const p = static_cast<uint16_t *>(a.out) + t * a.out_stride + (i - t * a.H);
+            if (EP_IN_BOUNDS(a.chk, epk::kSiteMoeOut, p, 2, a.out, 2 * ((a.T - 1) * a.out_stride + a.H)))
+                *p = 0;
+        }
+        __syncthreads();
+        if (warp == 1)
+            tmem_free(tmem, 512);
+        return;
+    }
+
+    // gate and up (or one) tiles of the first product; the second product of the experts
+    constexpr int kParts = LINEAR ? 1 : 2;
+    const int total1 = A * a.mt1 * a.kc1, total2 = LINEAR ? 0 : A * a.mt2 * a.kc2;
+    const int G1 = min(G, total1), G2 = min(G, total2);
+    const int begin1 = share_begin(total1, min(blk, G1), G1), end1 = share_begin(total1, min(blk + 1, G1), G1);
+    const int begin2 = LINEAR ? 0 : share_begin(total2, min(blk, G2), G2);
+    const int end2 = LINEAR ? 0 : share_begin(total2, min(blk + 1, G2), G2);
+    const int width = LINEAR ? div_up(sh.nmax, 16) * 16 : div_up(sh.nmax, 8) * 16;  // rows of a token tile, columns of a sum
+    const int stage_b = width * 256;  // two 64-input halves
+    const int stages_b = min(kMaxStagesB, a.bytes_b / stage_b);
+    const int sums = min(kMaxSums, 256 / width);
+    const int groups1 = 128 / a.group1, groups2 = 128 / a.group2;
+
+    if (warp == 0 && lane == 0) {
+        // ---- weight tiles ----
+        const uint64_t policy = policy_evict_first();
+        int it = 0;
+        bool run = true;
+        auto load = [&](const uint8_t *src, uint32_t bytes) {
+            const int s = it % a.stages;
+            if (!mbar_wait(smem_u32(&sh.empty_a[s]), ((it / a.stages) & 1) ^ 1, abort, kWaitEmptyA))
+                return false;
+            const uint32_t bar = smem_u32(&sh.full_a[s]);
+            mbar_expect(bar, bytes);
+            bulk_load(ring_a + s * a.stage_a, src, bytes, bar, policy);
+            ++it;
+            return true;
+        };
+        for (int u = begin1; run && u < end1; ++u) {
+            const int tile = u / a.kc1, kc = u - tile * a.kc1;
+            const int i = tile / a.mt1, m = tile - i * a.mt1;
+            for (int g = 0; run && g < kParts; ++g) {
+                const size_t mat = static_cast<size_t>(li.expert[i]) * kParts + g;
+                run = load(a.w1 + ((mat * a.mt1 + m) * a.kc1 + kc) * a.tile1, a.tile1);
+            }
+        }
+        for (int u = begin2; run && u < end2; ++u) {
+            const int tile = u / a.kc2, kc = u - tile * a.kc2;
+            const int m = tile / A;
+            const size_t mat = li.expert[tile - m * A];
+            run = load(a.w2 + ((mat * a.mt2 + m) * a.kc2 + kc) * a.tile2, a.tile2);
+        }
+        sh.issued_a = it;
+    } else if (warp == 2 && lane == 0) {
+        // ---- token tiles ----
+        int it = 0;
+        bool run = true;
+        auto acquire = [&](uint32_t bytes, uint32_t &dst, uint32_t &bar) {
+            const int s = it % stages_b;
+            if (!mbar_wait(smem_u32(&sh.empty_b[s]), ((it / stages_b) & 1) ^ 1, abort, kWaitEmptyB))
+                return false;
+            bar = smem_u32(&sh.full_b[s]);
+            dst = ring_b + s * stage_b;
+            mbar_expect(bar, bytes);
+            ++it;
+            return true;
+        };
+        for (int u = begin1; run && u < end1; ++u) {
+            const int tile = u / a.kc1, kc = u - tile * a.kc1, i = tile / a.mt1;
+            const int off = li.offset[i], n = li.offset[i + 1] - off;
+            uint32_t dst, bar;
+            if (LINEAR) {
+                const int n8 = div_up(n, 8);
+                run = acquire(n8 * 2048, dst, bar);
+                for (int b = 0; run && b < n8; ++b)
+                    for (int half = 0; half < 2; ++half)
+                        tma_load_2d(dst + half * width * 128 + b * 1024, &a.mx, bar, kc * 128 + half * 64, b * 8);
+            } else {
+                const int quads = div_up(n, 4);
+                run = acquire(quads * 1024, dst, bar);
+                for (int q = 0; run && q < quads; ++q) {
+                    const int j = 4 * q, l = n - 1;
+                    const int r0 = li.token[off + j], r1 = li.token[off + min(j + 1, l)];
+                    const int r2 = li.token[off + min(j + 2, l)], r3 = li.token[off + min(j + 3, l)];
+                    for (int half = 0; half < 2; ++half)
+                        tma_gather4(dst + half * width * 128 + q * 512, &a.mx, bar, kc * 128 + half * 64, r0, r1, r2, r3);
+                }
+            }
+        }
+        if (run && begin2 < end2) {
+            const unsigned long long t0 = now_ns();
+            while (ld_acquire(a.done) < A * a.mt1) {
+                if (*abort || now_ns() - t0 > kWaitNs) {
+                    *abort = *abort ? *abort : kWaitDone;
+                    run = false;
+                    break;
+                }
+            }
+            fence_async_proxy();
+        }
+        for (int u = begin2; run && u < end2; ++u) {
+            const int tile = u / a.kc2, kc = u - tile * a.kc2, i = tile % A;
+            const int off = li.offset[i], n8 = div_up(li.offset[i + 1] - off, 8);
+            uint32_t dst, bar;
+            run = acquire(n8 * 4096, dst, bar);
+            for (int b = 0; run && b < n8; ++b)
+                for (int half = 0; half < 2; ++half) {
+                    const uint32_t to = dst + half * width * 128;
+                    tma_load_2d(to + b * 1024, &a.mh, bar, kc * 128 + half * 64, off + b * 8);
+                    tma_load_2d(to + (n8 + b) * 1024, &a.mh, bar, kc * 128 + half * 64, a.P + off + b * 8);
+                }
+        }
+        sh.issued_b = it;
+    } else if (warp == 1 && lane == 0) {
+        // ---- matrix instructions ----
+        int it_t = 0, it_b = 0, it_d = 0;
+        bool run = true;
+        for (int product = 0; run && product < 2; ++product) {
+            const int kc_n = product ? a.kc2 : a.kc1, end = product ? end2 : end1;
+            const int parts = product ? 1 : kParts, groups = product ? groups2 : groups1, steps = 8 / groups;
+            for (int u = product ? begin2 : begin1; run && u < end; ++u) {
+                const int tile = u / kc_n;
+                const int i = product ? tile % A : tile / a.mt1;
+                const int n = li.offset[i + 1] - li.offset[i];
+                const int N = product ? div_up(n, 8) * 16 : div_up(n, 16) * 16;
+                const uint32_t idesc = idesc_f16(kTileRows, N, BF16);
+                const int sb = it_b % stages_b;
+                run = mbar_wait(smem_u32(&sh.full_b[sb]), (it_b / stages_b) & 1, abort, kWaitFullB);
+                const uint32_t b0 = ring_b + sb * stage_b;
+                for (int g = 0; run && g < parts; ++g) {
+                    const int t = it_t % kTmemA;
+                    run = mbar_wait(smem_u32(&sh.full_t[t]), (it_t / kTmemA) & 1, abort, kWaitFullA);
+                    for (int q = 0; run && q < groups; ++q) {
+                        const int s = it_d % sums;
+                        run = mbar_wait(smem_u32(&sh.empty_d[s]), ((it_d / sums) & 1) ^ 1, abort, kWaitEmptyD);
+                        if (!run)
+                            break;
+                        tc_fence_after();
+                        for (int c = 0; c < steps; ++c) {
+                            const int k16 = q * steps + c;  // sixteenths of inputs within the tile
+                            const uint32_t b = b0 + (k16 >> 2) * width * 128;
+                            mma_ts(tmem + 256 + s * width, tmem + t * 64 + k16 * 8, desc_sw128(b) + 2 * (k16 & 3), idesc,
+                                   c > 0);
+                        }
+                        tc_commit(smem_u32(&sh.full_d[s]));
+                        ++it_d;
+                    }
+                    tc_commit(smem_u32(&sh.empty_t[t]));
+                    ++it_t;
+                }
+                tc_commit(smem_u32(&sh.empty_b[sb]));
+                ++it_b;
+            }
+        }
+        tc_commit(smem_u32(&sh.drain));
+        mbar_wait(smem_u32(&sh.drain), 0, nullptr, kWaitOther);
+    } else if (warp >= 4 && warp < 12) {
+        // ---- codes to 16-bit weights in tensor memory; the two warpgroups take tiles in turn ----
+        const int wg = (warp - 4) >> 2, row = tid & 127;
+        const uint32_t lanes = tmem + (static_cast<uint32_t>(warp & 3) << 21);
+        const int tiles1 = (end1 - begin1) * kParts, tiles = tiles1 + (end2 - begin2);
+        bool run = true;
+        for (int it = wg; run && it < tiles; it += 2) {
+            const bool second = it >= tiles1;
+            const int group = second ? a.group2 : a.group1, groups = 128 / group;
+            const bool zeros = second ? a.zeros2 : a.zeros1;
+            const int s = it % a.stages, t = it % kTmemA;
+            run = mbar_wait(smem_u32(&sh.full_a[s]), (it / a.stages) & 1, abort, kWaitFullA) &&
+                  mbar_wait(smem_u32(&sh.empty_t[t]), ((it / kTmemA) & 1) ^ 1, abort, kWaitEmptyA);
+            run = __all_sync(~0u, run);
+            if (!run)
+                break;
+            tc_fence_after();
+            const uint8_t *const tile = ring_a_p + s * a.stage_a;
+            const uint8_t *const zp = tile + 8192 + groups * 256;
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const uint4 w = *reinterpret_cast<const uint4 *>(tile + q * 2048 + row * 16);
+                const uint32_t z = zeros ? zp[(q * 32 / group) * 128 + row] : 8;
+                const uint32_t zz = (BF16 ? 0x43004300u : 0x64006400u) + z * 0x10001u;
+                uint32_t r[16];
+                decode<BF16>(w.x, zz, r);
+                decode<BF16>(w.y, zz, r + 4);
+                decode<BF16>(w.z, zz, r + 8);
+                decode<BF16>(w.w, zz, r + 12);
+                tmem_st16(lanes + t * 64 + q * 16, r);
+            }
+            tmem_wait_st();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) {
+                mbar_arrive(smem_u32(&sh.empty_a[s]));
+                mbar_arrive(smem_u32(&sh.full_t[t]));
+            }
+        }
+    } else if (warp >= 12) {
+        // ---- scales and results; the two warpgroups share the columns ----
+        const int wg = (warp - 12) >> 2, row = tid & 127, rtid = tid - 384;
+        const uint32_t lanes = tmem + 256 + (static_cast<uint32_t>(warp & 3) << 21);
+        int it_a = 0, it_d = 0;
+        bool run = true;
+        float v[2][32];  // sums of this thread's row: gate and up (or the one product), up to 32 columns
+
+        auto arrive_last = [&](int *counter, int parts) {
+            __threadfence();
+            named_sync(1, kResults);
+            if (rtid == 0)
+                sh.last = add_acq_rel(counter) == parts - 1;
+            named_sync(1, kResults);
+            const bool last = sh.last != 0;
+            if (last)
+                __threadfence();
+            return last;
+        };
+        // Adds s times the sum of each group of one weight tile to v[p], columns [c0, c0 + 8 nb) of the sum and,
+        // where lo > 0, those `lo` further.
+        auto add_tile = [&](float *p, int groups, int c0, int nb, int lo) {
+            const int st = it_a % a.stages;
+            run = run && mbar_wait(smem_u32(&sh.full_a[st]), (it_a / a.stages) & 1, abort, kWaitFullA);
+            const uint8_t *const sc = ring_a_p + st * a.stage_a + 8192;
+            for (int q = 0; q < groups; ++q) {
+                const int d = it_d % sums;
+                run = run && mbar_wait(smem_u32(&sh.full_d[d]), (it_d / sums) & 1, abort, kWaitFullD);
+                run = __all_sync(~0u, run);
+                if (!run)
+                    return;
+                tc_fence_after();
+                const uint16_t raw = *reinterpret_cast<const uint16_t *>(sc + q * 256 + row * 2);
+                const float s = a.scale_fp16 ? __half2float(__ushort_as_half(raw))
+                                             : __uint_as_float(static_cast<uint32_t>(raw) << 16);
+#pragma unroll
+                for (int b = 0; b < 4; ++b)
+                    if (b < nb) {
+                        float x[8], y[8];
+                        tmem_ld8(lanes + d * width + c0 + b * 8, x);
+                        if (lo > 0)
+                            tmem_ld8(lanes + d * width + lo + c0 + b * 8, y);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int c = 0; c < 8; ++c)
+                            p[b * 8 + c] = fmaf(s, lo > 0 ? x[c] + y[c] : x[c], p[b * 8 + c]);
+                    }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive(smem_u32(&sh.empty_d[d]));
+                ++it_d;
+            }
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive(smem_u32(&sh.empty_a[st]));
+            ++it_a;
+        };
+
+        for (int u = begin1; run && u < end1;) {
+            const int tile = u / a.kc1, k0 = u - tile * a.kc1, k1 = min(a.kc1, k0 + end1 - u);
+            const int i = tile / a.mt1, m = tile - i * a.mt1;
+            const int off = li.offset[i], n = li.offset[i + 1] - off;
+            const int blocks = div_up(n, 8), half = div_up(blocks, 2);  // columns by eights: this warpgroup's
+            const int c0 = wg ? half * 8 : 0, nb = wg ? blocks - half : half, n8 = blocks * 8;
+            const int first_unit = tile * a.kc1;
+            const int b0 = share_owner(total1, first_unit, G1), b1 = share_owner(total1, first_unit + a.kc1 - 1, G1);
+            const int col = m * kTileRows + row;
+#pragma unroll
+            for (int c = 0; c < 32; ++c)
+                v[0][c] = v[1][c] = 0.0f;
+            for (int k = k0; run && k < k1; ++k) {
+                add_tile(v[0], groups1, c0, nb, 0);
+                if (!LINEAR)
+                    add_tile(v[1], groups1, c0, nb, 0);
+            }
+            run = named_all(2, kResults, run);
+            if (!run)
+                break;
+            auto result = [&](int j, float gate, float up) {
+                if (j >= n)
+                    return;
+                if (LINEAR) {
+                    if (col < a.I) {
+                        uint16_t *const p = static_cast<uint16_t *>(a.out) + j * a.out_stride + col;
+                        if (EP_IN_BOUNDS(a.chk, epk::kSiteMoeOut, p, 2, a.out, 2 * ((a.T - 1) * a.out_stride + a.I)))
+                            *p = BF16 ? __bfloat16_as_ushort(__float2bfloat16_rn(gate))
+                                      : __half_as_ushort(__float2half_rn(gate));
+                    }
+                } else if (col < a.I) {
+                    __nv_bfloat16 hi, lo;
+                    split(swiglu(gate, up), hi, lo);
+                    a.h[static_cast<size_t>(off + j) * a.h_stride + col] = hi;
+                    a.h[static_cast<size_t>(a.P + off + j) * a.h_stride + col] = lo;
+                }
+            };
+            bool mine = b0 == b1;
+            if (mine) {
+#pragma unroll
+                for (int c = 0; c < 32; ++c)
+                    if (c < nb * 8)
+                        result(c0 + c, v[0][c], v[1][c]);
+            } else {
+                float *const part = a.part + static_cast<size_t>(part_slot(total1, blk, G1, first_unit)) * a.part_floats;
+#pragma unroll
+                for (int c = 0; c < 32; ++c)
+                    if (c < nb * 8) {
+                        part[(c0 + c) * kTileRows + row] = v[0][c];
+                        if (!LINEAR)
+                            part[(n8 + c0 + c) * kTileRows + row] = v[1][c];
+                    }
+                if (arrive_last(a.tiles + tile, b1 - b0 + 1)) {
+                    mine = true;
+                    for (int j = c0; j < c0 + nb * 8; j += 8) {
+                        float g[8] = {}, w[8] = {};
+                        for (int b = b0; b <= b1; ++b) {
+                            const float *const p =
+                                a.part + static_cast<size_t>(part_slot(total1, b, G1, first_unit)) * a.part_floats;
+#pragma unroll
+                            for (int c = 0; c < 8; ++c) {
+                                g[c] += __ldcg(p + (j + c) * kTileRows + row);
+                                if (!LINEAR)
+                                    w[c] += __ldcg(p + (n8 + j + c) * kTileRows + row);
+                            }
+                        }
+#pragma unroll
+                        for (int c = 0; c < 8; ++c)
+                            result(j + c, g[c], w[c]);
+                    }
+                }
+            }
+            if (!LINEAR && mine) {
+                fence_async_proxy();
+                __threadfence();
+                named_sync(1, kResults);
+                if (rtid == 0)
+                    add_acq_rel(a.done);
+            }
+            u += k1 - k0;
+        }
+
+        const int group = LINEAR ? 1 : A * a.kc2;
+        for (int u = begin2; !LINEAR && run && u < end2;) {
+            const int m = u / group, stop = min(end2, (m + 1) * group), first_unit = m * group;
+            const int b0 = share_owner(total2, first_unit, G2), b1 = share_owner(total2, first_unit + group - 1, G2);
+            for (int t = wg; t < T8; t += 2)
+                acc[t * kTileRows + row] = 0.0f;
+            while (run && u < stop) {
+                const int tile = u / a.kc2, k0 = u - tile * a.kc2, k1 = min(a.kc2, k0 + stop - u);
+                const int i = tile - m * A, off = li.offset[i], n = li.offset[i + 1] - off;
+                const int blocks = div_up(n, 8), half = div_up(blocks, 2);
+                const int c0 = wg ? half * 8 : 0, nb = wg ? blocks - half : half;
+#pragma unroll
+                for (int c = 0; c < 32; ++c)
+                    v[0][c] = 0.0f;
+                for (int k = k0; run && k < k1; ++k)
+                    add_tile(v[0], groups2, c0, nb, blocks * 8);
+                // also: the other warpgroup's rows of acc for the experts before are written
+                run = named_all(2, kResults, run);
+                if (!run)
+                    break;
+#pragma unroll
+                for (int c = 0; c < 32; ++c)
+                    if (c < nb * 8 && c0 + c < n) {
+                        float *const s = acc + li.token[off + c0 + c] * kTileRows + row;
+                        *s = fmaf(li.weight[off + c0 + c], v[0][c], *s);
+                    }
+                u += k1 - k0;
+            }
+            run = named_all(2, kResults, run);
+            if (!run)
+                break;
+            const int col = m * kTileRows + row;
+            auto store = [&](int t, float r) {
+                __nv_bfloat16 *const p = static_cast<__nv_bfloat16 *>(a.out) + t * a.out_stride + col;
+                if (t < a.T && col < a.H &&
+                    EP_IN_BOUNDS(a.chk, epk::kSiteMoeOut, p, 2, a.out, 2 * ((a.T - 1) * a.out_stride + a.H)))
+                    *p = __float2bfloat16_rn(r);
+            };
+            if (b0 == b1) {
+                for (int t = wg; t < a.T; t += 2)
+                    store(t, acc[t * kTileRows + row]);
+            } else {
+                float *const part = a.part + static_cast<size_t>(part_slot(total2, blk, G2, first_unit)) * a.part_floats;
+                for (int t = wg; t < a.T; t += 2)
+                    part[t * kTileRows + row] = acc[t * kTileRows + row];
+                if (arrive_last(a.tiles + a.E * a.mt1 + m, b1 - b0 + 1)) {
+                    for (int t = wg * 8; t < a.T; t += 16) {
+                        float r[8] = {};
+                        for (int b = b0; b <= b1; ++b) {
+                            const float *const p =
+                                a.part + static_cast<size_t>(part_slot(total2, b, G2, first_unit)) * a.part_floats;
+#pragma unroll
+                            for (int c = 0; c < 8; ++c)
+                                if (t + c < a.T)
+                                    r[c] += __ldcg(p + (t + c) * kTileRows + row);
+                        }
+#pragma unroll
+                        for (int c = 0; c < 8; ++c)
+                            store(t + c, r[c]);
+                    }
+                }
+            }
+            named_sync(1, kResults);  // acc is read before the next row tile clears it
+        }
+    }
+    __syncwarp();
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+
+    if (sh.abort) {
+        if (tid == 0) {
+            for (int i = max(0, sh.issued_a - a.stages); i < sh.issued_a; ++i)
+                mbar_wait(smem_u32(&sh.full_a[i % a.stages]), (i / a.stages) & 1, nullptr, kWaitOther);
+            for (int i = max(0, sh.issued_b - stages_b); i < sh.issued_b; ++i)
+                mbar_wait(smem_u32(&sh.full_b[i % stages_b]), (i / stages_b) & 1, nullptr, kWaitOther);
+            atomicAdd_system(a.err + sh.abort, 1u);
+            __threadfence_system();
+            atomicAdd_system(a.err, 1u);
+        }
+        __syncthreads();
+    }
+    if (warp == 1)
+        tmem_free(tmem, 512);
+
+    if (tid == 0)
+        sh.reset = add_acq_rel(a.leaving) == G - 1;
+    __syncthreads();
+    if (sh.reset) {
+        for (int i = tid; i < A * a.mt1; i += kThreads)
+            a.tiles[i] = 0;
+        for (int i = tid; !LINEAR && i < a.mt2; i += kThreads)
+            a.tiles[a.E * a.mt1 + i] = 0;
+        if (tid == 0)
+            *a.done = *a.leaving = 0;
+    }
+}
+
+// One thread per 32 codes of a tile: [4][128 rows][16 bytes], then scales and
+// zero points [groups][128 rows]. Rows and inputs outside the matrix become
+// codes of 0 with a scale of 0.
+__global__ void __launch_bounds__(256) pack_kernel(const __grid_constant__ PackArgs a)
+{
+    const long long id = static_cast<long long>(blockIdx.x) * 256 + threadIdx.x;
+    const int row = static_cast<int>(id & 127), q = static_cast<int>((id >> 7) & 3);
+    const long long tile = id >> 9;
+    if (tile >= a.mats * a.mt * a.kc)
+        return;
+    const long long mat = tile / (static_cast<long long>(a.mt) * a.kc);
+    const int m = static_cast<int>(tile / a.kc - mat * a.mt), kc = static_cast<int>(tile % a.kc);
+    const int r = m * 128 + row, k = kc * 128 + q * 32;
+    const bool inside = r < a.rows && k < a.cols;  // cols is a multiple of 32
+    const long long src_row = mat * a.rows + r;
+    uint32_t in[4] = {0, 0, 0, 0}, out[4];
+    if (inside) {
+        const uint8_t *const p = a.codes + src_row * (a.cols / 2) + k / 2;
+        for (int i = 0; i < 16; ++i)
+            in[i / 4] |= static_cast<uint32_t>(p[i]) << (8 * (i % 4));
+    }
+#pragma unroll
+    for (int w = 0; w < 4; ++w) {  // codes 0..7 in order -> even ones in the low half, odd ones in the high half
+        uint32_t o = 0;
+#pragma unroll
+        for (int c = 0; c < 8; ++c)
+            o |= ((in[w] >> (4 * c)) & 15u) << ((c >> 1) * 4 + (c & 1) * 16);
+        out[w] = o;
+    }
+    uint8_t *const dst = a.dst + tile * a.tile_bytes;
+    *reinterpret_cast<uint4 *>(dst + q * 2048 + row * 16) = make_uint4(out[0], out[1], out[2], out[3]);
+    const int groups = 128 / a.group;
+    for (int g = q; g < groups; g += 4) {
+        const int kg = kc * 128 + g * a.group;
+        const bool in_g = r < a.rows && kg < a.cols;
+        const long long at = src_row * (a.cols / a.group) + kg / a.group;
+        reinterpret_cast<uint16_t *>(dst + 8192)[g * 128 + row] = in_g ? a.scales[at] : 0;
+        if (a.zeros)
+            (dst + 8192 + groups * 256)[g * 128 + row] = in_g ? (a.zeros[at] & 15) : 0;
+    }
+}
+
+}  // namespace
+
+int int4_tile_bytes(int group, bool zeros)
+{
+    return 8192 + 128 / group * 256 + (zeros ? 128 / group * 128 : 0);
+}
+
+size_t int4_part_floats(int T, bool linear)
+{
+    const int T8 = (T + 7) & ~7;
+    return static_cast<size_t>(linear ? 1 : 2) * T8 * kTileRows;
+}
+
+size_t int4_smem(Int4Args *a, bool linear)
+{
+    const int T8 = (a->T + 7) & ~7;
+    size_t lists = (linear ? 0 : static_cast<size_t>(T8) * kTileRows * 4) + static_cast<size_t>(a->E) * 8 +
+                   static_cast<size_t>(a->P) * 4 + static_cast<size_t>(a->E) * 2 + static_cast<size_t>(a->E + 1) * 2 +
+                   static_cast<size_t>(a->P);
+    a->bytes_b = T8 <= 8 ? 32 * 1024 : 64 * 1024;  // at least 2 stages of the largest token tile
+    a->stage_a = a->tile1 > a->tile2 ? a->tile1 : a->tile2;
+    a->part_floats = static_cast<int>(int4_part_floats(a->T, linear));
+    const size_t room = kSmemMax - sizeof(Shared) - 1024 - lists - a->bytes_b - 64;
+    a->stages = static_cast<int>(room / a->stage_a);
+    if (a->stages > kMaxStagesA)
+        a->stages = kMaxStagesA;
+    return 1024 + static_cast<size_t>(a->stages) * a->stage_a + a->bytes_b + lists;
+}
+
+cudaError_t launch_int4(const Int4Args &a, bool linear, bool bf16, int grid, size_t smem, cudaStream_t stream)
+{
+    using Kernel = void (*)(Int4Args);
+    static const Kernel kernels[3] = {int4_kernel<false, true>, int4_kernel<true, true>, int4_kernel<true, false>};
+    static const cudaError_t attr = [] {
+        cudaError_t ce = cudaSuccess;
+        for (Kernel k : kernels)
+            if (ce == cudaSuccess)
+                ce = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                          kSmemMax - 64 - static_cast<int>(sizeof(Shared)));
+        return ce;
+    }();
+    if (attr != cudaSuccess)
+        return attr;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeCooperative;
+    at[0].val.cooperative = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernels[linear ? (bf16 ? 1 : 2) : 0], a);
+}
+
+cudaError_t launch_pack(const PackArgs &a, cudaStream_t stream)
+{
+    const long long threads = a.mats * a.mt * a.kc * 512;
+    pack_kernel<<<static_cast<unsigned>((threads + 255) / 256), 256, 0, stream>>>(a);
+    return cudaGetLastError();
+}
+
+cudaError_t int4_binary_version(int *v)
+{
+    cudaFuncAttributes fa;
+    const cudaError_t ce = cudaFuncGetAttributes(&fa, int4_kernel<false, true>);
+    if (ce == cudaSuccess)
+        *v = fa.binaryVersion;
+    return ce;
+}
+
+}  // namespace moe

@@ -50,6 +50,7 @@ cudaError_t router_binary_version(int *v);
 // ---- experts with dense bf16 weights (moe_experts.cu) ---------------------------
 
 constexpr int kTileRows = 128;              // weight rows of a tile: the MMA's M
+constexpr int kSmemMax = 227 * 1024;        // shared memory of a block, static and dynamic
 constexpr int kChunk = 64;                  // inputs of a bf16 chunk: one 128-byte swizzled row
 constexpr int kStageA = kTileRows * kChunk * 2;
 
@@ -81,6 +82,45 @@ cudaError_t experts_binary_version(int *v);
 size_t experts_smem(ExpertsArgs *a);
 // Floats of one block's part (two per block) for up to T tokens.
 size_t experts_part_floats(int T);
+
+// ---- products with 4-bit weights (moe_int4.cu) -------------------------------------
+
+struct Int4Args {
+    CUtensorMap mx;  // x [T, H]: one-row boxes (experts) or 8-row boxes (linear) of 64 columns
+    CUtensorMap mh;  // h [2 P, I], boxes 64 x 8 (experts)
+    const uint8_t *w1, *w2;  // packed tiles [matrix][row tile][chunk]
+    const int32_t *ids;
+    const float *weights;
+    void *out;
+    long long out_stride;
+    __nv_bfloat16 *h;
+    float *part;
+    int *done, *leaving, *tiles;
+    unsigned int *err;
+    int T, K, P, E, first;
+    int H, I;  // linear: inputs, outputs
+    int mt1, kc1, mt2, kc2;
+    int group1, group2, zeros1, zeros2, tile1, tile2, scale_fp16;
+    int h_stride;
+    int stages, stage_a, bytes_b, part_floats;
+    epk::CheckCtx chk;
+};
+
+struct PackArgs {
+    const uint8_t *codes;    // [mats, rows, cols / 2]
+    const uint16_t *scales;  // [mats, rows, cols / group]
+    const uint8_t *zeros;    // likewise, or NULL
+    uint8_t *dst;
+    long long mats;
+    int rows, cols, group, mt, kc, tile_bytes;
+};
+
+int int4_tile_bytes(int group, bool zeros);  // of one tile of 128 rows x 128 inputs
+size_t int4_part_floats(int T, bool linear);
+size_t int4_smem(Int4Args *a, bool linear);
+cudaError_t launch_int4(const Int4Args &a, bool linear, bool bf16, int grid, size_t smem, cudaStream_t stream);
+cudaError_t launch_pack(const PackArgs &a, cudaStream_t stream);
+cudaError_t int4_binary_version(int *v);
 
 // Binary versions of this library's MoE kernels, as epk::kernel_binary_versions.
 cudaError_t kernel_binary_versions(int *out, int max, int *n);

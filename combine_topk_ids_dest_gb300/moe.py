@@ -3,7 +3,8 @@
 :class:`EpRouter` makes the ``topk_ids`` and ``topk_weights`` that
 ``EpComm.dispatch`` takes; :class:`EpExperts` computes the experts for a few
 tokens, on all experts or on the rows one rank received; :class:`EpMoeLayer`
-is both, a whole layer on one GPU. All work runs in the CUDA library on
+is both, a whole layer on one GPU; :class:`Int4Linear` is a product with 4-bit
+weights. All work runs in the CUDA library on
 torch's current stream of the tensors' device; torch supplies device memory
 and streams only. Weights are kept by reference, not copied.
 
@@ -76,6 +77,15 @@ class _Handle:
         n = x.shape[0]
         return n, (x.stride(0) if n > 1 else cols)
 
+    def _out(self, out, n, cols, dtype):
+        """`out`, or a new tensor, [n, cols] of dtype, and its row stride."""
+        if out is None:
+            return torch.empty((n, cols), dtype=dtype, device=self.device), cols
+        m, stride = self._rows(out, cols, dtype, "out")
+        if m != n:
+            raise ValueError(f"out must have {n} rows, got {m}")
+        return out, stride
+
     def _call(self, fn, *args):
         """fn(handle, *args, stream) on the handle's device."""
         if torch.cuda.current_device() != self._index:
@@ -142,39 +152,130 @@ class EpRouter(_Handle):
         return ids, weights
 
 
-class EpExperts(_Handle):
+class Int4Weight:
+    """4-bit weights ``[..., rows, cols]`` with a scale, and optionally a zero point, per ``group`` columns:
+    ``w = scale * (code - zero)``, ``zero`` 8 where none are given.
+
+    ``codes`` uint8 [..., rows, cols/2] (the low four bits are the even column),
+    ``scales`` bf16 or fp16 [..., rows, cols/group], ``zeros`` uint8 of the same
+    shape or None. ``group`` (32, 64 or 128) follows from the shapes.
+    """
+
+    def __init__(self, codes: torch.Tensor, scales: torch.Tensor, zeros: Optional[torch.Tensor] = None):
+        device = _device_of(codes, "codes")
+        if codes.dtype is not torch.uint8 or codes.dim() < 2 or scales.dtype not in _DTYPES:
+            raise ValueError("codes must be a uint8 tensor [..., rows, cols/2], scales bfloat16 or float16")
+        cols, n = 2 * int(codes.shape[-1]), int(scales.shape[-1]) if scales.dim() else 0
+        self.group = cols // n if n and cols % n == 0 else 0
+        if self.group not in (32, 64, 128):
+            raise ValueError(f"{cols} columns with {n} scales: groups must be of 32, 64 or 128 columns")
+        self.shape = tuple(int(d) for d in codes.shape[:-1]) + (cols,)
+        shape = self.shape[:-1] + (n,)
+        self.codes = _weight("codes", codes, torch.uint8, codes.shape, device)
+        self.scales = _weight("scales", scales, scales.dtype, shape, device)
+        self.zeros = None if zeros is None else _weight("zeros", zeros, torch.uint8, shape, device)
+        self.device = device
+
+    def pack(self, mats: int, rows: int) -> torch.Tensor:
+        """The weight as ``mats`` matrices of ``rows`` rows, in the operators' order (ep_weight_pack)."""
+        L = _lib.load()
+        w = _lib.EpIntWeightC(self.codes.data_ptr(), self.scales.data_ptr(),
+                              0 if self.zeros is None else self.zeros.data_ptr(), _DTYPES[self.scales.dtype], mats, rows,
+                              self.shape[-1], self.group)
+        need = ctypes.c_size_t(0)
+        check(L.ep_weight_packed_size(ctypes.byref(w), ctypes.byref(need)))
+        with torch.cuda.device(self.device):
+            packed = torch.empty(need.value, dtype=torch.uint8, device=self.device)
+            check(L.ep_weight_pack(ctypes.byref(w), packed.data_ptr(), need.value,
+                                   torch.cuda.current_stream().cuda_stream))
+        return packed
+
+    def _c(self, packed: torch.Tensor) -> "_lib.EpWeightC":
+        return _lib.EpWeightC(packed.data_ptr(), self.group, int(self.zeros is not None), _DTYPES[self.scales.dtype])
+
+
+class _Workspace(_Handle):
+    """A handle with a workspace that torch allocates."""
+
+    def _create(self, cfg, size, create):
+        need = ctypes.c_size_t(0)
+        check(size(ctypes.byref(cfg), ctypes.byref(need)))
+        h = ctypes.c_void_p()
+        with torch.cuda.device(self.device):
+            self._ws = torch.empty(need.value, dtype=torch.uint8, device=self.device)
+            # the handle's counters are cleared on the default stream: this stream may still use the memory,
+            # and its packing of the weights has to be done before another stream's call
+            torch.cuda.current_stream().synchronize()
+            check(create(ctypes.byref(cfg), self._ws.data_ptr(), need.value, ctypes.byref(h)))
+        self._h = h.value
+
+
+class Int4Linear(_Workspace):
+    """``y = x @ W.T`` for up to ``max_tokens`` (at most 64) rows, W an :class:`Int4Weight` [outputs, inputs].
+
+    x is bf16 or fp16, y has its type. The weight is packed here once; the
+    Int4Weight is not needed afterwards.
+    """
+
+    _destroy = "ep_linear_destroy"
+
+    def __init__(self, weight: Int4Weight, max_tokens: int = 64):
+        if not isinstance(weight, Int4Weight) or len(weight.shape) != 2:
+            raise ValueError("weight must be an Int4Weight [outputs, inputs]")
+        self.outputs, self.inputs = weight.shape
+        self.max_tokens = int(max_tokens)
+        self._open(weight.device)
+        self._packed = weight.pack(1, self.outputs)
+        cfg = _lib.EpLinearConfigC(self.inputs, self.outputs, self.max_tokens, weight._c(self._packed))
+        self._create(cfg, self._L.ep_linear_workspace_size, self._L.ep_linear_create)
+
+    def __call__(self, x: torch.Tensor, out: Optional[torch.Tensor] = None) -> torch.Tensor:
+        """``x`` [tokens, inputs] -> [tokens, outputs] (``out`` if given)."""
+        dtype = x.dtype
+        if dtype not in _DTYPES:
+            raise ValueError(f"x is {dtype}, expected bfloat16 or float16")
+        n, stride = self._rows(x, self.inputs, dtype)
+        out, out_stride = self._out(out, n, self.outputs, dtype)
+        self._call(self._L.ep_linear_run, _DTYPES[dtype], x.data_ptr(), stride, n, out.data_ptr(), out_stride)
+        return out
+
+
+class EpExperts(_Workspace):
     """The experts of an MoE layer for up to ``max_tokens`` (at most 64) tokens.
 
     ``gate_up`` [experts, 2*intermediate, hidden] (gate rows, then up rows) and
-    ``down`` [experts, hidden, intermediate] are bf16 tensors. The experts are
-    the global ids ``first_expert ..``; ids outside them are skipped, so one
-    rank's experts run on the rows ``EpComm.dispatch`` delivered and write the
-    rows ``EpComm.combine`` adds up.
+    ``down`` [experts, hidden, intermediate] are both bf16 tensors (kept by
+    reference) or both :class:`Int4Weight` (packed here once, not needed
+    afterwards). The experts are the global ids ``first_expert ..``; ids
+    outside them are skipped, so one rank's experts run on the rows
+    ``EpComm.dispatch`` delivered and write the rows ``EpComm.combine`` adds up.
     """
 
     _destroy = "ep_experts_destroy"
 
     def __init__(self, gate_up, down, top_k: int, max_tokens: int = 64, first_expert: int = 0):
-        device = _device_of(gate_up, "gate_up")
-        if gate_up.dim() != 3 or gate_up.shape[1] % 2:
+        packed = isinstance(gate_up, Int4Weight)
+        if packed != isinstance(down, Int4Weight):
+            raise ValueError("gate_up and down must both be tensors or both Int4Weight")
+        device = gate_up.device if packed else _device_of(gate_up, "gate_up")
+        if len(gate_up.shape) != 3 or gate_up.shape[1] % 2:
             raise ValueError("gate_up must be [experts, 2*intermediate, hidden]")
         E, I2, H = (int(n) for n in gate_up.shape)
         self.num_experts, self.intermediate, self.hidden = E, I2 // 2, H
         self.top_k, self.max_tokens, self.first_expert = int(top_k), int(max_tokens), int(first_expert)
         self.dtype = torch.bfloat16
-        self._w = (_weight("gate_up", gate_up, torch.bfloat16, (E, I2, H), device),
-                   _weight("down", down, torch.bfloat16, (E, H, I2 // 2), device))
         self._open(device)
-        cfg = _lib.EpExpertsConfigC(E, self.first_expert, self.top_k, H, I2 // 2, self.max_tokens,
-                                    _lib.EpWeightC(gate_up.data_ptr(), 0), _lib.EpWeightC(down.data_ptr(), 0))
-        need = ctypes.c_size_t(0)
-        check(self._L.ep_experts_workspace_size(ctypes.byref(cfg), ctypes.byref(need)))
-        h = ctypes.c_void_p()
-        with torch.cuda.device(device):
-            self._ws = torch.empty(need.value, dtype=torch.uint8, device=device)
-            torch.cuda.current_stream().synchronize()  # the memory may still be in use on this stream
-            check(self._L.ep_experts_create(ctypes.byref(cfg), self._ws.data_ptr(), need.value, ctypes.byref(h)))
-        self._h = h.value
+        if packed:
+            if down.shape != (E, H, I2 // 2) or down.device != device:
+                raise ValueError(f"down must be {(E, H, I2 // 2)} on {device}, got {down.shape} on {down.device}")
+            self._w = (gate_up.pack(2 * E, I2 // 2), down.pack(E, H))
+            cw = gate_up._c(self._w[0]), down._c(self._w[1])
+        else:
+            self._w = (_weight("gate_up", gate_up, torch.bfloat16, (E, I2, H), device),
+                       _weight("down", down, torch.bfloat16, (E, H, I2 // 2), device))
+            cw = tuple(_lib.EpWeightC(w.data_ptr(), 0, 0, 0) for w in self._w)
+        cfg = _lib.EpExpertsConfigC(E, self.first_expert, self.top_k, H, I2 // 2, self.max_tokens, *cw)
+        self._create(cfg, self._L.ep_experts_workspace_size, self._L.ep_experts_create)
 
     def __call__(self, x: torch.Tensor, topk_ids: torch.Tensor, topk_weights: torch.Tensor,
                  out: Optional[torch.Tensor] = None) -> torch.Tensor:
@@ -185,13 +286,7 @@ class EpExperts(_Handle):
             if t.dtype is not dtype or t.get_device() != self._index or tuple(t.shape) != (n, self.top_k) \
                     or not t.is_contiguous():
                 raise ValueError(f"{name} must be a contiguous {dtype} tensor [{n}, {self.top_k}] on {self.device}")
-        if out is None:
-            out = torch.empty((n, self.hidden), dtype=self.dtype, device=x.device)
-            out_stride = self.hidden
-        else:
-            m, out_stride = self._rows(out, self.hidden, self.dtype, "out")
-            if m != n:
-                raise ValueError(f"out must have {n} rows, got {m}")
+        out, out_stride = self._out(out, n, self.hidden, self.dtype)
         self._call(self._L.ep_experts_run, x.data_ptr(), stride, topk_ids.data_ptr(), topk_weights.data_ptr(), n,
                    out.data_ptr(), out_stride)
         return out

@@ -35,7 +35,7 @@ extern "C" {
 
 #define EP_MOE_MAX_TOKENS 64     /* rows of one experts or linear call */
 #define EP_MOE_MAX_EXPERTS 512   /* experts of a router; local experts of an experts handle */
-#define EP_MOE_MAX_DIM 65536     /* hidden, intermediate, inputs, outputs / 16 */
+#define EP_MOE_MAX_DIM 65536     /* hidden, intermediate, inputs */
 
 /* ---- router ------------------------------------------------------------------
  * l = x W^T in fp32; s = sigmoid(l), or softmax(l) over the experts.
@@ -84,6 +84,65 @@ ep_status ep_router_run(ep_router *r, const void *x, long long x_stride, int num
 
 ep_status ep_router_destroy(ep_router *r);
 
+/* ---- 4-bit weights -------------------------------------------------------------
+ * w[r][c] = scale[r][c / group] * (code[r][c] - zero[r][c / group])
+ * codes 0..15, two to a byte, the even column in the low four bits; zero
+ * points 0..15 (8 without them). The operators read them in a packed order:
+ * tiles of 128 rows x 128 columns with their scales and zero points.
+ */
+typedef struct {
+    const uint8_t *codes;  /* device [mats, rows, cols / 2] */
+    const void *scales;    /* device [mats, rows, cols / group], EP_DTYPE_BF16 or EP_DTYPE_FP16 */
+    const uint8_t *zeros;  /* device [mats, rows, cols / group], or NULL */
+    ep_dtype scale_dtype;
+    int mats, rows, cols;  /* rows, cols >= 1; cols a multiple of group */
+    int group;             /* 32, 64 or 128 */
+} ep_int_weight;
+
+/* A weight as the operators take it: group 0: data is bf16, contiguous,
+ * 16-byte aligned, kept and not copied; group 32, 64 or 128: data is what
+ * ep_weight_pack wrote. */
+typedef struct {
+    const void *data;
+    int group;
+    int has_zeros;         /* packed: with zero points */
+    ep_dtype scale_dtype;  /* packed */
+} ep_weight;
+
+ep_status ep_weight_packed_size(const ep_int_weight *w, size_t *bytes);
+
+/* Packs w into packed: device, 128-byte aligned, of at least
+ * ep_weight_packed_size bytes. w is not needed once the queued work has run.
+ * (gate_up of experts is packed as 2*experts matrices of `intermediate` rows.) */
+ep_status ep_weight_pack(const ep_int_weight *w, void *packed, size_t bytes, void *stream);
+
+/* ---- linear ----------------------------------------------------------------------
+ * y = x W^T with packed 4-bit W [outputs, inputs]: sums are fp32, no weight is
+ * rounded, y is rounded once.
+ */
+typedef struct ep_linear ep_linear;
+
+typedef struct {
+    int inputs;       /* a multiple of the group, <= EP_MOE_MAX_DIM */
+    int outputs;      /* 1 .. 16 * EP_MOE_MAX_DIM */
+    int max_tokens;   /* 1..EP_MOE_MAX_TOKENS */
+    ep_weight weight; /* packed, kept */
+} ep_linear_config;
+
+ep_status ep_linear_workspace_size(const ep_linear_config *cfg, size_t *bytes);
+
+/* workspace as for ep_experts_create. */
+ep_status ep_linear_create(const ep_linear_config *cfg, void *workspace, size_t bytes, ep_linear **out);
+
+/* x: device [num_tokens, inputs], rows x_stride elements apart (a multiple
+ * of 8), 16-byte aligned; y: device [num_tokens, outputs], rows y_stride
+ * elements apart; both of dtype, EP_DTYPE_BF16 or EP_DTYPE_FP16.
+ * 0 <= num_tokens <= max_tokens; 0 does nothing. y may not overlap x. */
+ep_status ep_linear_run(ep_linear *h, ep_dtype dtype, const void *x, long long x_stride, int num_tokens, void *y,
+                        long long y_stride, void *stream);
+
+ep_status ep_linear_destroy(ep_linear *h);
+
 /* ---- experts -------------------------------------------------------------------
  * y_t = sum_k w_tk * W2_e ( silu(W1_e x_t) * (W3_e x_t) ),  e = ids[t, k] - first_expert
  * over the k whose e lies in [0, num_experts); a token with none gets 0.
@@ -92,13 +151,6 @@ ep_status ep_router_destroy(ep_router *r);
  */
 typedef struct ep_experts ep_experts;
 
-/* A weight of `experts` matrices [rows, cols]. group 0: data is bf16,
- * contiguous, 16-byte aligned. */
-typedef struct {
-    const void *data;
-    int group;
-} ep_weight;
-
 typedef struct {
     int num_experts;    /* local experts, 1..EP_MOE_MAX_EXPERTS */
     int first_expert;   /* global id of the first */
@@ -106,7 +158,7 @@ typedef struct {
     int hidden;         /* a multiple of 8 (of the group, for 4-bit weights), <= EP_MOE_MAX_DIM */
     int intermediate;   /* likewise */
     int max_tokens;     /* 1..EP_MOE_MAX_TOKENS */
-    ep_weight gate_up;  /* [num_experts, 2*intermediate, hidden]: gate rows, then up rows; kept, not copied */
+    ep_weight gate_up;  /* [num_experts, 2*intermediate, hidden]: gate rows, then up rows */
     ep_weight down;     /* [num_experts, hidden, intermediate] */
 } ep_experts_config;
 
