@@ -26,8 +26,7 @@
 //    sums are fp32, y is rounded once.
 //  - For each row tile of y a block adds its experts' contributions, times
 //    the routing weight, in fp32 in ascending expert order.
-#include "moe_device.h"
-#include "moe_internal.h"
+#include "moe_sched.h"
 
 namespace moe {
 
@@ -50,33 +49,6 @@ struct Shared {
     int last, reset;
 };
 
-// Lists of the chosen experts, in dynamic shared memory.
-struct Lists {
-    unsigned long long *mask;  // [E] tokens of each expert
-    float *weight;             // [P] routing weight of each (expert, token) pair
-    unsigned short *expert;    // [E] active experts, ascending
-    unsigned short *offset;    // [E + 1] their first pair
-    unsigned char *token;      // [P] tokens, ascending per expert
-};
-
-static __device__ __forceinline__ int div_up(int a, int b) { return (a + b - 1) / b; }
-
-// Two bf16 values whose sum carries 16 bits of v's mantissa (v itself where it is not finite).
-static __device__ __forceinline__ void split(float v, __nv_bfloat16 &hi, __nv_bfloat16 &lo)
-{
-    hi = __float2bfloat16_rn(v);
-    const float r = v - __bfloat162float(hi);
-    lo = __float2bfloat16_rn(isfinite(r) ? r : 0.0f);
-}
-
-static __device__ __forceinline__ float swiglu(float gate, float up) { return gate / (1.0f + expf(-gate)) * up; }
-
-// Slot (first or last share) in which block b keeps its part of the tile that begins at unit `begin`.
-static __device__ __forceinline__ int part_slot(int total, int b, int G, int begin)
-{
-    return 2 * b + (begin <= share_begin(total, b, G) ? 0 : 1);
-}
-
 __global__ void __launch_bounds__(kThreads, 1) experts_kernel(const __grid_constant__ ExpertsArgs a)
 {
     extern __shared__ uint8_t dyn[];
@@ -87,12 +59,7 @@ __global__ void __launch_bounds__(kThreads, 1) experts_kernel(const __grid_const
     uint8_t *const after = dyn + (ring_b - dyn0) + a.bytes_b;
     const int T8 = (a.T + 7) & ~7;
     float *const acc = reinterpret_cast<float *>(after);
-    Lists li;
-    li.mask = reinterpret_cast<unsigned long long *>(acc + T8 * kTileRows);
-    li.weight = reinterpret_cast<float *>(li.mask + a.E);
-    li.expert = reinterpret_cast<unsigned short *>(li.weight + a.P);
-    li.offset = li.expert + a.E;
-    li.token = reinterpret_cast<unsigned char *>(li.offset + a.E + 1);
+    const Lists li(acc + T8 * kTileRows, a.E, a.P);
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int G = gridDim.x, blk = blockIdx.x;
@@ -121,75 +88,15 @@ __global__ void __launch_bounds__(kThreads, 1) experts_kernel(const __grid_const
     }
     if (warp == 1)
         tmem_alloc(smem_u32(&sh.tmem), kTmemCols);
-    for (int e = tid; e < a.E; e += kThreads)
-        li.mask[e] = 0;
-    __syncthreads();
-
-    // tokens of each expert (a bit set, so the order of the threads does not matter)
-    for (int i = tid; i < a.P; i += kThreads) {
-        if (!EP_IN_BOUNDS(a.chk, epk::kSiteMoeIds, a.ids + i, 4, a.ids, 4LL * a.P))
-            continue;
-        const int e = a.ids[i] - a.first;
-        if (e >= 0 && e < a.E)
-            atomicOr(&li.mask[e], 1ULL << (i / a.K));
-    }
-    __syncthreads();
-    if (warp == 0) {
-        int n_active = 0, n_pairs = 0, nmax = 0;
-        for (int e0 = 0; e0 < a.E; e0 += 32) {
-            const int e = e0 + lane;
-            const int n = e < a.E ? __popcll(li.mask[e]) : 0;
-            const unsigned live = __ballot_sync(~0u, n > 0);
-            int sum = n;  // inclusive prefix sum over the lanes
-            for (int d = 1; d < 32; d <<= 1) {
-                const int v = __shfl_up_sync(~0u, sum, d);
-                if (lane >= d)
-                    sum += v;
-            }
-            if (n > 0) {
-                const int at = n_active + __popc(live & ((1u << lane) - 1));
-                li.expert[at] = static_cast<unsigned short>(e);
-                li.offset[at] = static_cast<unsigned short>(n_pairs + sum - n);
-            }
-            n_active += __popc(live);
-            n_pairs += __shfl_sync(~0u, sum, 31);
-            nmax = max(nmax, __reduce_max_sync(~0u, n));
-        }
-        if (lane == 0) {
-            li.offset[n_active] = static_cast<unsigned short>(n_pairs);
-            sh.active = n_active;
-            sh.nmax = nmax;
-        }
-    }
-    __syncthreads();
-    const int A = sh.active;
-    for (int i = tid; i < A; i += kThreads) {
-        const int e = li.expert[i];
-        int at = li.offset[i];
-        for (unsigned long long m = li.mask[e]; m; m &= m - 1, ++at) {
-            const int t = __ffsll(static_cast<long long>(m)) - 1;
-            float w = 0.0f;  // an expert named twice by a token counts twice
-            for (int k = 0; k < a.K; ++k)
-                if (a.ids[t * a.K + k] - a.first == e &&
-                    EP_IN_BOUNDS(a.chk, epk::kSiteMoeWeights, a.weights + t * a.K + k, 4, a.weights, 4LL * a.P))
-                    w += a.weights[t * a.K + k];
-            li.token[at] = static_cast<unsigned char>(t);
-            li.weight[at] = w;
-        }
-    }
+    build_lists(a, li, sh, tid, kThreads);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = sh.tmem;
+    const int A = sh.active;
 
     if (A == 0) {  // no token chose an expert of this handle
-        for (long long i = static_cast<long long>(blk) * kThreads + tid; i < static_cast<long long>(a.T) * a.H;
-             i += static_cast<long long>(G) * kThreads) {
-            const long long t = i / a.H;
-            __nv_bfloat16 *const p = a.out + t * a.out_stride + (i - t * a.H);
-            if (EP_IN_BOUNDS(a.chk, epk::kSiteMoeOut, p, 2, a.out, 2 * ((a.T - 1) * a.out_stride + a.H)))
-                *p = __float2bfloat16_rn(0.0f);
-        }
+        clear_out(a, blk, G, tid, kThreads);
         __syncthreads();
         if (warp == 1)
             tmem_free(tmem, kTmemCols);
@@ -201,122 +108,107 @@ __global__ void __launch_bounds__(kThreads, 1) experts_kernel(const __grid_const
     const int G1 = min(G, total1), G2 = min(G, total2);
     const int begin1 = share_begin(total1, min(blk, G1), G1), end1 = share_begin(total1, min(blk + 1, G1), G1);
     const int begin2 = share_begin(total2, min(blk, G2), G2), end2 = share_begin(total2, min(blk + 1, G2), G2);
-    const int stage_b = div_up(sh.nmax, 8) * 16 * 128;  // 8 tokens: up to 16 rows of 128 bytes
+    const int stage_b = ceil_div(sh.nmax, 8) * 16 * 128;  // 8 tokens: up to 16 rows of 128 bytes
     const int stages_b = min(kMaxStagesB, a.bytes_b / stage_b);
 
     if (warp == 0 && lane == 0) {
         // ---- weight tiles ----
         const uint64_t policy = policy_evict_first();
-        int it = 0;
+        Cursor at;
+        int issued = 0;
         bool run = true;
         auto load = [&](const CUtensorMap *map, int x, int y, int z) {
-            const int s = it % a.stages;
-            if (!mbar_wait(smem_u32(&sh.empty_a[s]), ((it / a.stages) & 1) ^ 1, abort, kWaitEmptyA))
+            if (!mbar_wait(smem_u32(&sh.empty_a[at.s]), at.parity ^ 1, abort, kWaitEmptyA))
                 return false;
-            const uint32_t bar = smem_u32(&sh.full_a[s]);
+            const uint32_t bar = smem_u32(&sh.full_a[at.s]);
             mbar_expect(bar, kStageA);
-            tma_load_3d(ring_a + s * kStageA, map, bar, x, y, z, policy);
-            ++it;
+            tma_load_3d(ring_a + at.s * kStageA, map, bar, x, y, z, policy);
+            at.next(a.stages);
+            ++issued;
             return true;
         };
-        for (int u = begin1; run && u < end1; ++u) {
-            const int tile = u / a.kc1, kc = u - tile * a.kc1;
-            const int i = tile / a.mt1, m = tile - i * a.mt1, e = li.expert[i];
-            run = load(&a.mw1, kc * kChunk, m * kTileRows, 2 * e) &&
-                  load(&a.mw1, kc * kChunk, m * kTileRows, 2 * e + 1);
+        for (Walk w(begin1, end1, a.kc1, a.mt1, false); run && w.more(); w.next()) {
+            const int e = li.expert[w.i];
+            for (int k = w.k; run && k < w.k + w.len; ++k)
+                run = load(&a.mw1, k * kChunk, w.m * kTileRows, 2 * e) &&
+                      load(&a.mw1, k * kChunk, w.m * kTileRows, 2 * e + 1);
         }
-        for (int u = begin2; run && u < end2; ++u) {
-            const int tile = u / a.kc2, kc = u - tile * a.kc2;
-            const int m = tile / A, e = li.expert[tile - m * A];
-            run = load(&a.mw2, kc * kChunk, m * kTileRows, e);
+        for (Walk w(begin2, end2, a.kc2, A, true); run && w.more(); w.next()) {
+            const int e = li.expert[w.i];
+            for (int k = w.k; run && k < w.k + w.len; ++k)
+                run = load(&a.mw2, k * kChunk, w.m * kTileRows, e);
         }
-        sh.issued_a = it;
+        sh.issued_a = issued;
     } else if (warp == 2 && lane == 0) {
         // ---- token tiles ----
-        int it = 0;
+        Cursor at;
+        int issued = 0;
         bool run = true;
-        auto acquire = [&](uint32_t bytes, uint32_t &dst, uint32_t &bar) {
-            const int s = it % stages_b;
-            if (!mbar_wait(smem_u32(&sh.empty_b[s]), ((it / stages_b) & 1) ^ 1, abort, kWaitEmptyB))
+        uint32_t dst = 0, bar = 0;
+        auto acquire = [&](uint32_t bytes) {
+            if (!mbar_wait(smem_u32(&sh.empty_b[at.s]), at.parity ^ 1, abort, kWaitEmptyB))
                 return false;
-            bar = smem_u32(&sh.full_b[s]);
-            dst = ring_b + s * stage_b;
+            bar = smem_u32(&sh.full_b[at.s]);
+            dst = ring_b + at.s * stage_b;
             mbar_expect(bar, bytes);
-            ++it;
+            at.next(stages_b);
+            ++issued;
             return true;
         };
-        for (int u = begin1; run && u < end1; ++u) {
-            const int tile = u / a.kc1, kc = u - tile * a.kc1, i = tile / a.mt1;
-            const int off = li.offset[i], n = li.offset[i + 1] - off, quads = div_up(n, 4);
-            uint32_t dst, bar;
-            run = acquire(quads * 512, dst, bar);
-            for (int q = 0; run && q < quads; ++q) {  // short of a fourth row: the last one again
-                const int j = 4 * q, l = n - 1;
-                tma_gather4(dst + q * 512, &a.mx, bar, kc * kChunk, li.token[off + j], li.token[off + min(j + 1, l)],
-                            li.token[off + min(j + 2, l)], li.token[off + min(j + 3, l)]);
-            }
+        for (Walk w(begin1, end1, a.kc1, a.mt1, false); run && w.more(); w.next()) {
+            const int n = li.count(w.i), quads = ceil_div(n, 4);
+            const unsigned char *const tok = li.token + li.offset[w.i];
+            for (int k = w.k; k < w.k + w.len && (run = acquire(quads * 512)); ++k)
+                for (int j = 0; j < n; j += 4)  // short of a fourth row: the last one again
+                    tma_gather4(dst + j * 128, &a.mx, bar, k * kChunk, tok[j], tok[min(j + 1, n - 1)],
+                                tok[min(j + 2, n - 1)], tok[min(j + 3, n - 1)]);
         }
-        if (run && begin2 < end2) {  // h is complete when every tile of the first product is
-            const unsigned long long t0 = now_ns();
-            while (ld_acquire(a.done) < A * a.mt1) {
-                if (*abort || now_ns() - t0 > kWaitNs) {
-                    *abort = *abort ? *abort : kWaitDone;
-                    run = false;
-                    break;
+        if (run && begin2 < end2)  // h is complete when every tile of the first product is
+            run = wait_products(a, A * a.mt1, abort);
+        for (Walk w(begin2, end2, a.kc2, A, true); run && w.more(); w.next()) {
+            const int off = li.offset[w.i], n8 = ceil_div(li.count(w.i), 8);
+            for (int k = w.k; k < w.k + w.len && (run = acquire(n8 * 2048)); ++k)
+                for (int b = 0; b < n8; ++b) {
+                    tma_load_2d(dst + b * 1024, &a.mh, bar, k * kChunk, off + b * 8);
+                    tma_load_2d(dst + (n8 + b) * 1024, &a.mh, bar, k * kChunk, a.P + off + b * 8);
                 }
-            }
-            fence_async_proxy();
         }
-        for (int u = begin2; run && u < end2; ++u) {
-            const int tile = u / a.kc2, kc = u - tile * a.kc2, i = tile % A;
-            const int off = li.offset[i], n8 = div_up(li.offset[i + 1] - off, 8);
-            uint32_t dst, bar;
-            run = acquire(n8 * 2048, dst, bar);
-            for (int b = 0; run && b < n8; ++b) {
-                tma_load_2d(dst + b * 1024, &a.mh, bar, kc * kChunk, off + b * 8);
-                tma_load_2d(dst + (n8 + b) * 1024, &a.mh, bar, kc * kChunk, a.P + off + b * 8);
-            }
-        }
-        sh.issued_b = it;
+        sh.issued_b = issued;
     } else if (warp == 1 && lane == 0) {
         // ---- matrix instructions ----
-        int it_a = 0, it_b = 0, seg = 0;
+        Cursor at_a, at_b, at_d;
         bool run = true;
         for (int product = 0; run && product < 2; ++product) {
-            const int kc_n = product ? a.kc2 : a.kc1, end = product ? end2 : end1;
             const int parts = product ? 1 : 2;  // gate and up share the token tile
-            for (int u = product ? begin2 : begin1; run && u < end;) {
-                const int tile = u / kc_n, k0 = u - tile * kc_n, k1 = min(kc_n, k0 + end - u);
-                const int i = product ? tile % A : tile / a.mt1;
-                const int n = li.offset[i + 1] - li.offset[i];
-                const int N = product ? div_up(n, 8) * 16 : div_up(n, 16) * 16;
+            for (Walk w(product ? begin2 : begin1, product ? end2 : end1, product ? a.kc2 : a.kc1,
+                        product ? A : a.mt1, product != 0);
+                 run && w.more(); w.next()) {
+                const int n = li.count(w.i);
+                const int N = product ? ceil_div(n, 8) * 16 : ceil_div(n, 16) * 16;
                 const uint32_t idesc = idesc_f16(kTileRows, N, 1);
-                const uint32_t d = tmem + (seg & 1) * 128;
-                run = mbar_wait(smem_u32(&sh.empty_d[seg & 1]), ((seg >> 1) & 1) ^ 1, abort, kWaitEmptyD);
+                const uint32_t d = tmem + at_d.s * 128;
+                run = mbar_wait(smem_u32(&sh.empty_d[at_d.s]), at_d.parity ^ 1, abort, kWaitEmptyD);
                 tc_fence_after();
-                for (int k = k0; run && k < k1; ++k) {
-                    const int sb = it_b % stages_b;
-                    run = mbar_wait(smem_u32(&sh.full_b[sb]), (it_b / stages_b) & 1, abort, kWaitFullB);
+                for (int k = 0; run && k < w.len; ++k) {
+                    run = mbar_wait(smem_u32(&sh.full_b[at_b.s]), at_b.parity, abort, kWaitFullB);
                     for (int g = 0; run && g < parts; ++g) {
-                        const int sa = it_a % a.stages;
-                        run = mbar_wait(smem_u32(&sh.full_a[sa]), (it_a / a.stages) & 1, abort, kWaitFullA);
+                        run = mbar_wait(smem_u32(&sh.full_a[at_a.s]), at_a.parity, abort, kWaitFullA);
                         if (!run)
                             break;
                         tc_fence_after();
-                        const uint64_t da = desc_sw128(ring_a + sa * kStageA);
-                        const uint64_t db = desc_sw128(ring_b + sb * stage_b);
+                        const uint64_t da = desc_sw128(ring_a + at_a.s * kStageA);
+                        const uint64_t db = desc_sw128(ring_b + at_b.s * stage_b);
 #pragma unroll
                         for (int q = 0; q < 4; ++q)  // 16 inputs each: 32 bytes further, in 16-byte units
-                            mma_ss(d + g * N, da + 2 * q, db + 2 * q, idesc, k > k0 || q > 0);
-                        tc_commit(smem_u32(&sh.empty_a[sa]));
-                        ++it_a;
+                            mma_ss(d + g * N, da + 2 * q, db + 2 * q, idesc, k > 0 || q > 0);
+                        tc_commit(smem_u32(&sh.empty_a[at_a.s]));
+                        at_a.next(a.stages);
                     }
-                    tc_commit(smem_u32(&sh.empty_b[sb]));
-                    ++it_b;
+                    tc_commit(smem_u32(&sh.empty_b[at_b.s]));
+                    at_b.next(stages_b);
                 }
-                tc_commit(smem_u32(&sh.full_d[seg & 1]));
-                ++seg;
-                u += k1 - k0;
+                tc_commit(smem_u32(&sh.full_d[at_d.s]));
+                at_d.next(2);
             }
         }
         tc_commit(smem_u32(&sh.drain));
@@ -325,7 +217,7 @@ __global__ void __launch_bounds__(kThreads, 1) experts_kernel(const __grid_const
         // ---- results ----
         const int row = tid - 128;
         const uint32_t lanes = tmem + (static_cast<uint32_t>(warp - 4) << 21);
-        int seg = 0;
+        Cursor at_d;
         bool run = true;
 
         // Counts this block's part of a tile; true in the block whose part was the last.
@@ -341,19 +233,17 @@ __global__ void __launch_bounds__(kThreads, 1) experts_kernel(const __grid_const
             return last;
         };
 
-        for (int u = begin1; run && u < end1; ++seg) {
-            const int tile = u / a.kc1, k0 = u - tile * a.kc1, k1 = min(a.kc1, k0 + end1 - u);
-            const int i = tile / a.mt1, m = tile - i * a.mt1;
-            const int off = li.offset[i], n = li.offset[i + 1] - off, N = div_up(n, 16) * 16, n8 = (n + 7) & ~7;
-            const int first_unit = tile * a.kc1;
+        for (Walk w(begin1, end1, a.kc1, a.mt1, false); run && w.more(); w.next()) {
+            const int tile = w.i * a.mt1 + w.m, first_unit = tile * a.kc1;
+            const int off = li.offset[w.i], n = li.count(w.i), N = ceil_div(n, 16) * 16, n8 = (n + 7) & ~7;
             const int b0 = share_owner(total1, first_unit, G1), b1 = share_owner(total1, first_unit + a.kc1 - 1, G1);
-            const int col = m * kTileRows + row;  // of h
-            run = mbar_wait(smem_u32(&sh.full_d[seg & 1]), (seg >> 1) & 1, abort, kWaitFullD);
+            const int col = w.m * kTileRows + row;  // of h
+            run = mbar_wait(smem_u32(&sh.full_d[at_d.s]), at_d.parity, abort, kWaitFullD);
             run = named_all(2, 128, run);  // the four warps leave together, or not at all
             if (!run)
                 break;
             tc_fence_after();
-            const uint32_t d = lanes + (seg & 1) * 128;
+            const uint32_t d = lanes + at_d.s * 128;
             float *const part = a.part + static_cast<size_t>(part_slot(total1, blk, G1, first_unit)) * a.part_floats;
             auto finish = [&](int j, float gate, float up) {
                 if (j < n && col < a.I) {
@@ -379,7 +269,8 @@ __global__ void __launch_bounds__(kThreads, 1) experts_kernel(const __grid_const
                 }
             }
             tc_fence_before();
-            mbar_arrive(smem_u32(&sh.empty_d[seg & 1]));
+            mbar_arrive(smem_u32(&sh.empty_d[at_d.s]));
+            at_d.next(2);
             bool mine = b0 == b1;
             if (!mine && arrive_last(a.tiles + tile, b1 - b0 + 1)) {
                 mine = true;
@@ -406,24 +297,22 @@ __global__ void __launch_bounds__(kThreads, 1) experts_kernel(const __grid_const
                 if (row == 0)
                     add_acq_rel(a.done);
             }
-            u += k1 - k0;
         }
 
         const int group = A * a.kc2;  // units of one row tile of y, over all experts
-        for (int u = begin2; run && u < end2;) {
-            const int m = u / group, stop = min(end2, (m + 1) * group), first_unit = m * group;
+        for (Walk w(begin2, end2, a.kc2, A, true); run && w.more();) {
+            const int m = w.m, first_unit = m * group;
             const int b0 = share_owner(total2, first_unit, G2), b1 = share_owner(total2, first_unit + group - 1, G2);
             for (int t = 0; t < T8; ++t)
                 acc[t * kTileRows + row] = 0.0f;
-            for (; run && u < stop; ++seg) {
-                const int tile = u / a.kc2, k0 = u - tile * a.kc2, k1 = min(a.kc2, k0 + stop - u);
-                const int i = tile - m * A, off = li.offset[i], n = li.offset[i + 1] - off, n8 = (n + 7) & ~7;
-                run = mbar_wait(smem_u32(&sh.full_d[seg & 1]), (seg >> 1) & 1, abort, kWaitFullD);
+            for (; run && w.more() && w.m == m; w.next()) {
+                const int off = li.offset[w.i], n = li.count(w.i), n8 = (n + 7) & ~7;
+                run = mbar_wait(smem_u32(&sh.full_d[at_d.s]), at_d.parity, abort, kWaitFullD);
                 run = named_all(2, 128, run);  // the four warps leave together, or not at all
                 if (!run)
                     break;
                 tc_fence_after();
-                const uint32_t d = lanes + (seg & 1) * 128;
+                const uint32_t d = lanes + at_d.s * 128;
                 for (int j = 0; j < n8; j += 8) {
                     float hi[8], lo[8];
                     tmem_ld8(d + j, hi);
@@ -437,8 +326,8 @@ __global__ void __launch_bounds__(kThreads, 1) experts_kernel(const __grid_const
                         }
                 }
                 tc_fence_before();
-                mbar_arrive(smem_u32(&sh.empty_d[seg & 1]));
-                u += k1 - k0;
+                mbar_arrive(smem_u32(&sh.empty_d[at_d.s]));
+                at_d.next(2);
             }
             if (!run)
                 break;
@@ -520,8 +409,7 @@ size_t experts_part_floats(int T)
 size_t experts_smem(ExpertsArgs *a)
 {
     const int T8 = (a->T + 7) & ~7;
-    size_t lists = static_cast<size_t>(T8) * kTileRows * 4 + static_cast<size_t>(a->E) * 8 + static_cast<size_t>(a->P) * 4 +
-                   static_cast<size_t>(a->E) * 2 + static_cast<size_t>(a->E + 1) * 2 + static_cast<size_t>(a->P);
+    const size_t lists = static_cast<size_t>(T8) * kTileRows * 4 + lists_bytes(a->E, a->P);
     a->bytes_b = T8 <= 8 ? 24 * 1024 : 48 * 1024;  // at least 12 and 3 stages of the largest token tile
     a->part_floats = static_cast<int>(experts_part_floats(a->T));
     const size_t room = kSmemMax - sizeof(Shared) - 1024 - lists - a->bytes_b - 64;

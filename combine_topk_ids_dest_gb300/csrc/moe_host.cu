@@ -539,6 +539,7 @@ ep_status ep_linear_run(ep_linear *h, ep_dtype dtype, const void *x, long long x
     a.err = h->base.flags.err;
     a.mt1 = div_up(c.outputs, 128);
     a.kc1 = div_up(c.inputs, 128);
+    a.mt2 = a.kc2 = 1;  // there is no second product
     a.group1 = a.group2 = c.weight.group;
     a.zeros1 = a.zeros2 = c.weight.has_zeros != 0;
     a.tile1 = a.tile2 = moe::int4_tile_bytes(c.weight.group, a.zeros1);

@@ -14,8 +14,7 @@
 // tile's write and read at this rate. Scales are applied to sums, not to
 // weights: each group's sum is an accumulator of its own, and two more
 // warpgroups add s times it to fp32 registers. So no weight is rounded.
-#include "moe_device.h"
-#include "moe_internal.h"
+#include "moe_sched.h"
 
 namespace moe {
 
@@ -40,29 +39,6 @@ struct Shared {
     int issued_a, issued_b;
     int last, reset;
 };
-
-struct Lists {
-    unsigned long long *mask;
-    float *weight;
-    unsigned short *expert, *offset;
-    unsigned char *token;
-};
-
-static __device__ __forceinline__ int div_up(int a, int b) { return (a + b - 1) / b; }
-
-static __device__ __forceinline__ void split(float v, __nv_bfloat16 &hi, __nv_bfloat16 &lo)
-{
-    hi = __float2bfloat16_rn(v);
-    const float r = v - __bfloat162float(hi);
-    lo = __float2bfloat16_rn(isfinite(r) ? r : 0.0f);
-}
-
-static __device__ __forceinline__ float swiglu(float gate, float up) { return gate / (1.0f + expf(-gate)) * up; }
-
-static __device__ __forceinline__ int part_slot(int total, int b, int G, int begin)
-{
-    return 2 * b + (begin <= share_begin(total, b, G) ? 0 : 1);
-}
 
 // Eight codes to four pairs q - z. Code 2p is at bits 4p, code 2p + 1 at bits
 // 4p + 16, so a shift and a mask leave a pair; or-ing the exponent of 128
@@ -99,12 +75,7 @@ __global__ void __launch_bounds__(kThreads, 1) int4_kernel(const __grid_constant
     uint8_t *const ring_a_p = dyn + (ring_a - dyn0);
     const int T8 = (a.T + 7) & ~7;
     float *const acc = reinterpret_cast<float *>(ring_a_p + a.stages * a.stage_a);
-    Lists li;
-    li.mask = reinterpret_cast<unsigned long long *>(acc + (LINEAR ? 0 : T8 * kTileRows));
-    li.weight = reinterpret_cast<float *>(li.mask + a.E);
-    li.expert = reinterpret_cast<unsigned short *>(li.weight + a.P);
-    li.offset = li.expert + a.E;
-    li.token = reinterpret_cast<unsigned char *>(li.offset + a.E + 1);
+    const Lists li(acc + (LINEAR ? 0 : T8 * kTileRows), a.E, a.P);
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int G = gridDim.x, blk = blockIdx.x;
@@ -146,59 +117,7 @@ __global__ void __launch_bounds__(kThreads, 1) int4_kernel(const __grid_constant
             sh.nmax = a.T;
         }
     } else {
-        for (int e = tid; e < a.E; e += kThreads)
-            li.mask[e] = 0;
-        __syncthreads();
-        for (int i = tid; i < a.P; i += kThreads) {
-            if (!EP_IN_BOUNDS(a.chk, epk::kSiteMoeIds, a.ids + i, 4, a.ids, 4LL * a.P))
-                continue;
-            const int e = a.ids[i] - a.first;
-            if (e >= 0 && e < a.E)
-                atomicOr(&li.mask[e], 1ULL << (i / a.K));
-        }
-        __syncthreads();
-        if (warp == 0) {
-            int n_active = 0, n_pairs = 0, nmax = 0;
-            for (int e0 = 0; e0 < a.E; e0 += 32) {
-                const int e = e0 + lane;
-                const int n = e < a.E ? __popcll(li.mask[e]) : 0;
-                const unsigned live = __ballot_sync(~0u, n > 0);
-                int sum = n;
-                for (int d = 1; d < 32; d <<= 1) {
-                    const int v = __shfl_up_sync(~0u, sum, d);
-                    if (lane >= d)
-                        sum += v;
-                }
-                if (n > 0) {
-                    const int at = n_active + __popc(live & ((1u << lane) - 1));
-                    li.expert[at] = static_cast<unsigned short>(e);
-                    li.offset[at] = static_cast<unsigned short>(n_pairs + sum - n);
-                }
-                n_active += __popc(live);
-                n_pairs += __shfl_sync(~0u, sum, 31);
-                nmax = max(nmax, __reduce_max_sync(~0u, n));
-            }
-            if (lane == 0) {
-                li.offset[n_active] = static_cast<unsigned short>(n_pairs);
-                sh.active = n_active;
-                sh.nmax = nmax;
-            }
-        }
-        __syncthreads();
-        for (int i = tid; i < sh.active; i += kThreads) {
-            const int e = li.expert[i];
-            int at = li.offset[i];
-            for (unsigned long long m = li.mask[e]; m; m &= m - 1, ++at) {
-                const int t = __ffsll(static_cast<long long>(m)) - 1;
-                float w = 0.0f;
-                for (int k = 0; k < a.K; ++k)
-                    if (a.ids[t * a.K + k] - a.first == e &&
-                        EP_IN_BOUNDS(a.chk, epk::kSiteMoeWeights, a.weights + t * a.K + k, 4, a.weights, 4LL * a.P))
-                        w += a.weights[t * a.K + k];
-                li.token[at] = static_cast<unsigned char>(t);
-                li.weight[at] = w;
-            }
-        }
+        build_lists(a, li, sh, tid, kThreads);
     }
     tc_fence_before();
     __syncthreads();
@@ -207,13 +126,7 @@ __global__ void __launch_bounds__(kThreads, 1) int4_kernel(const __grid_constant
     const int A = sh.active;
 
     if (A == 0) {
-        for (long long i = static_cast<long long>(blk) * kThreads + tid; i < static_cast<long long>(a.T) * a.H;
-             i += static_cast<long long>(G) * kThreads) {
-            const long long t = i / a.H;
-            uint16_t *const p = static_cast<uint16_t *>(a.out) + t * a.out_stride + (i - t * a.H);
-            if (EP_IN_BOUNDS(a.chk, epk::kSiteMoeOut, p, 2, a.out, 2 * ((a.T - 1) * a.out_stride + a.H)))
-                *p = 0;
-        }
+        clear_out(a, blk, G, tid, kThreads);
         __syncthreads();
         if (warp == 1)
             tmem_free(tmem, 512);
@@ -227,141 +140,126 @@ __global__ void __launch_bounds__(kThreads, 1) int4_kernel(const __grid_constant
     const int begin1 = share_begin(total1, min(blk, G1), G1), end1 = share_begin(total1, min(blk + 1, G1), G1);
     const int begin2 = LINEAR ? 0 : share_begin(total2, min(blk, G2), G2);
     const int end2 = LINEAR ? 0 : share_begin(total2, min(blk + 1, G2), G2);
-    const int width = LINEAR ? div_up(sh.nmax, 16) * 16 : div_up(sh.nmax, 8) * 16;  // rows of a token tile, columns of a sum
+    const int width = LINEAR ? ceil_div(sh.nmax, 16) * 16 : ceil_div(sh.nmax, 8) * 16;  // rows of a token tile, columns of a sum
     const int stage_b = width * 256;  // two 64-input halves
     const int stages_b = min(kMaxStagesB, a.bytes_b / stage_b);
     const int sums = min(kMaxSums, 256 / width);
-    const int groups1 = 128 / a.group1, groups2 = 128 / a.group2;
+    const int groups1 = 4 >> a.shift1, groups2 = 4 >> a.shift2;
 
     if (warp == 0 && lane == 0) {
         // ---- weight tiles ----
         const uint64_t policy = policy_evict_first();
-        int it = 0;
+        Cursor at;
+        int issued = 0;
         bool run = true;
         auto load = [&](const uint8_t *src, uint32_t bytes) {
-            const int s = it % a.stages;
-            if (!mbar_wait(smem_u32(&sh.empty_a[s]), ((it / a.stages) & 1) ^ 1, abort, kWaitEmptyA))
+            if (!mbar_wait(smem_u32(&sh.empty_a[at.s]), at.parity ^ 1, abort, kWaitEmptyA))
                 return false;
-            const uint32_t bar = smem_u32(&sh.full_a[s]);
+            const uint32_t bar = smem_u32(&sh.full_a[at.s]);
             mbar_expect(bar, bytes);
-            bulk_load(ring_a + s * a.stage_a, src, bytes, bar, policy);
-            ++it;
+            bulk_load(ring_a + at.s * a.stage_a, src, bytes, bar, policy);
+            at.next(a.stages);
+            ++issued;
             return true;
         };
-        for (int u = begin1; run && u < end1; ++u) {
-            const int tile = u / a.kc1, kc = u - tile * a.kc1;
-            const int i = tile / a.mt1, m = tile - i * a.mt1;
-            for (int g = 0; run && g < kParts; ++g) {
-                const size_t mat = static_cast<size_t>(li.expert[i]) * kParts + g;
-                run = load(a.w1 + ((mat * a.mt1 + m) * a.kc1 + kc) * a.tile1, a.tile1);
-            }
+        const size_t up = static_cast<size_t>(a.mt1) * a.kc1 * a.tile1;  // from a gate tile to its up tile
+        for (Walk w(begin1, end1, a.kc1, a.mt1, false); run && w.more(); w.next()) {
+            const uint8_t *src =
+                a.w1 + ((static_cast<size_t>(li.expert[w.i]) * kParts * a.mt1 + w.m) * a.kc1 + w.k) * a.tile1;
+            for (int k = 0; run && k < w.len; ++k, src += a.tile1)
+                run = load(src, a.tile1) && (LINEAR || load(src + up, a.tile1));
         }
-        for (int u = begin2; run && u < end2; ++u) {
-            const int tile = u / a.kc2, kc = u - tile * a.kc2;
-            const int m = tile / A;
-            const size_t mat = li.expert[tile - m * A];
-            run = load(a.w2 + ((mat * a.mt2 + m) * a.kc2 + kc) * a.tile2, a.tile2);
+        for (Walk w(begin2, end2, a.kc2, A, true); run && w.more(); w.next()) {
+            const uint8_t *src = a.w2 + ((static_cast<size_t>(li.expert[w.i]) * a.mt2 + w.m) * a.kc2 + w.k) * a.tile2;
+            for (int k = 0; run && k < w.len; ++k, src += a.tile2)
+                run = load(src, a.tile2);
         }
-        sh.issued_a = it;
+        sh.issued_a = issued;
     } else if (warp == 2 && lane == 0) {
         // ---- token tiles ----
-        int it = 0;
+        Cursor at;
+        int issued = 0;
         bool run = true;
-        auto acquire = [&](uint32_t bytes, uint32_t &dst, uint32_t &bar) {
-            const int s = it % stages_b;
-            if (!mbar_wait(smem_u32(&sh.empty_b[s]), ((it / stages_b) & 1) ^ 1, abort, kWaitEmptyB))
+        uint32_t dst = 0, bar = 0;
+        const uint32_t half = width * 128;  // from the tile's first 64 inputs to the others
+        auto acquire = [&](uint32_t bytes) {
+            if (!mbar_wait(smem_u32(&sh.empty_b[at.s]), at.parity ^ 1, abort, kWaitEmptyB))
                 return false;
-            bar = smem_u32(&sh.full_b[s]);
-            dst = ring_b + s * stage_b;
+            bar = smem_u32(&sh.full_b[at.s]);
+            dst = ring_b + at.s * stage_b;
             mbar_expect(bar, bytes);
-            ++it;
+            at.next(stages_b);
+            ++issued;
             return true;
         };
-        for (int u = begin1; run && u < end1; ++u) {
-            const int tile = u / a.kc1, kc = u - tile * a.kc1, i = tile / a.mt1;
-            const int off = li.offset[i], n = li.offset[i + 1] - off;
-            uint32_t dst, bar;
-            if (LINEAR) {
-                const int n8 = div_up(n, 8);
-                run = acquire(n8 * 2048, dst, bar);
-                for (int b = 0; run && b < n8; ++b)
-                    for (int half = 0; half < 2; ++half)
-                        tma_load_2d(dst + half * width * 128 + b * 1024, &a.mx, bar, kc * 128 + half * 64, b * 8);
-            } else {
-                const int quads = div_up(n, 4);
-                run = acquire(quads * 1024, dst, bar);
-                for (int q = 0; run && q < quads; ++q) {
-                    const int j = 4 * q, l = n - 1;
-                    const int r0 = li.token[off + j], r1 = li.token[off + min(j + 1, l)];
-                    const int r2 = li.token[off + min(j + 2, l)], r3 = li.token[off + min(j + 3, l)];
-                    for (int half = 0; half < 2; ++half)
-                        tma_gather4(dst + half * width * 128 + q * 512, &a.mx, bar, kc * 128 + half * 64, r0, r1, r2, r3);
-                }
+        for (Walk w(begin1, end1, a.kc1, a.mt1, false); run && w.more(); w.next()) {
+            const int n = li.count(w.i);
+            const unsigned char *const tok = li.token + li.offset[w.i];
+            const uint32_t bytes = LINEAR ? ceil_div(n, 8) * 2048 : ceil_div(n, 4) * 1024;
+            for (int k = w.k; k < w.k + w.len && (run = acquire(bytes)); ++k) {
+                if (LINEAR)
+                    for (int j = 0; j < n; j += 8) {
+                        tma_load_2d(dst + j * 128, &a.mx, bar, k * 128, j);
+                        tma_load_2d(dst + half + j * 128, &a.mx, bar, k * 128 + 64, j);
+                    }
+                else
+                    for (int j = 0; j < n; j += 4) {  // short of a fourth row: the last one again
+                        const int r0 = tok[j], r1 = tok[min(j + 1, n - 1)], r2 = tok[min(j + 2, n - 1)],
+                                  r3 = tok[min(j + 3, n - 1)];
+                        tma_gather4(dst + j * 128, &a.mx, bar, k * 128, r0, r1, r2, r3);
+                        tma_gather4(dst + half + j * 128, &a.mx, bar, k * 128 + 64, r0, r1, r2, r3);
+                    }
             }
         }
-        if (run && begin2 < end2) {
-            const unsigned long long t0 = now_ns();
-            while (ld_acquire(a.done) < A * a.mt1) {
-                if (*abort || now_ns() - t0 > kWaitNs) {
-                    *abort = *abort ? *abort : kWaitDone;
-                    run = false;
-                    break;
-                }
-            }
-            fence_async_proxy();
-        }
-        for (int u = begin2; run && u < end2; ++u) {
-            const int tile = u / a.kc2, kc = u - tile * a.kc2, i = tile % A;
-            const int off = li.offset[i], n8 = div_up(li.offset[i + 1] - off, 8);
-            uint32_t dst, bar;
-            run = acquire(n8 * 4096, dst, bar);
-            for (int b = 0; run && b < n8; ++b)
-                for (int half = 0; half < 2; ++half) {
-                    const uint32_t to = dst + half * width * 128;
-                    tma_load_2d(to + b * 1024, &a.mh, bar, kc * 128 + half * 64, off + b * 8);
-                    tma_load_2d(to + (n8 + b) * 1024, &a.mh, bar, kc * 128 + half * 64, a.P + off + b * 8);
+        if (run && begin2 < end2)
+            run = wait_products(a, A * a.mt1, abort);
+        for (Walk w(begin2, end2, a.kc2, A, true); run && w.more(); w.next()) {
+            const int off = li.offset[w.i], n8 = ceil_div(li.count(w.i), 8);
+            for (int k = w.k; k < w.k + w.len && (run = acquire(n8 * 4096)); ++k)
+                for (int b = 0; b < n8; ++b) {
+                    const int x = k * 128, r = off + b * 8;
+                    tma_load_2d(dst + b * 1024, &a.mh, bar, x, r);
+                    tma_load_2d(dst + (n8 + b) * 1024, &a.mh, bar, x, a.P + r);
+                    tma_load_2d(dst + half + b * 1024, &a.mh, bar, x + 64, r);
+                    tma_load_2d(dst + half + (n8 + b) * 1024, &a.mh, bar, x + 64, a.P + r);
                 }
         }
-        sh.issued_b = it;
+        sh.issued_b = issued;
     } else if (warp == 1 && lane == 0) {
         // ---- matrix instructions ----
-        int it_t = 0, it_b = 0, it_d = 0;
+        Cursor at_t, at_b, at_d;
         bool run = true;
         for (int product = 0; run && product < 2; ++product) {
-            const int kc_n = product ? a.kc2 : a.kc1, end = product ? end2 : end1;
             const int parts = product ? 1 : kParts, groups = product ? groups2 : groups1, steps = 8 / groups;
-            for (int u = product ? begin2 : begin1; run && u < end; ++u) {
-                const int tile = u / kc_n;
-                const int i = product ? tile % A : tile / a.mt1;
-                const int n = li.offset[i + 1] - li.offset[i];
-                const int N = product ? div_up(n, 8) * 16 : div_up(n, 16) * 16;
+            for (Walk w(product ? begin2 : begin1, product ? end2 : end1, product ? a.kc2 : a.kc1,
+                        product ? A : a.mt1, product != 0);
+                 run && w.more(); w.next()) {
+                const int n = li.count(w.i);
+                const int N = product ? ceil_div(n, 8) * 16 : ceil_div(n, 16) * 16;
                 const uint32_t idesc = idesc_f16(kTileRows, N, BF16);
-                const int sb = it_b % stages_b;
-                run = mbar_wait(smem_u32(&sh.full_b[sb]), (it_b / stages_b) & 1, abort, kWaitFullB);
-                const uint32_t b0 = ring_b + sb * stage_b;
-                for (int g = 0; run && g < parts; ++g) {
-                    const int t = it_t % kTmemA;
-                    run = mbar_wait(smem_u32(&sh.full_t[t]), (it_t / kTmemA) & 1, abort, kWaitFullA);
-                    for (int q = 0; run && q < groups; ++q) {
-                        const int s = it_d % sums;
-                        run = mbar_wait(smem_u32(&sh.empty_d[s]), ((it_d / sums) & 1) ^ 1, abort, kWaitEmptyD);
-                        if (!run)
-                            break;
-                        tc_fence_after();
-                        for (int c = 0; c < steps; ++c) {
-                            const int k16 = q * steps + c;  // sixteenths of inputs within the tile
-                            const uint32_t b = b0 + (k16 >> 2) * width * 128;
-                            mma_ts(tmem + 256 + s * width, tmem + t * 64 + k16 * 8, desc_sw128(b) + 2 * (k16 & 3), idesc,
-                                   c > 0);
+                for (int k = 0; run && k < w.len; ++k) {
+                    run = mbar_wait(smem_u32(&sh.full_b[at_b.s]), at_b.parity, abort, kWaitFullB);
+                    const uint64_t db = desc_sw128(ring_b + at_b.s * stage_b);
+                    for (int g = 0; run && g < parts; ++g) {
+                        run = mbar_wait(smem_u32(&sh.full_t[at_t.s]), at_t.parity, abort, kWaitFullA);
+                        int k16 = 0;  // sixteenths of inputs within the tile
+                        for (int q = 0; run && q < groups; ++q) {
+                            run = mbar_wait(smem_u32(&sh.empty_d[at_d.s]), at_d.parity ^ 1, abort, kWaitEmptyD);
+                            if (!run)
+                                break;
+                            tc_fence_after();
+                            for (int c = 0; c < steps; ++c, ++k16)
+                                mma_ts(tmem + 256 + at_d.s * width, tmem + at_t.s * 64 + k16 * 8,
+                                       db + (k16 >> 2) * (width * 8) + 2 * (k16 & 3), idesc, c > 0);
+                            tc_commit(smem_u32(&sh.full_d[at_d.s]));
+                            at_d.next(sums);
                         }
-                        tc_commit(smem_u32(&sh.full_d[s]));
-                        ++it_d;
+                        tc_commit(smem_u32(&sh.empty_t[at_t.s]));
+                        at_t.next(kTmemA);
                     }
-                    tc_commit(smem_u32(&sh.empty_t[t]));
-                    ++it_t;
+                    tc_commit(smem_u32(&sh.empty_b[at_b.s]));
+                    at_b.next(stages_b);
                 }
-                tc_commit(smem_u32(&sh.empty_b[sb]));
-                ++it_b;
             }
         }
         tc_commit(smem_u32(&sh.drain));
@@ -371,24 +269,33 @@ __global__ void __launch_bounds__(kThreads, 1) int4_kernel(const __grid_constant
         const int wg = (warp - 4) >> 2, row = tid & 127;
         const uint32_t lanes = tmem + (static_cast<uint32_t>(warp & 3) << 21);
         const int tiles1 = (end1 - begin1) * kParts, tiles = tiles1 + (end2 - begin2);
+        Cursor at_a, at_t;
         bool run = true;
+        if (wg) {
+            at_a.next(a.stages);
+            at_t.next(kTmemA);
+        }
         for (int it = wg; run && it < tiles; it += 2) {
             const bool second = it >= tiles1;
-            const int group = second ? a.group2 : a.group1, groups = 128 / group;
+            const int shift = second ? a.shift2 : a.shift1;  // log2 of the group in 32 inputs
             const bool zeros = second ? a.zeros2 : a.zeros1;
-            const int s = it % a.stages, t = it % kTmemA;
-            run = mbar_wait(smem_u32(&sh.full_a[s]), (it / a.stages) & 1, abort, kWaitFullA) &&
-                  mbar_wait(smem_u32(&sh.empty_t[t]), ((it / kTmemA) & 1) ^ 1, abort, kWaitEmptyA);
+            const int s = at_a.s, t = at_t.s;
+            run = mbar_wait(smem_u32(&sh.full_a[s]), at_a.parity, abort, kWaitFullA) &&
+                  mbar_wait(smem_u32(&sh.empty_t[t]), at_t.parity ^ 1, abort, kWaitEmptyA);
+            at_a.next(a.stages);
+            at_a.next(a.stages);
+            at_t.next(kTmemA);
+            at_t.next(kTmemA);
             run = __all_sync(~0u, run);
             if (!run)
                 break;
             tc_fence_after();
             const uint8_t *const tile = ring_a_p + s * a.stage_a;
-            const uint8_t *const zp = tile + 8192 + groups * 256;
+            const uint8_t *const zp = tile + 8192 + (1024 >> shift) + row;
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
                 const uint4 w = *reinterpret_cast<const uint4 *>(tile + q * 2048 + row * 16);
-                const uint32_t z = zeros ? zp[(q * 32 / group) * 128 + row] : 8;
+                const uint32_t z = zeros ? zp[(q >> shift) * 128] : 8;
                 const uint32_t zz = (BF16 ? 0x43004300u : 0x64006400u) + z * 0x10001u;
                 uint32_t r[16];
                 decode<BF16>(w.x, zz, r);
@@ -409,7 +316,7 @@ __global__ void __launch_bounds__(kThreads, 1) int4_kernel(const __grid_constant
         // ---- scales and results; the two warpgroups share the columns ----
         const int wg = (warp - 12) >> 2, row = tid & 127, rtid = tid - 384;
         const uint32_t lanes = tmem + 256 + (static_cast<uint32_t>(warp & 3) << 21);
-        int it_a = 0, it_d = 0;
+        Cursor at_a, at_d;
         bool run = true;
         float v[2][32];  // sums of this thread's row: gate and up (or the one product), up to 32 columns
 
@@ -427,12 +334,11 @@ __global__ void __launch_bounds__(kThreads, 1) int4_kernel(const __grid_constant
         // Adds s times the sum of each group of one weight tile to v[p], columns [c0, c0 + 8 nb) of the sum and,
         // where lo > 0, those `lo` further.
         auto add_tile = [&](float *p, int groups, int c0, int nb, int lo) {
-            const int st = it_a % a.stages;
-            run = run && mbar_wait(smem_u32(&sh.full_a[st]), (it_a / a.stages) & 1, abort, kWaitFullA);
-            const uint8_t *const sc = ring_a_p + st * a.stage_a + 8192;
+            run = run && mbar_wait(smem_u32(&sh.full_a[at_a.s]), at_a.parity, abort, kWaitFullA);
+            const uint8_t *const sc = ring_a_p + at_a.s * a.stage_a + 8192;
             for (int q = 0; q < groups; ++q) {
-                const int d = it_d % sums;
-                run = run && mbar_wait(smem_u32(&sh.full_d[d]), (it_d / sums) & 1, abort, kWaitFullD);
+                const int d = at_d.s;
+                run = run && mbar_wait(smem_u32(&sh.full_d[d]), at_d.parity, abort, kWaitFullD);
                 run = __all_sync(~0u, run);
                 if (!run)
                     return;
@@ -456,27 +362,25 @@ __global__ void __launch_bounds__(kThreads, 1) int4_kernel(const __grid_constant
                 __syncwarp();
                 if (lane == 0)
                     mbar_arrive(smem_u32(&sh.empty_d[d]));
-                ++it_d;
+                at_d.next(sums);
             }
             __syncwarp();
             if (lane == 0)
-                mbar_arrive(smem_u32(&sh.empty_a[st]));
-            ++it_a;
+                mbar_arrive(smem_u32(&sh.empty_a[at_a.s]));
+            at_a.next(a.stages);
         };
 
-        for (int u = begin1; run && u < end1;) {
-            const int tile = u / a.kc1, k0 = u - tile * a.kc1, k1 = min(a.kc1, k0 + end1 - u);
-            const int i = tile / a.mt1, m = tile - i * a.mt1;
-            const int off = li.offset[i], n = li.offset[i + 1] - off;
-            const int blocks = div_up(n, 8), half = div_up(blocks, 2);  // columns by eights: this warpgroup's
+        for (Walk w(begin1, end1, a.kc1, a.mt1, false); run && w.more(); w.next()) {
+            const int off = li.offset[w.i], n = li.count(w.i), tile = w.i * a.mt1 + w.m;
+            const int blocks = ceil_div(n, 8), half = ceil_div(blocks, 2);  // columns by eights: this warpgroup's
             const int c0 = wg ? half * 8 : 0, nb = wg ? blocks - half : half, n8 = blocks * 8;
             const int first_unit = tile * a.kc1;
             const int b0 = share_owner(total1, first_unit, G1), b1 = share_owner(total1, first_unit + a.kc1 - 1, G1);
-            const int col = m * kTileRows + row;
+            const int col = w.m * kTileRows + row;
 #pragma unroll
             for (int c = 0; c < 32; ++c)
                 v[0][c] = v[1][c] = 0.0f;
-            for (int k = k0; run && k < k1; ++k) {
+            for (int k = 0; run && k < w.len; ++k) {
                 add_tile(v[0], groups1, c0, nb, 0);
                 if (!LINEAR)
                     add_tile(v[1], groups1, c0, nb, 0);
@@ -519,7 +423,7 @@ __global__ void __launch_bounds__(kThreads, 1) int4_kernel(const __grid_constant
                 if (arrive_last(a.tiles + tile, b1 - b0 + 1)) {
                     mine = true;
                     for (int j = c0; j < c0 + nb * 8; j += 8) {
-                        float g[8] = {}, w[8] = {};
+                        float g[8] = {}, r[8] = {};
                         for (int b = b0; b <= b1; ++b) {
                             const float *const p =
                                 a.part + static_cast<size_t>(part_slot(total1, b, G1, first_unit)) * a.part_floats;
@@ -527,12 +431,12 @@ __global__ void __launch_bounds__(kThreads, 1) int4_kernel(const __grid_constant
                             for (int c = 0; c < 8; ++c) {
                                 g[c] += __ldcg(p + (j + c) * kTileRows + row);
                                 if (!LINEAR)
-                                    w[c] += __ldcg(p + (n8 + j + c) * kTileRows + row);
+                                    r[c] += __ldcg(p + (n8 + j + c) * kTileRows + row);
                             }
                         }
 #pragma unroll
                         for (int c = 0; c < 8; ++c)
-                            result(j + c, g[c], w[c]);
+                            result(j + c, g[c], r[c]);
                     }
                 }
             }
@@ -543,24 +447,22 @@ __global__ void __launch_bounds__(kThreads, 1) int4_kernel(const __grid_constant
                 if (rtid == 0)
                     add_acq_rel(a.done);
             }
-            u += k1 - k0;
         }
 
         const int group = LINEAR ? 1 : A * a.kc2;
-        for (int u = begin2; !LINEAR && run && u < end2;) {
-            const int m = u / group, stop = min(end2, (m + 1) * group), first_unit = m * group;
+        for (Walk w(begin2, end2, a.kc2, A, true); !LINEAR && run && w.more();) {
+            const int m = w.m, first_unit = m * group;
             const int b0 = share_owner(total2, first_unit, G2), b1 = share_owner(total2, first_unit + group - 1, G2);
             for (int t = wg; t < T8; t += 2)
                 acc[t * kTileRows + row] = 0.0f;
-            while (run && u < stop) {
-                const int tile = u / a.kc2, k0 = u - tile * a.kc2, k1 = min(a.kc2, k0 + stop - u);
-                const int i = tile - m * A, off = li.offset[i], n = li.offset[i + 1] - off;
-                const int blocks = div_up(n, 8), half = div_up(blocks, 2);
+            for (; run && w.more() && w.m == m; w.next()) {
+                const int off = li.offset[w.i], n = li.count(w.i);
+                const int blocks = ceil_div(n, 8), half = ceil_div(blocks, 2);
                 const int c0 = wg ? half * 8 : 0, nb = wg ? blocks - half : half;
 #pragma unroll
                 for (int c = 0; c < 32; ++c)
                     v[0][c] = 0.0f;
-                for (int k = k0; run && k < k1; ++k)
+                for (int k = 0; run && k < w.len; ++k)
                     add_tile(v[0], groups2, c0, nb, blocks * 8);
                 // also: the other warpgroup's rows of acc for the experts before are written
                 run = named_all(2, kResults, run);
@@ -572,7 +474,6 @@ __global__ void __launch_bounds__(kThreads, 1) int4_kernel(const __grid_constant
                         float *const s = acc + li.token[off + c0 + c] * kTileRows + row;
                         *s = fmaf(li.weight[off + c0 + c], v[0][c], *s);
                     }
-                u += k1 - k0;
             }
             run = named_all(2, kResults, run);
             if (!run)
@@ -702,10 +603,10 @@ size_t int4_part_floats(int T, bool linear)
 size_t int4_smem(Int4Args *a, bool linear)
 {
     const int T8 = (a->T + 7) & ~7;
-    size_t lists = (linear ? 0 : static_cast<size_t>(T8) * kTileRows * 4) + static_cast<size_t>(a->E) * 8 +
-                   static_cast<size_t>(a->P) * 4 + static_cast<size_t>(a->E) * 2 + static_cast<size_t>(a->E + 1) * 2 +
-                   static_cast<size_t>(a->P);
+    const size_t lists = (linear ? 0 : static_cast<size_t>(T8) * kTileRows * 4) + lists_bytes(a->E, a->P);
     a->bytes_b = T8 <= 8 ? 32 * 1024 : 64 * 1024;  // at least 2 stages of the largest token tile
+    a->shift1 = a->group1 == 32 ? 0 : a->group1 == 64 ? 1 : 2;
+    a->shift2 = a->group2 == 32 ? 0 : a->group2 == 64 ? 1 : 2;
     a->stage_a = a->tile1 > a->tile2 ? a->tile1 : a->tile2;
     a->part_floats = static_cast<int>(int4_part_floats(a->T, linear));
     const size_t room = kSmemMax - sizeof(Shared) - 1024 - lists - a->bytes_b - 64;

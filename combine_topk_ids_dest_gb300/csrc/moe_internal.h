@@ -100,7 +100,8 @@ struct Int4Args {
     int T, K, P, E, first;
     int H, I;  // linear: inputs, outputs
     int mt1, kc1, mt2, kc2;
-    int group1, group2, zeros1, zeros2, tile1, tile2, scale_fp16;
+    int group1, group2, shift1, shift2;  // shift: log2(group / 32)
+    int zeros1, zeros2, tile1, tile2, scale_fp16;
     int h_stride;
     int stages, stage_a, bytes_b, part_floats;
     epk::CheckCtx chk;
