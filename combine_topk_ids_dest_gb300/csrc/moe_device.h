@@ -23,6 +23,17 @@ static __device__ __forceinline__ uint32_t smem_u32(const void *p)
     return static_cast<uint32_t>(__cvta_generic_to_shared(p));
 }
 
+// True in one lane of a converged warp, the same one each time. The compiler
+// knows what elect.sync does: tcgen05 and TMA instructions under it are issued
+// with uniform registers at 36 to 55 cycles an MMA, against 190 under a test
+// of the lane's number.
+static __device__ __forceinline__ bool elect_one()
+{
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\tselp.u32 %0, 1, 0, e;\n\t}" : "=r"(p));
+    return p != 0;
+}
+
 static __device__ __forceinline__ unsigned long long now_ns()
 {
     unsigned long long t;
@@ -226,12 +237,30 @@ static __device__ __forceinline__ int ld_acquire(const int *p)
     return v;
 }
 
-// Adds 1 with release/acquire order and returns the old value.
-static __device__ __forceinline__ int add_acq_rel(int *p)
+// Adds n with release/acquire order and returns the old value. After a block
+// barrier it publishes what every thread of the barrier wrote.
+static __device__ __forceinline__ int add_acq_rel(int *p, int n)
 {
     int v;
-    asm volatile("atom.acq_rel.gpu.global.add.s32 %0, [%1], 1;" : "=r"(v) : "l"(p) : "memory");
+    asm volatile("atom.acq_rel.gpu.global.add.s32 %0, [%1], %2;" : "=r"(v) : "l"(p), "r"(n) : "memory");
     return v;
+}
+
+// Waits until *p has reached `target`.
+static __device__ __forceinline__ bool wait_count(const int *p, int target, volatile int *abort, int site)
+{
+    if (ld_acquire(p) >= target)
+        return true;
+    const unsigned long long t0 = now_ns();
+    while (ld_acquire(p) < target) {
+        if (*abort)
+            return false;
+        if (now_ns() - t0 > kWaitNs) {
+            *abort = site;
+            return false;
+        }
+    }
+    return true;
 }
 
 static __device__ __forceinline__ void named_sync(int id, int threads)

@@ -14,9 +14,9 @@
 //    tensor memory.
 //  - The work is cut evenly over the blocks in chunks of 64 inputs, wherever
 //    row tiles begin and end: 8 experts' tiles divide 152 SMs badly, their
-//    chunks do not. A tile that is shared by several blocks is written as
-//    fp32 parts; the block whose part arrives last adds them up in order of
-//    the inputs, so results do not depend on who is last.
+//    chunks do not. A tile that several blocks share is written as fp32
+//    parts; after their last chunk each of them adds up the parts of some of
+//    its columns, in the order of the inputs: results do not depend on timing.
 //  - The second product's weights do not depend on the first's result, so the
 //    ring runs on into them: while h is finished and its last tile announced,
 //    the ring (up to 192 KB per SM) already fills with W2.
@@ -46,7 +46,8 @@ struct Shared {
     int abort;
     int active, nmax;   // experts that any token chose; the most tokens of one
     int issued_a, issued_b;
-    int last, reset;
+    int reset;
+    Rests rests[2];  // of the two products
 };
 
 __global__ void __launch_bounds__(kThreads, 1) experts_kernel(const __grid_constant__ ExpertsArgs a)
@@ -61,12 +62,12 @@ __global__ void __launch_bounds__(kThreads, 1) experts_kernel(const __grid_const
     float *const acc = reinterpret_cast<float *>(after);
     const Lists li(acc + T8 * kTileRows, a.E, a.P);
 
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int tid = threadIdx.x, warp = __shfl_sync(~0u, tid >> 5, 0);
     const int G = gridDim.x, blk = blockIdx.x;
     volatile int *const abort = &sh.abort;
 
     if (tid == 0) {
-        sh.abort = sh.reset = sh.issued_a = sh.issued_b = 0;
+        sh.abort = sh.reset = sh.rests[0].n = sh.rests[1].n = sh.issued_a = sh.issued_b = 0;
         for (int i = 0; i < kMaxStagesA; ++i) {
             mbar_init(smem_u32(&sh.full_a[i]), 1);
             mbar_init(smem_u32(&sh.empty_a[i]), 1);
@@ -104,14 +105,14 @@ __global__ void __launch_bounds__(kThreads, 1) experts_kernel(const __grid_const
     }
 
     const int total1 = A * a.mt1 * a.kc1, total2 = A * a.mt2 * a.kc2;
-    // no more shares than units: then every block of a run of blocks has a part in the tile they share
-    const int G1 = min(G, total1), G2 = min(G, total2);
-    const int begin1 = share_begin(total1, min(blk, G1), G1), end1 = share_begin(total1, min(blk + 1, G1), G1);
-    const int begin2 = share_begin(total2, min(blk, G2), G2), end2 = share_begin(total2, min(blk + 1, G2), G2);
+    const Shares shares1(total1, G), shares2(total2, G);
+    const int begin1 = shares1.begin(blk), end1 = shares1.begin(blk + 1);
+    const int begin2 = shares2.begin(blk), end2 = shares2.begin(blk + 1);
+    const int pairs = li.offset[A];
     const int stage_b = ceil_div(sh.nmax, 8) * 16 * 128;  // 8 tokens: up to 16 rows of 128 bytes
     const int stages_b = min(kMaxStagesB, a.bytes_b / stage_b);
 
-    if (warp == 0 && lane == 0) {
+    if (warp == 0 && elect_one()) {
         // ---- weight tiles ----
         const uint64_t policy = policy_evict_first();
         Cursor at;
@@ -139,7 +140,7 @@ __global__ void __launch_bounds__(kThreads, 1) experts_kernel(const __grid_const
                 run = load(&a.mw2, k * kChunk, w.m * kTileRows, e);
         }
         sh.issued_a = issued;
-    } else if (warp == 2 && lane == 0) {
+    } else if (warp == 2 && elect_one()) {
         // ---- token tiles ----
         Cursor at;
         int issued = 0;
@@ -163,8 +164,10 @@ __global__ void __launch_bounds__(kThreads, 1) experts_kernel(const __grid_const
                     tma_gather4(dst + j * 128, &a.mx, bar, k * kChunk, tok[j], tok[min(j + 1, n - 1)],
                                 tok[min(j + 2, n - 1)], tok[min(j + 3, n - 1)]);
         }
-        if (run && begin2 < end2)  // h is complete when every tile of the first product is
-            run = wait_products(a, A * a.mt1, abort);
+        if (run && begin2 < end2) {  // h is complete
+            run = wait_count(a.done, a.mt1 * pairs, abort, kWaitDone);
+            fence_async_proxy();
+        }
         for (Walk w(begin2, end2, a.kc2, A, true); run && w.more(); w.next()) {
             const int off = li.offset[w.i], n8 = ceil_div(li.count(w.i), 8);
             for (int k = w.k; k < w.k + w.len && (run = acquire(n8 * 2048)); ++k)
@@ -174,7 +177,7 @@ __global__ void __launch_bounds__(kThreads, 1) experts_kernel(const __grid_const
                 }
         }
         sh.issued_b = issued;
-    } else if (warp == 1 && lane == 0) {
+    } else if (warp == 1 && elect_one()) {
         // ---- matrix instructions ----
         Cursor at_a, at_b, at_d;
         bool run = true;
@@ -220,39 +223,42 @@ __global__ void __launch_bounds__(kThreads, 1) experts_kernel(const __grid_const
         Cursor at_d;
         bool run = true;
 
-        // Counts this block's part of a tile; true in the block whose part was the last.
-        auto arrive_last = [&](int *counter, int parts) {
-            __threadfence();
+        auto leave = [&](Rests &rests, int i, int m, const Split &sp, int *counter) {
+            if (row == 0)
+                rests.of[rests.n++] = Rest{i, m, sp};
             named_sync(1, 128);
             if (row == 0)
-                sh.last = add_acq_rel(counter) == parts - 1;
+                add_acq_rel(counter, 1);
+        };
+        auto parts_written = [&](int *counter, const Split &sp) {
+            return named_all(2, 128, row != 0 || wait_count(counter, sp.parts(), abort, kWaitOther));
+        };
+        // h of these columns of a tile goes out to the TMA reads of every block.
+        auto announce = [&](int columns) {
+            fence_async_proxy();
             named_sync(1, 128);
-            const bool last = sh.last != 0;
-            if (last)
-                __threadfence();
-            return last;
+            if (row == 0)
+                add_acq_rel(a.done, columns);
+        };
+        auto store_h = [&](int off, int j, int col, float gate, float up) {
+            __nv_bfloat16 hi, lo;
+            split(swiglu(gate, up), hi, lo);
+            a.h[static_cast<size_t>(off + j) * a.h_stride + col] = hi;
+            a.h[static_cast<size_t>(a.P + off + j) * a.h_stride + col] = lo;
         };
 
         for (Walk w(begin1, end1, a.kc1, a.mt1, false); run && w.more(); w.next()) {
-            const int tile = w.i * a.mt1 + w.m, first_unit = tile * a.kc1;
+            const int tile = w.i * a.mt1 + w.m;
             const int off = li.offset[w.i], n = li.count(w.i), N = ceil_div(n, 16) * 16, n8 = (n + 7) & ~7;
-            const int b0 = share_owner(total1, first_unit, G1), b1 = share_owner(total1, first_unit + a.kc1 - 1, G1);
             const int col = w.m * kTileRows + row;  // of h
+            const Split sp(shares1, tile * a.kc1, a.kc1);
+            float *const part = a.part + static_cast<size_t>(sp.slot(blk)) * a.part_floats + row;
             run = mbar_wait(smem_u32(&sh.full_d[at_d.s]), at_d.parity, abort, kWaitFullD);
             run = named_all(2, 128, run);  // the four warps leave together, or not at all
             if (!run)
                 break;
             tc_fence_after();
             const uint32_t d = lanes + at_d.s * 128;
-            float *const part = a.part + static_cast<size_t>(part_slot(total1, blk, G1, first_unit)) * a.part_floats;
-            auto finish = [&](int j, float gate, float up) {
-                if (j < n && col < a.I) {
-                    __nv_bfloat16 hi, lo;
-                    split(swiglu(gate, up), hi, lo);
-                    a.h[static_cast<size_t>(off + j) * a.h_stride + col] = hi;
-                    a.h[static_cast<size_t>(a.P + off + j) * a.h_stride + col] = lo;
-                }
-            };
             for (int j = 0; j < n8; j += 8) {
                 float g[8], v[8];
                 tmem_ld8(d + j, g);
@@ -260,55 +266,62 @@ __global__ void __launch_bounds__(kThreads, 1) experts_kernel(const __grid_const
                 tmem_wait_ld();
 #pragma unroll
                 for (int c = 0; c < 8; ++c) {
-                    if (b0 == b1) {
-                        finish(j + c, g[c], v[c]);
-                    } else {
-                        part[(j + c) * kTileRows + row] = g[c];
-                        part[(n8 + j + c) * kTileRows + row] = v[c];
+                    if (j + c >= n)
+                        break;
+                    if (sp.shared()) {
+                        part[(j + c) * kTileRows] = g[c];
+                        part[(n + j + c) * kTileRows] = v[c];
+                    } else if (col < a.I) {
+                        store_h(off, j + c, col, g[c], v[c]);
                     }
                 }
             }
             tc_fence_before();
             mbar_arrive(smem_u32(&sh.empty_d[at_d.s]));
             at_d.next(2);
-            bool mine = b0 == b1;
-            if (!mine && arrive_last(a.tiles + tile, b1 - b0 + 1)) {
-                mine = true;
-                for (int j = 0; j < n8; j += 8) {
-                    float g[8] = {}, v[8] = {};
-                    for (int b = b0; b <= b1; ++b) {
-                        const float *const p =
-                            a.part + static_cast<size_t>(part_slot(total1, b, G1, first_unit)) * a.part_floats;
+            if (sp.shared())
+                leave(sh.rests[0], w.i, w.m, sp, a.tiles + tile);
+            else
+                announce(n);
+        }
+        for (int r = 0; run && r < sh.rests[0].n; ++r) {
+            const Rest &rest = sh.rests[0].of[r];
+            const int i = rest.i, m = rest.m, off = li.offset[i], n = li.count(i);
+            const Split sp = rest.sp;
+            const int lo = sp.column(n, blk), hi = sp.column(n, blk + 1), col = m * kTileRows + row;
+            if (lo == hi)
+                continue;
+            run = parts_written(a.tiles + i * a.mt1 + m, sp);
+            if (!run)
+                break;
+            for (int j = lo; j < hi; j += 4) {
+                float g[4], v[4];
+                sum_parts<4>(a.part + j * kTileRows + row, a.part_floats, sp, hi - j, g);
+                sum_parts<4>(a.part + (n + j) * kTileRows + row, a.part_floats, sp, hi - j, v);
 #pragma unroll
-                        for (int c = 0; c < 8; ++c) {
-                            g[c] += __ldcg(p + (j + c) * kTileRows + row);
-                            v[c] += __ldcg(p + (n8 + j + c) * kTileRows + row);
-                        }
-                    }
-#pragma unroll
-                    for (int c = 0; c < 8; ++c)
-                        finish(j + c, g[c], v[c]);
-                }
+                for (int c = 0; c < 4; ++c)
+                    if (j + c < hi && col < a.I)
+                        store_h(off, j + c, col, g[c], v[c]);
             }
-            if (mine) {  // h of this tile goes out to the TMA reads of every block
-                fence_async_proxy();
-                __threadfence();
-                named_sync(1, 128);
-                if (row == 0)
-                    add_acq_rel(a.done);
-            }
+            announce(hi - lo);
         }
 
         const int group = A * a.kc2;  // units of one row tile of y, over all experts
+        auto store_y = [&](int m, int t, float v) {
+            const int col = m * kTileRows + row;
+            __nv_bfloat16 *const p = a.out + t * a.out_stride + col;
+            if (col < a.H && EP_IN_BOUNDS(a.chk, epk::kSiteMoeOut, p, 2, a.out, 2 * ((a.T - 1) * a.out_stride + a.H)))
+                *p = __float2bfloat16_rn(v);
+        };
         for (Walk w(begin2, end2, a.kc2, A, true); run && w.more();) {
-            const int m = w.m, first_unit = m * group;
-            const int b0 = share_owner(total2, first_unit, G2), b1 = share_owner(total2, first_unit + group - 1, G2);
-            for (int t = 0; t < T8; ++t)
+            const Walk first = w;
+            const Split sp(shares2, first.m * group, group);
+            for (int t = 0; t < a.T; ++t)
                 acc[t * kTileRows + row] = 0.0f;
-            for (; run && w.more() && w.m == m; w.next()) {
+            for (; run && w.more() && w.m == first.m; w.next()) {
                 const int off = li.offset[w.i], n = li.count(w.i), n8 = (n + 7) & ~7;
                 run = mbar_wait(smem_u32(&sh.full_d[at_d.s]), at_d.parity, abort, kWaitFullD);
-                run = named_all(2, 128, run);  // the four warps leave together, or not at all
+                run = named_all(2, 128, run);
                 if (!run)
                     break;
                 tc_fence_after();
@@ -331,36 +344,32 @@ __global__ void __launch_bounds__(kThreads, 1) experts_kernel(const __grid_const
             }
             if (!run)
                 break;
-            const int col = m * kTileRows + row;
-            auto store = [&](int t, float v) {
-                __nv_bfloat16 *const p = a.out + t * a.out_stride + col;
-                if (t < a.T && col < a.H &&
-                    EP_IN_BOUNDS(a.chk, epk::kSiteMoeOut, p, 2, a.out, 2 * ((a.T - 1) * a.out_stride + a.H)))
-                    *p = __float2bfloat16_rn(v);
-            };
-            if (b0 == b1) {
+            if (sp.shared()) {
+                float *const part = a.part + static_cast<size_t>(sp.slot(blk)) * a.part_floats + row;
                 for (int t = 0; t < a.T; ++t)
-                    store(t, acc[t * kTileRows + row]);
+                    part[t * kTileRows] = acc[t * kTileRows + row];
+                leave(sh.rests[1], first.i, first.m, sp, a.tiles + a.E * a.mt1 + first.m);
             } else {
-                float *const part = a.part + static_cast<size_t>(part_slot(total2, blk, G2, first_unit)) * a.part_floats;
                 for (int t = 0; t < a.T; ++t)
-                    part[t * kTileRows + row] = acc[t * kTileRows + row];
-                if (arrive_last(a.tiles + a.E * a.mt1 + m, b1 - b0 + 1)) {
-                    for (int t = 0; t < a.T; t += 8) {
-                        float v[8] = {};
-                        for (int b = b0; b <= b1; ++b) {
-                            const float *const p =
-                                a.part + static_cast<size_t>(part_slot(total2, b, G2, first_unit)) * a.part_floats;
+                    store_y(first.m, t, acc[t * kTileRows + row]);
+            }
+        }
+        for (int r = 0; run && r < sh.rests[1].n; ++r) {
+            const Rest &rest = sh.rests[1].of[r];
+            const Split sp = rest.sp;
+            const int m = rest.m, lo = sp.column(a.T, blk), hi = sp.column(a.T, blk + 1);
+            if (lo == hi)
+                continue;
+            run = parts_written(a.tiles + a.E * a.mt1 + m, sp);
+            if (!run)
+                break;
+            for (int t = lo; t < hi; t += 4) {
+                float v[4];
+                sum_parts<4>(a.part + t * kTileRows + row, a.part_floats, sp, hi - t, v);
 #pragma unroll
-                            for (int c = 0; c < 8; ++c)
-                                if (t + c < a.T)
-                                    v[c] += __ldcg(p + (t + c) * kTileRows + row);
-                        }
-#pragma unroll
-                        for (int c = 0; c < 8; ++c)
-                            store(t + c, v[c]);
-                    }
-                }
+                for (int c = 0; c < 4; ++c)
+                    if (t + c < hi)
+                        store_y(m, t + c, v[c]);
             }
         }
     }
@@ -386,7 +395,7 @@ __global__ void __launch_bounds__(kThreads, 1) experts_kernel(const __grid_const
 
     // the last block to leave clears the counters for the next launch
     if (tid == 0)
-        sh.reset = add_acq_rel(a.leaving) == G - 1;
+        sh.reset = add_acq_rel(a.leaving, 1) == G - 1;
     __syncthreads();
     if (sh.reset) {
         for (int i = tid; i < A * a.mt1; i += kThreads)

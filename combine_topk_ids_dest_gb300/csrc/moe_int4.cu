@@ -37,7 +37,8 @@ struct Shared {
     int abort;
     int active, nmax;
     int issued_a, issued_b;
-    int last, reset;
+    int reset;
+    Rests rests[2];  // of the two products
 };
 
 // Eight codes to four pairs q - z. Code 2p is at bits 4p, code 2p + 1 at bits
@@ -77,12 +78,12 @@ __global__ void __launch_bounds__(kThreads, 1) int4_kernel(const __grid_constant
     float *const acc = reinterpret_cast<float *>(ring_a_p + a.stages * a.stage_a);
     const Lists li(acc + (LINEAR ? 0 : T8 * kTileRows), a.E, a.P);
 
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int tid = threadIdx.x, warp = __shfl_sync(~0u, tid >> 5, 0), lane = tid & 31;
     const int G = gridDim.x, blk = blockIdx.x;
     volatile int *const abort = &sh.abort;
 
     if (tid == 0) {
-        sh.abort = sh.reset = sh.issued_a = sh.issued_b = 0;
+        sh.abort = sh.reset = sh.rests[0].n = sh.rests[1].n = sh.issued_a = sh.issued_b = 0;
         for (int i = 0; i < kMaxStagesA; ++i) {
             mbar_init(smem_u32(&sh.full_a[i]), 1);
             mbar_init(smem_u32(&sh.empty_a[i]), 4 + 8);  // the warps that read codes, then scales
@@ -136,17 +137,17 @@ __global__ void __launch_bounds__(kThreads, 1) int4_kernel(const __grid_constant
     // gate and up (or one) tiles of the first product; the second product of the experts
     constexpr int kParts = LINEAR ? 1 : 2;
     const int total1 = A * a.mt1 * a.kc1, total2 = LINEAR ? 0 : A * a.mt2 * a.kc2;
-    const int G1 = min(G, total1), G2 = min(G, total2);
-    const int begin1 = share_begin(total1, min(blk, G1), G1), end1 = share_begin(total1, min(blk + 1, G1), G1);
-    const int begin2 = LINEAR ? 0 : share_begin(total2, min(blk, G2), G2);
-    const int end2 = LINEAR ? 0 : share_begin(total2, min(blk + 1, G2), G2);
+    const Shares shares1(total1, G), shares2(total2, G);
+    const int begin1 = shares1.begin(blk), end1 = shares1.begin(blk + 1);
+    const int begin2 = LINEAR ? 0 : shares2.begin(blk), end2 = LINEAR ? 0 : shares2.begin(blk + 1);
+    const int pairs = li.offset[A];
     const int width = LINEAR ? ceil_div(sh.nmax, 16) * 16 : ceil_div(sh.nmax, 8) * 16;  // rows of a token tile, columns of a sum
     const int stage_b = width * 256;  // two 64-input halves
     const int stages_b = min(kMaxStagesB, a.bytes_b / stage_b);
     const int sums = min(kMaxSums, 256 / width);
     const int groups1 = 4 >> a.shift1, groups2 = 4 >> a.shift2;
 
-    if (warp == 0 && lane == 0) {
+    if (warp == 0 && elect_one()) {
         // ---- weight tiles ----
         const uint64_t policy = policy_evict_first();
         Cursor at;
@@ -175,7 +176,7 @@ __global__ void __launch_bounds__(kThreads, 1) int4_kernel(const __grid_constant
                 run = load(src, a.tile2);
         }
         sh.issued_a = issued;
-    } else if (warp == 2 && lane == 0) {
+    } else if (warp == 2 && elect_one()) {
         // ---- token tiles ----
         Cursor at;
         int issued = 0;
@@ -211,8 +212,10 @@ __global__ void __launch_bounds__(kThreads, 1) int4_kernel(const __grid_constant
                     }
             }
         }
-        if (run && begin2 < end2)
-            run = wait_products(a, A * a.mt1, abort);
+        if (run && begin2 < end2) {
+            run = wait_count(a.done, a.mt1 * pairs, abort, kWaitDone);
+            fence_async_proxy();
+        }
         for (Walk w(begin2, end2, a.kc2, A, true); run && w.more(); w.next()) {
             const int off = li.offset[w.i], n8 = ceil_div(li.count(w.i), 8);
             for (int k = w.k; k < w.k + w.len && (run = acquire(n8 * 4096)); ++k)
@@ -225,7 +228,7 @@ __global__ void __launch_bounds__(kThreads, 1) int4_kernel(const __grid_constant
                 }
         }
         sh.issued_b = issued;
-    } else if (warp == 1 && lane == 0) {
+    } else if (warp == 1 && elect_one()) {
         // ---- matrix instructions ----
         Cursor at_t, at_b, at_d;
         bool run = true;
@@ -320,16 +323,21 @@ __global__ void __launch_bounds__(kThreads, 1) int4_kernel(const __grid_constant
         bool run = true;
         float v[2][32];  // sums of this thread's row: gate and up (or the one product), up to 32 columns
 
-        auto arrive_last = [&](int *counter, int parts) {
-            __threadfence();
+        auto leave = [&](Rests &rests, int i, int m, const Split &sp, int *counter) {
+            if (rtid == 0)
+                rests.of[rests.n++] = Rest{i, m, sp};
             named_sync(1, kResults);
             if (rtid == 0)
-                sh.last = add_acq_rel(counter) == parts - 1;
+                add_acq_rel(counter, 1);
+        };
+        auto parts_written = [&](int *counter, const Split &sp) {
+            return named_all(2, kResults, rtid != 0 || wait_count(counter, sp.parts(), abort, kWaitOther));
+        };
+        auto announce = [&](int columns) {
+            fence_async_proxy();
             named_sync(1, kResults);
-            const bool last = sh.last != 0;
-            if (last)
-                __threadfence();
-            return last;
+            if (rtid == 0)
+                add_acq_rel(a.done, columns);
         };
         // Adds s times the sum of each group of one weight tile to v[p], columns [c0, c0 + 8 nb) of the sum and,
         // where lo > 0, those `lo` further.
@@ -370,13 +378,29 @@ __global__ void __launch_bounds__(kThreads, 1) int4_kernel(const __grid_constant
             at_a.next(a.stages);
         };
 
+        // column j of row tile m: h, or y of the linear layer
+        auto result = [&](int off, int m, int j, float gate, float up) {
+            const int col = m * kTileRows + row;
+            if (col >= a.I)
+                return;
+            if (LINEAR) {
+                uint16_t *const p = static_cast<uint16_t *>(a.out) + j * a.out_stride + col;
+                if (EP_IN_BOUNDS(a.chk, epk::kSiteMoeOut, p, 2, a.out, 2 * ((a.T - 1) * a.out_stride + a.I)))
+                    *p = BF16 ? __bfloat16_as_ushort(__float2bfloat16_rn(gate))
+                              : __half_as_ushort(__float2half_rn(gate));
+            } else {
+                __nv_bfloat16 hi, lo;
+                split(swiglu(gate, up), hi, lo);
+                a.h[static_cast<size_t>(off + j) * a.h_stride + col] = hi;
+                a.h[static_cast<size_t>(a.P + off + j) * a.h_stride + col] = lo;
+            }
+        };
+
         for (Walk w(begin1, end1, a.kc1, a.mt1, false); run && w.more(); w.next()) {
             const int off = li.offset[w.i], n = li.count(w.i), tile = w.i * a.mt1 + w.m;
             const int blocks = ceil_div(n, 8), half = ceil_div(blocks, 2);  // columns by eights: this warpgroup's
-            const int c0 = wg ? half * 8 : 0, nb = wg ? blocks - half : half, n8 = blocks * 8;
-            const int first_unit = tile * a.kc1;
-            const int b0 = share_owner(total1, first_unit, G1), b1 = share_owner(total1, first_unit + a.kc1 - 1, G1);
-            const int col = w.m * kTileRows + row;
+            const int c0 = wg ? half * 8 : 0, nb = wg ? blocks - half : half;
+            const Split sp(shares1, tile * a.kc1, a.kc1);
 #pragma unroll
             for (int c = 0; c < 32; ++c)
                 v[0][c] = v[1][c] = 0.0f;
@@ -388,72 +412,60 @@ __global__ void __launch_bounds__(kThreads, 1) int4_kernel(const __grid_constant
             run = named_all(2, kResults, run);
             if (!run)
                 break;
-            auto result = [&](int j, float gate, float up) {
-                if (j >= n)
-                    return;
-                if (LINEAR) {
-                    if (col < a.I) {
-                        uint16_t *const p = static_cast<uint16_t *>(a.out) + j * a.out_stride + col;
-                        if (EP_IN_BOUNDS(a.chk, epk::kSiteMoeOut, p, 2, a.out, 2 * ((a.T - 1) * a.out_stride + a.I)))
-                            *p = BF16 ? __bfloat16_as_ushort(__float2bfloat16_rn(gate))
-                                      : __half_as_ushort(__float2half_rn(gate));
-                    }
-                } else if (col < a.I) {
-                    __nv_bfloat16 hi, lo;
-                    split(swiglu(gate, up), hi, lo);
-                    a.h[static_cast<size_t>(off + j) * a.h_stride + col] = hi;
-                    a.h[static_cast<size_t>(a.P + off + j) * a.h_stride + col] = lo;
-                }
-            };
-            bool mine = b0 == b1;
-            if (mine) {
+            float *const part = a.part + static_cast<size_t>(sp.slot(blk)) * a.part_floats + row;
 #pragma unroll
-                for (int c = 0; c < 32; ++c)
-                    if (c < nb * 8)
-                        result(c0 + c, v[0][c], v[1][c]);
-            } else {
-                float *const part = a.part + static_cast<size_t>(part_slot(total1, blk, G1, first_unit)) * a.part_floats;
-#pragma unroll
-                for (int c = 0; c < 32; ++c)
-                    if (c < nb * 8) {
-                        part[(c0 + c) * kTileRows + row] = v[0][c];
+            for (int c = 0; c < 32; ++c) {
+                const int j = c0 + c;
+                if (c < nb * 8 && j < n) {
+                    if (sp.shared()) {
+                        part[j * kTileRows] = v[0][c];
                         if (!LINEAR)
-                            part[(n8 + c0 + c) * kTileRows + row] = v[1][c];
-                    }
-                if (arrive_last(a.tiles + tile, b1 - b0 + 1)) {
-                    mine = true;
-                    for (int j = c0; j < c0 + nb * 8; j += 8) {
-                        float g[8] = {}, r[8] = {};
-                        for (int b = b0; b <= b1; ++b) {
-                            const float *const p =
-                                a.part + static_cast<size_t>(part_slot(total1, b, G1, first_unit)) * a.part_floats;
-#pragma unroll
-                            for (int c = 0; c < 8; ++c) {
-                                g[c] += __ldcg(p + (j + c) * kTileRows + row);
-                                if (!LINEAR)
-                                    r[c] += __ldcg(p + (n8 + j + c) * kTileRows + row);
-                            }
-                        }
-#pragma unroll
-                        for (int c = 0; c < 8; ++c)
-                            result(j + c, g[c], r[c]);
+                            part[(n + j) * kTileRows] = v[1][c];
+                    } else {
+                        result(off, w.m, j, v[0][c], v[1][c]);
                     }
                 }
             }
-            if (!LINEAR && mine) {
-                fence_async_proxy();
-                __threadfence();
-                named_sync(1, kResults);
-                if (rtid == 0)
-                    add_acq_rel(a.done);
+            if (sp.shared())
+                leave(sh.rests[0], w.i, w.m, sp, a.tiles + tile);
+            else if (!LINEAR)
+                announce(n);
+        }
+        for (int r = 0; run && r < sh.rests[0].n; ++r) {
+            const Rest &rest = sh.rests[0].of[r];
+            const int i = rest.i, m = rest.m, off = li.offset[i], n = li.count(i);
+            const Split sp = rest.sp;
+            const int lo = sp.column(n, blk), hi = sp.column(n, blk + 1);
+            if (lo == hi)
+                continue;
+            run = parts_written(a.tiles + i * a.mt1 + m, sp);
+            if (!run)
+                break;
+            for (int j = lo + 2 * wg; j < hi; j += 4) {
+                float g[2], u[2] = {};
+                sum_parts<2>(a.part + j * kTileRows + row, a.part_floats, sp, hi - j, g);
+                if (!LINEAR)
+                    sum_parts<2>(a.part + (n + j) * kTileRows + row, a.part_floats, sp, hi - j, u);
+#pragma unroll
+                for (int c = 0; c < 2; ++c)
+                    if (j + c < hi)
+                        result(off, m, j + c, g[c], u[c]);
             }
+            if (!LINEAR)
+                announce(hi - lo);
         }
 
         const int group = LINEAR ? 1 : A * a.kc2;
+        auto store_y = [&](int m, int t, float r) {
+            const int col = m * kTileRows + row;
+            __nv_bfloat16 *const p = static_cast<__nv_bfloat16 *>(a.out) + t * a.out_stride + col;
+            if (col < a.H && EP_IN_BOUNDS(a.chk, epk::kSiteMoeOut, p, 2, a.out, 2 * ((a.T - 1) * a.out_stride + a.H)))
+                *p = __float2bfloat16_rn(r);
+        };
         for (Walk w(begin2, end2, a.kc2, A, true); !LINEAR && run && w.more();) {
-            const int m = w.m, first_unit = m * group;
-            const int b0 = share_owner(total2, first_unit, G2), b1 = share_owner(total2, first_unit + group - 1, G2);
-            for (int t = wg; t < T8; t += 2)
+            const int m = w.m, i0 = w.i;
+            const Split sp(shares2, m * group, group);
+            for (int t = wg; t < a.T; t += 2)
                 acc[t * kTileRows + row] = 0.0f;
             for (; run && w.more() && w.m == m; w.next()) {
                 const int off = li.offset[w.i], n = li.count(w.i);
@@ -478,38 +490,34 @@ __global__ void __launch_bounds__(kThreads, 1) int4_kernel(const __grid_constant
             run = named_all(2, kResults, run);
             if (!run)
                 break;
-            const int col = m * kTileRows + row;
-            auto store = [&](int t, float r) {
-                __nv_bfloat16 *const p = static_cast<__nv_bfloat16 *>(a.out) + t * a.out_stride + col;
-                if (t < a.T && col < a.H &&
-                    EP_IN_BOUNDS(a.chk, epk::kSiteMoeOut, p, 2, a.out, 2 * ((a.T - 1) * a.out_stride + a.H)))
-                    *p = __float2bfloat16_rn(r);
-            };
-            if (b0 == b1) {
+            if (sp.shared()) {
+                float *const part = a.part + static_cast<size_t>(sp.slot(blk)) * a.part_floats + row;
                 for (int t = wg; t < a.T; t += 2)
-                    store(t, acc[t * kTileRows + row]);
+                    part[t * kTileRows] = acc[t * kTileRows + row];
+                leave(sh.rests[1], i0, m, sp, a.tiles + a.E * a.mt1 + m);
             } else {
-                float *const part = a.part + static_cast<size_t>(part_slot(total2, blk, G2, first_unit)) * a.part_floats;
                 for (int t = wg; t < a.T; t += 2)
-                    part[t * kTileRows + row] = acc[t * kTileRows + row];
-                if (arrive_last(a.tiles + a.E * a.mt1 + m, b1 - b0 + 1)) {
-                    for (int t = wg * 8; t < a.T; t += 16) {
-                        float r[8] = {};
-                        for (int b = b0; b <= b1; ++b) {
-                            const float *const p =
-                                a.part + static_cast<size_t>(part_slot(total2, b, G2, first_unit)) * a.part_floats;
-#pragma unroll
-                            for (int c = 0; c < 8; ++c)
-                                if (t + c < a.T)
-                                    r[c] += __ldcg(p + (t + c) * kTileRows + row);
-                        }
-#pragma unroll
-                        for (int c = 0; c < 8; ++c)
-                            store(t + c, r[c]);
-                    }
-                }
+                    store_y(m, t, acc[t * kTileRows + row]);
+                named_sync(1, kResults);  // acc is read before the next row tile clears it
             }
-            named_sync(1, kResults);  // acc is read before the next row tile clears it
+        }
+        for (int r = 0; !LINEAR && run && r < sh.rests[1].n; ++r) {
+            const Rest &rest = sh.rests[1].of[r];
+            const Split sp = rest.sp;
+            const int m = rest.m, lo = sp.column(a.T, blk), hi = sp.column(a.T, blk + 1);
+            if (lo == hi)
+                continue;
+            run = parts_written(a.tiles + a.E * a.mt1 + m, sp);
+            if (!run)
+                break;
+            for (int t = lo + 2 * wg; t < hi; t += 4) {
+                float x[2];
+                sum_parts<2>(a.part + t * kTileRows + row, a.part_floats, sp, hi - t, x);
+#pragma unroll
+                for (int c = 0; c < 2; ++c)
+                    if (t + c < hi)
+                        store_y(m, t + c, x[c]);
+            }
         }
     }
     __syncwarp();
@@ -533,7 +541,7 @@ __global__ void __launch_bounds__(kThreads, 1) int4_kernel(const __grid_constant
         tmem_free(tmem, 512);
 
     if (tid == 0)
-        sh.reset = add_acq_rel(a.leaving) == G - 1;
+        sh.reset = add_acq_rel(a.leaving, 1) == G - 1;
     __syncthreads();
     if (sh.reset) {
         for (int i = tid; i < A * a.mt1; i += kThreads)

@@ -17,18 +17,6 @@ namespace moe {
 constexpr int kMaxTokens = EP_MOE_MAX_TOKENS;    // rows of one experts or linear call
 constexpr int kMaxLocal = EP_MOE_MAX_EXPERTS;    // experts of one handle
 
-// A contiguous share of `total` units for block b of G.
-static __host__ __device__ inline int share_begin(int total, int b, int G)
-{
-    return static_cast<int>(static_cast<long long>(total) * b / G);
-}
-
-// The block whose share holds unit u: the largest b with share_begin(b) <= u.
-static __host__ __device__ inline int share_owner(int total, int u, int G)
-{
-    return static_cast<int>(((static_cast<long long>(u) + 1) * G - 1) / total);
-}
-
 // ---- router (moe_router.cu) -------------------------------------------------------
 
 struct RouterArgs {
@@ -65,7 +53,7 @@ struct ExpertsArgs {
     long long out_stride;
     __nv_bfloat16 *h;
     float *part;
-    int *done;     // finished tiles of the first product
+    int *done;     // finished (row tile, token) pairs of the first product
     int *leaving;  // blocks that are done with the counters
     int *tiles;    // per tile: parts that have been written
     unsigned int *err;  // host memory: set when a wait ran out

@@ -54,10 +54,80 @@ struct Walk {
     }
 };
 
-// Slot (first or last share) in which block b keeps its part of the tile that begins at unit `begin`.
-static __device__ __forceinline__ int part_slot(int total, int b, int G, int begin)
+// `total` units cut into contiguous shares, one per block, that differ by one
+// at most; blocks beyond `total` have none, so every block of a run of blocks
+// has a part in a tile they share.
+struct Shares {
+    int each, more;  // units of a share; the first `more` blocks have one more
+
+    __device__ __forceinline__ Shares(int total, int G)
+    {
+        each = total / G;
+        more = total - each * G;
+    }
+    __device__ __forceinline__ int begin(int b) const { return b * each + min(b, more); }
+    __device__ __forceinline__ int owner(int u) const
+    {
+        const int edge = more * (each + 1);
+        return u < edge ? u / (each + 1) : more + (u - edge) / each;
+    }
+};
+
+// A tile that blocks b0..b1 share: each keeps its part in one of two slots,
+// the second if the tile begins after the block's share does.
+struct Split {
+    int b0, b1, slot0;
+
+    Split() = default;
+    __device__ __forceinline__ Split(const Shares &s, int first_unit, int units)
+        : b0(s.owner(first_unit)), b1(s.owner(first_unit + units - 1)),
+          slot0(2 * b0 + (first_unit > s.begin(b0) ? 1 : 0))
+    {
+    }
+    __device__ __forceinline__ bool shared() const { return b0 != b1; }
+    __device__ __forceinline__ int parts() const { return b1 - b0 + 1; }
+    __device__ __forceinline__ int slot(int b) const { return b == b0 ? slot0 : 2 * b; }
+    // Of n columns, the first that block b adds up (b == b1 + 1: n).
+    __device__ __forceinline__ int column(int n, int b) const { return n * (b - b0) / parts(); }
+};
+
+// A run of chunks whose tile other blocks share is left as a part and settled
+// after the product's last run, when the others are about to be done too:
+// each of them then adds up the parts of some columns. A block has at most
+// two such runs, the first and the last.
+struct Rest {
+    int i, m;
+    Split sp;
+};
+struct Rests {
+    int n;
+    Rest of[2];
+};
+
+// Sums v[c] of N columns of a shared tile (`cols` of them valid), this
+// thread's row, over the parts in the order of the inputs. `base` is the
+// first column in slot 0. Up to four parts' loads are in flight.
+template <int N>
+static __device__ __forceinline__ void sum_parts(const float *base, int part_floats, const Split &sp, int cols, float *v)
 {
-    return 2 * b + (begin <= share_begin(total, b, G) ? 0 : 1);
+#pragma unroll
+    for (int c = 0; c < N; ++c)
+        v[c] = c < cols ? __ldcg(base + static_cast<size_t>(sp.slot0) * part_floats + c * kTileRows) : 0.0f;
+    for (int b = sp.b0 + 1; b <= sp.b1; b += 4) {
+        float x[4][N];
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+#pragma unroll
+            for (int c = 0; c < N; ++c)
+                x[q][c] = b + q <= sp.b1 && c < cols
+                              ? __ldcg(base + static_cast<size_t>(2 * (b + q)) * part_floats + c * kTileRows)
+                              : 0.0f;
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+#pragma unroll
+            for (int c = 0; c < N; ++c)
+                v[c] += x[q][c];
+    }
 }
 
 // Two bf16 values whose sum carries 16 bits of v's mantissa (v itself where it is not finite).
@@ -154,24 +224,6 @@ static __device__ __forceinline__ void build_lists(const Args &a, const Lists &l
             li.weight[at] = w;
         }
     }
-}
-
-// Waits until every tile of the first product is announced; then orders TMA
-// reads of h after that.
-template <class Args>
-static __device__ __forceinline__ bool wait_products(const Args &a, int tiles, volatile int *abort)
-{
-    const unsigned long long t0 = now_ns();
-    while (ld_acquire(a.done) < tiles) {
-        if (*abort)
-            return false;
-        if (now_ns() - t0 > kWaitNs) {
-            *abort = kWaitDone;
-            return false;
-        }
-    }
-    fence_async_proxy();
-    return true;
 }
 
 // y = 0 where no token chose an expert of this handle.
