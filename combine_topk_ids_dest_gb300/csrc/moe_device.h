@@ -1,7 +1,8 @@
 // moe_device.h -- device helpers of the MoE operators: mbarriers with bounded
 // waits, TMA copies, tcgen05 matrix instructions and tensor-memory access.
 //
-// Every wait has a limit (kWaitNs of the GPU's nanosecond timer). A wait that
+// Every wait has a limit (kWaitCycles of the SM's clock, about 2 s; the
+// nanosecond timer takes longer to read than most waits last). A wait that
 // runs out sets the block's abort flag; every other wait of the block sees the
 // flag and gives up too, the roles leave their loops and the block ends
 // through its normal exit, which drains its copies and frees its tensor memory.
@@ -16,7 +17,7 @@
 
 namespace moe {
 
-constexpr unsigned long long kWaitNs = 2000000000ULL;
+constexpr long long kWaitCycles = 4000000000LL;
 
 static __device__ __forceinline__ uint32_t smem_u32(const void *p)
 {
@@ -32,13 +33,6 @@ static __device__ __forceinline__ bool elect_one()
     uint32_t p;
     asm volatile("{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\tselp.u32 %0, 1, 0, e;\n\t}" : "=r"(p));
     return p != 0;
-}
-
-static __device__ __forceinline__ unsigned long long now_ns()
-{
-    unsigned long long t;
-    asm volatile("mov.u64 %0, %globaltimer;" : "=l"(t));
-    return t;
 }
 
 // ---- mbarriers ----------------------------------------------------------------
@@ -58,9 +52,9 @@ static __device__ __forceinline__ void mbar_expect(uint32_t bar, uint32_t bytes)
     asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
 }
 
-static __device__ __forceinline__ void mbar_arrive(uint32_t bar)
+static __device__ __forceinline__ void mbar_arrive(uint32_t bar, uint32_t count = 1)
 {
-    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(count) : "memory");
 }
 
 static __device__ __forceinline__ bool mbar_try(uint32_t bar, uint32_t parity)
@@ -80,14 +74,14 @@ enum WaitSite { kWaitEmptyA = 1, kWaitEmptyB, kWaitEmptyD, kWaitFullA, kWaitFull
 
 static __device__ __noinline__ bool mbar_wait_slow(uint32_t bar, uint32_t parity, volatile int *abort, int site)
 {
-    const unsigned long long t0 = now_ns();
+    const long long t0 = clock64();
     for (;;) {
         for (int i = 0; i < 32; ++i)
             if (mbar_try(bar, parity))
                 return true;
         if (abort && *abort)
             return false;
-        if (now_ns() - t0 > kWaitNs) {
+        if (clock64() - t0 > kWaitCycles) {
             if (abort)
                 *abort = site;
             return false;
@@ -102,6 +96,13 @@ static __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, 
     if (mbar_try(bar, parity))
         return true;
     return mbar_wait_slow(bar, parity, abort, site);
+}
+
+// mbar_wait by a whole converged warp, with one answer for all lanes (which
+// lets the compiler keep what follows in uniform registers).
+static __device__ __forceinline__ bool mbar_wait_warp(uint32_t bar, uint32_t parity, volatile int *abort, int site)
+{
+    return __all_sync(~0u, mbar_wait(bar, parity, abort, site));
 }
 
 // ---- TMA ------------------------------------------------------------------------
@@ -207,15 +208,6 @@ static __device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b
                  : "memory");
 }
 
-// D[tmem] (+)= A[tmem] B[smem]^T
-static __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool add)
-{
-    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-                 "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-                 "r"(a), "l"(b), "r"(idesc), "r"(uint32_t(add))
-                 : "memory");
-}
-
 // 8 consecutive columns of this warp's 32 lanes (lane = row).
 static __device__ __forceinline__ void tmem_ld8(uint32_t addr, float *v)
 {
@@ -226,7 +218,23 @@ static __device__ __forceinline__ void tmem_ld8(uint32_t addr, float *v)
 }
 
 static __device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
-static __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// ---- warp-level MMA -------------------------------------------------------------
+
+// c[16 x 8] += a[16 x 16] b[16 x 8], bf16 or fp16 fragments
+template <bool BF16> static __device__ __forceinline__ void mma_16816(float *c, const uint32_t *a, uint32_t b0, uint32_t b1)
+{
+    if (BF16)
+        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+                     "{%0, %1, %2, %3};"
+                     : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                     : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+    else
+        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+                     "{%0, %1, %2, %3};"
+                     : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                     : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
 
 // ---- global flags -----------------------------------------------------------------
 
@@ -251,11 +259,11 @@ static __device__ __forceinline__ bool wait_count(const int *p, int target, vola
 {
     if (ld_acquire(p) >= target)
         return true;
-    const unsigned long long t0 = now_ns();
+    const long long t0 = clock64();
     while (ld_acquire(p) < target) {
         if (*abort)
             return false;
-        if (now_ns() - t0 > kWaitNs) {
+        if (clock64() - t0 > kWaitCycles) {
             *abort = site;
             return false;
         }

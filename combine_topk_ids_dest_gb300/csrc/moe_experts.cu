@@ -89,7 +89,7 @@ __global__ void __launch_bounds__(kThreads, 1) experts_kernel(const __grid_const
     }
     if (warp == 1)
         tmem_alloc(smem_u32(&sh.tmem), kTmemCols);
-    build_lists(a, li, sh, tid, kThreads);
+    build_lists(a, li, sh, tid, kThreads, kMaxTokens);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -177,8 +177,8 @@ __global__ void __launch_bounds__(kThreads, 1) experts_kernel(const __grid_const
                 }
         }
         sh.issued_b = issued;
-    } else if (warp == 1 && elect_one()) {
-        // ---- matrix instructions ----
+    } else if (warp == 1) {
+        // ---- matrix instructions: the warp waits, one lane issues ----
         Cursor at_a, at_b, at_d;
         bool run = true;
         for (int product = 0; run && product < 2; ++product) {
@@ -190,31 +190,35 @@ __global__ void __launch_bounds__(kThreads, 1) experts_kernel(const __grid_const
                 const int N = product ? ceil_div(n, 8) * 16 : ceil_div(n, 16) * 16;
                 const uint32_t idesc = idesc_f16(kTileRows, N, 1);
                 const uint32_t d = tmem + at_d.s * 128;
-                run = mbar_wait(smem_u32(&sh.empty_d[at_d.s]), at_d.parity ^ 1, abort, kWaitEmptyD);
-                tc_fence_after();
+                run = mbar_wait_warp(smem_u32(&sh.empty_d[at_d.s]), at_d.parity ^ 1, abort, kWaitEmptyD);
                 for (int k = 0; run && k < w.len; ++k) {
-                    run = mbar_wait(smem_u32(&sh.full_b[at_b.s]), at_b.parity, abort, kWaitFullB);
+                    run = mbar_wait_warp(smem_u32(&sh.full_b[at_b.s]), at_b.parity, abort, kWaitFullB);
+                    const uint64_t db = desc_sw128(ring_b + at_b.s * stage_b);
                     for (int g = 0; run && g < parts; ++g) {
-                        run = mbar_wait(smem_u32(&sh.full_a[at_a.s]), at_a.parity, abort, kWaitFullA);
+                        run = mbar_wait_warp(smem_u32(&sh.full_a[at_a.s]), at_a.parity, abort, kWaitFullA);
                         if (!run)
                             break;
                         tc_fence_after();
-                        const uint64_t da = desc_sw128(ring_a + at_a.s * kStageA);
-                        const uint64_t db = desc_sw128(ring_b + at_b.s * stage_b);
+                        if (elect_one()) {
+                            const uint64_t da = desc_sw128(ring_a + at_a.s * kStageA);
 #pragma unroll
-                        for (int q = 0; q < 4; ++q)  // 16 inputs each: 32 bytes further, in 16-byte units
-                            mma_ss(d + g * N, da + 2 * q, db + 2 * q, idesc, k > 0 || q > 0);
-                        tc_commit(smem_u32(&sh.empty_a[at_a.s]));
+                            for (int q = 0; q < 4; ++q)  // 16 inputs each: 32 bytes further, in 16-byte units
+                                mma_ss(d + g * N, da + 2 * q, db + 2 * q, idesc, k > 0 || q > 0);
+                            tc_commit(smem_u32(&sh.empty_a[at_a.s]));
+                            if (g == parts - 1)
+                                tc_commit(smem_u32(&sh.empty_b[at_b.s]));
+                        }
                         at_a.next(a.stages);
                     }
-                    tc_commit(smem_u32(&sh.empty_b[at_b.s]));
                     at_b.next(stages_b);
                 }
-                tc_commit(smem_u32(&sh.full_d[at_d.s]));
+                if (elect_one())
+                    tc_commit(smem_u32(&sh.full_d[at_d.s]));
                 at_d.next(2);
             }
         }
-        tc_commit(smem_u32(&sh.drain));
+        if (elect_one())
+            tc_commit(smem_u32(&sh.drain));
         mbar_wait(smem_u32(&sh.drain), 0, nullptr, kWaitOther);
     } else if (warp >= 4) {
         // ---- results ----

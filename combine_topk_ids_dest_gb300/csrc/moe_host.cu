@@ -84,7 +84,7 @@ EncodeTiled encode_tiled()
 }
 
 // A 16-bit tensor [.., rows, cols]: row stride and matrix stride in elements,
-// box_cols x box_rows boxes in 128-byte swizzled rows, zeros outside.
+// box_cols x box_rows boxes (of 64 columns: in 128-byte swizzled rows), zeros outside.
 ep_status encode_map(CUtensorMap *m, const char *what, int fp16, const void *base, long long cols, long long rows,
                      long long mats, long long row_stride, long long mat_stride, int box_cols, int box_rows)
 {
@@ -97,7 +97,8 @@ ep_status encode_map(CUtensorMap *m, const char *what, int fp16, const void *bas
     const cuuint32_t box[3] = {cuuint32_t(box_cols), cuuint32_t(box_rows), 1}, step[3] = {1, 1, 1};
     const CUresult r = fn(m, fp16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank,
                           const_cast<void *>(base), dims, strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                          CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                          box_cols == 64 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
+                          CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                           CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     if (r != CUDA_SUCCESS)
         return set_error(EP_ERR_CUDA, "cuTensorMapEncodeTiled of %s: error %d", what, static_cast<int>(r));
@@ -454,7 +455,7 @@ ep_status plan_linear(const ep_linear_config *c, LinearLayout *l)
         MOE_FAIL("weight: data is NULL or not 128-byte aligned");
     size_t off = align256(moe::int4_part_floats(c->max_tokens, true) * 4 * 2 * Base::kMaxBlocks);
     l->off_words = off;
-    l->words = kWords + div_up(c->outputs, 128);
+    l->words = kWords + 2 * size_t(div_up(c->outputs, 128));  // up to two runs over the weight
     l->total = off + align256(l->words * 4);
     return EP_OK;
 }
@@ -528,7 +529,7 @@ ep_status ep_linear_run(ep_linear *h, ep_dtype dtype, const void *x, long long x
     a.E = 1;
     a.H = c.inputs;
     a.I = c.outputs;
-    st = encode_map(&a.mx, "x", dtype == EP_DTYPE_FP16, x, a.H, a.T, 0, x_stride, 0, moe::kChunk, 8);
+    st = encode_map(&a.mx, "x", dtype == EP_DTYPE_FP16, x, a.H, a.T, 0, x_stride, 0, 32, 8);
     if (st != EP_OK)
         return st;
     a.w1 = static_cast<const uint8_t *>(c.weight.data);
@@ -612,14 +613,20 @@ ep_status plan_experts(const ep_experts_config *c, ExpertsLayout *l)
         MOE_FAIL("gate_up and down must have the same scale_dtype");
     const int pairs = c->max_tokens * c->top_k;
     const size_t part = w[0]->group ? moe::int4_part_floats(c->max_tokens, false) : moe::experts_part_floats(c->max_tokens);
-    l->h_stride = div_up(c->intermediate, 64) * 64;
     size_t off = 0;
     l->off_h = off;
-    off += align256(size_t(2) * pairs * l->h_stride * 2);
+    if (w[0]->group) {  // a row of h in two parts, in chunks of 128 inputs
+        l->h_stride = div_up(c->intermediate, 128) * 256;
+        off += align256(moe::int4_h_rows(c->max_tokens, c->top_k, c->num_experts) * l->h_stride * 2);
+    } else {
+        l->h_stride = div_up(c->intermediate, 64) * 64;
+        off += align256(size_t(2) * pairs * l->h_stride * 2);
+    }
     l->off_part = off;
     off += align256(part * 4 * 2 * Base::kMaxBlocks);
     l->off_words = off;
-    l->words = kWords + size_t(c->num_experts) * div_up(c->intermediate, 128) + div_up(c->hidden, 128);
+    l->words = kWords + size_t(w[0]->group ? 2 : 1) * c->num_experts * div_up(c->intermediate, 128) +
+               div_up(c->hidden, 128);
     off += align256(l->words * 4);
     l->total = off;
     return EP_OK;
@@ -628,7 +635,8 @@ ep_status plan_experts(const ep_experts_config *c, ExpertsLayout *l)
 // What both kernels' argument blocks have in common.
 template <class Args>
 ep_status experts_args(const ep_experts *h, Args &a, const ExpertsLayout &l, const void *x, long long x_stride,
-                       int num_tokens, const int32_t *ids, const float *weights, long long out_stride, int chunk)
+                       int num_tokens, const int32_t *ids, const float *weights, long long out_stride, int chunk,
+                       int box_cols)
 {
     const ep_experts_config &c = h->cfg;
     a.T = num_tokens;
@@ -650,10 +658,7 @@ ep_status experts_args(const ep_experts *h, Args &a, const ExpertsLayout &l, con
     a.kc1 = div_up(a.H, chunk);
     a.mt2 = div_up(a.H, moe::kTileRows);
     a.kc2 = div_up(a.I, chunk);
-    ep_status st = encode_map(&a.mx, "x", 0, x, a.H, a.T, 0, x_stride, 0, moe::kChunk, 1);
-    if (st == EP_OK)
-        st = encode_map(&a.mh, "h", 0, a.h, a.I, 2LL * a.P, 0, a.h_stride, 0, moe::kChunk, 8);
-    return st;
+    return encode_map(&a.mx, "x", 0, x, a.H, a.T, 0, x_stride, 0, box_cols, 1);
 }
 
 }  // namespace
@@ -731,7 +736,9 @@ ep_status ep_experts_run(ep_experts *h, const void *x, long long x_stride, const
     cudaError_t ce;
     if (c.gate_up.group == 0) {
         moe::ExpertsArgs a = {};
-        st = experts_args(h, a, l, x, x_stride, num_tokens, ids, weights, out_stride, moe::kChunk);
+        st = experts_args(h, a, l, x, x_stride, num_tokens, ids, weights, out_stride, moe::kChunk, moe::kChunk);
+        if (st == EP_OK)
+            st = encode_map(&a.mh, "h", 0, a.h, a.I, 2LL * a.P, 0, a.h_stride, 0, moe::kChunk, 8);
         if (st != EP_OK)
             return st;
         a.mw1 = h->mw1;
@@ -742,7 +749,7 @@ ep_status ep_experts_run(ep_experts *h, const void *x, long long x_stride, const
         ce = moe::launch_experts(a, h->base.sms, smem, s);
     } else {
         moe::Int4Args a = {};
-        st = experts_args(h, a, l, x, x_stride, num_tokens, ids, weights, out_stride, 128);
+        st = experts_args(h, a, l, x, x_stride, num_tokens, ids, weights, out_stride, 128, 32);
         if (st != EP_OK)
             return st;
         a.w1 = static_cast<const uint8_t *>(c.gate_up.data);

@@ -5,64 +5,158 @@
 //   linear:   y = x W^T
 //   experts:  as in moe_experts.cu
 //
-// The kernel is that of moe_experts.cu, with the weights' way to the MMA
-// lengthened by one step. A stage of the ring is a tile of 128 rows x 128
-// inputs, repacked once when the weight was taken: 8 KB of codes, its scales
-// and zero points. Two warpgroups (a thread is a weight row) turn codes into
-// q - z, whole numbers that 16 bits hold exactly, and store them to tensor
-// memory as the MMA's A operand: shared memory could not carry the 16-bit
-// tile's write and read at this rate. Scales are applied to sums, not to
-// weights: each group's sum is an accumulator of its own, and two more
-// warpgroups add s times it to fp32 registers. So no weight is rounded.
+// Work is cut and shared tiles are settled as in moe_experts.cu. A stage of
+// the weights' ring is a tile of 128 rows x 128 inputs, repacked once when
+// the weight was taken: 8 KB of codes, its scales and zero points. Four
+// groups of four warps take tiles in turn (gate tiles fall to groups 0 and
+// 2, up tiles to 1 and 3). A warp has 32 rows of its tile:
+//
+//  - codes are packed in the order of the MMA's A fragment, so a 16-byte
+//    load is four fragments; two or three instructions turn a pair of codes
+//    into 16-bit whole numbers q - z, which bf16 and fp16 hold exactly;
+//  - mma.sync adds a group's products in fp32, and s times that sum goes to
+//    the row's fp32 accumulators: no weight is rounded, and a scale costs
+//    one instruction per four sums instead of one per pair of weights;
+//  - the second product's token tile has the high and the low part of h; both
+//    are added to the same sums.
+//
+// Why warp-level MMA here: at 4 bits a weight the SM has 366 cycles for a
+// tile. Decoding takes 224 of them on the integer pipe whatever follows;
+// mma.sync takes 131 per 8 tokens from registers the decode has just
+// written. The same tile through tensor memory (16-bit weights stored as
+// tcgen05's A operand, 128 x 16 x 16 MMAs) was built first and took about
+// 1000: each tile passed through four hand-overs between warps.
+#include <type_traits>
+
 #include "moe_sched.h"
 
 namespace moe {
 
 namespace {
 
-constexpr int kThreads = 640;      // warps: weights, MMA, tokens, -, 8 x codes, 8 x results
+constexpr int kGroups = 4;                 // groups of four warps
+constexpr int kWorkers = kGroups * 128;
+constexpr int kThreads = kWorkers + 64;    // the last two warps bring weights and tokens
 constexpr int kMaxStagesA = 24;
 constexpr int kMaxStagesB = 16;
-constexpr int kTmemA = 4;          // 16-bit weight tiles in tensor memory, 64 columns each
-constexpr int kMaxSums = 16;       // accumulators in tensor memory, in the other 256 columns
-constexpr int kResults = 256;      // threads of the result warps
+constexpr int kCap = 32;                   // tokens of an entry: 4 column blocks of 8
+constexpr int kSumStride = kTileRows + 4;  // column stride of the groups' sums: fragments' stores hit all banks
 
 struct Shared {
     uint64_t full_a[kMaxStagesA], empty_a[kMaxStagesA];
     uint64_t full_b[kMaxStagesB], empty_b[kMaxStagesB];
-    uint64_t full_t[kTmemA], empty_t[kTmemA];
-    uint64_t full_d[kMaxSums], empty_d[kMaxSums];
-    uint64_t drain;
-    uint32_t tmem;
     int abort;
     int active, nmax;
     int issued_a, issued_b;
     int reset;
-    Rests rests[2];  // of the two products
+    Rests rests[2];
 };
 
-// Eight codes to four pairs q - z. Code 2p is at bits 4p, code 2p + 1 at bits
-// 4p + 16, so a shift and a mask leave a pair; or-ing the exponent of 128
-// (bf16; 1024 in fp16) makes them 128 + q, and `zz` holds 128 + z twice.
-template <bool BF16> static __device__ __forceinline__ void decode(uint32_t w, uint32_t zz, uint32_t *out)
+// Eight codes to the four registers of an A fragment: pair p has its codes at
+// bits 4p and 4p + 16, so a shift and a mask leave a pair; or-ing the exponent
+// of 128 (bf16; 1024 in fp16) makes them 128 + q. za and zb hold 128 + z twice,
+// for the fragment's rows r and r + 8.
+template <bool BF16> static __device__ __forceinline__ void decode(uint32_t w, uint32_t za, uint32_t zb, uint32_t *out)
 {
 #pragma unroll
     for (int p = 0; p < 4; ++p) {
         const uint32_t v = ((w >> (4 * p)) & 0x000F000Fu) | (BF16 ? 0x43004300u : 0x64006400u);
         if (BF16)
-            asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(out[p]) : "r"(v), "r"(zz));
+            asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(out[p]) : "r"(v), "r"(p & 1 ? zb : za));
         else
-            asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(out[p]) : "r"(v), "r"(zz));
+            asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(out[p]) : "r"(v), "r"(p & 1 ? zb : za));
     }
 }
 
-static __device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t *r)
+static __device__ __forceinline__ uint4 lds16(uint32_t addr)
 {
-    asm volatile("tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, "
-                 "%13, %14, %15, %16};" ::"r"(addr),
-                 "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
-                 "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
-                 : "memory");
+    uint4 v;
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr));
+    return v;
+}
+
+static __device__ __forceinline__ uint32_t lds_u16(uint32_t addr)
+{
+    uint16_t v;
+    asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(addr));
+    return v;
+}
+
+static __device__ __forceinline__ uint32_t lds_u8(uint32_t addr)
+{
+    uint32_t v;
+    asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(addr));
+    return v;
+}
+
+// How a weight's tiles are quantised.
+struct Quant {
+    int shift;  // log2(group / 32)
+    bool zeros, scale_fp16;
+};
+
+// Adds one weight tile times NT * 8 tokens (in `planes` parts) to the sums of
+// this warp's 32 rows: acc[column block][16-row half][fragment]. tile: shared
+// memory, codes of this warp's rows at its start + warp's offset; tokens: [planes][4][NT * 8][32] 16-bit.
+template <int NT, bool BF16>
+static __device__ __forceinline__ void add_tile(float (&acc)[NT][2][4], uint32_t tile, int rows32, int lane, uint32_t tokens,
+                                                int planes, const Quant &qt)
+{
+    const uint32_t codes = tile + rows32 * 2048 + lane * 16;
+    const uint32_t scales = tile + 8192 + (rows32 * 32 + (lane >> 2)) * 2;
+    const uint32_t zeros = tile + 8192 + (1024 >> qt.shift) + rows32 * 32 + (lane >> 2);
+    const uint32_t tok = tokens + (lane >> 2) * 64 + (lane & 3) * 16;
+    const uint32_t one = BF16 ? 0x43004300u : 0x64006400u;
+    uint32_t z[4] = {one + 0x00080008u, one + 0x00080008u, one + 0x00080008u, one + 0x00080008u};
+    float c[NT][2][4];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            c[nt][i >> 2][i & 3] = 0.0f;
+    uint4 w = lds16(codes);
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {  // 32 inputs each
+        if (qt.zeros && (q & ((1 << qt.shift) - 1)) == 0) {
+#pragma unroll
+            for (int h = 0; h < 4; ++h)  // rows r, r + 8, r + 16, r + 24
+                z[h] = one + lds_u8(zeros + (q >> qt.shift) * 128 + h * 8) * 0x00010001u;
+        }
+        uint32_t f[4][4];  // [2 * sixteen inputs + 16-row half]
+        decode<BF16>(w.x, z[0], z[1], f[0]);
+        decode<BF16>(w.y, z[2], z[3], f[1]);
+        decode<BF16>(w.z, z[0], z[1], f[2]);
+        decode<BF16>(w.w, z[2], z[3], f[3]);
+        if (q < 3)
+            w = lds16(codes + (q + 1) * 512);
+        for (int p = 0; p < planes; ++p)
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+                const uint4 b = lds16(tok + ((p * 4 + q) * NT + nt) * 512);
+                mma_16816<BF16>(c[nt][0], f[0], b.x, b.y);
+                mma_16816<BF16>(c[nt][1], f[1], b.x, b.y);
+                mma_16816<BF16>(c[nt][0], f[2], b.z, b.w);
+                mma_16816<BF16>(c[nt][1], f[3], b.z, b.w);
+            }
+        if ((q & ((1 << qt.shift) - 1)) == (1 << qt.shift) - 1) {  // the group's end
+            float s[4];
+#pragma unroll
+            for (int h = 0; h < 4; ++h) {
+                const uint32_t raw = lds_u16(scales + (q >> qt.shift) * 256 + h * 16);
+                s[h] = qt.scale_fp16 ? __half2float(__ushort_as_half(static_cast<unsigned short>(raw)))
+                                     : __uint_as_float(raw << 16);
+            }
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    float &x = c[nt][i >> 2][i & 3];
+                    float &y = acc[nt][i >> 2][i & 3];
+                    y = fmaf(s[(i >> 2) * 2 + ((i >> 1) & 1)], x, y);
+                    x = 0.0f;
+                }
+        }
+    }
 }
 
 template <bool LINEAR, bool BF16>
@@ -71,83 +165,63 @@ __global__ void __launch_bounds__(kThreads, 1) int4_kernel(const __grid_constant
     extern __shared__ uint8_t dyn[];
     __shared__ Shared sh;
     const uint32_t dyn0 = smem_u32(dyn);
-    const uint32_t ring_b = (dyn0 + 1023u) & ~1023u;
+    const uint32_t ring_b = (dyn0 + 127u) & ~127u;
     const uint32_t ring_a = ring_b + a.bytes_b;
-    uint8_t *const ring_a_p = dyn + (ring_a - dyn0);
-    const int T8 = (a.T + 7) & ~7;
-    float *const acc = reinterpret_cast<float *>(ring_a_p + a.stages * a.stage_a);
-    const Lists li(acc + (LINEAR ? 0 : T8 * kTileRows), a.E, a.P);
+    const uint32_t after = ring_a + a.stages * a.stage_a;
+    float *const sums = reinterpret_cast<float *>(dyn + (after - dyn0));  // [group][column][kSumStride]
+    float *const acc_y = sums + kGroups * a.cols * kSumStride;            // [T][128], of the second product
+    const Lists li(acc_y + (LINEAR ? 0 : a.T * kTileRows), a.E, a.P);
 
     const int tid = threadIdx.x, warp = __shfl_sync(~0u, tid >> 5, 0), lane = tid & 31;
     const int G = gridDim.x, blk = blockIdx.x;
     volatile int *const abort = &sh.abort;
+    constexpr int kParts = LINEAR ? 1 : 2;  // tiles that share a token tile in the first product
 
     if (tid == 0) {
         sh.abort = sh.reset = sh.rests[0].n = sh.rests[1].n = sh.issued_a = sh.issued_b = 0;
         for (int i = 0; i < kMaxStagesA; ++i) {
             mbar_init(smem_u32(&sh.full_a[i]), 1);
-            mbar_init(smem_u32(&sh.empty_a[i]), 4 + 8);  // the warps that read codes, then scales
+            mbar_init(smem_u32(&sh.empty_a[i]), 4);
         }
         for (int i = 0; i < kMaxStagesB; ++i) {
             mbar_init(smem_u32(&sh.full_b[i]), 1);
-            mbar_init(smem_u32(&sh.empty_b[i]), 1);
+            mbar_init(smem_u32(&sh.empty_b[i]), 4 * kParts);
         }
-        for (int i = 0; i < kTmemA; ++i) {
-            mbar_init(smem_u32(&sh.full_t[i]), 4);
-            mbar_init(smem_u32(&sh.empty_t[i]), 1);
-        }
-        for (int i = 0; i < kMaxSums; ++i) {
-            mbar_init(smem_u32(&sh.full_d[i]), 1);
-            mbar_init(smem_u32(&sh.empty_d[i]), 8);
-        }
-        mbar_init(smem_u32(&sh.drain), 1);
         mbar_init_fence();
         tma_prefetch_map(&a.mx);
-        if (!LINEAR)
-            tma_prefetch_map(&a.mh);
     }
-    if (warp == 1)
-        tmem_alloc(smem_u32(&sh.tmem), 512);
-
     if (LINEAR) {  // one "expert" whose tokens are the rows of x
         if (tid == 0) {
-            li.expert[0] = 0;
+            const int half = a.T > kCap ? ((a.T + 1) / 2 + 7) & ~7 : a.T;
+            sh.active = a.T > kCap ? 2 : 1;
+            sh.nmax = half;
+            li.expert[0] = li.expert[1] = 0;
             li.offset[0] = 0;
-            li.offset[1] = static_cast<unsigned short>(a.T);
-            sh.active = 1;
-            sh.nmax = a.T;
+            li.offset[1] = static_cast<unsigned short>(half);
+            li.offset[sh.active] = static_cast<unsigned short>(a.T);
         }
     } else {
-        build_lists(a, li, sh, tid, kThreads);
+        build_lists(a, li, sh, tid, kThreads, kCap);
     }
-    tc_fence_before();
     __syncthreads();
-    tc_fence_after();
-    const uint32_t tmem = sh.tmem;
     const int A = sh.active;
 
     if (A == 0) {
         clear_out(a, blk, G, tid, kThreads);
-        __syncthreads();
-        if (warp == 1)
-            tmem_free(tmem, 512);
         return;
     }
 
-    // gate and up (or one) tiles of the first product; the second product of the experts
-    constexpr int kParts = LINEAR ? 1 : 2;
     const int total1 = A * a.mt1 * a.kc1, total2 = LINEAR ? 0 : A * a.mt2 * a.kc2;
     const Shares shares1(total1, G), shares2(total2, G);
     const int begin1 = shares1.begin(blk), end1 = shares1.begin(blk + 1);
     const int begin2 = LINEAR ? 0 : shares2.begin(blk), end2 = LINEAR ? 0 : shares2.begin(blk + 1);
     const int pairs = li.offset[A];
-    const int width = LINEAR ? ceil_div(sh.nmax, 16) * 16 : ceil_div(sh.nmax, 8) * 16;  // rows of a token tile, columns of a sum
-    const int stage_b = width * 256;  // two 64-input halves
+    const int stage_b = ceil_div(sh.nmax, 8) * (LINEAR ? 2048 : 4096);  // 8 tokens x 128 inputs: 2 KB, h in two parts
     const int stages_b = min(kMaxStagesB, a.bytes_b / stage_b);
-    const int sums = min(kMaxSums, 256 / width);
-    const int groups1 = 4 >> a.shift1, groups2 = 4 >> a.shift2;
+    // h: per entry and chunk a tile [2 parts][4][tokens][32], tokens a multiple of 8
+    const auto h_entry = [&](int i) { return a.h + static_cast<size_t>(li.offset[i] + 7 * i) * a.h_stride; };
 
-    if (warp == 0 && elect_one()) {
+    if (warp == kWorkers / 32 && elect_one()) {
         // ---- weight tiles ----
         const uint64_t policy = policy_evict_first();
         Cursor at;
@@ -176,13 +250,12 @@ __global__ void __launch_bounds__(kThreads, 1) int4_kernel(const __grid_constant
                 run = load(src, a.tile2);
         }
         sh.issued_a = issued;
-    } else if (warp == 2 && elect_one()) {
+    } else if (warp == kWorkers / 32 + 1 && elect_one()) {
         // ---- token tiles ----
         Cursor at;
         int issued = 0;
         bool run = true;
         uint32_t dst = 0, bar = 0;
-        const uint32_t half = width * 128;  // from the tile's first 64 inputs to the others
         auto acquire = [&](uint32_t bytes) {
             if (!mbar_wait(smem_u32(&sh.empty_b[at.s]), at.parity ^ 1, abort, kWaitEmptyB))
                 return false;
@@ -194,236 +267,160 @@ __global__ void __launch_bounds__(kThreads, 1) int4_kernel(const __grid_constant
             return true;
         };
         for (Walk w(begin1, end1, a.kc1, a.mt1, false); run && w.more(); w.next()) {
-            const int n = li.count(w.i);
-            const unsigned char *const tok = li.token + li.offset[w.i];
-            const uint32_t bytes = LINEAR ? ceil_div(n, 8) * 2048 : ceil_div(n, 4) * 1024;
+            const int n = li.count(w.i), n8 = (n + 7) & ~7, off = li.offset[w.i];
+            const unsigned char *const tok = li.token + off;
+            const uint32_t bytes = (LINEAR ? n8 : (n + 3) & ~3) * 256;
             for (int k = w.k; k < w.k + w.len && (run = acquire(bytes)); ++k) {
-                if (LINEAR)
-                    for (int j = 0; j < n; j += 8) {
-                        tma_load_2d(dst + j * 128, &a.mx, bar, k * 128, j);
-                        tma_load_2d(dst + half + j * 128, &a.mx, bar, k * 128 + 64, j);
-                    }
-                else
+                if (LINEAR) {
+                    for (int j = 0; j < n; j += 8)
+                        for (int q = 0; q < 4; ++q)
+                            tma_load_2d(dst + (q * n8 + j) * 64, &a.mx, bar, k * 128 + q * 32, off + j);
+                } else {
                     for (int j = 0; j < n; j += 4) {  // short of a fourth row: the last one again
                         const int r0 = tok[j], r1 = tok[min(j + 1, n - 1)], r2 = tok[min(j + 2, n - 1)],
                                   r3 = tok[min(j + 3, n - 1)];
-                        tma_gather4(dst + j * 128, &a.mx, bar, k * 128, r0, r1, r2, r3);
-                        tma_gather4(dst + half + j * 128, &a.mx, bar, k * 128 + 64, r0, r1, r2, r3);
+                        for (int q = 0; q < 4; ++q)
+                            tma_gather4(dst + (q * n8 + j) * 64, &a.mx, bar, k * 128 + q * 32, r0, r1, r2, r3);
                     }
+                }
             }
         }
-        if (run && begin2 < end2) {
+        if (run && begin2 < end2) {  // h is complete
             run = wait_count(a.done, a.mt1 * pairs, abort, kWaitDone);
             fence_async_proxy();
         }
+        const uint64_t policy = policy_evict_first();
         for (Walk w(begin2, end2, a.kc2, A, true); run && w.more(); w.next()) {
-            const int off = li.offset[w.i], n8 = ceil_div(li.count(w.i), 8);
-            for (int k = w.k; k < w.k + w.len && (run = acquire(n8 * 4096)); ++k)
-                for (int b = 0; b < n8; ++b) {
-                    const int x = k * 128, r = off + b * 8;
-                    tma_load_2d(dst + b * 1024, &a.mh, bar, x, r);
-                    tma_load_2d(dst + (n8 + b) * 1024, &a.mh, bar, x, a.P + r);
-                    tma_load_2d(dst + half + b * 1024, &a.mh, bar, x + 64, r);
-                    tma_load_2d(dst + half + (n8 + b) * 1024, &a.mh, bar, x + 64, a.P + r);
-                }
+            const uint32_t bytes = ceil_div(li.count(w.i), 8) * 4096;
+            const uint8_t *src = reinterpret_cast<const uint8_t *>(h_entry(w.i)) + static_cast<size_t>(w.k) * bytes;
+            for (int k = 0; k < w.len && (run = acquire(bytes)); ++k, src += bytes)
+                bulk_load(dst, src, bytes, bar, policy);
         }
         sh.issued_b = issued;
-    } else if (warp == 1 && elect_one()) {
-        // ---- matrix instructions ----
-        Cursor at_t, at_b, at_d;
-        bool run = true;
-        for (int product = 0; run && product < 2; ++product) {
-            const int parts = product ? 1 : kParts, groups = product ? groups2 : groups1, steps = 8 / groups;
-            for (Walk w(product ? begin2 : begin1, product ? end2 : end1, product ? a.kc2 : a.kc1,
-                        product ? A : a.mt1, product != 0);
-                 run && w.more(); w.next()) {
-                const int n = li.count(w.i);
-                const int N = product ? ceil_div(n, 8) * 16 : ceil_div(n, 16) * 16;
-                const uint32_t idesc = idesc_f16(kTileRows, N, BF16);
-                for (int k = 0; run && k < w.len; ++k) {
-                    run = mbar_wait(smem_u32(&sh.full_b[at_b.s]), at_b.parity, abort, kWaitFullB);
-                    const uint64_t db = desc_sw128(ring_b + at_b.s * stage_b);
-                    for (int g = 0; run && g < parts; ++g) {
-                        run = mbar_wait(smem_u32(&sh.full_t[at_t.s]), at_t.parity, abort, kWaitFullA);
-                        int k16 = 0;  // sixteenths of inputs within the tile
-                        for (int q = 0; run && q < groups; ++q) {
-                            run = mbar_wait(smem_u32(&sh.empty_d[at_d.s]), at_d.parity ^ 1, abort, kWaitEmptyD);
-                            if (!run)
-                                break;
-                            tc_fence_after();
-                            for (int c = 0; c < steps; ++c, ++k16)
-                                mma_ts(tmem + 256 + at_d.s * width, tmem + at_t.s * 64 + k16 * 8,
-                                       db + (k16 >> 2) * (width * 8) + 2 * (k16 & 3), idesc, c > 0);
-                            tc_commit(smem_u32(&sh.full_d[at_d.s]));
-                            at_d.next(sums);
-                        }
-                        tc_commit(smem_u32(&sh.empty_t[at_t.s]));
-                        at_t.next(kTmemA);
-                    }
-                    tc_commit(smem_u32(&sh.empty_b[at_b.s]));
-                    at_b.next(stages_b);
-                }
-            }
-        }
-        tc_commit(smem_u32(&sh.drain));
-        mbar_wait(smem_u32(&sh.drain), 0, nullptr, kWaitOther);
-    } else if (warp >= 4 && warp < 12) {
-        // ---- codes to 16-bit weights in tensor memory; the two warpgroups take tiles in turn ----
-        const int wg = (warp - 4) >> 2, row = tid & 127;
-        const uint32_t lanes = tmem + (static_cast<uint32_t>(warp & 3) << 21);
-        const int tiles1 = (end1 - begin1) * kParts, tiles = tiles1 + (end2 - begin2);
-        Cursor at_a, at_t;
-        bool run = true;
-        if (wg) {
+    } else if (warp < kWorkers / 32) {
+        // ---- products ----
+        const int grp = warp >> 2, rows32 = warp & 3, row = tid & 127;
+        const Quant q1{a.shift1, a.zeros1 != 0, a.scale_fp16 != 0}, q2{a.shift2, a.zeros2 != 0, a.scale_fp16 != 0};
+        Cursor at_a, at_b;  // of this group's next tile
+        int turn = grp;     // tiles until this group's
+        for (int i = 0; i < grp; ++i) {
             at_a.next(a.stages);
-            at_t.next(kTmemA);
+            if (i % kParts == kParts - 1)
+                at_b.next(stages_b);
         }
-        for (int it = wg; run && it < tiles; it += 2) {
-            const bool second = it >= tiles1;
-            const int shift = second ? a.shift2 : a.shift1;  // log2 of the group in 32 inputs
-            const bool zeros = second ? a.zeros2 : a.zeros1;
-            const int s = at_a.s, t = at_t.s;
-            run = mbar_wait(smem_u32(&sh.full_a[s]), at_a.parity, abort, kWaitFullA) &&
-                  mbar_wait(smem_u32(&sh.empty_t[t]), at_t.parity ^ 1, abort, kWaitEmptyA);
-            at_a.next(a.stages);
-            at_a.next(a.stages);
-            at_t.next(kTmemA);
-            at_t.next(kTmemA);
-            run = __all_sync(~0u, run);
-            if (!run)
-                break;
-            tc_fence_after();
-            const uint8_t *const tile = ring_a_p + s * a.stage_a;
-            const uint8_t *const zp = tile + 8192 + (1024 >> shift) + row;
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                const uint4 w = *reinterpret_cast<const uint4 *>(tile + q * 2048 + row * 16);
-                const uint32_t z = zeros ? zp[(q >> shift) * 128] : 8;
-                const uint32_t zz = (BF16 ? 0x43004300u : 0x64006400u) + z * 0x10001u;
-                uint32_t r[16];
-                decode<BF16>(w.x, zz, r);
-                decode<BF16>(w.y, zz, r + 4);
-                decode<BF16>(w.z, zz, r + 8);
-                decode<BF16>(w.w, zz, r + 12);
-                tmem_st16(lanes + t * 64 + q * 16, r);
-            }
-            tmem_wait_st();
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) {
-                mbar_arrive(smem_u32(&sh.empty_a[s]));
-                mbar_arrive(smem_u32(&sh.full_t[t]));
-            }
-        }
-    } else if (warp >= 12) {
-        // ---- scales and results; the two warpgroups share the columns ----
-        const int wg = (warp - 12) >> 2, row = tid & 127, rtid = tid - 384;
-        const uint32_t lanes = tmem + 256 + (static_cast<uint32_t>(warp & 3) << 21);
-        Cursor at_a, at_d;
         bool run = true;
-        float v[2][32];  // sums of this thread's row: gate and up (or the one product), up to 32 columns
 
+        // This group's tiles of a run of `tiles`; its sums go to shared memory.
+        auto products = [&](auto blocks, int tiles, bool second) {
+            constexpr int NT = decltype(blocks)::value;
+            const Quant &qt = second ? q2 : q1;
+            float acc[NT][2][4];
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    acc[nt][i >> 2][i & 3] = 0.0f;
+            for (; run && turn < tiles; turn += kGroups) {
+                run = mbar_wait_warp(smem_u32(&sh.full_b[at_b.s]), at_b.parity, abort, kWaitFullB) &&
+                      mbar_wait_warp(smem_u32(&sh.full_a[at_a.s]), at_a.parity, abort, kWaitFullA);
+                if (!run)
+                    break;
+                add_tile<NT, BF16>(acc, ring_a + at_a.s * a.stage_a, rows32, lane, ring_b + at_b.s * stage_b,
+                                   second ? 2 : 1, qt);
+                __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive(smem_u32(&sh.empty_a[at_a.s]));
+                    mbar_arrive(smem_u32(&sh.empty_b[at_b.s]), second ? kParts : 1);
+                }
+                // the group's next tile is four on
+                for (int i = 0; i < kGroups; ++i)
+                    at_a.next(a.stages);
+                for (int i = 0; i < (second ? kGroups : kGroups / kParts); ++i)
+                    at_b.next(stages_b);
+            }
+            turn -= tiles;
+            named_sync(1, kWorkers);  // the sums of the run before are read
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const int col = nt * 8 + (lane & 3) * 2 + (i & 1);
+                    const int r = rows32 * 32 + (i >> 2) * 16 + ((i >> 1) & 1) * 8 + (lane >> 2);
+                    sums[(grp * a.cols + col) * kSumStride + r] = acc[nt][i >> 2][i & 3];
+                }
+            run = named_all(2, kWorkers, run);
+        };
+        auto run_products = [&](int n, int tiles, bool second) {
+            if (n <= 8)
+                products(std::integral_constant<int, 1>{}, tiles, second);
+            else if (n <= 16)
+                products(std::integral_constant<int, 2>{}, tiles, second);
+            else if (n <= 24)
+                products(std::integral_constant<int, 3>{}, tiles, second);
+            else
+                products(std::integral_constant<int, 4>{}, tiles, second);
+        };
+        // Column j of the groups' sums, this thread's row: all groups, or the even (0) or odd (1) ones.
+        auto sum_all = [&](int j) {
+            const float *const s = sums + j * kSumStride + row;
+            const int g = a.cols * kSumStride;
+            return (s[0] + s[g]) + (s[2 * g] + s[3 * g]);
+        };
+        auto sum_half = [&](int j, int odd) {
+            const float *const s = sums + j * kSumStride + row;
+            const int g = a.cols * kSumStride;
+            return s[odd * g] + s[(2 + odd) * g];
+        };
+
+        // As in moe_experts.cu: tiles shared with other blocks are settled after a product's last run.
         auto leave = [&](Rests &rests, int i, int m, const Split &sp, int *counter) {
-            if (rtid == 0)
+            if (tid == 0)
                 rests.of[rests.n++] = Rest{i, m, sp};
-            named_sync(1, kResults);
-            if (rtid == 0)
+            named_sync(1, kWorkers);
+            if (tid == 0)
                 add_acq_rel(counter, 1);
         };
         auto parts_written = [&](int *counter, const Split &sp) {
-            return named_all(2, kResults, rtid != 0 || wait_count(counter, sp.parts(), abort, kWaitOther));
+            return named_all(2, kWorkers, tid != 0 || wait_count(counter, sp.parts(), abort, kWaitOther));
         };
         auto announce = [&](int columns) {
             fence_async_proxy();
-            named_sync(1, kResults);
-            if (rtid == 0)
+            named_sync(1, kWorkers);
+            if (tid == 0)
                 add_acq_rel(a.done, columns);
         };
-        // Adds s times the sum of each group of one weight tile to v[p], columns [c0, c0 + 8 nb) of the sum and,
-        // where lo > 0, those `lo` further.
-        auto add_tile = [&](float *p, int groups, int c0, int nb, int lo) {
-            run = run && mbar_wait(smem_u32(&sh.full_a[at_a.s]), at_a.parity, abort, kWaitFullA);
-            const uint8_t *const sc = ring_a_p + at_a.s * a.stage_a + 8192;
-            for (int q = 0; q < groups; ++q) {
-                const int d = at_d.s;
-                run = run && mbar_wait(smem_u32(&sh.full_d[d]), at_d.parity, abort, kWaitFullD);
-                run = __all_sync(~0u, run);
-                if (!run)
-                    return;
-                tc_fence_after();
-                const uint16_t raw = *reinterpret_cast<const uint16_t *>(sc + q * 256 + row * 2);
-                const float s = a.scale_fp16 ? __half2float(__ushort_as_half(raw))
-                                             : __uint_as_float(static_cast<uint32_t>(raw) << 16);
-#pragma unroll
-                for (int b = 0; b < 4; ++b)
-                    if (b < nb) {
-                        float x[8], y[8];
-                        tmem_ld8(lanes + d * width + c0 + b * 8, x);
-                        if (lo > 0)
-                            tmem_ld8(lanes + d * width + lo + c0 + b * 8, y);
-                        tmem_wait_ld();
-#pragma unroll
-                        for (int c = 0; c < 8; ++c)
-                            p[b * 8 + c] = fmaf(s, lo > 0 ? x[c] + y[c] : x[c], p[b * 8 + c]);
-                    }
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0)
-                    mbar_arrive(smem_u32(&sh.empty_d[d]));
-                at_d.next(sums);
-            }
-            __syncwarp();
-            if (lane == 0)
-                mbar_arrive(smem_u32(&sh.empty_a[at_a.s]));
-            at_a.next(a.stages);
-        };
-
         // column j of row tile m: h, or y of the linear layer
-        auto result = [&](int off, int m, int j, float gate, float up) {
+        auto result = [&](int i, int m, int j, float gate, float up) {
             const int col = m * kTileRows + row;
-            if (col >= a.I)
-                return;
             if (LINEAR) {
-                uint16_t *const p = static_cast<uint16_t *>(a.out) + j * a.out_stride + col;
-                if (EP_IN_BOUNDS(a.chk, epk::kSiteMoeOut, p, 2, a.out, 2 * ((a.T - 1) * a.out_stride + a.I)))
+                uint16_t *const p = static_cast<uint16_t *>(a.out) + (li.offset[i] + j) * a.out_stride + col;
+                if (col < a.I &&
+                    EP_IN_BOUNDS(a.chk, epk::kSiteMoeOut, p, 2, a.out, 2 * ((a.T - 1) * a.out_stride + a.I)))
                     *p = BF16 ? __bfloat16_as_ushort(__float2bfloat16_rn(gate))
                               : __half_as_ushort(__float2half_rn(gate));
-            } else {
-                __nv_bfloat16 hi, lo;
-                split(swiglu(gate, up), hi, lo);
-                a.h[static_cast<size_t>(off + j) * a.h_stride + col] = hi;
-                a.h[static_cast<size_t>(a.P + off + j) * a.h_stride + col] = lo;
+            } else {  // rows past the intermediate size have scales of 0: their h is 0, as the token tiles need
+                const int n8 = (li.count(i) + 7) & ~7;
+                __nv_bfloat16 *const p = h_entry(i) + static_cast<size_t>(m) * n8 * 256 + ((row >> 5) * n8 + j) * 32 + (row & 31);
+                split(swiglu(gate, up), p[0], p[n8 * 128]);
             }
         };
+        const int set = tid >> 7;  // of columns
 
         for (Walk w(begin1, end1, a.kc1, a.mt1, false); run && w.more(); w.next()) {
-            const int off = li.offset[w.i], n = li.count(w.i), tile = w.i * a.mt1 + w.m;
-            const int blocks = ceil_div(n, 8), half = ceil_div(blocks, 2);  // columns by eights: this warpgroup's
-            const int c0 = wg ? half * 8 : 0, nb = wg ? blocks - half : half;
+            const int n = li.count(w.i), tile = w.i * a.mt1 + w.m;
             const Split sp(shares1, tile * a.kc1, a.kc1);
-#pragma unroll
-            for (int c = 0; c < 32; ++c)
-                v[0][c] = v[1][c] = 0.0f;
-            for (int k = 0; run && k < w.len; ++k) {
-                add_tile(v[0], groups1, c0, nb, 0);
-                if (!LINEAR)
-                    add_tile(v[1], groups1, c0, nb, 0);
-            }
-            run = named_all(2, kResults, run);
+            run_products(n, w.len * kParts, false);
             if (!run)
                 break;
             float *const part = a.part + static_cast<size_t>(sp.slot(blk)) * a.part_floats + row;
-#pragma unroll
-            for (int c = 0; c < 32; ++c) {
-                const int j = c0 + c;
-                if (c < nb * 8 && j < n) {
-                    if (sp.shared()) {
-                        part[j * kTileRows] = v[0][c];
-                        if (!LINEAR)
-                            part[(n + j) * kTileRows] = v[1][c];
-                    } else {
-                        result(off, w.m, j, v[0][c], v[1][c]);
-                    }
+            for (int j = set; j < n; j += kGroups) {
+                const float g = LINEAR ? sum_all(j) : sum_half(j, 0), u = LINEAR ? 0.0f : sum_half(j, 1);
+                if (sp.shared()) {
+                    part[j * kTileRows] = g;
+                    if (!LINEAR)
+                        part[(n + j) * kTileRows] = u;
+                } else {
+                    result(w.i, w.m, j, g, u);
                 }
             }
             if (sp.shared())
@@ -433,7 +430,7 @@ __global__ void __launch_bounds__(kThreads, 1) int4_kernel(const __grid_constant
         }
         for (int r = 0; run && r < sh.rests[0].n; ++r) {
             const Rest &rest = sh.rests[0].of[r];
-            const int i = rest.i, m = rest.m, off = li.offset[i], n = li.count(i);
+            const int i = rest.i, m = rest.m, n = li.count(i);
             const Split sp = rest.sp;
             const int lo = sp.column(n, blk), hi = sp.column(n, blk + 1);
             if (lo == hi)
@@ -441,20 +438,24 @@ __global__ void __launch_bounds__(kThreads, 1) int4_kernel(const __grid_constant
             run = parts_written(a.tiles + i * a.mt1 + m, sp);
             if (!run)
                 break;
-            for (int j = lo + 2 * wg; j < hi; j += 4) {
-                float g[2], u[2] = {};
-                sum_parts<2>(a.part + j * kTileRows + row, a.part_floats, sp, hi - j, g);
+            for (int j = lo + set; j < hi; j += kGroups) {
+                float g[1], u[1] = {};
+                sum_parts<1>(a.part + j * kTileRows + row, a.part_floats, sp, 1, g);
                 if (!LINEAR)
-                    sum_parts<2>(a.part + (n + j) * kTileRows + row, a.part_floats, sp, hi - j, u);
-#pragma unroll
-                for (int c = 0; c < 2; ++c)
-                    if (j + c < hi)
-                        result(off, m, j + c, g[c], u[c]);
+                    sum_parts<1>(a.part + (n + j) * kTileRows + row, a.part_floats, sp, 1, u);
+                result(i, m, j, g[0], u[0]);
             }
             if (!LINEAR)
                 announce(hi - lo);
         }
 
+        if (!LINEAR) {  // the groups' turns and token tiles start anew
+            const int tiles1 = (end1 - begin1) * 2;
+            turn = (grp + kGroups - tiles1 % kGroups) % kGroups;
+            at_a = at_b = Cursor();
+            at_a.skip(tiles1 + turn, a.stages);
+            at_b.skip(end1 - begin1 + turn, stages_b);
+        }
         const int group = LINEAR ? 1 : A * a.kc2;
         auto store_y = [&](int m, int t, float r) {
             const int col = m * kTileRows + row;
@@ -465,41 +466,29 @@ __global__ void __launch_bounds__(kThreads, 1) int4_kernel(const __grid_constant
         for (Walk w(begin2, end2, a.kc2, A, true); !LINEAR && run && w.more();) {
             const int m = w.m, i0 = w.i;
             const Split sp(shares2, m * group, group);
-            for (int t = wg; t < a.T; t += 2)
-                acc[t * kTileRows + row] = 0.0f;
+            for (int t = set; t < a.T; t += kGroups)
+                acc_y[t * kTileRows + row] = 0.0f;
             for (; run && w.more() && w.m == m; w.next()) {
                 const int off = li.offset[w.i], n = li.count(w.i);
-                const int blocks = ceil_div(n, 8), half = ceil_div(blocks, 2);
-                const int c0 = wg ? half * 8 : 0, nb = wg ? blocks - half : half;
-#pragma unroll
-                for (int c = 0; c < 32; ++c)
-                    v[0][c] = 0.0f;
-                for (int k = 0; run && k < w.len; ++k)
-                    add_tile(v[0], groups2, c0, nb, blocks * 8);
-                // also: the other warpgroup's rows of acc for the experts before are written
-                run = named_all(2, kResults, run);
-                if (!run)
-                    break;
-#pragma unroll
-                for (int c = 0; c < 32; ++c)
-                    if (c < nb * 8 && c0 + c < n) {
-                        float *const s = acc + li.token[off + c0 + c] * kTileRows + row;
-                        *s = fmaf(li.weight[off + c0 + c], v[0][c], *s);
-                    }
+                run_products(n, w.len, true);  // its barriers also order the threads' turns at a row of acc_y
+                for (int j = set; run && j < n; j += kGroups) {
+                    float *const s = acc_y + li.token[off + j] * kTileRows + row;
+                    *s = fmaf(li.weight[off + j], sum_all(j), *s);
+                }
             }
-            run = named_all(2, kResults, run);
+            run = named_all(2, kWorkers, run);
             if (!run)
                 break;
             if (sp.shared()) {
                 float *const part = a.part + static_cast<size_t>(sp.slot(blk)) * a.part_floats + row;
-                for (int t = wg; t < a.T; t += 2)
-                    part[t * kTileRows] = acc[t * kTileRows + row];
-                leave(sh.rests[1], i0, m, sp, a.tiles + a.E * a.mt1 + m);
+                for (int t = set; t < a.T; t += kGroups)
+                    part[t * kTileRows] = acc_y[t * kTileRows + row];
+                leave(sh.rests[1], i0, m, sp, a.tiles + 2 * a.E * a.mt1 + m);
             } else {
-                for (int t = wg; t < a.T; t += 2)
-                    store_y(m, t, acc[t * kTileRows + row]);
-                named_sync(1, kResults);  // acc is read before the next row tile clears it
+                for (int t = set; t < a.T; t += kGroups)
+                    store_y(m, t, acc_y[t * kTileRows + row]);
             }
+            // a thread clears and reads the same tokens of acc_y: no barrier until the next products
         }
         for (int r = 0; !LINEAR && run && r < sh.rests[1].n; ++r) {
             const Rest &rest = sh.rests[1].of[r];
@@ -507,25 +496,20 @@ __global__ void __launch_bounds__(kThreads, 1) int4_kernel(const __grid_constant
             const int m = rest.m, lo = sp.column(a.T, blk), hi = sp.column(a.T, blk + 1);
             if (lo == hi)
                 continue;
-            run = parts_written(a.tiles + a.E * a.mt1 + m, sp);
+            run = parts_written(a.tiles + 2 * a.E * a.mt1 + m, sp);
             if (!run)
                 break;
-            for (int t = lo + 2 * wg; t < hi; t += 4) {
-                float x[2];
-                sum_parts<2>(a.part + t * kTileRows + row, a.part_floats, sp, hi - t, x);
-#pragma unroll
-                for (int c = 0; c < 2; ++c)
-                    if (t + c < hi)
-                        store_y(m, t + c, x[c]);
+            for (int t = lo + set; t < hi; t += kGroups) {
+                float x[1];
+                sum_parts<1>(a.part + t * kTileRows + row, a.part_floats, sp, 1, x);
+                store_y(m, t, x[0]);
             }
         }
     }
     __syncwarp();
-    tc_fence_before();
     __syncthreads();
-    tc_fence_after();
 
-    if (sh.abort) {
+    if (sh.abort) {  // copies in flight land before the block's memory is given back
         if (tid == 0) {
             for (int i = max(0, sh.issued_a - a.stages); i < sh.issued_a; ++i)
                 mbar_wait(smem_u32(&sh.full_a[i % a.stages]), (i / a.stages) & 1, nullptr, kWaitOther);
@@ -537,8 +521,6 @@ __global__ void __launch_bounds__(kThreads, 1) int4_kernel(const __grid_constant
         }
         __syncthreads();
     }
-    if (warp == 1)
-        tmem_free(tmem, 512);
 
     if (tid == 0)
         sh.reset = add_acq_rel(a.leaving, 1) == G - 1;
@@ -547,51 +529,53 @@ __global__ void __launch_bounds__(kThreads, 1) int4_kernel(const __grid_constant
         for (int i = tid; i < A * a.mt1; i += kThreads)
             a.tiles[i] = 0;
         for (int i = tid; !LINEAR && i < a.mt2; i += kThreads)
-            a.tiles[a.E * a.mt1 + i] = 0;
+            a.tiles[2 * a.E * a.mt1 + i] = 0;
         if (tid == 0)
             *a.done = *a.leaving = 0;
     }
 }
 
-// One thread per 32 codes of a tile: [4][128 rows][16 bytes], then scales and
-// zero points [groups][128 rows]. Rows and inputs outside the matrix become
-// codes of 0 with a scale of 0.
+// One thread per 32 codes of a tile. Codes: [4 x 32 rows][4 x 32 inputs][lane][4 words];
+// word 2 s + f of lane 4 g + t is the A fragment of rows 16 f + g and + 8, inputs 8 t + 4 s
+// .. + 3 (the MMA's sixteen inputs are any sixteen, the token tiles are read in the same
+// order). Then scales and zero points [groups][128 rows]. Rows and inputs outside the
+// matrix become codes of 0 with a scale of 0.
 __global__ void __launch_bounds__(256) pack_kernel(const __grid_constant__ PackArgs a)
 {
     const long long id = static_cast<long long>(blockIdx.x) * 256 + threadIdx.x;
-    const int row = static_cast<int>(id & 127), q = static_cast<int>((id >> 7) & 3);
+    const int lane = static_cast<int>(id & 31), q = static_cast<int>((id >> 5) & 3), rb = static_cast<int>((id >> 7) & 3);
     const long long tile = id >> 9;
     if (tile >= a.mats * a.mt * a.kc)
         return;
     const long long mat = tile / (static_cast<long long>(a.mt) * a.kc);
     const int m = static_cast<int>(tile / a.kc - mat * a.mt), kc = static_cast<int>(tile % a.kc);
-    const int r = m * 128 + row, k = kc * 128 + q * 32;
-    const bool inside = r < a.rows && k < a.cols;  // cols is a multiple of 32
-    const long long src_row = mat * a.rows + r;
-    uint32_t in[4] = {0, 0, 0, 0}, out[4];
-    if (inside) {
-        const uint8_t *const p = a.codes + src_row * (a.cols / 2) + k / 2;
-        for (int i = 0; i < 16; ++i)
-            in[i / 4] |= static_cast<uint32_t>(p[i]) << (8 * (i % 4));
-    }
+    const int k = kc * 128 + q * 32 + (lane & 3) * 8;  // cols is a multiple of 32
+    uint32_t word[4] = {0, 0, 0, 0};
 #pragma unroll
-    for (int w = 0; w < 4; ++w) {  // codes 0..7 in order -> even ones in the low half, odd ones in the high half
-        uint32_t o = 0;
+    for (int half = 0; half < 4; ++half) {  // rows g, g + 8 of fragment 0, then of fragment 1
+        const int r = m * 128 + rb * 32 + half * 8 + (lane >> 2);
+        uint32_t in = 0;  // the row's 8 codes from k on
+        if (r < a.rows && k < a.cols) {
+            const uint8_t *const p = a.codes + (mat * a.rows + r) * (a.cols / 2) + k / 2;
+            in = p[0] | p[1] << 8 | p[2] << 16 | static_cast<uint32_t>(p[3]) << 24;
+        }
+        const int f = half >> 1, low = half & 1;  // fragment; its row r (0) or r + 8 (1)
 #pragma unroll
-        for (int c = 0; c < 8; ++c)
-            o |= ((in[w] >> (4 * c)) & 15u) << ((c >> 1) * 4 + (c & 1) * 16);
-        out[w] = o;
+        for (int c = 0; c < 8; ++c) {  // input 4 s + 2 v + e: word 2 s + f, pair 2 v + low, element e
+            const int s = c >> 2, v = (c >> 1) & 1, e = c & 1;
+            word[2 * s + f] |= ((in >> (4 * c)) & 15u) << ((2 * v + low) * 4 + e * 16);
+        }
     }
     uint8_t *const dst = a.dst + tile * a.tile_bytes;
-    *reinterpret_cast<uint4 *>(dst + q * 2048 + row * 16) = make_uint4(out[0], out[1], out[2], out[3]);
-    const int groups = 128 / a.group;
-    for (int g = q; g < groups; g += 4) {
-        const int kg = kc * 128 + g * a.group;
-        const bool in_g = r < a.rows && kg < a.cols;
-        const long long at = src_row * (a.cols / a.group) + kg / a.group;
-        reinterpret_cast<uint16_t *>(dst + 8192)[g * 128 + row] = in_g ? a.scales[at] : 0;
+    *reinterpret_cast<uint4 *>(dst + ((rb * 4 + q) * 32 + lane) * 16) = make_uint4(word[0], word[1], word[2], word[3]);
+    const int groups = 128 / a.group, row = rb * 32 + lane, r = m * 128 + row;
+    if (q < groups) {
+        const int kg = kc * 128 + q * a.group;
+        const bool in = r < a.rows && kg < a.cols;
+        const long long at = (mat * a.rows + r) * (a.cols / a.group) + kg / a.group;
+        reinterpret_cast<uint16_t *>(dst + 8192)[q * 128 + row] = in ? a.scales[at] : 0;
         if (a.zeros)
-            (dst + 8192 + groups * 256)[g * 128 + row] = in_g ? (a.zeros[at] & 15) : 0;
+            (dst + 8192 + groups * 256)[q * 128 + row] = in ? (a.zeros[at] & 15) : 0;
     }
 }
 
@@ -604,24 +588,33 @@ int int4_tile_bytes(int group, bool zeros)
 
 size_t int4_part_floats(int T, bool linear)
 {
-    const int T8 = (T + 7) & ~7;
-    return static_cast<size_t>(linear ? 1 : 2) * T8 * kTileRows;
+    const int n = T < kCap ? T : kCap;  // columns of an entry, gate and up, or tokens of a row tile of y
+    const int cols = linear ? n : (2 * n > T ? 2 * n : T);
+    return static_cast<size_t>(cols) * kTileRows;
+}
+
+size_t int4_h_rows(int T, int K, int E)
+{
+    // an entry's rows are rounded up to a multiple of 8: 7 more for each of up to two entries per expert
+    const int pairs = T * K, entries = pairs < 2 * E ? pairs : 2 * E;
+    return static_cast<size_t>(pairs) + 7 * static_cast<size_t>(entries) + 8;
 }
 
 size_t int4_smem(Int4Args *a, bool linear)
 {
-    const int T8 = (a->T + 7) & ~7;
-    const size_t lists = (linear ? 0 : static_cast<size_t>(T8) * kTileRows * 4) + lists_bytes(a->E, a->P);
-    a->bytes_b = T8 <= 8 ? 32 * 1024 : 64 * 1024;  // at least 2 stages of the largest token tile
+    a->cols = ((a->T < kCap ? a->T : kCap) + 7) & ~7;
+    const size_t lists = (linear ? 0 : static_cast<size_t>(a->T) * kTileRows * 4) +
+                         static_cast<size_t>(kGroups) * a->cols * kSumStride * 4 + lists_bytes(a->E, a->P);
+    a->bytes_b = a->cols <= 8 ? 32 * 1024 : 48 * 1024;  // at least 8 and 3 stages of the largest token tile
     a->shift1 = a->group1 == 32 ? 0 : a->group1 == 64 ? 1 : 2;
     a->shift2 = a->group2 == 32 ? 0 : a->group2 == 64 ? 1 : 2;
     a->stage_a = a->tile1 > a->tile2 ? a->tile1 : a->tile2;
     a->part_floats = static_cast<int>(int4_part_floats(a->T, linear));
-    const size_t room = kSmemMax - sizeof(Shared) - 1024 - lists - a->bytes_b - 64;
+    const size_t room = kSmemMax - sizeof(Shared) - 128 - lists - a->bytes_b - 64;
     a->stages = static_cast<int>(room / a->stage_a);
     if (a->stages > kMaxStagesA)
         a->stages = kMaxStagesA;
-    return 1024 + static_cast<size_t>(a->stages) * a->stage_a + a->bytes_b + lists;
+    return 128 + static_cast<size_t>(a->stages) * a->stage_a + a->bytes_b + lists;
 }
 
 cudaError_t launch_int4(const Int4Args &a, bool linear, bool bf16, int grid, size_t smem, cudaStream_t stream)

@@ -20,6 +20,12 @@ struct Cursor {
             parity ^= 1;
         }
     }
+    // To position i of the sequence.
+    __device__ __forceinline__ void skip(int i, int n)
+    {
+        s = i % n;
+        parity = (i / n) & 1;
+    }
 };
 
 // Walks a block's share [begin, end) of one product's units (chunks of
@@ -140,12 +146,13 @@ static __device__ __forceinline__ void split(float v, __nv_bfloat16 &hi, __nv_bf
 
 static __device__ __forceinline__ float swiglu(float gate, float up) { return gate / (1.0f + expf(-gate)) * up; }
 
-// Lists of the chosen experts, in dynamic shared memory.
+// Lists of the chosen experts, in dynamic shared memory. An entry is an expert
+// with up to `cap` of its tokens; an expert with more has two entries.
 struct Lists {
     unsigned long long *mask;  // [E] tokens of each expert
-    float *weight;             // [P] routing weight of each (expert, token) pair
-    unsigned short *expert;    // [E] active experts, ascending
-    unsigned short *offset;    // [E + 1] their first pair
+    float *weight;             // [P] routing weight of each (entry, token) pair
+    unsigned short *expert;    // [2 E] of each entry, ascending
+    unsigned short *offset;    // [2 E + 1] the entry's first pair
     unsigned char *token;      // [P] tokens, ascending per expert
 
     __device__ __forceinline__ Lists(void *at, int E, int P)
@@ -153,20 +160,21 @@ struct Lists {
         mask = static_cast<unsigned long long *>(at);
         weight = reinterpret_cast<float *>(mask + E);
         expert = reinterpret_cast<unsigned short *>(weight + P);
-        offset = expert + E;
-        token = reinterpret_cast<unsigned char *>(offset + E + 1);
+        offset = expert + 2 * E;
+        token = reinterpret_cast<unsigned char *>(offset + 2 * E + 1);
     }
     __device__ __forceinline__ int count(int i) const { return offset[i + 1] - offset[i]; }
 };
 
-static inline size_t lists_bytes(int E, int P) { return size_t(E) * 12 + size_t(P) * 5 + 2; }
+static inline size_t lists_bytes(int E, int P) { return size_t(E) * 16 + size_t(P) * 5 + 2; }
 
 // Builds the lists; every block does, from the ids themselves. A token's bit
 // in its expert's mask makes the order of the threads irrelevant. All
-// threads of the block call it; the caller synchronises before the lists are
-// read (active and nmax, the most tokens of one expert, before that too).
+// threads of the block call it; the caller synchronises before it reads
+// token and weight. sh.active: entries, sh.nmax: the most tokens of one.
 template <class Args, class Shared>
-static __device__ __forceinline__ void build_lists(const Args &a, const Lists &li, Shared &sh, int tid, int threads)
+static __device__ __forceinline__ void build_lists(const Args &a, const Lists &li, Shared &sh, int tid, int threads,
+                                                   int cap)
 {
     for (int e = tid; e < a.E; e += threads)
         li.mask[e] = 0;
@@ -181,11 +189,11 @@ static __device__ __forceinline__ void build_lists(const Args &a, const Lists &l
     __syncthreads();
     if (tid < 32) {
         const int lane = tid;
-        int n_active = 0, n_pairs = 0, nmax = 0;
+        int entries = 0, pairs = 0, nmax = 0;
         for (int e0 = 0; e0 < a.E; e0 += 32) {
             const int e = e0 + lane;
             const int n = e < a.E ? __popcll(li.mask[e]) : 0;
-            const unsigned live = __ballot_sync(~0u, n > 0);
+            const unsigned live = __ballot_sync(~0u, n > 0), two = __ballot_sync(~0u, n > cap);
             if (live == 0)
                 continue;
             int sum = n;  // inclusive prefix sum over the lanes
@@ -194,26 +202,35 @@ static __device__ __forceinline__ void build_lists(const Args &a, const Lists &l
                 if (lane >= d)
                     sum += v;
             }
+            const int half = n > cap ? (n + 1) / 2 : n;
             if (n > 0) {
-                const int at = n_active + __popc(live & ((1u << lane) - 1));
+                const unsigned before = (1u << lane) - 1;
+                const int at = entries + __popc(live & before) + __popc(two & before), off = pairs + sum - n;
                 li.expert[at] = static_cast<unsigned short>(e);
-                li.offset[at] = static_cast<unsigned short>(n_pairs + sum - n);
+                li.offset[at] = static_cast<unsigned short>(off);
+                if (n > cap) {
+                    li.expert[at + 1] = static_cast<unsigned short>(e);
+                    li.offset[at + 1] = static_cast<unsigned short>(off + half);
+                }
             }
-            n_active += __popc(live);
-            n_pairs += __shfl_sync(~0u, sum, 31);
-            nmax = max(nmax, __reduce_max_sync(~0u, n));
+            entries += __popc(live) + __popc(two);
+            pairs += __shfl_sync(~0u, sum, 31);
+            nmax = max(nmax, __reduce_max_sync(~0u, half));
         }
         if (lane == 0) {
-            li.offset[n_active] = static_cast<unsigned short>(n_pairs);
-            sh.active = n_active;
+            li.offset[entries] = static_cast<unsigned short>(pairs);
+            sh.active = entries;
             sh.nmax = nmax;
         }
     }
     __syncthreads();
     for (int i = tid; i < sh.active; i += threads) {
         const int e = li.expert[i];
-        int at = li.offset[i];
-        for (unsigned long long m = li.mask[e]; m; m &= m - 1, ++at) {
+        unsigned long long m = li.mask[e];
+        if (i > 0 && li.expert[i - 1] == e)  // the second entry: past the first one's tokens
+            for (int j = li.count(i - 1); j > 0; --j)
+                m &= m - 1;
+        for (int at = li.offset[i]; at < li.offset[i + 1]; ++at, m &= m - 1) {
             const int t = __ffsll(static_cast<long long>(m)) - 1;
             float w = 0.0f;  // an expert named twice by a token counts twice
             for (int k = 0; k < a.K; ++k)

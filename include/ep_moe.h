@@ -20,7 +20,7 @@
  * stay valid until it has run.
  *
  * The experts and linear kernels' blocks wait for one another (they are
- * launched cooperatively) and every wait has a limit of 2 s. If one runs out
+ * launched cooperatively) and every wait has a limit of about 2 s. If one runs out
  * the kernel ends, that call's output is undefined, and the handle's next
  * call returns EP_ERR_CUDA once.
  */
