@@ -89,38 +89,28 @@ static __device__ __forceinline__ uint32_t lds_u8(uint32_t addr)
     return v;
 }
 
-// How a weight's tiles are quantised.
-struct Quant {
-    int shift;  // log2(group / 32)
-    bool zeros, scale_fp16;
-};
-
-// Adds one weight tile times NT * 8 tokens (in `planes` parts) to the sums of
-// this warp's 32 rows: acc[column block][16-row half][fragment]. tile: shared
-// memory, codes of this warp's rows at its start + warp's offset; tokens: [planes][4][NT * 8][32] 16-bit.
-template <int NT, bool BF16>
+// Adds one weight tile times NT * 8 tokens (in PLANES parts) to the sums of
+// this warp's 32 rows: acc[column block][16-row half][fragment]. SHIFT:
+// log2(group / 32). tile: the tile in shared memory; tokens: [PLANES][4][NT * 8][32] 16-bit.
+template <int NT, int SHIFT, int PLANES, bool BF16>
 static __device__ __forceinline__ void add_tile(float (&acc)[NT][2][4], uint32_t tile, int rows32, int lane, uint32_t tokens,
-                                                int planes, const Quant &qt)
+                                                bool with_zeros, bool scale_fp16)
 {
+    constexpr int kQ = 1 << SHIFT;  // 32-input steps of a group
     const uint32_t codes = tile + rows32 * 2048 + lane * 16;
-    const uint32_t scales = tile + 8192 + (rows32 * 32 + (lane >> 2)) * 2;
-    const uint32_t zeros = tile + 8192 + (1024 >> qt.shift) + rows32 * 32 + (lane >> 2);
+    const uint32_t row = rows32 * 32 + (lane >> 2);
+    const uint32_t scales = tile + 8192 + row * 2, zeros = tile + 8192 + (1024 >> SHIFT) + row;
     const uint32_t tok = tokens + (lane >> 2) * 64 + (lane & 3) * 16;
-    const uint32_t one = BF16 ? 0x43004300u : 0x64006400u;
+    constexpr uint32_t one = BF16 ? 0x43004300u : 0x64006400u;
     uint32_t z[4] = {one + 0x00080008u, one + 0x00080008u, one + 0x00080008u, one + 0x00080008u};
     float c[NT][2][4];
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-            c[nt][i >> 2][i & 3] = 0.0f;
     uint4 w = lds16(codes);
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {  // 32 inputs each
-        if (qt.zeros && (q & ((1 << qt.shift) - 1)) == 0) {
+    for (int q = 0; q < 4; ++q) {
+        if (q % kQ == 0 && with_zeros) {
 #pragma unroll
             for (int h = 0; h < 4; ++h)  // rows r, r + 8, r + 16, r + 24
-                z[h] = one + lds_u8(zeros + (q >> qt.shift) * 128 + h * 8) * 0x00010001u;
+                z[h] = one + lds_u8(zeros + (q >> SHIFT) * 128 + h * 8) * 0x00010001u;
         }
         uint32_t f[4][4];  // [2 * sixteen inputs + 16-row half]
         decode<BF16>(w.x, z[0], z[1], f[0]);
@@ -129,31 +119,35 @@ static __device__ __forceinline__ void add_tile(float (&acc)[NT][2][4], uint32_t
         decode<BF16>(w.w, z[2], z[3], f[3]);
         if (q < 3)
             w = lds16(codes + (q + 1) * 512);
-        for (int p = 0; p < planes; ++p)
+#pragma unroll
+        for (int p = 0; p < PLANES; ++p)
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
                 const uint4 b = lds16(tok + ((p * 4 + q) * NT + nt) * 512);
-                mma_16816<BF16>(c[nt][0], f[0], b.x, b.y);
-                mma_16816<BF16>(c[nt][1], f[1], b.x, b.y);
-                mma_16816<BF16>(c[nt][0], f[2], b.z, b.w);
-                mma_16816<BF16>(c[nt][1], f[3], b.z, b.w);
+                if (q % kQ == 0 && p == 0) {
+                    mma_16816<BF16, false>(c[nt][0], f[0], b.x, b.y);
+                    mma_16816<BF16, false>(c[nt][1], f[1], b.x, b.y);
+                } else {
+                    mma_16816<BF16, true>(c[nt][0], f[0], b.x, b.y);
+                    mma_16816<BF16, true>(c[nt][1], f[1], b.x, b.y);
+                }
+                mma_16816<BF16, true>(c[nt][0], f[2], b.z, b.w);
+                mma_16816<BF16, true>(c[nt][1], f[3], b.z, b.w);
             }
-        if ((q & ((1 << qt.shift) - 1)) == (1 << qt.shift) - 1) {  // the group's end
+        if (q % kQ == kQ - 1) {  // the group's end
             float s[4];
 #pragma unroll
             for (int h = 0; h < 4; ++h) {
-                const uint32_t raw = lds_u16(scales + (q >> qt.shift) * 256 + h * 16);
-                s[h] = qt.scale_fp16 ? __half2float(__ushort_as_half(static_cast<unsigned short>(raw)))
-                                     : __uint_as_float(raw << 16);
+                const uint32_t raw = lds_u16(scales + (q >> SHIFT) * 256 + h * 16);
+                s[h] = scale_fp16 ? __half2float(__ushort_as_half(static_cast<unsigned short>(raw)))
+                                  : __uint_as_float(raw << 16);
             }
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
-                    float &x = c[nt][i >> 2][i & 3];
                     float &y = acc[nt][i >> 2][i & 3];
-                    y = fmaf(s[(i >> 2) * 2 + ((i >> 1) & 1)], x, y);
-                    x = 0.0f;
+                    y = fmaf(s[(i >> 2) * 2 + ((i >> 1) & 1)], c[nt][i >> 2][i & 3], y);
                 }
         }
     }
@@ -300,7 +294,6 @@ __global__ void __launch_bounds__(kThreads, 1) int4_kernel(const __grid_constant
     } else if (warp < kWorkers / 32) {
         // ---- products ----
         const int grp = warp >> 2, rows32 = warp & 3, row = tid & 127;
-        const Quant q1{a.shift1, a.zeros1 != 0, a.scale_fp16 != 0}, q2{a.shift2, a.zeros2 != 0, a.scale_fp16 != 0};
         Cursor at_a, at_b;  // of this group's next tile
         int turn = grp;     // tiles until this group's
         for (int i = 0; i < grp; ++i) {
@@ -311,9 +304,10 @@ __global__ void __launch_bounds__(kThreads, 1) int4_kernel(const __grid_constant
         bool run = true;
 
         // This group's tiles of a run of `tiles`; its sums go to shared memory.
-        auto products = [&](auto blocks, int tiles, bool second) {
-            constexpr int NT = decltype(blocks)::value;
-            const Quant &qt = second ? q2 : q1;
+        auto products = [&](auto blocks, auto log_group, auto second, int tiles) {
+            constexpr int NT = decltype(blocks)::value, SHIFT = decltype(log_group)::value;
+            constexpr bool SECOND = decltype(second)::value;
+            const bool with_zeros = SECOND ? a.zeros2 : a.zeros1, scale_fp16 = a.scale_fp16;
             float acc[NT][2][4];
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
@@ -325,18 +319,15 @@ __global__ void __launch_bounds__(kThreads, 1) int4_kernel(const __grid_constant
                       mbar_wait_warp(smem_u32(&sh.full_a[at_a.s]), at_a.parity, abort, kWaitFullA);
                 if (!run)
                     break;
-                add_tile<NT, BF16>(acc, ring_a + at_a.s * a.stage_a, rows32, lane, ring_b + at_b.s * stage_b,
-                                   second ? 2 : 1, qt);
+                add_tile<NT, SHIFT, SECOND ? 2 : 1, BF16>(acc, ring_a + at_a.s * a.stage_a, rows32, lane,
+                                                          ring_b + at_b.s * stage_b, with_zeros, scale_fp16);
                 __syncwarp();
                 if (lane == 0) {
                     mbar_arrive(smem_u32(&sh.empty_a[at_a.s]));
-                    mbar_arrive(smem_u32(&sh.empty_b[at_b.s]), second ? kParts : 1);
+                    mbar_arrive(smem_u32(&sh.empty_b[at_b.s]), SECOND ? kParts : 1);
                 }
-                // the group's next tile is four on
-                for (int i = 0; i < kGroups; ++i)
-                    at_a.next(a.stages);
-                for (int i = 0; i < (second ? kGroups : kGroups / kParts); ++i)
-                    at_b.next(stages_b);
+                at_a.advance(kGroups, a.stages);  // the group's next tile
+                at_b.advance(SECOND ? kGroups : kGroups / kParts, stages_b);
             }
             turn -= tiles;
             named_sync(1, kWorkers);  // the sums of the run before are read
@@ -350,15 +341,24 @@ __global__ void __launch_bounds__(kThreads, 1) int4_kernel(const __grid_constant
                 }
             run = named_all(2, kWorkers, run);
         };
-        auto run_products = [&](int n, int tiles, bool second) {
-            if (n <= 8)
-                products(std::integral_constant<int, 1>{}, tiles, second);
-            else if (n <= 16)
-                products(std::integral_constant<int, 2>{}, tiles, second);
-            else if (n <= 24)
-                products(std::integral_constant<int, 3>{}, tiles, second);
+        auto by_group = [&](auto blocks, auto second, int tiles) {
+            const int shift = decltype(second)::value ? a.shift2 : a.shift1;
+            if (shift == 0)
+                products(blocks, std::integral_constant<int, 0>{}, second, tiles);
+            else if (shift == 1)
+                products(blocks, std::integral_constant<int, 1>{}, second, tiles);
             else
-                products(std::integral_constant<int, 4>{}, tiles, second);
+                products(blocks, std::integral_constant<int, 2>{}, second, tiles);
+        };
+        auto run_products = [&](auto second, int n, int tiles) {
+            if (n <= 8)
+                by_group(std::integral_constant<int, 1>{}, second, tiles);
+            else if (n <= 16)
+                by_group(std::integral_constant<int, 2>{}, second, tiles);
+            else if (n <= 24)
+                by_group(std::integral_constant<int, 3>{}, second, tiles);
+            else
+                by_group(std::integral_constant<int, 4>{}, second, tiles);
         };
         // Column j of the groups' sums, this thread's row: all groups, or the even (0) or odd (1) ones.
         auto sum_all = [&](int j) {
@@ -409,7 +409,7 @@ __global__ void __launch_bounds__(kThreads, 1) int4_kernel(const __grid_constant
         for (Walk w(begin1, end1, a.kc1, a.mt1, false); run && w.more(); w.next()) {
             const int n = li.count(w.i), tile = w.i * a.mt1 + w.m;
             const Split sp(shares1, tile * a.kc1, a.kc1);
-            run_products(n, w.len * kParts, false);
+            run_products(std::false_type{}, n, w.len * kParts);
             if (!run)
                 break;
             float *const part = a.part + static_cast<size_t>(sp.slot(blk)) * a.part_floats + row;
@@ -470,7 +470,7 @@ __global__ void __launch_bounds__(kThreads, 1) int4_kernel(const __grid_constant
                 acc_y[t * kTileRows + row] = 0.0f;
             for (; run && w.more() && w.m == m; w.next()) {
                 const int off = li.offset[w.i], n = li.count(w.i);
-                run_products(n, w.len, true);  // its barriers also order the threads' turns at a row of acc_y
+                run_products(std::true_type{}, n, w.len);  // its barriers also order the threads' turns at a row of acc_y
                 for (int j = set; run && j < n; j += kGroups) {
                     float *const s = acc_y + li.token[off + j] * kTileRows + row;
                     *s = fmaf(li.weight[off + j], sum_all(j), *s);

@@ -20,6 +20,14 @@ struct Cursor {
             parity ^= 1;
         }
     }
+    __device__ __forceinline__ void advance(int k, int n)
+    {
+        s += k;
+        while (s >= n) {
+            s -= n;
+            parity ^= 1;
+        }
+    }
     // To position i of the sequence.
     __device__ __forceinline__ void skip(int i, int n)
     {
