@@ -157,7 +157,10 @@ ep_status finish(cudaError_t ce, const char *what, unsigned long long *rec, cuda
 
 struct ep_router {
     ep_router_config cfg;
-    int device;
+    int device, sms;
+    int *counters;
+    Flags flags;
+    CUtensorMap mw;
 };
 
 namespace {
@@ -190,7 +193,7 @@ ep_status check_router(const ep_router_config *c)
     return EP_OK;
 }
 
-moe::RouterArgs router_args(const ep_router_config &c, int num_tokens)
+moe::RouterArgs router_args(const ep_router_config &c, int sms, int num_tokens)
 {
     moe::RouterArgs a = {};
     a.weight = c.weight;
@@ -205,6 +208,7 @@ moe::RouterArgs router_args(const ep_router_config &c, int num_tokens)
     a.top_groups = c.top_groups;
     a.renormalize = c.renormalize != 0;
     a.scale = c.scale;
+    a.sms = sms;
     return a;
 }
 
@@ -220,8 +224,8 @@ ep_status ep_router_create(const ep_router_config *cfg, ep_router **out)
     ep_status st = check_router(cfg);
     if (st != EP_OK)
         return st;
-    int dev = 0;
-    st = current_device(&dev, nullptr);
+    int dev = 0, sms = 0;
+    st = current_device(&dev, &sms);
     if (st != EP_OK)
         return st;
     ep_router *r = new (std::nothrow) ep_router();
@@ -229,6 +233,28 @@ ep_status ep_router_create(const ep_router_config *cfg, ep_router **out)
         return set_error(EP_ERR_OOM, "host allocation of the handle failed");
     r->cfg = *cfg;
     r->device = dev;
+    r->sms = sms;
+    st = encode_map(&r->mw, "weight", cfg->dtype == EP_DTYPE_FP16, cfg->weight, cfg->hidden, cfg->num_experts, 0,
+                    cfg->hidden, 0, moe::kChunk, moe::router_columns(cfg->num_experts));
+    if (st == EP_OK)
+        st = r->flags.make();
+    if (st == EP_OK) {
+        const size_t bytes = moe::router_counters(sms) * sizeof(int);
+        cudaError_t ce = cudaMalloc(reinterpret_cast<void **>(&r->counters), bytes);
+        if (ce == cudaSuccess)
+            ce = cudaMemset(r->counters, 0, bytes);
+        if (ce == cudaSuccess)
+            ce = cudaStreamSynchronize(nullptr);
+        if (ce != cudaSuccess)
+            st = cuda_error(ce, "the router's counters");
+    }
+    if (st != EP_OK) {
+        if (r->counters)
+            cudaFree(r->counters);
+        r->flags.free();
+        delete r;
+        return st;
+    }
     *out = r;
     return set_error(EP_OK, "");
 }
@@ -239,7 +265,7 @@ ep_status ep_router_workspace_size(const ep_router *r, int num_tokens, size_t *b
         MOE_FAIL("handle or bytes is NULL");
     if (num_tokens < 0)
         MOE_FAIL("num_tokens=%d < 0", num_tokens);
-    *bytes = moe::router_workspace(router_args(r->cfg, num_tokens));
+    *bytes = moe::router_workspace(router_args(r->cfg, r->sms, num_tokens));
     return set_error(EP_OK, "");
 }
 
@@ -262,7 +288,7 @@ ep_status ep_router_run(ep_router *r, const void *x, long long x_stride, int num
         MOE_FAIL("x_stride=%lld must be a multiple of 8 and at least hidden=%d", x_stride, r->cfg.hidden);
     if (!ids || !weights || !aligned(ids, 4) || !aligned(weights, 4))
         MOE_FAIL("ids or weights is NULL or not 4-byte aligned");
-    moe::RouterArgs a = router_args(r->cfg, num_tokens);
+    moe::RouterArgs a = router_args(r->cfg, r->sms, num_tokens);
     const size_t need = moe::router_workspace(a);
     if (need && (!workspace || !aligned(workspace, 256) || workspace_bytes < need))
         MOE_FAIL("workspace has %zu bytes, needs %zu, 256-byte aligned", workspace ? workspace_bytes : size_t(0), need);
@@ -270,7 +296,16 @@ ep_status ep_router_run(ep_router *r, const void *x, long long x_stride, int num
     a.x_stride = x_stride;
     a.ids = ids;
     a.weights = weights;
-    a.logits = static_cast<float *>(workspace);
+    st = r->flags.take();
+    if (st == EP_OK && moe::router_many(a))
+        st = encode_map(&a.mx, "x", r->cfg.dtype == EP_DTYPE_FP16, x, a.H, a.T, 0, x_stride, 0, moe::kChunk,
+                        moe::router_rows(a));
+    if (st != EP_OK)
+        return st;
+    a.mw = r->mw;
+    a.parts = static_cast<float *>(workspace);
+    a.counters = r->counters;
+    a.err = r->flags.err;
     unsigned long long *rec = epk::check_record();
     a.chk = epk::check_ctx(rec);
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
@@ -279,7 +314,12 @@ ep_status ep_router_run(ep_router *r, const void *x, long long x_stride, int num
 
 ep_status ep_router_destroy(ep_router *r)
 {
-    delete r;
+    if (r) {
+        if (r->counters)
+            cudaFree(r->counters);  // waits for work that uses them
+        r->flags.free();
+        delete r;
+    }
     return set_error(EP_OK, "");
 }
 

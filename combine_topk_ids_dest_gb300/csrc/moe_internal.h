@@ -17,29 +17,46 @@ namespace moe {
 constexpr int kMaxTokens = EP_MOE_MAX_TOKENS;    // rows of one experts or linear call
 constexpr int kMaxLocal = EP_MOE_MAX_EXPERTS;    // experts of one handle
 
+constexpr int kTileRows = 128;              // weight rows of a tile: the MMA's M
+constexpr int kSmemMax = 227 * 1024;        // shared memory of a block, static and dynamic
+constexpr int kChunk = 64;                  // inputs of a 16-bit chunk: one 128-byte swizzled row
+
 // ---- router (moe_router.cu) -------------------------------------------------------
 
+// Experts of one MMA of the router: all, or half of them where there are more
+// than 256, rounded up to a multiple of 16.
+static __host__ __device__ inline int router_columns(int E)
+{
+    const int one = (E + 15) & ~15;
+    return one <= 256 ? one : ((E + 1) / 2 + 15) & ~15;
+}
+
 struct RouterArgs {
+    CUtensorMap mx;  // x [T, H], boxes 64 x rows (many tokens)
+    CUtensorMap mw;  // weight [E, H], boxes 64 x router_columns(E)
     const void *x, *weight;
     const float *bias;
     long long x_stride;
     int32_t *ids;
     float *weights;
-    float *logits;  // workspace [T, E]
-    int T, H, E, K, bf16, scoring, groups, top_groups, renormalize;
+    float *parts;   // workspace
+    int *counters;  // zero between launches
+    unsigned int *err;
+    int T, H, E, K, bf16, scoring, groups, top_groups, renormalize, sms;
+    int rows, stages, tmem_cols;
     float scale;
     epk::CheckCtx chk;
 };
 
 size_t router_workspace(const RouterArgs &a);
+int router_counters(int sms);
+bool router_many(const RouterArgs &a);  // whether the launch uses mx and mw
+int router_rows(const RouterArgs &a);   // box rows of mx
 cudaError_t launch_router(const RouterArgs &a, cudaStream_t stream);
 cudaError_t router_binary_version(int *v);
 
 // ---- experts with dense bf16 weights (moe_experts.cu) ---------------------------
 
-constexpr int kTileRows = 128;              // weight rows of a tile: the MMA's M
-constexpr int kSmemMax = 227 * 1024;        // shared memory of a block, static and dynamic
-constexpr int kChunk = 64;                  // inputs of a bf16 chunk: one 128-byte swizzled row
 constexpr int kStageA = kTileRows * kChunk * 2;
 
 struct ExpertsArgs {

@@ -1,4 +1,24 @@
 // moe_router.cu -- a token's top-k experts and weights from its hidden row.
+//
+//   l = x Wg^T (fp32);  s = sigmoid(l) or softmax(l);  choose by s (+ bias)
+//
+// Two kernels, both from hidden rows to ids and weights:
+//
+//  - few tokens (up to kFewTokens): latency counts, the router's weight is
+//    spread over the SMs. A block takes 16 experts, a slice of the inputs and
+//    up to 16 tokens; its warps load MMA fragments straight from global
+//    memory (any 16 inputs may be a k-step, so a lane's share of a 32-input
+//    step is 16 contiguous bytes). Slices are written as fp32 parts and the
+//    block that arrives last for its tokens adds them up, one warp a token.
+//  - many tokens: a GEMM of [tokens x hidden] with the whole expert axis as
+//    the accumulator's columns, D[128 tokens, E] in tensor memory, so each
+//    thread finds all of a token's logits in its lane and no logit is written
+//    out. Tiles are as high as one wave of blocks needs, up to 128 tokens.
+//    With too few tiles for the SMs the inputs are split over blocks as well;
+//    parts go through memory and each block of a tile chooses for its share
+//    of the tokens.
+#include <type_traits>
+
 #include "moe_device.h"
 #include "moe_internal.h"
 
@@ -6,46 +26,8 @@ namespace moe {
 
 namespace {
 
-constexpr int kPerLane = kMaxLocal / 32;
-
-template <typename T> static __device__ __forceinline__ float2 unpack(uint32_t v);
-template <> __device__ __forceinline__ float2 unpack<__nv_bfloat16>(uint32_t v)
-{
-    return __bfloat1622float2(*reinterpret_cast<__nv_bfloat162 *>(&v));
-}
-template <> __device__ __forceinline__ float2 unpack<__half>(uint32_t v)
-{
-    return __half22float2(*reinterpret_cast<__half2 *>(&v));
-}
-
-// One warp per (token, expert).
-template <typename T>
-__global__ void __launch_bounds__(256) logits_kernel(const __grid_constant__ RouterArgs a)
-{
-    const int e = blockIdx.x * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
-    if (e >= a.E)
-        return;
-    for (int t = blockIdx.y; t < a.T; t += gridDim.y) {
-        const uint4 *const x = reinterpret_cast<const uint4 *>(static_cast<const T *>(a.x) + t * a.x_stride);
-        const uint4 *const w = reinterpret_cast<const uint4 *>(static_cast<const T *>(a.weight) +
-                                                              static_cast<size_t>(e) * a.H);
-        float s = 0.0f;
-        for (int i = lane; i < a.H / 8; i += 32) {
-            const uint4 p = x[i], q = w[i];
-            const uint32_t pv[4] = {p.x, p.y, p.z, p.w}, qv[4] = {q.x, q.y, q.z, q.w};
-#pragma unroll
-            for (int c = 0; c < 4; ++c) {
-                const float2 f = unpack<T>(pv[c]), g = unpack<T>(qv[c]);
-                s = fmaf(f.x, g.x, s);
-                s = fmaf(f.y, g.y, s);
-            }
-        }
-        for (int d = 16; d; d >>= 1)
-            s += __shfl_xor_sync(~0u, s, d);
-        if (lane == 0)
-            a.logits[static_cast<size_t>(t) * a.E + e] = s;
-    }
-}
+constexpr int kFewTokens = 256;
+constexpr int kManyExperts = 384;  // a tile's scores fit shared memory; above, slices of kFewTokens
 
 // Order-preserving image of a float in the unsigned integers; NaN and -infinity give 0 (never chosen).
 static __device__ __forceinline__ uint32_t ordered(float v)
@@ -56,49 +38,63 @@ static __device__ __forceinline__ uint32_t ordered(float v)
     return (b & 0x80000000u) ? ~b : (b | 0x80000000u);
 }
 
-// One warp: the choice of one token from its logits. Lane l holds experts l, l + 32, ...
-static __device__ void choose(const RouterArgs &a, int t, const float *logits, int lane)
+static __device__ __forceinline__ float unordered(uint32_t v)
 {
-    float s[kPerLane];
-    uint32_t c[kPerLane];
-    const int n = (a.E + 31) / 32;
-    float top = -INFINITY;
-#pragma unroll
-    for (int i = 0; i < kPerLane; ++i) {
-        const int e = lane + 32 * i;
-        s[i] = (i < n && e < a.E) ? logits[e] : -INFINITY;
-        top = fmaxf(top, s[i]);
-    }
-    float inv = 1.0f;
-    const bool by_logit = a.scoring == EP_SCORE_SOFTMAX && a.bias == nullptr && a.groups == 1;
+    return v == 0 ? -INFINITY : __uint_as_float((v & 0x80000000u) ? (v & 0x7FFFFFFFu) : ~v);
+}
+
+static __device__ __forceinline__ bool ranks_by_logit(const RouterArgs &a)
+{
+    return a.scoring == EP_SCORE_SOFTMAX && a.bias == nullptr && a.groups == 1;
+}
+
+static __device__ __forceinline__ float sigmoid(float l) { return 1.0f / (1.0f + expf(-l)); }
+
+static __device__ __forceinline__ void store_choice(const RouterArgs &a, int t, int k, int id, float w)
+{
+    const size_t at = static_cast<size_t>(t) * a.K + k;
+    if (EP_IN_BOUNDS(a.chk, epk::kSiteMoeIds, a.ids + at, 4, a.ids, 4LL * a.T * a.K))
+        a.ids[at] = id;
+    if (EP_IN_BOUNDS(a.chk, epk::kSiteMoeWeights, a.weights + at, 4, a.weights, 4LL * a.T * a.K))
+        a.weights[at] = w * a.scale;
+}
+
+// One warp: the choice of one token from its logits; s[i] of lane l is expert l + 32 i.
+template <int N> static __device__ void choose_warp(const RouterArgs &a, int t, float (&s)[N], int lane)
+{
+    uint32_t c[N];
+    const bool by_logit = ranks_by_logit(a);
     if (a.scoring == EP_SCORE_SOFTMAX) {
+        float top = -INFINITY, sum = 0.0f;
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+            top = fmaxf(top, s[i]);
         for (int d = 16; d; d >>= 1)
             top = fmaxf(top, __shfl_xor_sync(~0u, top, d));
-        float sum = 0.0f;
 #pragma unroll
-        for (int i = 0; i < kPerLane; ++i) {
-            const int e = lane + 32 * i;
-            if (i < n && e < a.E) {
-                if (by_logit)
-                    c[i] = ordered(s[i]);
+        for (int i = 0; i < N; ++i)
+            if (lane + 32 * i < a.E) {
+                c[i] = ordered(s[i]);
                 s[i] = expf(s[i] - top);
                 sum += s[i];
             }
-        }
         for (int d = 16; d; d >>= 1)
             sum += __shfl_xor_sync(~0u, sum, d);
-        inv = sum;
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+            s[i] = s[i] / sum;
+    } else {
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+            s[i] = sigmoid(s[i]);
     }
 #pragma unroll
-    for (int i = 0; i < kPerLane; ++i) {
+    for (int i = 0; i < N; ++i) {
         const int e = lane + 32 * i;
-        if (i < n && e < a.E) {
-            s[i] = a.scoring == EP_SCORE_SOFTMAX ? s[i] / inv : 1.0f / (1.0f + expf(-s[i]));
-            if (!by_logit)
-                c[i] = ordered(a.bias ? s[i] + a.bias[e] : s[i]);
-        } else {
+        if (e >= a.E)
             c[i] = 0;
-        }
+        else if (!by_logit)
+            c[i] = ordered(a.bias ? s[i] + a.bias[e] : s[i]);
     }
     if (a.groups > 1) {
         const int per = a.E / a.groups;
@@ -106,34 +102,31 @@ static __device__ void choose(const RouterArgs &a, int t, const float *logits, i
         for (int g = 0; g < a.groups; ++g) {
             uint32_t b1 = 0, b2 = 0;
 #pragma unroll
-            for (int i = 0; i < kPerLane; ++i)
-                if (i < n && (lane + 32 * i) / per == g) {
+            for (int i = 0; i < N; ++i) {
+                const int e = lane + 32 * i;
+                if (e >= g * per && e < (g + 1) * per) {
                     b2 = max(b2, min(b1, c[i]));
                     b1 = max(b1, c[i]);
                 }
+            }
             const uint32_t m1 = __reduce_max_sync(~0u, b1);
             const int owner = __ffs(__ballot_sync(~0u, b1 == m1)) - 1;
             const uint32_t m2 = __reduce_max_sync(~0u, lane == owner ? b2 : b1);
-            auto back = [](uint32_t v) {
-                return v == 0 ? -INFINITY : __uint_as_float((v & 0x80000000u) ? (v & 0x7FFFFFFFu) : ~v);
-            };
-            const float sum = per == 1 ? back(m1) : back(m1) + back(m2);
             if (lane == g)
-                value = ordered(sum);
+                value = ordered(per == 1 ? unordered(m1) : unordered(m1) + unordered(m2));
         }
         unsigned keep = 0;
         bool open = lane < a.groups;
         for (int k = 0; k < a.top_groups; ++k) {
             const uint32_t m = __reduce_max_sync(~0u, open ? value : 0);
-            const unsigned eq = __ballot_sync(~0u, open && value == m);
-            const int g = __ffs(eq) - 1;
+            const int g = __ffs(__ballot_sync(~0u, open && value == m)) - 1;
             keep |= 1u << g;
             if (lane == g)
                 open = false;
         }
 #pragma unroll
-        for (int i = 0; i < kPerLane; ++i)
-            if (i < n && !((keep >> min((lane + 32 * i) / per, 31)) & 1))
+        for (int i = 0; i < N; ++i)
+            if (!((keep >> min((lane + 32 * i) / per, 31)) & 1))
                 c[i] = 0;
     }
     int id = EP_INVALID_EXPERT_ID;  // of choice `lane`
@@ -141,24 +134,23 @@ static __device__ void choose(const RouterArgs &a, int t, const float *logits, i
     for (int k = 0; k < a.K; ++k) {
         uint32_t best = 0;
 #pragma unroll
-        for (int i = 0; i < kPerLane; ++i)
-            if (i < n)
-                best = max(best, c[i]);
+        for (int i = 0; i < N; ++i)
+            best = max(best, c[i]);
         const uint32_t m = __reduce_max_sync(~0u, best);
         if (m == 0)
             break;  // nothing left to choose
         int at = 0x7FFFFFFF;
         float v = 0.0f;
 #pragma unroll
-        for (int i = kPerLane - 1; i >= 0; --i)
-            if (i < n && c[i] == m) {
+        for (int i = N - 1; i >= 0; --i)
+            if (c[i] == m) {
                 at = lane + 32 * i;
                 v = s[i];
             }
         const int e = __reduce_min_sync(~0u, at);
         v = __shfl_sync(~0u, v, e & 31);
 #pragma unroll
-        for (int i = 0; i < kPerLane; ++i)
+        for (int i = 0; i < N; ++i)
             if (lane + 32 * i == e)
                 c[i] = 0;
         if (lane == k) {
@@ -167,49 +159,553 @@ static __device__ void choose(const RouterArgs &a, int t, const float *logits, i
         }
     }
     if (a.renormalize) {
-        float sum = lane < a.K ? w : 0.0f;
+        float sum = w;  // lanes without a choice have 0
         for (int d = 16; d; d >>= 1)
             sum += __shfl_xor_sync(~0u, sum, d);
         w = id >= 0 ? w / sum : 0.0f;
     }
-    if (lane < a.K) {
-        const size_t at = static_cast<size_t>(t) * a.K + lane;
-        if (EP_IN_BOUNDS(a.chk, epk::kSiteMoeIds, a.ids + at, 4, a.ids, 4LL * a.T * a.K))
-            a.ids[at] = id;
-        if (EP_IN_BOUNDS(a.chk, epk::kSiteMoeWeights, a.weights + at, 4, a.weights, 4LL * a.T * a.K))
-            a.weights[at] = w * a.scale;
+    if (lane < a.K)
+        store_choice(a, t, lane, id, w);
+}
+
+// ---- few tokens --------------------------------------------------------------------
+
+// Sixteen bytes of a row, zeros past its end.
+static __device__ __forceinline__ uint4 load_row(const uint16_t *row, int k, int H, bool valid)
+{
+    return valid && k < H ? __ldg(reinterpret_cast<const uint4 *>(row + k)) : make_uint4(0, 0, 0, 0);
+}
+
+// grid (16-expert blocks, input slices, token blocks of 8 NT); 8 warps that share the slice's 32-input steps.
+template <int NT, int N, bool BF16>
+__global__ void __launch_bounds__(256) few_kernel(const __grid_constant__ RouterArgs a)
+{
+    __shared__ float red[8][16][NT * 8 + 1];
+    __shared__ int last;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t4 = lane & 3;
+    const int e0 = blockIdx.x * 16, t0 = blockIdx.z * NT * 8, splits = gridDim.y;
+    const int steps = (a.H + 31) / 32, share = splits * 8, mine = blockIdx.y * 8 + warp;
+    const int s0 = steps * mine / share, s1 = steps * (mine + 1) / share;
+    const uint16_t *const W = static_cast<const uint16_t *>(a.weight), *const X = static_cast<const uint16_t *>(a.x);
+    const bool ok0 = e0 + g < a.E, ok1 = e0 + g + 8 < a.E;
+    const uint16_t *const w0 = W + static_cast<size_t>(ok0 ? e0 + g : 0) * a.H;
+    const uint16_t *const w1 = W + static_cast<size_t>(ok1 ? e0 + g + 8 : 0) * a.H;
+    float c[NT][4] = {};
+    for (int s = s0; s < s1; s += 4) {
+        uint4 p[4], q[4], x[4][NT];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int k = (s + i) * 32 + t4 * 8;
+            const bool in = s + i < s1;
+            p[i] = load_row(w0, k, a.H, in && ok0);
+            q[i] = load_row(w1, k, a.H, in && ok1);
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+                const int t = t0 + nt * 8 + g;
+                x[i][nt] = load_row(X + (t < a.T ? t : 0) * a.x_stride, k, a.H, in && t < a.T);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const uint32_t f0[4] = {p[i].x, q[i].x, p[i].y, q[i].y}, f1[4] = {p[i].z, q[i].z, p[i].w, q[i].w};
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+                mma_16816<BF16, true>(c[nt], f0, x[i][nt].x, x[i][nt].y);
+                mma_16816<BF16, true>(c[nt], f1, x[i][nt].z, x[i][nt].w);
+            }
+        }
+    }
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            red[warp][g + (i >> 1) * 8][nt * 8 + t4 * 2 + (i & 1)] = c[nt][i];
+    __syncthreads();
+    for (int i = threadIdx.x; i < NT * 8 * 16; i += 256) {
+        const int t = i >> 4, e = i & 15;
+        float v = 0.0f;
+#pragma unroll
+        for (int w = 0; w < 8; ++w)
+            v += red[w][e][t];
+        if (t0 + t < a.T && e0 + e < a.E)
+            a.parts[(static_cast<size_t>(blockIdx.y) * a.T + t0 + t) * a.E + e0 + e] = v;
+    }
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        const int blocks = gridDim.x * splits;
+        last = add_acq_rel(a.counters + blockIdx.z, 1) == blocks - 1;
+        if (last)
+            a.counters[blockIdx.z] = 0;  // for the next launch
+    }
+    __syncthreads();
+    if (!last)
+        return;
+    for (int t = t0 + warp; t < min(t0 + NT * 8, a.T); t += 8) {
+        float l[N];
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+            l[i] = lane + 32 * i < a.E ? 0.0f : -INFINITY;
+        const float *const p = a.parts + static_cast<size_t>(t) * a.E;
+        const size_t next = static_cast<size_t>(a.T) * a.E;
+        for (int s = 0; s < splits; s += 4) {
+            float v[4][N];
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+#pragma unroll
+                for (int i = 0; i < N; ++i)
+                    v[q][i] = s + q < splits && lane + 32 * i < a.E ? __ldcg(p + (s + q) * next + lane + 32 * i) : 0.0f;
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+#pragma unroll
+                for (int i = 0; i < N; ++i)
+                    l[i] += v[q][i];
+        }
+        choose_warp<N>(a, t, l, lane);
     }
 }
 
-__global__ void __launch_bounds__(256) choose_kernel(const __grid_constant__ RouterArgs a)
+// ---- many tokens -------------------------------------------------------------------
+
+constexpr int kThreads = 384;  // warps: copies, MMA, -, -, then 8 that score and choose
+constexpr int kMaxStages = 8;
+constexpr int kBuckets = 16;
+
+struct Shared {
+    uint64_t full[kMaxStages], empty[kMaxStages], done, drain;
+    uint32_t tmem;
+    int abort, issued;
+};
+
+// One thread: the choice of one token. score[e * 128] is expert e's score (its
+// logit where the rank goes by logits). Experts are kept in 16 buckets of which
+// the thread holds the largest values, so a pick looks through one bucket only.
+static __device__ void choose_thread(const RouterArgs &a, int t, float *score, const float *bias, float top, float sum)
 {
-    const int t = blockIdx.x * 8 + (threadIdx.x >> 5);
-    if (t < a.T)
-        choose(a, t, a.logits + static_cast<size_t>(t) * a.E, threadIdx.x & 31);
+    const bool by_logit = ranks_by_logit(a);
+    const int E = a.E, size = (E + kBuckets - 1) / kBuckets;
+    auto value = [&](int e) { return a.bias ? score[e * 128] + bias[e] : score[e * 128]; };
+    if (a.groups > 1) {
+        const int per = E / a.groups;
+        float v[2];  // group values are formed again for each pick: few groups, and no array of them
+        unsigned keep = 0;
+        auto group_value = [&](int g) {
+            float b1 = -INFINITY, b2 = -INFINITY;
+            for (int e = g * per; e < (g + 1) * per; ++e) {
+                const float c = value(e);
+                if (c > b1) {
+                    b2 = b1;
+                    b1 = c;
+                } else if (c > b2) {
+                    b2 = c;
+                }
+            }
+            const float v = per == 1 ? b1 : b1 + b2;
+            return v > -INFINITY ? v : -INFINITY;  // infinities of both signs
+        };
+        // values go to the space behind the scores
+        float *const values = score + static_cast<size_t>(E) * 128;
+        for (int g = 0; g < a.groups; ++g)
+            values[g * 128] = group_value(g);
+        for (int k = 0; k < a.top_groups; ++k) {
+            int best = -1;
+            v[0] = 0.0f;
+            for (int g = 0; g < a.groups; ++g) {
+                v[1] = values[g * 128];
+                if (!((keep >> g) & 1) && (best < 0 || v[1] > v[0])) {
+                    best = g;
+                    v[0] = v[1];
+                }
+            }
+            keep |= 1u << best;
+        }
+        for (int g = 0; g < a.groups; ++g)
+            if (!((keep >> g) & 1))
+                for (int e = g * per; e < (g + 1) * per; ++e)
+                    score[e * 128] = __uint_as_float(0x7FC00000u);  // NaN is never chosen
+    }
+    float most[kBuckets];
+#pragma unroll
+    for (int b = 0; b < kBuckets; ++b) {
+        most[b] = -INFINITY;
+        for (int e = b * size; e < min((b + 1) * size, E); ++e) {
+            const float c = value(e);
+            most[b] = c > most[b] ? c : most[b];
+        }
+    }
+    float w[EP_MAX_TOP_K > 8 ? 8 : EP_MAX_TOP_K], total = 0.0f;  // the first eight weights stay in registers
+    const size_t at = static_cast<size_t>(t) * a.K;
+    int n = 0;
+    auto pick = [&](float &weight) {
+        float best = -INFINITY;
+        int b = -1;
+#pragma unroll
+        for (int i = 0; i < kBuckets; ++i)
+            if (most[i] > best) {
+                best = most[i];
+                b = i;
+            }
+        if (b < 0)
+            return -1;
+        float rest = -INFINITY;
+        int id = -1;
+        for (int e = b * size; e < min((b + 1) * size, E); ++e) {
+            const float c = value(e);
+            if (id < 0 && c == best)
+                id = e;
+            else if (c > rest)
+                rest = c;
+        }
+        weight = by_logit ? expf(score[id * 128] - top) / sum : score[id * 128];
+        score[id * 128] = __uint_as_float(0x7FC00000u);
+#pragma unroll
+        for (int i = 0; i < kBuckets; ++i)
+            if (i == b)
+                most[i] = rest;
+        return id;
+    };
+    (void)at;
+    for (; n < a.K; ++n) {
+        float weight = 0.0f;
+        const int id = pick(weight);
+        if (id < 0)
+            break;
+        total += weight;
+        if (n < 8) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                if (i == n)
+                    w[i] = weight;
+        }
+        // unscaled for now where a sum has still to come
+        if (EP_IN_BOUNDS(a.chk, epk::kSiteMoeIds, a.ids + at + n, 4, a.ids, 4LL * a.T * a.K))
+            a.ids[at + n] = id;
+        if ((n >= 8 || !a.renormalize) &&
+            EP_IN_BOUNDS(a.chk, epk::kSiteMoeWeights, a.weights + at + n, 4, a.weights, 4LL * a.T * a.K))
+            a.weights[at + n] = a.renormalize ? weight : weight * a.scale;
+    }
+    if (a.renormalize) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (i < n && EP_IN_BOUNDS(a.chk, epk::kSiteMoeWeights, a.weights + at + i, 4, a.weights, 4LL * a.T * a.K))
+                a.weights[at + i] = w[i] / total * a.scale;
+        for (int i = 8; i < n; ++i)
+            if (EP_IN_BOUNDS(a.chk, epk::kSiteMoeWeights, a.weights + at + i, 4, a.weights, 4LL * a.T * a.K))
+                a.weights[at + i] = a.weights[at + i] / total * a.scale;
+    }
+    for (; n < a.K; ++n)
+        store_choice(a, t, n, EP_INVALID_EXPERT_ID, 0.0f);
+}
+
+// grid (token tiles, input splits). Dynamic shared memory: the ring, used again
+// for scores [E + groups][128] and the bias.
+template <bool BF16>
+__global__ void __launch_bounds__(kThreads, 1) many_kernel(const __grid_constant__ RouterArgs a)
+{
+    extern __shared__ uint8_t dyn[];
+    __shared__ Shared sh;
+    const uint32_t dyn0 = smem_u32(dyn), ring = (dyn0 + 1023u) & ~1023u;
+    float *const scores = reinterpret_cast<float *>(dyn + (ring - dyn0));
+    float *const bias = scores + (a.E + 32) * 128;
+    const int tid = threadIdx.x, warp = __shfl_sync(~0u, tid >> 5, 0), lane = tid & 31;
+    const int tile = blockIdx.x, split = blockIdx.y, splits = gridDim.y;
+    const int t0 = tile * a.rows, rows = min(a.rows, a.T - t0);
+    const int half = router_columns(a.E), E16 = a.E > half ? 2 * half : half;  // columns of one MMA, of all
+    const int bytes_x = a.rows * 128, stage = 16384 + E16 * 128;
+    const int chunks = (a.H + kChunk - 1) / kChunk;
+    const int c0 = static_cast<int>(static_cast<long long>(chunks) * split / splits);
+    const int c1 = static_cast<int>(static_cast<long long>(chunks) * (split + 1) / splits);
+    volatile int *const abort = &sh.abort;
+
+    if (tid == 0) {
+        sh.abort = sh.issued = 0;
+        for (int i = 0; i < kMaxStages; ++i) {
+            mbar_init(smem_u32(&sh.full[i]), 1);
+            mbar_init(smem_u32(&sh.empty[i]), 1);
+        }
+        mbar_init(smem_u32(&sh.done), 1);
+        mbar_init(smem_u32(&sh.drain), 1);
+        mbar_init_fence();
+        tma_prefetch_map(&a.mx);
+        tma_prefetch_map(&a.mw);
+    }
+    if (warp == 1)
+        tmem_alloc(smem_u32(&sh.tmem), a.tmem_cols);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = sh.tmem;
+
+    if (warp == 0 && elect_one()) {
+        int s = 0, it = 0;
+        uint32_t parity = 0;
+        for (int c = c0; c < c1; ++c, ++it) {
+            if (!mbar_wait(smem_u32(&sh.empty[s]), parity ^ 1, abort, kWaitEmptyA))
+                break;
+            const uint32_t bar = smem_u32(&sh.full[s]), at = ring + s * stage;
+            mbar_expect(bar, bytes_x + E16 * 128);
+            tma_load_2d(at, &a.mx, bar, c * kChunk, t0);
+            for (int e = 0; e < E16; e += half)
+                tma_load_2d(at + 16384 + e * 128, &a.mw, bar, c * kChunk, e);
+            if (++s == a.stages) {
+                s = 0;
+                parity ^= 1;
+            }
+        }
+        sh.issued = it;
+    } else if (warp == 1) {
+        int s = 0;
+        uint32_t parity = 0;
+        const uint32_t idesc = idesc_f16(128, half, BF16);
+        for (int c = c0; c < c1; ++c) {
+            if (!mbar_wait_warp(smem_u32(&sh.full[s]), parity, abort, kWaitFullA))
+                break;
+            tc_fence_after();
+            if (elect_one()) {
+                const uint32_t at = ring + s * stage;
+                const uint64_t da = desc_sw128(at), db = desc_sw128(at + 16384);
+                for (int e = 0; e < E16; e += half)
+#pragma unroll
+                    for (int q = 0; q < 4; ++q)
+                        mma_ss(tmem + e, da + 2 * q, db + e * 8 + 2 * q, idesc, c > c0 || q > 0);
+                tc_commit(smem_u32(&sh.empty[s]));
+            }
+            if (++s == a.stages) {
+                s = 0;
+                parity ^= 1;
+            }
+        }
+        if (elect_one()) {
+            tc_commit(smem_u32(&sh.done));
+            tc_commit(smem_u32(&sh.drain));
+        }
+        mbar_wait(smem_u32(&sh.drain), 0, nullptr, kWaitOther);
+    } else if (warp >= 4) {
+        // 8 warps: two threads to a token, each with half of the experts' scores
+        const int row = tid & 127, part = (warp - 4) >> 2, wtid = tid - 128;
+        const uint32_t lanes = tmem + (static_cast<uint32_t>(warp & 3) << 21);
+        const int mid = ((a.E + 15) / 16) * 8, b0 = part ? mid : 0, b1 = part ? a.E : min(mid, a.E);
+        bool run = mbar_wait_warp(smem_u32(&sh.done), 0, abort, kWaitFullD);
+        run = named_all(2, 256, run);
+        tc_fence_after();
+        if (run && splits == 1) {
+            for (int e = b0; e < b1; e += 8) {  // every MMA has been read: the ring is free
+                float v[8];
+                tmem_ld8(lanes + e, v);
+                tmem_wait_ld();
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    if (e + i < b1)
+                        scores[(e + i) * 128 + row] = v[i];
+            }
+        } else if (run) {
+            const size_t tile_floats = static_cast<size_t>(a.E) * 128;
+            float *const p = a.parts + (static_cast<size_t>(tile) * splits + split) * tile_floats;
+            for (int e = b0; e < b1; e += 8) {
+                float v[8];
+                tmem_ld8(lanes + e, v);
+                tmem_wait_ld();
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    if (e + i < b1)
+                        p[(e + i) * 128 + row] = v[i];
+            }
+            named_sync(1, 256);
+            if (wtid == 0) {
+                add_acq_rel(a.counters + tile, 1);
+                run = wait_count(a.counters + tile, splits, abort, kWaitOther);
+            }
+            run = named_all(2, 256, run);
+        }
+        // this block's tokens of the tile
+        const int r0 = rows * split / splits, r1 = rows * (split + 1) / splits, n = r1 - r0;
+        if (run && splits > 1) {  // threads to (token, expert) pairs: 32 tokens' loads side by side
+            const size_t tile_floats = static_cast<size_t>(a.E) * 128;
+            const float *const p = a.parts + static_cast<size_t>(tile) * splits * tile_floats + r0;
+            const int wide = n > 64 ? 128 : n > 32 ? 64 : 32, r = wtid % wide;
+            for (int e = wtid / wide; e < a.E; e += 256 / wide)
+                if (r < n) {
+                    float v = 0.0f;
+                    for (int s = 0; s < splits; s += 4) {
+                        float x[4];
+#pragma unroll
+                        for (int q = 0; q < 4; ++q)
+                            x[q] = s + q < splits ? __ldcg(p + (s + q) * tile_floats + e * 128 + r) : 0.0f;
+#pragma unroll
+                        for (int q = 0; q < 4; ++q)
+                            v += x[q];
+                    }
+                    scores[e * 128 + r] = v;
+                }
+        }
+        if (run) {
+            for (int e = wtid; e < a.E; e += 256)
+                bias[e] = a.bias ? a.bias[e] : 0.0f;
+            named_sync(1, 256);
+            // scores from logits; for softmax the two threads of a token exchange the largest logit and the sum
+            float *const mine = scores + row, *const xch = bias + a.E + part * 128 + row;
+            const float *const other = bias + a.E + (part ^ 1) * 128 + row;
+            float top = -INFINITY, sum = 0.0f;
+            if (a.scoring == EP_SCORE_SOFTMAX) {
+                for (int e = b0; e < b1; ++e)
+                    top = fmaxf(top, mine[e * 128]);
+                *xch = top;
+                named_sync(1, 256);
+                top = fmaxf(top, *other);
+                named_sync(1, 256);
+                const bool keep = ranks_by_logit(a);
+                for (int e = b0; e < b1; ++e) {
+                    const float x = expf(mine[e * 128] - top);
+                    sum += x;
+                    if (!keep)
+                        mine[e * 128] = x;
+                }
+                *xch = sum;
+                named_sync(1, 256);
+                sum = part ? *other + sum : sum + *other;
+                if (!keep)
+                    for (int e = b0; e < b1; ++e)
+                        mine[e * 128] = mine[e * 128] / sum;
+            } else {
+                for (int e = b0; e < b1; ++e)
+                    mine[e * 128] = sigmoid(mine[e * 128]);
+            }
+            named_sync(1, 256);
+            if (part == 0 && row < n)
+                choose_thread(a, t0 + r0 + row, mine, bias, top, sum);
+        }
+    }
+    __syncwarp();
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (sh.abort) {
+        if (tid == 0) {
+            for (int i = max(0, sh.issued - a.stages); i < sh.issued; ++i)
+                mbar_wait(smem_u32(&sh.full[i % a.stages]), (i / a.stages) & 1, nullptr, kWaitOther);
+            atomicAdd_system(a.err + sh.abort, 1u);
+            __threadfence_system();
+            atomicAdd_system(a.err, 1u);
+        }
+        __syncthreads();
+    }
+    if (warp == 1)
+        tmem_free(tmem, a.tmem_cols);
+    if (splits > 1 && tid == 0 && add_acq_rel(a.counters + gridDim.x + tile, 1) == splits - 1)
+        a.counters[tile] = a.counters[gridDim.x + tile] = 0;  // for the next launch
+    (void)lane;
+}
+
+int few_splits(const RouterArgs &a) { return (((a.H + 31) / 32) + 31) / 32; }  // four steps a warp
+
+struct ManyPlan {
+    int rows, tiles, splits;
+};
+
+// Tiles as high as one more wave of blocks needs, or, where that leaves SMs idle, split inputs.
+ManyPlan plan_many(const RouterArgs &a)
+{
+    ManyPlan p;
+    const int waves = (a.T + a.sms * 128 - 1) / (a.sms * 128);
+    p.rows = (a.T + waves * a.sms - 1) / (waves * a.sms);
+    if (p.rows < 64)
+        p.rows = 128;
+    p.tiles = (a.T + p.rows - 1) / p.rows;
+    const int chunks = (a.H + kChunk - 1) / kChunk;
+    p.splits = p.tiles < a.sms ? a.sms / p.tiles : 1;
+    if (p.splits > chunks)
+        p.splits = chunks;
+    return p;
 }
 
 }  // namespace
 
-size_t router_workspace(const RouterArgs &a) { return static_cast<size_t>(a.T) * a.E * sizeof(float); }
+bool router_many(const RouterArgs &a) { return a.T > kFewTokens && a.E <= kManyExperts; }
 
-cudaError_t launch_router(const RouterArgs &a, cudaStream_t stream)
+size_t router_workspace(const RouterArgs &a)
 {
-    const dim3 grid((a.E + 7) / 8, a.T < 65535 ? a.T : 65535);
-    if (a.bf16)
-        logits_kernel<__nv_bfloat16><<<grid, 256, 0, stream>>>(a);
+    if (a.T == 0)
+        return 0;
+    if (!router_many(a))
+        return static_cast<size_t>(few_splits(a)) * (a.T < kFewTokens ? a.T : kFewTokens) * a.E * sizeof(float);
+    const ManyPlan p = plan_many(a);
+    return p.splits == 1 ? 0 : static_cast<size_t>(p.tiles) * p.splits * a.E * 128 * sizeof(float);
+}
+
+int router_counters(int sms) { return 2 * sms + kFewTokens; }
+
+
+int router_rows(const RouterArgs &a) { return plan_many(a).rows; }
+
+namespace {
+
+template <int NT, bool BF16> void launch_few(const RouterArgs &a, cudaStream_t stream)
+{
+    const dim3 grid((a.E + 15) / 16, few_splits(a), (a.T + NT * 8 - 1) / (NT * 8));
+    if (a.E <= 128)
+        few_kernel<NT, 4, BF16><<<grid, 256, 0, stream>>>(a);
+    else if (a.E <= 256)
+        few_kernel<NT, 8, BF16><<<grid, 256, 0, stream>>>(a);
     else
-        logits_kernel<__half><<<grid, 256, 0, stream>>>(a);
-    const cudaError_t ce = cudaGetLastError();
-    if (ce != cudaSuccess)
-        return ce;
-    choose_kernel<<<(a.T + 7) / 8, 256, 0, stream>>>(a);
-    return cudaGetLastError();
+        few_kernel<NT, 16, BF16><<<grid, 256, 0, stream>>>(a);
+}
+
+template <bool BF16> cudaError_t launch_many(RouterArgs a, cudaStream_t stream)
+{
+    static const cudaError_t attr =
+        cudaFuncSetAttribute(many_kernel<BF16>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             kSmemMax - 64 - static_cast<int>(sizeof(Shared)));
+    if (attr != cudaSuccess)
+        return attr;
+    const ManyPlan p = plan_many(a);
+    const int half = router_columns(a.E), E16 = a.E > half ? 2 * half : half, stage = 16384 + E16 * 128;
+    a.rows = p.rows;
+    a.tmem_cols = E16 > 256 ? 512 : E16 > 128 ? 256 : 128;
+    a.stages = (kSmemMax - 2048 - static_cast<int>(sizeof(Shared))) / stage;
+    if (a.stages > kMaxStages)
+        a.stages = kMaxStages;
+    const size_t choice = (static_cast<size_t>(a.E + 32) * 128 + a.E + 256) * 4;
+    size_t smem = static_cast<size_t>(a.stages) * stage;
+    smem = 1024 + (smem > choice ? smem : choice);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(p.tiles, p.splits);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeCooperative;  // the blocks of a tile wait for one another's parts
+    at[0].val.cooperative = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = p.splits > 1 ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, many_kernel<BF16>, a);
+}
+
+}  // namespace
+
+cudaError_t launch_router(const RouterArgs &all, cudaStream_t stream)
+{
+    if (router_many(all))
+        return all.bf16 ? launch_many<true>(all, stream) : launch_many<false>(all, stream);
+    RouterArgs a = all;
+    for (int t = 0; t < all.T; t += kFewTokens) {
+        a.T = all.T - t < kFewTokens ? all.T - t : kFewTokens;
+        a.x = static_cast<const uint16_t *>(all.x) + t * all.x_stride;
+        a.ids = all.ids + static_cast<size_t>(t) * a.K;
+        a.weights = all.weights + static_cast<size_t>(t) * a.K;
+        if (a.T <= 8)
+            a.bf16 ? launch_few<1, true>(a, stream) : launch_few<1, false>(a, stream);
+        else
+            a.bf16 ? launch_few<2, true>(a, stream) : launch_few<2, false>(a, stream);
+        const cudaError_t ce = cudaGetLastError();
+        if (ce != cudaSuccess)
+            return ce;
+    }
+    return cudaSuccess;
 }
 
 cudaError_t router_binary_version(int *v)
 {
     cudaFuncAttributes fa;
-    cudaError_t ce = cudaFuncGetAttributes(&fa, choose_kernel);
+    cudaError_t ce = cudaFuncGetAttributes(&fa, many_kernel<true>);
     if (ce == cudaSuccess)
         *v = fa.binaryVersion;
     return ce;
