@@ -227,13 +227,13 @@ static __device__ __forceinline__ void mma_16816(float *c, const uint32_t *a, ui
 {
     const float z = 0.0f;
     if (BF16)
-        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
                      "{%10, %11, %12, %13};"
                      : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
                      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(ADD ? c[0] : z),
                        "f"(ADD ? c[1] : z), "f"(ADD ? c[2] : z), "f"(ADD ? c[3] : z));
     else
-        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
                      "{%10, %11, %12, %13};"
                      : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
                      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(ADD ? c[0] : z),

@@ -68,49 +68,29 @@ template <bool BF16> static __device__ __forceinline__ void decode(uint32_t w, u
     }
 }
 
-static __device__ __forceinline__ uint4 lds16(uint32_t addr)
-{
-    uint4 v;
-    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr));
-    return v;
-}
-
-static __device__ __forceinline__ uint32_t lds_u16(uint32_t addr)
-{
-    uint16_t v;
-    asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(addr));
-    return v;
-}
-
-static __device__ __forceinline__ uint32_t lds_u8(uint32_t addr)
-{
-    uint32_t v;
-    asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(addr));
-    return v;
-}
-
 // Adds one weight tile times NT * 8 tokens (in PLANES parts) to the sums of
 // this warp's 32 rows: acc[column block][16-row half][fragment]. SHIFT:
 // log2(group / 32). tile: the tile in shared memory; tokens: [PLANES][4][NT * 8][32] 16-bit.
 template <int NT, int SHIFT, int PLANES, bool BF16>
-static __device__ __forceinline__ void add_tile(float (&acc)[NT][2][4], uint32_t tile, int rows32, int lane, uint32_t tokens,
-                                                bool with_zeros, bool scale_fp16)
+static __device__ __forceinline__ void add_tile(float (&acc)[NT][2][4], const uint8_t *tile, int rows32, int lane,
+                                                const uint8_t *tokens, bool with_zeros, bool scale_fp16)
 {
     constexpr int kQ = 1 << SHIFT;  // 32-input steps of a group
-    const uint32_t codes = tile + rows32 * 2048 + lane * 16;
-    const uint32_t row = rows32 * 32 + (lane >> 2);
-    const uint32_t scales = tile + 8192 + row * 2, zeros = tile + 8192 + (1024 >> SHIFT) + row;
-    const uint32_t tok = tokens + (lane >> 2) * 64 + (lane & 3) * 16;
+    const uint4 *const codes = reinterpret_cast<const uint4 *>(tile + rows32 * 2048) + lane;
+    const int row = rows32 * 32 + (lane >> 2);
+    const uint16_t *const scales = reinterpret_cast<const uint16_t *>(tile + 8192) + row;
+    const uint8_t *const zeros = tile + 8192 + (1024 >> SHIFT) + row;
+    const uint4 *const tok = reinterpret_cast<const uint4 *>(tokens) + lane;
     constexpr uint32_t one = BF16 ? 0x43004300u : 0x64006400u;
     uint32_t z[4] = {one + 0x00080008u, one + 0x00080008u, one + 0x00080008u, one + 0x00080008u};
     float c[NT][2][4];
-    uint4 w = lds16(codes);
+    uint4 w = codes[0];
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
         if (q % kQ == 0 && with_zeros) {
 #pragma unroll
             for (int h = 0; h < 4; ++h)  // rows r, r + 8, r + 16, r + 24
-                z[h] = one + lds_u8(zeros + (q >> SHIFT) * 128 + h * 8) * 0x00010001u;
+                z[h] = one + zeros[(q >> SHIFT) * 128 + h * 8] * 0x00010001u;
         }
         uint32_t f[4][4];  // [2 * sixteen inputs + 16-row half]
         decode<BF16>(w.x, z[0], z[1], f[0]);
@@ -118,12 +98,12 @@ static __device__ __forceinline__ void add_tile(float (&acc)[NT][2][4], uint32_t
         decode<BF16>(w.z, z[0], z[1], f[2]);
         decode<BF16>(w.w, z[2], z[3], f[3]);
         if (q < 3)
-            w = lds16(codes + (q + 1) * 512);
+            w = codes[(q + 1) * 32];
 #pragma unroll
         for (int p = 0; p < PLANES; ++p)
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
-                const uint4 b = lds16(tok + ((p * 4 + q) * NT + nt) * 512);
+                const uint4 b = tok[((p * 4 + q) * NT + nt) * 32];
                 if (q % kQ == 0 && p == 0) {
                     mma_16816<BF16, false>(c[nt][0], f[0], b.x, b.y);
                     mma_16816<BF16, false>(c[nt][1], f[1], b.x, b.y);
@@ -138,7 +118,7 @@ static __device__ __forceinline__ void add_tile(float (&acc)[NT][2][4], uint32_t
             float s[4];
 #pragma unroll
             for (int h = 0; h < 4; ++h) {
-                const uint32_t raw = lds_u16(scales + (q >> SHIFT) * 256 + h * 16);
+                const uint32_t raw = scales[(q >> SHIFT) * 128 + h * 8];
                 s[h] = scale_fp16 ? __half2float(__ushort_as_half(static_cast<unsigned short>(raw)))
                                   : __uint_as_float(raw << 16);
             }
@@ -162,6 +142,7 @@ __global__ void __launch_bounds__(kThreads, 1) int4_kernel(const __grid_constant
     const uint32_t ring_b = (dyn0 + 127u) & ~127u;
     const uint32_t ring_a = ring_b + a.bytes_b;
     const uint32_t after = ring_a + a.stages * a.stage_a;
+    const uint8_t *const ring_b_p = dyn + (ring_b - dyn0), *const ring_a_p = dyn + (ring_a - dyn0);
     float *const sums = reinterpret_cast<float *>(dyn + (after - dyn0));  // [group][column][kSumStride]
     float *const acc_y = sums + kGroups * a.cols * kSumStride;            // [T][128], of the second product
     const Lists li(acc_y + (LINEAR ? 0 : a.T * kTileRows), a.E, a.P);
@@ -319,8 +300,8 @@ __global__ void __launch_bounds__(kThreads, 1) int4_kernel(const __grid_constant
                       mbar_wait_warp(smem_u32(&sh.full_a[at_a.s]), at_a.parity, abort, kWaitFullA);
                 if (!run)
                     break;
-                add_tile<NT, SHIFT, SECOND ? 2 : 1, BF16>(acc, ring_a + at_a.s * a.stage_a, rows32, lane,
-                                                          ring_b + at_b.s * stage_b, with_zeros, scale_fp16);
+                add_tile<NT, SHIFT, SECOND ? 2 : 1, BF16>(acc, ring_a_p + at_a.s * a.stage_a, rows32, lane,
+                                                          ring_b_p + at_b.s * stage_b, with_zeros, scale_fp16);
                 __syncwarp();
                 if (lane == 0) {
                     mbar_arrive(smem_u32(&sh.empty_a[at_a.s]));
