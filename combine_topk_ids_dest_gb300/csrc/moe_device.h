@@ -105,6 +105,35 @@ static __device__ __forceinline__ bool mbar_wait_warp(uint32_t bar, uint32_t par
     return __all_sync(~0u, mbar_wait(bar, parity, abort, site));
 }
 
+// Both of two barriers, by a whole converged warp: one vote and one branch
+// where both phases have completed (a branch costs some 25 cycles).
+static __device__ __forceinline__ bool mbar_wait2_warp(uint32_t bar1, uint32_t parity1, uint32_t bar2, uint32_t parity2,
+                                                       volatile int *abort, int site1, int site2)
+{
+    uint32_t ok;
+    asm volatile("{\n\t.reg .pred p, q;\n\t"
+                 "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+                 "mbarrier.try_wait.parity.shared::cta.b64 q, [%3], %4;\n\t"
+                 "and.pred p, p, q;\n\t"
+                 "selp.u32 %0, 1, 0, p;\n\t}"
+                 : "=r"(ok)
+                 : "r"(bar1), "r"(parity1), "r"(bar2), "r"(parity2)
+                 : "memory");
+    if (__all_sync(~0u, ok))
+        return true;
+    return __all_sync(~0u, mbar_wait(bar1, parity1, abort, site1) && mbar_wait(bar2, parity2, abort, site2));
+}
+
+// mbar_arrive on two barriers where `me` is true, without a branch.
+static __device__ __forceinline__ void mbar_arrive2_if(bool me, uint32_t bar1, uint32_t bar2, uint32_t count2)
+{
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %0, 0;\n\t"
+                 "@p mbarrier.arrive.shared::cta.b64 _, [%1];\n\t"
+                 "@p mbarrier.arrive.shared::cta.b64 _, [%2], %3;\n\t}" ::"r"(uint32_t(me)),
+                 "r"(bar1), "r"(bar2), "r"(count2)
+                 : "memory");
+}
+
 // ---- TMA ------------------------------------------------------------------------
 
 static __device__ __forceinline__ void tma_prefetch_map(const CUtensorMap *m)

@@ -60,7 +60,8 @@ template <bool BF16> static __device__ __forceinline__ void decode(uint32_t w, u
 {
 #pragma unroll
     for (int p = 0; p < 4; ++p) {
-        const uint32_t v = ((w >> (4 * p)) & 0x000F000Fu) | (BF16 ? 0x43004300u : 0x64006400u);
+        uint32_t v;  // (w >> 4p & mask) | exponent: one instruction after the shift, which two constants in C are not
+        asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(v) : "r"(w >> (4 * p)), "r"(0x000F000Fu), "r"(BF16 ? 0x43004300u : 0x64006400u));
         if (BF16)
             asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(out[p]) : "r"(v), "r"(p & 1 ? zb : za));
         else
@@ -143,8 +144,8 @@ __global__ void __launch_bounds__(kThreads, 1) int4_kernel(const __grid_constant
     const uint32_t ring_a = ring_b + a.bytes_b;
     const uint32_t after = ring_a + a.stages * a.stage_a;
     const uint8_t *const ring_b_p = dyn + (ring_b - dyn0), *const ring_a_p = dyn + (ring_a - dyn0);
-    float *const sums = reinterpret_cast<float *>(dyn + (after - dyn0));  // [group][column][kSumStride]
-    float *const acc_y = sums + kGroups * a.cols * kSumStride;            // [T][128], of the second product
+    float *const sums = reinterpret_cast<float *>(dyn + (after - dyn0));  // [2][column][kSumStride]
+    float *const acc_y = sums + 2 * a.cols * kSumStride;            // [T][128], of the second product
     const Lists li(acc_y + (LINEAR ? 0 : a.T * kTileRows), a.E, a.P);
 
     const int tid = threadIdx.x, warp = __shfl_sync(~0u, tid >> 5, 0), lane = tid & 31;
@@ -283,6 +284,8 @@ __global__ void __launch_bounds__(kThreads, 1) int4_kernel(const __grid_constant
                 at_b.next(stages_b);
         }
         bool run = true;
+        constexpr uint32_t empty_a = offsetof(Shared, empty_a) - offsetof(Shared, full_a);
+        constexpr uint32_t empty_b = offsetof(Shared, empty_b) - offsetof(Shared, full_b);
 
         // This group's tiles of a run of `tiles`; its sums go to shared memory.
         auto products = [&](auto blocks, auto log_group, auto second, int tiles) {
@@ -295,31 +298,38 @@ __global__ void __launch_bounds__(kThreads, 1) int4_kernel(const __grid_constant
 #pragma unroll
                 for (int i = 0; i < 8; ++i)
                     acc[nt][i >> 2][i & 3] = 0.0f;
-            for (; run && turn < tiles; turn += kGroups) {
-                run = mbar_wait_warp(smem_u32(&sh.full_b[at_b.s]), at_b.parity, abort, kWaitFullB) &&
-                      mbar_wait_warp(smem_u32(&sh.full_a[at_a.s]), at_a.parity, abort, kWaitFullA);
-                if (!run)
+            for (; turn < tiles; turn += kGroups) {
+                const uint32_t fa = smem_u32(&sh.full_a[at_a.s]), fb = smem_u32(&sh.full_b[at_b.s]);
+                if (!mbar_wait2_warp(fa, at_a.parity, fb, at_b.parity, abort, kWaitFullA, kWaitFullB)) {
+                    run = false;
+                    turn = tiles;
                     break;
+                }
                 add_tile<NT, SHIFT, SECOND ? 2 : 1, BF16>(acc, ring_a_p + at_a.s * a.stage_a, rows32, lane,
                                                           ring_b_p + at_b.s * stage_b, with_zeros, scale_fp16);
                 __syncwarp();
-                if (lane == 0) {
-                    mbar_arrive(smem_u32(&sh.empty_a[at_a.s]));
-                    mbar_arrive(smem_u32(&sh.empty_b[at_b.s]), SECOND ? kParts : 1);
-                }
+                mbar_arrive2_if(lane == 0, fa + empty_a, fb + empty_b, SECOND ? kParts : 1);
                 at_a.advance(kGroups, a.stages);  // the group's next tile
                 at_b.advance(SECOND ? kGroups : kGroups / kParts, stages_b);
             }
             turn -= tiles;
             named_sync(1, kWorkers);  // the sums of the run before are read
+            float *const mine = sums + ((grp & 1) * a.cols + (lane & 3) * 2) * kSumStride + rows32 * 32 + (lane >> 2);
+            if (grp >= 2) {
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
+                for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const int col = nt * 8 + (lane & 3) * 2 + (i & 1);
-                    const int r = rows32 * 32 + (i >> 2) * 16 + ((i >> 1) & 1) * 8 + (lane >> 2);
-                    sums[(grp * a.cols + col) * kSumStride + r] = acc[nt][i >> 2][i & 3];
-                }
+                    for (int i = 0; i < 8; ++i)
+                        mine[(nt * 8 + (i & 1)) * kSumStride + (i >> 1) * 8] = acc[nt][i >> 2][i & 3];
+            }
+            named_sync(1, kWorkers);
+            if (grp < 2) {
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        mine[(nt * 8 + (i & 1)) * kSumStride + (i >> 1) * 8] += acc[nt][i >> 2][i & 3];
+            }
             run = named_all(2, kWorkers, run);
         };
         auto by_group = [&](auto blocks, auto second, int tiles) {
@@ -341,17 +351,9 @@ __global__ void __launch_bounds__(kThreads, 1) int4_kernel(const __grid_constant
             else
                 by_group(std::integral_constant<int, 4>{}, second, tiles);
         };
-        // Column j of the groups' sums, this thread's row: all groups, or the even (0) or odd (1) ones.
-        auto sum_all = [&](int j) {
-            const float *const s = sums + j * kSumStride + row;
-            const int g = a.cols * kSumStride;
-            return (s[0] + s[g]) + (s[2 * g] + s[3 * g]);
-        };
-        auto sum_half = [&](int j, int odd) {
-            const float *const s = sums + j * kSumStride + row;
-            const int g = a.cols * kSumStride;
-            return s[odd * g] + s[(2 + odd) * g];
-        };
+        // Column j of the sums, this thread's row: of the even (0) or odd (1) groups, or all.
+        auto sum_half = [&](int j, int odd) { return sums[(odd * a.cols + j) * kSumStride + row]; };
+        auto sum_all = [&](int j) { return sum_half(j, 0) + sum_half(j, 1); };
 
         // As in moe_experts.cu: tiles shared with other blocks are settled after a product's last run.
         auto leave = [&](Rests &rests, int i, int m, const Split &sp, int *counter) {
@@ -585,8 +587,9 @@ size_t int4_smem(Int4Args *a, bool linear)
 {
     a->cols = ((a->T < kCap ? a->T : kCap) + 7) & ~7;
     const size_t lists = (linear ? 0 : static_cast<size_t>(a->T) * kTileRows * 4) +
-                         static_cast<size_t>(kGroups) * a->cols * kSumStride * 4 + lists_bytes(a->E, a->P);
-    a->bytes_b = a->cols <= 8 ? 32 * 1024 : 48 * 1024;  // at least 8 and 3 stages of the largest token tile
+                         static_cast<size_t>(2) * a->cols * kSumStride * 4 + lists_bytes(a->E, a->P);
+    // at least 8 or 4 stages of the largest token tile: a group's next tile is up to four stages on
+    a->bytes_b = a->cols <= 8 ? 32 * 1024 : 64 * 1024;
     a->shift1 = a->group1 == 32 ? 0 : a->group1 == 64 ? 1 : 2;
     a->shift2 = a->group2 == 32 ? 0 : a->group2 == 64 ? 1 : 2;
     a->stage_a = a->tile1 > a->tile2 ? a->tile1 : a->tile2;

@@ -20,13 +20,12 @@ struct Cursor {
             parity ^= 1;
         }
     }
+    // k <= n
     __device__ __forceinline__ void advance(int k, int n)
     {
-        s += k;
-        while (s >= n) {
-            s -= n;
-            parity ^= 1;
-        }
+        const int to = s + k;
+        parity ^= to >= n ? 1 : 0;
+        s = to >= n ? to - n : to;
     }
     // To position i of the sequence.
     __device__ __forceinline__ void skip(int i, int n)
