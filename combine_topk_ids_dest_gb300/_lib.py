@@ -111,7 +111,7 @@ class EpWeightC(ctypes.Structure):
 class EpIntWeightC(ctypes.Structure):
     _fields_ = [("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p), ("zeros", ctypes.c_void_p),
                 ("scale_dtype", ctypes.c_int), ("mats", ctypes.c_int), ("rows", ctypes.c_int),
-                ("cols", ctypes.c_int), ("group", ctypes.c_int)]
+                ("cols", ctypes.c_int), ("group", ctypes.c_int), ("gate_up", ctypes.c_int)]
 
 
 class EpLinearConfigC(ctypes.Structure):

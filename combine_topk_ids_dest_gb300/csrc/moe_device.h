@@ -125,12 +125,12 @@ static __device__ __forceinline__ bool mbar_wait2_warp(uint32_t bar1, uint32_t p
 }
 
 // mbar_arrive on two barriers where `me` is true, without a branch.
-static __device__ __forceinline__ void mbar_arrive2_if(bool me, uint32_t bar1, uint32_t bar2, uint32_t count2)
+static __device__ __forceinline__ void mbar_arrive2_if(bool me, uint32_t bar1, uint32_t bar2)
 {
     asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %0, 0;\n\t"
                  "@p mbarrier.arrive.shared::cta.b64 _, [%1];\n\t"
-                 "@p mbarrier.arrive.shared::cta.b64 _, [%2], %3;\n\t}" ::"r"(uint32_t(me)),
-                 "r"(bar1), "r"(bar2), "r"(count2)
+                 "@p mbarrier.arrive.shared::cta.b64 _, [%2];\n\t}" ::"r"(uint32_t(me)),
+                 "r"(bar1), "r"(bar2)
                  : "memory");
 }
 
@@ -153,6 +153,14 @@ static __device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorM
     asm volatile("cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
                  "[%0], [%1, {%3, %4}], [%2];" ::"r"(dst),
                  "l"(m), "r"(bar), "r"(x), "r"(y)
+                 : "memory");
+}
+
+static __device__ __forceinline__ void tma_load_box(uint32_t dst, const CUtensorMap *m, uint32_t bar, int x, int y, int z)
+{
+    asm volatile("cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
+                 "[%0], [%1, {%3, %4, %5}], [%2];" ::"r"(dst),
+                 "l"(m), "r"(bar), "r"(x), "r"(y), "r"(z)
                  : "memory");
 }
 

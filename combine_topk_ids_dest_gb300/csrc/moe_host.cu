@@ -105,6 +105,25 @@ ep_status encode_map(CUtensorMap *m, const char *what, int fp16, const void *bas
     return EP_OK;
 }
 
+// A 16-bit tensor [rows, 32 n] as [n][rows][32]: boxes of all its inner 32
+// columns, box_rows rows and box_steps steps of 32, zeros outside.
+ep_status encode_steps(CUtensorMap *m, const char *what, int fp16, const void *base, long long steps, long long rows,
+                       long long row_stride, int box_rows, int box_steps)
+{
+    EncodeTiled fn = encode_tiled();
+    if (!fn)
+        return set_error(EP_ERR_CUDA, "cuTensorMapEncodeTiled is not available");
+    const cuuint64_t dims[3] = {32, cuuint64_t(rows), cuuint64_t(steps)}, strides[2] = {cuuint64_t(row_stride) * 2, 64};
+    const cuuint32_t box[3] = {32, cuuint32_t(box_rows), cuuint32_t(box_steps)}, step[3] = {1, 1, 1};
+    const CUresult r = fn(m, fp16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3,
+                          const_cast<void *>(base), dims, strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                          CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (r != CUDA_SUCCESS)
+        return set_error(EP_ERR_CUDA, "cuTensorMapEncodeTiled of %s: error %d", what, static_cast<int>(r));
+    return EP_OK;
+}
+
 // Device words and the host flag of a handle whose blocks wait for one another.
 struct Flags {
     unsigned int *err = nullptr;  // pinned host memory the kernels can write
@@ -341,6 +360,8 @@ ep_status check_int_weight(const ep_int_weight *w)
         MOE_FAIL("group=%d: use 32, 64 or 128", w->group);
     if (w->mats < 1 || w->rows < 1 || w->cols < 1 || w->cols % w->group)
         MOE_FAIL("mats=%d, rows=%d, cols=%d: positive, cols a multiple of group=%d", w->mats, w->rows, w->cols, w->group);
+    if (w->gate_up && w->mats % 2)
+        MOE_FAIL("gate_up: mats=%d is odd", w->mats);
     if (w->cols > EP_MOE_MAX_DIM || w->rows > 16 * EP_MOE_MAX_DIM || w->mats > 2 * EP_MOE_MAX_EXPERTS)
         MOE_FAIL("mats=%d, rows=%d, cols=%d are limited to %d, %d, %d", w->mats, w->rows, w->cols,
                  2 * EP_MOE_MAX_EXPERTS, 16 * EP_MOE_MAX_DIM, EP_MOE_MAX_DIM);
@@ -457,6 +478,7 @@ ep_status ep_weight_pack(const ep_int_weight *w, void *packed, size_t bytes, voi
     a.mt = div_up(w->rows, 128);
     a.kc = div_up(w->cols, 128);
     a.tile_bytes = moe::int4_tile_bytes(w->group, w->zeros != nullptr);
+    a.pairs = w->gate_up != 0;
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
     const cudaError_t ce = moe::launch_pack(a, s);
     return ce == cudaSuccess ? set_error(EP_OK, "") : cuda_error(ce, "ep_weight_pack");
@@ -569,7 +591,9 @@ ep_status ep_linear_run(ep_linear *h, ep_dtype dtype, const void *x, long long x
     a.E = 1;
     a.H = c.inputs;
     a.I = c.outputs;
-    st = encode_map(&a.mx, "x", dtype == EP_DTYPE_FP16, x, a.H, a.T, 0, x_stride, 0, 32, 8);
+    const int rows = moe::int4_linear_rows(a.T);
+    a.box_bytes = rows * 512;
+    st = encode_steps(&a.mx, "x", dtype == EP_DTYPE_FP16, x, a.H / 32, a.T, x_stride, rows, 8);
     if (st != EP_OK)
         return st;
     a.w1 = static_cast<const uint8_t *>(c.weight.data);
@@ -698,6 +722,8 @@ ep_status experts_args(const ep_experts *h, Args &a, const ExpertsLayout &l, con
     a.kc1 = div_up(a.H, chunk);
     a.mt2 = div_up(a.H, moe::kTileRows);
     a.kc2 = div_up(a.I, chunk);
+    if (box_cols == 32 && a.T <= 8)
+        return encode_steps(&a.mx, "x", 0, x, a.H / 32, a.T, x_stride, 8, 4);
     return encode_map(&a.mx, "x", 0, x, a.H, a.T, 0, x_stride, 0, box_cols, 1);
 }
 
@@ -802,6 +828,7 @@ ep_status ep_experts_run(ep_experts *h, const void *x, long long x_stride, const
         a.tile2 = moe::int4_tile_bytes(a.group2, a.zeros2);
         a.scale_fp16 = c.gate_up.scale_dtype == EP_DTYPE_FP16;
         a.out = out;
+        a.box_bytes = 2048;
         a.chk = epk::check_ctx(rec);
         const size_t smem = moe::int4_smem(&a, false);
         ce = moe::launch_int4(a, false, true, h->base.sms, smem, s);

@@ -5,11 +5,14 @@
 //   linear:   y = x W^T
 //   experts:  as in moe_experts.cu
 //
-// Work is cut and shared tiles are settled as in moe_experts.cu. A stage of
-// the weights' ring is a tile of 128 rows x 128 inputs, repacked once when
-// the weight was taken: 8 KB of codes, its scales and zero points. Four
-// groups of four warps take tiles in turn (gate tiles fall to groups 0 and
-// 2, up tiles to 1 and 3). A warp has 32 rows of its tile:
+// Work is cut and shared tiles are settled as in moe_experts.cu. A weight is
+// repacked once, when it is taken, to tiles of 128 rows x 128 inputs: 8 KB of
+// codes, their scales and zero points. A unit of work, and a stage of the
+// weights' ring, is two tiles that lie side by side: the gate and the up tile
+// of a chunk of inputs, or two chunks of the other products; one copy of 17
+// KB each, since a copy's issue costs the producer more than its bytes. Four
+// groups of four warps take the tiles in turn (the first tile of a unit falls
+// to groups 0 and 2, the second to 1 and 3). A warp has 32 rows of its tile:
 //
 //  - codes are packed in the order of the MMA's A fragment, so a 16-byte
 //    load is four fragments; two or three instructions turn a pair of codes
@@ -37,7 +40,7 @@ namespace {
 constexpr int kGroups = 4;                 // groups of four warps
 constexpr int kWorkers = kGroups * 128;
 constexpr int kThreads = kWorkers + 64;    // the last two warps bring weights and tokens
-constexpr int kMaxStagesA = 24;
+constexpr int kMaxStagesA = 12;
 constexpr int kMaxStagesB = 16;
 constexpr int kCap = 32;                   // tokens of an entry: 4 column blocks of 8
 constexpr int kSumStride = kTileRows + 4;  // column stride of the groups' sums: fragments' stores hit all banks
@@ -151,26 +154,25 @@ __global__ void __launch_bounds__(kThreads, 1) int4_kernel(const __grid_constant
     const int tid = threadIdx.x, warp = __shfl_sync(~0u, tid >> 5, 0), lane = tid & 31;
     const int G = gridDim.x, blk = blockIdx.x;
     volatile int *const abort = &sh.abort;
-    constexpr int kParts = LINEAR ? 1 : 2;  // tiles that share a token tile in the first product
 
     if (tid == 0) {
         sh.abort = sh.reset = sh.rests[0].n = sh.rests[1].n = sh.issued_a = sh.issued_b = 0;
         for (int i = 0; i < kMaxStagesA; ++i) {
             mbar_init(smem_u32(&sh.full_a[i]), 1);
-            mbar_init(smem_u32(&sh.empty_a[i]), 4);
+            mbar_init(smem_u32(&sh.empty_a[i]), 8);
         }
         for (int i = 0; i < kMaxStagesB; ++i) {
             mbar_init(smem_u32(&sh.full_b[i]), 1);
-            mbar_init(smem_u32(&sh.empty_b[i]), 4 * kParts);
+            mbar_init(smem_u32(&sh.empty_b[i]), 8);
         }
         mbar_init_fence();
         tma_prefetch_map(&a.mx);
     }
     if (LINEAR) {  // one "expert" whose tokens are the rows of x
         if (tid == 0) {
-            const int half = a.T > kCap ? ((a.T + 1) / 2 + 7) & ~7 : a.T;
-            sh.active = a.T > kCap ? 2 : 1;
-            sh.nmax = half;
+            const int rows = a.box_bytes / 512, half = min(a.T, rows);  // int4_linear_rows
+            sh.active = a.T > rows ? 2 : 1;
+            sh.nmax = rows;
             li.expert[0] = li.expert[1] = 0;
             li.offset[0] = 0;
             li.offset[1] = static_cast<unsigned short>(half);
@@ -187,12 +189,17 @@ __global__ void __launch_bounds__(kThreads, 1) int4_kernel(const __grid_constant
         return;
     }
 
-    const int total1 = A * a.mt1 * a.kc1, total2 = LINEAR ? 0 : A * a.mt2 * a.kc2;
+    // units along the inputs; the last one of an odd number of chunks is half empty
+    const int ku1 = LINEAR ? (a.kc1 + 1) / 2 : a.kc1, ku2 = (a.kc2 + 1) / 2;
+    const int total1 = A * a.mt1 * ku1, total2 = LINEAR ? 0 : A * a.mt2 * ku2;
     const Shares shares1(total1, G), shares2(total2, G);
     const int begin1 = shares1.begin(blk), end1 = shares1.begin(blk + 1);
     const int begin2 = LINEAR ? 0 : shares2.begin(blk), end2 = LINEAR ? 0 : shares2.begin(blk + 1);
     const int pairs = li.offset[A];
-    const int stage_b = ceil_div(sh.nmax, 8) * (LINEAR ? 2048 : 4096);  // 8 tokens x 128 inputs: 2 KB, h in two parts
+    // A unit's token tile, in 8-token steps of 2 KB a chunk: two chunks, or one, and later two in two parts.
+    const int stage_b = ceil_div(sh.nmax, 8) * (LINEAR ? 4096 : 8192);
+    // With up to 8 tokens every expert's token tile is all of x: a sum's column is the token. Else the tokens are gathered.
+    const bool whole = LINEAR || a.T <= 8;
     const int stages_b = min(kMaxStagesB, a.bytes_b / stage_b);
     // h: per entry and chunk a tile [2 parts][4][tokens][32], tokens a multiple of 8
     const auto h_entry = [&](int i) { return a.h + static_cast<size_t>(li.offset[i] + 7 * i) * a.h_stride; };
@@ -213,17 +220,17 @@ __global__ void __launch_bounds__(kThreads, 1) int4_kernel(const __grid_constant
             ++issued;
             return true;
         };
-        const size_t up = static_cast<size_t>(a.mt1) * a.kc1 * a.tile1;  // from a gate tile to its up tile
-        for (Walk w(begin1, end1, a.kc1, a.mt1, false); run && w.more(); w.next()) {
-            const uint8_t *src =
-                a.w1 + ((static_cast<size_t>(li.expert[w.i]) * kParts * a.mt1 + w.m) * a.kc1 + w.k) * a.tile1;
-            for (int k = 0; run && k < w.len; ++k, src += a.tile1)
-                run = load(src, a.tile1) && (LINEAR || load(src + up, a.tile1));
+        // tiles: [matrix][row tile][chunk]; gate and up tiles side by side
+        for (Walk w(begin1, end1, ku1, a.mt1, false); run && w.more(); w.next()) {
+            const int tiles = LINEAR ? a.kc1 : 2 * a.kc1;
+            const uint8_t *src = a.w1 + ((static_cast<size_t>(li.expert[w.i]) * a.mt1 + w.m) * tiles + 2 * w.k) * a.tile1;
+            for (int k = w.k; run && k < w.k + w.len; ++k, src += 2 * a.tile1)
+                run = load(src, 2 * k + 1 < tiles ? 2 * a.tile1 : a.tile1);
         }
-        for (Walk w(begin2, end2, a.kc2, A, true); run && w.more(); w.next()) {
-            const uint8_t *src = a.w2 + ((static_cast<size_t>(li.expert[w.i]) * a.mt2 + w.m) * a.kc2 + w.k) * a.tile2;
-            for (int k = 0; run && k < w.len; ++k, src += a.tile2)
-                run = load(src, a.tile2);
+        for (Walk w(begin2, end2, ku2, A, true); run && w.more(); w.next()) {
+            const uint8_t *src = a.w2 + ((static_cast<size_t>(li.expert[w.i]) * a.mt2 + w.m) * a.kc2 + 2 * w.k) * a.tile2;
+            for (int k = w.k; run && k < w.k + w.len; ++k, src += 2 * a.tile2)
+                run = load(src, 2 * k + 1 < a.kc2 ? 2 * a.tile2 : a.tile2);
         }
         sh.issued_a = issued;
     } else if (warp == kWorkers / 32 + 1 && elect_one()) {
@@ -242,15 +249,13 @@ __global__ void __launch_bounds__(kThreads, 1) int4_kernel(const __grid_constant
             ++issued;
             return true;
         };
-        for (Walk w(begin1, end1, a.kc1, a.mt1, false); run && w.more(); w.next()) {
+        for (Walk w(begin1, end1, ku1, a.mt1, false); run && w.more(); w.next()) {
             const int n = li.count(w.i), n8 = (n + 7) & ~7, off = li.offset[w.i];
             const unsigned char *const tok = li.token + off;
-            const uint32_t bytes = (LINEAR ? n8 : (n + 3) & ~3) * 256;
+            const uint32_t bytes = whole ? a.box_bytes : ((n + 3) & ~3) * 256;
             for (int k = w.k; k < w.k + w.len && (run = acquire(bytes)); ++k) {
-                if (LINEAR) {
-                    for (int j = 0; j < n; j += 8)
-                        for (int q = 0; q < 4; ++q)
-                            tma_load_2d(dst + (q * n8 + j) * 64, &a.mx, bar, k * 128 + q * 32, off + j);
+                if (whole) {  // [inputs / 32][tokens][32]
+                    tma_load_box(dst, &a.mx, bar, 0, LINEAR ? off : 0, LINEAR ? 8 * k : 4 * k);
                 } else {
                     for (int j = 0; j < n; j += 4) {  // short of a fourth row: the last one again
                         const int r0 = tok[j], r1 = tok[min(j + 1, n - 1)], r2 = tok[min(j + 2, n - 1)],
@@ -266,29 +271,31 @@ __global__ void __launch_bounds__(kThreads, 1) int4_kernel(const __grid_constant
             fence_async_proxy();
         }
         const uint64_t policy = policy_evict_first();
-        for (Walk w(begin2, end2, a.kc2, A, true); run && w.more(); w.next()) {
-            const uint32_t bytes = ceil_div(li.count(w.i), 8) * 4096;
-            const uint8_t *src = reinterpret_cast<const uint8_t *>(h_entry(w.i)) + static_cast<size_t>(w.k) * bytes;
-            for (int k = 0; k < w.len && (run = acquire(bytes)); ++k, src += bytes)
-                bulk_load(dst, src, bytes, bar, policy);
+        for (Walk w(begin2, end2, ku2, A, true); run && w.more(); w.next()) {
+            const uint32_t chunk = ceil_div(li.count(w.i), 8) * 4096;
+            const uint8_t *src = reinterpret_cast<const uint8_t *>(h_entry(w.i)) + static_cast<size_t>(2 * w.k) * chunk;
+            for (int k = w.k; run && k < w.k + w.len; ++k, src += 2 * chunk) {
+                const uint32_t bytes = 2 * k + 1 < a.kc2 ? 2 * chunk : chunk;
+                run = acquire(bytes);
+                if (run)
+                    bulk_load(dst, src, bytes, bar, policy);
+            }
         }
         sh.issued_b = issued;
     } else if (warp < kWorkers / 32) {
         // ---- products ----
         const int grp = warp >> 2, rows32 = warp & 3, row = tid & 127;
-        Cursor at_a, at_b;  // of this group's next tile
-        int turn = grp;     // tiles until this group's
-        for (int i = 0; i < grp; ++i) {
-            at_a.next(a.stages);
-            if (i % kParts == kParts - 1)
-                at_b.next(stages_b);
-        }
+        const int tile = grp & 1;  // of a unit
+        Cursor at_a, at_b;         // of this group's next unit
+        int turn = grp >> 1;       // units until then
+        at_a.s = at_b.s = turn;
         bool run = true;
         constexpr uint32_t empty_a = offsetof(Shared, empty_a) - offsetof(Shared, full_a);
         constexpr uint32_t empty_b = offsetof(Shared, empty_b) - offsetof(Shared, full_b);
 
-        // This group's tiles of a run of `tiles`; its sums go to shared memory.
-        auto products = [&](auto blocks, auto log_group, auto second, int tiles) {
+        // This group's tiles of a run of `units`; its sums go to shared memory. kc: chunks along the inputs,
+        // k: the run's first unit there.
+        auto products = [&](auto blocks, auto log_group, auto second, int units, int k, int kc) {
             constexpr int NT = decltype(blocks)::value, SHIFT = decltype(log_group)::value;
             constexpr bool SECOND = decltype(second)::value;
             const bool with_zeros = SECOND ? a.zeros2 : a.zeros1, scale_fp16 = a.scale_fp16;
@@ -298,21 +305,25 @@ __global__ void __launch_bounds__(kThreads, 1) int4_kernel(const __grid_constant
 #pragma unroll
                 for (int i = 0; i < 8; ++i)
                     acc[nt][i >> 2][i & 3] = 0.0f;
-            for (; turn < tiles; turn += kGroups) {
+            // rows of 32 inputs and one token are 64 bytes: the second chunk's token tile
+            const int chunk_b = !tile ? 0 : LINEAR ? NT * 8 * 256 : SECOND ? NT * 8 * 512 : 0;
+            for (; turn < units; turn += 2) {
                 const uint32_t fa = smem_u32(&sh.full_a[at_a.s]), fb = smem_u32(&sh.full_b[at_b.s]);
                 if (!mbar_wait2_warp(fa, at_a.parity, fb, at_b.parity, abort, kWaitFullA, kWaitFullB)) {
                     run = false;
-                    turn = tiles;
+                    turn = units;
                     break;
                 }
-                add_tile<NT, SHIFT, SECOND ? 2 : 1, BF16>(acc, ring_a_p + at_a.s * a.stage_a, rows32, lane,
-                                                          ring_b_p + at_b.s * stage_b, with_zeros, scale_fp16);
+                if ((!LINEAR && !SECOND) || 2 * (k + turn) + tile < kc)
+                    add_tile<NT, SHIFT, SECOND ? 2 : 1, BF16>(
+                        acc, ring_a_p + at_a.s * a.stage_a + tile * (SECOND ? a.tile2 : a.tile1), rows32, lane,
+                        ring_b_p + at_b.s * stage_b + chunk_b, with_zeros, scale_fp16);
                 __syncwarp();
-                mbar_arrive2_if(lane == 0, fa + empty_a, fb + empty_b, SECOND ? kParts : 1);
-                at_a.advance(kGroups, a.stages);  // the group's next tile
-                at_b.advance(SECOND ? kGroups : kGroups / kParts, stages_b);
+                mbar_arrive2_if(lane == 0, fa + empty_a, fb + empty_b);
+                at_a.advance(2, a.stages);  // the group's next unit
+                at_b.advance(2, stages_b);
             }
-            turn -= tiles;
+            turn -= units;
             named_sync(1, kWorkers);  // the sums of the run before are read
             float *const mine = sums + ((grp & 1) * a.cols + (lane & 3) * 2) * kSumStride + rows32 * 32 + (lane >> 2);
             if (grp >= 2) {
@@ -332,24 +343,24 @@ __global__ void __launch_bounds__(kThreads, 1) int4_kernel(const __grid_constant
             }
             run = named_all(2, kWorkers, run);
         };
-        auto by_group = [&](auto blocks, auto second, int tiles) {
+        auto by_group = [&](auto blocks, auto second, int units, int k, int kc) {
             const int shift = decltype(second)::value ? a.shift2 : a.shift1;
             if (shift == 0)
-                products(blocks, std::integral_constant<int, 0>{}, second, tiles);
+                products(blocks, std::integral_constant<int, 0>{}, second, units, k, kc);
             else if (shift == 1)
-                products(blocks, std::integral_constant<int, 1>{}, second, tiles);
+                products(blocks, std::integral_constant<int, 1>{}, second, units, k, kc);
             else
-                products(blocks, std::integral_constant<int, 2>{}, second, tiles);
+                products(blocks, std::integral_constant<int, 2>{}, second, units, k, kc);
         };
-        auto run_products = [&](auto second, int n, int tiles) {
+        auto run_products = [&](auto second, int n, int units, int k, int kc) {
             if (n <= 8)
-                by_group(std::integral_constant<int, 1>{}, second, tiles);
+                by_group(std::integral_constant<int, 1>{}, second, units, k, kc);
             else if (n <= 16)
-                by_group(std::integral_constant<int, 2>{}, second, tiles);
+                by_group(std::integral_constant<int, 2>{}, second, units, k, kc);
             else if (n <= 24)
-                by_group(std::integral_constant<int, 3>{}, second, tiles);
+                by_group(std::integral_constant<int, 3>{}, second, units, k, kc);
             else
-                by_group(std::integral_constant<int, 4>{}, second, tiles);
+                by_group(std::integral_constant<int, 4>{}, second, units, k, kc);
         };
         // Column j of the sums, this thread's row: of the even (0) or odd (1) groups, or all.
         auto sum_half = [&](int j, int odd) { return sums[(odd * a.cols + j) * kSumStride + row]; };
@@ -389,15 +400,17 @@ __global__ void __launch_bounds__(kThreads, 1) int4_kernel(const __grid_constant
         };
         const int set = tid >> 7;  // of columns
 
-        for (Walk w(begin1, end1, a.kc1, a.mt1, false); run && w.more(); w.next()) {
-            const int n = li.count(w.i), tile = w.i * a.mt1 + w.m;
-            const Split sp(shares1, tile * a.kc1, a.kc1);
-            run_products(std::false_type{}, n, w.len * kParts);
+        for (Walk w(begin1, end1, ku1, a.mt1, false); run && w.more(); w.next()) {
+            const int n = li.count(w.i), row_tile = w.i * a.mt1 + w.m;
+            const unsigned char *const tok = li.token + li.offset[w.i];
+            const Split sp(shares1, row_tile * ku1, ku1);
+            run_products(std::false_type{}, LINEAR ? sh.nmax : n, w.len, w.k, a.kc1);
             if (!run)
                 break;
             float *const part = a.part + static_cast<size_t>(sp.slot(blk)) * a.part_floats + row;
             for (int j = set; j < n; j += kGroups) {
-                const float g = LINEAR ? sum_all(j) : sum_half(j, 0), u = LINEAR ? 0.0f : sum_half(j, 1);
+                const int c = !LINEAR && whole ? tok[j] : j;  // the sum's column
+                const float g = LINEAR ? sum_all(c) : sum_half(c, 0), u = LINEAR ? 0.0f : sum_half(c, 1);
                 if (sp.shared()) {
                     part[j * kTileRows] = g;
                     if (!LINEAR)
@@ -407,7 +420,7 @@ __global__ void __launch_bounds__(kThreads, 1) int4_kernel(const __grid_constant
                 }
             }
             if (sp.shared())
-                leave(sh.rests[0], w.i, w.m, sp, a.tiles + tile);
+                leave(sh.rests[0], w.i, w.m, sp, a.tiles + row_tile);
             else if (!LINEAR)
                 announce(n);
         }
@@ -432,28 +445,21 @@ __global__ void __launch_bounds__(kThreads, 1) int4_kernel(const __grid_constant
                 announce(hi - lo);
         }
 
-        if (!LINEAR) {  // the groups' turns and token tiles start anew
-            const int tiles1 = (end1 - begin1) * 2;
-            turn = (grp + kGroups - tiles1 % kGroups) % kGroups;
-            at_a = at_b = Cursor();
-            at_a.skip(tiles1 + turn, a.stages);
-            at_b.skip(end1 - begin1 + turn, stages_b);
-        }
-        const int group = LINEAR ? 1 : A * a.kc2;
+        const int group = LINEAR ? 1 : A * ku2;
         auto store_y = [&](int m, int t, float r) {
             const int col = m * kTileRows + row;
             __nv_bfloat16 *const p = static_cast<__nv_bfloat16 *>(a.out) + t * a.out_stride + col;
             if (col < a.H && EP_IN_BOUNDS(a.chk, epk::kSiteMoeOut, p, 2, a.out, 2 * ((a.T - 1) * a.out_stride + a.H)))
                 *p = __float2bfloat16_rn(r);
         };
-        for (Walk w(begin2, end2, a.kc2, A, true); !LINEAR && run && w.more();) {
+        for (Walk w(begin2, end2, ku2, A, true); !LINEAR && run && w.more();) {
             const int m = w.m, i0 = w.i;
             const Split sp(shares2, m * group, group);
             for (int t = set; t < a.T; t += kGroups)
                 acc_y[t * kTileRows + row] = 0.0f;
             for (; run && w.more() && w.m == m; w.next()) {
                 const int off = li.offset[w.i], n = li.count(w.i);
-                run_products(std::true_type{}, n, w.len);  // its barriers also order the threads' turns at a row of acc_y
+                run_products(std::true_type{}, n, w.len, w.k, a.kc2);  // its barriers also order the threads' turns at a row of acc_y
                 for (int j = set; run && j < n; j += kGroups) {
                     float *const s = acc_y + li.token[off + j] * kTileRows + row;
                     *s = fmaf(li.weight[off + j], sum_all(j), *s);
@@ -549,7 +555,8 @@ __global__ void __launch_bounds__(256) pack_kernel(const __grid_constant__ PackA
             word[2 * s + f] |= ((in >> (4 * c)) & 15u) << ((2 * v + low) * 4 + e * 16);
         }
     }
-    uint8_t *const dst = a.dst + tile * a.tile_bytes;
+    const long long to = a.pairs ? ((mat / 2 * a.mt + m) * a.kc + kc) * 2 + mat % 2 : tile;
+    uint8_t *const dst = a.dst + to * a.tile_bytes;
     *reinterpret_cast<uint4 *>(dst + ((rb * 4 + q) * 32 + lane) * 16) = make_uint4(word[0], word[1], word[2], word[3]);
     const int groups = 128 / a.group, row = rb * 32 + lane, r = m * 128 + row;
     if (q < groups) {
@@ -583,16 +590,24 @@ size_t int4_h_rows(int T, int K, int E)
     return static_cast<size_t>(pairs) + 7 * static_cast<size_t>(entries) + 8;
 }
 
+int int4_linear_rows(int T)
+{
+    const int n = T > kCap ? (T + 1) / 2 : T;
+    return (n + 7) & ~7;
+}
+
 size_t int4_smem(Int4Args *a, bool linear)
 {
     a->cols = ((a->T < kCap ? a->T : kCap) + 7) & ~7;
     const size_t lists = (linear ? 0 : static_cast<size_t>(a->T) * kTileRows * 4) +
                          static_cast<size_t>(2) * a->cols * kSumStride * 4 + lists_bytes(a->E, a->P);
-    // at least 8 or 4 stages of the largest token tile: a group's next tile is up to four stages on
-    a->bytes_b = a->cols <= 8 ? 32 * 1024 : 64 * 1024;
+    // the largest token tile: 8 KB for 8 tokens (4 for the linear layer); at least 2 stages, a group's next is two on
+    a->bytes_b = (linear || a->cols <= 16 ? 4 : 2) * a->cols * (linear ? 512 : 1024);
+    if (a->bytes_b < 32 * 1024)
+        a->bytes_b = 32 * 1024;
     a->shift1 = a->group1 == 32 ? 0 : a->group1 == 64 ? 1 : 2;
     a->shift2 = a->group2 == 32 ? 0 : a->group2 == 64 ? 1 : 2;
-    a->stage_a = a->tile1 > a->tile2 ? a->tile1 : a->tile2;
+    a->stage_a = 2 * (a->tile1 > a->tile2 ? a->tile1 : a->tile2);
     a->part_floats = static_cast<int>(int4_part_floats(a->T, linear));
     const size_t room = kSmemMax - sizeof(Shared) - 128 - lists - a->bytes_b - 64;
     a->stages = static_cast<int>(room / a->stage_a);

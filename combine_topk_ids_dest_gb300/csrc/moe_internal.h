@@ -91,7 +91,7 @@ size_t experts_part_floats(int T);
 // ---- products with 4-bit weights (moe_int4.cu) -------------------------------------
 
 struct Int4Args {
-    CUtensorMap mx;  // x [T, H]: one-row boxes (experts) or 8-row boxes (linear) of 32 columns
+    CUtensorMap mx;  // x: boxes 32 x 1 of [T, H], or boxes 32 x tokens x 4 (linear: 8) of [H / 32, T, 32]
     const uint8_t *w1, *w2;  // packed tiles [matrix][row tile][chunk]
     const int32_t *ids;
     const float *weights;
@@ -107,7 +107,7 @@ struct Int4Args {
     int group1, group2, shift1, shift2;  // shift: log2(group / 32)
     int zeros1, zeros2, tile1, tile2, scale_fp16;
     int h_stride;
-    int stages, stage_a, bytes_b, part_floats, cols;
+    int stages, stage_a, bytes_b, part_floats, cols, box_bytes;
     epk::CheckCtx chk;
 };
 
@@ -118,11 +118,13 @@ struct PackArgs {
     uint8_t *dst;
     long long mats;
     int rows, cols, group, mt, kc, tile_bytes;
+    int pairs;  // tiles of matrices 2 i and 2 i + 1 side by side
 };
 
 int int4_tile_bytes(int group, bool zeros);  // of one tile of 128 rows x 128 inputs
 size_t int4_part_floats(int T, bool linear);
 size_t int4_h_rows(int T, int K, int E);
+int int4_linear_rows(int T);  // rows of x one run over the weight takes: T in one or two runs, a multiple of 8
 size_t int4_smem(Int4Args *a, bool linear);
 cudaError_t launch_int4(const Int4Args &a, bool linear, bool bf16, int grid, size_t smem, cudaStream_t stream);
 cudaError_t launch_pack(const PackArgs &a, cudaStream_t stream);

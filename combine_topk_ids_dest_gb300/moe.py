@@ -176,12 +176,12 @@ class Int4Weight:
         self.zeros = None if zeros is None else _weight("zeros", zeros, torch.uint8, shape, device)
         self.device = device
 
-    def pack(self, mats: int, rows: int) -> torch.Tensor:
+    def pack(self, mats: int, rows: int, gate_up: bool = False) -> torch.Tensor:
         """The weight as ``mats`` matrices of ``rows`` rows, in the operators' order (ep_weight_pack)."""
         L = _lib.load()
         w = _lib.EpIntWeightC(self.codes.data_ptr(), self.scales.data_ptr(),
                               0 if self.zeros is None else self.zeros.data_ptr(), _DTYPES[self.scales.dtype], mats, rows,
-                              self.shape[-1], self.group)
+                              self.shape[-1], self.group, int(gate_up))
         need = ctypes.c_size_t(0)
         check(L.ep_weight_packed_size(ctypes.byref(w), ctypes.byref(need)))
         with torch.cuda.device(self.device):
@@ -268,7 +268,7 @@ class EpExperts(_Workspace):
         if packed:
             if down.shape != (E, H, I2 // 2) or down.device != device:
                 raise ValueError(f"down must be {(E, H, I2 // 2)} on {device}, got {down.shape} on {down.device}")
-            self._w = (gate_up.pack(2 * E, I2 // 2), down.pack(E, H))
+            self._w = (gate_up.pack(2 * E, I2 // 2, gate_up=True), down.pack(E, H))
             cw = gate_up._c(self._w[0]), down._c(self._w[1])
         else:
             self._w = (_weight("gate_up", gate_up, torch.bfloat16, (E, I2, H), device),

@@ -97,6 +97,8 @@ typedef struct {
     ep_dtype scale_dtype;
     int mats, rows, cols;  /* rows, cols >= 1; cols a multiple of group */
     int group;             /* 32, 64 or 128 */
+    int gate_up;           /* 0, or 1: matrices are gate and up in turn (mats even), packed for
+                              ep_experts_config.gate_up */
 } ep_int_weight;
 
 /* A weight as the operators take it: group 0: data is bf16, contiguous,
@@ -113,7 +115,8 @@ ep_status ep_weight_packed_size(const ep_int_weight *w, size_t *bytes);
 
 /* Packs w into packed: device, 128-byte aligned, of at least
  * ep_weight_packed_size bytes. w is not needed once the queued work has run.
- * (gate_up of experts is packed as 2*experts matrices of `intermediate` rows.) */
+ * gate_up of experts is packed as 2*experts matrices of `intermediate` rows,
+ * with the gate_up field set. */
 ep_status ep_weight_pack(const ep_int_weight *w, void *packed, size_t bytes, void *stream);
 
 /* ---- linear ----------------------------------------------------------------------
