@@ -66,27 +66,25 @@ __global__ void __launch_bounds__(kThreads, 1) experts_kernel(const __grid_const
     const int G = gridDim.x, blk = blockIdx.x;
     volatile int *const abort = &sh.abort;
 
-    if (tid == 0) {
-        sh.abort = sh.reset = sh.rests[0].n = sh.rests[1].n = sh.issued_a = sh.issued_b = 0;
-        for (int i = 0; i < kMaxStagesA; ++i) {
-            mbar_init(smem_u32(&sh.full_a[i]), 1);
-            mbar_init(smem_u32(&sh.empty_a[i]), 1);
-        }
-        for (int i = 0; i < kMaxStagesB; ++i) {
-            mbar_init(smem_u32(&sh.full_b[i]), 1);
-            mbar_init(smem_u32(&sh.empty_b[i]), 1);
-        }
-        for (int i = 0; i < 2; ++i) {
-            mbar_init(smem_u32(&sh.full_d[i]), 1);
-            mbar_init(smem_u32(&sh.empty_d[i]), 128);
-        }
+    if (tid < kMaxStagesA) {
+        mbar_init(smem_u32(&sh.full_a[tid]), 1);
+        mbar_init(smem_u32(&sh.empty_a[tid]), 1);
+    } else if (tid >= 64 && tid < 64 + kMaxStagesB) {
+        mbar_init(smem_u32(&sh.full_b[tid - 64]), 1);
+        mbar_init(smem_u32(&sh.empty_b[tid - 64]), 1);
+    } else if (tid >= 96 && tid < 98) {
+        mbar_init(smem_u32(&sh.full_d[tid - 96]), 1);
+        mbar_init(smem_u32(&sh.empty_d[tid - 96]), 128);
+    } else if (tid == 128) {
         mbar_init(smem_u32(&sh.drain), 1);
-        mbar_init_fence();
+        sh.abort = sh.reset = sh.rests[0].n = sh.rests[1].n = sh.issued_a = sh.issued_b = 0;
+    } else if (tid == 160) {
         tma_prefetch_map(&a.mx);
         tma_prefetch_map(&a.mw1);
         tma_prefetch_map(&a.mw2);
         tma_prefetch_map(&a.mh);
     }
+    mbar_init_fence();
     if (warp == 1)
         tmem_alloc(smem_u32(&sh.tmem), kTmemCols);
     build_lists(a, li, sh, tid, kThreads, kMaxTokens);
@@ -227,12 +225,11 @@ __global__ void __launch_bounds__(kThreads, 1) experts_kernel(const __grid_const
         Cursor at_d;
         bool run = true;
 
-        auto leave = [&](Rests &rests, int i, int m, const Split &sp, int *counter) {
-            if (row == 0)
-                rests.of[rests.n++] = Rest{i, m, sp};
+        // Rests: counted once the product's last run is written.
+        auto arrive = [&](const Rests &rests, int *counters, bool second) {
             named_sync(1, 128);
-            if (row == 0)
-                add_acq_rel(counter, 1);
+            if (row < rests.n)
+                add_acq_rel(counters + (second ? rests.of[row].m : rests.of[row].i * a.mt1 + rests.of[row].m), 1);
         };
         auto parts_written = [&](int *counter, const Split &sp) {
             return named_all(2, 128, row != 0 || wait_count(counter, sp.parts(), abort, kWaitOther));
@@ -244,6 +241,10 @@ __global__ void __launch_bounds__(kThreads, 1) experts_kernel(const __grid_const
             if (row == 0)
                 add_acq_rel(a.done, columns);
         };
+        // A run's part: the block's second slot unless it is the first run of its share.
+        auto part_of = [&](bool first) {
+            return a.part + static_cast<size_t>(2 * blk + (first ? 0 : 1)) * a.part_floats + row;
+        };
         auto store_h = [&](int off, int j, int col, float gate, float up) {
             __nv_bfloat16 hi, lo;
             split(swiglu(gate, up), hi, lo);
@@ -251,12 +252,12 @@ __global__ void __launch_bounds__(kThreads, 1) experts_kernel(const __grid_const
             a.h[static_cast<size_t>(a.P + off + j) * a.h_stride + col] = lo;
         };
 
+        int announced = 0;  // columns of h that are written and not yet announced
         for (Walk w(begin1, end1, a.kc1, a.mt1, false); run && w.more(); w.next()) {
-            const int tile = w.i * a.mt1 + w.m;
             const int off = li.offset[w.i], n = li.count(w.i), N = ceil_div(n, 16) * 16, n8 = (n + 7) & ~7;
             const int col = w.m * kTileRows + row;  // of h
-            const Split sp(shares1, tile * a.kc1, a.kc1);
-            float *const part = a.part + static_cast<size_t>(sp.slot(blk)) * a.part_floats + row;
+            const bool shared = w.k != 0 || w.len != a.kc1;
+            float *const part = part_of(w.left == end1 - begin1);
             run = mbar_wait(smem_u32(&sh.full_d[at_d.s]), at_d.parity, abort, kWaitFullD);
             run = named_all(2, 128, run);  // the four warps leave together, or not at all
             if (!run)
@@ -272,7 +273,7 @@ __global__ void __launch_bounds__(kThreads, 1) experts_kernel(const __grid_const
                 for (int c = 0; c < 8; ++c) {
                     if (j + c >= n)
                         break;
-                    if (sp.shared()) {
+                    if (shared) {
                         part[(j + c) * kTileRows] = g[c];
                         part[(n + j + c) * kTileRows] = v[c];
                     } else if (col < a.I) {
@@ -283,15 +284,16 @@ __global__ void __launch_bounds__(kThreads, 1) experts_kernel(const __grid_const
             tc_fence_before();
             mbar_arrive(smem_u32(&sh.empty_d[at_d.s]));
             at_d.next(2);
-            if (sp.shared())
-                leave(sh.rests[0], w.i, w.m, sp, a.tiles + tile);
-            else
-                announce(n);
+            if (!shared)
+                announced += n;
+            else if (row == 0)
+                sh.rests[0].of[sh.rests[0].n++] = Rest{w.i, w.m};
         }
+        if (run)
+            arrive(sh.rests[0], a.tiles, false);
         for (int r = 0; run && r < sh.rests[0].n; ++r) {
-            const Rest &rest = sh.rests[0].of[r];
-            const int i = rest.i, m = rest.m, off = li.offset[i], n = li.count(i);
-            const Split sp = rest.sp;
+            const int i = sh.rests[0].of[r].i, m = sh.rests[0].of[r].m, off = li.offset[i], n = li.count(i);
+            const Split sp(shares1, (i * a.mt1 + m) * a.kc1, a.kc1);
             const int lo = sp.column(n, blk), hi = sp.column(n, blk + 1), col = m * kTileRows + row;
             if (lo == hi)
                 continue;
@@ -307,8 +309,10 @@ __global__ void __launch_bounds__(kThreads, 1) experts_kernel(const __grid_const
                     if (j + c < hi && col < a.I)
                         store_h(off, j + c, col, g[c], v[c]);
             }
-            announce(hi - lo);
+            announced += hi - lo;
         }
+        if (run && announced > 0)
+            announce(announced);
 
         const int group = A * a.kc2;  // units of one row tile of y, over all experts
         auto store_y = [&](int m, int t, float v) {
@@ -319,7 +323,6 @@ __global__ void __launch_bounds__(kThreads, 1) experts_kernel(const __grid_const
         };
         for (Walk w(begin2, end2, a.kc2, A, true); run && w.more();) {
             const Walk first = w;
-            const Split sp(shares2, first.m * group, group);
             for (int t = 0; t < a.T; ++t)
                 acc[t * kTileRows + row] = 0.0f;
             for (; run && w.more() && w.m == first.m; w.next()) {
@@ -348,20 +351,24 @@ __global__ void __launch_bounds__(kThreads, 1) experts_kernel(const __grid_const
             }
             if (!run)
                 break;
-            if (sp.shared()) {
-                float *const part = a.part + static_cast<size_t>(sp.slot(blk)) * a.part_floats + row;
+            // an earlier block began this row tile, or a later one ends it
+            if (first.i != 0 || first.k != 0 || (!w.more() && end2 != (first.m + 1) * group)) {
+                float *const part = part_of(first.left == end2 - begin2);
                 for (int t = 0; t < a.T; ++t)
                     part[t * kTileRows] = acc[t * kTileRows + row];
-                leave(sh.rests[1], first.i, first.m, sp, a.tiles + a.E * a.mt1 + first.m);
+                if (row == 0)
+                    sh.rests[1].of[sh.rests[1].n++] = Rest{first.i, first.m};
             } else {
                 for (int t = 0; t < a.T; ++t)
                     store_y(first.m, t, acc[t * kTileRows + row]);
             }
         }
+        if (run)
+            arrive(sh.rests[1], a.tiles + a.E * a.mt1, true);
         for (int r = 0; run && r < sh.rests[1].n; ++r) {
-            const Rest &rest = sh.rests[1].of[r];
-            const Split sp = rest.sp;
-            const int m = rest.m, lo = sp.column(a.T, blk), hi = sp.column(a.T, blk + 1);
+            const int m = sh.rests[1].of[r].m;
+            const Split sp(shares2, m * group, group);
+            const int lo = sp.column(a.T, blk), hi = sp.column(a.T, blk + 1);
             if (lo == hi)
                 continue;
             run = parts_written(a.tiles + a.E * a.mt1 + m, sp);

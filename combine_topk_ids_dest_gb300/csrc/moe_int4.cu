@@ -37,9 +37,11 @@ namespace moe {
 
 namespace {
 
-constexpr int kGroups = 4;                 // groups of four warps
+constexpr int kGroups = 4;                 // groups of four warps that multiply
 constexpr int kWorkers = kGroups * 128;
-constexpr int kThreads = kWorkers + 64;    // the last two warps bring weights and tokens
+// then a warpgroup for results and one of which two warps bring weights and tokens
+constexpr int kResults = 128;
+constexpr int kThreads = kWorkers + kResults + 128;
 constexpr int kMaxStagesA = 12;
 constexpr int kMaxStagesB = 16;
 constexpr int kCap = 32;                   // tokens of an entry: 4 column blocks of 8
@@ -48,6 +50,7 @@ constexpr int kSumStride = kTileRows + 4;  // column stride of the groups' sums:
 struct Shared {
     uint64_t full_a[kMaxStagesA], empty_a[kMaxStagesA];
     uint64_t full_b[kMaxStagesB], empty_b[kMaxStagesB];
+    uint64_t full_s, empty_s;  // the groups' sums of a run
     int abort;
     int active, nmax;
     int issued_a, issued_b;
@@ -80,6 +83,9 @@ static __device__ __forceinline__ void add_tile(float (&acc)[NT][2][4], const ui
                                                 const uint8_t *tokens, bool with_zeros, bool scale_fp16)
 {
     constexpr int kQ = 1 << SHIFT;  // 32-input steps of a group
+    // From three column blocks on, a group's sum is scaled in steps of 32 inputs: it then needs registers for one
+    // block at a time, and the MMAs take longer than the scaling.
+    constexpr bool kSteps = NT >= 3 || kQ == 1;
     const uint4 *const codes = reinterpret_cast<const uint4 *>(tile + rows32 * 2048) + lane;
     const int row = rows32 * 32 + (lane >> 2);
     const uint16_t *const scales = reinterpret_cast<const uint16_t *>(tile + 8192) + row;
@@ -87,7 +93,7 @@ static __device__ __forceinline__ void add_tile(float (&acc)[NT][2][4], const ui
     const uint4 *const tok = reinterpret_cast<const uint4 *>(tokens) + lane;
     constexpr uint32_t one = BF16 ? 0x43004300u : 0x64006400u;
     uint32_t z[4] = {one + 0x00080008u, one + 0x00080008u, one + 0x00080008u, one + 0x00080008u};
-    float c[NT][2][4];
+    float s[4], c[kSteps ? 1 : NT][2][4];
     uint4 w = codes[0];
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
@@ -95,6 +101,14 @@ static __device__ __forceinline__ void add_tile(float (&acc)[NT][2][4], const ui
 #pragma unroll
             for (int h = 0; h < 4; ++h)  // rows r, r + 8, r + 16, r + 24
                 z[h] = one + zeros[(q >> SHIFT) * 128 + h * 8] * 0x00010001u;
+        }
+        if (kSteps ? q % kQ == 0 : q % kQ == kQ - 1) {
+#pragma unroll
+            for (int h = 0; h < 4; ++h) {
+                const uint32_t raw = scales[(q >> SHIFT) * 128 + h * 8];
+                s[h] = scale_fp16 ? __half2float(__ushort_as_half(static_cast<unsigned short>(raw)))
+                                  : __uint_as_float(raw << 16);
+            }
         }
         uint32_t f[4][4];  // [2 * sixteen inputs + 16-row half]
         decode<BF16>(w.x, z[0], z[1], f[0]);
@@ -104,35 +118,28 @@ static __device__ __forceinline__ void add_tile(float (&acc)[NT][2][4], const ui
         if (q < 3)
             w = codes[(q + 1) * 32];
 #pragma unroll
-        for (int p = 0; p < PLANES; ++p)
+        for (int nt = 0; nt < NT; ++nt) {
+            float(&d)[2][4] = c[kSteps ? 0 : nt];
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
+            for (int p = 0; p < PLANES; ++p) {
                 const uint4 b = tok[((p * 4 + q) * NT + nt) * 32];
-                if (q % kQ == 0 && p == 0) {
-                    mma_16816<BF16, false>(c[nt][0], f[0], b.x, b.y);
-                    mma_16816<BF16, false>(c[nt][1], f[1], b.x, b.y);
+                if (p == 0 && (kSteps || q % kQ == 0)) {
+                    mma_16816<BF16, false>(d[0], f[0], b.x, b.y);
+                    mma_16816<BF16, false>(d[1], f[1], b.x, b.y);
                 } else {
-                    mma_16816<BF16, true>(c[nt][0], f[0], b.x, b.y);
-                    mma_16816<BF16, true>(c[nt][1], f[1], b.x, b.y);
+                    mma_16816<BF16, true>(d[0], f[0], b.x, b.y);
+                    mma_16816<BF16, true>(d[1], f[1], b.x, b.y);
                 }
-                mma_16816<BF16, true>(c[nt][0], f[2], b.z, b.w);
-                mma_16816<BF16, true>(c[nt][1], f[3], b.z, b.w);
+                mma_16816<BF16, true>(d[0], f[2], b.z, b.w);
+                mma_16816<BF16, true>(d[1], f[3], b.z, b.w);
             }
-        if (q % kQ == kQ - 1) {  // the group's end
-            float s[4];
-#pragma unroll
-            for (int h = 0; h < 4; ++h) {
-                const uint32_t raw = scales[(q >> SHIFT) * 128 + h * 8];
-                s[h] = scale_fp16 ? __half2float(__ushort_as_half(static_cast<unsigned short>(raw)))
-                                  : __uint_as_float(raw << 16);
-            }
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
+            if (kSteps || q % kQ == kQ - 1) {
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
                     float &y = acc[nt][i >> 2][i & 3];
-                    y = fmaf(s[(i >> 2) * 2 + ((i >> 1) & 1)], c[nt][i >> 2][i & 3], y);
+                    y = fmaf(s[(i >> 2) * 2 + ((i >> 1) & 1)], d[i >> 2][i & 3], y);
                 }
+            }
         }
     }
 }
@@ -142,34 +149,30 @@ __global__ void __launch_bounds__(kThreads, 1) int4_kernel(const __grid_constant
 {
     extern __shared__ uint8_t dyn[];
     __shared__ Shared sh;
-    const uint32_t dyn0 = smem_u32(dyn);
-    const uint32_t ring_b = (dyn0 + 127u) & ~127u;
-    const uint32_t ring_a = ring_b + a.bytes_b;
-    const uint32_t after = ring_a + a.stages * a.stage_a;
-    const uint8_t *const ring_b_p = dyn + (ring_b - dyn0), *const ring_a_p = dyn + (ring_a - dyn0);
-    float *const sums = reinterpret_cast<float *>(dyn + (after - dyn0));  // [2][column][kSumStride]
-    float *const acc_y = sums + 2 * a.cols * kSumStride;            // [T][128], of the second product
+    const uint32_t dyn0 = smem_u32(dyn), base = (dyn0 + 127u) & ~127u;
+    // dynamic shared memory: y's accumulators, lists, the groups' sums, the rings
+    float *const acc_y = reinterpret_cast<float *>(dyn + (base - dyn0));  // [T][128], of the second product
     const Lists li(acc_y + (LINEAR ? 0 : a.T * kTileRows), a.E, a.P);
 
     const int tid = threadIdx.x, warp = __shfl_sync(~0u, tid >> 5, 0), lane = tid & 31;
     const int G = gridDim.x, blk = blockIdx.x;
     volatile int *const abort = &sh.abort;
 
-    if (tid == 0) {
+    if (tid < kMaxStagesA) {
+        mbar_init(smem_u32(&sh.full_a[tid]), 1);
+        mbar_init(smem_u32(&sh.empty_a[tid]), 8);
+    } else if (tid >= 32 && tid < 32 + kMaxStagesB) {
+        mbar_init(smem_u32(&sh.full_b[tid - 32]), 1);
+        mbar_init(smem_u32(&sh.empty_b[tid - 32]), 8);
+    } else if (tid == 64) {
+        mbar_init(smem_u32(&sh.full_s), kWorkers / 32);
+        mbar_init(smem_u32(&sh.empty_s), kResults / 32);
         sh.abort = sh.reset = sh.rests[0].n = sh.rests[1].n = sh.issued_a = sh.issued_b = 0;
-        for (int i = 0; i < kMaxStagesA; ++i) {
-            mbar_init(smem_u32(&sh.full_a[i]), 1);
-            mbar_init(smem_u32(&sh.empty_a[i]), 8);
-        }
-        for (int i = 0; i < kMaxStagesB; ++i) {
-            mbar_init(smem_u32(&sh.full_b[i]), 1);
-            mbar_init(smem_u32(&sh.empty_b[i]), 8);
-        }
-        mbar_init_fence();
         tma_prefetch_map(&a.mx);
     }
+    mbar_init_fence();
     if (LINEAR) {  // one "expert" whose tokens are the rows of x
-        if (tid == 0) {
+        if (tid == 96) {
             const int rows = a.box_bytes / 512, half = min(a.T, rows);  // int4_linear_rows
             sh.active = a.T > rows ? 2 : 1;
             sh.nmax = rows;
@@ -197,14 +200,23 @@ __global__ void __launch_bounds__(kThreads, 1) int4_kernel(const __grid_constant
     const int begin2 = LINEAR ? 0 : shares2.begin(blk), end2 = LINEAR ? 0 : shares2.begin(blk + 1);
     const int pairs = li.offset[A];
     // A unit's token tile, in 8-token steps of 2 KB a chunk: two chunks, or one, and later two in two parts.
-    const int stage_b = ceil_div(sh.nmax, 8) * (LINEAR ? 4096 : 8192);
+    const int cols = (sh.nmax + 7) & ~7, stage_b = cols * (LINEAR ? 512 : 1024);
     // With up to 8 tokens every expert's token tile is all of x: a sum's column is the token. Else the tokens are gathered.
     const bool whole = LINEAR || a.T <= 8;
-    const int stages_b = min(kMaxStagesB, a.bytes_b / stage_b);
+    // the groups' sums take what this launch's largest entry needs, the rings the rest: an eighth to a
+    // half for tokens
+    const uint32_t sums_at = (base + a.fixed_bytes + 127u) & ~127u;
+    float *const sums = reinterpret_cast<float *>(dyn + (sums_at - dyn0));  // [group][column][kSumStride]
+    const uint32_t ring_b = sums_at + kGroups * cols * kSumStride * 4;
+    const int room = a.smem - static_cast<int>(ring_b - dyn0);
+    const int stages_b = max(2, min(kMaxStagesB, room / 4 / stage_b));
+    const uint32_t ring_a = ring_b + stages_b * stage_b;
+    const int stages = min(kMaxStagesA, (room - stages_b * stage_b) / a.stage_a);
+    const uint8_t *const ring_b_p = dyn + (ring_b - dyn0), *const ring_a_p = dyn + (ring_a - dyn0);
     // h: per entry and chunk a tile [2 parts][4][tokens][32], tokens a multiple of 8
     const auto h_entry = [&](int i) { return a.h + static_cast<size_t>(li.offset[i] + 7 * i) * a.h_stride; };
 
-    if (warp == kWorkers / 32 && elect_one()) {
+    if (warp == (kWorkers + kResults) / 32 && elect_one()) {
         // ---- weight tiles ----
         const uint64_t policy = policy_evict_first();
         Cursor at;
@@ -216,7 +228,7 @@ __global__ void __launch_bounds__(kThreads, 1) int4_kernel(const __grid_constant
             const uint32_t bar = smem_u32(&sh.full_a[at.s]);
             mbar_expect(bar, bytes);
             bulk_load(ring_a + at.s * a.stage_a, src, bytes, bar, policy);
-            at.next(a.stages);
+            at.next(stages);
             ++issued;
             return true;
         };
@@ -233,7 +245,7 @@ __global__ void __launch_bounds__(kThreads, 1) int4_kernel(const __grid_constant
                 run = load(src, 2 * k + 1 < a.kc2 ? 2 * a.tile2 : a.tile2);
         }
         sh.issued_a = issued;
-    } else if (warp == kWorkers / 32 + 1 && elect_one()) {
+    } else if (warp == (kWorkers + kResults) / 32 + 1 && elect_one()) {
         // ---- token tiles ----
         Cursor at;
         int issued = 0;
@@ -284,7 +296,8 @@ __global__ void __launch_bounds__(kThreads, 1) int4_kernel(const __grid_constant
         sh.issued_b = issued;
     } else if (warp < kWorkers / 32) {
         // ---- products ----
-        const int grp = warp >> 2, rows32 = warp & 3, row = tid & 127;
+        const int grp = warp >> 2, rows32 = warp & 3;
+        uint32_t run_parity = 1;  // of empty_s
         const int tile = grp & 1;  // of a unit
         Cursor at_a, at_b;         // of this group's next unit
         int turn = grp >> 1;       // units until then
@@ -320,28 +333,24 @@ __global__ void __launch_bounds__(kThreads, 1) int4_kernel(const __grid_constant
                         ring_b_p + at_b.s * stage_b + chunk_b, with_zeros, scale_fp16);
                 __syncwarp();
                 mbar_arrive2_if(lane == 0, fa + empty_a, fb + empty_b);
-                at_a.advance(2, a.stages);  // the group's next unit
+                at_a.advance(2, stages);  // the group's next unit
                 at_b.advance(2, stages_b);
             }
             turn -= units;
-            named_sync(1, kWorkers);  // the sums of the run before are read
-            float *const mine = sums + ((grp & 1) * a.cols + (lane & 3) * 2) * kSumStride + rows32 * 32 + (lane >> 2);
-            if (grp >= 2) {
+            // the sums of the run before have been read
+            run = run && mbar_wait_warp(smem_u32(&sh.empty_s), run_parity, abort, kWaitEmptyD);
+            run_parity ^= 1;
+            if (!run)
+                return;
+            float *const mine = sums + (grp * cols + (lane & 3) * 2) * kSumStride + rows32 * 32 + (lane >> 2);
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
+            for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                    for (int i = 0; i < 8; ++i)
-                        mine[(nt * 8 + (i & 1)) * kSumStride + (i >> 1) * 8] = acc[nt][i >> 2][i & 3];
-            }
-            named_sync(1, kWorkers);
-            if (grp < 2) {
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                    for (int i = 0; i < 8; ++i)
-                        mine[(nt * 8 + (i & 1)) * kSumStride + (i >> 1) * 8] += acc[nt][i >> 2][i & 3];
-            }
-            run = named_all(2, kWorkers, run);
+                for (int i = 0; i < 8; ++i)
+                    mine[(nt * 8 + (i & 1)) * kSumStride + (i >> 1) * 8] = acc[nt][i >> 2][i & 3];
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive(smem_u32(&sh.full_s));
         };
         auto by_group = [&](auto blocks, auto second, int units, int k, int kc) {
             const int shift = decltype(second)::value ? a.shift2 : a.shift1;
@@ -362,29 +371,51 @@ __global__ void __launch_bounds__(kThreads, 1) int4_kernel(const __grid_constant
             else
                 by_group(std::integral_constant<int, 4>{}, second, units, k, kc);
         };
-        // Column j of the sums, this thread's row: of the even (0) or odd (1) groups, or all.
-        auto sum_half = [&](int j, int odd) { return sums[(odd * a.cols + j) * kSumStride + row]; };
-        auto sum_all = [&](int j) { return sum_half(j, 0) + sum_half(j, 1); };
+        for (Walk w(begin1, end1, ku1, a.mt1, false); run && w.more(); w.next())
+            run_products(std::false_type{}, LINEAR ? sh.nmax : li.count(w.i), w.len, w.k, a.kc1);
+        for (Walk w(begin2, end2, ku2, A, true); !LINEAR && run && w.more(); w.next())
+            run_products(std::true_type{}, li.count(w.i), w.len, w.k, a.kc2);
+    } else if (warp < (kWorkers + kResults) / 32) {
+        // ---- results: a thread has rows rtid and rtid + 64 of a tile ----
+        const int rtid = tid - kWorkers;
+        uint32_t parity = 0;  // of full_s
+        bool run = true;
+        // Waits for a run's sums. The two warps leave together, or not at all.
+        auto sums_ready = [&] {
+            const bool ok = named_all(2, kResults, mbar_wait(smem_u32(&sh.full_s), parity, abort, kWaitFullD));
+            parity ^= 1;
+            return ok;
+        };
+        auto sums_read = [&] {
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive(smem_u32(&sh.empty_s));
+        };
+        // Column j of the sums of a row: of the even (0) or odd (1) groups, or all.
+        auto sum_half = [&](int j, int row, int odd) {
+            const float *const s = sums + (odd * cols + j) * kSumStride + row;
+            return s[0] + s[2 * cols * kSumStride];
+        };
+        auto sum_all = [&](int j, int row) { return sum_half(j, row, 0) + sum_half(j, row, 1); };
 
         // As in moe_experts.cu: tiles shared with other blocks are settled after a product's last run.
-        auto leave = [&](Rests &rests, int i, int m, const Split &sp, int *counter) {
-            if (tid == 0)
-                rests.of[rests.n++] = Rest{i, m, sp};
-            named_sync(1, kWorkers);
-            if (tid == 0)
-                add_acq_rel(counter, 1);
+        auto arrive = [&](const Rests &rests, int *counters, bool second) {
+            named_sync(1, kResults);
+            if (rtid < rests.n)
+                add_acq_rel(counters + (second ? rests.of[rtid].m : rests.of[rtid].i * a.mt1 + rests.of[rtid].m), 1);
         };
         auto parts_written = [&](int *counter, const Split &sp) {
-            return named_all(2, kWorkers, tid != 0 || wait_count(counter, sp.parts(), abort, kWaitOther));
+            return named_all(2, kResults, rtid != 0 || wait_count(counter, sp.parts(), abort, kWaitOther));
         };
+        // h of these columns of a tile goes out to the copies of every block.
         auto announce = [&](int columns) {
             fence_async_proxy();
-            named_sync(1, kWorkers);
-            if (tid == 0)
+            named_sync(1, kResults);
+            if (rtid == 0)
                 add_acq_rel(a.done, columns);
         };
-        // column j of row tile m: h, or y of the linear layer
-        auto result = [&](int i, int m, int j, float gate, float up) {
+        // column j of a row of row tile m: h, or y of the linear layer
+        auto result = [&](int i, int m, int j, int row, float gate, float up) {
             const int col = m * kTileRows + row;
             if (LINEAR) {
                 uint16_t *const p = static_cast<uint16_t *>(a.out) + (li.offset[i] + j) * a.out_stride + col;
@@ -398,55 +429,64 @@ __global__ void __launch_bounds__(kThreads, 1) int4_kernel(const __grid_constant
                 split(swiglu(gate, up), p[0], p[n8 * 128]);
             }
         };
-        const int set = tid >> 7;  // of columns
+        // A run's part: the block's second slot unless it is the first run of its share.
+        auto part_of = [&](bool first) {
+            return a.part + static_cast<size_t>(2 * blk + (first ? 0 : 1)) * a.part_floats;
+        };
 
-        for (Walk w(begin1, end1, ku1, a.mt1, false); run && w.more(); w.next()) {
-            const int n = li.count(w.i), row_tile = w.i * a.mt1 + w.m;
+        int announced = 0;  // columns of h that are written and not yet announced
+        for (Walk w(begin1, end1, ku1, a.mt1, false); w.more(); w.next()) {
+            const int n = li.count(w.i);
             const unsigned char *const tok = li.token + li.offset[w.i];
-            const Split sp(shares1, row_tile * ku1, ku1);
-            run_products(std::false_type{}, LINEAR ? sh.nmax : n, w.len, w.k, a.kc1);
+            const bool shared = w.k != 0 || w.len != ku1, first = w.left == end1 - begin1;
+            run = sums_ready();
             if (!run)
                 break;
-            float *const part = a.part + static_cast<size_t>(sp.slot(blk)) * a.part_floats + row;
-            for (int j = set; j < n; j += kGroups) {
+            float *const part = part_of(first);
+            for (int j = 0; j < n; ++j) {
                 const int c = !LINEAR && whole ? tok[j] : j;  // the sum's column
-                const float g = LINEAR ? sum_all(c) : sum_half(c, 0), u = LINEAR ? 0.0f : sum_half(c, 1);
-                if (sp.shared()) {
-                    part[j * kTileRows] = g;
-                    if (!LINEAR)
-                        part[(n + j) * kTileRows] = u;
-                } else {
-                    result(w.i, w.m, j, g, u);
+                for (int row = rtid; row < kTileRows; row += kResults) {
+                    const float g = LINEAR ? sum_all(c, row) : sum_half(c, row, 0);
+                    const float u = LINEAR ? 0.0f : sum_half(c, row, 1);
+                    if (shared) {
+                        part[j * kTileRows + row] = g;
+                        if (!LINEAR)
+                            part[(n + j) * kTileRows + row] = u;
+                    } else {
+                        result(w.i, w.m, j, row, g, u);
+                    }
                 }
             }
-            if (sp.shared())
-                leave(sh.rests[0], w.i, w.m, sp, a.tiles + row_tile);
-            else if (!LINEAR)
-                announce(n);
+            sums_read();
+            if (!shared)
+                announced += n;
+            else if (rtid == 0)
+                sh.rests[0].of[sh.rests[0].n++] = Rest{w.i, w.m};
         }
-        for (int r = 0; run && r < sh.rests[0].n; ++r) {
-            const Rest &rest = sh.rests[0].of[r];
-            const int i = rest.i, m = rest.m, n = li.count(i);
-            const Split sp = rest.sp;
-            const int lo = sp.column(n, blk), hi = sp.column(n, blk + 1);
-            if (lo == hi)
-                continue;
-            run = parts_written(a.tiles + i * a.mt1 + m, sp);
-            if (!run)
-                break;
-            for (int j = lo + set; j < hi; j += kGroups) {
-                float g[1], u[1] = {};
-                sum_parts<1>(a.part + j * kTileRows + row, a.part_floats, sp, 1, g);
-                if (!LINEAR)
-                    sum_parts<1>(a.part + (n + j) * kTileRows + row, a.part_floats, sp, 1, u);
-                result(i, m, j, g[0], u[0]);
+        if (run) {
+            arrive(sh.rests[0], a.tiles, false);
+            for (int r = 0; run && r < sh.rests[0].n; ++r) {
+                const int i = sh.rests[0].of[r].i, m = sh.rests[0].of[r].m, n = li.count(i);
+                const Split sp(shares1, (i * a.mt1 + m) * ku1, ku1);
+                const int lo = sp.column(n, blk), hi = sp.column(n, blk + 1);
+                if (lo == hi)
+                    continue;
+                run = parts_written(a.tiles + i * a.mt1 + m, sp);
+                for (int j = lo; run && j < hi; ++j) {
+                    float g[1], u[1] = {};
+                    sum_parts<1>(a.part + j * kTileRows + rtid, a.part_floats, sp, 1, g);
+                    if (!LINEAR)
+                        sum_parts<1>(a.part + (n + j) * kTileRows + rtid, a.part_floats, sp, 1, u);
+                    result(i, m, j, rtid, g[0], u[0]);
+                }
+                announced += hi - lo;
             }
-            if (!LINEAR)
-                announce(hi - lo);
+            if (!LINEAR && run && announced > 0)
+                announce(announced);
         }
 
         const int group = LINEAR ? 1 : A * ku2;
-        auto store_y = [&](int m, int t, float r) {
+        auto store_y = [&](int m, int t, int row, float r) {
             const int col = m * kTileRows + row;
             __nv_bfloat16 *const p = static_cast<__nv_bfloat16 *>(a.out) + t * a.out_stride + col;
             if (col < a.H && EP_IN_BOUNDS(a.chk, epk::kSiteMoeOut, p, 2, a.out, 2 * ((a.T - 1) * a.out_stride + a.H)))
@@ -454,44 +494,53 @@ __global__ void __launch_bounds__(kThreads, 1) int4_kernel(const __grid_constant
         };
         for (Walk w(begin2, end2, ku2, A, true); !LINEAR && run && w.more();) {
             const int m = w.m, i0 = w.i;
-            const Split sp(shares2, m * group, group);
-            for (int t = set; t < a.T; t += kGroups)
-                acc_y[t * kTileRows + row] = 0.0f;
-            for (; run && w.more() && w.m == m; w.next()) {
+            const bool first = w.left == end2 - begin2;
+            bool shared = w.i != 0 || w.k != 0;  // an earlier block began this row tile
+            for (int t = rtid; t < a.T * kTileRows; t += kResults)  // a thread's own rows: no barrier
+                acc_y[t] = 0.0f;
+            for (; w.more() && w.m == m; w.next()) {
                 const int off = li.offset[w.i], n = li.count(w.i);
-                run_products(std::true_type{}, n, w.len, w.k, a.kc2);  // its barriers also order the threads' turns at a row of acc_y
-                for (int j = set; run && j < n; j += kGroups) {
-                    float *const s = acc_y + li.token[off + j] * kTileRows + row;
-                    *s = fmaf(li.weight[off + j], sum_all(j), *s);
+                run = sums_ready();
+                if (!run)
+                    break;
+                for (int j = 0; j < n; ++j) {
+                    float *const y = acc_y + li.token[off + j] * kTileRows;
+                    const float weight = li.weight[off + j];
+                    for (int row = rtid; row < kTileRows; row += kResults)
+                        y[row] = fmaf(weight, sum_all(j, row), y[row]);
                 }
+                sums_read();
             }
-            run = named_all(2, kWorkers, run);
             if (!run)
                 break;
-            if (sp.shared()) {
-                float *const part = a.part + static_cast<size_t>(sp.slot(blk)) * a.part_floats + row;
-                for (int t = set; t < a.T; t += kGroups)
-                    part[t * kTileRows] = acc_y[t * kTileRows + row];
-                leave(sh.rests[1], i0, m, sp, a.tiles + 2 * a.E * a.mt1 + m);
+            shared = shared || (!w.more() && end2 != (m + 1) * group);  // a later block ends it
+            if (shared) {
+                float *const part = part_of(first);
+                for (int t = rtid; t < a.T * kTileRows; t += kResults)
+                    part[t] = acc_y[t];
+                if (rtid == 0)
+                    sh.rests[1].of[sh.rests[1].n++] = Rest{i0, m};
             } else {
-                for (int t = set; t < a.T; t += kGroups)
-                    store_y(m, t, acc_y[t * kTileRows + row]);
+                for (int t = 0; t < a.T; ++t)
+                    for (int row = rtid; row < kTileRows; row += kResults)
+                        store_y(m, t, row, acc_y[t * kTileRows + row]);
             }
-            // a thread clears and reads the same tokens of acc_y: no barrier until the next products
         }
-        for (int r = 0; !LINEAR && run && r < sh.rests[1].n; ++r) {
-            const Rest &rest = sh.rests[1].of[r];
-            const Split sp = rest.sp;
-            const int m = rest.m, lo = sp.column(a.T, blk), hi = sp.column(a.T, blk + 1);
-            if (lo == hi)
-                continue;
-            run = parts_written(a.tiles + 2 * a.E * a.mt1 + m, sp);
-            if (!run)
-                break;
-            for (int t = lo + set; t < hi; t += kGroups) {
-                float x[1];
-                sum_parts<1>(a.part + t * kTileRows + row, a.part_floats, sp, 1, x);
-                store_y(m, t, x[0]);
+        if (!LINEAR && run) {
+            int *const counters = a.tiles + 2 * a.E * a.mt1;
+            arrive(sh.rests[1], counters, true);
+            for (int r = 0; run && r < sh.rests[1].n; ++r) {
+                const int m = sh.rests[1].of[r].m;
+                const Split sp(shares2, m * group, group);
+                const int lo = sp.column(a.T, blk), hi = sp.column(a.T, blk + 1);
+                if (lo == hi)
+                    continue;
+                run = parts_written(counters + m, sp);
+                for (int t = lo; run && t < hi; ++t) {
+                    float x[1];
+                    sum_parts<1>(a.part + t * kTileRows + rtid, a.part_floats, sp, 1, x);
+                    store_y(m, t, rtid, x[0]);
+                }
             }
         }
     }
@@ -500,8 +549,8 @@ __global__ void __launch_bounds__(kThreads, 1) int4_kernel(const __grid_constant
 
     if (sh.abort) {  // copies in flight land before the block's memory is given back
         if (tid == 0) {
-            for (int i = max(0, sh.issued_a - a.stages); i < sh.issued_a; ++i)
-                mbar_wait(smem_u32(&sh.full_a[i % a.stages]), (i / a.stages) & 1, nullptr, kWaitOther);
+            for (int i = max(0, sh.issued_a - stages); i < sh.issued_a; ++i)
+                mbar_wait(smem_u32(&sh.full_a[i % stages]), (i / stages) & 1, nullptr, kWaitOther);
             for (int i = max(0, sh.issued_b - stages_b); i < sh.issued_b; ++i)
                 mbar_wait(smem_u32(&sh.full_b[i % stages_b]), (i / stages_b) & 1, nullptr, kWaitOther);
             atomicAdd_system(a.err + sh.abort, 1u);
@@ -598,22 +647,13 @@ int int4_linear_rows(int T)
 
 size_t int4_smem(Int4Args *a, bool linear)
 {
-    a->cols = ((a->T < kCap ? a->T : kCap) + 7) & ~7;
-    const size_t lists = (linear ? 0 : static_cast<size_t>(a->T) * kTileRows * 4) +
-                         static_cast<size_t>(2) * a->cols * kSumStride * 4 + lists_bytes(a->E, a->P);
-    // the largest token tile: 8 KB for 8 tokens (4 for the linear layer); at least 2 stages, a group's next is two on
-    a->bytes_b = (linear || a->cols <= 16 ? 4 : 2) * a->cols * (linear ? 512 : 1024);
-    if (a->bytes_b < 32 * 1024)
-        a->bytes_b = 32 * 1024;
+    a->fixed_bytes = (linear ? 0 : a->T * kTileRows * 4) + static_cast<int>(lists_bytes(a->E, a->P));
     a->shift1 = a->group1 == 32 ? 0 : a->group1 == 64 ? 1 : 2;
     a->shift2 = a->group2 == 32 ? 0 : a->group2 == 64 ? 1 : 2;
     a->stage_a = 2 * (a->tile1 > a->tile2 ? a->tile1 : a->tile2);
     a->part_floats = static_cast<int>(int4_part_floats(a->T, linear));
-    const size_t room = kSmemMax - sizeof(Shared) - 128 - lists - a->bytes_b - 64;
-    a->stages = static_cast<int>(room / a->stage_a);
-    if (a->stages > kMaxStagesA)
-        a->stages = kMaxStagesA;
-    return 128 + static_cast<size_t>(a->stages) * a->stage_a + a->bytes_b + lists;
+    a->smem = (kSmemMax - static_cast<int>(sizeof(Shared)) - 64) & ~127;  // all of it: the rings take the rest
+    return a->smem;
 }
 
 cudaError_t launch_int4(const Int4Args &a, bool linear, bool bf16, int grid, size_t smem, cudaStream_t stream)

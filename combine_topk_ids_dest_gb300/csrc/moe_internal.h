@@ -107,7 +107,7 @@ struct Int4Args {
     int group1, group2, shift1, shift2;  // shift: log2(group / 32)
     int zeros1, zeros2, tile1, tile2, scale_fp16;
     int h_stride;
-    int stages, stage_a, bytes_b, part_floats, cols, box_bytes;
+    int smem, fixed_bytes, stage_a, part_floats, box_bytes;
     epk::CheckCtx chk;
 };
 

@@ -110,22 +110,21 @@ struct Split {
 // two such runs, the first and the last.
 struct Rest {
     int i, m;
-    Split sp;
 };
 struct Rests {
     int n;
     Rest of[2];
 };
 
-// Sums v[c] of N columns of a shared tile (`cols` of them valid), this
-// thread's row, over the parts in the order of the inputs. `base` is the
-// first column in slot 0. Up to four parts' loads are in flight.
-template <int N>
+// Sums v[c] of N values of a shared tile, STEP apart (`cols` of them valid),
+// over the parts in the order of the inputs. `base` is the first value in
+// slot 0. Up to four parts' loads are in flight.
+template <int N, int STEP = kTileRows>
 static __device__ __forceinline__ void sum_parts(const float *base, int part_floats, const Split &sp, int cols, float *v)
 {
 #pragma unroll
     for (int c = 0; c < N; ++c)
-        v[c] = c < cols ? __ldcg(base + static_cast<size_t>(sp.slot0) * part_floats + c * kTileRows) : 0.0f;
+        v[c] = c < cols ? __ldcg(base + static_cast<size_t>(sp.slot0) * part_floats + c * STEP) : 0.0f;
     for (int b = sp.b0 + 1; b <= sp.b1; b += 4) {
         float x[4][N];
 #pragma unroll
@@ -133,7 +132,7 @@ static __device__ __forceinline__ void sum_parts(const float *base, int part_flo
 #pragma unroll
             for (int c = 0; c < N; ++c)
                 x[q][c] = b + q <= sp.b1 && c < cols
-                              ? __ldcg(base + static_cast<size_t>(2 * (b + q)) * part_floats + c * kTileRows)
+                              ? __ldcg(base + static_cast<size_t>(2 * (b + q)) * part_floats + c * STEP)
                               : 0.0f;
 #pragma unroll
         for (int q = 0; q < 4; ++q)
