@@ -47,6 +47,7 @@ struct Shared {
     int active, nmax;   // experts that any token chose; the most tokens of one
     int issued_a, issued_b;
     int reset;
+    int3 totals[kMaxLocal / 32];
     Rests rests[2];  // of the two products
 };
 

@@ -49,12 +49,13 @@ constexpr int kSumStride = kTileRows + 4;  // column stride of the groups' sums:
 
 struct Shared {
     uint64_t full_a[kMaxStagesA], empty_a[kMaxStagesA];
-    uint64_t full_b[kMaxStagesB], empty_b[kMaxStagesB];
+    uint64_t full_b[2][kMaxStagesB], empty_b[2][kMaxStagesB];  // a ring for each product
     uint64_t full_s, empty_s;  // the groups' sums of a run
     int abort;
     int active, nmax;
-    int issued_a, issued_b;
+    int issued_a, issued_b[2];
     int reset;
+    int3 totals[kMaxLocal / 32];
     Rests rests[2];
 };
 
@@ -161,13 +162,13 @@ __global__ void __launch_bounds__(kThreads, 1) int4_kernel(const __grid_constant
     if (tid < kMaxStagesA) {
         mbar_init(smem_u32(&sh.full_a[tid]), 1);
         mbar_init(smem_u32(&sh.empty_a[tid]), 8);
-    } else if (tid >= 32 && tid < 32 + kMaxStagesB) {
-        mbar_init(smem_u32(&sh.full_b[tid - 32]), 1);
-        mbar_init(smem_u32(&sh.empty_b[tid - 32]), 8);
+    } else if (tid >= 32 && tid < 32 + 2 * kMaxStagesB) {
+        mbar_init(smem_u32(&sh.full_b[0][tid - 32]), 1);
+        mbar_init(smem_u32(&sh.empty_b[0][tid - 32]), 8);
     } else if (tid == 64) {
         mbar_init(smem_u32(&sh.full_s), kWorkers / 32);
         mbar_init(smem_u32(&sh.empty_s), kResults / 32);
-        sh.abort = sh.reset = sh.rests[0].n = sh.rests[1].n = sh.issued_a = sh.issued_b = 0;
+        sh.abort = sh.reset = sh.rests[0].n = sh.rests[1].n = sh.issued_a = sh.issued_b[0] = sh.issued_b[1] = 0;
         tma_prefetch_map(&a.mx);
     }
     mbar_init_fence();
@@ -199,19 +200,22 @@ __global__ void __launch_bounds__(kThreads, 1) int4_kernel(const __grid_constant
     const int begin1 = shares1.begin(blk), end1 = shares1.begin(blk + 1);
     const int begin2 = LINEAR ? 0 : shares2.begin(blk), end2 = LINEAR ? 0 : shares2.begin(blk + 1);
     const int pairs = li.offset[A];
-    // A unit's token tile, in 8-token steps of 2 KB a chunk: two chunks, or one, and later two in two parts.
-    const int cols = (sh.nmax + 7) & ~7, stage_b = cols * (LINEAR ? 512 : 1024);
+    // A unit's token tile, in 8-token steps of 2 KB a chunk: two chunks, or one (and in the second product two
+    // chunks in two parts). The second product's ring begins where the first's did, which is empty by then: h
+    // is complete when every block is through with the first.
+    const int cols = (sh.nmax + 7) & ~7, stage_b1 = cols * (LINEAR ? 512 : 256), stage_b2 = cols * (LINEAR ? 512 : 1024);
     // With up to 8 tokens every expert's token tile is all of x: a sum's column is the token. Else the tokens are gathered.
     const bool whole = LINEAR || a.T <= 8;
-    // the groups' sums take what this launch's largest entry needs, the rings the rest: an eighth to a
-    // half for tokens
+    // the groups' sums take what this launch's largest entry needs; the rings share the rest so that about as many
+    // token tiles as weight tiles are on their way
     const uint32_t sums_at = (base + a.fixed_bytes + 127u) & ~127u;
     float *const sums = reinterpret_cast<float *>(dyn + (sums_at - dyn0));  // [group][column][kSumStride]
     const uint32_t ring_b = sums_at + kGroups * cols * kSumStride * 4;
     const int room = a.smem - static_cast<int>(ring_b - dyn0);
-    const int stages_b = max(2, min(kMaxStagesB, room / 4 / stage_b));
-    const uint32_t ring_a = ring_b + stages_b * stage_b;
-    const int stages = min(kMaxStagesA, (room - stages_b * stage_b) / a.stage_a);
+    const int stages_b2 = max(2, min(kMaxStagesB, room / (a.stage_a + stage_b2)));
+    const int stages_b1 = min(kMaxStagesB, stages_b2 * stage_b2 / stage_b1);
+    const uint32_t ring_a = ring_b + stages_b2 * stage_b2;
+    const int stages = min(kMaxStagesA, (room - stages_b2 * stage_b2) / a.stage_a);
     const uint8_t *const ring_b_p = dyn + (ring_b - dyn0), *const ring_a_p = dyn + (ring_a - dyn0);
     // h: per entry and chunk a tile [2 parts][4][tokens][32], tokens a multiple of 8
     const auto h_entry = [&](int i) { return a.h + static_cast<size_t>(li.offset[i] + 7 * i) * a.h_stride; };
@@ -251,13 +255,13 @@ __global__ void __launch_bounds__(kThreads, 1) int4_kernel(const __grid_constant
         int issued = 0;
         bool run = true;
         uint32_t dst = 0, bar = 0;
-        auto acquire = [&](uint32_t bytes) {
-            if (!mbar_wait(smem_u32(&sh.empty_b[at.s]), at.parity ^ 1, abort, kWaitEmptyB))
+        auto acquire = [&](int product, uint32_t bytes) {
+            if (!mbar_wait(smem_u32(&sh.empty_b[product][at.s]), at.parity ^ 1, abort, kWaitEmptyB))
                 return false;
-            bar = smem_u32(&sh.full_b[at.s]);
-            dst = ring_b + at.s * stage_b;
+            bar = smem_u32(&sh.full_b[product][at.s]);
+            dst = ring_b + at.s * (product ? stage_b2 : stage_b1);
             mbar_expect(bar, bytes);
-            at.next(stages_b);
+            at.next(product ? stages_b2 : stages_b1);
             ++issued;
             return true;
         };
@@ -265,7 +269,7 @@ __global__ void __launch_bounds__(kThreads, 1) int4_kernel(const __grid_constant
             const int n = li.count(w.i), n8 = (n + 7) & ~7, off = li.offset[w.i];
             const unsigned char *const tok = li.token + off;
             const uint32_t bytes = whole ? a.box_bytes : ((n + 3) & ~3) * 256;
-            for (int k = w.k; k < w.k + w.len && (run = acquire(bytes)); ++k) {
+            for (int k = w.k; k < w.k + w.len && (run = acquire(0, bytes)); ++k) {
                 if (whole) {  // [inputs / 32][tokens][32]
                     tma_load_box(dst, &a.mx, bar, 0, LINEAR ? off : 0, LINEAR ? 8 * k : 4 * k);
                 } else {
@@ -282,18 +286,21 @@ __global__ void __launch_bounds__(kThreads, 1) int4_kernel(const __grid_constant
             run = wait_count(a.done, a.mt1 * pairs, abort, kWaitDone);
             fence_async_proxy();
         }
+        sh.issued_b[0] = issued;
+        issued = 0;
+        at = Cursor();
         const uint64_t policy = policy_evict_first();
         for (Walk w(begin2, end2, ku2, A, true); run && w.more(); w.next()) {
             const uint32_t chunk = ceil_div(li.count(w.i), 8) * 4096;
             const uint8_t *src = reinterpret_cast<const uint8_t *>(h_entry(w.i)) + static_cast<size_t>(2 * w.k) * chunk;
             for (int k = w.k; run && k < w.k + w.len; ++k, src += 2 * chunk) {
                 const uint32_t bytes = 2 * k + 1 < a.kc2 ? 2 * chunk : chunk;
-                run = acquire(bytes);
+                run = acquire(1, bytes);
                 if (run)
                     bulk_load(dst, src, bytes, bar, policy);
             }
         }
-        sh.issued_b = issued;
+        sh.issued_b[1] = issued;
     } else if (warp < kWorkers / 32) {
         // ---- products ----
         const int grp = warp >> 2, rows32 = warp & 3;
@@ -321,7 +328,7 @@ __global__ void __launch_bounds__(kThreads, 1) int4_kernel(const __grid_constant
             // rows of 32 inputs and one token are 64 bytes: the second chunk's token tile
             const int chunk_b = !tile ? 0 : LINEAR ? NT * 8 * 256 : SECOND ? NT * 8 * 512 : 0;
             for (; turn < units; turn += 2) {
-                const uint32_t fa = smem_u32(&sh.full_a[at_a.s]), fb = smem_u32(&sh.full_b[at_b.s]);
+                const uint32_t fa = smem_u32(&sh.full_a[at_a.s]), fb = smem_u32(&sh.full_b[SECOND][at_b.s]);
                 if (!mbar_wait2_warp(fa, at_a.parity, fb, at_b.parity, abort, kWaitFullA, kWaitFullB)) {
                     run = false;
                     turn = units;
@@ -330,11 +337,11 @@ __global__ void __launch_bounds__(kThreads, 1) int4_kernel(const __grid_constant
                 if ((!LINEAR && !SECOND) || 2 * (k + turn) + tile < kc)
                     add_tile<NT, SHIFT, SECOND ? 2 : 1, BF16>(
                         acc, ring_a_p + at_a.s * a.stage_a + tile * (SECOND ? a.tile2 : a.tile1), rows32, lane,
-                        ring_b_p + at_b.s * stage_b + chunk_b, with_zeros, scale_fp16);
+                        ring_b_p + at_b.s * (SECOND ? stage_b2 : stage_b1) + chunk_b, with_zeros, scale_fp16);
                 __syncwarp();
                 mbar_arrive2_if(lane == 0, fa + empty_a, fb + empty_b);
                 at_a.advance(2, stages);  // the group's next unit
-                at_b.advance(2, stages_b);
+                at_b.advance(2, SECOND ? stages_b2 : stages_b1);
             }
             turn -= units;
             // the sums of the run before have been read
@@ -373,14 +380,16 @@ __global__ void __launch_bounds__(kThreads, 1) int4_kernel(const __grid_constant
         };
         for (Walk w(begin1, end1, ku1, a.mt1, false); run && w.more(); w.next())
             run_products(std::false_type{}, LINEAR ? sh.nmax : li.count(w.i), w.len, w.k, a.kc1);
+        at_b = Cursor();
+        at_b.s = turn;
         for (Walk w(begin2, end2, ku2, A, true); !LINEAR && run && w.more(); w.next())
             run_products(std::true_type{}, li.count(w.i), w.len, w.k, a.kc2);
     } else if (warp < (kWorkers + kResults) / 32) {
-        // ---- results: a thread has rows rtid and rtid + 64 of a tile ----
-        const int rtid = tid - kWorkers;
+        // ---- results: a thread is a row of a tile ----
+        const int row = tid - kWorkers;
         uint32_t parity = 0;  // of full_s
         bool run = true;
-        // Waits for a run's sums. The two warps leave together, or not at all.
+        // Waits for a run's sums. The four warps leave together, or not at all.
         auto sums_ready = [&] {
             const bool ok = named_all(2, kResults, mbar_wait(smem_u32(&sh.full_s), parity, abort, kWaitFullD));
             parity ^= 1;
@@ -391,31 +400,41 @@ __global__ void __launch_bounds__(kThreads, 1) int4_kernel(const __grid_constant
             if (lane == 0)
                 mbar_arrive(smem_u32(&sh.empty_s));
         };
-        // Column j of the sums of a row: of the even (0) or odd (1) groups, or all.
-        auto sum_half = [&](int j, int row, int odd) {
-            const float *const s = sums + (odd * cols + j) * kSumStride + row;
-            return s[0] + s[2 * cols * kSumStride];
+        // Four columns of the sums from column c[0] .. c[3] on, this thread's row: of the even (0) or odd (1)
+        // groups, or all. The loads of all four are in flight at once.
+        auto sum_half = [&](const int (&c)[4], int odd, float (&v)[4]) {
+            const float *const s = sums + odd * cols * kSumStride + row;
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                v[i] = s[c[i] * kSumStride] + s[(2 * cols + c[i]) * kSumStride];
         };
-        auto sum_all = [&](int j, int row) { return sum_half(j, row, 0) + sum_half(j, row, 1); };
+        auto sum_all = [&](const int (&c)[4], float (&v)[4]) {
+            float x[4];
+            sum_half(c, 0, v);
+            sum_half(c, 1, x);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                v[i] += x[i];
+        };
 
         // As in moe_experts.cu: tiles shared with other blocks are settled after a product's last run.
         auto arrive = [&](const Rests &rests, int *counters, bool second) {
             named_sync(1, kResults);
-            if (rtid < rests.n)
-                add_acq_rel(counters + (second ? rests.of[rtid].m : rests.of[rtid].i * a.mt1 + rests.of[rtid].m), 1);
+            if (row < rests.n)
+                add_acq_rel(counters + (second ? rests.of[row].m : rests.of[row].i * a.mt1 + rests.of[row].m), 1);
         };
         auto parts_written = [&](int *counter, const Split &sp) {
-            return named_all(2, kResults, rtid != 0 || wait_count(counter, sp.parts(), abort, kWaitOther));
+            return named_all(2, kResults, row != 0 || wait_count(counter, sp.parts(), abort, kWaitOther));
         };
         // h of these columns of a tile goes out to the copies of every block.
         auto announce = [&](int columns) {
             fence_async_proxy();
             named_sync(1, kResults);
-            if (rtid == 0)
+            if (row == 0)
                 add_acq_rel(a.done, columns);
         };
-        // column j of a row of row tile m: h, or y of the linear layer
-        auto result = [&](int i, int m, int j, int row, float gate, float up) {
+        // column j of row tile m: h, or y of the linear layer
+        auto result = [&](int i, int m, int j, float gate, float up) {
             const int col = m * kTileRows + row;
             if (LINEAR) {
                 uint16_t *const p = static_cast<uint16_t *>(a.out) + (li.offset[i] + j) * a.out_stride + col;
@@ -431,7 +450,7 @@ __global__ void __launch_bounds__(kThreads, 1) int4_kernel(const __grid_constant
         };
         // A run's part: the block's second slot unless it is the first run of its share.
         auto part_of = [&](bool first) {
-            return a.part + static_cast<size_t>(2 * blk + (first ? 0 : 1)) * a.part_floats;
+            return a.part + static_cast<size_t>(2 * blk + (first ? 0 : 1)) * a.part_floats + row;
         };
 
         int announced = 0;  // columns of h that are written and not yet announced
@@ -443,24 +462,37 @@ __global__ void __launch_bounds__(kThreads, 1) int4_kernel(const __grid_constant
             if (!run)
                 break;
             float *const part = part_of(first);
-            for (int j = 0; j < n; ++j) {
-                const int c = !LINEAR && whole ? tok[j] : j;  // the sum's column
-                for (int row = rtid; row < kTileRows; row += kResults) {
-                    const float g = LINEAR ? sum_all(c, row) : sum_half(c, row, 0);
-                    const float u = LINEAR ? 0.0f : sum_half(c, row, 1);
+            for (int j = 0; j < n; j += 4) {
+                int c[4];  // the sums' columns
+                float g[4], u[4] = {};
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int k = min(j + i, n - 1);
+                    c[i] = !LINEAR && whole ? tok[k] : k;
+                }
+                if (LINEAR) {
+                    sum_all(c, g);
+                } else {
+                    sum_half(c, 0, g);
+                    sum_half(c, 1, u);
+                }
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    if (j + i >= n)
+                        break;
                     if (shared) {
-                        part[j * kTileRows + row] = g;
+                        part[(j + i) * kTileRows] = g[i];
                         if (!LINEAR)
-                            part[(n + j) * kTileRows + row] = u;
+                            part[(n + j + i) * kTileRows] = u[i];
                     } else {
-                        result(w.i, w.m, j, row, g, u);
+                        result(w.i, w.m, j + i, g[i], u[i]);
                     }
                 }
             }
             sums_read();
             if (!shared)
                 announced += n;
-            else if (rtid == 0)
+            else if (row == 0)
                 sh.rests[0].of[sh.rests[0].n++] = Rest{w.i, w.m};
         }
         if (run) {
@@ -474,10 +506,10 @@ __global__ void __launch_bounds__(kThreads, 1) int4_kernel(const __grid_constant
                 run = parts_written(a.tiles + i * a.mt1 + m, sp);
                 for (int j = lo; run && j < hi; ++j) {
                     float g[1], u[1] = {};
-                    sum_parts<1>(a.part + j * kTileRows + rtid, a.part_floats, sp, 1, g);
+                    sum_parts<1>(a.part + j * kTileRows + row, a.part_floats, sp, 1, g);
                     if (!LINEAR)
-                        sum_parts<1>(a.part + (n + j) * kTileRows + rtid, a.part_floats, sp, 1, u);
-                    result(i, m, j, rtid, g[0], u[0]);
+                        sum_parts<1>(a.part + (n + j) * kTileRows + row, a.part_floats, sp, 1, u);
+                    result(i, m, j, g[0], u[0]);
                 }
                 announced += hi - lo;
             }
@@ -486,7 +518,7 @@ __global__ void __launch_bounds__(kThreads, 1) int4_kernel(const __grid_constant
         }
 
         const int group = LINEAR ? 1 : A * ku2;
-        auto store_y = [&](int m, int t, int row, float r) {
+        auto store_y = [&](int m, int t, float r) {
             const int col = m * kTileRows + row;
             __nv_bfloat16 *const p = static_cast<__nv_bfloat16 *>(a.out) + t * a.out_stride + col;
             if (col < a.H && EP_IN_BOUNDS(a.chk, epk::kSiteMoeOut, p, 2, a.out, 2 * ((a.T - 1) * a.out_stride + a.H)))
@@ -496,18 +528,26 @@ __global__ void __launch_bounds__(kThreads, 1) int4_kernel(const __grid_constant
             const int m = w.m, i0 = w.i;
             const bool first = w.left == end2 - begin2;
             bool shared = w.i != 0 || w.k != 0;  // an earlier block began this row tile
-            for (int t = rtid; t < a.T * kTileRows; t += kResults)  // a thread's own rows: no barrier
-                acc_y[t] = 0.0f;
+            for (int t = 0; t < a.T; ++t)  // a thread's own row: no barrier
+                acc_y[t * kTileRows + row] = 0.0f;
             for (; w.more() && w.m == m; w.next()) {
                 const int off = li.offset[w.i], n = li.count(w.i);
                 run = sums_ready();
                 if (!run)
                     break;
-                for (int j = 0; j < n; ++j) {
-                    float *const y = acc_y + li.token[off + j] * kTileRows;
-                    const float weight = li.weight[off + j];
-                    for (int row = rtid; row < kTileRows; row += kResults)
-                        y[row] = fmaf(weight, sum_all(j, row), y[row]);
+                for (int j = 0; j < n; j += 4) {
+                    int c[4];
+                    float v[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        c[i] = min(j + i, n - 1);
+                    sum_all(c, v);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        if (j + i < n) {  // a token is in one column of an entry
+                            float *const y = acc_y + li.token[off + j + i] * kTileRows + row;
+                            *y = fmaf(li.weight[off + j + i], v[i], *y);
+                        }
                 }
                 sums_read();
             }
@@ -516,14 +556,13 @@ __global__ void __launch_bounds__(kThreads, 1) int4_kernel(const __grid_constant
             shared = shared || (!w.more() && end2 != (m + 1) * group);  // a later block ends it
             if (shared) {
                 float *const part = part_of(first);
-                for (int t = rtid; t < a.T * kTileRows; t += kResults)
-                    part[t] = acc_y[t];
-                if (rtid == 0)
+                for (int t = 0; t < a.T; ++t)
+                    part[t * kTileRows] = acc_y[t * kTileRows + row];
+                if (row == 0)
                     sh.rests[1].of[sh.rests[1].n++] = Rest{i0, m};
             } else {
                 for (int t = 0; t < a.T; ++t)
-                    for (int row = rtid; row < kTileRows; row += kResults)
-                        store_y(m, t, row, acc_y[t * kTileRows + row]);
+                    store_y(m, t, acc_y[t * kTileRows + row]);
             }
         }
         if (!LINEAR && run) {
@@ -538,8 +577,8 @@ __global__ void __launch_bounds__(kThreads, 1) int4_kernel(const __grid_constant
                 run = parts_written(counters + m, sp);
                 for (int t = lo; run && t < hi; ++t) {
                     float x[1];
-                    sum_parts<1>(a.part + t * kTileRows + rtid, a.part_floats, sp, 1, x);
-                    store_y(m, t, rtid, x[0]);
+                    sum_parts<1>(a.part + t * kTileRows + row, a.part_floats, sp, 1, x);
+                    store_y(m, t, x[0]);
                 }
             }
         }
@@ -551,8 +590,11 @@ __global__ void __launch_bounds__(kThreads, 1) int4_kernel(const __grid_constant
         if (tid == 0) {
             for (int i = max(0, sh.issued_a - stages); i < sh.issued_a; ++i)
                 mbar_wait(smem_u32(&sh.full_a[i % stages]), (i / stages) & 1, nullptr, kWaitOther);
-            for (int i = max(0, sh.issued_b - stages_b); i < sh.issued_b; ++i)
-                mbar_wait(smem_u32(&sh.full_b[i % stages_b]), (i / stages_b) & 1, nullptr, kWaitOther);
+            for (int product = 0; product < 2; ++product) {
+                const int n = product ? stages_b2 : stages_b1;
+                for (int i = max(0, sh.issued_b[product] - n); i < sh.issued_b[product]; ++i)
+                    mbar_wait(smem_u32(&sh.full_b[product][i % n]), (i / n) & 1, nullptr, kWaitOther);
+            }
             atomicAdd_system(a.err + sh.abort, 1u);
             __threadfence_system();
             atomicAdd_system(a.err, 1u);

@@ -638,15 +638,23 @@ int router_rows(const RouterArgs &a) { return plan_many(a).rows; }
 
 namespace {
 
-template <int NT, bool BF16> void launch_few(const RouterArgs &a, cudaStream_t stream)
+template <int NT, int N, bool BF16> cudaError_t launch_few_n(const RouterArgs &a, cudaStream_t stream)
 {
+    // the experts kernel that usually follows needs all of the SM's memory as shared memory: no change of the split
+    static const cudaError_t attr = cudaFuncSetAttribute(
+        few_kernel<NT, N, BF16>, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared);
+    if (attr != cudaSuccess)
+        return attr;
     const dim3 grid((a.E + 15) / 16, few_splits(a), (a.T + NT * 8 - 1) / (NT * 8));
-    if (a.E <= 128)
-        few_kernel<NT, 4, BF16><<<grid, 256, 0, stream>>>(a);
-    else if (a.E <= 256)
-        few_kernel<NT, 8, BF16><<<grid, 256, 0, stream>>>(a);
-    else
-        few_kernel<NT, 16, BF16><<<grid, 256, 0, stream>>>(a);
+    few_kernel<NT, N, BF16><<<grid, 256, 0, stream>>>(a);
+    return cudaGetLastError();
+}
+
+template <int NT, bool BF16> cudaError_t launch_few(const RouterArgs &a, cudaStream_t stream)
+{
+    return a.E <= 128   ? launch_few_n<NT, 4, BF16>(a, stream)
+           : a.E <= 256 ? launch_few_n<NT, 8, BF16>(a, stream)
+                        : launch_few_n<NT, 16, BF16>(a, stream);
 }
 
 template <bool BF16> cudaError_t launch_many(RouterArgs a, cudaStream_t stream)
@@ -691,11 +699,8 @@ cudaError_t launch_router(const RouterArgs &all, cudaStream_t stream)
         a.x = static_cast<const uint16_t *>(all.x) + t * all.x_stride;
         a.ids = all.ids + static_cast<size_t>(t) * a.K;
         a.weights = all.weights + static_cast<size_t>(t) * a.K;
-        if (a.T <= 8)
-            a.bf16 ? launch_few<1, true>(a, stream) : launch_few<1, false>(a, stream);
-        else
-            a.bf16 ? launch_few<2, true>(a, stream) : launch_few<2, false>(a, stream);
-        const cudaError_t ce = cudaGetLastError();
+        const cudaError_t ce = a.T <= 8 ? (a.bf16 ? launch_few<1, true>(a, stream) : launch_few<1, false>(a, stream))
+                                        : (a.bf16 ? launch_few<2, true>(a, stream) : launch_few<2, false>(a, stream));
         if (ce != cudaSuccess)
             return ce;
     }

@@ -157,92 +157,113 @@ static __device__ __forceinline__ float swiglu(float gate, float up) { return ga
 struct Lists {
     unsigned long long *mask;  // [E] tokens of each expert
     float *weight;             // [P] routing weight of each (entry, token) pair
+    float *given;              // [P] the call's weights
     unsigned short *expert;    // [2 E] of each entry, ascending
     unsigned short *offset;    // [2 E + 1] the entry's first pair
+    unsigned short *start;     // [E] each active expert's first pair
+    short *id;                 // [P] the call's ids, local
     unsigned char *token;      // [P] tokens, ascending per expert
 
     __device__ __forceinline__ Lists(void *at, int E, int P)
     {
         mask = static_cast<unsigned long long *>(at);
         weight = reinterpret_cast<float *>(mask + E);
-        expert = reinterpret_cast<unsigned short *>(weight + P);
+        given = weight + P;
+        expert = reinterpret_cast<unsigned short *>(given + P);
         offset = expert + 2 * E;
-        token = reinterpret_cast<unsigned char *>(offset + 2 * E + 1);
+        start = offset + 2 * E + 1;
+        id = reinterpret_cast<short *>(start + E);
+        token = reinterpret_cast<unsigned char *>(id + P);
     }
     __device__ __forceinline__ int count(int i) const { return offset[i + 1] - offset[i]; }
 };
 
-static inline size_t lists_bytes(int E, int P) { return size_t(E) * 16 + size_t(P) * 5 + 2; }
+static inline size_t lists_bytes(int E, int P) { return size_t(E) * 18 + size_t(P) * 11 + 2; }
 
-// Builds the lists; every block does, from the ids themselves. A token's bit
-// in its expert's mask makes the order of the threads irrelevant. All
-// threads of the block call it; the caller synchronises before it reads
-// token and weight. sh.active: entries, sh.nmax: the most tokens of one.
+// Builds the lists; every block does, from the ids themselves, with one trip
+// to memory and four barriers. A token's bit in its expert's mask makes the
+// order of the threads irrelevant. All threads of the block call it; the
+// caller synchronises before it reads them. sh.active: entries, sh.nmax: the
+// most tokens of one, sh.totals: scratch.
 template <class Args, class Shared>
 static __device__ __forceinline__ void build_lists(const Args &a, const Lists &li, Shared &sh, int tid, int threads,
                                                    int cap)
 {
+    const int warp = tid >> 5, lane = tid & 31, blocks = (a.E + 31) / 32;
+    for (int i = tid; i < a.P; i += threads) {
+        int e = -1;
+        float w = 0.0f;
+        if (EP_IN_BOUNDS(a.chk, epk::kSiteMoeIds, a.ids + i, 4, a.ids, 4LL * a.P))
+            e = a.ids[i] - a.first;
+        if (EP_IN_BOUNDS(a.chk, epk::kSiteMoeWeights, a.weights + i, 4, a.weights, 4LL * a.P))
+            w = a.weights[i];
+        li.id[i] = static_cast<short>(e >= 0 && e < a.E ? e : -1);
+        li.given[i] = w;
+    }
     for (int e = tid; e < a.E; e += threads)
         li.mask[e] = 0;
     __syncthreads();
-    for (int i = tid; i < a.P; i += threads) {
-        if (!EP_IN_BOUNDS(a.chk, epk::kSiteMoeIds, a.ids + i, 4, a.ids, 4LL * a.P))
-            continue;
-        const int e = a.ids[i] - a.first;
-        if (e >= 0 && e < a.E)
-            atomicOr(&li.mask[e], 1ULL << (i / a.K));
+    for (int i = tid; i < a.P; i += threads)
+        if (li.id[i] >= 0)
+            atomicOr(&li.mask[li.id[i]], 1ULL << (i / a.K));
+    __syncthreads();
+    // 32 experts to a warp: counts of entries and pairs before each expert, first within the 32
+    for (int b = warp; b < blocks; b += threads / 32) {
+        const int e = b * 32 + lane, n = e < a.E ? __popcll(li.mask[e]) : 0;
+        const unsigned live = __ballot_sync(~0u, n > 0), two = __ballot_sync(~0u, n > cap);
+        const int pairs = __reduce_add_sync(~0u, n), most = __reduce_max_sync(~0u, n > cap ? (n + 1) / 2 : n);
+        if (lane == 0)
+            sh.totals[b] = make_int3(__popc(live) + __popc(two), pairs, most);
     }
     __syncthreads();
-    if (tid < 32) {
-        const int lane = tid;
-        int entries = 0, pairs = 0, nmax = 0;
-        for (int e0 = 0; e0 < a.E; e0 += 32) {
-            const int e = e0 + lane;
-            const int n = e < a.E ? __popcll(li.mask[e]) : 0;
-            const unsigned live = __ballot_sync(~0u, n > 0), two = __ballot_sync(~0u, n > cap);
-            if (live == 0)
-                continue;
+    for (int b = warp; b < blocks; b += threads / 32) {
+        int entries = 0, pairs = 0, most = 0;
+        for (int c = 0; c < b; ++c) {
+            entries += sh.totals[c].x;
+            pairs += sh.totals[c].y;
+            most = max(most, sh.totals[c].z);
+        }
+        const int e = b * 32 + lane, n = e < a.E ? __popcll(li.mask[e]) : 0;
+        const unsigned live = __ballot_sync(~0u, n > 0), two = __ballot_sync(~0u, n > cap), before = (1u << lane) - 1;
+        if (live) {
             int sum = n;  // inclusive prefix sum over the lanes
             for (int d = 1; d < 32; d <<= 1) {
                 const int v = __shfl_up_sync(~0u, sum, d);
                 if (lane >= d)
                     sum += v;
             }
-            const int half = n > cap ? (n + 1) / 2 : n;
             if (n > 0) {
-                const unsigned before = (1u << lane) - 1;
                 const int at = entries + __popc(live & before) + __popc(two & before), off = pairs + sum - n;
                 li.expert[at] = static_cast<unsigned short>(e);
-                li.offset[at] = static_cast<unsigned short>(off);
+                li.offset[at] = li.start[e] = static_cast<unsigned short>(off);
                 if (n > cap) {
                     li.expert[at + 1] = static_cast<unsigned short>(e);
-                    li.offset[at + 1] = static_cast<unsigned short>(off + half);
+                    li.offset[at + 1] = static_cast<unsigned short>(off + (n + 1) / 2);
                 }
             }
-            entries += __popc(live) + __popc(two);
-            pairs += __shfl_sync(~0u, sum, 31);
-            nmax = max(nmax, __reduce_max_sync(~0u, half));
         }
-        if (lane == 0) {
-            li.offset[entries] = static_cast<unsigned short>(pairs);
+        if (b == blocks - 1 && lane == 0) {
+            entries += sh.totals[b].x;
+            li.offset[entries] = static_cast<unsigned short>(pairs + sh.totals[b].y);
             sh.active = entries;
-            sh.nmax = nmax;
+            sh.nmax = max(most, sh.totals[b].z);
         }
     }
     __syncthreads();
-    for (int i = tid; i < sh.active; i += threads) {
-        const int e = li.expert[i];
-        unsigned long long m = li.mask[e];
-        if (i > 0 && li.expert[i - 1] == e)  // the second entry: past the first one's tokens
-            for (int j = li.count(i - 1); j > 0; --j)
-                m &= m - 1;
-        for (int at = li.offset[i]; at < li.offset[i + 1]; ++at, m &= m - 1) {
-            const int t = __ffsll(static_cast<long long>(m)) - 1;
-            float w = 0.0f;  // an expert named twice by a token counts twice
-            for (int k = 0; k < a.K; ++k)
-                if (a.ids[t * a.K + k] - a.first == e &&
-                    EP_IN_BOUNDS(a.chk, epk::kSiteMoeWeights, a.weights + t * a.K + k, 4, a.weights, 4LL * a.P))
-                    w += a.weights[t * a.K + k];
+    for (int i = tid; i < a.P; i += threads) {
+        const int e = li.id[i];
+        if (e < 0)
+            continue;
+        const int t = i / a.K, first = t * a.K;
+        float w = 0.0f;  // an expert named twice by a token counts twice, at its first place
+        bool earlier = false;
+        for (int k = first; k < first + a.K; ++k)
+            if (li.id[k] == e) {
+                earlier = earlier || k < i;
+                w += li.given[k];
+            }
+        if (!earlier) {
+            const int at = li.start[e] + __popcll(li.mask[e] & ((1ULL << t) - 1));
             li.token[at] = static_cast<unsigned char>(t);
             li.weight[at] = w;
         }
