@@ -26,8 +26,9 @@ namespace moe {
 
 namespace {
 
-constexpr int kFewTokens = 256;
-constexpr int kManyExperts = 384;  // a tile's scores fit shared memory; above, slices of kFewTokens
+constexpr int kFewTokens = 64;
+constexpr int kSlice = 256;         // tokens of one launch of the kernel for few
+constexpr int kManyExperts = 384;  // a tile's scores fit shared memory; above, the kernel for few
 
 // Order-preserving image of a float in the unsigned integers; NaN and -infinity give 0 (never chosen).
 static __device__ __forceinline__ uint32_t ordered(float v)
@@ -99,7 +100,17 @@ template <int N> static __device__ void choose_warp(const RouterArgs &a, int t, 
     if (a.groups > 1) {
         const int per = a.E / a.groups;
         uint32_t value = 0;  // of group `lane`
-        for (int g = 0; g < a.groups; ++g) {
+        if (per == 32) {  // group g is c[g] of the lanes
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                const uint32_t m1 = __reduce_max_sync(~0u, c[i]);
+                const int owner = __ffs(__ballot_sync(~0u, c[i] == m1)) - 1;
+                const uint32_t m2 = __reduce_max_sync(~0u, lane == owner ? 0 : c[i]);
+                if (lane == i)
+                    value = ordered(unordered(m1) + unordered(m2));
+            }
+        }
+        for (int g = 0; per != 32 && g < a.groups; ++g) {
             uint32_t b1 = 0, b2 = 0;
 #pragma unroll
             for (int i = 0; i < N; ++i) {
@@ -168,6 +179,30 @@ template <int N> static __device__ void choose_warp(const RouterArgs &a, int t, 
         store_choice(a, t, lane, id, w);
 }
 
+// The same, the logits being sums of `parts` rows of E, `next` apart.
+template <int N>
+static __device__ void choose_from_parts(const RouterArgs &a, int t, const float *p, size_t next, int parts, int lane)
+{
+    float l[N];
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+        l[i] = lane + 32 * i < a.E ? 0.0f : -INFINITY;
+    for (int s = 0; s < parts; s += 4) {
+        float v[4][N];
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+#pragma unroll
+            for (int i = 0; i < N; ++i)
+                v[q][i] = s + q < parts && lane + 32 * i < a.E ? __ldcg(p + (s + q) * next + lane + 32 * i) : 0.0f;
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+#pragma unroll
+            for (int i = 0; i < N; ++i)
+                l[i] += v[q][i];
+    }
+    choose_warp<N>(a, t, l, lane);
+}
+
 // ---- few tokens --------------------------------------------------------------------
 
 // Sixteen bytes of a row, zeros past its end.
@@ -176,15 +211,17 @@ static __device__ __forceinline__ uint4 load_row(const uint16_t *row, int k, int
     return valid && k < H ? __ldg(reinterpret_cast<const uint4 *>(row + k)) : make_uint4(0, 0, 0, 0);
 }
 
-// grid (16-expert blocks, input slices, token blocks of 8 NT); 8 warps that share the slice's 32-input steps.
+// grid (16-expert blocks, input slices, token blocks of 8 NT); 8 NT warps that share the slice's 32-input steps,
+// so that the last block has a warp for each token.
 template <int NT, int N, bool BF16>
-__global__ void __launch_bounds__(256) few_kernel(const __grid_constant__ RouterArgs a)
+__global__ void __launch_bounds__(NT * 256) few_kernel(const __grid_constant__ RouterArgs a)
 {
-    __shared__ float red[8][16][NT * 8 + 1];
+    constexpr int kWarps = NT * 8;
+    __shared__ float red[kWarps][16][NT * 8 + 1];
     __shared__ int last;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t4 = lane & 3;
     const int e0 = blockIdx.x * 16, t0 = blockIdx.z * NT * 8, splits = gridDim.y;
-    const int steps = (a.H + 31) / 32, share = splits * 8, mine = blockIdx.y * 8 + warp;
+    const int steps = (a.H + 31) / 32, share = splits * kWarps, mine = blockIdx.y * kWarps + warp;
     const int s0 = steps * mine / share, s1 = steps * (mine + 1) / share;
     const uint16_t *const W = static_cast<const uint16_t *>(a.weight), *const X = static_cast<const uint16_t *>(a.x);
     const bool ok0 = e0 + g < a.E, ok1 = e0 + g + 8 < a.E;
@@ -221,11 +258,11 @@ __global__ void __launch_bounds__(256) few_kernel(const __grid_constant__ Router
         for (int i = 0; i < 4; ++i)
             red[warp][g + (i >> 1) * 8][nt * 8 + t4 * 2 + (i & 1)] = c[nt][i];
     __syncthreads();
-    for (int i = threadIdx.x; i < NT * 8 * 16; i += 256) {
+    for (int i = threadIdx.x; i < NT * 8 * 16; i += kWarps * 32) {
         const int t = i >> 4, e = i & 15;
         float v = 0.0f;
 #pragma unroll
-        for (int w = 0; w < 8; ++w)
+        for (int w = 0; w < kWarps; ++w)
             v += red[w][e][t];
         if (t0 + t < a.T && e0 + e < a.E)
             a.parts[(static_cast<size_t>(blockIdx.y) * a.T + t0 + t) * a.E + e0 + e] = v;
@@ -240,28 +277,9 @@ __global__ void __launch_bounds__(256) few_kernel(const __grid_constant__ Router
     __syncthreads();
     if (!last)
         return;
-    for (int t = t0 + warp; t < min(t0 + NT * 8, a.T); t += 8) {
-        float l[N];
-#pragma unroll
-        for (int i = 0; i < N; ++i)
-            l[i] = lane + 32 * i < a.E ? 0.0f : -INFINITY;
-        const float *const p = a.parts + static_cast<size_t>(t) * a.E;
-        const size_t next = static_cast<size_t>(a.T) * a.E;
-        for (int s = 0; s < splits; s += 4) {
-            float v[4][N];
-#pragma unroll
-            for (int q = 0; q < 4; ++q)
-#pragma unroll
-                for (int i = 0; i < N; ++i)
-                    v[q][i] = s + q < splits && lane + 32 * i < a.E ? __ldcg(p + (s + q) * next + lane + 32 * i) : 0.0f;
-#pragma unroll
-            for (int q = 0; q < 4; ++q)
-#pragma unroll
-                for (int i = 0; i < N; ++i)
-                    l[i] += v[q][i];
-        }
-        choose_warp<N>(a, t, l, lane);
-    }
+    const int t = t0 + warp;
+    if (t < a.T)
+        choose_from_parts<N>(a, t, a.parts + static_cast<size_t>(t) * a.E, static_cast<size_t>(a.T) * a.E, splits, lane);
 }
 
 // ---- many tokens -------------------------------------------------------------------
@@ -398,7 +416,7 @@ static __device__ void choose_thread(const RouterArgs &a, int t, float *score, c
 
 // grid (token tiles, input splits). Dynamic shared memory: the ring, used again
 // for scores [E + groups][128] and the bias.
-template <bool BF16>
+template <int N, bool BF16>
 __global__ void __launch_bounds__(kThreads, 1) many_kernel(const __grid_constant__ RouterArgs a)
 {
     extern __shared__ uint8_t dyn[];
@@ -434,6 +452,8 @@ __global__ void __launch_bounds__(kThreads, 1) many_kernel(const __grid_constant
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = sh.tmem;
+    // Up to four accumulators along the inputs, added up in fp32: long sums in one lose twice the last bits.
+    const int spans = min(4, a.tmem_cols / E16);
 
     if (warp == 0 && elect_one()) {
         int s = 0, it = 0;
@@ -456,7 +476,15 @@ __global__ void __launch_bounds__(kThreads, 1) many_kernel(const __grid_constant
         int s = 0;
         uint32_t parity = 0;
         const uint32_t idesc = idesc_f16(128, half, BF16);
+        int span = 0, next = c0;  // the accumulator in use, and the chunk from which it is another
+        uint32_t d = tmem;
         for (int c = c0; c < c1; ++c) {
+            const bool first = c == next;
+            if (first) {
+                d = tmem + span * E16;
+                next = c0 + (c1 - c0) * ++span / spans;
+                next = next > c ? next : c + 1;
+            }
             if (!mbar_wait_warp(smem_u32(&sh.full[s]), parity, abort, kWaitFullA))
                 break;
             tc_fence_after();
@@ -466,7 +494,7 @@ __global__ void __launch_bounds__(kThreads, 1) many_kernel(const __grid_constant
                 for (int e = 0; e < E16; e += half)
 #pragma unroll
                     for (int q = 0; q < 4; ++q)
-                        mma_ss(tmem + e, da + 2 * q, db + e * 8 + 2 * q, idesc, c > c0 || q > 0);
+                        mma_ss(d + e, da + 2 * q, db + e * 8 + 2 * q, idesc, !first || q > 0);
                 tc_commit(smem_u32(&sh.empty[s]));
             }
             if (++s == a.stages) {
@@ -487,27 +515,44 @@ __global__ void __launch_bounds__(kThreads, 1) many_kernel(const __grid_constant
         bool run = mbar_wait_warp(smem_u32(&sh.done), 0, abort, kWaitFullD);
         run = named_all(2, 256, run);
         tc_fence_after();
+        const int used = min(spans, c1 - c0);
+        auto logits = [&](int e, float (&v)[8]) {
+            float x[8];
+            tmem_ld8(lanes + e, v);
+            for (int i = 1; i < used; ++i) {
+                tmem_ld8(lanes + i * E16 + e, x);
+                tmem_wait_ld();
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    v[j] += x[j];
+            }
+            tmem_wait_ld();
+        };
         if (run && splits == 1) {
             for (int e = b0; e < b1; e += 8) {  // every MMA has been read: the ring is free
                 float v[8];
-                tmem_ld8(lanes + e, v);
-                tmem_wait_ld();
+                logits(e, v);
 #pragma unroll
                 for (int i = 0; i < 8; ++i)
                     if (e + i < b1)
                         scores[(e + i) * 128 + row] = v[i];
             }
-        } else if (run) {
-            const size_t tile_floats = static_cast<size_t>(a.E) * 128;
-            float *const p = a.parts + (static_cast<size_t>(tile) * splits + split) * tile_floats;
+        } else if (run) {  // parts: [tile][split][token][E]
+            float *const p = a.parts + ((static_cast<size_t>(tile) * splits + split) * 128 + row) * a.E;
             for (int e = b0; e < b1; e += 8) {
                 float v[8];
-                tmem_ld8(lanes + e, v);
-                tmem_wait_ld();
+                logits(e, v);
+                if (row >= rows)
+                    continue;
+                if (a.E % 4 == 0 && e + 8 <= b1) {  // a sector for each thread
+                    *reinterpret_cast<float4 *>(p + e) = make_float4(v[0], v[1], v[2], v[3]);
+                    *reinterpret_cast<float4 *>(p + e + 4) = make_float4(v[4], v[5], v[6], v[7]);
+                } else {
 #pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    if (e + i < b1)
-                        p[(e + i) * 128 + row] = v[i];
+                    for (int i = 0; i < 8; ++i)
+                        if (e + i < b1)
+                            p[e + i] = v[i];
+                }
             }
             named_sync(1, 256);
             if (wtid == 0) {
@@ -515,29 +560,14 @@ __global__ void __launch_bounds__(kThreads, 1) many_kernel(const __grid_constant
                 run = wait_count(a.counters + tile, splits, abort, kWaitOther);
             }
             run = named_all(2, 256, run);
+            // this block's tokens of the tile, a warp each
+            const int r0 = rows * split / splits, r1 = rows * (split + 1) / splits;
+            const float *const from = a.parts + static_cast<size_t>(tile) * splits * 128 * a.E;
+            for (int r = r0 + warp - 4; run && r < r1; r += 8)
+                choose_from_parts<N>(a, t0 + r, from + static_cast<size_t>(r) * a.E, static_cast<size_t>(128) * a.E, splits,
+                                     lane);
         }
-        // this block's tokens of the tile
-        const int r0 = rows * split / splits, r1 = rows * (split + 1) / splits, n = r1 - r0;
-        if (run && splits > 1) {  // threads to (token, expert) pairs: 32 tokens' loads side by side
-            const size_t tile_floats = static_cast<size_t>(a.E) * 128;
-            const float *const p = a.parts + static_cast<size_t>(tile) * splits * tile_floats + r0;
-            const int wide = n > 64 ? 128 : n > 32 ? 64 : 32, r = wtid % wide;
-            for (int e = wtid / wide; e < a.E; e += 256 / wide)
-                if (r < n) {
-                    float v = 0.0f;
-                    for (int s = 0; s < splits; s += 4) {
-                        float x[4];
-#pragma unroll
-                        for (int q = 0; q < 4; ++q)
-                            x[q] = s + q < splits ? __ldcg(p + (s + q) * tile_floats + e * 128 + r) : 0.0f;
-#pragma unroll
-                        for (int q = 0; q < 4; ++q)
-                            v += x[q];
-                    }
-                    scores[e * 128 + r] = v;
-                }
-        }
-        if (run) {
+        if (run && splits == 1) {
             for (int e = wtid; e < a.E; e += 256)
                 bias[e] = a.bias ? a.bias[e] : 0.0f;
             named_sync(1, 256);
@@ -570,8 +600,8 @@ __global__ void __launch_bounds__(kThreads, 1) many_kernel(const __grid_constant
                     mine[e * 128] = sigmoid(mine[e * 128]);
             }
             named_sync(1, 256);
-            if (part == 0 && row < n)
-                choose_thread(a, t0 + r0 + row, mine, bias, top, sum);
+            if (part == 0 && row < rows)
+                choose_thread(a, t0 + row, mine, bias, top, sum);
         }
     }
     __syncwarp();
@@ -592,28 +622,33 @@ __global__ void __launch_bounds__(kThreads, 1) many_kernel(const __grid_constant
         tmem_free(tmem, a.tmem_cols);
     if (splits > 1 && tid == 0 && add_acq_rel(a.counters + gridDim.x + tile, 1) == splits - 1)
         a.counters[tile] = a.counters[gridDim.x + tile] = 0;  // for the next launch
-    (void)lane;
 }
 
-int few_splits(const RouterArgs &a) { return (((a.H + 31) / 32) + 31) / 32; }  // four steps a warp
+int few_splits(const RouterArgs &a) { return (((a.H + 31) / 32) + 31) / 32; }  // four steps a warp, two of 16 warps
 
 struct ManyPlan {
     int rows, tiles, splits;
 };
 
-// Tiles as high as one more wave of blocks needs, or, where that leaves SMs idle, split inputs.
+// Up to 16 splits of the inputs, as far as a wave of blocks with full tiles
+// leaves SMs idle (a block then chooses for a few tokens, a warp each), and
+// tiles as high as that many blocks need.
 ManyPlan plan_many(const RouterArgs &a)
 {
     ManyPlan p;
-    const int waves = (a.T + a.sms * 128 - 1) / (a.sms * 128);
-    p.rows = (a.T + waves * a.sms - 1) / (waves * a.sms);
-    if (p.rows < 64)
-        p.rows = 128;
-    p.tiles = (a.T + p.rows - 1) / p.rows;
     const int chunks = (a.H + kChunk - 1) / kChunk;
-    p.splits = p.tiles < a.sms ? a.sms / p.tiles : 1;
-    if (p.splits > chunks)
-        p.splits = chunks;
+    p.splits = a.sms * 128 / a.T;
+    p.splits = p.splits > 16 ? 16 : p.splits;
+    p.splits = p.splits > chunks ? chunks : p.splits;
+    if (p.splits <= 1) {
+        const int waves = (a.T + a.sms * 128 - 1) / (a.sms * 128);
+        p.splits = 1;
+        p.rows = (a.T + waves * a.sms - 1) / (waves * a.sms);
+    } else {
+        const int tiles = a.sms / p.splits;
+        p.rows = (a.T + tiles - 1) / tiles;
+    }
+    p.tiles = (a.T + p.rows - 1) / p.rows;
     return p;
 }
 
@@ -626,12 +661,12 @@ size_t router_workspace(const RouterArgs &a)
     if (a.T == 0)
         return 0;
     if (!router_many(a))
-        return static_cast<size_t>(few_splits(a)) * (a.T < kFewTokens ? a.T : kFewTokens) * a.E * sizeof(float);
+        return static_cast<size_t>(few_splits(a)) * (a.T < kSlice ? a.T : kSlice) * a.E * sizeof(float);
     const ManyPlan p = plan_many(a);
     return p.splits == 1 ? 0 : static_cast<size_t>(p.tiles) * p.splits * a.E * 128 * sizeof(float);
 }
 
-int router_counters(int sms) { return 2 * sms + kFewTokens; }
+int router_counters(int sms) { return 2 * sms + kSlice; }
 
 
 int router_rows(const RouterArgs &a) { return plan_many(a).rows; }
@@ -646,7 +681,7 @@ template <int NT, int N, bool BF16> cudaError_t launch_few_n(const RouterArgs &a
     if (attr != cudaSuccess)
         return attr;
     const dim3 grid((a.E + 15) / 16, few_splits(a), (a.T + NT * 8 - 1) / (NT * 8));
-    few_kernel<NT, N, BF16><<<grid, 256, 0, stream>>>(a);
+    few_kernel<NT, N, BF16><<<grid, NT * 256, 0, stream>>>(a);
     return cudaGetLastError();
 }
 
@@ -657,17 +692,17 @@ template <int NT, bool BF16> cudaError_t launch_few(const RouterArgs &a, cudaStr
                         : launch_few_n<NT, 16, BF16>(a, stream);
 }
 
-template <bool BF16> cudaError_t launch_many(RouterArgs a, cudaStream_t stream)
+template <int N, bool BF16> cudaError_t launch_many_n(RouterArgs a, cudaStream_t stream)
 {
     static const cudaError_t attr =
-        cudaFuncSetAttribute(many_kernel<BF16>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+        cudaFuncSetAttribute(many_kernel<N, BF16>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              kSmemMax - 64 - static_cast<int>(sizeof(Shared)));
     if (attr != cudaSuccess)
         return attr;
     const ManyPlan p = plan_many(a);
     const int half = router_columns(a.E), E16 = a.E > half ? 2 * half : half, stage = 16384 + E16 * 128;
     a.rows = p.rows;
-    a.tmem_cols = E16 > 256 ? 512 : E16 > 128 ? 256 : 128;
+    a.tmem_cols = 512;
     a.stages = (kSmemMax - 2048 - static_cast<int>(sizeof(Shared))) / stage;
     if (a.stages > kMaxStages)
         a.stages = kMaxStages;
@@ -684,7 +719,14 @@ template <bool BF16> cudaError_t launch_many(RouterArgs a, cudaStream_t stream)
     at[0].val.cooperative = 1;
     cfg.attrs = at;
     cfg.numAttrs = p.splits > 1 ? 1 : 0;
-    return cudaLaunchKernelEx(&cfg, many_kernel<BF16>, a);
+    return cudaLaunchKernelEx(&cfg, many_kernel<N, BF16>, a);
+}
+
+template <bool BF16> cudaError_t launch_many(const RouterArgs &a, cudaStream_t stream)
+{
+    return a.E <= 128   ? launch_many_n<4, BF16>(a, stream)
+           : a.E <= 256 ? launch_many_n<8, BF16>(a, stream)
+                        : launch_many_n<12, BF16>(a, stream);
 }
 
 }  // namespace
@@ -694,8 +736,8 @@ cudaError_t launch_router(const RouterArgs &all, cudaStream_t stream)
     if (router_many(all))
         return all.bf16 ? launch_many<true>(all, stream) : launch_many<false>(all, stream);
     RouterArgs a = all;
-    for (int t = 0; t < all.T; t += kFewTokens) {
-        a.T = all.T - t < kFewTokens ? all.T - t : kFewTokens;
+    for (int t = 0; t < all.T; t += kSlice) {
+        a.T = all.T - t < kSlice ? all.T - t : kSlice;
         a.x = static_cast<const uint16_t *>(all.x) + t * all.x_stride;
         a.ids = all.ids + static_cast<size_t>(t) * a.K;
         a.weights = all.weights + static_cast<size_t>(t) * a.K;
@@ -710,7 +752,7 @@ cudaError_t launch_router(const RouterArgs &all, cudaStream_t stream)
 cudaError_t router_binary_version(int *v)
 {
     cudaFuncAttributes fa;
-    cudaError_t ce = cudaFuncGetAttributes(&fa, many_kernel<true>);
+    cudaError_t ce = cudaFuncGetAttributes(&fa, many_kernel<8, true>);
     if (ce == cudaSuccess)
         *v = fa.binaryVersion;
     return ce;
