@@ -173,6 +173,16 @@ static __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorM
                  : "memory");
 }
 
+// The same box into this offset of every block of the cluster that `mask` names.
+static __device__ __forceinline__ void tma_load_2d_all(uint32_t dst, const CUtensorMap *m, uint32_t bar, int x, int y,
+                                                       uint16_t mask)
+{
+    asm volatile("cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.multicast::cluster "
+                 "[%0], [%1, {%3, %4}], [%2], %5;" ::"r"(dst),
+                 "l"(m), "r"(bar), "r"(x), "r"(y), "h"(mask)
+                 : "memory");
+}
+
 // Four rows r0..r3 of a two-dimensional map (box one row high), to 4 consecutive tile rows.
 static __device__ __forceinline__ void tma_gather4(uint32_t dst, const CUtensorMap *m, uint32_t bar, int x, int r0,
                                                    int r1, int r2, int r3)
@@ -217,6 +227,19 @@ static __device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.
 static __device__ __forceinline__ void tc_commit(uint32_t bar)
 {
     asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+}
+
+// The same, on the barrier at this offset of every block of the cluster that `mask` names.
+static __device__ __forceinline__ void tc_commit_all(uint32_t bar, uint16_t mask)
+{
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
+                 "h"(mask)
+                 : "memory");
+}
+
+static __device__ __forceinline__ void cluster_sync()
+{
+    asm volatile("barrier.cluster.arrive.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
 }
 
 // Instruction descriptor of kind::f16: fp32 accumulators, A and B both bf16

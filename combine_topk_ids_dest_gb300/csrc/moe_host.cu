@@ -254,7 +254,7 @@ ep_status ep_router_create(const ep_router_config *cfg, ep_router **out)
     r->device = dev;
     r->sms = sms;
     st = encode_map(&r->mw, "weight", cfg->dtype == EP_DTYPE_FP16, cfg->weight, cfg->hidden, cfg->num_experts, 0,
-                    cfg->hidden, 0, moe::kChunk, moe::router_columns(cfg->num_experts));
+                    cfg->hidden, 0, moe::kChunk, moe::router_all_columns(cfg->num_experts) / 2);
     if (st == EP_OK)
         st = r->flags.make();
     if (st == EP_OK) {

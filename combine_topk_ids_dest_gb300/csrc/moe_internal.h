@@ -31,9 +31,16 @@ static __host__ __device__ inline int router_columns(int E)
     return one <= 256 ? one : ((E + 1) / 2 + 15) & ~15;
 }
 
+// Columns of the router's accumulator.
+static __host__ __device__ inline int router_all_columns(int E)
+{
+    const int one = router_columns(E);
+    return E > one ? 2 * one : one;
+}
+
 struct RouterArgs {
     CUtensorMap mx;  // x [T, H], boxes 64 x rows (many tokens)
-    CUtensorMap mw;  // weight [E, H], boxes 64 x router_columns(E)
+    CUtensorMap mw;  // weight [E, H], boxes 64 x half of the accumulator's columns
     const void *x, *weight;
     const float *bias;
     long long x_stride;

@@ -294,66 +294,74 @@ struct Shared {
     int abort, issued;
 };
 
+// How a tile's experts are bucketed: a pick then looks through one bucket
+// only. Groups are the buckets where there are 2 to 16 of them.
+struct Buckets {
+    int n, size;
+    bool groups;
+};
+
+static __device__ __forceinline__ Buckets buckets_of(const RouterArgs &a)
+{
+    const bool groups = a.groups > 1 && a.groups <= kBuckets;
+    return {groups ? a.groups : kBuckets, groups ? a.E / a.groups : (a.E + kBuckets - 1) / kBuckets, groups};
+}
+
+// The two largest choice values of experts [e0, e1) of a token (score[e * 128]).
+static __device__ __forceinline__ void two_largest(const float *score, const float *bias, int e0, int e1, float &b1, float &b2)
+{
+    b1 = b2 = -INFINITY;
+#pragma unroll 4
+    for (int e = e0; e < e1; ++e) {
+        const float c = score[e * 128] + bias[e];
+        const float v = c > -INFINITY ? c : -INFINITY;  // NaN is never chosen
+        b2 = fmaxf(b2, fminf(b1, v));
+        b1 = fmaxf(b1, v);
+    }
+}
+
+// The groups that take part, as a bit set, from their values[g * 128].
+static __device__ unsigned best_groups(const RouterArgs &a, const float *values)
+{
+    unsigned keep = 0;
+    for (int k = 0; k < a.top_groups; ++k) {
+        int best = -1;
+        float most = 0.0f;
+        for (int g = 0; g < a.groups; ++g) {
+            const float v = values[g * 128];
+            if (!((keep >> g) & 1) && (best < 0 || v > most)) {
+                best = g;
+                most = v;
+            }
+        }
+        keep |= 1u << best;
+    }
+    return keep;
+}
+
+static __device__ __forceinline__ float group_value(float b1, float b2, int per)
+{
+    const float v = per == 1 ? b1 : b1 + b2;
+    return v > -INFINITY ? v : -INFINITY;  // infinities of both signs
+}
+
 // One thread: the choice of one token. score[e * 128] is expert e's score (its
-// logit where the rank goes by logits). Experts are kept in 16 buckets of which
-// the thread holds the largest values, so a pick looks through one bucket only.
-static __device__ void choose_thread(const RouterArgs &a, int t, float *score, const float *bias, float top, float sum)
+// logit where the rank goes by logits), most[b * 128] bucket b's largest value
+// and value[b * 128] a group's.
+static __device__ void choose_thread(const RouterArgs &a, int t, float *score, const float *most_of, const float *values,
+                                     const float *bias, float top, float sum)
 {
     const bool by_logit = ranks_by_logit(a);
-    const int E = a.E, size = (E + kBuckets - 1) / kBuckets;
-    auto value = [&](int e) { return a.bias ? score[e * 128] + bias[e] : score[e * 128]; };
-    if (a.groups > 1) {
-        const int per = E / a.groups;
-        float v[2];  // group values are formed again for each pick: few groups, and no array of them
-        unsigned keep = 0;
-        auto group_value = [&](int g) {
-            float b1 = -INFINITY, b2 = -INFINITY;
-            for (int e = g * per; e < (g + 1) * per; ++e) {
-                const float c = value(e);
-                if (c > b1) {
-                    b2 = b1;
-                    b1 = c;
-                } else if (c > b2) {
-                    b2 = c;
-                }
-            }
-            const float v = per == 1 ? b1 : b1 + b2;
-            return v > -INFINITY ? v : -INFINITY;  // infinities of both signs
-        };
-        // values go to the space behind the scores
-        float *const values = score + static_cast<size_t>(E) * 128;
-        for (int g = 0; g < a.groups; ++g)
-            values[g * 128] = group_value(g);
-        for (int k = 0; k < a.top_groups; ++k) {
-            int best = -1;
-            v[0] = 0.0f;
-            for (int g = 0; g < a.groups; ++g) {
-                v[1] = values[g * 128];
-                if (!((keep >> g) & 1) && (best < 0 || v[1] > v[0])) {
-                    best = g;
-                    v[0] = v[1];
-                }
-            }
-            keep |= 1u << best;
-        }
-        for (int g = 0; g < a.groups; ++g)
-            if (!((keep >> g) & 1))
-                for (int e = g * per; e < (g + 1) * per; ++e)
-                    score[e * 128] = __uint_as_float(0x7FC00000u);  // NaN is never chosen
-    }
+    const Buckets bk = buckets_of(a);
+    const unsigned keep = bk.groups ? best_groups(a, values) : ~0u;
     float most[kBuckets];
 #pragma unroll
-    for (int b = 0; b < kBuckets; ++b) {
-        most[b] = -INFINITY;
-        for (int e = b * size; e < min((b + 1) * size, E); ++e) {
-            const float c = value(e);
-            most[b] = c > most[b] ? c : most[b];
-        }
-    }
-    float w[EP_MAX_TOP_K > 8 ? 8 : EP_MAX_TOP_K], total = 0.0f;  // the first eight weights stay in registers
+    for (int b = 0; b < kBuckets; ++b)
+        most[b] = b < bk.n && ((keep >> b) & 1) ? most_of[b * 128] : -INFINITY;
     const size_t at = static_cast<size_t>(t) * a.K;
+    float w[8], total = 0.0f;  // the first eight weights stay in registers
     int n = 0;
-    auto pick = [&](float &weight) {
+    for (; n < a.K; ++n) {
         float best = -INFINITY;
         int b = -1;
 #pragma unroll
@@ -363,59 +371,48 @@ static __device__ void choose_thread(const RouterArgs &a, int t, float *score, c
                 b = i;
             }
         if (b < 0)
-            return -1;
+            break;  // nothing left to choose
         float rest = -INFINITY;
         int id = -1;
-        for (int e = b * size; e < min((b + 1) * size, E); ++e) {
-            const float c = value(e);
-            if (id < 0 && c == best)
-                id = e;
-            else if (c > rest)
-                rest = c;
+        const int end = min((b + 1) * bk.size, a.E);
+#pragma unroll 4
+        for (int e = b * bk.size; e < end; ++e) {
+            const float c = score[e * 128] + bias[e];
+            const bool hit = id < 0 && c == best;
+            id = hit ? e : id;
+            rest = !hit && c > rest ? c : rest;
         }
-        weight = by_logit ? expf(score[id * 128] - top) / sum : score[id * 128];
-        score[id * 128] = __uint_as_float(0x7FC00000u);
+        const float s = score[id * 128], weight = by_logit ? expf(s - top) / sum : s;
+        score[id * 128] = __uint_as_float(0x7FC00000u);  // NaN is never chosen
 #pragma unroll
         for (int i = 0; i < kBuckets; ++i)
-            if (i == b)
-                most[i] = rest;
-        return id;
-    };
-    (void)at;
-    for (; n < a.K; ++n) {
-        float weight = 0.0f;
-        const int id = pick(weight);
-        if (id < 0)
-            break;
+            most[i] = i == b ? rest : most[i];
         total += weight;
-        if (n < 8) {
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-                if (i == n)
-                    w[i] = weight;
-        }
-        // unscaled for now where a sum has still to come
-        if (EP_IN_BOUNDS(a.chk, epk::kSiteMoeIds, a.ids + at + n, 4, a.ids, 4LL * a.T * a.K))
-            a.ids[at + n] = id;
-        if ((n >= 8 || !a.renormalize) &&
-            EP_IN_BOUNDS(a.chk, epk::kSiteMoeWeights, a.weights + at + n, 4, a.weights, 4LL * a.T * a.K))
-            a.weights[at + n] = a.renormalize ? weight : weight * a.scale;
-    }
-    if (a.renormalize) {
 #pragma unroll
         for (int i = 0; i < 8; ++i)
-            if (i < n && EP_IN_BOUNDS(a.chk, epk::kSiteMoeWeights, a.weights + at + i, 4, a.weights, 4LL * a.T * a.K))
-                a.weights[at + i] = w[i] / total * a.scale;
-        for (int i = 8; i < n; ++i)
-            if (EP_IN_BOUNDS(a.chk, epk::kSiteMoeWeights, a.weights + at + i, 4, a.weights, 4LL * a.T * a.K))
-                a.weights[at + i] = a.weights[at + i] / total * a.scale;
+            w[i] = i == n ? weight : w[i];
+        if (EP_IN_BOUNDS(a.chk, epk::kSiteMoeIds, a.ids + at + n, 4, a.ids, 4LL * a.T * a.K))
+            a.ids[at + n] = id;
+        if (n >= 8 && EP_IN_BOUNDS(a.chk, epk::kSiteMoeWeights, a.weights + at + n, 4, a.weights, 4LL * a.T * a.K))
+            a.weights[at + n] = weight;
     }
+    if (!a.renormalize)
+        total = 1.0f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        if (i < n && EP_IN_BOUNDS(a.chk, epk::kSiteMoeWeights, a.weights + at + i, 4, a.weights, 4LL * a.T * a.K))
+            a.weights[at + i] = w[i] / total * a.scale;
+    for (int i = 8; i < n; ++i)
+        if (EP_IN_BOUNDS(a.chk, epk::kSiteMoeWeights, a.weights + at + i, 4, a.weights, 4LL * a.T * a.K))
+            a.weights[at + i] = a.weights[at + i] / total * a.scale;
     for (; n < a.K; ++n)
         store_choice(a, t, n, EP_INVALID_EXPERT_ID, 0.0f);
 }
 
-// grid (token tiles, input splits). Dynamic shared memory: the ring, used again
-// for scores [E + groups][128] and the bias.
+// grid (token tiles, input splits). Without splits two blocks make a cluster:
+// each brings half of the weight's rows of a chunk to both. Dynamic shared
+// memory: the ring, used again for scores [E][128], 32 rows of bucket and group
+// values, and the bias.
 template <int N, bool BF16>
 __global__ void __launch_bounds__(kThreads, 1) many_kernel(const __grid_constant__ RouterArgs a)
 {
@@ -427,18 +424,20 @@ __global__ void __launch_bounds__(kThreads, 1) many_kernel(const __grid_constant
     const int tid = threadIdx.x, warp = __shfl_sync(~0u, tid >> 5, 0), lane = tid & 31;
     const int tile = blockIdx.x, split = blockIdx.y, splits = gridDim.y;
     const int t0 = tile * a.rows, rows = min(a.rows, a.T - t0);
-    const int half = router_columns(a.E), E16 = a.E > half ? 2 * half : half;  // columns of one MMA, of all
+    const int half = router_columns(a.E), E16 = router_all_columns(a.E);  // columns of one MMA, of all
     const int bytes_x = a.rows * 128, stage = 16384 + E16 * 128;
     const int chunks = (a.H + kChunk - 1) / kChunk;
     const int c0 = static_cast<int>(static_cast<long long>(chunks) * split / splits);
     const int c1 = static_cast<int>(static_cast<long long>(chunks) * (split + 1) / splits);
     volatile int *const abort = &sh.abort;
 
+    const int cluster = splits == 1 ? 2 : 1, rank = splits == 1 ? tile & 1 : 0;
+
     if (tid == 0) {
         sh.abort = sh.issued = 0;
         for (int i = 0; i < kMaxStages; ++i) {
             mbar_init(smem_u32(&sh.full[i]), 1);
-            mbar_init(smem_u32(&sh.empty[i]), 1);
+            mbar_init(smem_u32(&sh.empty[i]), cluster);
         }
         mbar_init(smem_u32(&sh.done), 1);
         mbar_init(smem_u32(&sh.drain), 1);
@@ -450,6 +449,7 @@ __global__ void __launch_bounds__(kThreads, 1) many_kernel(const __grid_constant
         tmem_alloc(smem_u32(&sh.tmem), a.tmem_cols);
     tc_fence_before();
     __syncthreads();
+    cluster_sync();  // no copy reaches a block before its barriers are set
     tc_fence_after();
     const uint32_t tmem = sh.tmem;
     // Up to four accumulators along the inputs, added up in fp32: long sums in one lose twice the last bits.
@@ -464,8 +464,13 @@ __global__ void __launch_bounds__(kThreads, 1) many_kernel(const __grid_constant
             const uint32_t bar = smem_u32(&sh.full[s]), at = ring + s * stage;
             mbar_expect(bar, bytes_x + E16 * 128);
             tma_load_2d(at, &a.mx, bar, c * kChunk, t0);
-            for (int e = 0; e < E16; e += half)
-                tma_load_2d(at + 16384 + e * 128, &a.mw, bar, c * kChunk, e);
+            const int part = E16 / 2;  // the map's box: half of the experts
+            if (cluster == 2) {
+                tma_load_2d_all(at + 16384 + rank * part * 128, &a.mw, bar, c * kChunk, rank * part, 3);
+            } else {
+                tma_load_2d(at + 16384, &a.mw, bar, c * kChunk, 0);
+                tma_load_2d(at + 16384 + part * 128, &a.mw, bar, c * kChunk, part);
+            }
             if (++s == a.stages) {
                 s = 0;
                 parity ^= 1;
@@ -495,7 +500,10 @@ __global__ void __launch_bounds__(kThreads, 1) many_kernel(const __grid_constant
 #pragma unroll
                     for (int q = 0; q < 4; ++q)
                         mma_ss(d + e, da + 2 * q, db + e * 8 + 2 * q, idesc, !first || q > 0);
-                tc_commit(smem_u32(&sh.empty[s]));
+                if (cluster == 2)
+                    tc_commit_all(smem_u32(&sh.empty[s]), 3);
+                else
+                    tc_commit(smem_u32(&sh.empty[s]));
             }
             if (++s == a.stages) {
                 s = 0;
@@ -528,14 +536,17 @@ __global__ void __launch_bounds__(kThreads, 1) many_kernel(const __grid_constant
             }
             tmem_wait_ld();
         };
+        float top = -INFINITY, sum = 0.0f;
         if (run && splits == 1) {
-            for (int e = b0; e < b1; e += 8) {  // every MMA has been read: the ring is free
+            for (int e = b0; e < b1; e += 8) {
                 float v[8];
                 logits(e, v);
 #pragma unroll
                 for (int i = 0; i < 8; ++i)
-                    if (e + i < b1)
-                        scores[(e + i) * 128 + row] = v[i];
+                    if (e + i < b1) {
+                        top = fmaxf(top, v[i]);
+                        scores[(e + i) * 128 + row] = a.scoring == EP_SCORE_SIGMOID ? sigmoid(v[i]) : v[i];
+                    }
             }
         } else if (run) {  // parts: [tile][split][token][E]
             float *const p = a.parts + ((static_cast<size_t>(tile) * splits + split) * 128 + row) * a.E;
@@ -570,19 +581,16 @@ __global__ void __launch_bounds__(kThreads, 1) many_kernel(const __grid_constant
         if (run && splits == 1) {
             for (int e = wtid; e < a.E; e += 256)
                 bias[e] = a.bias ? a.bias[e] : 0.0f;
-            named_sync(1, 256);
-            // scores from logits; for softmax the two threads of a token exchange the largest logit and the sum
-            float *const mine = scores + row, *const xch = bias + a.E + part * 128 + row;
-            const float *const other = bias + a.E + (part ^ 1) * 128 + row;
-            float top = -INFINITY, sum = 0.0f;
-            if (a.scoring == EP_SCORE_SOFTMAX) {
-                for (int e = b0; e < b1; ++e)
-                    top = fmaxf(top, mine[e * 128]);
+            float *const mine = scores + row, *const most = mine + a.E * 128, *const values = most + kBuckets * 128;
+            if (a.scoring == EP_SCORE_SOFTMAX) {  // the two threads of a token exchange the largest logit and the sum
+                float *const xch = bias + a.E + part * 128 + row;
+                const float *const other = bias + a.E + (part ^ 1) * 128 + row;
                 *xch = top;
                 named_sync(1, 256);
                 top = fmaxf(top, *other);
                 named_sync(1, 256);
                 const bool keep = ranks_by_logit(a);
+#pragma unroll 4
                 for (int e = b0; e < b1; ++e) {
                     const float x = expf(mine[e * 128] - top);
                     sum += x;
@@ -592,16 +600,40 @@ __global__ void __launch_bounds__(kThreads, 1) many_kernel(const __grid_constant
                 *xch = sum;
                 named_sync(1, 256);
                 sum = part ? *other + sum : sum + *other;
-                if (!keep)
+                if (!keep) {
+#pragma unroll 4
                     for (int e = b0; e < b1; ++e)
                         mine[e * 128] = mine[e * 128] / sum;
-            } else {
-                for (int e = b0; e < b1; ++e)
-                    mine[e * 128] = sigmoid(mine[e * 128]);
+                }
+            }
+            named_sync(1, 256);
+            const Buckets bk = buckets_of(a);
+            if (a.groups > kBuckets) {  // many small groups: NaN for the experts of those that do not take part
+                const int per = a.E / a.groups;
+                float b1v, b2v;
+                for (int g = part; g < a.groups; g += 2) {
+                    two_largest(mine, bias, g * per, (g + 1) * per, b1v, b2v);
+                    most[g * 128] = group_value(b1v, b2v, per);
+                }
+                named_sync(1, 256);
+                const unsigned kept = best_groups(a, most);
+                named_sync(1, 256);
+                for (int g = part; g < a.groups; g += 2)
+                    if (!((kept >> g) & 1))
+                        for (int e = g * per; e < (g + 1) * per; ++e)
+                            mine[e * 128] = __uint_as_float(0x7FC00000u);
+                named_sync(1, 256);
+            }
+            for (int b = part; b < bk.n; b += 2) {
+                float b1v, b2v;
+                two_largest(mine, bias, b * bk.size, min((b + 1) * bk.size, a.E), b1v, b2v);
+                most[b * 128] = b1v;
+                if (bk.groups)
+                    values[b * 128] = group_value(b1v, b2v, bk.size);
             }
             named_sync(1, 256);
             if (part == 0 && row < rows)
-                choose_thread(a, t0 + row, mine, bias, top, sum);
+                choose_thread(a, t0 + row, mine, most, values, bias, top, sum);
         }
     }
     __syncwarp();
@@ -620,6 +652,7 @@ __global__ void __launch_bounds__(kThreads, 1) many_kernel(const __grid_constant
     }
     if (warp == 1)
         tmem_free(tmem, a.tmem_cols);
+    cluster_sync();  // the other block's copies and arrivals have come
     if (splits > 1 && tid == 0 && add_acq_rel(a.counters + gridDim.x + tile, 1) == splits - 1)
         a.counters[tile] = a.counters[gridDim.x + tile] = 0;  // for the next launch
 }
@@ -700,7 +733,7 @@ template <int N, bool BF16> cudaError_t launch_many_n(RouterArgs a, cudaStream_t
     if (attr != cudaSuccess)
         return attr;
     const ManyPlan p = plan_many(a);
-    const int half = router_columns(a.E), E16 = a.E > half ? 2 * half : half, stage = 16384 + E16 * 128;
+    const int E16 = router_all_columns(a.E), stage = 16384 + E16 * 128;
     a.rows = p.rows;
     a.tmem_cols = 512;
     a.stages = (kSmemMax - 2048 - static_cast<int>(sizeof(Shared))) / stage;
@@ -710,15 +743,21 @@ template <int N, bool BF16> cudaError_t launch_many_n(RouterArgs a, cudaStream_t
     size_t smem = static_cast<size_t>(a.stages) * stage;
     smem = 1024 + (smem > choice ? smem : choice);
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(p.tiles, p.splits);
+    cfg.gridDim = dim3(p.splits == 1 ? (p.tiles + 1) & ~1 : p.tiles, p.splits);
     cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
     cudaLaunchAttribute at[1];
-    at[0].id = cudaLaunchAttributeCooperative;  // the blocks of a tile wait for one another's parts
-    at[0].val.cooperative = 1;
+    if (p.splits > 1) {  // the blocks of a tile wait for one another's parts
+        at[0].id = cudaLaunchAttributeCooperative;
+        at[0].val.cooperative = 1;
+    } else {
+        at[0].id = cudaLaunchAttributeClusterDimension;
+        at[0].val.clusterDim.x = 2;
+        at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+    }
     cfg.attrs = at;
-    cfg.numAttrs = p.splits > 1 ? 1 : 0;
+    cfg.numAttrs = 1;
     return cudaLaunchKernelEx(&cfg, many_kernel<N, BF16>, a);
 }
 
