@@ -50,7 +50,7 @@ EXPORTS = ("ep_is_supported", "ep_workspace_size", "ep_create", "ep_create_with_
 MOE_EXPORTS = ("ep_router_create", "ep_router_workspace_size", "ep_router_run", "ep_router_destroy",
                "ep_experts_workspace_size", "ep_experts_create", "ep_experts_run", "ep_experts_destroy",
                "ep_weight_packed_size", "ep_weight_pack", "ep_linear_workspace_size", "ep_linear_create",
-               "ep_linear_run", "ep_linear_destroy")
+               "ep_linear_run", "ep_linear_destroy", "ep_layer_run")
 EP_MOE_MAX_TOKENS = 64
 EP_MOE_MAX_EXPERTS = 512
 EP_SCORE_SOFTMAX = 0
@@ -216,6 +216,7 @@ def load(build_if_missing: bool = True) -> ctypes.CDLL:
         L.ep_linear_create.argtypes = [ctypes.POINTER(EpLinearConfigC), P, sz, PP]
         L.ep_linear_run.argtypes = [P, i32, P, ll, i32, P, ll, P]
         L.ep_linear_destroy.argtypes = [P]
+        L.ep_layer_run.argtypes = [P, P, P, ll, i32, P, P, P, ll, P]
         for name in MOE_EXPORTS:
             getattr(L, name).restype = i32
         if checked():

@@ -258,7 +258,7 @@ ep_status ep_router_create(const ep_router_config *cfg, ep_router **out)
     if (st == EP_OK)
         st = r->flags.make();
     if (st == EP_OK) {
-        const size_t bytes = moe::router_counters(sms) * sizeof(int);
+        const size_t bytes = moe::router_counters(sms) * sizeof(int) + moe::router_few_parts(router_args(*cfg, sms, 1));
         cudaError_t ce = cudaMalloc(reinterpret_cast<void **>(&r->counters), bytes);
         if (ce == cudaSuccess)
             ce = cudaMemset(r->counters, 0, bytes);
@@ -322,8 +322,10 @@ ep_status ep_router_run(ep_router *r, const void *x, long long x_stride, int num
     if (st != EP_OK)
         return st;
     a.mw = r->mw;
-    a.parts = static_cast<float *>(workspace);
     a.counters = r->counters;
+    // a few tokens' parts are the handle's own, behind the counters
+    a.parts = need ? static_cast<float *>(workspace)
+                   : reinterpret_cast<float *>(r->counters + moe::router_counters(r->sms));
     a.err = r->flags.err;
     unsigned long long *rec = epk::check_record();
     a.chk = epk::check_ctx(rec);
@@ -834,6 +836,27 @@ ep_status ep_experts_run(ep_experts *h, const void *x, long long x_stride, const
         ce = moe::launch_int4(a, false, true, h->base.sms, smem, s);
     }
     return finish(ce, "ep_experts_run", rec, s);
+}
+
+ep_status ep_layer_run(ep_router *r, ep_experts *h, const void *x, long long x_stride, int num_tokens,
+                       int32_t *ids, float *weights, void *out, long long out_stride, void *stream)
+{
+    if (!r || !h)
+        MOE_FAIL("a handle is NULL");
+    if (r->cfg.hidden != h->cfg.hidden || r->cfg.top_k != h->cfg.top_k || r->cfg.dtype != EP_DTYPE_BF16)
+        MOE_FAIL("router (hidden %d, top_k %d, dtype %d) and experts (hidden %d, top_k %d, bf16) differ", r->cfg.hidden,
+                 r->cfg.top_k, static_cast<int>(r->cfg.dtype), h->cfg.hidden, h->cfg.top_k);
+    if (num_tokens < 0 || num_tokens > h->cfg.max_tokens)
+        MOE_FAIL("num_tokens=%d outside [0, max_tokens=%d]", num_tokens, h->cfg.max_tokens);
+    if (num_tokens > 0) {  // nothing is queued unless both calls will be
+        const ep_status st = check_rows("out", out, out_stride, h->cfg.hidden, 2, 1);
+        if (st != EP_OK)
+            return st;
+    }
+    const ep_status st = ep_router_run(r, x, x_stride, num_tokens, ids, weights, nullptr, 0, stream);
+    if (st != EP_OK)
+        return st;
+    return ep_experts_run(h, x, x_stride, ids, weights, num_tokens, out, out_stride, stream);
 }
 
 ep_status ep_experts_destroy(ep_experts *h)

@@ -56,7 +56,8 @@ struct RouterArgs {
 };
 
 size_t router_workspace(const RouterArgs &a);
-int router_counters(int sms);
+int router_counters(int sms);  // words, a multiple of 64
+size_t router_few_parts(const RouterArgs &a);  // bytes of parts for up to kMaxTokens rows
 bool router_many(const RouterArgs &a);  // whether the launch uses mx and mw
 int router_rows(const RouterArgs &a);   // box rows of mx
 cudaError_t launch_router(const RouterArgs &a, cudaStream_t stream);

@@ -26,7 +26,7 @@ namespace moe {
 
 namespace {
 
-constexpr int kFewTokens = 64;
+constexpr int kFewTokens = kMaxTokens;
 constexpr int kSlice = 256;         // tokens of one launch of the kernel for few
 constexpr int kManyExperts = 384;  // a tile's scores fit shared memory; above, the kernel for few
 
@@ -691,7 +691,7 @@ bool router_many(const RouterArgs &a) { return a.T > kFewTokens && a.E <= kManyE
 
 size_t router_workspace(const RouterArgs &a)
 {
-    if (a.T == 0)
+    if (a.T <= kFewTokens)
         return 0;
     if (!router_many(a))
         return static_cast<size_t>(few_splits(a)) * (a.T < kSlice ? a.T : kSlice) * a.E * sizeof(float);
@@ -699,7 +699,9 @@ size_t router_workspace(const RouterArgs &a)
     return p.splits == 1 ? 0 : static_cast<size_t>(p.tiles) * p.splits * a.E * 128 * sizeof(float);
 }
 
-int router_counters(int sms) { return 2 * sms + kSlice; }
+int router_counters(int sms) { return (2 * sms + kSlice + 63) & ~63; }
+
+size_t router_few_parts(const RouterArgs &a) { return static_cast<size_t>(few_splits(a)) * kFewTokens * a.E * sizeof(float); }
 
 
 int router_rows(const RouterArgs &a) { return plan_many(a).rows; }

@@ -47,8 +47,7 @@ class _Handle:
 
     def _open(self, device: torch.device):
         self._L = _lib.load()
-        self.device = device
-        self._index = device.index
+        self.device, self._index = device, device.index  # a tensor's device: it has an index
         self._h = None
 
     def destroy(self) -> None:
@@ -72,10 +71,14 @@ class _Handle:
         """Row count and stride of an operand [rows, cols] whose rows are contiguous."""
         if x.dtype is not dtype or x.get_device() != self._index:
             raise ValueError(f"{name} is {x.dtype} on {x.device}, expected {dtype} on {self.device}")
-        if x.dim() != 2 or x.shape[1] != cols or (x.stride(1) != 1 and cols != 1):
-            raise ValueError(f"{name} must be a [tokens, {cols}] tensor with contiguous rows, got {tuple(x.shape)}")
-        n = x.shape[0]
-        return n, (x.stride(0) if n > 1 else cols)
+        shape = x.shape
+        if len(shape) != 2 or shape[1] != cols:
+            raise ValueError(f"{name} must be a [tokens, {cols}] tensor, got {tuple(shape)}")
+        if x.is_contiguous():
+            return shape[0], cols
+        if x.stride(1) != 1 and cols != 1:
+            raise ValueError(f"{name} must have contiguous rows, got strides {x.stride()}")
+        return shape[0], x.stride(0)
 
     def _out(self, out, n, cols, dtype):
         """`out`, or a new tensor, [n, cols] of dtype, and its row stride."""
@@ -88,10 +91,14 @@ class _Handle:
 
     def _call(self, fn, *args):
         """fn(handle, *args, stream) on the handle's device."""
-        if torch.cuda.current_device() != self._index:
-            with torch.cuda.device(self._index):
-                return check(fn(self._live(), *args, torch.cuda.current_stream().cuda_stream))
-        status = fn(self._live(), *args, torch._C._cuda_getCurrentRawStream(self._index))
+        h, index = self._h, self._index
+        if h is None:
+            self._live()
+        if torch._C._cuda_getDevice() != index:
+            with torch.cuda.device(index):
+                status = fn(h, *args, torch._C._cuda_getCurrentRawStream(index))
+        else:
+            status = fn(h, *args, torch._C._cuda_getCurrentRawStream(index))
         if status:
             check(status)
 
@@ -131,25 +138,29 @@ class EpRouter(_Handle):
         with torch.cuda.device(device):
             check(self._L.ep_router_create(ctypes.byref(cfg), ctypes.byref(h)))
         self._h = h.value
-        self._need = {}  # workspace bytes by row count
+        self._run = self._L.ep_router_run
 
-    def _workspace(self, n: int) -> Tuple[Optional[torch.Tensor], int]:
-        need = self._need.get(n)
-        if need is None:
-            size = ctypes.c_size_t(0)
-            check(self._L.ep_router_workspace_size(self._live(), n, ctypes.byref(size)))
-            need = self._need[n] = size.value
-        return (torch.empty(need, dtype=torch.uint8, device=self.device) if need else None), need
+    def _workspace(self, n: int) -> Optional[torch.Tensor]:
+        """The workspace of a call with more rows than the handle has room for itself."""
+        if n <= _lib.EP_MOE_MAX_TOKENS:
+            return None
+        size = ctypes.c_size_t(0)
+        check(self._L.ep_router_workspace_size(self._live(), n, ctypes.byref(size)))
+        return torch.empty(size.value, dtype=torch.uint8, device=self.device) if size.value else None
 
     def __call__(self, x: torch.Tensor) -> Tuple[torch.Tensor, torch.Tensor]:
         """``x`` [tokens, hidden] -> ids int32 and weights fp32, both [tokens, top_k]."""
         n, stride = self._rows(x, self.hidden, self.dtype)
-        ids = torch.empty((n, self.top_k), dtype=torch.int32, device=x.device)
-        weights = torch.empty((n, self.top_k), dtype=torch.float32, device=x.device)
-        ws, need = self._workspace(n)
-        self._call(self._L.ep_router_run, x.data_ptr(), stride, n, ids.data_ptr(), weights.data_ptr(),
-                   ws.data_ptr() if need else 0, need)
+        ids, weights = self._outputs(n)
+        ws = self._workspace(n)
+        self._call(self._run, x.data_ptr(), stride, n, ids.data_ptr(), weights.data_ptr(),
+                   0 if ws is None else ws.data_ptr(), 0 if ws is None else ws.numel())
         return ids, weights
+
+    def _outputs(self, n: int):
+        shape, device = (n, self.top_k), self.device
+        return (torch.empty(shape, dtype=torch.int32, device=device),
+                torch.empty(shape, dtype=torch.float32, device=device))
 
 
 class Int4Weight:
@@ -228,6 +239,7 @@ class Int4Linear(_Workspace):
         self._packed = weight.pack(1, self.outputs)
         cfg = _lib.EpLinearConfigC(self.inputs, self.outputs, self.max_tokens, weight._c(self._packed))
         self._create(cfg, self._L.ep_linear_workspace_size, self._L.ep_linear_create)
+        self._run = self._L.ep_linear_run
 
     def __call__(self, x: torch.Tensor, out: Optional[torch.Tensor] = None) -> torch.Tensor:
         """``x`` [tokens, inputs] -> [tokens, outputs] (``out`` if given)."""
@@ -236,7 +248,7 @@ class Int4Linear(_Workspace):
             raise ValueError(f"x is {dtype}, expected bfloat16 or float16")
         n, stride = self._rows(x, self.inputs, dtype)
         out, out_stride = self._out(out, n, self.outputs, dtype)
-        self._call(self._L.ep_linear_run, _DTYPES[dtype], x.data_ptr(), stride, n, out.data_ptr(), out_stride)
+        self._call(self._run, _DTYPES[dtype], x.data_ptr(), stride, n, out.data_ptr(), out_stride)
         return out
 
 
@@ -276,6 +288,7 @@ class EpExperts(_Workspace):
             cw = tuple(_lib.EpWeightC(w.data_ptr(), 0, 0, 0) for w in self._w)
         cfg = _lib.EpExpertsConfigC(E, self.first_expert, self.top_k, H, I2 // 2, self.max_tokens, *cw)
         self._create(cfg, self._L.ep_experts_workspace_size, self._L.ep_experts_create)
+        self._run = self._L.ep_experts_run
 
     def __call__(self, x: torch.Tensor, topk_ids: torch.Tensor, topk_weights: torch.Tensor,
                  out: Optional[torch.Tensor] = None) -> torch.Tensor:
@@ -287,7 +300,7 @@ class EpExperts(_Workspace):
                     or not t.is_contiguous():
                 raise ValueError(f"{name} must be a contiguous {dtype} tensor [{n}, {self.top_k}] on {self.device}")
         out, out_stride = self._out(out, n, self.hidden, self.dtype)
-        self._call(self._L.ep_experts_run, x.data_ptr(), stride, topk_ids.data_ptr(), topk_weights.data_ptr(), n,
+        self._call(self._run, x.data_ptr(), stride, topk_ids.data_ptr(), topk_weights.data_ptr(), n,
                    out.data_ptr(), out_stride)
         return out
 
@@ -296,11 +309,19 @@ class EpMoeLayer:
     """A whole MoE layer for a few tokens on one GPU: router, then experts."""
 
     def __init__(self, router: EpRouter, experts: EpExperts):
-        if router.hidden != experts.hidden or router.top_k != experts.top_k or router.dtype is not experts.dtype:
-            raise ValueError("router and experts must have the same hidden size, top_k and dtype")
+        if router.hidden != experts.hidden or router.top_k != experts.top_k or router.dtype is not experts.dtype \
+                or router.device != experts.device:
+            raise ValueError("router and experts must have the same hidden size, top_k, dtype and device")
         self.router, self.experts = router, experts
+        self._run = experts._L.ep_layer_run
 
     def __call__(self, x: torch.Tensor, out: Optional[torch.Tensor] = None):
-        """``x`` [tokens, hidden] -> (y [tokens, hidden], ids, weights)."""
-        ids, weights = self.router(x)
-        return self.experts(x, ids, weights, out), ids, weights
+        """``x`` bf16 [tokens, hidden] -> (y bf16 [tokens, hidden] (``out`` if given), ids int32 and
+        weights fp32 [tokens, top_k])."""
+        router, experts = self.router, self.experts
+        n, stride = router._rows(x, router.hidden, router.dtype)
+        ids, weights = router._outputs(n)
+        out, out_stride = experts._out(out, n, experts.hidden, experts.dtype)
+        router._call(self._run, experts._live(), x.data_ptr(), stride, n, ids.data_ptr(), weights.data_ptr(),
+                     out.data_ptr(), out_stride)
+        return out, ids, weights

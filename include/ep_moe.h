@@ -78,7 +78,7 @@ ep_status ep_router_workspace_size(const ep_router *r, int num_tokens, size_t *b
  * of 8, >= hidden), 16-byte aligned; ids: device int32 and weights: device
  * fp32 [num_tokens, top_k], contiguous. workspace: device, 256-byte aligned,
  * of workspace_bytes >= ep_router_workspace_size (used by this call alone).
- * num_tokens 0 does nothing. */
+ * num_tokens 0 does nothing. Up to EP_MOE_MAX_TOKENS rows need no workspace. */
 ep_status ep_router_run(ep_router *r, const void *x, long long x_stride, int num_tokens, int32_t *ids,
                         float *weights, void *workspace, size_t workspace_bytes, void *stream);
 
@@ -180,6 +180,12 @@ ep_status ep_experts_run(ep_experts *h, const void *x, long long x_stride, const
                          const float *weights, int num_tokens, void *out, long long out_stride, void *stream);
 
 ep_status ep_experts_destroy(ep_experts *h);
+
+/* A whole MoE layer: ep_router_run, then ep_experts_run on its ids and
+ * weights (which are outputs here). Both handles have the same hidden size
+ * and top_k, the router's dtype is bf16; num_tokens <= max_tokens. */
+ep_status ep_layer_run(ep_router *r, ep_experts *h, const void *x, long long x_stride, int num_tokens,
+                       int32_t *ids, float *weights, void *out, long long out_stride, void *stream);
 
 #ifdef __cplusplus
 }
