@@ -35,6 +35,12 @@ static __device__ __forceinline__ bool elect_one()
     return p != 0;
 }
 
+// Programmatic dependent launch: lets the next kernel of the stream start as
+// SMs come free; and waits for the kernel before this one to be complete and
+// its writes to be visible. Both do nothing without the launch attribute.
+static __device__ __forceinline__ void pdl_launch_next() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+static __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
 // ---- mbarriers ----------------------------------------------------------------
 
 static __device__ __forceinline__ void mbar_init(uint32_t bar, uint32_t count)

@@ -20,8 +20,9 @@
 //  - mma.sync adds a group's products in fp32, and s times that sum goes to
 //    the row's fp32 accumulators: no weight is rounded, and a scale costs
 //    one instruction per four sums instead of one per pair of weights;
-//  - the second product's token tile has the high and the low part of h; both
-//    are added to the same sums.
+//  - the second product's token tile has the high and the low part of h, in
+//    columns side by side for up to four tokens, else in two tiles that are
+//    added to the same sums.
 //
 // Why warp-level MMA here: at 4 bits a weight the SM has 366 cycles for a
 // tile. Decoding takes 224 of them on the integer pipe whatever follows;
@@ -42,9 +43,11 @@ constexpr int kWorkers = kGroups * 128;
 // then a warpgroup for results and one of which two warps bring weights and tokens
 constexpr int kResults = 128;
 constexpr int kThreads = kWorkers + kResults + 128;
+constexpr int kCopyWarp = (kWorkers + kResults) / 32;  // brings weights; the next one tokens
 constexpr int kMaxStagesA = 12;
 constexpr int kMaxStagesB = 16;
 constexpr int kCap = 32;                   // tokens of an entry: 4 column blocks of 8
+constexpr int kSideBySide = 4;             // up to so many tokens have both parts of h in one column block
 constexpr int kSumStride = kTileRows + 4;  // column stride of the groups' sums: fragments' stores hit all banks
 
 struct Shared {
@@ -54,7 +57,7 @@ struct Shared {
     int abort;
     int active, nmax;
     int issued_a, issued_b[2];
-    int reset;
+    int reset, last;
     int3 totals[kMaxLocal / 32];
     Rests rests[2];
 };
@@ -159,9 +162,11 @@ __global__ void __launch_bounds__(kThreads, 1) int4_kernel(const __grid_constant
     const int G = gridDim.x, blk = blockIdx.x;
     volatile int *const abort = &sh.abort;
 
-    if (tid < kMaxStagesA) {
-        mbar_init(smem_u32(&sh.full_a[tid]), 1);
-        mbar_init(smem_u32(&sh.empty_a[tid]), 8);
+    // The weights' warp sets up its own barriers: in the linear layer, whose weights and share need no list and no
+    // earlier kernel, it starts before the block has met.
+    if (warp == kCopyWarp && lane < kMaxStagesA) {
+        mbar_init(smem_u32(&sh.full_a[lane]), 1);
+        mbar_init(smem_u32(&sh.empty_a[lane]), 8);
     } else if (tid >= 32 && tid < 32 + 2 * kMaxStagesB) {
         mbar_init(smem_u32(&sh.full_b[0][tid - 32]), 1);
         mbar_init(smem_u32(&sh.empty_b[0][tid - 32]), 8);
@@ -172,21 +177,13 @@ __global__ void __launch_bounds__(kThreads, 1) int4_kernel(const __grid_constant
         tma_prefetch_map(&a.mx);
     }
     mbar_init_fence();
-    if (LINEAR) {  // one "expert" whose tokens are the rows of x
-        if (tid == 96) {
-            const int rows = a.box_bytes / 512, half = min(a.T, rows);  // int4_linear_rows
-            sh.active = a.T > rows ? 2 : 1;
-            sh.nmax = rows;
-            li.expert[0] = li.expert[1] = 0;
-            li.offset[0] = 0;
-            li.offset[1] = static_cast<unsigned short>(half);
-            li.offset[sh.active] = static_cast<unsigned short>(a.T);
-        }
-    } else {
+    if (!LINEAR) {
         build_lists(a, li, sh, tid, kThreads, kCap);
+        __syncthreads();
     }
-    __syncthreads();
-    const int A = sh.active;
+    // the linear layer: one "expert" whose tokens are the rows of x, or two with half of them each
+    const int rows = a.box_bytes / 512;  // int4_linear_rows
+    const int A = LINEAR ? (a.T > rows ? 2 : 1) : sh.active, nmax = LINEAR ? rows : sh.nmax;
 
     if (A == 0) {
         clear_out(a, blk, G, tid, kThreads);
@@ -199,11 +196,11 @@ __global__ void __launch_bounds__(kThreads, 1) int4_kernel(const __grid_constant
     const Shares shares1(total1, G), shares2(total2, G);
     const int begin1 = shares1.begin(blk), end1 = shares1.begin(blk + 1);
     const int begin2 = LINEAR ? 0 : shares2.begin(blk), end2 = LINEAR ? 0 : shares2.begin(blk + 1);
-    const int pairs = li.offset[A];
+    const int pairs = LINEAR ? a.T : li.offset[A];
     // A unit's token tile, in 8-token steps of 2 KB a chunk: two chunks, or one (and in the second product two
     // chunks in two parts). The second product's ring begins where the first's did, which is empty by then: h
     // is complete when every block is through with the first.
-    const int cols = (sh.nmax + 7) & ~7, stage_b1 = cols * (LINEAR ? 512 : 256), stage_b2 = cols * (LINEAR ? 512 : 1024);
+    const int cols = (nmax + 7) & ~7, stage_b1 = cols * (LINEAR ? 512 : 256), stage_b2 = cols * (LINEAR ? 512 : 1024);
     // With up to 8 tokens every expert's token tile is all of x: a sum's column is the token. Else the tokens are gathered.
     const bool whole = LINEAR || a.T <= 8;
     // the groups' sums take what this launch's largest entry needs; the rings share the rest so that about as many
@@ -217,31 +214,65 @@ __global__ void __launch_bounds__(kThreads, 1) int4_kernel(const __grid_constant
     const uint32_t ring_a = ring_b + stages_b2 * stage_b2;
     const int stages = min(kMaxStagesA, (room - stages_b2 * stage_b2) / a.stage_a);
     const uint8_t *const ring_b_p = dyn + (ring_b - dyn0), *const ring_a_p = dyn + (ring_a - dyn0);
-    // h: per entry and chunk a tile [2 parts][4][tokens][32], tokens a multiple of 8
+    // h: per entry and chunk a tile [2 parts][4][tokens][32], tokens a multiple of 8; or, for up to kSideBySide
+    // tokens, [4][8][32] with the low parts in rows 4 to 7
     const auto h_entry = [&](int i) { return a.h + static_cast<size_t>(li.offset[i] + 7 * i) * a.h_stride; };
 
-    if (warp == (kWorkers + kResults) / 32 && elect_one()) {
+    // tiles of w1: [matrix][row tile][chunk]; gate and up tiles side by side
+    const int tiles1 = LINEAR ? a.kc1 : 2 * a.kc1;
+    const auto w1_tiles = [&](int expert, int m, int k) {
+        return a.w1 + ((static_cast<size_t>(expert) * a.mt1 + m) * tiles1 + 2 * k) * a.tile1;
+    };
+    int ahead = 0;  // weight tiles of the linear layer on their way before the block has met
+    if (LINEAR) {
+        pdl_launch_next();
+        if (warp == kCopyWarp) {
+            __syncwarp();
+            if (elect_one()) {
+                const uint64_t policy = policy_evict_first();
+                for (Walk w(begin1, end1, ku1, a.mt1, false); ahead < stages && w.more(); w.next()) {
+                    const uint8_t *src = w1_tiles(0, w.m, w.k);
+                    for (int k = w.k; ahead < stages && k < w.k + w.len; ++k, ++ahead, src += 2 * a.tile1) {
+                        const uint32_t bar = smem_u32(&sh.full_a[ahead]), bytes = 2 * k + 1 < tiles1 ? 2 * a.tile1 : a.tile1;
+                        mbar_expect(bar, bytes);
+                        bulk_load(ring_a + ahead * a.stage_a, src, bytes, bar, policy);
+                    }
+                }
+            }
+        } else {
+            if (tid == 96) {
+                li.expert[0] = li.expert[1] = 0;
+                li.offset[0] = 0;
+                li.offset[1] = static_cast<unsigned short>(min(a.T, rows));
+                li.offset[A] = static_cast<unsigned short>(a.T);
+            }
+            pdl_wait();  // x, y, the parts and the counters are the earlier kernel's until it is done
+        }
+        __syncthreads();
+    }
+
+    if (warp == kCopyWarp && elect_one()) {
         // ---- weight tiles ----
         const uint64_t policy = policy_evict_first();
         Cursor at;
         int issued = 0;
         bool run = true;
         auto load = [&](const uint8_t *src, uint32_t bytes) {
-            if (!mbar_wait(smem_u32(&sh.empty_a[at.s]), at.parity ^ 1, abort, kWaitEmptyA))
-                return false;
-            const uint32_t bar = smem_u32(&sh.full_a[at.s]);
-            mbar_expect(bar, bytes);
-            bulk_load(ring_a + at.s * a.stage_a, src, bytes, bar, policy);
+            if (issued >= ahead) {
+                if (!mbar_wait(smem_u32(&sh.empty_a[at.s]), at.parity ^ 1, abort, kWaitEmptyA))
+                    return false;
+                const uint32_t bar = smem_u32(&sh.full_a[at.s]);
+                mbar_expect(bar, bytes);
+                bulk_load(ring_a + at.s * a.stage_a, src, bytes, bar, policy);
+            }
             at.next(stages);
             ++issued;
             return true;
         };
-        // tiles: [matrix][row tile][chunk]; gate and up tiles side by side
         for (Walk w(begin1, end1, ku1, a.mt1, false); run && w.more(); w.next()) {
-            const int tiles = LINEAR ? a.kc1 : 2 * a.kc1;
-            const uint8_t *src = a.w1 + ((static_cast<size_t>(li.expert[w.i]) * a.mt1 + w.m) * tiles + 2 * w.k) * a.tile1;
+            const uint8_t *src = w1_tiles(li.expert[w.i], w.m, w.k);
             for (int k = w.k; run && k < w.k + w.len; ++k, src += 2 * a.tile1)
-                run = load(src, 2 * k + 1 < tiles ? 2 * a.tile1 : a.tile1);
+                run = load(src, 2 * k + 1 < tiles1 ? 2 * a.tile1 : a.tile1);
         }
         for (Walk w(begin2, end2, ku2, A, true); run && w.more(); w.next()) {
             const uint8_t *src = a.w2 + ((static_cast<size_t>(li.expert[w.i]) * a.mt2 + w.m) * a.kc2 + 2 * w.k) * a.tile2;
@@ -249,7 +280,7 @@ __global__ void __launch_bounds__(kThreads, 1) int4_kernel(const __grid_constant
                 run = load(src, 2 * k + 1 < a.kc2 ? 2 * a.tile2 : a.tile2);
         }
         sh.issued_a = issued;
-    } else if (warp == (kWorkers + kResults) / 32 + 1 && elect_one()) {
+    } else if (warp == kCopyWarp + 1 && elect_one()) {
         // ---- token tiles ----
         Cursor at;
         int issued = 0;
@@ -291,7 +322,8 @@ __global__ void __launch_bounds__(kThreads, 1) int4_kernel(const __grid_constant
         at = Cursor();
         const uint64_t policy = policy_evict_first();
         for (Walk w(begin2, end2, ku2, A, true); run && w.more(); w.next()) {
-            const uint32_t chunk = ceil_div(li.count(w.i), 8) * 4096;
+            const int n = li.count(w.i);
+            const uint32_t chunk = n <= kSideBySide ? 2048 : ceil_div(n, 8) * 4096;
             const uint8_t *src = reinterpret_cast<const uint8_t *>(h_entry(w.i)) + static_cast<size_t>(2 * w.k) * chunk;
             for (int k = w.k; run && k < w.k + w.len; ++k, src += 2 * chunk) {
                 const uint32_t bytes = 2 * k + 1 < a.kc2 ? 2 * chunk : chunk;
@@ -315,9 +347,11 @@ __global__ void __launch_bounds__(kThreads, 1) int4_kernel(const __grid_constant
 
         // This group's tiles of a run of `units`; its sums go to shared memory. kc: chunks along the inputs,
         // k: the run's first unit there.
-        auto products = [&](auto blocks, auto log_group, auto second, int units, int k, int kc) {
+        auto products = [&](auto blocks, auto log_group, auto planes, int units, int k, int kc) {
+            // planes: 0 for the first product, else the parts of h in a token tile
             constexpr int NT = decltype(blocks)::value, SHIFT = decltype(log_group)::value;
-            constexpr bool SECOND = decltype(second)::value;
+            constexpr int PLANES = decltype(planes)::value ? decltype(planes)::value : 1;
+            constexpr bool SECOND = decltype(planes)::value != 0;
             const bool with_zeros = SECOND ? a.zeros2 : a.zeros1, scale_fp16 = a.scale_fp16;
             float acc[NT][2][4];
 #pragma unroll
@@ -326,7 +360,7 @@ __global__ void __launch_bounds__(kThreads, 1) int4_kernel(const __grid_constant
                 for (int i = 0; i < 8; ++i)
                     acc[nt][i >> 2][i & 3] = 0.0f;
             // rows of 32 inputs and one token are 64 bytes: the second chunk's token tile
-            const int chunk_b = !tile ? 0 : LINEAR ? NT * 8 * 256 : SECOND ? NT * 8 * 512 : 0;
+            const int chunk_b = !tile || (!LINEAR && !SECOND) ? 0 : NT * 8 * 256 * PLANES;
             for (; turn < units; turn += 2) {
                 const uint32_t fa = smem_u32(&sh.full_a[at_a.s]), fb = smem_u32(&sh.full_b[SECOND][at_b.s]);
                 if (!mbar_wait2_warp(fa, at_a.parity, fb, at_b.parity, abort, kWaitFullA, kWaitFullB)) {
@@ -335,7 +369,7 @@ __global__ void __launch_bounds__(kThreads, 1) int4_kernel(const __grid_constant
                     break;
                 }
                 if ((!LINEAR && !SECOND) || 2 * (k + turn) + tile < kc)
-                    add_tile<NT, SHIFT, SECOND ? 2 : 1, BF16>(
+                    add_tile<NT, SHIFT, PLANES, BF16>(
                         acc, ring_a_p + at_a.s * a.stage_a + tile * (SECOND ? a.tile2 : a.tile1), rows32, lane,
                         ring_b_p + at_b.s * (SECOND ? stage_b2 : stage_b1) + chunk_b, with_zeros, scale_fp16);
                 __syncwarp();
@@ -359,31 +393,34 @@ __global__ void __launch_bounds__(kThreads, 1) int4_kernel(const __grid_constant
             if (lane == 0)
                 mbar_arrive(smem_u32(&sh.full_s));
         };
-        auto by_group = [&](auto blocks, auto second, int units, int k, int kc) {
-            const int shift = decltype(second)::value ? a.shift2 : a.shift1;
+        auto by_group = [&](auto blocks, auto planes, int units, int k, int kc) {
+            const int shift = decltype(planes)::value ? a.shift2 : a.shift1;
             if (shift == 0)
-                products(blocks, std::integral_constant<int, 0>{}, second, units, k, kc);
+                products(blocks, std::integral_constant<int, 0>{}, planes, units, k, kc);
             else if (shift == 1)
-                products(blocks, std::integral_constant<int, 1>{}, second, units, k, kc);
+                products(blocks, std::integral_constant<int, 1>{}, planes, units, k, kc);
             else
-                products(blocks, std::integral_constant<int, 2>{}, second, units, k, kc);
+                products(blocks, std::integral_constant<int, 2>{}, planes, units, k, kc);
         };
-        auto run_products = [&](auto second, int n, int units, int k, int kc) {
+        auto run_products = [&](auto planes, int n, int units, int k, int kc) {
             if (n <= 8)
-                by_group(std::integral_constant<int, 1>{}, second, units, k, kc);
+                by_group(std::integral_constant<int, 1>{}, planes, units, k, kc);
             else if (n <= 16)
-                by_group(std::integral_constant<int, 2>{}, second, units, k, kc);
+                by_group(std::integral_constant<int, 2>{}, planes, units, k, kc);
             else if (n <= 24)
-                by_group(std::integral_constant<int, 3>{}, second, units, k, kc);
+                by_group(std::integral_constant<int, 3>{}, planes, units, k, kc);
             else
-                by_group(std::integral_constant<int, 4>{}, second, units, k, kc);
+                by_group(std::integral_constant<int, 4>{}, planes, units, k, kc);
         };
         for (Walk w(begin1, end1, ku1, a.mt1, false); run && w.more(); w.next())
-            run_products(std::false_type{}, LINEAR ? sh.nmax : li.count(w.i), w.len, w.k, a.kc1);
+            run_products(std::integral_constant<int, 0>{}, LINEAR ? nmax : li.count(w.i), w.len, w.k, a.kc1);
         at_b = Cursor();
         at_b.s = turn;
         for (Walk w(begin2, end2, ku2, A, true); !LINEAR && run && w.more(); w.next())
-            run_products(std::true_type{}, li.count(w.i), w.len, w.k, a.kc2);
+            if (li.count(w.i) <= kSideBySide)
+                by_group(std::integral_constant<int, 1>{}, std::integral_constant<int, 1>{}, w.len, w.k, a.kc2);
+            else
+                run_products(std::integral_constant<int, 2>{}, li.count(w.i), w.len, w.k, a.kc2);
     } else if (warp < (kWorkers + kResults) / 32) {
         // ---- results: a thread is a row of a tile ----
         const int row = tid - kWorkers;
@@ -443,9 +480,11 @@ __global__ void __launch_bounds__(kThreads, 1) int4_kernel(const __grid_constant
                     *p = BF16 ? __bfloat16_as_ushort(__float2bfloat16_rn(gate))
                               : __half_as_ushort(__float2half_rn(gate));
             } else {  // rows past the intermediate size have scales of 0: their h is 0, as the token tiles need
-                const int n8 = (li.count(i) + 7) & ~7;
-                __nv_bfloat16 *const p = h_entry(i) + static_cast<size_t>(m) * n8 * 256 + ((row >> 5) * n8 + j) * 32 + (row & 31);
-                split(swiglu(gate, up), p[0], p[n8 * 128]);
+                const int n = li.count(i), n8 = (n + 7) & ~7;
+                const bool side = n <= kSideBySide;
+                __nv_bfloat16 *const p = h_entry(i) + static_cast<size_t>(m) * n8 * (side ? 128 : 256) +
+                                         ((row >> 5) * n8 + j) * 32 + (row & 31);
+                split(swiglu(gate, up), p[0], p[side ? kSideBySide * 32 : n8 * 128]);
             }
         };
         // A run's part: the block's second slot unless it is the first run of its share.
@@ -495,7 +534,26 @@ __global__ void __launch_bounds__(kThreads, 1) int4_kernel(const __grid_constant
             else if (row == 0)
                 sh.rests[0].of[sh.rests[0].n++] = Rest{w.i, w.m};
         }
-        if (run) {
+        if (LINEAR && run) {  // the block whose part of a tile is the last adds them up: no block waits for another
+            named_sync(1, kResults);
+            for (int r = 0; r < sh.rests[0].n; ++r) {
+                const int i = sh.rests[0].of[r].i, m = sh.rests[0].of[r].m, n = li.count(i), tile = i * a.mt1 + m;
+                const Split sp(shares1, tile * ku1, ku1);
+                if (row == 0)
+                    sh.last = add_acq_rel(a.tiles + tile, 1) == sp.parts() - 1;
+                named_sync(1, kResults);
+                for (int j = 0; sh.last && j < n; j += 4) {
+                    float y[4];
+                    sum_parts<4>(a.part + j * kTileRows + row, a.part_floats, sp, n - j, y);
+#pragma unroll
+                    for (int c = 0; c < 4; ++c)
+                        if (j + c < n)
+                            result(i, m, j + c, y[c], 0.0f);
+                }
+                named_sync(1, kResults);
+            }
+        }
+        if (!LINEAR && run) {
             arrive(sh.rests[0], a.tiles, false);
             for (int r = 0; run && r < sh.rests[0].n; ++r) {
                 const int i = sh.rests[0].of[r].i, m = sh.rests[0].of[r].m, n = li.count(i);
@@ -507,13 +565,12 @@ __global__ void __launch_bounds__(kThreads, 1) int4_kernel(const __grid_constant
                 for (int j = lo; run && j < hi; ++j) {
                     float g[1], u[1] = {};
                     sum_parts<1>(a.part + j * kTileRows + row, a.part_floats, sp, 1, g);
-                    if (!LINEAR)
-                        sum_parts<1>(a.part + (n + j) * kTileRows + row, a.part_floats, sp, 1, u);
+                    sum_parts<1>(a.part + (n + j) * kTileRows + row, a.part_floats, sp, 1, u);
                     result(i, m, j, g[0], u[0]);
                 }
                 announced += hi - lo;
             }
-            if (!LINEAR && run && announced > 0)
+            if (run && announced > 0)
                 announce(announced);
         }
 
@@ -542,6 +599,16 @@ __global__ void __launch_bounds__(kThreads, 1) int4_kernel(const __grid_constant
                     for (int i = 0; i < 4; ++i)
                         c[i] = min(j + i, n - 1);
                     sum_all(c, v);
+                    if (n <= kSideBySide) {  // the low parts' columns
+                        float x[4];
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            c[i] += kSideBySide;
+                        sum_all(c, x);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            v[i] += x[i];
+                    }
 #pragma unroll
                     for (int i = 0; i < 4; ++i)
                         if (j + i < n) {  // a token is in one column of an entry
@@ -718,8 +785,13 @@ cudaError_t launch_int4(const Int4Args &a, bool linear, bool bf16, int grid, siz
     cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
     cudaLaunchAttribute at[1];
-    at[0].id = cudaLaunchAttributeCooperative;
-    at[0].val.cooperative = 1;
+    if (linear) {  // weights are fetched while the kernel before is finishing
+        at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        at[0].val.programmaticStreamSerializationAllowed = 1;
+    } else {  // the blocks wait for one another's h
+        at[0].id = cudaLaunchAttributeCooperative;
+        at[0].val.cooperative = 1;
+    }
     cfg.attrs = at;
     cfg.numAttrs = 1;
     return cudaLaunchKernelEx(&cfg, kernels[linear ? (bf16 ? 1 : 2) : 0], a);

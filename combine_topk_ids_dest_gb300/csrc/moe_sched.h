@@ -73,11 +73,8 @@ struct Walk {
 struct Shares {
     int each, more;  // units of a share; the first `more` blocks have one more
 
-    __device__ __forceinline__ Shares(int total, int G)
-    {
-        each = total / G;
-        more = total - each * G;
-    }
+    __device__ __forceinline__ Shares(int total, int G) : Shares(total / G, total, G) {}
+    __device__ __forceinline__ Shares(int each_, int total, int G) : each(each_), more(total - each_ * G) {}
     __device__ __forceinline__ int begin(int b) const { return b * each + min(b, more); }
     __device__ __forceinline__ int owner(int u) const
     {
