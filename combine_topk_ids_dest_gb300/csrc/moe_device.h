@@ -111,21 +111,29 @@ static __device__ __forceinline__ bool mbar_wait_warp(uint32_t bar, uint32_t par
     return __all_sync(~0u, mbar_wait(bar, parity, abort, site));
 }
 
-// Both of two barriers, by a whole converged warp: one vote and one branch
-// where both phases have completed (a branch costs some 25 cycles).
-static __device__ __forceinline__ bool mbar_wait2_warp(uint32_t bar1, uint32_t parity1, uint32_t bar2, uint32_t parity2,
-                                                       volatile int *abort, int site1, int site2)
+// Whether the phases of both of two barriers have completed; this lane's view.
+static __device__ __forceinline__ uint32_t mbar_peek2(uint32_t bar1, uint32_t parity1, uint32_t bar2, uint32_t parity2)
 {
     uint32_t ok;
     asm volatile("{\n\t.reg .pred p, q;\n\t"
-                 "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-                 "mbarrier.try_wait.parity.shared::cta.b64 q, [%3], %4;\n\t"
+                 "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+                 "mbarrier.test_wait.parity.shared::cta.b64 q, [%3], %4;\n\t"
                  "and.pred p, p, q;\n\t"
                  "selp.u32 %0, 1, 0, p;\n\t}"
                  : "=r"(ok)
                  : "r"(bar1), "r"(parity1), "r"(bar2), "r"(parity2)
                  : "memory");
-    if (__all_sync(~0u, ok))
+    return ok;
+}
+
+// Waits for both of two barriers, by a whole converged warp. ready: what
+// mbar_peek2 said of them at some time before, whose answer is at hand by now:
+// then it is one vote and one branch (a branch costs some 25 cycles, a test
+// that has to be waited for some 100).
+static __device__ __forceinline__ bool mbar_wait2_warp(uint32_t ready, uint32_t bar1, uint32_t parity1, uint32_t bar2,
+                                                       uint32_t parity2, volatile int *abort, int site1, int site2)
+{
+    if (__all_sync(~0u, ready))
         return true;
     return __all_sync(~0u, mbar_wait(bar1, parity1, abort, site1) && mbar_wait(bar2, parity2, abort, site2));
 }

@@ -482,7 +482,11 @@ ep_status ep_weight_pack(const ep_int_weight *w, void *packed, size_t bytes, voi
     a.tile_bytes = moe::int4_tile_bytes(w->group, w->zeros != nullptr);
     a.pairs = w->gate_up != 0;
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
-    const cudaError_t ce = moe::launch_pack(a, s);
+    cudaError_t ce = moe::launch_pack(a, s);
+    // A linear layer reads its weights while the kernel before it is finishing; what it waits for in full is
+    // anything but a kernel.
+    if (ce == cudaSuccess)
+        ce = cudaLaunchHostFunc(s, [](void *) {}, nullptr);
     return ce == cudaSuccess ? set_error(EP_OK, "") : cuda_error(ce, "ep_weight_pack");
 }
 

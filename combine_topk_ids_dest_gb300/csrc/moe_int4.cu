@@ -81,10 +81,12 @@ template <bool BF16> static __device__ __forceinline__ void decode(uint32_t w, u
 
 // Adds one weight tile times NT * 8 tokens (in PLANES parts) to the sums of
 // this warp's 32 rows: acc[column block][16-row half][fragment]. SHIFT:
-// log2(group / 32). tile: the tile in shared memory; tokens: [PLANES][4][NT * 8][32] 16-bit.
-template <int NT, int SHIFT, int PLANES, bool BF16>
+// log2(group / 32). tile: the tile in shared memory; tokens: [PLANES][4][NT * 8][32] 16-bit. meanwhile() is
+// called where its loads' latency is hidden.
+template <int NT, int SHIFT, int PLANES, bool BF16, class Meanwhile>
 static __device__ __forceinline__ void add_tile(float (&acc)[NT][2][4], const uint8_t *tile, int rows32, int lane,
-                                                const uint8_t *tokens, bool with_zeros, bool scale_fp16)
+                                                const uint8_t *tokens, bool with_zeros, bool scale_fp16,
+                                                Meanwhile meanwhile)
 {
     constexpr int kQ = 1 << SHIFT;  // 32-input steps of a group
     // From three column blocks on, a group's sum is scaled in steps of 32 inputs: it then needs registers for one
@@ -121,6 +123,8 @@ static __device__ __forceinline__ void add_tile(float (&acc)[NT][2][4], const ui
         decode<BF16>(w.w, z[2], z[3], f[3]);
         if (q < 3)
             w = codes[(q + 1) * 32];
+        else
+            meanwhile();
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
             float(&d)[2][4] = c[kSteps ? 0 : nt];
@@ -341,6 +345,7 @@ __global__ void __launch_bounds__(kThreads, 1) int4_kernel(const __grid_constant
         Cursor at_a, at_b;         // of this group's next unit
         int turn = grp >> 1;       // units until then
         at_a.s = at_b.s = turn;
+        uint32_t ready = 0;        // whether that unit has landed
         bool run = true;
         constexpr uint32_t empty_a = offsetof(Shared, empty_a) - offsetof(Shared, full_a);
         constexpr uint32_t empty_b = offsetof(Shared, empty_b) - offsetof(Shared, full_b);
@@ -363,19 +368,25 @@ __global__ void __launch_bounds__(kThreads, 1) int4_kernel(const __grid_constant
             const int chunk_b = !tile || (!LINEAR && !SECOND) ? 0 : NT * 8 * 256 * PLANES;
             for (; turn < units; turn += 2) {
                 const uint32_t fa = smem_u32(&sh.full_a[at_a.s]), fb = smem_u32(&sh.full_b[SECOND][at_b.s]);
-                if (!mbar_wait2_warp(fa, at_a.parity, fb, at_b.parity, abort, kWaitFullA, kWaitFullB)) {
+                if (!mbar_wait2_warp(ready, fa, at_a.parity, fb, at_b.parity, abort, kWaitFullA, kWaitFullB)) {
                     run = false;
                     turn = units;
                     break;
                 }
-                if ((!LINEAR && !SECOND) || 2 * (k + turn) + tile < kc)
-                    add_tile<NT, SHIFT, PLANES, BF16>(
-                        acc, ring_a_p + at_a.s * a.stage_a + tile * (SECOND ? a.tile2 : a.tile1), rows32, lane,
-                        ring_b_p + at_b.s * (SECOND ? stage_b2 : stage_b1) + chunk_b, with_zeros, scale_fp16);
-                __syncwarp();
-                mbar_arrive2_if(lane == 0, fa + empty_a, fb + empty_b);
+                const uint8_t *const at = ring_a_p + at_a.s * a.stage_a + tile * (SECOND ? a.tile2 : a.tile1);
+                const uint8_t *const tok = ring_b_p + at_b.s * (SECOND ? stage_b2 : stage_b1) + chunk_b;
                 at_a.advance(2, stages);  // the group's next unit
                 at_b.advance(2, SECOND ? stages_b2 : stages_b1);
+                auto peek = [&] {
+                    ready = mbar_peek2(smem_u32(&sh.full_a[at_a.s]), at_a.parity, smem_u32(&sh.full_b[SECOND][at_b.s]),
+                                       at_b.parity);
+                };
+                if ((!LINEAR && !SECOND) || 2 * (k + turn) + tile < kc)
+                    add_tile<NT, SHIFT, PLANES, BF16>(acc, at, rows32, lane, tok, with_zeros, scale_fp16, peek);
+                else
+                    peek();
+                __syncwarp();
+                mbar_arrive2_if(lane == 0, fa + empty_a, fb + empty_b);
             }
             turn -= units;
             // the sums of the run before have been read
@@ -416,6 +427,7 @@ __global__ void __launch_bounds__(kThreads, 1) int4_kernel(const __grid_constant
             run_products(std::integral_constant<int, 0>{}, LINEAR ? nmax : li.count(w.i), w.len, w.k, a.kc1);
         at_b = Cursor();
         at_b.s = turn;
+        ready = 0;
         for (Walk w(begin2, end2, ku2, A, true); !LINEAR && run && w.more(); w.next())
             if (li.count(w.i) <= kSideBySide)
                 by_group(std::integral_constant<int, 1>{}, std::integral_constant<int, 1>{}, w.len, w.k, a.kc2);

@@ -116,7 +116,11 @@ ep_status ep_weight_packed_size(const ep_int_weight *w, size_t *bytes);
 /* Packs w into packed: device, 128-byte aligned, of at least
  * ep_weight_packed_size bytes. w is not needed once the queued work has run.
  * gate_up of experts is packed as 2*experts matrices of `intermediate` rows,
- * with the gate_up field set. */
+ * with the gate_up field set. The queued work ends with a host function, so
+ * that what follows on the stream starts after it in full: ep_linear_run reads
+ * its weight before the kernel queued before it has ended. Packed bytes that
+ * come from elsewhere are put in place by a copy, not by a kernel right before
+ * the call. */
 ep_status ep_weight_pack(const ep_int_weight *w, void *packed, size_t bytes, void *stream);
 
 /* ---- linear ----------------------------------------------------------------------
