@@ -78,7 +78,7 @@ static __device__ __forceinline__ bool mbar_try(uint32_t bar, uint32_t parity)
 // Which wait gave up first in a block (the abort flag's value).
 enum WaitSite { kWaitEmptyA = 1, kWaitEmptyB, kWaitEmptyD, kWaitFullA, kWaitFullB, kWaitFullD, kWaitDone, kWaitOther };
 
-static __device__ __noinline__ bool mbar_wait_slow(uint32_t bar, uint32_t parity, volatile int *abort, int site)
+static __device__ __forceinline__ bool mbar_wait_slow(uint32_t bar, uint32_t parity, volatile int *abort, int site)
 {
     const long long t0 = clock64();
     for (;;) {

@@ -40,9 +40,9 @@ namespace {
 
 constexpr int kGroups = 4;                 // groups of four warps that multiply
 constexpr int kWorkers = kGroups * 128;
-// then a warpgroup for results and one of which two warps bring weights and tokens
+// then a warpgroup for results and two warps that bring weights and tokens
 constexpr int kResults = 128;
-constexpr int kThreads = kWorkers + kResults + 128;
+constexpr int kThreads = kWorkers + kResults + 64;
 constexpr int kCopyWarp = (kWorkers + kResults) / 32;  // brings weights; the next one tokens
 constexpr int kMaxStagesA = 12;
 constexpr int kMaxStagesB = 16;
@@ -60,7 +60,18 @@ struct Shared {
     int reset, last;
     int3 totals[kMaxLocal / 32];
     Rests rests[2];
+    int cut[4];  // this block's shares: where the first and the second product's begin and end
+    // what run_tiles needs; offsets are from the dynamic shared memory's start
+    uint32_t ring_a, ring_b, sums;
+    int stages, stage_a, stages_b[2], stage_b[2], tile[2], zeros[2], cols, scale_fp16;
 };
+
+__shared__ Shared sh;
+extern __shared__ uint8_t dyn[];
+
+// Cost of a unit of an entry with this many column blocks: measured 16, 21, 29
+// and 38 for one to four (0.54 to 1.26 us; 128 inputs a scale).
+constexpr int kUnitCost = 10, kBlockCost = 7;
 
 // Eight codes to the four registers of an A fragment: pair p has its codes at
 // bits 4p and 4p + 16, so a shift and a mask leave a pair; or-ing the exponent
@@ -152,11 +163,104 @@ static __device__ __forceinline__ void add_tile(float (&acc)[NT][2][4], const ui
     }
 }
 
+// Where a worker warp is in the rings, in one word.
+struct Place {
+    Cursor a, b;          // its group's next unit
+    int turn;             // units until then
+    uint32_t ready;       // whether that unit has landed
+    uint32_t run_parity;  // of empty_s
+    bool run;
+
+    __device__ __forceinline__ explicit Place(uint32_t w)
+        : turn(w >> 12 & 1), ready(w >> 13 & 1), run_parity(w >> 14 & 1), run(w >> 15)
+    {
+        a.s = w & 31;
+        a.parity = w >> 5 & 1;
+        b.s = w >> 6 & 31;
+        b.parity = w >> 11 & 1;
+    }
+    __device__ __forceinline__ uint32_t word() const
+    {
+        return a.s | a.parity << 5 | b.s << 6 | b.parity << 11 | turn << 12 | ready << 13 | run_parity << 14 |
+               uint32_t(run) << 15;
+    }
+    // Before the first unit of a product: group pairs take the units in turn. The weights' ring goes on.
+    static __device__ __forceinline__ uint32_t first(int turn) { return turn | turn << 6 | turn << 12 | 1 << 14 | 1 << 15; }
+    static __device__ __forceinline__ uint32_t second(uint32_t w)
+    {
+        return (w & ~(63u << 6) & ~(1u << 13)) | (w >> 12 & 1) << 6;
+    }
+};
+
+// A worker warp's tiles of a run of `units`, of which its group has one in the
+// first `valid`; its sums go to shared memory. PLANES: 0 for the first product
+// (PAIR: the unit is a gate and an up tile with one token tile), else the parts
+// of h in a token tile of the second. Not inlined: among thirty of them and the
+// rest of the kernel the compiler kept some fifteen of the loop's values in
+// memory, each time round.
+template <int NT, int SHIFT, int PLANES, bool PAIR, bool BF16>
+static __device__ __noinline__ uint32_t run_tiles(uint32_t word, int units, int valid)
+{
+    constexpr bool SECOND = PLANES != 0;
+    constexpr uint32_t empty_a = offsetof(Shared, empty_a) - offsetof(Shared, full_a);
+    constexpr uint32_t empty_b = offsetof(Shared, empty_b) - offsetof(Shared, full_b);
+    Place at(word);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, grp = warp >> 2, rows32 = warp & 3, tile = grp & 1;
+    const int stages = sh.stages, stages_b = sh.stages_b[SECOND], stage_a = sh.stage_a, stage_b = sh.stage_b[SECOND];
+    const uint8_t *const ring_a = dyn + sh.ring_a + tile * sh.tile[SECOND];
+    // rows of 32 inputs and one token are 64 bytes: the second chunk's token tile
+    const uint8_t *const ring_b = dyn + sh.ring_b + (PAIR ? 0 : tile * NT * 8 * 256 * (SECOND ? PLANES : 1));
+    const bool with_zeros = sh.zeros[SECOND], scale_fp16 = sh.scale_fp16;
+    volatile int *const abort = &sh.abort;
+    float acc[NT][2][4];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            acc[nt][i >> 2][i & 3] = 0.0f;
+    int turn = at.turn;
+    for (; turn < units; turn += 2) {
+        const uint32_t fa = smem_u32(&sh.full_a[at.a.s]), fb = smem_u32(&sh.full_b[SECOND][at.b.s]);
+        if (!mbar_wait2_warp(at.ready, fa, at.a.parity, fb, at.b.parity, abort, kWaitFullA, kWaitFullB)) {
+            at.run = false;
+            return at.word();
+        }
+        const uint8_t *const weights = ring_a + at.a.s * stage_a, *const tokens = ring_b + at.b.s * stage_b;
+        at.a.advance(2, stages);  // the group's next unit
+        at.b.advance(2, stages_b);
+        auto peek = [&] {
+            at.ready = mbar_peek2(smem_u32(&sh.full_a[at.a.s]), at.a.parity, smem_u32(&sh.full_b[SECOND][at.b.s]),
+                                  at.b.parity);
+        };
+        if (PAIR || turn < valid)
+            add_tile<NT, SHIFT, SECOND ? PLANES : 1, BF16>(acc, weights, rows32, lane, tokens, with_zeros, scale_fp16, peek);
+        else
+            peek();
+        __syncwarp();
+        mbar_arrive2_if(lane == 0, fa + empty_a, fb + empty_b);
+    }
+    at.turn = turn - units;
+    // the sums of the run before have been read
+    at.run = mbar_wait_warp(smem_u32(&sh.empty_s), at.run_parity, abort, kWaitEmptyD);
+    at.run_parity ^= 1;
+    if (at.run) {
+        float *const mine = reinterpret_cast<float *>(dyn + sh.sums) + (grp * sh.cols + (lane & 3) * 2) * kSumStride +
+                            rows32 * 32 + (lane >> 2);
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                mine[(nt * 8 + (i & 1)) * kSumStride + (i >> 1) * 8] = acc[nt][i >> 2][i & 3];
+        __syncwarp();
+        if (lane == 0)
+            mbar_arrive(smem_u32(&sh.full_s));
+    }
+    return at.word();
+}
+
 template <bool LINEAR, bool BF16>
 __global__ void __launch_bounds__(kThreads, 1) int4_kernel(const __grid_constant__ Int4Args a)
 {
-    extern __shared__ uint8_t dyn[];
-    __shared__ Shared sh;
     const uint32_t dyn0 = smem_u32(dyn), base = (dyn0 + 127u) & ~127u;
     // dynamic shared memory: y's accumulators, lists, the groups' sums, the rings
     float *const acc_y = reinterpret_cast<float *>(dyn + (base - dyn0));  // [T][128], of the second product
@@ -196,10 +300,32 @@ __global__ void __launch_bounds__(kThreads, 1) int4_kernel(const __grid_constant
 
     // units along the inputs; the last one of an odd number of chunks is half empty
     const int ku1 = LINEAR ? (a.kc1 + 1) / 2 : a.kc1, ku2 = (a.kc2 + 1) / 2;
-    const int total1 = A * a.mt1 * ku1, total2 = LINEAR ? 0 : A * a.mt2 * ku2;
-    const Shares shares1(total1, G), shares2(total2, G);
-    const int begin1 = shares1.begin(blk), end1 = shares1.begin(blk + 1);
-    const int begin2 = LINEAR ? 0 : shares2.begin(blk), end2 = LINEAR ? 0 : shares2.begin(blk + 1);
+    const int total1 = A * a.mt1 * ku1;
+    // Costs: of a unit of entry i, of a unit of every entry before it
+    const auto cost = [&](int i) { return kUnitCost + kBlockCost * (li.blocks[i + 1] - li.blocks[i]); };
+    const auto costs = [&](int i) { return static_cast<uint32_t>(kUnitCost * i + kBlockCost * li.blocks[i]); };
+    const Shares shares(total1, G);  // of the linear layer, whose units are alike
+    const uint32_t units1 = a.mt1 * ku1, units2 = ku2;  // of an entry, or of one in a row tile
+    const auto cost_shares = [&](bool second) {
+        return CostShares(costs(A) * (second ? a.mt2 * units2 : units1), kUnitCost + kBlockCost * ((nmax + 7) / 8), G);
+    };
+    if (!LINEAR && warp < 4) {  // a warp finds one end of a share
+        const bool second = warp & 2;
+        const int b = blk + (warp & 1);
+        const uint32_t units = second ? units2 : units1;
+        if (nmax <= 8) {  // all units cost the same
+            sh.cut[warp] = CostShares(A * units * (second ? a.mt2 : 1), 1, G).begin(b);
+        } else {
+            const uint32_t all = units * costs(A), place = cost_shares(second).begin(b), outer = place / all;
+            const uint32_t rest = place - outer * all;
+            int i = 0;  // entries that begin there or before
+#pragma unroll 1
+            for (int k = lane; k < A; k += 32)
+                i += rest >= units * costs(k) ? 1 : 0;
+            i = __reduce_add_sync(~0u, i) - 1;
+            sh.cut[warp] = (outer * A + i) * units + (rest - units * costs(i) + cost(i) - 1) / cost(i);
+        }
+    }
     const int pairs = LINEAR ? a.T : li.offset[A];
     // A unit's token tile, in 8-token steps of 2 KB a chunk: two chunks, or one (and in the second product two
     // chunks in two parts). The second product's ring begins where the first's did, which is empty by then: h
@@ -217,10 +343,30 @@ __global__ void __launch_bounds__(kThreads, 1) int4_kernel(const __grid_constant
     const int stages_b1 = min(kMaxStagesB, stages_b2 * stage_b2 / stage_b1);
     const uint32_t ring_a = ring_b + stages_b2 * stage_b2;
     const int stages = min(kMaxStagesA, (room - stages_b2 * stage_b2) / a.stage_a);
-    const uint8_t *const ring_b_p = dyn + (ring_b - dyn0), *const ring_a_p = dyn + (ring_a - dyn0);
+    if (tid == kThreads - 1) {
+        sh.ring_a = ring_a - dyn0;
+        sh.ring_b = ring_b - dyn0;
+        sh.sums = sums_at - dyn0;
+        sh.stages = stages;
+        sh.stage_a = a.stage_a;
+        sh.stages_b[0] = stages_b1;
+        sh.stages_b[1] = stages_b2;
+        sh.stage_b[0] = stage_b1;
+        sh.stage_b[1] = stage_b2;
+        sh.tile[0] = a.tile1;
+        sh.tile[1] = a.tile2;
+        sh.zeros[0] = a.zeros1;
+        sh.zeros[1] = a.zeros2;
+        sh.cols = cols;
+        sh.scale_fp16 = a.scale_fp16;
+    }
+    if (!LINEAR)
+        __syncthreads();
+    const int begin1 = LINEAR ? shares.begin(blk) : sh.cut[0], end1 = LINEAR ? shares.begin(blk + 1) : sh.cut[1];
+    const int begin2 = LINEAR ? 0 : sh.cut[2], end2 = LINEAR ? 0 : sh.cut[3];
     // h: per entry and chunk a tile [2 parts][4][tokens][32], tokens a multiple of 8; or, for up to kSideBySide
     // tokens, [4][8][32] with the low parts in rows 4 to 7
-    const auto h_entry = [&](int i) { return a.h + static_cast<size_t>(li.offset[i] + 7 * i) * a.h_stride; };
+    const auto h_entry = [&](int i) { return a.h + static_cast<size_t>(li.blocks[i] * 8) * a.h_stride; };
 
     // tiles of w1: [matrix][row tile][chunk]; gate and up tiles side by side
     const int tiles1 = LINEAR ? a.kc1 : 2 * a.kc1;
@@ -339,79 +485,19 @@ __global__ void __launch_bounds__(kThreads, 1) int4_kernel(const __grid_constant
         sh.issued_b[1] = issued;
     } else if (warp < kWorkers / 32) {
         // ---- products ----
-        const int grp = warp >> 2, rows32 = warp & 3;
-        uint32_t run_parity = 1;  // of empty_s
-        const int tile = grp & 1;  // of a unit
-        Cursor at_a, at_b;         // of this group's next unit
-        int turn = grp >> 1;       // units until then
-        at_a.s = at_b.s = turn;
-        uint32_t ready = 0;        // whether that unit has landed
-        bool run = true;
-        constexpr uint32_t empty_a = offsetof(Shared, empty_a) - offsetof(Shared, full_a);
-        constexpr uint32_t empty_b = offsetof(Shared, empty_b) - offsetof(Shared, full_b);
-
-        // This group's tiles of a run of `units`; its sums go to shared memory. kc: chunks along the inputs,
-        // k: the run's first unit there.
-        auto products = [&](auto blocks, auto log_group, auto planes, int units, int k, int kc) {
-            // planes: 0 for the first product, else the parts of h in a token tile
-            constexpr int NT = decltype(blocks)::value, SHIFT = decltype(log_group)::value;
-            constexpr int PLANES = decltype(planes)::value ? decltype(planes)::value : 1;
-            constexpr bool SECOND = decltype(planes)::value != 0;
-            const bool with_zeros = SECOND ? a.zeros2 : a.zeros1, scale_fp16 = a.scale_fp16;
-            float acc[NT][2][4];
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    acc[nt][i >> 2][i & 3] = 0.0f;
-            // rows of 32 inputs and one token are 64 bytes: the second chunk's token tile
-            const int chunk_b = !tile || (!LINEAR && !SECOND) ? 0 : NT * 8 * 256 * PLANES;
-            for (; turn < units; turn += 2) {
-                const uint32_t fa = smem_u32(&sh.full_a[at_a.s]), fb = smem_u32(&sh.full_b[SECOND][at_b.s]);
-                if (!mbar_wait2_warp(ready, fa, at_a.parity, fb, at_b.parity, abort, kWaitFullA, kWaitFullB)) {
-                    run = false;
-                    turn = units;
-                    break;
-                }
-                const uint8_t *const at = ring_a_p + at_a.s * a.stage_a + tile * (SECOND ? a.tile2 : a.tile1);
-                const uint8_t *const tok = ring_b_p + at_b.s * (SECOND ? stage_b2 : stage_b1) + chunk_b;
-                at_a.advance(2, stages);  // the group's next unit
-                at_b.advance(2, SECOND ? stages_b2 : stages_b1);
-                auto peek = [&] {
-                    ready = mbar_peek2(smem_u32(&sh.full_a[at_a.s]), at_a.parity, smem_u32(&sh.full_b[SECOND][at_b.s]),
-                                       at_b.parity);
-                };
-                if ((!LINEAR && !SECOND) || 2 * (k + turn) + tile < kc)
-                    add_tile<NT, SHIFT, PLANES, BF16>(acc, at, rows32, lane, tok, with_zeros, scale_fp16, peek);
-                else
-                    peek();
-                __syncwarp();
-                mbar_arrive2_if(lane == 0, fa + empty_a, fb + empty_b);
-            }
-            turn -= units;
-            // the sums of the run before have been read
-            run = run && mbar_wait_warp(smem_u32(&sh.empty_s), run_parity, abort, kWaitEmptyD);
-            run_parity ^= 1;
-            if (!run)
-                return;
-            float *const mine = sums + (grp * cols + (lane & 3) * 2) * kSumStride + rows32 * 32 + (lane >> 2);
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    mine[(nt * 8 + (i & 1)) * kSumStride + (i >> 1) * 8] = acc[nt][i >> 2][i & 3];
-            __syncwarp();
-            if (lane == 0)
-                mbar_arrive(smem_u32(&sh.full_s));
-        };
+        const int tile = warp >> 2 & 1;  // of a unit
+        uint32_t at = Place::first(warp >> 3);
+        // A run of `units` from unit k on, kc chunks along the inputs.
         auto by_group = [&](auto blocks, auto planes, int units, int k, int kc) {
-            const int shift = decltype(planes)::value ? a.shift2 : a.shift1;
+            constexpr int NT = decltype(blocks)::value, PLANES = decltype(planes)::value;
+            constexpr bool PAIR = !LINEAR && PLANES == 0;
+            const int shift = PLANES ? a.shift2 : a.shift1, valid = (kc - tile + 1) / 2 - k;
             if (shift == 0)
-                products(blocks, std::integral_constant<int, 0>{}, planes, units, k, kc);
+                at = run_tiles<NT, 0, PLANES, PAIR, BF16>(at, units, valid);
             else if (shift == 1)
-                products(blocks, std::integral_constant<int, 1>{}, planes, units, k, kc);
+                at = run_tiles<NT, 1, PLANES, PAIR, BF16>(at, units, valid);
             else
-                products(blocks, std::integral_constant<int, 2>{}, planes, units, k, kc);
+                at = run_tiles<NT, 2, PLANES, PAIR, BF16>(at, units, valid);
         };
         auto run_products = [&](auto planes, int n, int units, int k, int kc) {
             if (n <= 8)
@@ -423,16 +509,16 @@ __global__ void __launch_bounds__(kThreads, 1) int4_kernel(const __grid_constant
             else
                 by_group(std::integral_constant<int, 4>{}, planes, units, k, kc);
         };
-        for (Walk w(begin1, end1, ku1, a.mt1, false); run && w.more(); w.next())
+        for (Walk w(begin1, end1, ku1, a.mt1, false); Place(at).run && w.more(); w.next())
             run_products(std::integral_constant<int, 0>{}, LINEAR ? nmax : li.count(w.i), w.len, w.k, a.kc1);
-        at_b = Cursor();
-        at_b.s = turn;
-        ready = 0;
-        for (Walk w(begin2, end2, ku2, A, true); !LINEAR && run && w.more(); w.next())
-            if (li.count(w.i) <= kSideBySide)
-                by_group(std::integral_constant<int, 1>{}, std::integral_constant<int, 1>{}, w.len, w.k, a.kc2);
-            else
-                run_products(std::integral_constant<int, 2>{}, li.count(w.i), w.len, w.k, a.kc2);
+        if constexpr (!LINEAR) {
+            at = Place::second(at);
+            for (Walk w(begin2, end2, ku2, A, true); Place(at).run && w.more(); w.next())
+                if (li.count(w.i) <= kSideBySide)
+                    by_group(std::integral_constant<int, 1>{}, std::integral_constant<int, 1>{}, w.len, w.k, a.kc2);
+                else
+                    run_products(std::integral_constant<int, 2>{}, li.count(w.i), w.len, w.k, a.kc2);
+        }
     } else if (warp < (kWorkers + kResults) / 32) {
         // ---- results: a thread is a row of a tile ----
         const int row = tid - kWorkers;
@@ -550,7 +636,7 @@ __global__ void __launch_bounds__(kThreads, 1) int4_kernel(const __grid_constant
             named_sync(1, kResults);
             for (int r = 0; r < sh.rests[0].n; ++r) {
                 const int i = sh.rests[0].of[r].i, m = sh.rests[0].of[r].m, n = li.count(i), tile = i * a.mt1 + m;
-                const Split sp(shares1, tile * ku1, ku1);
+                const Split sp(shares, tile * ku1, ku1);
                 if (row == 0)
                     sh.last = add_acq_rel(a.tiles + tile, 1) == sp.parts() - 1;
                 named_sync(1, kResults);
@@ -569,7 +655,8 @@ __global__ void __launch_bounds__(kThreads, 1) int4_kernel(const __grid_constant
             arrive(sh.rests[0], a.tiles, false);
             for (int r = 0; run && r < sh.rests[0].n; ++r) {
                 const int i = sh.rests[0].of[r].i, m = sh.rests[0].of[r].m, n = li.count(i);
-                const Split sp(shares1, (i * a.mt1 + m) * ku1, ku1);
+                const uint32_t first = costs(i) * units1 + m * ku1 * cost(i);
+                const Split sp(cost_shares(false), first, first + (ku1 - 1) * cost(i), first - cost(m > 0 || i == 0 ? i : i - 1));
                 const int lo = sp.column(n, blk), hi = sp.column(n, blk + 1);
                 if (lo == hi)
                     continue;
@@ -649,7 +736,8 @@ __global__ void __launch_bounds__(kThreads, 1) int4_kernel(const __grid_constant
             arrive(sh.rests[1], counters, true);
             for (int r = 0; run && r < sh.rests[1].n; ++r) {
                 const int m = sh.rests[1].of[r].m;
-                const Split sp(shares2, m * group, group);
+                const uint32_t one = costs(A) * units2, first = one * m;
+                const Split sp(cost_shares(true), first, first + one - cost(A - 1), first - cost(A - 1));
                 const int lo = sp.column(a.T, blk), hi = sp.column(a.T, blk + 1);
                 if (lo == hi)
                     continue;

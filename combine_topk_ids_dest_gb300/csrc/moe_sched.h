@@ -83,6 +83,34 @@ struct Shares {
     }
 };
 
+// The same for units of different costs: block b has the units whose place, the
+// cost of all before them, is in [b, b + 1) times total / blocks. No share is
+// empty if that is at least the largest cost of a unit. Places fit 32 bits:
+// weights that a GPU's memory holds are far fewer units.
+struct CostShares {
+    uint32_t total, each, more;
+    int blocks;
+
+    // blocks: as many as have a share, G at most
+    __device__ __forceinline__ CostShares(uint32_t total_, uint32_t largest, int G)
+        : total(total_), blocks(static_cast<int>(min(static_cast<uint32_t>(G), total_ / largest)))
+    {
+        each = total / blocks;
+        more = total - each * blocks;
+    }
+    __device__ __forceinline__ uint32_t begin(int b) const
+    {
+        return b >= blocks ? total : each * b + (more * b + blocks - 1) / blocks;
+    }
+    __device__ __forceinline__ int owner(uint32_t place) const
+    {
+        int b = min(static_cast<int>(place / each), blocks - 1);  // or one of the few before it
+        while (begin(b) > place)
+            --b;
+        return b;
+    }
+};
+
 // A tile that blocks b0..b1 share: each keeps its part in one of two slots,
 // the second if the tile begins after the block's share does.
 struct Split {
@@ -97,6 +125,12 @@ struct Split {
     __device__ __forceinline__ bool shared() const { return b0 != b1; }
     __device__ __forceinline__ int parts() const { return b1 - b0 + 1; }
     __device__ __forceinline__ int slot(int b) const { return b == b0 ? slot0 : 2 * b; }
+    // As above where units' costs differ: the costs before the tile's first and last unit and before the unit that
+    // precedes it.
+    __device__ __forceinline__ Split(const CostShares &s, uint32_t first, uint32_t last, uint32_t before)
+        : b0(s.owner(first)), b1(s.owner(last)), slot0(2 * b0 + (first > 0 && before >= s.begin(b0) ? 1 : 0))
+    {
+    }
     // Of n columns, the first that block b adds up (b == b1 + 1: n).
     __device__ __forceinline__ int column(int n, int b) const { return n * (b - b0) / parts(); }
 };
@@ -157,6 +191,7 @@ struct Lists {
     float *given;              // [P] the call's weights
     unsigned short *expert;    // [2 E] of each entry, ascending
     unsigned short *offset;    // [2 E + 1] the entry's first pair
+    unsigned short *blocks;    // [2 E + 1] column blocks of 8 tokens before the entry
     unsigned short *start;     // [E] each active expert's first pair
     short *id;                 // [P] the call's ids, local
     unsigned char *token;      // [P] tokens, ascending per expert
@@ -168,14 +203,15 @@ struct Lists {
         given = weight + P;
         expert = reinterpret_cast<unsigned short *>(given + P);
         offset = expert + 2 * E;
-        start = offset + 2 * E + 1;
+        blocks = offset + 2 * E + 1;
+        start = blocks + 2 * E + 1;
         id = reinterpret_cast<short *>(start + E);
         token = reinterpret_cast<unsigned char *>(id + P);
     }
     __device__ __forceinline__ int count(int i) const { return offset[i + 1] - offset[i]; }
 };
 
-static inline size_t lists_bytes(int E, int P) { return size_t(E) * 18 + size_t(P) * 11 + 2; }
+static inline size_t lists_bytes(int E, int P) { return size_t(E) * 22 + size_t(P) * 11 + 4; }
 
 // Builds the lists; every block does, from the ids themselves, with one trip
 // to memory and four barriers. A token's bit in its expert's mask makes the
@@ -186,7 +222,7 @@ template <class Args, class Shared>
 static __device__ __forceinline__ void build_lists(const Args &a, const Lists &li, Shared &sh, int tid, int threads,
                                                    int cap)
 {
-    const int warp = tid >> 5, lane = tid & 31, blocks = (a.E + 31) / 32;
+    const int warp = tid >> 5, lane = tid & 31, batches = (a.E + 31) / 32;
     for (int i = tid; i < a.P; i += threads) {
         int e = -1;
         float w = 0.0f;
@@ -204,44 +240,54 @@ static __device__ __forceinline__ void build_lists(const Args &a, const Lists &l
         if (li.id[i] >= 0)
             atomicOr(&li.mask[li.id[i]], 1ULL << (i / a.K));
     __syncthreads();
-    // 32 experts to a warp: counts of entries and pairs before each expert, first within the 32
-    for (int b = warp; b < blocks; b += threads / 32) {
+    // 32 experts to a warp: entries, pairs and column blocks before each expert, first within the 32. Pairs are in the
+    // low and blocks in the high half of a word.
+    const auto counts = [&](int n) {
+        const int n1 = n > cap ? (n + 1) / 2 : n;
+        return n | ((n1 + 7) / 8 + (n - n1 + 7) / 8) << 16;
+    };
+    for (int b = warp; b < batches; b += threads / 32) {
         const int e = b * 32 + lane, n = e < a.E ? __popcll(li.mask[e]) : 0;
         const unsigned live = __ballot_sync(~0u, n > 0), two = __ballot_sync(~0u, n > cap);
-        const int pairs = __reduce_add_sync(~0u, n), most = __reduce_max_sync(~0u, n > cap ? (n + 1) / 2 : n);
+        const int sum = __reduce_add_sync(~0u, counts(n)), most = __reduce_max_sync(~0u, n > cap ? (n + 1) / 2 : n);
         if (lane == 0)
-            sh.totals[b] = make_int3(__popc(live) + __popc(two), pairs, most);
+            sh.totals[b] = make_int3(__popc(live) + __popc(two), sum, most);
     }
     __syncthreads();
-    for (int b = warp; b < blocks; b += threads / 32) {
-        int entries = 0, pairs = 0, most = 0;
+    for (int b = warp; b < batches; b += threads / 32) {
+        int entries = 0, sums = 0, most = 0;
         for (int c = 0; c < b; ++c) {
             entries += sh.totals[c].x;
-            pairs += sh.totals[c].y;
+            sums += sh.totals[c].y;
             most = max(most, sh.totals[c].z);
         }
         const int e = b * 32 + lane, n = e < a.E ? __popcll(li.mask[e]) : 0;
         const unsigned live = __ballot_sync(~0u, n > 0), two = __ballot_sync(~0u, n > cap), before = (1u << lane) - 1;
         if (live) {
-            int sum = n;  // inclusive prefix sum over the lanes
+            int sum = counts(n);  // inclusive prefix sum over the lanes
             for (int d = 1; d < 32; d <<= 1) {
                 const int v = __shfl_up_sync(~0u, sum, d);
                 if (lane >= d)
                     sum += v;
             }
             if (n > 0) {
-                const int at = entries + __popc(live & before) + __popc(two & before), off = pairs + sum - n;
+                const int at = entries + __popc(live & before) + __popc(two & before), to = sums + sum - counts(n);
+                const int off = to & 0xFFFF, blk = to >> 16;
                 li.expert[at] = static_cast<unsigned short>(e);
                 li.offset[at] = li.start[e] = static_cast<unsigned short>(off);
+                li.blocks[at] = static_cast<unsigned short>(blk);
                 if (n > cap) {
                     li.expert[at + 1] = static_cast<unsigned short>(e);
                     li.offset[at + 1] = static_cast<unsigned short>(off + (n + 1) / 2);
+                    li.blocks[at + 1] = static_cast<unsigned short>(blk + ((n + 1) / 2 + 7) / 8);
                 }
             }
         }
-        if (b == blocks - 1 && lane == 0) {
+        if (b == batches - 1 && lane == 0) {
             entries += sh.totals[b].x;
-            li.offset[entries] = static_cast<unsigned short>(pairs + sh.totals[b].y);
+            sums += sh.totals[b].y;
+            li.offset[entries] = static_cast<unsigned short>(sums & 0xFFFF);
+            li.blocks[entries] = static_cast<unsigned short>(sums >> 16);
             sh.active = entries;
             sh.nmax = max(most, sh.totals[b].z);
         }
