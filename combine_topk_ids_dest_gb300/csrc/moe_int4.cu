@@ -661,11 +661,13 @@ __global__ void __launch_bounds__(kThreads, 1) int4_kernel(const __grid_constant
                 if (lo == hi)
                     continue;
                 run = parts_written(a.tiles + i * a.mt1 + m, sp);
-                for (int j = lo; run && j < hi; ++j) {
-                    float g[1], u[1] = {};
-                    sum_parts<1>(a.part + j * kTileRows + row, a.part_floats, sp, 1, g);
-                    sum_parts<1>(a.part + (n + j) * kTileRows + row, a.part_floats, sp, 1, u);
-                    result(i, m, j, g[0], u[0]);
+                for (int j = lo; run && j < hi; j += 4) {
+                    float v[8];  // gate, up
+                    sum_parts<8>(a.part + j * kTileRows + row, a.part_floats, sp, hi - j, v, n * kTileRows);
+#pragma unroll
+                    for (int c = 0; c < 4; ++c)
+                        if (j + c < hi)
+                            result(i, m, j + c, v[c], v[4 + c]);
                 }
                 announced += hi - lo;
             }
@@ -742,10 +744,13 @@ __global__ void __launch_bounds__(kThreads, 1) int4_kernel(const __grid_constant
                 if (lo == hi)
                     continue;
                 run = parts_written(counters + m, sp);
-                for (int t = lo; run && t < hi; ++t) {
-                    float x[1];
-                    sum_parts<1>(a.part + t * kTileRows + row, a.part_floats, sp, 1, x);
-                    store_y(m, t, x[0]);
+                for (int t = lo; run && t < hi; t += 4) {
+                    float y[4];
+                    sum_parts<4>(a.part + t * kTileRows + row, a.part_floats, sp, hi - t, y);
+#pragma unroll
+                    for (int c = 0; c < 4; ++c)
+                        if (t + c < hi)
+                            store_y(m, t + c, y[c]);
                 }
             }
         }

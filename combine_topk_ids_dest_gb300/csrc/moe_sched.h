@@ -147,26 +147,30 @@ struct Rests {
     Rest of[2];
 };
 
-// Sums v[c] of N values of a shared tile, STEP apart (`cols` of them valid),
-// over the parts in the order of the inputs. `base` is the first value in
-// slot 0. Up to four parts' loads are in flight.
-template <int N, int STEP = kTileRows>
-static __device__ __forceinline__ void sum_parts(const float *base, int part_floats, const Split &sp, int cols, float *v)
+// Sums v[c] of N values of a shared tile over the parts, in the order of the
+// inputs: four columns, of which the first `cols` are there (the rest are 0),
+// or twice four, `second` values apart. `base` is the first value in slot 0. Four parts'
+// loads are in flight, or two.
+template <int N>
+static __device__ __forceinline__ void sum_parts(const float *base, int part_floats, const Split &sp, int cols, float *v,
+                                                 int second = 0)
 {
+    static_assert(N == 4 || N == 8, "");
+    constexpr int kFlight = N > 4 ? 2 : 4;
 #pragma unroll
     for (int c = 0; c < N; ++c)
-        v[c] = c < cols ? __ldcg(base + static_cast<size_t>(sp.slot0) * part_floats + c * STEP) : 0.0f;
-    for (int b = sp.b0 + 1; b <= sp.b1; b += 4) {
-        float x[4][N];
+        v[c] = (c & 3) < cols ? __ldcg(base + static_cast<size_t>(sp.slot0) * part_floats + (c & 3) * kTileRows + (c >> 2) * second) : 0.0f;
+    for (int b = sp.b0 + 1; b <= sp.b1; b += kFlight) {
+        float x[kFlight][N];
 #pragma unroll
-        for (int q = 0; q < 4; ++q)
+        for (int q = 0; q < kFlight; ++q)
 #pragma unroll
             for (int c = 0; c < N; ++c)
-                x[q][c] = b + q <= sp.b1 && c < cols
-                              ? __ldcg(base + static_cast<size_t>(2 * (b + q)) * part_floats + c * STEP)
+                x[q][c] = b + q <= sp.b1 && (c & 3) < cols
+                              ? __ldcg(base + static_cast<size_t>(2 * (b + q)) * part_floats + (c & 3) * kTileRows + (c >> 2) * second)
                               : 0.0f;
 #pragma unroll
-        for (int q = 0; q < 4; ++q)
+        for (int q = 0; q < kFlight; ++q)
 #pragma unroll
             for (int c = 0; c < N; ++c)
                 v[c] += x[q][c];
