@@ -40,10 +40,10 @@ namespace {
 
 constexpr int kGroups = 4;                 // groups of four warps that multiply
 constexpr int kWorkers = kGroups * 128;
-// then a warpgroup for results and two warps that bring weights and tokens
+// then a warpgroup for results, a warp that brings weights and two that bring tokens
 constexpr int kResults = 128;
-constexpr int kThreads = kWorkers + kResults + 64;
-constexpr int kCopyWarp = (kWorkers + kResults) / 32;  // brings weights; the next one tokens
+constexpr int kThreads = kWorkers + kResults + 96;
+constexpr int kCopyWarp = (kWorkers + kResults) / 32;  // brings weights; the next ones tokens
 constexpr int kMaxStagesA = 12;
 constexpr int kMaxStagesB = 16;
 constexpr int kCap = 32;                   // tokens of an entry: 4 column blocks of 8
@@ -56,7 +56,7 @@ struct Shared {
     uint64_t full_s, empty_s;  // the groups' sums of a run
     int abort;
     int active, nmax;
-    int issued_a, issued_b[2];
+    int issued_a, issued_b[2][2];  // of each product by each warp
     int reset, last;
     int3 totals[kMaxLocal / 32];
     Rests rests[2];
@@ -270,18 +270,25 @@ __global__ void __launch_bounds__(kThreads, 1) int4_kernel(const __grid_constant
     const int G = gridDim.x, blk = blockIdx.x;
     volatile int *const abort = &sh.abort;
 
+    // With up to 8 tokens every expert's token tile is all of x: a sum's column is the token. Else the tokens are
+    // gathered, half the inputs by each of two warps: a gather of four rows of 64 bytes costs its thread 85 cycles,
+    // and a unit of an expert with five tokens would take 10 % longer.
+    const bool whole = LINEAR || a.T <= 8;
+
     // The weights' warp sets up its own barriers: in the linear layer, whose weights and share need no list and no
     // earlier kernel, it starts before the block has met.
     if (warp == kCopyWarp && lane < kMaxStagesA) {
         mbar_init(smem_u32(&sh.full_a[lane]), 1);
         mbar_init(smem_u32(&sh.empty_a[lane]), 8);
     } else if (tid >= 32 && tid < 32 + 2 * kMaxStagesB) {
-        mbar_init(smem_u32(&sh.full_b[0][tid - 32]), 1);
+        mbar_init(smem_u32(&sh.full_b[0][tid - 32]), !whole && tid < 32 + kMaxStagesB ? 2 : 1);
         mbar_init(smem_u32(&sh.empty_b[0][tid - 32]), 8);
     } else if (tid == 64) {
         mbar_init(smem_u32(&sh.full_s), kWorkers / 32);
         mbar_init(smem_u32(&sh.empty_s), kResults / 32);
-        sh.abort = sh.reset = sh.rests[0].n = sh.rests[1].n = sh.issued_a = sh.issued_b[0] = sh.issued_b[1] = 0;
+        sh.abort = sh.reset = sh.rests[0].n = sh.rests[1].n = sh.issued_a = 0;
+        for (int i = 0; i < 4; ++i)
+            sh.issued_b[i >> 1][i & 1] = 0;
         tma_prefetch_map(&a.mx);
     }
     mbar_init_fence();
@@ -331,8 +338,6 @@ __global__ void __launch_bounds__(kThreads, 1) int4_kernel(const __grid_constant
     // chunks in two parts). The second product's ring begins where the first's did, which is empty by then: h
     // is complete when every block is through with the first.
     const int cols = (nmax + 7) & ~7, stage_b1 = cols * (LINEAR ? 512 : 256), stage_b2 = cols * (LINEAR ? 512 : 1024);
-    // With up to 8 tokens every expert's token tile is all of x: a sum's column is the token. Else the tokens are gathered.
-    const bool whole = LINEAR || a.T <= 8;
     // the groups' sums take what this launch's largest entry needs; the rings share the rest so that about as many
     // token tiles as weight tiles are on their way
     const uint32_t sums_at = (base + a.fixed_bytes + 127u) & ~127u;
@@ -430,8 +435,9 @@ __global__ void __launch_bounds__(kThreads, 1) int4_kernel(const __grid_constant
                 run = load(src, 2 * k + 1 < a.kc2 ? 2 * a.tile2 : a.tile2);
         }
         sh.issued_a = issued;
-    } else if (warp == kCopyWarp + 1 && elect_one()) {
+    } else if (warp > kCopyWarp && elect_one()) {
         // ---- token tiles ----
+        const int half = warp - kCopyWarp - 1;
         Cursor at;
         int issued = 0;
         bool run = true;
@@ -446,10 +452,10 @@ __global__ void __launch_bounds__(kThreads, 1) int4_kernel(const __grid_constant
             ++issued;
             return true;
         };
-        for (Walk w(begin1, end1, ku1, a.mt1, false); run && w.more(); w.next()) {
+        for (Walk w(begin1, end1, ku1, a.mt1, false); (half == 0 || !whole) && run && w.more(); w.next()) {
             const int n = li.count(w.i), n8 = (n + 7) & ~7, off = li.offset[w.i];
             const unsigned char *const tok = li.token + off;
-            const uint32_t bytes = whole ? a.box_bytes : ((n + 3) & ~3) * 256;
+            const uint32_t bytes = whole ? a.box_bytes : ((n + 3) & ~3) * 128;
             for (int k = w.k; k < w.k + w.len && (run = acquire(0, bytes)); ++k) {
                 if (whole) {  // [inputs / 32][tokens][32]
                     tma_load_box(dst, &a.mx, bar, 0, LINEAR ? off : 0, LINEAR ? 8 * k : 4 * k);
@@ -457,21 +463,21 @@ __global__ void __launch_bounds__(kThreads, 1) int4_kernel(const __grid_constant
                     for (int j = 0; j < n; j += 4) {  // short of a fourth row: the last one again
                         const int r0 = tok[j], r1 = tok[min(j + 1, n - 1)], r2 = tok[min(j + 2, n - 1)],
                                   r3 = tok[min(j + 3, n - 1)];
-                        for (int q = 0; q < 4; ++q)
+                        for (int q = 2 * half; q < 2 * half + 2; ++q)
                             tma_gather4(dst + (q * n8 + j) * 64, &a.mx, bar, k * 128 + q * 32, r0, r1, r2, r3);
                     }
                 }
             }
         }
-        if (run && begin2 < end2) {  // h is complete
+        sh.issued_b[0][half] = issued;
+        if (run && half == 0 && begin2 < end2) {  // h is complete
             run = wait_count(a.done, a.mt1 * pairs, abort, kWaitDone);
             fence_async_proxy();
         }
-        sh.issued_b[0] = issued;
         issued = 0;
         at = Cursor();
         const uint64_t policy = policy_evict_first();
-        for (Walk w(begin2, end2, ku2, A, true); run && w.more(); w.next()) {
+        for (Walk w(begin2, end2, ku2, A, true); half == 0 && run && w.more(); w.next()) {
             const int n = li.count(w.i);
             const uint32_t chunk = n <= kSideBySide ? 2048 : ceil_div(n, 8) * 4096;
             const uint8_t *src = reinterpret_cast<const uint8_t *>(h_entry(w.i)) + static_cast<size_t>(2 * w.k) * chunk;
@@ -482,7 +488,7 @@ __global__ void __launch_bounds__(kThreads, 1) int4_kernel(const __grid_constant
                     bulk_load(dst, src, bytes, bar, policy);
             }
         }
-        sh.issued_b[1] = issued;
+        sh.issued_b[1][half] = issued;
     } else if (warp < kWorkers / 32) {
         // ---- products ----
         const int tile = warp >> 2 & 1;  // of a unit
@@ -763,9 +769,14 @@ __global__ void __launch_bounds__(kThreads, 1) int4_kernel(const __grid_constant
             for (int i = max(0, sh.issued_a - stages); i < sh.issued_a; ++i)
                 mbar_wait(smem_u32(&sh.full_a[i % stages]), (i / stages) & 1, nullptr, kWaitOther);
             for (int product = 0; product < 2; ++product) {
-                const int n = product ? stages_b2 : stages_b1;
-                for (int i = max(0, sh.issued_b[product] - n); i < sh.issued_b[product]; ++i)
-                    mbar_wait(smem_u32(&sh.full_b[product][i % n]), (i / n) & 1, nullptr, kWaitOther);
+                const int n = product ? stages_b2 : stages_b1, i0 = sh.issued_b[product][0], i1 = sh.issued_b[product][1];
+                const int both = product || whole ? max(i0, i1) : min(i0, i1);
+                for (int i = max(0, max(i0, i1) - n); i < max(i0, i1); ++i) {
+                    const uint32_t bar = smem_u32(&sh.full_b[product][i % n]);
+                    if (i >= both)  // for the warp that gave up before
+                        mbar_arrive(bar);
+                    mbar_wait(bar, (i / n) & 1, nullptr, kWaitOther);
+                }
             }
             atomicAdd_system(a.err + sh.abort, 1u);
             __threadfence_system();
