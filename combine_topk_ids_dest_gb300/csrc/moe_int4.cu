@@ -69,9 +69,10 @@ struct Shared {
 __shared__ Shared sh;
 extern __shared__ uint8_t dyn[];
 
-// Cost of a unit of an entry with this many column blocks: measured 16, 21, 29
-// and 38 for one to four (0.54 to 1.26 us; 128 inputs a scale).
-constexpr int kUnitCost = 10, kBlockCost = 7;
+// Cost of a unit of an entry with this many column blocks. Measured for one to
+// four of them 16, 21, 32 and 40 (0.47 to 1.18 us) in the first product, and
+// 18, 29, 45 and 62 in the second, whose blocks share its entries more evenly.
+constexpr int kUnitCost = 9, kBlockCost = 8;
 
 // Eight codes to the four registers of an A fragment: pair p has its codes at
 // bits 4p and 4p + 16, so a shift and a mask leave a pair; or-ing the exponent
