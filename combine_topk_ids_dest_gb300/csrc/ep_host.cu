@@ -950,13 +950,13 @@ ep_status ep_binary_version(int *version)
     if (!version)
         return fail(EP_ERR_INVALID_ARG, "version is NULL");
     *version = 0;
-    int v[24], n = 0;
+    int v[48], n = 0;
     cudaError_t ce = epk::kernel_binary_versions(v, 15, &n);
     if (ce == cudaSuccess && n < 16)
         ce = epk::noalloc_binary_version(&v[n++]);
     if (ce == cudaSuccess) {
         int more = 0;
-        ce = moe::kernel_binary_versions(v + n, 24 - n, &more);
+        ce = moe::kernel_binary_versions(v + n, 48 - n, &more);
         n += more;
     }
     if (ce != cudaSuccess) {

@@ -460,13 +460,6 @@ cudaError_t launch_experts(const ExpertsArgs &a, int grid, size_t smem, cudaStre
     return cudaLaunchKernelEx(&cfg, experts_kernel, a);
 }
 
-cudaError_t experts_binary_version(int *v)
-{
-    cudaFuncAttributes fa;
-    const cudaError_t ce = cudaFuncGetAttributes(&fa, experts_kernel);
-    if (ce == cudaSuccess)
-        *v = fa.binaryVersion;
-    return ce;
-}
+std::vector<const void *> experts_kernels() { return {reinterpret_cast<const void *>(experts_kernel)}; }
 
 }  // namespace moe

@@ -876,16 +876,15 @@ ep_status ep_experts_destroy(ep_experts *h)
 
 cudaError_t moe::kernel_binary_versions(int *out, int max, int *n)
 {
-    cudaError_t (*const fns[])(int *) = {moe::router_binary_version, moe::experts_binary_version,
-                                          moe::int4_binary_version};
     *n = 0;
-    for (auto *f : fns) {
-        int v = 0;
-        const cudaError_t ce = f(&v);
-        if (ce != cudaSuccess)
-            return ce;
-        if (*n < max)
-            out[(*n)++] = v;
-    }
+    for (const auto &list : {moe::router_kernels(), moe::experts_kernels(), moe::int4_kernels()})
+        for (const void *f : list) {
+            cudaFuncAttributes attr;
+            const cudaError_t ce = cudaFuncGetAttributes(&attr, f);
+            if (ce != cudaSuccess)
+                return ce;
+            if (*n < max)
+                out[(*n)++] = attr.binaryVersion;
+        }
     return cudaSuccess;
 }

@@ -921,13 +921,10 @@ cudaError_t launch_pack(const PackArgs &a, cudaStream_t stream)
     return cudaGetLastError();
 }
 
-cudaError_t int4_binary_version(int *v)
+std::vector<const void *> int4_kernels()
 {
-    cudaFuncAttributes fa;
-    const cudaError_t ce = cudaFuncGetAttributes(&fa, int4_kernel<false, true>);
-    if (ce == cudaSuccess)
-        *v = fa.binaryVersion;
-    return ce;
+    return {reinterpret_cast<const void *>(int4_kernel<false, true>), reinterpret_cast<const void *>(int4_kernel<true, true>),
+            reinterpret_cast<const void *>(int4_kernel<true, false>), reinterpret_cast<const void *>(pack_kernel)};
 }
 
 }  // namespace moe

@@ -4,6 +4,7 @@
 
 #include <cstddef>
 #include <cstdint>
+#include <vector>
 
 #include <cuda.h>
 #include <cuda_bf16.h>
@@ -61,7 +62,7 @@ size_t router_few_parts(const RouterArgs &a);  // bytes of parts for up to kMaxT
 bool router_many(const RouterArgs &a);  // whether the launch uses mx and mw
 int router_rows(const RouterArgs &a);   // box rows of mx
 cudaError_t launch_router(const RouterArgs &a, cudaStream_t stream);
-cudaError_t router_binary_version(int *v);
+std::vector<const void *> router_kernels();  // every kernel of the file
 
 // ---- experts with dense bf16 weights (moe_experts.cu) ---------------------------
 
@@ -90,7 +91,7 @@ struct ExpertsArgs {
 };
 
 cudaError_t launch_experts(const ExpertsArgs &a, int grid, size_t smem, cudaStream_t stream);
-cudaError_t experts_binary_version(int *v);
+std::vector<const void *> experts_kernels();  // every kernel of the file
 // Dynamic shared memory of a launch for T tokens; sets stages, bytes_b and part_floats.
 size_t experts_smem(ExpertsArgs *a);
 // Floats of one block's part (two per block) for up to T tokens.
@@ -136,7 +137,7 @@ int int4_linear_rows(int T);  // rows of x one run over the weight takes: T in o
 size_t int4_smem(Int4Args *a, bool linear);
 cudaError_t launch_int4(const Int4Args &a, bool linear, bool bf16, int grid, size_t smem, cudaStream_t stream);
 cudaError_t launch_pack(const PackArgs &a, cudaStream_t stream);
-cudaError_t int4_binary_version(int *v);
+std::vector<const void *> int4_kernels();  // every kernel of the file
 
 // Binary versions of this library's MoE kernels, as epk::kernel_binary_versions.
 cudaError_t kernel_binary_versions(int *out, int max, int *n);

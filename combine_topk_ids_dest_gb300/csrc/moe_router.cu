@@ -790,13 +790,17 @@ cudaError_t launch_router(const RouterArgs &all, cudaStream_t stream)
     return cudaSuccess;
 }
 
-cudaError_t router_binary_version(int *v)
+std::vector<const void *> router_kernels()
 {
-    cudaFuncAttributes fa;
-    cudaError_t ce = cudaFuncGetAttributes(&fa, many_kernel<8, true>);
-    if (ce == cudaSuccess)
-        *v = fa.binaryVersion;
-    return ce;
+#define FEW(NT, BF16)                                                                                   \
+    reinterpret_cast<const void *>(few_kernel<NT, 4, BF16>), reinterpret_cast<const void *>(few_kernel<NT, 8, BF16>), \
+        reinterpret_cast<const void *>(few_kernel<NT, 16, BF16>)
+#define MANY(BF16)                                                                                      \
+    reinterpret_cast<const void *>(many_kernel<4, BF16>), reinterpret_cast<const void *>(many_kernel<8, BF16>),       \
+        reinterpret_cast<const void *>(many_kernel<12, BF16>)
+    return {FEW(1, true), FEW(1, false), FEW(2, true), FEW(2, false), MANY(true), MANY(false)};
+#undef FEW
+#undef MANY
 }
 
 }  // namespace moe

@@ -27,12 +27,6 @@ struct Cursor {
         parity ^= to >= n ? 1 : 0;
         s = to >= n ? to - n : to;
     }
-    // To position i of the sequence.
-    __device__ __forceinline__ void skip(int i, int n)
-    {
-        s = i % n;
-        parity = (i / n) & 1;
-    }
 };
 
 // Walks a block's share [begin, end) of one product's units (chunks of
