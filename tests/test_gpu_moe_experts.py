@@ -57,6 +57,16 @@ def test_every_token_to_one_expert(cuda_device, group, T):
     _check(*_case(T, 320, 192, 4, 1, group, seed=T, ids=ids))
 
 
+@pytest.mark.parametrize("group,H,I", [(0, 640, 1000), (32, 640, 992), (64, 1152, 704), (128, 512, 384), (32, 96, 64)])
+@pytest.mark.parametrize("order", [1, -1])
+def test_experts_of_very_different_sizes(cuda_device, group, H, I, order):
+    sizes = [1, 4, 5, 8, 9, 16, 17, 24, 25, 32, 33, 64][::order]
+    t = torch.arange(64, device="cuda")[:, None]
+    e = torch.arange(len(sizes), device="cuda")[None, :]
+    ids = torch.where((t + 5 * e) % 64 < torch.tensor(sizes, device="cuda"), e, -1).int()
+    _check(*_case(64, H, I, len(sizes), len(sizes), group, seed=H, ids=ids))
+
+
 @pytest.mark.parametrize("group", [0, 32])
 @pytest.mark.parametrize("T", [1, 6, 40])
 def test_absent_doubled_and_foreign_ids(cuda_device, group, T):
