@@ -16,7 +16,16 @@
 //    out. Tiles are as high as one wave of blocks needs, up to 128 tokens.
 //    With too few tiles for the SMs the inputs are split over blocks as well;
 //    parts go through memory and each block of a tile chooses for its share
-//    of the tokens.
+//    of the tokens. Otherwise two blocks share each chunk of the weight, one
+//    half fetched by each and multicast to both.
+//
+// What bounds them: latency for few tokens (one token, 128 experts x 4096: 5.7
+// us in a graph, 10.5 with the host's launch; 128 tokens, 256 experts x 7168,
+// inputs split over 16 blocks: 17 us). 16001 tokens x 7168 to 256 experts take
+// 79 us: 35 us are the bytes' and 31 the MMAs'; shared memory serves both the
+// copies in and the 128 x 256 MMAs' operands, which leaves the tensor pipe at
+// 34 % and DRAM at 40 %, and choosing the experts from the accumulators takes
+// the last 12 us of each block.
 #include <type_traits>
 
 #include "moe_device.h"

@@ -19,10 +19,11 @@
  * calls can be captured. Tensors that a capture or a queued call uses must
  * stay valid until it has run.
  *
- * The experts and linear kernels' blocks wait for one another (they are
- * launched cooperatively) and every wait has a limit of about 2 s. If one runs out
- * the kernel ends, that call's output is undefined, and the handle's next
- * call returns EP_ERR_CUDA once.
+ * The blocks of the experts' kernels, and of the router's where it splits the
+ * inputs, wait for one another (they are launched cooperatively); every wait,
+ * for a copy too, has a limit of about 2 s. If one runs out the kernel ends,
+ * that call's output is undefined, and the handle's next call returns
+ * EP_ERR_CUDA once.
  */
 #ifndef EP_MOE_GB300_H
 #define EP_MOE_GB300_H
