@@ -170,6 +170,15 @@ static __device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorM
                  : "memory");
 }
 
+// Into this block's memory; bar may be the other block's of a pair.
+static __device__ __forceinline__ void tma_load_2d_pair(uint32_t dst, const CUtensorMap *m, uint32_t bar, int x, int y)
+{
+    asm volatile("cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
+                 "[%0], [%1, {%3, %4}], [%2];" ::"r"(dst),
+                 "l"(m), "r"(bar), "r"(x), "r"(y)
+                 : "memory");
+}
+
 static __device__ __forceinline__ void tma_load_box(uint32_t dst, const CUtensorMap *m, uint32_t bar, int x, int y, int z)
 {
     asm volatile("cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
@@ -184,16 +193,6 @@ static __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorM
     asm volatile("cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint "
                  "[%0], [%1, {%3, %4, %5}], [%2], %6;" ::"r"(dst),
                  "l"(m), "r"(bar), "r"(x), "r"(y), "r"(z), "l"(policy)
-                 : "memory");
-}
-
-// The same box into this offset of every block of the cluster that `mask` names.
-static __device__ __forceinline__ void tma_load_2d_all(uint32_t dst, const CUtensorMap *m, uint32_t bar, int x, int y,
-                                                       uint16_t mask)
-{
-    asm volatile("cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.multicast::cluster "
-                 "[%0], [%1, {%3, %4}], [%2], %5;" ::"r"(dst),
-                 "l"(m), "r"(bar), "r"(x), "r"(y), "h"(mask)
                  : "memory");
 }
 
@@ -222,16 +221,25 @@ static __device__ __forceinline__ void fence_async_proxy() { asm volatile("fence
 
 // ---- tcgen05 --------------------------------------------------------------------
 
-static __device__ __forceinline__ void tmem_alloc(uint32_t smem_dst, uint32_t cols)
+// PAIR: for matrix instructions of two neighbouring blocks (cta_group::2); both
+// blocks call it, and all tcgen05 instructions of a kernel are of one kind.
+template <bool PAIR = false> static __device__ __forceinline__ void tmem_alloc(uint32_t smem_dst, uint32_t cols)
 {
-    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_dst), "r"(cols)
-                 : "memory");
-    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    if (PAIR) {
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_dst), "r"(cols) : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+    } else {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_dst), "r"(cols) : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
 }
 
-static __device__ __forceinline__ void tmem_free(uint32_t addr, uint32_t cols)
+template <bool PAIR = false> static __device__ __forceinline__ void tmem_free(uint32_t addr, uint32_t cols)
 {
-    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(addr), "r"(cols) : "memory");
+    if (PAIR)
+        asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(addr), "r"(cols) : "memory");
+    else
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(addr), "r"(cols) : "memory");
 }
 
 static __device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
@@ -243,17 +251,25 @@ static __device__ __forceinline__ void tc_commit(uint32_t bar)
     asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
 }
 
-// The same, on the barrier at this offset of every block of the cluster that `mask` names.
-static __device__ __forceinline__ void tc_commit_all(uint32_t bar, uint16_t mask)
+// The same for the instructions of a pair, on the barrier at this offset of both blocks.
+static __device__ __forceinline__ void tc_commit_pair(uint32_t bar)
 {
-    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
-                 "h"(mask)
+    asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
+                 "h"(static_cast<uint16_t>(3))
                  : "memory");
 }
 
 static __device__ __forceinline__ void cluster_sync()
 {
     asm volatile("barrier.cluster.arrive.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
+}
+
+// The address of this offset in the cluster's first block.
+static __device__ __forceinline__ uint32_t in_first_block(uint32_t at)
+{
+    uint32_t r;
+    asm("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(r) : "r"(at));
+    return r;
 }
 
 // Instruction descriptor of kind::f16: fp32 accumulators, A and B both bf16
@@ -278,6 +294,16 @@ static __device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b
 {
     asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
                  "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+                 "l"(a), "l"(b), "r"(idesc), "r"(uint32_t(add))
+                 : "memory");
+}
+
+// The same by a pair of blocks, issued in the first: 256 rows of A, 128 in each block's memory, and half of B's rows
+// in each (at the same offsets); a block's tensor memory gets the sums of its rows with all of B.
+static __device__ __forceinline__ void mma_ss_pair(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add)
+{
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+                 "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
                  "l"(a), "l"(b), "r"(idesc), "r"(uint32_t(add))
                  : "memory");
 }

@@ -25,11 +25,11 @@ constexpr int kChunk = 64;                  // inputs of a 16-bit chunk: one 128
 // ---- router (moe_router.cu) -------------------------------------------------------
 
 // Experts of one MMA of the router: all, or half of them where there are more
-// than 256, rounded up to a multiple of 16.
+// than 256, rounded up to a multiple of 32.
 static __host__ __device__ inline int router_columns(int E)
 {
-    const int one = (E + 15) & ~15;
-    return one <= 256 ? one : ((E + 1) / 2 + 15) & ~15;
+    const int one = (E + 31) & ~31;
+    return one <= 256 ? one : ((E + 1) / 2 + 31) & ~31;
 }
 
 // Columns of the router's accumulator.

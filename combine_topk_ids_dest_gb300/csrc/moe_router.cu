@@ -418,11 +418,13 @@ static __device__ void choose_thread(const RouterArgs &a, int t, float *score, c
         store_choice(a, t, n, EP_INVALID_EXPERT_ID, 0.0f);
 }
 
-// grid (token tiles, input splits). Without splits two blocks make a cluster:
-// each brings half of the weight's rows of a chunk to both. Dynamic shared
+// grid (token tiles, input splits). Without splits (PAIR) two blocks make a
+// cluster and multiply together: each has its tokens and half of the weight's
+// rows of a chunk in shared memory, so the weight is read once for 256 tokens.
+// The first block issues, and both blocks' copies report to its barriers. Dynamic shared
 // memory: the ring, used again for scores [E][128], 32 rows of bucket and group
 // values, and the bias.
-template <int N, bool BF16>
+template <int N, bool BF16, bool PAIR>
 __global__ void __launch_bounds__(kThreads, 1) many_kernel(const __grid_constant__ RouterArgs a)
 {
     extern __shared__ uint8_t dyn[];
@@ -434,19 +436,19 @@ __global__ void __launch_bounds__(kThreads, 1) many_kernel(const __grid_constant
     const int tile = blockIdx.x, split = blockIdx.y, splits = gridDim.y;
     const int t0 = tile * a.rows, rows = min(a.rows, a.T - t0);
     const int half = router_columns(a.E), E16 = router_all_columns(a.E);  // columns of one MMA, of all
-    const int bytes_x = a.rows * 128, stage = 16384 + E16 * 128;
+    const int bytes_x = a.rows * 128, bytes_w = E16 * (PAIR ? 64 : 128), stage = 16384 + bytes_w;
     const int chunks = (a.H + kChunk - 1) / kChunk;
     const int c0 = static_cast<int>(static_cast<long long>(chunks) * split / splits);
     const int c1 = static_cast<int>(static_cast<long long>(chunks) * (split + 1) / splits);
     volatile int *const abort = &sh.abort;
 
-    const int cluster = splits == 1 ? 2 : 1, rank = splits == 1 ? tile & 1 : 0;
+    const int rank = PAIR ? tile & 1 : 0;
 
     if (tid == 0) {
         sh.abort = sh.issued = 0;
         for (int i = 0; i < kMaxStages; ++i) {
             mbar_init(smem_u32(&sh.full[i]), 1);
-            mbar_init(smem_u32(&sh.empty[i]), cluster);
+            mbar_init(smem_u32(&sh.empty[i]), 1);
         }
         mbar_init(smem_u32(&sh.done), 1);
         mbar_init(smem_u32(&sh.drain), 1);
@@ -455,7 +457,7 @@ __global__ void __launch_bounds__(kThreads, 1) many_kernel(const __grid_constant
         tma_prefetch_map(&a.mw);
     }
     if (warp == 1)
-        tmem_alloc(smem_u32(&sh.tmem), a.tmem_cols);
+        tmem_alloc<PAIR>(smem_u32(&sh.tmem), a.tmem_cols);
     tc_fence_before();
     __syncthreads();
     cluster_sync();  // no copy reaches a block before its barriers are set
@@ -470,13 +472,18 @@ __global__ void __launch_bounds__(kThreads, 1) many_kernel(const __grid_constant
         for (int c = c0; c < c1; ++c, ++it) {
             if (!mbar_wait(smem_u32(&sh.empty[s]), parity ^ 1, abort, kWaitEmptyA))
                 break;
-            const uint32_t bar = smem_u32(&sh.full[s]), at = ring + s * stage;
-            mbar_expect(bar, bytes_x + E16 * 128);
-            tma_load_2d(at, &a.mx, bar, c * kChunk, t0);
+            const uint32_t at = ring + s * stage;
             const int part = E16 / 2;  // the map's box: half of the experts
-            if (cluster == 2) {
-                tma_load_2d_all(at + 16384 + rank * part * 128, &a.mw, bar, c * kChunk, rank * part, 3);
+            if (PAIR) {
+                const uint32_t bar = in_first_block(smem_u32(&sh.full[s]));
+                if (rank == 0)
+                    mbar_expect(smem_u32(&sh.full[s]), 2 * (bytes_x + bytes_w));
+                tma_load_2d_pair(at, &a.mx, bar, c * kChunk, t0);
+                tma_load_2d_pair(at + 16384, &a.mw, bar, c * kChunk, rank * part);
             } else {
+                const uint32_t bar = smem_u32(&sh.full[s]);
+                mbar_expect(bar, bytes_x + bytes_w);
+                tma_load_2d(at, &a.mx, bar, c * kChunk, t0);
                 tma_load_2d(at + 16384, &a.mw, bar, c * kChunk, 0);
                 tma_load_2d(at + 16384 + part * 128, &a.mw, bar, c * kChunk, part);
             }
@@ -489,10 +496,10 @@ __global__ void __launch_bounds__(kThreads, 1) many_kernel(const __grid_constant
     } else if (warp == 1) {
         int s = 0;
         uint32_t parity = 0;
-        const uint32_t idesc = idesc_f16(128, half, BF16);
+        const uint32_t idesc = idesc_f16(PAIR ? 256 : 128, half, BF16);
         int span = 0, next = c0;  // the accumulator in use, and the chunk from which it is another
         uint32_t d = tmem;
-        for (int c = c0; c < c1; ++c) {
+        for (int c = c0; c < c1 && rank == 0; ++c) {
             const bool first = c == next;
             if (first) {
                 d = tmem + span * E16;
@@ -507,10 +514,14 @@ __global__ void __launch_bounds__(kThreads, 1) many_kernel(const __grid_constant
                 const uint64_t da = desc_sw128(at), db = desc_sw128(at + 16384);
                 for (int e = 0; e < E16; e += half)
 #pragma unroll
-                    for (int q = 0; q < 4; ++q)
-                        mma_ss(d + e, da + 2 * q, db + e * 8 + 2 * q, idesc, !first || q > 0);
-                if (cluster == 2)
-                    tc_commit_all(smem_u32(&sh.empty[s]), 3);
+                    for (int q = 0; q < 4; ++q) {
+                        if (PAIR)
+                            mma_ss_pair(d + e, da + 2 * q, db + e * 4 + 2 * q, idesc, !first || q > 0);
+                        else
+                            mma_ss(d + e, da + 2 * q, db + e * 8 + 2 * q, idesc, !first || q > 0);
+                    }
+                if (PAIR)
+                    tc_commit_pair(smem_u32(&sh.empty[s]));
                 else
                     tc_commit(smem_u32(&sh.empty[s]));
             }
@@ -519,9 +530,14 @@ __global__ void __launch_bounds__(kThreads, 1) many_kernel(const __grid_constant
                 parity ^= 1;
             }
         }
-        if (elect_one()) {
-            tc_commit(smem_u32(&sh.done));
-            tc_commit(smem_u32(&sh.drain));
+        if (rank == 0 && elect_one()) {
+            if (PAIR) {
+                tc_commit_pair(smem_u32(&sh.done));
+                tc_commit_pair(smem_u32(&sh.drain));
+            } else {
+                tc_commit(smem_u32(&sh.done));
+                tc_commit(smem_u32(&sh.drain));
+            }
         }
         mbar_wait(smem_u32(&sh.drain), 0, nullptr, kWaitOther);
     } else if (warp >= 4) {
@@ -533,11 +549,13 @@ __global__ void __launch_bounds__(kThreads, 1) many_kernel(const __grid_constant
         run = named_all(2, 256, run);
         tc_fence_after();
         const int used = min(spans, c1 - c0);
+        // A pair's second instruction (more than 256 experts) takes the second half of each block's experts.
         auto logits = [&](int e, float (&v)[8]) {
             float x[8];
-            tmem_ld8(lanes + e, v);
+            const int all = E16 / 2, in = e % all, col = !PAIR || half == E16 ? e : (2 * in >= half ? half / 2 : 0) + in + (e >= all ? half / 2 : 0);
+            tmem_ld8(lanes + col, v);
             for (int i = 1; i < used; ++i) {
-                tmem_ld8(lanes + i * E16 + e, x);
+                tmem_ld8(lanes + i * E16 + col, x);
                 tmem_wait_ld();
 #pragma unroll
                 for (int j = 0; j < 8; ++j)
@@ -546,7 +564,7 @@ __global__ void __launch_bounds__(kThreads, 1) many_kernel(const __grid_constant
             tmem_wait_ld();
         };
         float top = -INFINITY, sum = 0.0f;
-        if (run && splits == 1) {
+        if (run && PAIR) {
             for (int e = b0; e < b1; e += 8) {
                 float v[8];
                 logits(e, v);
@@ -587,7 +605,7 @@ __global__ void __launch_bounds__(kThreads, 1) many_kernel(const __grid_constant
                 choose_from_parts<N>(a, t0 + r, from + static_cast<size_t>(r) * a.E, static_cast<size_t>(128) * a.E, splits,
                                      lane);
         }
-        if (run && splits == 1) {
+        if (run && PAIR) {
             for (int e = wtid; e < a.E; e += 256)
                 bias[e] = a.bias ? a.bias[e] : 0.0f;
             float *const mine = scores + row, *const most = mine + a.E * 128, *const values = most + kBuckets * 128;
@@ -651,8 +669,12 @@ __global__ void __launch_bounds__(kThreads, 1) many_kernel(const __grid_constant
     tc_fence_after();
     if (sh.abort) {
         if (tid == 0) {
-            for (int i = max(0, sh.issued - a.stages); i < sh.issued; ++i)
-                mbar_wait(smem_u32(&sh.full[i % a.stages]), (i / a.stages) & 1, nullptr, kWaitOther);
+            bool landed = true;
+            for (int i = max(0, sh.issued - a.stages); rank == 0 && landed && i < sh.issued; ++i)
+                landed = mbar_wait(smem_u32(&sh.full[i % a.stages]), (i / a.stages) & 1, nullptr, kWaitOther);
+            if (PAIR)  // copies that the first block no longer counts land meanwhile
+                for (const long long from = clock64(); clock64() - from < 1000000;) {
+                }
             atomicAdd_system(a.err + sh.abort, 1u);
             __threadfence_system();
             atomicAdd_system(a.err, 1u);
@@ -660,7 +682,7 @@ __global__ void __launch_bounds__(kThreads, 1) many_kernel(const __grid_constant
         __syncthreads();
     }
     if (warp == 1)
-        tmem_free(tmem, a.tmem_cols);
+        tmem_free<PAIR>(tmem, a.tmem_cols);
     cluster_sync();  // the other block's copies and arrivals have come
     if (splits > 1 && tid == 0 && add_acq_rel(a.counters + gridDim.x + tile, 1) == splits - 1)
         a.counters[tile] = a.counters[gridDim.x + tile] = 0;  // for the next launch
@@ -736,15 +758,14 @@ template <int NT, bool BF16> cudaError_t launch_few(const RouterArgs &a, cudaStr
                         : launch_few_n<NT, 16, BF16>(a, stream);
 }
 
-template <int N, bool BF16> cudaError_t launch_many_n(RouterArgs a, cudaStream_t stream)
+template <int N, bool BF16, bool PAIR> cudaError_t launch_many_n(RouterArgs a, const ManyPlan &p, cudaStream_t stream)
 {
     static const cudaError_t attr =
-        cudaFuncSetAttribute(many_kernel<N, BF16>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+        cudaFuncSetAttribute(many_kernel<N, BF16, PAIR>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              kSmemMax - 64 - static_cast<int>(sizeof(Shared)));
     if (attr != cudaSuccess)
         return attr;
-    const ManyPlan p = plan_many(a);
-    const int E16 = router_all_columns(a.E), stage = 16384 + E16 * 128;
+    const int E16 = router_all_columns(a.E), stage = 16384 + E16 * (PAIR ? 64 : 128);
     a.rows = p.rows;
     a.tmem_cols = 512;
     a.stages = (kSmemMax - 2048 - static_cast<int>(sizeof(Shared))) / stage;
@@ -754,12 +775,12 @@ template <int N, bool BF16> cudaError_t launch_many_n(RouterArgs a, cudaStream_t
     size_t smem = static_cast<size_t>(a.stages) * stage;
     smem = 1024 + (smem > choice ? smem : choice);
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(p.splits == 1 ? (p.tiles + 1) & ~1 : p.tiles, p.splits);
+    cfg.gridDim = dim3(PAIR ? (p.tiles + 1) & ~1 : p.tiles, p.splits);
     cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
     cudaLaunchAttribute at[1];
-    if (p.splits > 1) {  // the blocks of a tile wait for one another's parts
+    if (!PAIR) {  // the blocks of a tile wait for one another's parts
         at[0].id = cudaLaunchAttributeCooperative;
         at[0].val.cooperative = 1;
     } else {
@@ -769,14 +790,18 @@ template <int N, bool BF16> cudaError_t launch_many_n(RouterArgs a, cudaStream_t
     }
     cfg.attrs = at;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, many_kernel<N, BF16>, a);
+    return cudaLaunchKernelEx(&cfg, many_kernel<N, BF16, PAIR>, a);
 }
 
 template <bool BF16> cudaError_t launch_many(const RouterArgs &a, cudaStream_t stream)
 {
-    return a.E <= 128   ? launch_many_n<4, BF16>(a, stream)
-           : a.E <= 256 ? launch_many_n<8, BF16>(a, stream)
-                        : launch_many_n<12, BF16>(a, stream);
+    const ManyPlan p = plan_many(a);
+    const bool pair = p.splits == 1;
+    if (a.E <= 128)
+        return pair ? launch_many_n<4, BF16, true>(a, p, stream) : launch_many_n<4, BF16, false>(a, p, stream);
+    if (a.E <= 256)
+        return pair ? launch_many_n<8, BF16, true>(a, p, stream) : launch_many_n<8, BF16, false>(a, p, stream);
+    return pair ? launch_many_n<12, BF16, true>(a, p, stream) : launch_many_n<12, BF16, false>(a, p, stream);
 }
 
 }  // namespace
@@ -804,10 +829,10 @@ std::vector<const void *> router_kernels()
 #define FEW(NT, BF16)                                                                                   \
     reinterpret_cast<const void *>(few_kernel<NT, 4, BF16>), reinterpret_cast<const void *>(few_kernel<NT, 8, BF16>), \
         reinterpret_cast<const void *>(few_kernel<NT, 16, BF16>)
-#define MANY(BF16)                                                                                      \
-    reinterpret_cast<const void *>(many_kernel<4, BF16>), reinterpret_cast<const void *>(many_kernel<8, BF16>),       \
-        reinterpret_cast<const void *>(many_kernel<12, BF16>)
-    return {FEW(1, true), FEW(1, false), FEW(2, true), FEW(2, false), MANY(true), MANY(false)};
+#define MANY(BF16, PAIR)                                                                                \
+    reinterpret_cast<const void *>(many_kernel<4, BF16, PAIR>), reinterpret_cast<const void *>(many_kernel<8, BF16, PAIR>), \
+        reinterpret_cast<const void *>(many_kernel<12, BF16, PAIR>)
+    return {FEW(1, true), FEW(1, false), FEW(2, true), FEW(2, false), MANY(true, false), MANY(false, false), MANY(true, true), MANY(false, true)};
 #undef FEW
 #undef MANY
 }
