@@ -58,7 +58,9 @@ static __device__ __forceinline__ bool ranks_by_logit(const RouterArgs &a)
     return a.scoring == EP_SCORE_SOFTMAX && a.bias == nullptr && a.groups == 1;
 }
 
-static __device__ __forceinline__ float sigmoid(float l) { return 1.0f / (1.0f + expf(-l)); }
+// The quotient is within 2 units of the last place (0 where it would be below 2^-126); the correctly rounded one has a
+// branch for each score.
+static __device__ __forceinline__ float sigmoid(float l) { return __fdividef(1.0f, 1.0f + expf(-l)); }
 
 static __device__ __forceinline__ void store_choice(const RouterArgs &a, int t, int k, int id, float w)
 {
