@@ -295,7 +295,8 @@ __global__ void __launch_bounds__(NT * 256) few_kernel(const __grid_constant__ R
 
 // ---- many tokens -------------------------------------------------------------------
 
-constexpr int kThreads = 384;  // warps: copies, MMA, -, -, then 8 that score and choose
+constexpr int kScorers = 512;  // threads that score and choose, four to a token
+constexpr int kThreads = 128 + kScorers;  // warps: copies, MMA, -, -, then those
 constexpr int kMaxStages = 8;
 constexpr int kBuckets = 16;
 
@@ -356,68 +357,93 @@ static __device__ __forceinline__ float group_value(float b1, float b2, int per)
     return v > -INFINITY ? v : -INFINITY;  // infinities of both signs
 }
 
-// One thread: the choice of one token. score[e * 128] is expert e's score (its
-// logit where the rank goes by logits), most[b * 128] bucket b's largest value
-// and value[b * 128] a group's.
-static __device__ void choose_thread(const RouterArgs &a, int t, float *score, const float *most_of, const float *values,
-                                     const float *bias, float top, float sum)
+// Four neighbouring lanes, q = 0 to 3: the choice of one token; the warp is
+// converged. score[e * 128] is expert e's score (its logit where the rank goes
+// by logits), most_of[b * 128] bucket b's largest value and values[b * 128] a
+// group's. A pick takes the bucket with the largest value and looks through it
+// for the expert, whose score then becomes NaN, and for the next largest. One
+// thread a token took 8 us for 128 tokens and eight picks. live: the token
+// exists, its results are written.
+static __device__ void choose_quad(const RouterArgs &a, int t, bool live, float *score, const float *most_of,
+                                   const float *values, const float *bias, float top, float sum, int q)
 {
+    constexpr int kMine = kBuckets / 4, kNone = 0x7FFFFFFF;
     const bool by_logit = ranks_by_logit(a);
     const Buckets bk = buckets_of(a);
     const unsigned keep = bk.groups ? best_groups(a, values) : ~0u;
-    float most[kBuckets];
+    float most[kMine];  // of buckets 4 q .. 4 q + 3
 #pragma unroll
-    for (int b = 0; b < kBuckets; ++b)
-        most[b] = b < bk.n && ((keep >> b) & 1) ? most_of[b * 128] : -INFINITY;
+    for (int i = 0; i < kMine; ++i) {
+        const int b = q * kMine + i;
+        most[i] = b < bk.n && ((keep >> b) & 1) ? most_of[b * 128] : -INFINITY;
+    }
     const size_t at = static_cast<size_t>(t) * a.K;
-    float w[8], total = 0.0f;  // the first eight weights stay in registers
-    int n = 0;
-    for (; n < a.K; ++n) {
+    float w[EP_MAX_TOP_K / 4], total = 0.0f;  // of choices q, q + 4, ...
+    int count = 0;
+    for (int n = 0; n < a.K; ++n) {
         float best = -INFINITY;
-        int b = -1;
+        int b = kNone;
 #pragma unroll
-        for (int i = 0; i < kBuckets; ++i)
+        for (int i = 0; i < kMine; ++i)
             if (most[i] > best) {
                 best = most[i];
-                b = i;
+                b = q * kMine + i;
             }
-        if (b < 0)
-            break;  // nothing left to choose
+#pragma unroll
+        for (int d = 1; d < 4; d <<= 1) {
+            const float v = __shfl_xor_sync(~0u, best, d);
+            const int o = __shfl_xor_sync(~0u, b, d);
+            const bool take = v > best || (v == best && o < b);
+            best = take ? v : best;
+            b = take ? o : b;
+        }
+        const bool any = b != kNone;  // something is left to choose
         float rest = -INFINITY;
-        int id = -1;
-        const int end = min((b + 1) * bk.size, a.E);
+        int id = kNone;
+        const int end = any ? min((b + 1) * bk.size, a.E) : 0;
 #pragma unroll 4
-        for (int e = b * bk.size; e < end; ++e) {
+        for (int e = any ? b * bk.size + q : 0; e < end; e += 4) {
             const float c = score[e * 128] + bias[e];
-            const bool hit = id < 0 && c == best;
+            const bool hit = id == kNone && c == best;
             id = hit ? e : id;
             rest = !hit && c > rest ? c : rest;
         }
-        const float s = score[id * 128], weight = by_logit ? expf(s - top) / sum : s;
-        score[id * 128] = __uint_as_float(0x7FC00000u);  // NaN is never chosen
+        __syncwarp();
+        int first = id;
 #pragma unroll
-        for (int i = 0; i < kBuckets; ++i)
-            most[i] = i == b ? rest : most[i];
+        for (int d = 1; d < 4; d <<= 1)
+            first = min(first, __shfl_xor_sync(~0u, first, d));
+        if (id != kNone && id != first)  // as large, but not the lowest index
+            rest = best;
+#pragma unroll
+        for (int d = 1; d < 4; d <<= 1)
+            rest = fmaxf(rest, __shfl_xor_sync(~0u, rest, d));
+        const float x = any ? score[first * 128] : 0.0f, weight = by_logit && any ? expf(x - top) / sum : x;
+        __syncwarp();
+        if (any && q == 0)
+            score[first * 128] = __uint_as_float(0x7FC00000u);  // NaN is never chosen
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < kMine; ++i)
+            most[i] = q * kMine + i == b ? rest : most[i];
         total += weight;
+        count += any ? 1 : 0;
+        if ((n & 3) == q) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-            w[i] = i == n ? weight : w[i];
-        if (EP_IN_BOUNDS(a.chk, epk::kSiteMoeIds, a.ids + at + n, 4, a.ids, 4LL * a.T * a.K))
-            a.ids[at + n] = id;
-        if (n >= 8 && EP_IN_BOUNDS(a.chk, epk::kSiteMoeWeights, a.weights + at + n, 4, a.weights, 4LL * a.T * a.K))
-            a.weights[at + n] = weight;
+            for (int i = 0; i < EP_MAX_TOP_K / 4; ++i)
+                w[i] = i == n >> 2 ? weight : w[i];
+            if (live && EP_IN_BOUNDS(a.chk, epk::kSiteMoeIds, a.ids + at + n, 4, a.ids, 4LL * a.T * a.K))
+                a.ids[at + n] = any ? first : EP_INVALID_EXPERT_ID;
+        }
     }
     if (!a.renormalize)
         total = 1.0f;
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-        if (i < n && EP_IN_BOUNDS(a.chk, epk::kSiteMoeWeights, a.weights + at + i, 4, a.weights, 4LL * a.T * a.K))
-            a.weights[at + i] = w[i] / total * a.scale;
-    for (int i = 8; i < n; ++i)
-        if (EP_IN_BOUNDS(a.chk, epk::kSiteMoeWeights, a.weights + at + i, 4, a.weights, 4LL * a.T * a.K))
-            a.weights[at + i] = a.weights[at + i] / total * a.scale;
-    for (; n < a.K; ++n)
-        store_choice(a, t, n, EP_INVALID_EXPERT_ID, 0.0f);
+    for (int i = 0; i < EP_MAX_TOP_K / 4; ++i) {
+        const int n = 4 * i + q;
+        if (live && n < a.K && EP_IN_BOUNDS(a.chk, epk::kSiteMoeWeights, a.weights + at + n, 4, a.weights, 4LL * a.T * a.K))
+            a.weights[at + n] = n < count ? w[i] / total * a.scale : 0.0f;
+    }
 }
 
 // grid (token tiles, input splits). Without splits (PAIR) two blocks make a
@@ -543,12 +569,13 @@ __global__ void __launch_bounds__(kThreads, 1) many_kernel(const __grid_constant
         }
         mbar_wait(smem_u32(&sh.drain), 0, nullptr, kWaitOther);
     } else if (warp >= 4) {
-        // 8 warps: two threads to a token, each with half of the experts' scores
+        // four threads to a token, each with a quarter of the experts' scores
+        constexpr int kParts = kScorers / 128;
         const int row = tid & 127, part = (warp - 4) >> 2, wtid = tid - 128;
         const uint32_t lanes = tmem + (static_cast<uint32_t>(warp & 3) << 21);
-        const int mid = ((a.E + 15) / 16) * 8, b0 = part ? mid : 0, b1 = part ? a.E : min(mid, a.E);
+        const int mine8 = (a.E + 8 * kParts - 1) / (8 * kParts) * 8, b0 = min(part * mine8, a.E), b1 = min(b0 + mine8, a.E);
         bool run = mbar_wait_warp(smem_u32(&sh.done), 0, abort, kWaitFullD);
-        run = named_all(2, 256, run);
+        run = named_all(2, kScorers, run);
         tc_fence_after();
         const int used = min(spans, c1 - c0);
         // A pair's second instruction (more than 256 experts) takes the second half of each block's experts.
@@ -594,30 +621,31 @@ __global__ void __launch_bounds__(kThreads, 1) many_kernel(const __grid_constant
                             p[e + i] = v[i];
                 }
             }
-            named_sync(1, 256);
+            named_sync(1, kScorers);
             if (wtid == 0) {
                 add_acq_rel(a.counters + tile, 1);
                 run = wait_count(a.counters + tile, splits, abort, kWaitOther);
             }
-            run = named_all(2, 256, run);
+            run = named_all(2, kScorers, run);
             // this block's tokens of the tile, a warp each
             const int r0 = rows * split / splits, r1 = rows * (split + 1) / splits;
             const float *const from = a.parts + static_cast<size_t>(tile) * splits * 128 * a.E;
-            for (int r = r0 + warp - 4; run && r < r1; r += 8)
+            for (int r = r0 + warp - 4; run && r < r1; r += kScorers / 32)
                 choose_from_parts<N>(a, t0 + r, from + static_cast<size_t>(r) * a.E, static_cast<size_t>(128) * a.E, splits,
                                      lane);
         }
         if (run && PAIR) {
-            for (int e = wtid; e < a.E; e += 256)
+            for (int e = wtid; e < a.E; e += kScorers)
                 bias[e] = a.bias ? a.bias[e] : 0.0f;
             float *const mine = scores + row, *const most = mine + a.E * 128, *const values = most + kBuckets * 128;
-            if (a.scoring == EP_SCORE_SOFTMAX) {  // the two threads of a token exchange the largest logit and the sum
-                float *const xch = bias + a.E + part * 128 + row;
-                const float *const other = bias + a.E + (part ^ 1) * 128 + row;
-                *xch = top;
-                named_sync(1, 256);
-                top = fmaxf(top, *other);
-                named_sync(1, 256);
+            float *const xch = bias + a.E;  // [parts][128]
+            if (a.scoring == EP_SCORE_SOFTMAX) {  // the threads of a token exchange the largest logit and the sum
+                xch[part * 128 + row] = top;
+                named_sync(1, kScorers);
+#pragma unroll
+                for (int i = 0; i < kParts; ++i)
+                    top = fmaxf(top, xch[i * 128 + row]);
+                named_sync(1, kScorers);
                 const bool keep = ranks_by_logit(a);
 #pragma unroll 4
                 for (int e = b0; e < b1; ++e) {
@@ -626,43 +654,54 @@ __global__ void __launch_bounds__(kThreads, 1) many_kernel(const __grid_constant
                     if (!keep)
                         mine[e * 128] = x;
                 }
-                *xch = sum;
-                named_sync(1, 256);
-                sum = part ? *other + sum : sum + *other;
+                xch[part * 128 + row] = sum;
+                named_sync(1, kScorers);
+                sum = 0.0f;
+#pragma unroll
+                for (int i = 0; i < kParts; ++i)
+                    sum += xch[i * 128 + row];
                 if (!keep) {
 #pragma unroll 4
                     for (int e = b0; e < b1; ++e)
                         mine[e * 128] = mine[e * 128] / sum;
                 }
+                named_sync(1, kScorers);
+                if (part == 0) {
+                    xch[row] = top;
+                    xch[128 + row] = sum;
+                }
             }
-            named_sync(1, 256);
+            named_sync(1, kScorers);
             const Buckets bk = buckets_of(a);
             if (a.groups > kBuckets) {  // many small groups: NaN for the experts of those that do not take part
                 const int per = a.E / a.groups;
                 float b1v, b2v;
-                for (int g = part; g < a.groups; g += 2) {
+                for (int g = part; g < a.groups; g += kParts) {
                     two_largest(mine, bias, g * per, (g + 1) * per, b1v, b2v);
                     most[g * 128] = group_value(b1v, b2v, per);
                 }
-                named_sync(1, 256);
+                named_sync(1, kScorers);
                 const unsigned kept = best_groups(a, most);
-                named_sync(1, 256);
-                for (int g = part; g < a.groups; g += 2)
+                named_sync(1, kScorers);
+                for (int g = part; g < a.groups; g += kParts)
                     if (!((kept >> g) & 1))
                         for (int e = g * per; e < (g + 1) * per; ++e)
                             mine[e * 128] = __uint_as_float(0x7FC00000u);
-                named_sync(1, 256);
+                named_sync(1, kScorers);
             }
-            for (int b = part; b < bk.n; b += 2) {
+            for (int b = part; b < bk.n; b += kParts) {
                 float b1v, b2v;
                 two_largest(mine, bias, b * bk.size, min((b + 1) * bk.size, a.E), b1v, b2v);
                 most[b * 128] = b1v;
                 if (bk.groups)
                     values[b * 128] = group_value(b1v, b2v, bk.size);
             }
-            named_sync(1, 256);
-            if (part == 0 && row < rows)
-                choose_thread(a, t0 + row, mine, most, values, bias, top, sum);
+            named_sync(1, kScorers);
+            const int token = wtid >> 2;
+            float *const its = scores + token;
+            const bool softmax = a.scoring == EP_SCORE_SOFTMAX;
+            choose_quad(a, t0 + token, token < rows, its, its + a.E * 128, its + (a.E + kBuckets) * 128, bias,
+                        softmax ? xch[token] : 0.0f, softmax ? xch[128 + token] : 0.0f, wtid & 3);
         }
     }
     __syncwarp();
@@ -773,7 +812,7 @@ template <int N, bool BF16, bool PAIR> cudaError_t launch_many_n(RouterArgs a, c
     a.stages = (kSmemMax - 2048 - static_cast<int>(sizeof(Shared))) / stage;
     if (a.stages > kMaxStages)
         a.stages = kMaxStages;
-    const size_t choice = (static_cast<size_t>(a.E + 32) * 128 + a.E + 256) * 4;
+    const size_t choice = (static_cast<size_t>(a.E + 32) * 128 + a.E + kScorers) * 4;
     size_t smem = static_cast<size_t>(a.stages) * stage;
     smem = 1024 + (smem > choice ? smem : choice);
     cudaLaunchConfig_t cfg = {};
