@@ -299,6 +299,10 @@ constexpr int kScorers = 512;  // threads that score and choose, four to a token
 constexpr int kThreads = 128 + kScorers;  // warps: copies, MMA, -, -, then those
 constexpr int kMaxStages = 8;
 constexpr int kBuckets = 16;
+// Scores lie [expert][token], 136 to a row: the choice's lanes, eight tokens times four experts in a row, then read 32
+// banks, and the biases of the same place in several buckets of 32 lie in different ones.
+constexpr int kScoreStride = 136;
+static __host__ __device__ __forceinline__ int bias_at(int e) { return e + (e >> 5); }
 
 struct Shared {
     uint64_t full[kMaxStages], empty[kMaxStages], done, drain;
@@ -319,20 +323,20 @@ static __device__ __forceinline__ Buckets buckets_of(const RouterArgs &a)
     return {groups ? a.groups : kBuckets, groups ? a.E / a.groups : (a.E + kBuckets - 1) / kBuckets, groups};
 }
 
-// The two largest choice values of experts [e0, e1) of a token (score[e * 128]).
+// The two largest choice values of experts [e0, e1) of a token (score[e * kScoreStride]).
 static __device__ __forceinline__ void two_largest(const float *score, const float *bias, int e0, int e1, float &b1, float &b2)
 {
     b1 = b2 = -INFINITY;
 #pragma unroll 4
     for (int e = e0; e < e1; ++e) {
-        const float c = score[e * 128] + bias[e];
+        const float c = score[e * kScoreStride] + bias[bias_at(e)];
         const float v = c > -INFINITY ? c : -INFINITY;  // NaN is never chosen
         b2 = fmaxf(b2, fminf(b1, v));
         b1 = fmaxf(b1, v);
     }
 }
 
-// The groups that take part, as a bit set, from their values[g * 128].
+// The groups that take part, as a bit set, from their values[g * kScoreStride].
 static __device__ unsigned best_groups(const RouterArgs &a, const float *values)
 {
     unsigned keep = 0;
@@ -340,7 +344,7 @@ static __device__ unsigned best_groups(const RouterArgs &a, const float *values)
         int best = -1;
         float most = 0.0f;
         for (int g = 0; g < a.groups; ++g) {
-            const float v = values[g * 128];
+            const float v = values[g * kScoreStride];
             if (!((keep >> g) & 1) && (best < 0 || v > most)) {
                 best = g;
                 most = v;
@@ -358,8 +362,8 @@ static __device__ __forceinline__ float group_value(float b1, float b2, int per)
 }
 
 // Four neighbouring lanes, q = 0 to 3: the choice of one token; the warp is
-// converged. score[e * 128] is expert e's score (its logit where the rank goes
-// by logits), most_of[b * 128] bucket b's largest value and values[b * 128] a
+// converged. score[e * kScoreStride] is expert e's score (its logit where the rank goes
+// by logits), most_of[b * kScoreStride] bucket b's largest value and values[b * kScoreStride] a
 // group's. A pick takes the bucket with the largest value and looks through it
 // for the expert, whose score then becomes NaN, and for the next largest. One
 // thread a token took 8 us for 128 tokens and eight picks. live: the token
@@ -370,12 +374,27 @@ static __device__ void choose_quad(const RouterArgs &a, int t, bool live, float 
     constexpr int kMine = kBuckets / 4, kNone = 0x7FFFFFFF;
     const bool by_logit = ranks_by_logit(a);
     const Buckets bk = buckets_of(a);
-    const unsigned keep = bk.groups ? best_groups(a, values) : ~0u;
     float most[kMine];  // of buckets 4 q .. 4 q + 3
 #pragma unroll
     for (int i = 0; i < kMine; ++i) {
         const int b = q * kMine + i;
-        most[i] = b < bk.n && ((keep >> b) & 1) ? most_of[b * 128] : -INFINITY;
+        most[i] = b < bk.n ? most_of[b * kScoreStride] : -INFINITY;
+    }
+    if (bk.groups) {  // a group takes part if fewer than top_groups come before it
+        float v[kBuckets];
+#pragma unroll
+        for (int g = 0; g < kBuckets; ++g)
+            v[g] = g < bk.n ? values[g * kScoreStride] : -INFINITY;
+#pragma unroll
+        for (int i = 0; i < kMine; ++i) {
+            const int b = q * kMine + i;
+            const float own = b < bk.n ? values[b * kScoreStride] : -INFINITY;
+            int before = 0;
+#pragma unroll
+            for (int g = 0; g < kBuckets; ++g)
+                before += g < bk.n && (v[g] > own || (v[g] == own && g < b)) ? 1 : 0;
+            most[i] = before < a.top_groups ? most[i] : -INFINITY;
+        }
     }
     const size_t at = static_cast<size_t>(t) * a.K;
     float w[EP_MAX_TOP_K / 4], total = 0.0f;  // of choices q, q + 4, ...
@@ -401,12 +420,17 @@ static __device__ void choose_quad(const RouterArgs &a, int t, bool live, float 
         float rest = -INFINITY;
         int id = kNone;
         const int end = any ? min((b + 1) * bk.size, a.E) : 0;
-#pragma unroll 4
-        for (int e = any ? b * bk.size + q : 0; e < end; e += 4) {
-            const float c = score[e * 128] + bias[e];
-            const bool hit = id == kNone && c == best;
-            id = hit ? e : id;
-            rest = !hit && c > rest ? c : rest;
+        for (int e0 = any ? b * bk.size + q : 0; e0 < end; e0 += 32) {
+            float c[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                c[i] = e0 + 4 * i < end ? score[(e0 + 4 * i) * kScoreStride] + bias[bias_at(e0 + 4 * i)] : -INFINITY;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const bool hit = id == kNone && c[i] == best;
+                id = hit ? e0 + 4 * i : id;
+                rest = !hit && c[i] > rest ? c[i] : rest;
+            }
         }
         __syncwarp();
         int first = id;
@@ -418,10 +442,10 @@ static __device__ void choose_quad(const RouterArgs &a, int t, bool live, float 
 #pragma unroll
         for (int d = 1; d < 4; d <<= 1)
             rest = fmaxf(rest, __shfl_xor_sync(~0u, rest, d));
-        const float x = any ? score[first * 128] : 0.0f, weight = by_logit && any ? expf(x - top) / sum : x;
+        const float x = any ? score[first * kScoreStride] : 0.0f, weight = by_logit && any ? expf(x - top) / sum : x;
         __syncwarp();
         if (any && q == 0)
-            score[first * 128] = __uint_as_float(0x7FC00000u);  // NaN is never chosen
+            score[first * kScoreStride] = __uint_as_float(0x7FC00000u);  // NaN is never chosen
         __syncwarp();
 #pragma unroll
         for (int i = 0; i < kMine; ++i)
@@ -450,7 +474,7 @@ static __device__ void choose_quad(const RouterArgs &a, int t, bool live, float 
 // cluster and multiply together: each has its tokens and half of the weight's
 // rows of a chunk in shared memory, so the weight is read once for 256 tokens.
 // The first block issues, and both blocks' copies report to its barriers. Dynamic shared
-// memory: the ring, used again for scores [E][128], 32 rows of bucket and group
+// memory: the ring, used again for scores [E][136], 32 rows of bucket and group
 // values, and the bias.
 template <int N, bool BF16, bool PAIR>
 __global__ void __launch_bounds__(kThreads, 1) many_kernel(const __grid_constant__ RouterArgs a)
@@ -459,7 +483,7 @@ __global__ void __launch_bounds__(kThreads, 1) many_kernel(const __grid_constant
     __shared__ Shared sh;
     const uint32_t dyn0 = smem_u32(dyn), ring = (dyn0 + 1023u) & ~1023u;
     float *const scores = reinterpret_cast<float *>(dyn + (ring - dyn0));
-    float *const bias = scores + (a.E + 32) * 128;
+    float *const bias = scores + (a.E + 32) * kScoreStride;
     const int tid = threadIdx.x, warp = __shfl_sync(~0u, tid >> 5, 0), lane = tid & 31;
     const int tile = blockIdx.x, split = blockIdx.y, splits = gridDim.y;
     const int t0 = tile * a.rows, rows = min(a.rows, a.T - t0);
@@ -601,7 +625,7 @@ __global__ void __launch_bounds__(kThreads, 1) many_kernel(const __grid_constant
                 for (int i = 0; i < 8; ++i)
                     if (e + i < b1) {
                         top = fmaxf(top, v[i]);
-                        scores[(e + i) * 128 + row] = a.scoring == EP_SCORE_SIGMOID ? sigmoid(v[i]) : v[i];
+                        scores[(e + i) * kScoreStride + row] = a.scoring == EP_SCORE_SIGMOID ? sigmoid(v[i]) : v[i];
                     }
             }
         } else if (run) {  // parts: [tile][split][token][E]
@@ -636,9 +660,9 @@ __global__ void __launch_bounds__(kThreads, 1) many_kernel(const __grid_constant
         }
         if (run && PAIR) {
             for (int e = wtid; e < a.E; e += kScorers)
-                bias[e] = a.bias ? a.bias[e] : 0.0f;
-            float *const mine = scores + row, *const most = mine + a.E * 128, *const values = most + kBuckets * 128;
-            float *const xch = bias + a.E;  // [parts][128]
+                bias[bias_at(e)] = a.bias ? a.bias[e] : 0.0f;
+            float *const mine = scores + row, *const most = mine + a.E * kScoreStride, *const values = most + kBuckets * kScoreStride;
+            float *const xch = bias + bias_at(a.E);  // [parts][128]
             if (a.scoring == EP_SCORE_SOFTMAX) {  // the threads of a token exchange the largest logit and the sum
                 xch[part * 128 + row] = top;
                 named_sync(1, kScorers);
@@ -649,10 +673,10 @@ __global__ void __launch_bounds__(kThreads, 1) many_kernel(const __grid_constant
                 const bool keep = ranks_by_logit(a);
 #pragma unroll 4
                 for (int e = b0; e < b1; ++e) {
-                    const float x = expf(mine[e * 128] - top);
+                    const float x = expf(mine[e * kScoreStride] - top);
                     sum += x;
                     if (!keep)
-                        mine[e * 128] = x;
+                        mine[e * kScoreStride] = x;
                 }
                 xch[part * 128 + row] = sum;
                 named_sync(1, kScorers);
@@ -663,7 +687,7 @@ __global__ void __launch_bounds__(kThreads, 1) many_kernel(const __grid_constant
                 if (!keep) {
 #pragma unroll 4
                     for (int e = b0; e < b1; ++e)
-                        mine[e * 128] = mine[e * 128] / sum;
+                        mine[e * kScoreStride] = mine[e * kScoreStride] / sum;
                 }
                 named_sync(1, kScorers);
                 if (part == 0) {
@@ -678,7 +702,7 @@ __global__ void __launch_bounds__(kThreads, 1) many_kernel(const __grid_constant
                 float b1v, b2v;
                 for (int g = part; g < a.groups; g += kParts) {
                     two_largest(mine, bias, g * per, (g + 1) * per, b1v, b2v);
-                    most[g * 128] = group_value(b1v, b2v, per);
+                    most[g * kScoreStride] = group_value(b1v, b2v, per);
                 }
                 named_sync(1, kScorers);
                 const unsigned kept = best_groups(a, most);
@@ -686,21 +710,21 @@ __global__ void __launch_bounds__(kThreads, 1) many_kernel(const __grid_constant
                 for (int g = part; g < a.groups; g += kParts)
                     if (!((kept >> g) & 1))
                         for (int e = g * per; e < (g + 1) * per; ++e)
-                            mine[e * 128] = __uint_as_float(0x7FC00000u);
+                            mine[e * kScoreStride] = __uint_as_float(0x7FC00000u);
                 named_sync(1, kScorers);
             }
             for (int b = part; b < bk.n; b += kParts) {
                 float b1v, b2v;
                 two_largest(mine, bias, b * bk.size, min((b + 1) * bk.size, a.E), b1v, b2v);
-                most[b * 128] = b1v;
+                most[b * kScoreStride] = b1v;
                 if (bk.groups)
-                    values[b * 128] = group_value(b1v, b2v, bk.size);
+                    values[b * kScoreStride] = group_value(b1v, b2v, bk.size);
             }
             named_sync(1, kScorers);
             const int token = wtid >> 2;
             float *const its = scores + token;
             const bool softmax = a.scoring == EP_SCORE_SOFTMAX;
-            choose_quad(a, t0 + token, token < rows, its, its + a.E * 128, its + (a.E + kBuckets) * 128, bias,
+            choose_quad(a, t0 + token, token < rows, its, its + a.E * kScoreStride, its + (a.E + kBuckets) * kScoreStride, bias,
                         softmax ? xch[token] : 0.0f, softmax ? xch[128 + token] : 0.0f, wtid & 3);
         }
     }
@@ -812,7 +836,7 @@ template <int N, bool BF16, bool PAIR> cudaError_t launch_many_n(RouterArgs a, c
     a.stages = (kSmemMax - 2048 - static_cast<int>(sizeof(Shared))) / stage;
     if (a.stages > kMaxStages)
         a.stages = kMaxStages;
-    const size_t choice = (static_cast<size_t>(a.E + 32) * 128 + a.E + kScorers) * 4;
+    const size_t choice = (static_cast<size_t>(a.E + 32) * kScoreStride + bias_at(a.E) + kScorers) * 4;
     size_t smem = static_cast<size_t>(a.stages) * stage;
     smem = 1024 + (smem > choice ? smem : choice);
     cudaLaunchConfig_t cfg = {};
