@@ -16,16 +16,18 @@
 //    out. Tiles are as high as one wave of blocks needs, up to 128 tokens.
 //    With too few tiles for the SMs the inputs are split over blocks as well;
 //    parts go through memory and each block of a tile chooses for its share
-//    of the tokens. Otherwise two blocks share each chunk of the weight, one
-//    half fetched by each and multicast to both.
+//    of the tokens. Otherwise two blocks multiply together, which halves the
+//    weight's traffic into and out of shared memory (one block for itself,
+//    with the weight multicast, left the MMAs waiting: 60 us for the products
+//    below, now 38).
 //
-// What bounds them: latency for few tokens (one token, 128 experts x 4096: 5.7
-// us in a graph, 10.5 with the host's launch; 128 tokens, 256 experts x 7168,
-// inputs split over 16 blocks: 17 us). 16001 tokens x 7168 to 256 experts take
-// 79 us: 35 us are the bytes' and 31 the MMAs'; shared memory serves both the
-// copies in and the 128 x 256 MMAs' operands, which leaves the tensor pipe at
-// 34 % and DRAM at 40 %, and choosing the experts from the accumulators takes
-// the last 12 us of each block.
+// What bounds them: latency for few tokens (one token, 128 experts x 4096: 5.6
+// us in a graph, 10 with the host's launch; 128 tokens, 256 experts x 7168,
+// inputs split over 16 blocks: 16 us). 16001 tokens x 7168 to 256 experts take
+// 56 us, 4.2 TB/s: the products 38, at 35 us for their bytes and 31 for the
+// MMAs, then scores 5, buckets 2.5 and eight picks 8, latency and issue of
+// dependent comparisons, while no tile is left to multiply meanwhile. The
+// tensor pipe is active 52 % of the time, DRAM 50 %.
 #include <type_traits>
 
 #include "moe_device.h"
@@ -365,9 +367,10 @@ static __device__ __forceinline__ float group_value(float b1, float b2, int per)
 // converged. score[e * kScoreStride] is expert e's score (its logit where the rank goes
 // by logits), most_of[b * kScoreStride] bucket b's largest value and values[b * kScoreStride] a
 // group's. A pick takes the bucket with the largest value and looks through it
-// for the expert, whose score then becomes NaN, and for the next largest. One
-// thread a token took 8 us for 128 tokens and eight picks. live: the token
-// exists, its results are written.
+// for the expert, whose score then becomes NaN, and for the next largest. With
+// one thread a token the tile of 128 took longer although it had four warps
+// only: 61 against 58 us for the call of 16001. live: the token exists, its
+// results are written.
 static __device__ void choose_quad(const RouterArgs &a, int t, bool live, float *score, const float *most_of,
                                    const float *values, const float *bias, float top, float sum, int q)
 {
