@@ -762,25 +762,28 @@ struct ManyPlan {
     int rows, tiles, splits;
 };
 
-// Up to 16 splits of the inputs, as far as a wave of blocks with full tiles
-// leaves SMs idle (a block then chooses for a few tokens, a warp each), and
-// tiles as high as that many blocks need.
+// Up to 16 splits of the inputs, as far as they leave one wave of blocks with
+// tiles of at most 128 tokens (a block then chooses for a few tokens, a warp
+// each), and tiles as high as that many blocks need. Tiles come first: 1300
+// tokens are 11 of them, 13 splits of which fit 152 SMs; 14, which the SMs
+// would hold by the number of tokens, leave blocks for 10.
 ManyPlan plan_many(const RouterArgs &a)
 {
     ManyPlan p;
     const int chunks = (a.H + kChunk - 1) / kChunk;
-    p.splits = a.sms * 128 / a.T;
+    const int full = static_cast<int>((a.T + 127LL) / 128);  // tiles of 128
+    p.splits = a.sms / full;
     p.splits = p.splits > 16 ? 16 : p.splits;
     p.splits = p.splits > chunks ? chunks : p.splits;
     if (p.splits <= 1) {
-        const int waves = (a.T + a.sms * 128 - 1) / (a.sms * 128);
+        const long long wave = (full + a.sms - 1) / a.sms * static_cast<long long>(a.sms);
         p.splits = 1;
-        p.rows = (a.T + waves * a.sms - 1) / (waves * a.sms);
+        p.rows = static_cast<int>((a.T + wave - 1) / wave);
     } else {
-        const int tiles = a.sms / p.splits;
+        const int tiles = a.sms / p.splits;  // full or more
         p.rows = (a.T + tiles - 1) / tiles;
     }
-    p.tiles = (a.T + p.rows - 1) / p.rows;
+    p.tiles = static_cast<int>((a.T + p.rows - 1LL) / p.rows);
     return p;
 }
 
