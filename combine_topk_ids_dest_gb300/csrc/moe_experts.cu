@@ -70,7 +70,7 @@ __global__ void __launch_bounds__(kThreads, 1) experts_kernel(const __grid_const
     uint8_t *const after = dyn + (ring_b - dyn0) + a.bytes_b;
     const int T8 = (a.T + 7) & ~7;
     float *const acc = reinterpret_cast<float *>(after);
-    const Lists li(acc + T8 * kTileRows, a.E, a.P);
+    const Lists li(acc + T8 * kTileRows, acc, a.E, a.P);
 
     const int tid = threadIdx.x, warp = __shfl_sync(~0u, tid >> 5, 0);
     const int G = gridDim.x, blk = blockIdx.x;

@@ -50,17 +50,15 @@ namespace moe {
 
 namespace {
 
-constexpr int kGroups = 4;                 // groups of four warps that multiply
+constexpr int kGroups = kInt4Groups;
 constexpr int kWorkers = kGroups * 128;
 // then a warpgroup for results, a warp that brings weights and two that bring tokens
 constexpr int kResults = 128;
 constexpr int kThreads = kWorkers + kResults + 96;
 constexpr int kCopyWarp = (kWorkers + kResults) / 32;  // brings weights; the next ones tokens
-constexpr int kMaxStagesA = 12;
-constexpr int kMaxStagesB = 16;
+constexpr int kMaxStagesA = kInt4StagesA, kMaxStagesB = kInt4StagesB;
 constexpr int kCap = 32;                   // tokens of an entry: 4 column blocks of 8
 constexpr int kSideBySide = 4;             // up to so many tokens have both parts of h in one column block
-constexpr int kSumStride = kTileRows + 4;  // column stride of the groups' sums: fragments' stores hit all banks
 
 struct Shared {
     uint64_t full_a[kMaxStagesA], empty_a[kMaxStagesA];
@@ -257,13 +255,13 @@ static __device__ __noinline__ uint32_t run_tiles(uint32_t word, int units, int 
     at.run = mbar_wait_warp(smem_u32(&sh.empty_s), at.run_parity, abort, kWaitEmptyD);
     at.run_parity ^= 1;
     if (at.run) {
-        float *const mine = reinterpret_cast<float *>(dyn + sh.sums) + (grp * sh.cols + (lane & 3) * 2) * kSumStride +
+        float *const mine = reinterpret_cast<float *>(dyn + sh.sums) + (grp * sh.cols + (lane & 3) * 2) * kInt4SumStride +
                             rows32 * 32 + (lane >> 2);
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int i = 0; i < 8; ++i)
-                mine[(nt * 8 + (i & 1)) * kSumStride + (i >> 1) * 8] = acc[nt][i >> 2][i & 3];
+                mine[(nt * 8 + (i & 1)) * kInt4SumStride + (i >> 1) * 8] = acc[nt][i >> 2][i & 3];
         __syncwarp();
         if (lane == 0)
             mbar_arrive(smem_u32(&sh.full_s));
@@ -277,7 +275,7 @@ __global__ void __launch_bounds__(kThreads, 1) int4_kernel(const __grid_constant
     const uint32_t dyn0 = smem_u32(dyn), base = (dyn0 + 127u) & ~127u;
     // dynamic shared memory: y's accumulators, lists, the groups' sums, the rings
     float *const acc_y = reinterpret_cast<float *>(dyn + (base - dyn0));  // [T][128], of the second product
-    const Lists li(acc_y + (LINEAR ? 0 : a.T * kTileRows), a.E, a.P);
+    const Lists li(acc_y + (LINEAR ? 0 : a.T * kTileRows), acc_y, a.E, a.P);
 
     const int tid = threadIdx.x, warp = __shfl_sync(~0u, tid >> 5, 0), lane = tid & 31;
     const int G = gridDim.x, blk = blockIdx.x;
@@ -347,24 +345,15 @@ __global__ void __launch_bounds__(kThreads, 1) int4_kernel(const __grid_constant
         }
     }
     const int pairs = LINEAR ? a.T : li.offset[A];
-    // A unit's token tile, in 8-token steps of 2 KB a chunk: two chunks, or one (and in the second product two
-    // chunks in two parts). The second product's ring begins where the first's did, which is empty by then: h
-    // is complete when every block is through with the first.
-    const int cols = (nmax + 7) & ~7, stage_b1 = cols * (LINEAR ? 512 : 256), stage_b2 = cols * (LINEAR ? 512 : 1024);
-    // the groups' sums take what this launch's largest entry needs; the rings share the rest so that about as many
-    // token tiles as weight tiles are on their way
-    const uint32_t sums_at = (base + a.fixed_bytes + 127u) & ~127u;
-    float *const sums = reinterpret_cast<float *>(dyn + (sums_at - dyn0));  // [group][column][kSumStride]
-    const uint32_t ring_b = sums_at + kGroups * cols * kSumStride * 4;
-    const int room = a.smem - static_cast<int>(ring_b - dyn0);
-    const int stages_b2 = max(2, min(kMaxStagesB, room / (a.stage_a + stage_b2)));
-    const int stages_b1 = min(kMaxStagesB, stages_b2 * stage_b2 / stage_b1);
-    const uint32_t ring_a = ring_b + stages_b2 * stage_b2;
-    const int stages = min(kMaxStagesA, (room - stages_b2 * stage_b2) / a.stage_a);
+    const Int4Layout lay = int4_layout(LINEAR, a.smem - static_cast<int>(base - dyn0), a.fixed_bytes, a.stage_a, nmax);
+    const int cols = lay.cols, stages = lay.stages, stage_b1 = lay.stage_b[0], stage_b2 = lay.stage_b[1];
+    const int stages_b1 = lay.stages_b[0], stages_b2 = lay.stages_b[1];
+    float *const sums = reinterpret_cast<float *>(dyn + (base - dyn0) + lay.sums);  // [group][column][kInt4SumStride]
+    const uint32_t ring_a = base + lay.ring_a, ring_b = base + lay.ring_b;
     if (tid == kThreads - 1) {
         sh.ring_a = ring_a - dyn0;
         sh.ring_b = ring_b - dyn0;
-        sh.sums = sums_at - dyn0;
+        sh.sums = base + lay.sums - dyn0;
         sh.stages = stages;
         sh.stage_a = a.stage_a;
         sh.stages_b[0] = stages_b1;
@@ -557,10 +546,10 @@ __global__ void __launch_bounds__(kThreads, 1) int4_kernel(const __grid_constant
         // Four columns of the sums from column c[0] .. c[3] on, this thread's row: of the even (0) or odd (1)
         // groups, or all. The loads of all four are in flight at once.
         auto sum_half = [&](const int (&c)[4], int odd, float (&v)[4]) {
-            const float *const s = sums + odd * cols * kSumStride + row;
+            const float *const s = sums + odd * cols * kInt4SumStride + row;
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-                v[i] = s[c[i] * kSumStride] + s[(2 * cols + c[i]) * kSumStride];
+                v[i] = s[c[i] * kInt4SumStride] + s[(2 * cols + c[i]) * kInt4SumStride];
         };
         auto sum_all = [&](const int (&c)[4], float (&v)[4]) {
             float x[4];

@@ -120,6 +120,44 @@ struct Int4Args {
     epk::CheckCtx chk;
 };
 
+constexpr int kInt4StagesA = 12, kInt4StagesB = 16;  // most stages of the rings of weights and tokens
+constexpr int kInt4SumStride = kTileRows + 4;        // column stride of the groups' sums: fragments' stores hit all banks
+constexpr int kInt4Groups = 4;                       // groups of four warps that multiply
+
+// Dynamic shared memory of the 4-bit kernel, in bytes from its first 128-byte
+// boundary on: what does not depend on the ids (fixed_bytes), the groups' sums
+// of this launch's largest entry, the rings. Two pairs of groups take the units
+// in turn, each from its own stage on, so a ring has two stages at least: every
+// handle that can be made has room for them (the CPU tests try all).
+struct Int4Layout {
+    int cols;                  // columns of a sum
+    int stage_b[2], stages_b[2];  // token rings of the two products: bytes of a stage, stages
+    int stages;                // of the weights' ring
+    int sums, ring_b, ring_a;  // where they begin
+};
+
+// smem: bytes there are. A unit's token tile, in 8-token steps of 2 KB a chunk: two chunks, or one (and in the second
+// product two chunks in two parts). The second product's ring begins where the first's did, which is empty by then: h
+// is complete when every block is through with the first. The rings share the room so that about as many token tiles
+// as weight tiles are on their way.
+static __host__ __device__ __forceinline__ Int4Layout int4_layout(bool linear, int smem, int fixed_bytes, int stage_a,
+                                                                  int nmax)
+{
+    const auto least = [](int x, int y) { return x < y ? x : y; };
+    Int4Layout l;
+    l.cols = (nmax + 7) & ~7;
+    l.stage_b[0] = l.cols * (linear ? 512 : 256);
+    l.stage_b[1] = l.cols * (linear ? 512 : 1024);
+    l.sums = (fixed_bytes + 127) & ~127;
+    l.ring_b = l.sums + kInt4Groups * l.cols * kInt4SumStride * 4;
+    const int room = smem - l.ring_b, both = least(kInt4StagesB, room / (stage_a + l.stage_b[1]));
+    l.stages_b[1] = both < 2 ? 2 : both;
+    l.stages_b[0] = least(kInt4StagesB, l.stages_b[1] * l.stage_b[1] / l.stage_b[0]);
+    l.ring_a = l.ring_b + l.stages_b[1] * l.stage_b[1];
+    l.stages = least(kInt4StagesA, (smem - l.ring_a) / stage_a);
+    return l;
+}
+
 struct PackArgs {
     const uint8_t *codes;    // [mats, rows, cols / 2]
     const uint16_t *scales;  // [mats, rows, cols / group]

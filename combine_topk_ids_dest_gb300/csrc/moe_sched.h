@@ -182,34 +182,37 @@ static __device__ __forceinline__ void split(float v, __nv_bfloat16 &hi, __nv_bf
 static __device__ __forceinline__ float swiglu(float gate, float up) { return gate / (1.0f + expf(-gate)) * up; }
 
 // Lists of the chosen experts, in dynamic shared memory. An entry is an expert
-// with up to `cap` of its tokens; an expert with more has two entries.
+// with up to `cap` of its tokens; an expert with more has two entries. What
+// only building them needs lies in `scratch`, 6 P bytes: the kernels give the
+// sums of y, which come into use long after (up to 12 KB less for the rings).
 struct Lists {
     unsigned long long *mask;  // [E] tokens of each expert
     float *weight;             // [P] routing weight of each (entry, token) pair
-    float *given;              // [P] the call's weights
+    float *given;              // [P] the call's weights; scratch
     unsigned short *expert;    // [2 E] of each entry, ascending
     unsigned short *offset;    // [2 E + 1] the entry's first pair
     unsigned short *blocks;    // [2 E + 1] column blocks of 8 tokens before the entry
     unsigned short *start;     // [E] each active expert's first pair
-    short *id;                 // [P] the call's ids, local
+    short *id;                 // [P] the call's ids, local; scratch
     unsigned char *token;      // [P] tokens, ascending per expert
 
-    __device__ __forceinline__ Lists(void *at, int E, int P)
+    __device__ __forceinline__ Lists(void *at, void *scratch, int E, int P)
     {
         mask = static_cast<unsigned long long *>(at);
         weight = reinterpret_cast<float *>(mask + E);
-        given = weight + P;
-        expert = reinterpret_cast<unsigned short *>(given + P);
+        given = static_cast<float *>(scratch);
+        expert = reinterpret_cast<unsigned short *>(weight + P);
         offset = expert + 2 * E;
         blocks = offset + 2 * E + 1;
         start = blocks + 2 * E + 1;
-        id = reinterpret_cast<short *>(start + E);
-        token = reinterpret_cast<unsigned char *>(id + P);
+        id = reinterpret_cast<short *>(given + P);
+        token = reinterpret_cast<unsigned char *>(start + E);
     }
     __device__ __forceinline__ int count(int i) const { return offset[i + 1] - offset[i]; }
 };
 
-static inline size_t lists_bytes(int E, int P) { return size_t(E) * 22 + size_t(P) * 11 + 4; }
+static inline size_t lists_bytes(int E, int P) { return size_t(E) * 22 + size_t(P) * 5 + 4; }
+static_assert(6 * EP_MAX_TOP_K <= 4 * kTileRows, "the scratch fits a token's row of the sums of y");
 
 // Builds the lists; every block does, from the ids themselves, with one trip
 // to memory and four barriers. A token's bit in its expert's mask makes the

@@ -61,6 +61,7 @@ cudaError_t record(const void *func, dim3 grid, dim3 block, size_t smem, void **
     Launch l{name->second, s.device, grid, block, smem, {}};
     const size_t bytes = l.name.find("many_kernel") != std::string::npos   ? sizeof(moe::RouterArgs)
                          : l.name.find("int4_kernel") != std::string::npos ? sizeof(moe::Int4Args)
+                         : l.name.find("experts_kernel") != std::string::npos ? sizeof(moe::ExpertsArgs)
                                                                            : 0;
     if (bytes)
         l.args.assign(static_cast<unsigned char *>(args[0]), static_cast<unsigned char *>(args[0]) + bytes);
@@ -238,6 +239,60 @@ void fake_router_args(int i, int *v)
     const moe::RouterArgs &a = *reinterpret_cast<const moe::RouterArgs *>(state().launches[i].args.data());
     v[0] = a.rows;
     v[1] = a.stages;
+}
+// Every accepted call of 4-bit experts: up to `tokens` tokens, `top_k` choices, `experts` experts, weight tiles of
+// groups of 32 to 128 with and without zero points, entries of 8 to 32 tokens; and every linear call. v: the fewest stages
+// of the three rings, and the configuration (T, K, E, group, zeros, nmax) where the weights' ring has fewest; the
+// largest number of bytes by which a launch's memory ends after what it has.
+void fake_int4_walk(int tokens, int top_k, int experts, int *v)
+{
+    v[0] = v[1] = v[2] = 1 << 30;
+    v[9] = -(1 << 30);
+    const auto look = [&](bool linear, int T, int K, int E, int group, int zeros) {
+        moe::Int4Args a = {};
+        a.T = T;
+        a.E = E;
+        a.P = linear ? 0 : T * K;
+        a.group1 = a.group2 = group;
+        a.tile1 = moe::int4_tile_bytes(group, zeros != 0);
+        a.tile2 = moe::int4_tile_bytes(128, false);  // the largest tile sets the stage
+        const int have = static_cast<int>(moe::int4_smem(&a, linear)) - 127;  // the worst alignment of its start
+        for (int nmax = 8; nmax <= 32 && nmax <= ((T + 7) & ~7); nmax += 8) {
+            const moe::Int4Layout l = moe::int4_layout(linear, have, a.fixed_bytes, a.stage_a, nmax);
+            v[1] = l.stages_b[0] < v[1] ? l.stages_b[0] : v[1];
+            v[2] = l.stages_b[1] < v[2] ? l.stages_b[1] : v[2];
+            const int end = l.ring_a + l.stages * a.stage_a - have;
+            v[9] = end > v[9] ? end : v[9];
+            if (l.stages < v[0]) {
+                const int at[7] = {l.stages, T, K, E, group, zeros, nmax};
+                v[0] = at[0];
+                memcpy(v + 3, at + 1, 6 * sizeof(int));
+            }
+        }
+    };
+    for (int group = 32; group <= 128; group *= 2)
+        for (int zeros = 0; zeros < 2; ++zeros)
+            for (int T = 1; T <= tokens; ++T) {
+                look(true, T, 1, 1, group, zeros);
+                for (int K = 1; K <= top_k; ++K)
+                    for (int E = 1; E <= experts; ++E)
+                        look(false, T, K, E, group, zeros);
+            }
+}
+// Launch i, of the 4-bit kernel: what its layout follows from.
+void fake_int4_args(int i, int *v)
+{
+    const moe::Int4Args &a = *reinterpret_cast<const moe::Int4Args *>(state().launches[i].args.data());
+    v[0] = a.smem;
+    v[1] = a.fixed_bytes;
+    v[2] = a.stage_a;
+}
+// Launch i, of the bf16 experts: stages of the weights' ring, and of the tokens' for an entry of all tokens.
+void fake_experts_args(int i, int *v)
+{
+    const moe::ExpertsArgs &a = *reinterpret_cast<const moe::ExpertsArgs *>(state().launches[i].args.data());
+    v[0] = a.stages;
+    v[1] = a.bytes_b / ((a.T + 7) / 8 * 16 * 128);
 }
 
 }  // extern "C"

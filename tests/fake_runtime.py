@@ -71,3 +71,27 @@ class Fake:
         size = ctypes.c_size_t(0)
         assert self.L.ep_router_workspace_size(h, n, ctypes.byref(size)) == _lib.EP_OK
         return self.L.ep_router_run(h, ADDRESS, hidden, n, ADDRESS, ADDRESS, ADDRESS, size.value, None), size.value
+
+    def experts(self, group=0, zeros=0, **kw):
+        b = dict(num_experts=8, first_expert=0, top_k=8, hidden=256, intermediate=256, max_tokens=64)
+        b.update(kw)
+        w = [_lib.EpWeightC(ADDRESS, group, zeros, 0)] * 2
+        cfg = _lib.EpExpertsConfigC(*b.values(), *w)
+        h = ctypes.c_void_p()
+        assert self.L.ep_experts_create(ctypes.byref(cfg), None, 0, ctypes.byref(h)) == _lib.EP_OK, self.message()
+        return h.value
+
+    def linear(self, inputs=256, outputs=300, max_tokens=64):
+        cfg = _lib.EpLinearConfigC(inputs, outputs, max_tokens, _lib.EpWeightC(ADDRESS, 128, 0, 0))
+        h = ctypes.c_void_p()
+        assert self.L.ep_linear_create(ctypes.byref(cfg), None, 0, ctypes.byref(h)) == _lib.EP_OK, self.message()
+        return h.value
+
+    def run_experts(self, h, n, hidden=256):
+        return self.L.ep_experts_run(h, ADDRESS, hidden, ADDRESS, ADDRESS, n, ADDRESS, hidden, None)
+
+    def run_linear(self, h, n, inputs=256, outputs=300):
+        return self.L.ep_linear_run(h, _lib.EP_DTYPE_BF16, ADDRESS, inputs, n, ADDRESS, outputs, None)
+
+    def run_layer(self, r, h, n, hidden=256):
+        return self.L.ep_layer_run(r, h, ADDRESS, hidden, n, ADDRESS, ADDRESS, ADDRESS, hidden, None)

@@ -4,6 +4,7 @@ import pytest
 import torch
 
 from combine_topk_ids_dest_gb300 import EpRouter
+from test_gpu_moe_experts import _case, _check as _check_experts
 from test_gpu_moe_router import _check, _inputs
 
 pytestmark = pytest.mark.gpu
@@ -16,3 +17,15 @@ def test_router_where_the_number_of_splits_changes(cuda_device, T, H):
     x, w, b = _inputs(T, H, 256, seed=T, bias=True)
     router = EpRouter(w, 8, "sigmoid", bias=b, num_groups=8, top_groups=4, scale=2.5)
     assert _check(router, x, w, b, 8, "sigmoid", 8, 4, scale=2.5) > 0.5
+
+
+@pytest.mark.parametrize("T,E,K,group,zeros", [(64, 512, 32, 32, True), (64, 512, 22, 32, True), (58, 504, 32, 32, False),
+                                               (64, 384, 26, 64, True), (64, 512, 29, 128, False), (63, 257, 32, 0, False),
+                                               (64, 512, 32, 0, False)])
+def test_experts_with_long_lists(cuda_device, T, E, K, group, zeros):
+    """Lists, sums and rings at their largest: experts of 64 tokens (two entries), of 25 to 32, of a few."""
+    gen = torch.Generator(device="cuda").manual_seed(K)
+    ids = torch.rand(T, E, generator=gen, device="cuda").argsort(1)[:, :K].int()
+    ids[:, :4] = torch.tensor([0, E - 1, E // 2, 3], device="cuda")
+    ids[: T // 2, 4] = 5
+    _check_experts(*_case(T, 128 if group == 128 else 192, 128 if group else 136, E, K, group, zeros, seed=E + K, ids=ids))

@@ -41,3 +41,30 @@ def test_router_tiles_hold_their_rows(fake, sms, hidden, E):
             assert tiles * splits <= sms and splits <= -(-hidden // 64)
             assert workspace >= tiles * splits * 128 * E * 4
     assert fake.L.ep_router_destroy(h) == _lib.EP_OK
+
+
+def test_int4_rings_have_two_stages(fake):
+    """Two pairs of groups step through the weights' ring by two, each from its own stage on: one stage would let them
+    read past the block's memory. Every number of tokens, choices and experts, every kind of tile and entry."""
+    v = (ctypes.c_int * 10)()
+    fake.L.fake_int4_walk(64, 32, 512, v)
+    least_a, least_b1, least_b2, *where, past = v
+    assert least_a >= 2 and least_b1 >= 2 and least_b2 >= 2, (least_a, least_b1, least_b2, where)
+    assert past <= 0
+
+
+def test_experts_of_the_largest_size_launch(fake):
+    args = (ctypes.c_int * 3)()
+    for group, zeros in ((0, 0), (32, 1), (128, 0)):
+        h = fake.experts(group, zeros, num_experts=512, top_k=32)
+        fake.L.fake_clear()
+        assert fake.run_experts(h, 64) == _lib.EP_OK, fake.message()
+        (name, _, grid, _, smem), = fake.launches()
+        assert grid == (152, 1, 1) and smem <= 227 * 1024
+        if group:
+            fake.L.fake_int4_args(0, args)
+            assert "int4_kernel" in name and args[0] == smem
+        else:
+            fake.L.fake_experts_args(0, args)
+            assert "experts_kernel" in name and args[0] >= 2 and args[1] >= 2
+        assert fake.L.ep_experts_destroy(h) == _lib.EP_OK
