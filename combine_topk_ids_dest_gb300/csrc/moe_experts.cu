@@ -449,13 +449,14 @@ size_t experts_smem(ExpertsArgs *a)
     return 1024 + static_cast<size_t>(a->stages) * kStageA + a->bytes_b + lists;
 }
 
+cudaError_t experts_setup()
+{
+    return cudaFuncSetAttribute(experts_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                kSmemMax - 64 - static_cast<int>(sizeof(Shared)));
+}
+
 cudaError_t launch_experts(const ExpertsArgs &a, int grid, size_t smem, cudaStream_t stream)
 {
-    static const cudaError_t attr =
-        cudaFuncSetAttribute(experts_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             kSmemMax - 64 - static_cast<int>(sizeof(Shared)));
-    if (attr != cudaSuccess)
-        return attr;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(grid);
     cfg.blockDim = dim3(kThreads);

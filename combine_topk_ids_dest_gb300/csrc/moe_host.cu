@@ -255,6 +255,11 @@ ep_status ep_router_create(const ep_router_config *cfg, ep_router **out)
     r->sms = sms;
     st = encode_map(&r->mw, "weight", cfg->dtype == EP_DTYPE_FP16, cfg->weight, cfg->hidden, cfg->num_experts, 0,
                     cfg->hidden, 0, moe::kChunk, moe::router_all_columns(cfg->num_experts) / 2);
+    if (st == EP_OK) {
+        const cudaError_t ce = moe::router_setup(router_args(*cfg, sms, 1));
+        if (ce != cudaSuccess)
+            st = cuda_error(ce, "the router's kernels");
+    }
     if (st == EP_OK)
         st = r->flags.make();
     if (st == EP_OK) {
@@ -385,7 +390,9 @@ struct Base {
     bool owns_ws = false;
     Flags flags;
 
-    ep_status open(void *workspace, size_t bytes, size_t need, size_t off_words, size_t words)
+    // setup: sets the attributes of the handle's kernels on the current device.
+    template <class Setup>
+    ep_status open(void *workspace, size_t bytes, size_t need, size_t off_words, size_t words, Setup setup)
     {
         if (workspace && (!aligned(workspace, 256) || bytes < need))
             MOE_FAIL("workspace has %zu bytes, needs %zu, 256-byte aligned", bytes, need);
@@ -393,19 +400,22 @@ struct Base {
         if (st != EP_OK)
             return st;
         sms = sms < kMaxBlocks ? sms : kMaxBlocks;
+        cudaError_t ce = setup();
+        if (ce != cudaSuccess)
+            return cuda_error(ce, "the handle's kernels");
         st = flags.make();
         if (st != EP_OK)
             return st;
         ws = static_cast<uint8_t *>(workspace);
         if (!ws) {
-            const cudaError_t ce = cudaMalloc(reinterpret_cast<void **>(&ws), need);
+            ce = cudaMalloc(reinterpret_cast<void **>(&ws), need);
             if (ce != cudaSuccess) {
                 ws = nullptr;
                 return cuda_error(ce, "cudaMalloc");
             }
             owns_ws = true;
         }
-        cudaError_t ce = cudaMemset(ws + off_words, 0, words * 4);
+        ce = cudaMemset(ws + off_words, 0, words * 4);
         if (ce == cudaSuccess)
             ce = cudaStreamSynchronize(nullptr);
         return ce == cudaSuccess ? EP_OK : cuda_error(ce, "clearing the counters");
@@ -557,7 +567,7 @@ ep_status ep_linear_create(const ep_linear_config *cfg, void *workspace, size_t 
     if (!h)
         return set_error(EP_ERR_OOM, "host allocation of the handle failed");
     h->cfg = *cfg;
-    st = h->base.open(workspace, bytes, l.total, l.off_words, l.words);
+    st = h->base.open(workspace, bytes, l.total, l.off_words, l.words, [] { return moe::int4_setup(true); });
     if (st != EP_OK) {
         h->base.close();
         delete h;
@@ -763,7 +773,8 @@ ep_status ep_experts_create(const ep_experts_config *cfg, void *workspace, size_
         return set_error(EP_ERR_OOM, "host allocation of the handle failed");
     h->cfg = *cfg;
     const long long E = cfg->num_experts, H = cfg->hidden, I = cfg->intermediate;
-    st = h->base.open(workspace, bytes, l.total, l.off_words, l.words);
+    st = h->base.open(workspace, bytes, l.total, l.off_words, l.words,
+                      [&] { return cfg->gate_up.group ? moe::int4_setup(false) : moe::experts_setup(); });
     if (st == EP_OK && cfg->gate_up.group == 0)
         st = encode_map(&h->mw1, "gate_up", 0, cfg->gate_up.data, H, I, 2 * E, H, I * H, moe::kChunk, moe::kTileRows);
     if (st == EP_OK && cfg->gate_up.group == 0)

@@ -883,20 +883,29 @@ size_t int4_smem(Int4Args *a, bool linear)
     return a->smem;
 }
 
+namespace {
+
+using Kernel = void (*)(Int4Args);
+
+Kernel kernel_of(bool linear, bool bf16)
+{
+    return !linear ? int4_kernel<false, true> : bf16 ? int4_kernel<true, true> : int4_kernel<true, false>;
+}
+
+}  // namespace
+
+cudaError_t int4_setup(bool linear)
+{
+    cudaError_t ce = cudaSuccess;
+    for (const bool bf16 : {true, false})
+        if (ce == cudaSuccess && (linear || bf16))
+            ce = cudaFuncSetAttribute(kernel_of(linear, bf16), cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                      kSmemMax - 64 - static_cast<int>(sizeof(Shared)));
+    return ce;
+}
+
 cudaError_t launch_int4(const Int4Args &a, bool linear, bool bf16, int grid, size_t smem, cudaStream_t stream)
 {
-    using Kernel = void (*)(Int4Args);
-    static const Kernel kernels[3] = {int4_kernel<false, true>, int4_kernel<true, true>, int4_kernel<true, false>};
-    static const cudaError_t attr = [] {
-        cudaError_t ce = cudaSuccess;
-        for (Kernel k : kernels)
-            if (ce == cudaSuccess)
-                ce = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                          kSmemMax - 64 - static_cast<int>(sizeof(Shared)));
-        return ce;
-    }();
-    if (attr != cudaSuccess)
-        return attr;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(grid);
     cfg.blockDim = dim3(kThreads);
@@ -912,7 +921,7 @@ cudaError_t launch_int4(const Int4Args &a, bool linear, bool bf16, int grid, siz
     }
     cfg.attrs = at;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kernels[linear ? (bf16 ? 1 : 2) : 0], a);
+    return cudaLaunchKernelEx(&cfg, kernel_of(linear, bf16), a);
 }
 
 cudaError_t launch_pack(const PackArgs &a, cudaStream_t stream)

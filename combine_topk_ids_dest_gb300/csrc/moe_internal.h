@@ -61,6 +61,9 @@ int router_counters(int sms);  // words, a multiple of 64
 size_t router_few_parts(const RouterArgs &a);  // bytes of parts for up to kMaxTokens rows
 bool router_many(const RouterArgs &a);  // whether the launch uses mx and mw
 int router_rows(const RouterArgs &a);   // box rows of mx
+// A kernel's attributes belong to one device's copy of it: the setups set, on the current device, those that the
+// launches of a handle with these arguments need. Called whenever a handle is made.
+cudaError_t router_setup(const RouterArgs &a);
 cudaError_t launch_router(const RouterArgs &a, cudaStream_t stream);
 std::vector<const void *> router_kernels();  // every kernel of the file
 
@@ -90,6 +93,7 @@ struct ExpertsArgs {
     epk::CheckCtx chk;
 };
 
+cudaError_t experts_setup();
 cudaError_t launch_experts(const ExpertsArgs &a, int grid, size_t smem, cudaStream_t stream);
 std::vector<const void *> experts_kernels();  // every kernel of the file
 // Dynamic shared memory of a launch for T tokens; sets stages, bytes_b and part_floats.
@@ -173,6 +177,7 @@ size_t int4_part_floats(int T, bool linear);
 size_t int4_h_rows(int T, int K, int E);
 int int4_linear_rows(int T);  // rows of x one run over the weight takes: T in one or two runs, a multiple of 8
 size_t int4_smem(Int4Args *a, bool linear);
+cudaError_t int4_setup(bool linear);
 cudaError_t launch_int4(const Int4Args &a, bool linear, bool bf16, int grid, size_t smem, cudaStream_t stream);
 cudaError_t launch_pack(const PackArgs &a, cudaStream_t stream);
 std::vector<const void *> int4_kernels();  // every kernel of the file

@@ -810,32 +810,35 @@ int router_rows(const RouterArgs &a) { return plan_many(a).rows; }
 
 namespace {
 
-template <int NT, int N, bool BF16> cudaError_t launch_few_n(const RouterArgs &a, cudaStream_t stream)
+using Kernel = void (*)(RouterArgs);
+
+template <int NT> Kernel few_of(const RouterArgs &a)
 {
-    // the experts kernel that usually follows needs all of the SM's memory as shared memory: no change of the split
-    static const cudaError_t attr = cudaFuncSetAttribute(
-        few_kernel<NT, N, BF16>, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared);
-    if (attr != cudaSuccess)
-        return attr;
+    if (a.E <= 128)
+        return a.bf16 ? few_kernel<NT, 4, true> : few_kernel<NT, 4, false>;
+    if (a.E <= 256)
+        return a.bf16 ? few_kernel<NT, 8, true> : few_kernel<NT, 8, false>;
+    return a.bf16 ? few_kernel<NT, 16, true> : few_kernel<NT, 16, false>;
+}
+
+template <bool PAIR> Kernel many_of(const RouterArgs &a)
+{
+    if (a.E <= 128)
+        return a.bf16 ? many_kernel<4, true, PAIR> : many_kernel<4, false, PAIR>;
+    if (a.E <= 256)
+        return a.bf16 ? many_kernel<8, true, PAIR> : many_kernel<8, false, PAIR>;
+    return a.bf16 ? many_kernel<12, true, PAIR> : many_kernel<12, false, PAIR>;
+}
+
+template <int NT> cudaError_t launch_few(const RouterArgs &a, cudaStream_t stream)
+{
     const dim3 grid((a.E + 15) / 16, few_splits(a), (a.T + NT * 8 - 1) / (NT * 8));
-    few_kernel<NT, N, BF16><<<grid, NT * 256, 0, stream>>>(a);
+    few_of<NT>(a)<<<grid, NT * 256, 0, stream>>>(a);
     return cudaGetLastError();
 }
 
-template <int NT, bool BF16> cudaError_t launch_few(const RouterArgs &a, cudaStream_t stream)
+template <bool PAIR> cudaError_t launch_many(RouterArgs a, const ManyPlan &p, cudaStream_t stream)
 {
-    return a.E <= 128   ? launch_few_n<NT, 4, BF16>(a, stream)
-           : a.E <= 256 ? launch_few_n<NT, 8, BF16>(a, stream)
-                        : launch_few_n<NT, 16, BF16>(a, stream);
-}
-
-template <int N, bool BF16, bool PAIR> cudaError_t launch_many_n(RouterArgs a, const ManyPlan &p, cudaStream_t stream)
-{
-    static const cudaError_t attr =
-        cudaFuncSetAttribute(many_kernel<N, BF16, PAIR>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             kSmemMax - 64 - static_cast<int>(sizeof(Shared)));
-    if (attr != cudaSuccess)
-        return attr;
     const int E16 = router_all_columns(a.E), stage = 16384 + E16 * (PAIR ? 64 : 128);
     a.rows = p.rows;
     a.tmem_cols = 512;
@@ -861,34 +864,38 @@ template <int N, bool BF16, bool PAIR> cudaError_t launch_many_n(RouterArgs a, c
     }
     cfg.attrs = at;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, many_kernel<N, BF16, PAIR>, a);
-}
-
-template <bool BF16> cudaError_t launch_many(const RouterArgs &a, cudaStream_t stream)
-{
-    const ManyPlan p = plan_many(a);
-    const bool pair = p.splits == 1;
-    if (a.E <= 128)
-        return pair ? launch_many_n<4, BF16, true>(a, p, stream) : launch_many_n<4, BF16, false>(a, p, stream);
-    if (a.E <= 256)
-        return pair ? launch_many_n<8, BF16, true>(a, p, stream) : launch_many_n<8, BF16, false>(a, p, stream);
-    return pair ? launch_many_n<12, BF16, true>(a, p, stream) : launch_many_n<12, BF16, false>(a, p, stream);
+    return cudaLaunchKernelEx(&cfg, many_of<PAIR>(a), a);
 }
 
 }  // namespace
 
+cudaError_t router_setup(const RouterArgs &a)
+{
+    cudaError_t ce = cudaSuccess;
+    // the experts kernel that usually follows needs all of the SM's memory as shared memory: no change of the split
+    for (const Kernel k : {few_of<1>(a), few_of<2>(a)})
+        if (ce == cudaSuccess)
+            ce = cudaFuncSetAttribute(k, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared);
+    for (const Kernel k : {many_of<true>(a), many_of<false>(a)})
+        if (ce == cudaSuccess && a.E <= kManyExperts)
+            ce = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                      kSmemMax - 64 - static_cast<int>(sizeof(Shared)));
+    return ce;
+}
+
 cudaError_t launch_router(const RouterArgs &all, cudaStream_t stream)
 {
-    if (router_many(all))
-        return all.bf16 ? launch_many<true>(all, stream) : launch_many<false>(all, stream);
+    if (router_many(all)) {
+        const ManyPlan p = plan_many(all);
+        return p.splits == 1 ? launch_many<true>(all, p, stream) : launch_many<false>(all, p, stream);
+    }
     RouterArgs a = all;
     for (int t = 0; t < all.T; t += kSlice) {
         a.T = all.T - t < kSlice ? all.T - t : kSlice;
         a.x = static_cast<const uint16_t *>(all.x) + t * all.x_stride;
         a.ids = all.ids + static_cast<size_t>(t) * a.K;
         a.weights = all.weights + static_cast<size_t>(t) * a.K;
-        const cudaError_t ce = a.T <= 8 ? (a.bf16 ? launch_few<1, true>(a, stream) : launch_few<1, false>(a, stream))
-                                        : (a.bf16 ? launch_few<2, true>(a, stream) : launch_few<2, false>(a, stream));
+        const cudaError_t ce = a.T <= 8 ? launch_few<1>(a, stream) : launch_few<2>(a, stream);
         if (ce != cudaSuccess)
             return ce;
     }

@@ -68,3 +68,24 @@ def test_experts_of_the_largest_size_launch(fake):
             fake.L.fake_experts_args(0, args)
             assert "experts_kernel" in name and args[0] >= 2 and args[1] >= 2
         assert fake.L.ep_experts_destroy(h) == _lib.EP_OK
+
+
+def test_handles_of_two_devices_launch_on_both(fake):
+    """A kernel's shared-memory limit belongs to the device that was current when it was set."""
+    made = []
+    for device in (0, 1, 0):
+        fake.L.fake_device(device)
+        made.append((device, fake.router(hidden=256), fake.experts(), fake.experts(64), fake.linear()))
+    for device, router, dense, int4, linear in made:
+        fake.L.fake_device(device)
+        fake.L.fake_clear()
+        for n in (1, 60, 300, 20000):
+            assert fake.route(router, n, 256)[0] == _lib.EP_OK, (device, n, fake.message())
+        for h in (dense, int4):
+            assert fake.run_experts(h, 5) == _lib.EP_OK, (device, fake.message())
+        assert fake.run_linear(linear, 5) == _lib.EP_OK, (device, fake.message())
+        assert [l[1] for l in fake.launches()] == [device] * 7
+    for device, router, dense, int4, linear in made:
+        fake.L.fake_device(device)
+        assert fake.L.ep_router_destroy(router) == fake.L.ep_experts_destroy(dense) == _lib.EP_OK
+        assert fake.L.ep_experts_destroy(int4) == fake.L.ep_linear_destroy(linear) == _lib.EP_OK
