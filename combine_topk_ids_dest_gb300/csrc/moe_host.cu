@@ -863,12 +863,15 @@ ep_status ep_layer_run(ep_router *r, ep_experts *h, const void *x, long long x_s
                  r->cfg.top_k, static_cast<int>(r->cfg.dtype), h->cfg.hidden, h->cfg.top_k);
     if (num_tokens < 0 || num_tokens > h->cfg.max_tokens)
         MOE_FAIL("num_tokens=%d outside [0, max_tokens=%d]", num_tokens, h->cfg.max_tokens);
-    if (num_tokens > 0) {  // nothing is queued unless both calls will be
-        const ep_status st = check_rows("out", out, out_stride, h->cfg.hidden, 2, 1);
-        if (st != EP_OK)
-            return st;
-    }
-    const ep_status st = ep_router_run(r, x, x_stride, num_tokens, ids, weights, nullptr, 0, stream);
+    // nothing is queued unless both calls will be: what only the second checks comes first
+    ep_status st = same_device(h->base.device);
+    if (st == EP_OK && num_tokens > 0)
+        st = check_rows("out", out, out_stride, h->cfg.hidden, 2, 1);
+    if (st == EP_OK && num_tokens > 0)
+        st = h->base.flags.take();
+    if (st != EP_OK)
+        return st;
+    st = ep_router_run(r, x, x_stride, num_tokens, ids, weights, nullptr, 0, stream);
     if (st != EP_OK)
         return st;
     return ep_experts_run(h, x, x_stride, ids, weights, num_tokens, out, out_stride, stream);

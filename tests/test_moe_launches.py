@@ -89,3 +89,23 @@ def test_handles_of_two_devices_launch_on_both(fake):
         fake.L.fake_device(device)
         assert fake.L.ep_router_destroy(router) == fake.L.ep_experts_destroy(dense) == _lib.EP_OK
         assert fake.L.ep_experts_destroy(int4) == fake.L.ep_linear_destroy(linear) == _lib.EP_OK
+
+
+def test_layer_queues_nothing_unless_both_calls_will_be(fake):
+    router, h = fake.router(hidden=256), fake.experts()
+    words = fake.L.fake_error_words()  # of the experts, which were made last
+    fake.L.fake_clear()
+    words[0] = words[7] = 1  # a wait of an earlier call ran out
+    assert fake.run_layer(router, h, 3) == _lib.EP_ERR_CUDA and "ran out" in fake.message()
+    assert fake.launches() == []
+    assert fake.run_layer(router, h, 3) == _lib.EP_OK and len(fake.launches()) == 2
+    fake.L.fake_device(1)
+    elsewhere = fake.experts()
+    fake.L.fake_device(0)
+    fake.L.fake_clear()
+    for n in (0, 3):
+        assert fake.run_layer(router, elsewhere, n) == _lib.EP_ERR_INVALID_ARG and "device 1" in fake.message()
+    assert fake.launches() == []
+    for x in (h, elsewhere):
+        fake.L.ep_experts_destroy(x)
+    fake.L.ep_router_destroy(router)
