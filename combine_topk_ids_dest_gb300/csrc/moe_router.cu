@@ -186,7 +186,7 @@ template <int N> static __device__ void choose_warp(const RouterArgs &a, int t, 
         float sum = w;  // lanes without a choice have 0
         for (int d = 16; d; d >>= 1)
             sum += __shfl_xor_sync(~0u, sum, d);
-        w = id >= 0 ? w / sum : 0.0f;
+        w = id >= 0 && sum != 0.0f ? w / sum : w;
     }
     if (lane < a.K)
         store_choice(a, t, lane, id, w);
@@ -463,7 +463,7 @@ static __device__ void choose_quad(const RouterArgs &a, int t, bool live, float 
                 a.ids[at + n] = any ? first : EP_INVALID_EXPERT_ID;
         }
     }
-    if (!a.renormalize)
+    if (!a.renormalize || total == 0.0f)  // scores that are all 0 stay so
         total = 1.0f;
 #pragma unroll
     for (int i = 0; i < EP_MAX_TOP_K / 4; ++i) {

@@ -47,7 +47,7 @@ extern "C" {
  * chosen, in descending order of c. Ties, of groups too, go to the lowest
  * index. A softmax router without bias and groups ranks by l itself.
  * weights = s of the chosen (without bias), divided by their sum if
- * renormalize, times scale.
+ * renormalize (scores that are all 0 in fp32 stay 0), times scale.
  * An expert whose c is -infinity (a bias of -infinity masks it) or NaN is
  * never chosen; where fewer than top_k are left, the remaining ids are
  * EP_INVALID_EXPERT_ID with weight 0, which ep_dispatch routes nowhere.
