@@ -60,9 +60,14 @@ static __device__ __forceinline__ bool ranks_by_logit(const RouterArgs &a)
     return a.scoring == EP_SCORE_SOFTMAX && a.bias == nullptr && a.groups == 1;
 }
 
-// The quotient is within 2 units of the last place (0 where it would be below 2^-126); the correctly rounded one has a
-// branch for each score.
-static __device__ __forceinline__ float sigmoid(float l) { return __fdividef(1.0f, 1.0f + expf(-l)); }
+// From exp(-|l|), so that the divisor lies in [1, 2] and small scores keep their value down to the subnormal ones
+// (1 / (1 + exp(-l)) is 0 from l = -88 on). The quotient is within 2 units of the last place; the correctly rounded
+// one has a branch for each score.
+static __device__ __forceinline__ float sigmoid(float l)
+{
+    const float x = expf(-fabsf(l));
+    return __fdividef(l < 0.0f ? x : 1.0f, 1.0f + x);
+}
 
 static __device__ __forceinline__ void store_choice(const RouterArgs &a, int t, int k, int id, float w)
 {

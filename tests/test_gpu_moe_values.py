@@ -36,3 +36,24 @@ def test_scores_of_zero_have_weights_of_zero(cuda_device, T):
     ids, weights = EpRouter(w, 3, "sigmoid")(x)
     assert ids.tolist() == [[3, 1, 0]] * T and bool((weights[:, 2] == 0).all())
     assert torch.allclose(weights.sum(1), torch.ones(T, device="cuda"), atol=1e-6)
+
+
+@pytest.mark.parametrize("T", TOKENS)
+def test_subnormal_sigmoid_scores(cuda_device, T):
+    """sigmoid(l) down to fp32's smallest numbers. Exponential and quotient are within 2 units each, or 2^-149 where the
+    result is subnormal; the sum and the division by it add a few units more."""
+    values = [-86.0 - 0.5 * e for e in range(20)]  # exp(-95.5) is 2300 times 2^-149
+    x, w = _logits(T, values)
+    s = torch.sigmoid(torch.tensor(values, dtype=torch.float64, device="cuda"))
+    off = 8 * 2.0 ** -24 + 3 * 2.0 ** -149 / s
+    order = [e for e in range(20) if e > 11][:6]
+    bias = torch.zeros(20, device="cuda")
+    bias[order] = torch.arange(6, 0, -1, device="cuda").float()
+    for scale in (1.0, 2.5):
+        ids, weights = EpRouter(w, 6, "sigmoid", bias=bias, scale=scale)(x)
+        assert ids.tolist() == [order] * T
+        want = s[order] / s[order].sum() * scale
+        assert bool(((weights.double() - want).abs() <= want * (off[order] + off[order].max() + 8 * 2.0 ** -24)).all())
+    ids, weights = EpRouter(w, 20, "sigmoid", renormalize=False)(x)
+    assert ids.tolist() == [list(range(20))] * T
+    assert bool(((weights.double() - s).abs() <= s * off).all())
