@@ -62,6 +62,19 @@ ep_status same_device(int want)
     return EP_OK;
 }
 
+// Waits for all work of a device: before a handle's memory is freed, or is its owner's again.
+void wait_for_device(int device)
+{
+    int now = device;
+    cudaGetDevice(&now);
+    if (now != device)
+        cudaSetDevice(device);
+    if (cudaDeviceSynchronize() != cudaSuccess)
+        cudaGetLastError();  // the next call reports it
+    if (now != device)
+        cudaSetDevice(now);
+}
+
 // cuTensorMapEncodeTiled, found through the runtime (the library does not link libcuda).
 using EncodeTiled = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
                                  const cuuint64_t *, const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave,
@@ -341,8 +354,8 @@ ep_status ep_router_run(ep_router *r, const void *x, long long x_stride, int num
 ep_status ep_router_destroy(ep_router *r)
 {
     if (r) {
-        if (r->counters)
-            cudaFree(r->counters);  // waits for work that uses them
+        wait_for_device(r->device);
+        cudaFree(r->counters);
         r->flags.free();
         delete r;
     }
@@ -422,8 +435,10 @@ struct Base {
     }
     void close()
     {
+        if (ws)  // the handle was made: work that uses it may be queued
+            wait_for_device(device);
         if (owns_ws && ws)
-            cudaFree(ws);  // waits for work that uses it
+            cudaFree(ws);
         ws = nullptr;
         flags.free();
     }

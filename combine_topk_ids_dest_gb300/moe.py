@@ -10,7 +10,7 @@ and streams only. Weights are kept by reference, not copied.
 
 Calls on one object must be ordered on the device (one stream, or streams
 with events between them): it holds one call's intermediate results. Create
-objects outside CUDA graph captures; calls can be captured.
+objects, and let them go, outside CUDA graph captures; calls can be captured.
 """
 from __future__ import annotations
 
@@ -51,7 +51,7 @@ class _Handle:
         self._h = None
 
     def destroy(self) -> None:
-        """Free the handle; repeated calls do nothing."""
+        """Wait for the device and free the handle; repeated calls do nothing."""
         h, self._h = getattr(self, "_h", None), None
         if h is not None:
             check(getattr(self._L, self._destroy)(h))

@@ -15,9 +15,10 @@
  * launches anything, queues its work on the given stream and returns.
  * Calls on one handle must be ordered on the device too (one stream, or
  * streams with events between them): a handle's workspace holds one call's
- * intermediate results. Handles are created outside stream captures; run
- * calls can be captured. Tensors that a capture or a queued call uses must
- * stay valid until it has run.
+ * intermediate results. Handles are created and destroyed outside stream
+ * captures; destroying one waits for its device, so that its workspace can be
+ * freed or used again at once. Run calls can be captured. Tensors that a
+ * capture or a queued call uses must stay valid until it has run.
  *
  * The blocks of the experts' kernels, and of the router's where it splits the
  * inputs, wait for one another (they are launched cooperatively); every wait,

@@ -109,3 +109,22 @@ def test_layer_queues_nothing_unless_both_calls_will_be(fake):
     for x in (h, elsewhere):
         fake.L.ep_experts_destroy(x)
     fake.L.ep_router_destroy(router)
+
+
+def test_destroy_waits_for_the_handles_device(fake):
+    """Queued work still uses a handle's workspace, which its owner may hand out again once destroy has returned, and its
+    error words, which destroy frees."""
+    fake.L.fake_device(1)
+    made = [("ep_router_destroy", fake.router(hidden=256)), ("ep_experts_destroy", fake.experts()),
+            ("ep_experts_destroy", fake.experts(64)), ("ep_linear_destroy", fake.linear())]
+    fake.L.fake_device(0)  # the device that is current at destroy may be another
+    for destroy, h in made:
+        fake.L.fake_clear()
+        assert getattr(fake.L, destroy)(h) == _lib.EP_OK
+        calls = fake.calls()
+        assert calls[0] == "cudaDeviceSynchronize 1" and "cudaFreeHost" in calls[1:], calls
+    h = fake.router(hidden=256)
+    fake.L.fake_clear()
+    assert fake.route(h, 1, 256)[0] == _lib.EP_OK
+    assert fake.launches()[0][1] == 0  # the current device is as it was
+    fake.L.ep_router_destroy(h)
