@@ -300,8 +300,8 @@ ep_status ep_router_workspace_size(const ep_router *r, int num_tokens, size_t *b
 {
     if (!r || !bytes)
         MOE_FAIL("handle or bytes is NULL");
-    if (num_tokens < 0)
-        MOE_FAIL("num_tokens=%d < 0", num_tokens);
+    if (num_tokens < 0 || num_tokens > EP_ROUTER_MAX_TOKENS)
+        MOE_FAIL("num_tokens=%d outside [0, %d]", num_tokens, EP_ROUTER_MAX_TOKENS);
     *bytes = moe::router_workspace(router_args(r->cfg, r->sms, num_tokens));
     return set_error(EP_OK, "");
 }
@@ -312,8 +312,8 @@ ep_status ep_router_run(ep_router *r, const void *x, long long x_stride, int num
     Range range("ep_router_run");
     if (!r)
         MOE_FAIL("handle is NULL");
-    if (num_tokens < 0)
-        MOE_FAIL("num_tokens=%d < 0", num_tokens);
+    if (num_tokens < 0 || num_tokens > EP_ROUTER_MAX_TOKENS)
+        MOE_FAIL("num_tokens=%d outside [0, %d]", num_tokens, EP_ROUTER_MAX_TOKENS);
     ep_status st = same_device(r->device);
     if (st != EP_OK)
         return st;

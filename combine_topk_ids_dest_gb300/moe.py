@@ -74,6 +74,8 @@ class _Handle:
         shape = x.shape
         if len(shape) != 2 or shape[1] != cols:
             raise ValueError(f"{name} must be a [tokens, {cols}] tensor, got {tuple(shape)}")
+        if shape[0] > 0x7FFFFFFF:
+            raise ValueError(f"{name} has {shape[0]} rows, at most 2^31 - 1 fit a call")
         if x.is_contiguous():
             return shape[0], cols
         if x.stride(1) != 1 and cols != 1:

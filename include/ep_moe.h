@@ -38,6 +38,7 @@ extern "C" {
 #define EP_MOE_MAX_TOKENS 64     /* rows of one experts or linear call */
 #define EP_MOE_MAX_EXPERTS 512   /* experts of a router; local experts of an experts handle */
 #define EP_MOE_MAX_DIM 65536     /* hidden, intermediate, inputs */
+#define EP_ROUTER_MAX_TOKENS 2147483136 /* rows of one router call: 2^31 - 512 */
 
 /* ---- router ------------------------------------------------------------------
  * l = x W^T in fp32; s = sigmoid(l), or softmax(l) over the experts.
@@ -80,7 +81,8 @@ ep_status ep_router_workspace_size(const ep_router *r, int num_tokens, size_t *b
  * of 8, >= hidden), 16-byte aligned; ids: device int32 and weights: device
  * fp32 [num_tokens, top_k], contiguous. workspace: device, 256-byte aligned,
  * of workspace_bytes >= ep_router_workspace_size (used by this call alone).
- * num_tokens 0 does nothing. Up to EP_MOE_MAX_TOKENS rows need no workspace. */
+ * 0 <= num_tokens <= EP_ROUTER_MAX_TOKENS; 0 does nothing. Up to
+ * EP_MOE_MAX_TOKENS rows need no workspace. */
 ep_status ep_router_run(ep_router *r, const void *x, long long x_stride, int num_tokens, int32_t *ids,
                         float *weights, void *workspace, size_t workspace_bytes, void *stream);
 

@@ -3,8 +3,9 @@ kernels' buffers hold, for every accepted call."""
 import ctypes
 
 import pytest
+import torch
 
-from combine_topk_ids_dest_gb300 import _lib
+from combine_topk_ids_dest_gb300 import EpRouter, _lib
 from fake_runtime import Fake
 
 
@@ -128,3 +129,35 @@ def test_destroy_waits_for_the_handles_device(fake):
     assert fake.route(h, 1, 256)[0] == _lib.EP_OK
     assert fake.launches()[0][1] == 0  # the current device is as it was
     fake.L.ep_router_destroy(h)
+
+
+def test_rows_that_the_kernels_cannot_count_are_refused(fake):
+    """Rows are int32 in the kernels, with a tile's or a slice's room above the last one."""
+    for E in (64, 512):  # tiles of many tokens; slices of 256
+        h = fake.router(hidden=8, num_experts=E)
+        for n in (2**31 - 1, 2**31 - 511):
+            fake.L.fake_clear()
+            size = ctypes.c_size_t(0)
+            assert fake.L.ep_router_workspace_size(h, n, ctypes.byref(size)) == _lib.EP_ERR_INVALID_ARG
+            assert fake.L.ep_router_run(h, 4096, 8, n, 4096, 4096, 4096, 1 << 40, None) == _lib.EP_ERR_INVALID_ARG
+            assert "num_tokens" in fake.message() and fake.launches() == []
+        fake.L.ep_router_destroy(h)
+    h = fake.router(hidden=8, num_experts=64)
+    fake.L.fake_clear()
+    assert fake.route(h, 2**31 - 512, 8)[0] == _lib.EP_OK, fake.message()
+    (_, _, (tiles, splits, _), _, _), = fake.launches()
+    args = (ctypes.c_int * 2)()
+    fake.L.fake_router_args(0, args)
+    assert splits == 1 and args[0] <= 128 and 2**31 - 512 <= tiles * args[0] <= 2**31 - 1
+    fake.L.ep_router_destroy(h)
+
+
+def test_binding_refuses_rows_that_do_not_fit_the_abi():
+    """The C ABI's counts are int: 2^32 + 5 rows would be taken for 5."""
+    h = EpRouter.__new__(EpRouter)
+    h._h, h._index, h.device = None, -1, torch.device("cpu")
+    x = torch.zeros(1, 8, dtype=torch.bfloat16)
+    assert h._rows(x.expand(2**31 - 1, 8), 8, torch.bfloat16)[0] == 2**31 - 1
+    for n in (2**31, 2**32 + 5):
+        with pytest.raises(ValueError, match="rows"):
+            h._rows(x.expand(n, 8), 8, torch.bfloat16)
