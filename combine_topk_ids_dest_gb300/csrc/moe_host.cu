@@ -1,5 +1,6 @@
 // moe_host.cu -- the C ABI of include/ep_moe.h: handles, argument checks,
 // tensor maps and launches of the MoE operators.
+#include <climits>
 #include <cmath>
 #include <cstring>
 #include <mutex>
@@ -681,8 +682,8 @@ ep_status plan_experts(const ep_experts_config *c, ExpertsLayout *l)
         MOE_FAIL("config is NULL");
     if (c->num_experts < 1 || c->num_experts > EP_MOE_MAX_EXPERTS)
         MOE_FAIL("num_experts=%d outside [1, %d]", c->num_experts, EP_MOE_MAX_EXPERTS);
-    if (c->first_expert < 0)
-        MOE_FAIL("first_expert=%d < 0", c->first_expert);
+    if (c->first_expert < 0 || c->first_expert > INT_MAX - (c->num_experts - 1))
+        MOE_FAIL("first_expert=%d: ids of %d experts must fit [0, 2^31)", c->first_expert, c->num_experts);
     if (c->top_k < 1 || c->top_k > EP_MAX_TOP_K)
         MOE_FAIL("top_k=%d outside [1, %d]", c->top_k, EP_MAX_TOP_K);
     if (c->max_tokens < 1 || c->max_tokens > EP_MOE_MAX_TOKENS)

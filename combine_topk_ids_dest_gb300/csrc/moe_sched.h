@@ -225,13 +225,13 @@ static __device__ __forceinline__ void build_lists(const Args &a, const Lists &l
 {
     const int warp = tid >> 5, lane = tid & 31, batches = (a.E + 31) / 32;
     for (int i = tid; i < a.P; i += threads) {
-        int e = -1;
+        unsigned int e = ~0u;  // the local id; foreign ones, negative ones too, come out as a.E or more
         float w = 0.0f;
         if (EP_IN_BOUNDS(a.chk, epk::kSiteMoeIds, a.ids + i, 4, a.ids, 4LL * a.P))
-            e = a.ids[i] - a.first;
+            e = static_cast<unsigned int>(a.ids[i]) - static_cast<unsigned int>(a.first);
         if (EP_IN_BOUNDS(a.chk, epk::kSiteMoeWeights, a.weights + i, 4, a.weights, 4LL * a.P))
             w = a.weights[i];
-        li.id[i] = static_cast<short>(e >= 0 && e < a.E ? e : -1);
+        li.id[i] = static_cast<short>(e < static_cast<unsigned int>(a.E) ? e : -1);
         li.given[i] = w;
     }
     for (int e = tid; e < a.E; e += threads)

@@ -164,7 +164,7 @@ typedef struct ep_experts ep_experts;
 
 typedef struct {
     int num_experts;    /* local experts, 1..EP_MOE_MAX_EXPERTS */
-    int first_expert;   /* global id of the first */
+    int first_expert;   /* global id of the first; the last one's fits int32 too */
     int top_k;          /* 1..EP_MAX_TOP_K */
     int hidden;         /* a multiple of 8 (of the group, for 4-bit weights), <= EP_MOE_MAX_DIM */
     int intermediate;   /* likewise */

@@ -29,3 +29,15 @@ def test_experts_with_long_lists(cuda_device, T, E, K, group, zeros):
     ids[:, :4] = torch.tensor([0, E - 1, E // 2, 3], device="cuda")
     ids[: T // 2, 4] = 5
     _check_experts(*_case(T, 128 if group == 128 else 192, 128 if group else 136, E, K, group, zeros, seed=E + K, ids=ids))
+
+
+@pytest.mark.parametrize("group", [0, 32])
+def test_experts_at_the_end_of_the_ids(cuda_device, group):
+    first = 2**31 - 6
+    gen = torch.Generator(device="cuda").manual_seed(3)
+    ids = torch.randint(first, 2**31, (9, 4), generator=gen, device="cuda").int()
+    ids[0] = torch.tensor([-2**31, -2**31 + 5, -1, 0], device="cuda")  # nothing here
+    ids[1] = torch.tensor([-2**31, 2**31 - 1, first - 1, first], device="cuda")
+    case = _case(9, 192, 160, 6, 4, group, ids=ids, seed=5)
+    _, y = _check_experts(*case, first=first)
+    assert bool((y[0] == 0).all()) and bool((y[1] != 0).any())

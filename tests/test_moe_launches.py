@@ -161,3 +161,18 @@ def test_binding_refuses_rows_that_do_not_fit_the_abi():
     for n in (2**31, 2**32 + 5):
         with pytest.raises(ValueError, match="rows"):
             h._rows(x.expand(n, 8), 8, torch.bfloat16)
+
+
+def test_experts_past_the_ids_are_refused(fake):
+    """An id is int32: with experts numbered past 2^31 - 1, id - first_expert of a negative id wrapped to one of them."""
+    size = ctypes.c_size_t(0)
+
+    def status(first, E):
+        w = [_lib.EpWeightC(4096, 0, 0, 0)] * 2
+        cfg = _lib.EpExpertsConfigC(E, first, 2, 64, 64, 8, *w)
+        return fake.L.ep_experts_workspace_size(ctypes.byref(cfg), ctypes.byref(size))
+
+    for first, E in ((0, 512), (2**31 - 8, 8), (2**31 - 1, 1)):
+        assert status(first, E) == _lib.EP_OK, fake.message()
+    for first, E in ((2**31 - 7, 8), (2**31 - 1, 2), (2**31 - 4, 512)):
+        assert status(first, E) == _lib.EP_ERR_INVALID_ARG and "first_expert" in fake.message()
