@@ -3,6 +3,7 @@
 import pytest
 import torch
 
+import moe_ref
 from combine_topk_ids_dest_gb300 import EpRouter
 from test_gpu_moe_experts import _case, _check as _check_experts
 from test_gpu_moe_router import _check, _inputs
@@ -41,3 +42,44 @@ def test_experts_at_the_end_of_the_ids(cuda_device, group):
     case = _case(9, 192, 160, 6, 4, group, ids=ids, seed=5)
     _, y = _check_experts(*case, first=first)
     assert bool((y[0] == 0).all()) and bool((y[1] != 0).any())
+
+
+@pytest.mark.parametrize("T,H,E,K,scoring,bias,groups,top_groups,dtype", [
+    (10000, 264, 160, 8, "sigmoid", True, 8, 4, torch.bfloat16), (9800, 520, 256, 8, "softmax", True, 1, 1, torch.float16),
+    (9900, 264, 256, 8, "softmax", False, 8, 3, torch.bfloat16), (10001, 264, 257, 6, "sigmoid", True, 1, 1, torch.bfloat16),
+    (9999, 200, 384, 10, "sigmoid", True, 24, 7, torch.float16), (9999, 200, 384, 32, "softmax", True, 1, 1, torch.bfloat16),
+    (12000, 72, 384, 8, "softmax", False, 32, 5, torch.bfloat16), (9800, 264, 300, 4, "softmax", False, 1, 1, torch.float16),
+    (30000, 128, 384, 4, "softmax", True, 12, 5, torch.bfloat16)])
+def test_router_for_many_tokens_and_experts(cuda_device, T, H, E, K, scoring, bias, groups, top_groups, dtype):
+    """Two blocks that multiply together: one instruction up to 256 experts, two above."""
+    x, w, b = _inputs(T, H, E, dtype, seed=E, bias=bias)
+    router = EpRouter(w, K, scoring, bias=b, num_groups=groups, top_groups=top_groups, scale=2.5)
+    _check(router, x, w, b, K, scoring, groups, top_groups, scale=2.5)
+
+
+@pytest.mark.parametrize("T", [3, 64, 65, 257, 700])
+@pytest.mark.parametrize("E,K,scoring,bias,groups,top_groups", [
+    (385, 8, "sigmoid", True, 1, 1), (449, 5, "softmax", True, 1, 1), (512, 8, "sigmoid", True, 32, 9),
+    (512, 32, "softmax", False, 8, 3), (400, 8, "softmax", False, 1, 1)])
+def test_router_of_more_than_384_experts(cuda_device, T, E, K, scoring, bias, groups, top_groups):
+    x, w, b = _inputs(T, 520, E, seed=E + T, bias=bias)
+    router = EpRouter(w, K, scoring, bias=b, num_groups=groups, top_groups=top_groups)
+    _check(router, x, w, b, K, scoring, groups, top_groups)
+
+
+@pytest.mark.parametrize("T", [40, 300, 10000])
+def test_equal_and_masked_experts_among_384(cuda_device, T):
+    x, w, _ = _inputs(T, 256, 4, seed=3)
+    ids, weights = EpRouter(w.repeat(96, 1).contiguous(), 16, "sigmoid")(x)  # experts e, e + 4, ... are the same
+    l = moe_ref.scores(x, w, "sigmoid")[0]
+    gap = torch.sort(l, dim=1, descending=True).values
+    sure = (gap[:, 0] - gap[:, 1]) > 1e-3
+    want = l.argmax(1)[:, None] + 4 * torch.arange(16, device="cuda")
+    assert torch.equal(ids[sure].long(), want[sure]) and torch.equal(weights[sure, 0], weights[sure, 15])
+    x, w, _ = _inputs(T, 256, 384, seed=4)
+    bias = torch.full((384,), -torch.inf, device="cuda")
+    left = [1, 127, 128, 255, 256, 383]
+    bias[left] = 0.0
+    ids, weights = EpRouter(w, 8, "sigmoid", bias=bias)(x)
+    assert bool((ids[:, :6].sort(1).values == torch.tensor(left, device="cuda")).all())
+    assert bool((ids[:, 6:] == -1).all()) and bool((weights[:, 6:] == 0).all())
