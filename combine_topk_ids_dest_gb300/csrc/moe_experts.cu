@@ -23,7 +23,10 @@
 //  - h is kept as the sum of two bf16 values, 16 bits of mantissa: the second
 //    product treats them as two columns, which costs nothing while the
 //    weights are the bottleneck. x and the weights are used as they are, all
-//    sums are fp32, y is rounded once.
+//    sums are fp32, y is rounded once. Against the 64-bit result that leaves
+//    5 to 9 of 1000 values of y at the other bf16 neighbour (4-bit experts,
+//    whose sums are shorter, 3; all 32-bit 0.4), and the norm of the error
+//    at 1.00008 of what the rounding of y alone gives, or less.
 //  - For each row tile of y a block adds its experts' contributions, times
 //    the routing weight, in fp32 in ascending expert order.
 //

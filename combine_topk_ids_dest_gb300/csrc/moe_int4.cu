@@ -80,14 +80,16 @@ __shared__ Shared sh;
 extern __shared__ uint8_t dyn[];
 
 // Cost of a unit of an entry with this many column blocks. Measured for one to
-// four of them 16, 21, 32 and 40 (0.47 to 1.18 us) in the first product, and
-// 18, 29, 45 and 62 in the second, whose blocks share its entries more evenly.
+// four of them 16, 21, 32 and 40 (0.47 to 1.18 us) in the first product, which
+// these fit, and 18, 29, 45 and 62 in the second, where they are up to a third
+// too low for large entries.
 constexpr int kUnitCost = 9, kBlockCost = 8;
 
 // Eight codes to the four registers of an A fragment: pair p has its codes at
 // bits 4p and 4p + 16, so a shift and a mask leave a pair; or-ing the exponent
-// of 128 (bf16; 1024 in fp16) makes them 128 + q. za and zb hold 128 + z twice,
-// for the fragment's rows r and r + 8.
+// of 128 (bf16; 1024 in fp16) makes them 128 + q (published for fp16 by Kim et
+// al., arXiv 2211.10017). za and zb hold 128 + z twice, for the fragment's rows
+// r and r + 8.
 template <bool BF16> static __device__ __forceinline__ void decode(uint32_t w, uint32_t za, uint32_t zb, uint32_t *out)
 {
 #pragma unroll

@@ -39,7 +39,10 @@ namespace {
 
 constexpr int kFewTokens = kMaxTokens;
 constexpr int kSlice = 256;         // tokens of one launch of the kernel for few
-constexpr int kManyExperts = 384;  // a tile's scores fit shared memory; above, the kernel for few
+// A tile's scores of up to so many experts fit shared memory. Above, the kernel for few tokens takes slices of 256, one
+// after the other: 65 tokens x 7168 to 512 experts 35 us, 256 tokens 88 us, 16001 tokens 5.8 ms, where 384 experts,
+// in one launch, take 75 us.
+constexpr int kManyExperts = 384;
 
 // Order-preserving image of a float in the unsigned integers; NaN and -infinity give 0 (never chosen).
 static __device__ __forceinline__ uint32_t ordered(float v)

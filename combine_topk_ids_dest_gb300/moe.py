@@ -263,6 +263,8 @@ class EpExperts(_Workspace):
     afterwards). The experts are the global ids ``first_expert ..``; ids
     outside them are skipped, so one rank's experts run on the rows
     ``EpComm.dispatch`` delivered and write the rows ``EpComm.combine`` adds up.
+    A receive buffer's slots all count, empty ones too: ``ep_size *
+    tokens_per_rank`` is at most 64 there.
     """
 
     _destroy = "ep_experts_destroy"

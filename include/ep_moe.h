@@ -10,9 +10,12 @@
  *             delivered, giving the rows a combine adds up);
  *  - linear:  y = x W^T for a few tokens, W in 4 bits with group scales.
  *
- * Statuses, ep_last_error, streams, devices, threads and the checked build
- * are as in ep.h: every call checks its arguments on the host before it
- * launches anything, queues its work on the given stream and returns.
+ * Statuses, ep_last_error, streams, devices and threads are as in ep.h: every
+ * call checks its arguments on the host before it launches anything, queues its
+ * work on the given stream and returns. The checked build reports as there, but
+ * tests fewer accesses here: the experts' reads of ids and weights, and all
+ * stores of ids, weights and results. Reads of x, weights and biases, packed
+ * weights and workspaces are not tested.
  * Calls on one handle must be ordered on the device too (one stream, or
  * streams with events between them): a handle's workspace holds one call's
  * intermediate results. Handles are created and destroyed outside stream
@@ -168,7 +171,8 @@ typedef struct {
     int top_k;          /* 1..EP_MAX_TOP_K */
     int hidden;         /* a multiple of 8 (of the group, for 4-bit weights), <= EP_MOE_MAX_DIM */
     int intermediate;   /* likewise */
-    int max_tokens;     /* 1..EP_MOE_MAX_TOKENS */
+    int max_tokens;     /* 1..EP_MOE_MAX_TOKENS; after a dispatch: the slots of a receive buffer,
+                           ep_size * tokens_per_rank, empty ones included */
     ep_weight gate_up;  /* [num_experts, 2*intermediate, hidden]: gate rows, then up rows */
     ep_weight down;     /* [num_experts, hidden, intermediate] */
 } ep_experts_config;
