@@ -50,7 +50,14 @@ EXPORTS = ("ep_is_supported", "ep_workspace_size", "ep_create", "ep_create_with_
 MOE_EXPORTS = ("ep_router_create", "ep_router_workspace_size", "ep_router_run", "ep_router_destroy",
                "ep_experts_workspace_size", "ep_experts_create", "ep_experts_run", "ep_experts_destroy",
                "ep_weight_packed_size", "ep_weight_pack", "ep_linear_workspace_size", "ep_linear_create",
-               "ep_linear_run", "ep_linear_destroy", "ep_layer_run")
+               "ep_linear_run", "ep_linear_destroy", "ep_layer_run",
+               "ep_norm_run", "ep_norm_backward_workspace_size", "ep_norm_backward",
+               "ep_ffn_create", "ep_ffn_workspace_size", "ep_ffn_run", "ep_ffn_backward", "ep_ffn_destroy")
+EP_NORM_MAX_HIDDEN = 16384
+EP_FFN_MAX_TOKENS = 16777216
+EP_FFN_RUN = 0
+EP_FFN_FORWARD = 1
+EP_FFN_BACKWARD = 2
 EP_MOE_MAX_TOKENS = 64
 EP_MOE_MAX_EXPERTS = 512
 EP_SCORE_SOFTMAX = 0
@@ -123,6 +130,31 @@ class EpExpertsConfigC(ctypes.Structure):
     _fields_ = [("num_experts", ctypes.c_int), ("first_expert", ctypes.c_int), ("top_k", ctypes.c_int),
                 ("hidden", ctypes.c_int), ("intermediate", ctypes.c_int), ("max_tokens", ctypes.c_int),
                 ("gate_up", EpWeightC), ("down", EpWeightC)]
+
+
+class EpNormConfigC(ctypes.Structure):
+    _fields_ = [("hidden", ctypes.c_int), ("dtype", ctypes.c_int), ("weight_dtype", ctypes.c_int),
+                ("eps", ctypes.c_float), ("weight", ctypes.c_void_p)]
+
+
+class EpNormRowsC(ctypes.Structure):
+    _fields_ = [("x", ctypes.c_void_p), ("x_stride", ctypes.c_longlong),
+                ("residual", ctypes.c_void_p), ("residual_stride", ctypes.c_longlong),
+                ("residual_out", ctypes.c_void_p), ("residual_out_stride", ctypes.c_longlong),
+                ("out", ctypes.c_void_p), ("out_stride", ctypes.c_longlong),
+                ("q", ctypes.c_void_p), ("scales", ctypes.c_void_p)]
+
+
+class EpFfnConfigC(ctypes.Structure):
+    _fields_ = [("hidden", ctypes.c_int), ("intermediate", ctypes.c_int), ("gate_up", ctypes.c_void_p),
+                ("down", ctypes.c_void_p)]
+
+
+class EpFfnGradsC(ctypes.Structure):
+    _fields_ = [("dy", ctypes.c_void_p), ("dy_stride", ctypes.c_longlong),
+                ("x", ctypes.c_void_p), ("x_stride", ctypes.c_longlong), ("saved", ctypes.c_void_p),
+                ("dx", ctypes.c_void_p), ("dx_stride", ctypes.c_longlong), ("dgate_up", ctypes.c_void_p),
+                ("ddown", ctypes.c_void_p), ("grad_dtype", ctypes.c_int), ("accumulate", ctypes.c_int)]
 
 
 class EpError(RuntimeError):
@@ -217,6 +249,14 @@ def load(build_if_missing: bool = True) -> ctypes.CDLL:
         L.ep_linear_run.argtypes = [P, i32, P, ll, i32, P, ll, P]
         L.ep_linear_destroy.argtypes = [P]
         L.ep_layer_run.argtypes = [P, P, P, ll, i32, P, P, P, ll, P]
+        L.ep_norm_run.argtypes = [ctypes.POINTER(EpNormConfigC), ctypes.POINTER(EpNormRowsC), i32, P]
+        L.ep_norm_backward_workspace_size.argtypes = [ctypes.POINTER(EpNormConfigC), i32, ctypes.POINTER(sz)]
+        L.ep_norm_backward.argtypes = [ctypes.POINTER(EpNormConfigC), P, ll, P, ll, P, ll, i32, P, ll, P, P, sz, P]
+        L.ep_ffn_create.argtypes = [ctypes.POINTER(EpFfnConfigC), PP]
+        L.ep_ffn_workspace_size.argtypes = [P, i32, i32, ctypes.POINTER(sz)]
+        L.ep_ffn_run.argtypes = [P, P, ll, i32, P, P, ll, P, sz, P]
+        L.ep_ffn_backward.argtypes = [P, ctypes.POINTER(EpFfnGradsC), i32, P, sz, P]
+        L.ep_ffn_destroy.argtypes = [P]
         for name in MOE_EXPORTS:
             getattr(L, name).restype = i32
         if checked():

@@ -1,0 +1,548 @@
+// moe_block_host.cu -- the C ABI of include/ep_moe.h, second part: the norm and
+// the feed-forward block, their argument checks, tensor maps and launches.
+#include <cmath>
+
+#include "moe_host.h"
+
+using namespace moe_host;
+
+namespace {
+
+int size_of(ep_dtype t) { return t == EP_DTYPE_FP32 ? 4 : 2; }
+
+// Bytes from the first to the last element of `rows` rows of `cols` elements, `stride` elements apart.
+size_t extent(long long rows, long long stride, long long cols, int size)
+{
+    return static_cast<size_t>((rows - 1) * stride + cols) * size;
+}
+
+struct Span {
+    const char *name;
+    const void *p;  // NULL: not there
+    size_t bytes;
+    long long stride;
+};
+
+bool overlap(const Span &a, const Span &b)
+{
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a.p), y = reinterpret_cast<uintptr_t>(b.p);
+    return a.p && b.p && x < y + b.bytes && y < x + a.bytes;
+}
+
+// An output that overlaps an input; in_place: other than as the very same rows.
+ep_status check_overlap(const Span &out, const Span &in, bool in_place)
+{
+    if (overlap(out, in) && !(in_place && out.p == in.p && out.stride == in.stride))
+        MOE_FAIL("%s overlaps %s", out.name, in.name);
+    return EP_OK;
+}
+
+ep_status check_workspace(const void *workspace, size_t have, size_t need)
+{
+    if (need && (!workspace || !aligned(workspace, 256) || have < need))
+        MOE_FAIL("workspace has %zu bytes, needs %zu, 256-byte aligned", workspace ? have : size_t(0), need);
+    return EP_OK;
+}
+
+ep_status check_norm(const ep_norm_config *c, int num_tokens)
+{
+    if (!c)
+        MOE_FAIL("config is NULL");
+    if (c->hidden < 8 || c->hidden > EP_NORM_MAX_HIDDEN || c->hidden % 8)
+        MOE_FAIL("hidden=%d must be a multiple of 8 in [8, %d]", c->hidden, EP_NORM_MAX_HIDDEN);
+    if (c->dtype != EP_DTYPE_BF16 && c->dtype != EP_DTYPE_FP16 && c->dtype != EP_DTYPE_FP32)
+        MOE_FAIL("dtype %d: use bf16, fp16 or fp32", static_cast<int>(c->dtype));
+    if (c->weight_dtype != c->dtype && c->weight_dtype != EP_DTYPE_FP32)
+        MOE_FAIL("weight_dtype %d: use dtype or fp32", static_cast<int>(c->weight_dtype));
+    if (!std::isfinite(c->eps) || !(c->eps > 0.0f))
+        MOE_FAIL("eps must be finite and above 0");
+    if (!c->weight || !aligned(c->weight, 16))
+        MOE_FAIL("weight is NULL or not 16-byte aligned");
+    if (num_tokens < 0)
+        MOE_FAIL("num_tokens=%d is negative", num_tokens);
+    return EP_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+// ---- norm -----------------------------------------------------------------------------
+
+ep_status ep_norm_run(const ep_norm_config *cfg, const ep_norm_rows *rows, int num_tokens, void *stream)
+{
+    Range range("ep_norm_run");
+    ep_status st = check_norm(cfg, num_tokens);
+    if (st != EP_OK)
+        return st;
+    if (!rows)
+        MOE_FAIL("rows is NULL");
+    int dev = 0;
+    moe::NormArgs a = {};
+    st = current_device(&dev, &a.sms);
+    if (st != EP_OK)
+        return st;
+    if (num_tokens == 0)
+        return set_error(EP_OK, "");
+    const ep_norm_rows &r = *rows;
+    const int H = cfg->hidden, size = size_of(cfg->dtype), groups = div_up(H, EP_SCALE_GROUP);
+    if (r.residual_out && !r.residual)
+        MOE_FAIL("residual_out without residual");
+    if ((r.q == nullptr) != (r.scales == nullptr))
+        MOE_FAIL("q and scales must be given together");
+    const Span all[4] = {{"x", r.x, extent(num_tokens, r.x_stride, H, size), r.x_stride},
+                         {"residual", r.residual, extent(num_tokens, r.residual_stride, H, size), r.residual_stride},
+                         {"residual_out", r.residual_out, extent(num_tokens, r.residual_out_stride, H, size), r.residual_out_stride},
+                         {"out", r.out, extent(num_tokens, r.out_stride, H, size), r.out_stride}};
+    for (const Span &s : all)
+        if (s.p || &s == all)
+            if ((st = check_rows(s.name, s.p, s.stride, H, 16, 8)) != EP_OK)
+                return st;
+    if (!aligned(r.q, 8) || !aligned(r.scales, 4))
+        MOE_FAIL("q is not 8-byte or scales not 4-byte aligned");
+    const Span eight[2] = {{"q", r.q, extent(num_tokens, H, H, 1), H}, {"scales", r.scales, extent(num_tokens, groups, groups, 4), groups}};
+    for (int o = 2; o < 4 && st == EP_OK; ++o)
+        for (int i = 0; i < o && st == EP_OK; ++i)
+            st = check_overlap(all[o], all[i], i < 2);
+    for (int o = 0; o < 2 && st == EP_OK; ++o) {
+        for (int i = 0; i < 4 && st == EP_OK; ++i)
+            st = check_overlap(eight[o], all[i], false);
+        for (int i = 0; i < o && st == EP_OK; ++i)
+            st = check_overlap(eight[o], eight[i], false);
+    }
+    if (st != EP_OK)
+        return st;
+    a.x = r.x;
+    a.residual = r.residual;
+    a.weight = cfg->weight;
+    a.x_stride = r.x_stride;
+    a.residual_stride = r.residual_stride;
+    a.residual_out_stride = r.residual_out_stride;
+    a.out_stride = r.out_stride;
+    a.residual_out = r.residual_out;
+    a.out = r.out;
+    a.q = static_cast<uint8_t *>(r.q);
+    a.scales = r.scales;
+    a.T = num_tokens;
+    a.H = H;
+    a.groups = groups;
+    a.dtype = cfg->dtype;
+    a.weight_fp32 = cfg->weight_dtype == EP_DTYPE_FP32;
+    a.eps = cfg->eps;
+    unsigned long long *rec = epk::check_record();
+    a.chk = epk::check_ctx(rec);
+    const cudaStream_t s = static_cast<cudaStream_t>(stream);
+    return finish(moe::launch_norm(a, s), "ep_norm_run", rec, s);
+}
+
+ep_status ep_norm_backward_workspace_size(const ep_norm_config *cfg, int num_tokens, size_t *bytes)
+{
+    if (!bytes)
+        MOE_FAIL("bytes is NULL");
+    ep_status st = check_norm(cfg, num_tokens);
+    if (st != EP_OK)
+        return st;
+    int dev = 0, sms = 0;
+    st = current_device(&dev, &sms);
+    if (st != EP_OK)
+        return st;
+    *bytes = align256(size_t(moe::norm_back_blocks(num_tokens, sms)) * cfg->hidden * 4);
+    return set_error(EP_OK, "");
+}
+
+ep_status ep_norm_backward(const ep_norm_config *cfg, const void *dy, long long dy_stride, const void *h,
+                           long long h_stride, const void *dh, long long dh_stride, int num_tokens, void *dx,
+                           long long dx_stride, float *dweight, void *workspace, size_t workspace_bytes, void *stream)
+{
+    Range range("ep_norm_backward");
+    ep_status st = check_norm(cfg, num_tokens);
+    if (st != EP_OK)
+        return st;
+    int dev = 0;
+    moe::NormBackArgs a = {};
+    st = current_device(&dev, &a.sms);
+    if (st != EP_OK)
+        return st;
+    const int H = cfg->hidden, size = size_of(cfg->dtype);
+    if (!aligned(dweight, 4))
+        MOE_FAIL("dweight is not 4-byte aligned");
+    if ((!dx && !dweight) || (num_tokens == 0 && !dweight))
+        return set_error(EP_OK, "");
+    if (num_tokens > 0) {
+        const Span in[3] = {{"dy", dy, extent(num_tokens, dy_stride, H, size), dy_stride},
+                            {"h", h, extent(num_tokens, h_stride, H, size), h_stride},
+                            {"dh", dh, extent(num_tokens, dh_stride, H, size), dh_stride}};
+        const Span out[2] = {{"dx", dx, extent(num_tokens, dx_stride, H, size), dx_stride}, {"dweight", dweight, size_t(H) * 4, H}};
+        for (int i = 0; i < 3 && st == EP_OK; ++i)
+            if (i < 2 || dh)
+                st = check_rows(in[i].name, in[i].p, in[i].stride, H, 16, 8);
+        if (st == EP_OK && dx)
+            st = check_rows("dx", dx, dx_stride, H, 16, 8);
+        for (int o = 0; o < 2 && st == EP_OK; ++o)
+            for (int i = 0; i < 3 && st == EP_OK; ++i)
+                st = check_overlap(out[o], in[i], o == 0);
+        if (st == EP_OK)
+            st = check_overlap(out[0], out[1], false);
+    }
+    const size_t need = dweight ? align256(size_t(moe::norm_back_blocks(num_tokens, a.sms)) * H * 4) : 0;
+    if (st == EP_OK)
+        st = check_workspace(workspace, workspace_bytes, need);
+    if (st != EP_OK)
+        return st;
+    a.dy = dy;
+    a.h = h;
+    a.dh = dh;
+    a.weight = cfg->weight;
+    a.dy_stride = dy_stride;
+    a.h_stride = h_stride;
+    a.dh_stride = dh_stride;
+    a.dx_stride = dx_stride;
+    a.dx = dx;
+    a.dweight = dweight;
+    a.parts = dweight ? static_cast<float *>(workspace) : nullptr;
+    a.T = num_tokens;
+    a.H = H;
+    a.dtype = cfg->dtype;
+    a.weight_fp32 = cfg->weight_dtype == EP_DTYPE_FP32;
+    a.eps = cfg->eps;
+    unsigned long long *rec = epk::check_record();
+    a.chk = epk::check_ctx(rec);
+    const cudaStream_t s = static_cast<cudaStream_t>(stream);
+    return finish(moe::launch_norm_back(a, s), "ep_norm_backward", rec, s);
+}
+
+}  // extern "C"
+
+// ---- feed-forward ------------------------------------------------------------------------
+
+struct ep_ffn {
+    ep_ffn_config cfg;
+    int device, sms;
+    Flags flags;
+    ep_experts *few;   // the block as one expert, for up to EP_MOE_MAX_TOKENS rows
+    int32_t *ids;      // of those rows: 0 ...
+    float *weights;    // ... with weight 1
+};
+
+namespace {
+
+ep_status check_ffn(const ep_ffn_config *c)
+{
+    if (!c)
+        MOE_FAIL("config is NULL");
+    if (c->hidden < 8 || c->hidden > EP_MOE_MAX_DIM || c->hidden % 8)
+        MOE_FAIL("hidden=%d must be a multiple of 8 in [8, %d]", c->hidden, EP_MOE_MAX_DIM);
+    if (c->intermediate < 8 || c->intermediate > EP_MOE_MAX_DIM || c->intermediate % 8)
+        MOE_FAIL("intermediate=%d must be a multiple of 8 in [8, %d]", c->intermediate, EP_MOE_MAX_DIM);
+    if (!c->gate_up || !aligned(c->gate_up, 16))
+        MOE_FAIL("gate_up is NULL or not 16-byte aligned");
+    if (!c->down || !aligned(c->down, 16))
+        MOE_FAIL("down is NULL or not 16-byte aligned");
+    return EP_OK;
+}
+
+ep_status check_ffn_tokens(const ep_ffn *h, int num_tokens)
+{
+    if (!h)
+        MOE_FAIL("handle is NULL");
+    if (num_tokens < 0 || num_tokens > EP_FFN_MAX_TOKENS)
+        MOE_FAIL("num_tokens=%d outside [0, %d]", num_tokens, EP_FFN_MAX_TOKENS);
+    return EP_OK;
+}
+
+bool few_rows(ep_ffn_call call, int num_tokens) { return call == EP_FFN_RUN && num_tokens <= EP_MOE_MAX_TOKENS; }
+
+// The intermediate rows; for the backward pass the gradients of gate and up too.
+struct FfnLayout {
+    size_t off_dgu, total;
+    FfnLayout(const ep_ffn_config &c, ep_ffn_call call, int num_tokens)
+    {
+        const size_t row = size_t(c.intermediate) * 2;
+        off_dgu = align256(num_tokens * row);
+        total = off_dgu + (call == EP_FFN_BACKWARD ? align256(num_tokens * 2 * row) : 0);
+        if (few_rows(call, num_tokens))
+            total = 0;
+    }
+};
+
+// A matrix operand as it lies in memory: `rows` rows of `cols` bf16, `stride` apart.
+struct Matrix {
+    const char *name;
+    const void *p;
+    long long rows, cols, stride;
+};
+
+// Plans and queues D[M, N] = A B^T. An operand is either [M or N, K], or [K, M or N] (mn).
+ep_status product(const ep_ffn *h, moe::FfnProduct &p, const Matrix &ma, const Matrix &mb, epk::CheckCtx chk, cudaStream_t s)
+{
+    moe::ffn_plan(&p, h->sms);
+    ep_status st = encode_map(&p.a.ma, ma.name, 0, ma.p, ma.cols, ma.rows, 0, ma.stride, 0, moe::kChunk, 64);
+    if (st == EP_OK)
+        st = encode_map(&p.a.mb, mb.name, 0, mb.p, mb.cols, mb.rows, 0, mb.stride, 0, moe::kChunk, p.b_mn ? 64 : p.box_b);
+    if (st != EP_OK)
+        return st;
+    p.a.err = h->flags.err;
+    p.a.chk = chk;
+    const cudaError_t ce = moe::launch_ffn(p, h->sms, s);
+    return ce == cudaSuccess ? EP_OK : cuda_error(ce, "launch");
+}
+
+}  // namespace
+
+extern "C" {
+
+ep_status ep_ffn_create(const ep_ffn_config *cfg, ep_ffn **out)
+{
+    if (!out)
+        MOE_FAIL("out is NULL");
+    *out = nullptr;
+    ep_status st = check_ffn(cfg);
+    if (st != EP_OK)
+        return st;
+    int dev = 0, sms = 0;
+    st = current_device(&dev, &sms);
+    if (st != EP_OK)
+        return st;
+    ep_ffn *h = new (std::nothrow) ep_ffn();
+    if (!h)
+        return set_error(EP_ERR_OOM, "host allocation of the handle failed");
+    h->cfg = *cfg;
+    h->device = dev;
+    h->sms = sms;
+    const ep_weight w[2] = {{cfg->gate_up, 0, 0, EP_DTYPE_BF16}, {cfg->down, 0, 0, EP_DTYPE_BF16}};
+    const ep_experts_config few = {1, 0, 1, cfg->hidden, cfg->intermediate, EP_MOE_MAX_TOKENS, w[0], w[1]};
+    st = ep_experts_create(&few, nullptr, 0, &h->few);
+    if (st == EP_OK)
+        st = h->flags.make();
+    if (st == EP_OK) {
+        cudaError_t ce = moe::ffn_setup();
+        if (ce == cudaSuccess)
+            ce = cudaMalloc(reinterpret_cast<void **>(&h->ids), EP_MOE_MAX_TOKENS * 8);
+        if (ce == cudaSuccess) {
+            h->weights = reinterpret_cast<float *>(h->ids + EP_MOE_MAX_TOKENS);
+            ce = cudaMemset(h->ids, 0, EP_MOE_MAX_TOKENS * 4);
+        }
+        if (ce == cudaSuccess)
+            ce = moe::launch_ffn_ones(h->weights, EP_MOE_MAX_TOKENS, nullptr);
+        if (ce == cudaSuccess)
+            ce = cudaStreamSynchronize(nullptr);
+        if (ce != cudaSuccess)
+            st = cuda_error(ce, "the handle's kernels and memory");
+    }
+    if (st != EP_OK) {
+        if (h->ids)
+            cudaFree(h->ids);
+        h->flags.free();
+        if (h->few)
+            ep_experts_destroy(h->few);
+        delete h;
+        return st;
+    }
+    *out = h;
+    return set_error(EP_OK, "");
+}
+
+ep_status ep_ffn_workspace_size(const ep_ffn *h, ep_ffn_call call, int num_tokens, size_t *bytes)
+{
+    const ep_status st = check_ffn_tokens(h, num_tokens);
+    if (st != EP_OK)
+        return st;
+    if (!bytes)
+        MOE_FAIL("bytes is NULL");
+    if (call != EP_FFN_RUN && call != EP_FFN_FORWARD && call != EP_FFN_BACKWARD)
+        MOE_FAIL("unknown call %d", static_cast<int>(call));
+    *bytes = FfnLayout(h->cfg, call, num_tokens).total;
+    return set_error(EP_OK, "");
+}
+
+ep_status ep_ffn_run(ep_ffn *h, const void *x, long long x_stride, int num_tokens, float *saved, void *out,
+                     long long out_stride, void *workspace, size_t workspace_bytes, void *stream)
+{
+    Range range("ep_ffn_run");
+    ep_status st = check_ffn_tokens(h, num_tokens);
+    if (st == EP_OK)
+        st = same_device(h->device);
+    if (st != EP_OK)
+        return st;
+    if (num_tokens == 0)
+        return set_error(EP_OK, "");
+    const int T = num_tokens, H = h->cfg.hidden, I = h->cfg.intermediate;
+    const ep_ffn_call call = saved ? EP_FFN_FORWARD : EP_FFN_RUN;
+    st = check_rows("x", x, x_stride, H, 16, 8);
+    if (st == EP_OK)
+        st = check_rows("out", out, out_stride, H, 2, 1);
+    if (st != EP_OK)
+        return st;
+    if (!aligned(saved, 16))
+        MOE_FAIL("saved is not 16-byte aligned");
+    const Span in = {"x", x, extent(T, x_stride, H, 2), x_stride}, y = {"out", out, extent(T, out_stride, H, 2), out_stride},
+               keep = {"saved", saved, extent(T, 2 * I, 2 * I, 4), 2 * I};
+    const FfnLayout l(h->cfg, call, T);
+    st = check_overlap(y, in, false);
+    if (st == EP_OK)
+        st = check_overlap(keep, in, false);
+    if (st == EP_OK)
+        st = check_overlap(keep, y, false);
+    if (st == EP_OK)
+        st = check_workspace(workspace, workspace_bytes, l.total);
+    if (st == EP_OK)
+        st = h->flags.take();
+    if (st != EP_OK)
+        return st;
+    if (few_rows(call, T))
+        return ep_experts_run(h->few, x, x_stride, h->ids, h->weights, T, out, out_stride, stream);
+    unsigned long long *rec = epk::check_record();
+    const epk::CheckCtx chk = epk::check_ctx(rec);
+    const cudaStream_t s = static_cast<cudaStream_t>(stream);
+    const Matrix mx = {"x", x, T, H, x_stride}, mh = {"h", workspace, T, I, I}, w1 = {"gate_up", h->cfg.gate_up, 2 * I, H, H},
+                 w2 = {"down", h->cfg.down, H, I, I};
+    moe::FfnProduct join = {};
+    join.epilogue = moe::kFfnJoin;
+    join.a.M = I;
+    join.a.N = T;
+    join.a.K = H;
+    join.a.out = workspace;
+    join.a.out_stride = I;
+    join.a.saved = saved;
+    st = product(h, join, w1, mx, chk, s);
+    if (st != EP_OK)
+        return st;
+    moe::FfnProduct p = {};
+    p.a.M = H;
+    p.a.N = T;
+    p.a.K = I;
+    p.a.out = out;
+    p.a.out_stride = out_stride;
+    st = product(h, p, w2, mh, chk, s);
+    return st == EP_OK ? finish(cudaSuccess, "ep_ffn_run", rec, s) : st;
+}
+
+ep_status ep_ffn_backward(ep_ffn *h, const ep_ffn_grads *grads, int num_tokens, void *workspace, size_t workspace_bytes,
+                          void *stream)
+{
+    Range range("ep_ffn_backward");
+    ep_status st = check_ffn_tokens(h, num_tokens);
+    if (st == EP_OK)
+        st = same_device(h->device);
+    if (st != EP_OK)
+        return st;
+    if (!grads)
+        MOE_FAIL("grads is NULL");
+    const ep_ffn_grads &g = *grads;
+    const int T = num_tokens, H = h->cfg.hidden, I = h->cfg.intermediate;
+    if (g.grad_dtype != EP_DTYPE_BF16 && g.grad_dtype != EP_DTYPE_FP32)
+        MOE_FAIL("grad_dtype %d: use bf16 or fp32", static_cast<int>(g.grad_dtype));
+    if (g.accumulate && g.grad_dtype != EP_DTYPE_FP32)
+        MOE_FAIL("accumulate needs fp32 gradients");
+    if (!aligned(g.dgate_up, 16) || !aligned(g.ddown, 16))
+        MOE_FAIL("dgate_up or ddown is not 16-byte aligned");
+    const int size = size_of(g.grad_dtype);
+    const size_t weight = size_t(H) * I * size;
+    const cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (T == 0) {
+        cudaError_t ce = cudaSuccess;
+        if (g.dgate_up && !g.accumulate)
+            ce = moe::launch_ffn_zero(g.dgate_up, 2 * weight, s);
+        if (ce == cudaSuccess && g.ddown && !g.accumulate)
+            ce = moe::launch_ffn_zero(g.ddown, weight, s);
+        return ce == cudaSuccess ? set_error(EP_OK, "") : cuda_error(ce, "ep_ffn_backward");
+    }
+    st = check_rows("dy", g.dy, g.dy_stride, H, 16, 8);
+    if (st == EP_OK)
+        st = check_rows("x", g.x, g.x_stride, H, 16, 8);
+    if (st == EP_OK && g.dx)
+        st = check_rows("dx", g.dx, g.dx_stride, H, 2, 1);
+    if (st != EP_OK)
+        return st;
+    if (!g.saved || !aligned(g.saved, 16))
+        MOE_FAIL("saved is NULL or not 16-byte aligned");
+    const Span in[3] = {{"dy", g.dy, extent(T, g.dy_stride, H, 2), g.dy_stride},
+                        {"x", g.x, extent(T, g.x_stride, H, 2), g.x_stride},
+                        {"saved", g.saved, extent(T, 2 * I, 2 * I, 4), 2 * I}};
+    const Span out[3] = {{"dx", g.dx, extent(T, g.dx_stride, H, 2), g.dx_stride},
+                         {"dgate_up", g.dgate_up, 2 * weight, H},
+                         {"ddown", g.ddown, weight, I}};
+    for (int o = 0; o < 3 && st == EP_OK; ++o) {
+        for (int i = 0; i < 3 && st == EP_OK; ++i)
+            st = check_overlap(out[o], in[i], false);
+        for (int i = 0; i < o && st == EP_OK; ++i)
+            st = check_overlap(out[o], out[i], false);
+    }
+    const FfnLayout l(h->cfg, EP_FFN_BACKWARD, T);
+    if (st == EP_OK)
+        st = check_workspace(workspace, workspace_bytes, l.total);
+    if (st == EP_OK)
+        st = h->flags.take();
+    if (st != EP_OK)
+        return st;
+    if (!g.dx && !g.dgate_up && !g.ddown)
+        return set_error(EP_OK, "");
+    unsigned long long *rec = epk::check_record();
+    const epk::CheckCtx chk = epk::check_ctx(rec);
+    __nv_bfloat16 *const dgu = reinterpret_cast<__nv_bfloat16 *>(static_cast<uint8_t *>(workspace) + l.off_dgu);
+    const Matrix mx = {"x", g.x, T, H, g.x_stride}, mdy = {"dy", g.dy, T, H, g.dy_stride}, mh = {"h", workspace, T, I, I},
+                 mdgu = {"dgate_up rows", dgu, T, 2 * I, 2 * I}, w1 = {"gate_up", h->cfg.gate_up, 2 * I, H, H},
+                 w2 = {"down", h->cfg.down, H, I, I};
+    {
+        moe::FfnProduct p = {};
+        p.epilogue = moe::kFfnSplit;
+        p.a_mn = true;
+        p.a.M = I;
+        p.a.N = T;
+        p.a.K = H;
+        p.a.out = workspace;
+        p.a.out_stride = I;
+        p.a.saved = const_cast<float *>(g.saved);
+        p.a.dgu = dgu;
+        st = product(h, p, w2, mdy, chk, s);
+    }
+    if (st == EP_OK && g.dx) {
+        moe::FfnProduct p = {};
+        p.a_mn = true;
+        p.a.M = H;
+        p.a.N = T;
+        p.a.K = 2 * I;
+        p.a.out = g.dx;
+        p.a.out_stride = g.dx_stride;
+        st = product(h, p, w1, mdgu, chk, s);
+    }
+    if (st == EP_OK && g.dgate_up) {
+        moe::FfnProduct p = {};
+        p.a_mn = p.b_mn = true;
+        p.a.M = H;
+        p.a.N = 2 * I;
+        p.a.K = T;
+        p.a.out = g.dgate_up;
+        p.a.out_stride = H;
+        p.a.fp32 = size == 4;
+        p.a.accumulate = g.accumulate != 0;
+        st = product(h, p, mx, mdgu, chk, s);
+    }
+    if (st == EP_OK && g.ddown) {
+        moe::FfnProduct p = {};
+        p.a_mn = p.b_mn = true;
+        p.a.M = I;
+        p.a.N = H;
+        p.a.K = T;
+        p.a.out = g.ddown;
+        p.a.out_stride = I;
+        p.a.fp32 = size == 4;
+        p.a.accumulate = g.accumulate != 0;
+        st = product(h, p, mh, mdy, chk, s);
+    }
+    return st == EP_OK ? finish(cudaSuccess, "ep_ffn_backward", rec, s) : st;
+}
+
+ep_status ep_ffn_destroy(ep_ffn *h)
+{
+    if (h) {
+        wait_for_device(h->device);
+        ep_experts_destroy(h->few);
+        cudaFree(h->ids);
+        h->flags.free();
+        delete h;
+    }
+    return set_error(EP_OK, "");
+}
+
+}  // extern "C"

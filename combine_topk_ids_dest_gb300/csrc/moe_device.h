@@ -264,6 +264,27 @@ static __device__ __forceinline__ void cluster_sync()
     asm volatile("barrier.cluster.arrive.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
 }
 
+// The address of this offset in the cluster's block `rank`.
+static __device__ __forceinline__ uint32_t in_block(uint32_t at, uint32_t rank)
+{
+    uint32_t r;
+    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(at), "r"(rank));
+    return r;
+}
+
+static __device__ __forceinline__ float ld_cluster(uint32_t at)
+{
+    float v;
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(at) : "memory");
+    return v;
+}
+
+// mbar_arrive on a barrier of any block of the cluster.
+static __device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar)
+{
+    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+
 // The address of this offset in the cluster's first block.
 static __device__ __forceinline__ uint32_t in_first_block(uint32_t at)
 {
@@ -286,6 +307,18 @@ static __host__ __device__ constexpr uint32_t idesc_f16(int M, int N, int bf16)
 static __device__ __forceinline__ uint64_t desc_sw128(uint32_t addr)
 {
     return uint64_t((addr & 0x3FFFF) >> 4) | (uint64_t(1) << 16) | (uint64_t(64) << 32) | (uint64_t(1) << 46) |
+           (uint64_t(2) << 61);
+}
+
+// Bits of the instruction descriptor: A, or B, has its rows contiguous (MN-major) instead of K.
+constexpr uint32_t kIdescAmn = 1u << 15, kIdescBmn = 1u << 16;
+
+// Shared-memory descriptor of an MN-major tile, 128-byte swizzle: blocks of 64
+// rows x 64 k, 8 KB each, a k after the other in 128 bytes; 8 k are 1024 bytes,
+// the next 64 rows 8 KB further. 16 k further: 2048 bytes.
+static __device__ __forceinline__ uint64_t desc_mn(uint32_t addr)
+{
+    return uint64_t((addr & 0x3FFFF) >> 4) | (uint64_t(512) << 16) | (uint64_t(64) << 32) | (uint64_t(1) << 46) |
            (uint64_t(2) << 61);
 }
 

@@ -182,6 +182,71 @@ cudaError_t launch_int4(const Int4Args &a, bool linear, bool bf16, int grid, siz
 cudaError_t launch_pack(const PackArgs &a, cudaStream_t stream);
 std::vector<const void *> int4_kernels();  // every kernel of the file
 
+// ---- norm (moe_norm.cu) ---------------------------------------------------------------
+
+constexpr int kNormRows = 4;  // most rows of a block
+
+struct NormArgs {
+    const void *x, *residual, *weight;
+    long long x_stride, residual_stride, residual_out_stride, out_stride;
+    void *residual_out, *out;
+    uint8_t *q;
+    float *scales;
+    int T, H, groups, dtype, weight_fp32, sms;
+    float eps;
+    epk::CheckCtx chk;
+};
+
+struct NormBackArgs {
+    const void *dy, *h, *dh, *weight;
+    long long dy_stride, h_stride, dh_stride, dx_stride;
+    void *dx;
+    float *dweight;
+    float *parts;  // [blocks, H], or NULL: no dweight
+    int T, H, dtype, weight_fp32, sms;
+    float eps;
+    epk::CheckCtx chk;
+};
+
+cudaError_t launch_norm(const NormArgs &a, cudaStream_t stream);
+cudaError_t launch_norm_back(const NormBackArgs &a, cudaStream_t stream);
+int norm_back_blocks(int T, int sms);  // parts of dweight
+std::vector<const void *> norm_kernels();  // every kernel of the file
+
+// ---- feed-forward block (moe_ffn.cu) ----------------------------------------------------
+
+// What a product's results become: stored as they are, gate and up joined, or the gradients of gate and up.
+enum FfnEpilogue { kFfnStore = 0, kFfnJoin, kFfnSplit };
+
+// One product D[M features, N rows] = A[M, K] B[N, K]^T; a tile is 128 features (joined: 64, with gate and up) of a
+// block by tile_n rows.
+struct FfnArgs {
+    CUtensorMap ma, mb;  // boxes of 64 x 64; mb with K contiguous: 64 x the rows of a block's tile
+    void *out;           // [N, M], rows out_stride apart: y, dx, the weights' gradients (N and M both features), h
+    long long out_stride;
+    float *saved;           // [N, 2 M]: g and u, written (joined) or read (split); NULL: not wanted
+    __nv_bfloat16 *dgu;     // [N, 2 M], split
+    unsigned int *err;
+    int M, N, K, tile_n, m_tiles, n_tiles, stages, split;
+    int fp32, accumulate;  // of out
+    epk::CheckCtx chk;
+};
+
+// A product as the host asks for it; the plan fills in the rest of a.
+struct FfnProduct {
+    FfnArgs a;
+    int epilogue;
+    bool a_mn, b_mn;  // the operand's features or rows are contiguous, not K
+    bool pair;
+    int box_b;        // rows of mb's box where K is contiguous
+};
+void ffn_plan(FfnProduct *p, int sms);
+cudaError_t ffn_setup();
+cudaError_t launch_ffn(const FfnProduct &p, int sms, cudaStream_t stream);
+cudaError_t launch_ffn_zero(void *p, size_t bytes, cudaStream_t stream);
+cudaError_t launch_ffn_ones(float *p, int n, cudaStream_t stream);
+std::vector<const void *> ffn_kernels();  // every kernel of the file
+
 // Binary versions of this library's MoE kernels, as epk::kernel_binary_versions.
 cudaError_t kernel_binary_versions(int *out, int max, int *n);
 

@@ -4,7 +4,9 @@
 ``EpComm.dispatch`` takes; :class:`EpExperts` computes the experts for a few
 tokens, on all experts or on the rows one rank received; :class:`EpMoeLayer`
 is both, a whole layer on one GPU; :class:`Int4Linear` is a product with 4-bit
-weights. All work runs in the CUDA library on
+weights. :class:`EpNorm` makes the rows that go in, in 8 bits for the dispatch
+too, and :class:`EpFfn` is the block of a dense layer or a shared expert, both
+with their gradients. All work runs in the CUDA library on
 torch's current stream of the tensors' device; torch supplies device memory
 and streams only. Weights are kept by reference, not copied.
 
@@ -15,7 +17,7 @@ objects, and let them go, outside CUDA graph captures; calls can be captured.
 from __future__ import annotations
 
 import ctypes
-from typing import Optional, Tuple
+from typing import NamedTuple, Optional, Tuple
 
 import torch
 
@@ -40,7 +42,46 @@ def _weight(name, t, dtype, shape, device):
     return t
 
 
-class _Handle:
+class _OnDevice:
+    """What lives on a device (``device``, ``_index``) and takes rows there."""
+
+    def _rows(self, x, cols, dtype, name="x"):
+        """Row count and stride of an operand [rows, cols] whose rows are contiguous."""
+        if x.dtype is not dtype or x.get_device() != self._index:
+            raise ValueError(f"{name} is {x.dtype} on {x.device}, expected {dtype} on {self.device}")
+        shape = x.shape
+        if len(shape) != 2 or shape[1] != cols:
+            raise ValueError(f"{name} must be a [tokens, {cols}] tensor, got {tuple(shape)}")
+        if shape[0] > 0x7FFFFFFF:
+            raise ValueError(f"{name} has {shape[0]} rows, at most 2^31 - 1 fit a call")
+        if x.is_contiguous():
+            return shape[0], cols
+        if x.stride(1) != 1 and cols != 1:
+            raise ValueError(f"{name} must have contiguous rows, got strides {x.stride()}")
+        return shape[0], x.stride(0)
+
+    def _out(self, out, n, cols, dtype, name="out"):
+        """`out`, or a new tensor, [n, cols] of dtype, and its row stride."""
+        if out is None:
+            return torch.empty((n, cols), dtype=dtype, device=self.device), cols
+        m, stride = self._rows(out, cols, dtype, name)
+        if m != n:
+            raise ValueError(f"{name} must have {n} rows, got {m}")
+        return out, stride
+
+    def _run_on(self, fn, *args):
+        """fn(*args, stream) on the device, whose errors are raised."""
+        index = self._index
+        if torch._C._cuda_getDevice() != index:
+            with torch.cuda.device(index):
+                status = fn(*args, torch._C._cuda_getCurrentRawStream(index))
+        else:
+            status = fn(*args, torch._C._cuda_getCurrentRawStream(index))
+        if status:
+            check(status)
+
+
+class _Handle(_OnDevice):
     """A handle of the C ABI and the device it lives on."""
 
     _destroy = ""
@@ -66,30 +107,6 @@ class _Handle:
         if self._h is None:
             raise EpError(_lib.EP_ERR_STATE, f"the {type(self).__name__} was destroyed")
         return self._h
-
-    def _rows(self, x, cols, dtype, name="x"):
-        """Row count and stride of an operand [rows, cols] whose rows are contiguous."""
-        if x.dtype is not dtype or x.get_device() != self._index:
-            raise ValueError(f"{name} is {x.dtype} on {x.device}, expected {dtype} on {self.device}")
-        shape = x.shape
-        if len(shape) != 2 or shape[1] != cols:
-            raise ValueError(f"{name} must be a [tokens, {cols}] tensor, got {tuple(shape)}")
-        if shape[0] > 0x7FFFFFFF:
-            raise ValueError(f"{name} has {shape[0]} rows, at most 2^31 - 1 fit a call")
-        if x.is_contiguous():
-            return shape[0], cols
-        if x.stride(1) != 1 and cols != 1:
-            raise ValueError(f"{name} must have contiguous rows, got strides {x.stride()}")
-        return shape[0], x.stride(0)
-
-    def _out(self, out, n, cols, dtype):
-        """`out`, or a new tensor, [n, cols] of dtype, and its row stride."""
-        if out is None:
-            return torch.empty((n, cols), dtype=dtype, device=self.device), cols
-        m, stride = self._rows(out, cols, dtype, "out")
-        if m != n:
-            raise ValueError(f"out must have {n} rows, got {m}")
-        return out, stride
 
     def _call(self, fn, *args):
         """fn(handle, *args, stream) on the handle's device."""
@@ -329,3 +346,187 @@ class EpMoeLayer:
         router._call(self._run, experts._live(), x.data_ptr(), stride, n, ids.data_ptr(), weights.data_ptr(),
                      out.data_ptr(), out_stride)
         return out, ids, weights
+
+
+_NORM_DTYPES = {**_DTYPES, torch.float32: _lib.EP_DTYPE_FP32}
+
+
+class EpNormResult(NamedTuple):
+    """What a call of :class:`EpNorm` returned; None for what was not asked for."""
+
+    out: Optional[torch.Tensor]       # the normed rows, in the type of x
+    residual: Optional[torch.Tensor]  # x + residual, in the type of x
+    q: Optional[torch.Tensor]         # the normed rows in float8_e4m3fn ...
+    scales: Optional[torch.Tensor]    # ... times these, fp32 [tokens, ceil(hidden / 128)]
+
+
+class EpNorm(_OnDevice):
+    """The residual's addition and the root-mean-square norm: ``s = x + residual``,
+    ``y = s / sqrt(mean(s * s) + eps) * weight``, in fp32.
+
+    ``weight`` [hidden] is of the rows' type or float32; ``dtype``, the rows' type (bfloat16, float16 or
+    float32), is the weight's unless given.
+    """
+
+    def __init__(self, weight: torch.Tensor, eps: float = 1e-6, dtype: Optional[torch.dtype] = None):
+        self.device = _device_of(weight, "weight")
+        self._index = self.device.index
+        self.dtype = weight.dtype if dtype is None else dtype
+        if self.dtype not in _NORM_DTYPES or weight.dtype not in (self.dtype, torch.float32) or weight.dim() != 1:
+            raise ValueError("weight must be a [hidden] tensor of the rows' type (bfloat16, float16 or float32) or float32")
+        self.hidden = int(weight.shape[0])
+        self._weight = _weight("weight", weight, weight.dtype, weight.shape, self.device)
+        self._L = _lib.load()
+        self._cfg = _lib.EpNormConfigC(self.hidden, _NORM_DTYPES[self.dtype], _NORM_DTYPES[weight.dtype], float(eps),
+                                       weight.data_ptr())
+        need = ctypes.c_size_t(0)  # also checks the configuration
+        with torch.cuda.device(self.device):
+            check(self._L.ep_norm_backward_workspace_size(ctypes.byref(self._cfg), 1, ctypes.byref(need)))
+
+    def __call__(self, x: torch.Tensor, residual: Optional[torch.Tensor] = None, plain: bool = True,
+                 quantized: bool = False, out: Optional[torch.Tensor] = None,
+                 residual_out: Optional[torch.Tensor] = None) -> EpNormResult:
+        """``x`` [tokens, hidden] -> the normed rows (``plain``: as ``out``; ``quantized``: as ``q`` with ``scales``,
+        what ``EpComm.dispatch`` takes as 8-bit rows), and with ``residual`` the sum ``x + residual``.
+
+        ``out`` and ``residual_out``, if given, receive the results; both may be ``x`` or ``residual``."""
+        n, stride = self._rows(x, self.hidden, self.dtype)
+        r = _lib.EpNormRowsC(x=x.data_ptr(), x_stride=stride)
+        if residual is not None:
+            m, r.residual_stride = self._rows(residual, self.hidden, self.dtype, "residual")
+            if m != n:
+                raise ValueError(f"residual must have {n} rows, got {m}")
+            r.residual = residual.data_ptr()
+            residual_out, r.residual_out_stride = self._out(residual_out, n, self.hidden, self.dtype, "residual_out")
+            r.residual_out = residual_out.data_ptr()
+        elif residual_out is not None:
+            raise ValueError("residual_out without residual")
+        if plain:
+            out, r.out_stride = self._out(out, n, self.hidden, self.dtype)
+            r.out = out.data_ptr()
+        elif out is not None:
+            raise ValueError("out without plain")
+        q = scales = None
+        if quantized:
+            q = torch.empty((n, self.hidden), dtype=torch.float8_e4m3fn, device=self.device)
+            scales = torch.empty((n, -(-self.hidden // _lib.EP_SCALE_GROUP)), dtype=torch.float32, device=self.device)
+            r.q, r.scales = q.data_ptr(), scales.data_ptr()
+        if n:
+            self._run_on(self._L.ep_norm_run, self._cfg, r, n)
+        return EpNormResult(out, residual_out, q, scales)
+
+    def backward(self, dy: torch.Tensor, h: torch.Tensor, dh: Optional[torch.Tensor] = None,
+                 dx: Optional[torch.Tensor] = None) -> Tuple[torch.Tensor, torch.Tensor]:
+        """Gradients of ``out = norm(h)``: (dx [tokens, hidden], dweight fp32 [hidden]).
+
+        ``h``: the rows that were normed (the call's ``residual``, or its ``x`` without one); ``dy``: the
+        gradient of the normed rows; ``dh``: the gradient that reaches ``h`` on another way, added to dx.
+        dx is the gradient of x and of residual alike; ``dx``, if given, receives it and may be ``dy``, ``h`` or ``dh``."""
+        n, stride = self._rows(dy, self.hidden, self.dtype, "dy")
+        args = [dy.data_ptr(), stride]
+        for name, t in (("h", h), ("dh", dh)):
+            if t is None and name == "dh":
+                args += [0, 0]
+                continue
+            m, stride = self._rows(t, self.hidden, self.dtype, name)
+            if m != n:
+                raise ValueError(f"{name} must have {n} rows, got {m}")
+            args += [t.data_ptr(), stride]
+        dx, stride = self._out(dx, n, self.hidden, self.dtype, "dx")
+        dweight = torch.empty(self.hidden, dtype=torch.float32, device=self.device)
+        need = ctypes.c_size_t(0)
+        with torch.cuda.device(self._index):
+            check(self._L.ep_norm_backward_workspace_size(self._cfg, n, ctypes.byref(need)))
+        ws = torch.empty(need.value, dtype=torch.uint8, device=self.device)
+        self._run_on(self._L.ep_norm_backward, self._cfg, *args, n, dx.data_ptr(), stride, dweight.data_ptr(),
+                     ws.data_ptr(), need.value)
+        return dx, dweight
+
+
+class EpFfn(_Handle):
+    """The gated feed-forward block of a dense layer, or of an expert that every token uses:
+    ``y = (silu(x @ W1.T) * (x @ W3.T)) @ W2.T``, for any number of tokens, and its gradients.
+
+    ``gate_up`` bf16 [2*intermediate, hidden] (W1's rows, then W3's) and ``down`` bf16 [hidden, intermediate]
+    are kept by reference; each call reads their present values.
+    """
+
+    _destroy = "ep_ffn_destroy"
+
+    def __init__(self, gate_up: torch.Tensor, down: torch.Tensor):
+        device = _device_of(gate_up, "gate_up")
+        if gate_up.dim() != 2 or gate_up.shape[0] % 2:
+            raise ValueError("gate_up must be [2*intermediate, hidden]")
+        self.intermediate, self.hidden = int(gate_up.shape[0]) // 2, int(gate_up.shape[1])
+        self.dtype = torch.bfloat16
+        self._w = (_weight("gate_up", gate_up, self.dtype, gate_up.shape, device),
+                   _weight("down", down, self.dtype, (self.hidden, self.intermediate), device))
+        self._open(device)
+        cfg = _lib.EpFfnConfigC(self.hidden, self.intermediate, gate_up.data_ptr(), down.data_ptr())
+        h = ctypes.c_void_p()
+        with torch.cuda.device(device):
+            check(self._L.ep_ffn_create(ctypes.byref(cfg), ctypes.byref(h)))
+        self._h = h.value
+
+    def _workspace(self, call: int, n: int) -> Tuple[Optional[torch.Tensor], int, int]:
+        """A call's workspace: the tensor, its address and its bytes."""
+        if call == _lib.EP_FFN_RUN and n <= _lib.EP_MOE_MAX_TOKENS:
+            return None, 0, 0
+        size = ctypes.c_size_t(0)
+        check(self._L.ep_ffn_workspace_size(self._live(), call, n, ctypes.byref(size)))
+        ws = torch.empty(size.value, dtype=torch.uint8, device=self.device)
+        return ws, ws.data_ptr(), size.value
+
+    def __call__(self, x: torch.Tensor, out: Optional[torch.Tensor] = None) -> torch.Tensor:
+        """``x`` bf16 [tokens, hidden] -> bf16 [tokens, hidden] (``out`` if given)."""
+        n, stride = self._rows(x, self.hidden, self.dtype)
+        out, out_stride = self._out(out, n, self.hidden, self.dtype)
+        ws, at, size = self._workspace(_lib.EP_FFN_RUN, n)
+        self._call(self._L.ep_ffn_run, x.data_ptr(), stride, n, 0, out.data_ptr(), out_stride, at, size)
+        return out
+
+    def forward(self, x: torch.Tensor, out: Optional[torch.Tensor] = None) -> Tuple[torch.Tensor, torch.Tensor]:
+        """The block for training: (y, saved), ``saved`` fp32 [tokens, 2*intermediate] for :meth:`backward`:
+        each row's ``x @ W1.T`` and ``x @ W3.T``."""
+        n, stride = self._rows(x, self.hidden, self.dtype)
+        out, out_stride = self._out(out, n, self.hidden, self.dtype)
+        saved = torch.empty((n, 2 * self.intermediate), dtype=torch.float32, device=self.device)
+        ws, at, size = self._workspace(_lib.EP_FFN_FORWARD, n)
+        if n:
+            self._call(self._L.ep_ffn_run, x.data_ptr(), stride, n, saved.data_ptr(), out.data_ptr(), out_stride, at, size)
+        return out, saved
+
+    def backward(self, dy: torch.Tensor, x: torch.Tensor, saved: torch.Tensor, need_dx: bool = True,
+                 need_weights: bool = True, dgate_up: Optional[torch.Tensor] = None,
+                 ddown: Optional[torch.Tensor] = None, accumulate: bool = False):
+        """Gradients (dx, dgate_up, ddown) from ``dy`` bf16 [tokens, hidden], for the ``x`` and the ``saved`` of
+        :meth:`forward` with the same weights; None where not needed.
+
+        The weights' gradients are new bf16 tensors, or are written into ``dgate_up`` and ``ddown`` (both bf16 or both
+        float32), which ``accumulate`` (float32 only) adds to."""
+        n, dy_stride = self._rows(dy, self.hidden, self.dtype, "dy")
+        m, x_stride = self._rows(x, self.hidden, self.dtype)
+        if m != n:
+            raise ValueError(f"x must have {n} rows, got {m}")
+        _weight("saved", saved, torch.float32, (n, 2 * self.intermediate), self.device)
+        grads = [dgate_up, ddown]
+        given = [t for t in grads if t is not None]
+        if len(given) == 1 or (given and not need_weights):
+            raise ValueError("dgate_up and ddown must be given together, with need_weights")
+        if accumulate and not (given and given[0].dtype is torch.float32):
+            raise ValueError("accumulate needs float32 dgate_up and ddown")
+        dtype = given[0].dtype if given else self.dtype
+        if dtype not in (self.dtype, torch.float32):
+            raise ValueError(f"dgate_up is {dtype}: use bfloat16 or float32")
+        if need_weights:
+            names = ("dgate_up", "ddown")
+            grads = [_weight(name, t, dtype, w.shape, self.device) for name, t, w in zip(names, grads, self._w)] if given \
+                else [torch.empty_like(w) for w in self._w]
+        dx = torch.empty((n, self.hidden), dtype=self.dtype, device=self.device) if need_dx else None
+        g = _lib.EpFfnGradsC(dy.data_ptr(), dy_stride, x.data_ptr(), x_stride, saved.data_ptr(),
+                             dx.data_ptr() if need_dx else 0, self.hidden,
+                             grads[0].data_ptr() if need_weights else 0, grads[1].data_ptr() if need_weights else 0,
+                             _lib.EP_DTYPE_FP32 if dtype is torch.float32 else _lib.EP_DTYPE_BF16, int(bool(accumulate)))
+        ws, at, size = self._workspace(_lib.EP_FFN_BACKWARD, n)
+        self._call(self._L.ep_ffn_backward, g, n, at, size)
+        return dx, grads[0], grads[1]

@@ -8,7 +8,10 @@
  *             weights: of all experts (router and experts are then a whole MoE
  *             layer on one GPU) or of one rank's (on the rows a dispatch
  *             delivered, giving the rows a combine adds up);
- *  - linear:  y = x W^T for a few tokens, W in 4 bits with group scales.
+ *  - linear:  y = x W^T for a few tokens, W in 4 bits with group scales;
+ *  - norm:    the residual's addition and the RMS norm before the layer, with
+ *             rows in 8 bits and their scales, as a dispatch carries them;
+ *  - ffn:     the gated feed-forward block of a dense layer or a shared expert.
  *
  * Statuses, ep_last_error, streams, devices and threads are as in ep.h: every
  * call checks its arguments on the host before it launches anything, queues its
@@ -198,6 +201,129 @@ ep_status ep_experts_destroy(ep_experts *h);
  * and top_k, the router's dtype is bf16; num_tokens <= max_tokens. */
 ep_status ep_layer_run(ep_router *r, ep_experts *h, const void *x, long long x_stride, int num_tokens,
                        int32_t *ids, float *weights, void *out, long long out_stride, void *stream);
+
+/* ---- norm ------------------------------------------------------------------------
+ * The residual's addition and the root-mean-square norm of each row:
+ *   s = x + residual;  r = 1 / sqrt(mean(s^2) + eps);  y = s r weight
+ * in fp32, out = y and residual_out = s rounded once to dtype. Rows in 8 bits,
+ * as ep_dispatch carries them: for each EP_SCALE_GROUP columns (the last
+ * group may have fewer) scale = max(max |y| / 448, 2^-126), q = y / scale
+ * rounded to e4m3, from the unrounded y; a group with an infinite or NaN y has
+ * a NaN scale and NaN codes. Rows whose sum of squares exceeds fp32 keep their
+ * value (the sum is taken again, scaled).
+ */
+#define EP_NORM_MAX_HIDDEN 16384
+#define EP_NORM_MAX_TOKENS 2147483647 /* rows of one call */
+
+typedef struct {
+    int hidden;            /* a multiple of 8, <= EP_NORM_MAX_HIDDEN */
+    ep_dtype dtype;        /* of x, residual, out, residual_out: EP_DTYPE_BF16, FP16 or FP32 */
+    ep_dtype weight_dtype; /* dtype, or EP_DTYPE_FP32 */
+    float eps;             /* finite, > 0 */
+    const void *weight;    /* device [hidden], 16-byte aligned */
+} ep_norm_config;
+
+/* One call's rows: x and residual [num_tokens, hidden], rows *_stride elements
+ * apart (a multiple of 8, >= hidden), 16-byte aligned. residual may be NULL,
+ * then residual_out is too (s is x). Each of residual_out, out and the pair
+ * q [num_tokens, hidden], scales [num_tokens, ceil(hidden / 128)] (contiguous;
+ * q 8-byte, scales 4-byte aligned) may be NULL. residual_out and out may be x or residual themselves
+ * (same address and stride); no other overlap. */
+typedef struct {
+    const void *x;
+    long long x_stride;
+    const void *residual;
+    long long residual_stride;
+    void *residual_out;
+    long long residual_out_stride;
+    void *out;
+    long long out_stride;
+    void *q;
+    float *scales;
+} ep_norm_rows;
+
+ep_status ep_norm_run(const ep_norm_config *cfg, const ep_norm_rows *rows, int num_tokens, void *stream);
+
+/* Gradients of out = norm(h), h the rows that were normed (x, or
+ * residual_out), from dy and, if not NULL, dh, the gradient that reaches h on
+ * another way (the residual stream):
+ *   n = h r;  g = dy weight;  dx = r (g - n mean(g n)) + dh;  dweight = sum_t dy n
+ * dx is the gradient of x and of residual alike, rounded once to dtype;
+ * dweight is fp32 [hidden], summed in an order that does not depend on timing.
+ * Either may be NULL. Rows as above, strides a multiple of 8; dx may be dy, h or
+ * dh itself. workspace: device, 256-byte aligned, of at least
+ * ep_norm_backward_workspace_size bytes (used by this call alone). Without
+ * rows dweight is 0. */
+ep_status ep_norm_backward_workspace_size(const ep_norm_config *cfg, int num_tokens, size_t *bytes);
+
+ep_status ep_norm_backward(const ep_norm_config *cfg, const void *dy, long long dy_stride, const void *h,
+                           long long h_stride, const void *dh, long long dh_stride, int num_tokens, void *dx,
+                           long long dx_stride, float *dweight, void *workspace, size_t workspace_bytes,
+                           void *stream);
+
+/* ---- feed-forward ------------------------------------------------------------------
+ * The gated block of a dense layer, or of an expert that every token uses:
+ *   g = x W1^T;  u = x W3^T;  h = silu(g) u;  y = h W2^T
+ * for any number of rows, and its gradients. bf16, sums fp32. Up to
+ * EP_MOE_MAX_TOKENS rows the intermediate row h keeps 16 bits of mantissa,
+ * above it is rounded to bf16, as are the gradients of g and u before they are
+ * multiplied; y and the gradients are rounded once. g and u are not rounded.
+ */
+typedef struct ep_ffn ep_ffn;
+
+typedef struct {
+    int hidden;          /* a multiple of 8, <= EP_MOE_MAX_DIM */
+    int intermediate;    /* likewise */
+    const void *gate_up; /* device bf16 [2 * intermediate, hidden], W1's rows, then W3's; 16-byte aligned */
+    const void *down;    /* device bf16 [hidden, intermediate], W2, 16-byte aligned; both kept, not copied:
+                            their values are read by each call */
+} ep_ffn_config;
+
+#define EP_FFN_MAX_TOKENS 16777216 /* rows of one call */
+
+typedef enum {
+    EP_FFN_RUN = 0,     /* ep_ffn_run without saved */
+    EP_FFN_FORWARD = 1, /* ep_ffn_run with saved */
+    EP_FFN_BACKWARD = 2 /* ep_ffn_backward */
+} ep_ffn_call;
+
+ep_status ep_ffn_create(const ep_ffn_config *cfg, ep_ffn **out);
+
+/* Bytes of device workspace such a call with num_tokens rows needs (may be 0). */
+ep_status ep_ffn_workspace_size(const ep_ffn *h, ep_ffn_call call, int num_tokens, size_t *bytes);
+
+/* x, out: device bf16 [num_tokens, hidden], rows x_stride / out_stride
+ * elements apart (x_stride a multiple of 8, both >= hidden), x 16-byte aligned. saved: NULL, or
+ * device fp32 [num_tokens, 2 * intermediate], contiguous, 16-byte aligned: receives g and u of
+ * each row, for ep_ffn_backward. workspace: device, 256-byte aligned (used by this call
+ * alone). 0 <= num_tokens <= EP_FFN_MAX_TOKENS; 0 does nothing. out may not overlap the inputs. */
+ep_status ep_ffn_run(ep_ffn *h, const void *x, long long x_stride, int num_tokens, float *saved, void *out,
+                     long long out_stride, void *workspace, size_t workspace_bytes, void *stream);
+
+/* Gradients from dy, for the x and the saved of a forward call and the same weights:
+ *   dh = dy W2;  dg = dh u silu'(g);  du = dh silu(g)
+ *   dx = dg W1 + du W3;  dW1 = dg^T x;  dW3 = du^T x;  dW2 = dy^T h
+ * dy, x, dx: rows as above (dy as x). dgate_up and ddown: device, contiguous, shaped
+ * like the weights, 16-byte aligned, of type grad_dtype: EP_DTYPE_BF16, or EP_DTYPE_FP32; with
+ * accumulate (fp32 only) they are added to. Each of dx, dgate_up and ddown may be NULL.
+ * Without rows weight gradients are 0 (with accumulate: unchanged). */
+typedef struct {
+    const void *dy;
+    long long dy_stride;
+    const void *x;
+    long long x_stride;
+    const float *saved;
+    void *dx;
+    long long dx_stride;
+    void *dgate_up, *ddown;
+    ep_dtype grad_dtype;
+    int accumulate; /* 0/1 */
+} ep_ffn_grads;
+
+ep_status ep_ffn_backward(ep_ffn *h, const ep_ffn_grads *grads, int num_tokens, void *workspace,
+                          size_t workspace_bytes, void *stream);
+
+ep_status ep_ffn_destroy(ep_ffn *h);
 
 #ifdef __cplusplus
 }
