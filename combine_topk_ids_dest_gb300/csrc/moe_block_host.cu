@@ -219,9 +219,6 @@ struct ep_ffn {
     ep_ffn_config cfg;
     int device, sms;
     Flags flags;
-    ep_experts *few;   // the block as one expert, for up to EP_MOE_MAX_TOKENS rows
-    int32_t *ids;      // of those rows: 0 ...
-    float *weights;    // ... with weight 1
 };
 
 namespace {
@@ -250,8 +247,6 @@ ep_status check_ffn_tokens(const ep_ffn *h, int num_tokens)
     return EP_OK;
 }
 
-bool few_rows(ep_ffn_call call, int num_tokens) { return call == EP_FFN_RUN && num_tokens <= EP_MOE_MAX_TOKENS; }
-
 // The intermediate rows; for the backward pass the gradients of gate and up too.
 struct FfnLayout {
     size_t off_dgu, total;
@@ -260,8 +255,6 @@ struct FfnLayout {
         const size_t row = size_t(c.intermediate) * 2;
         off_dgu = align256(num_tokens * row);
         total = off_dgu + (call == EP_FFN_BACKWARD ? align256(num_tokens * 2 * row) : 0);
-        if (few_rows(call, num_tokens))
-            total = 0;
     }
 };
 
@@ -282,6 +275,7 @@ ep_status product(const ep_ffn *h, moe::FfnProduct &p, const Matrix &ma, const M
     if (st != EP_OK)
         return st;
     p.a.err = h->flags.err;
+    p.a.aligned = aligned(p.a.out, 8) && p.a.out_stride % 4 == 0;
     p.a.chk = chk;
     const cudaError_t ce = moe::launch_ffn(p, h->sms, s);
     return ce == cudaSuccess ? EP_OK : cuda_error(ce, "launch");
@@ -309,32 +303,14 @@ ep_status ep_ffn_create(const ep_ffn_config *cfg, ep_ffn **out)
     h->cfg = *cfg;
     h->device = dev;
     h->sms = sms;
-    const ep_weight w[2] = {{cfg->gate_up, 0, 0, EP_DTYPE_BF16}, {cfg->down, 0, 0, EP_DTYPE_BF16}};
-    const ep_experts_config few = {1, 0, 1, cfg->hidden, cfg->intermediate, EP_MOE_MAX_TOKENS, w[0], w[1]};
-    st = ep_experts_create(&few, nullptr, 0, &h->few);
-    if (st == EP_OK)
-        st = h->flags.make();
+    st = h->flags.make();
     if (st == EP_OK) {
-        cudaError_t ce = moe::ffn_setup();
-        if (ce == cudaSuccess)
-            ce = cudaMalloc(reinterpret_cast<void **>(&h->ids), EP_MOE_MAX_TOKENS * 8);
-        if (ce == cudaSuccess) {
-            h->weights = reinterpret_cast<float *>(h->ids + EP_MOE_MAX_TOKENS);
-            ce = cudaMemset(h->ids, 0, EP_MOE_MAX_TOKENS * 4);
-        }
-        if (ce == cudaSuccess)
-            ce = moe::launch_ffn_ones(h->weights, EP_MOE_MAX_TOKENS, nullptr);
-        if (ce == cudaSuccess)
-            ce = cudaStreamSynchronize(nullptr);
+        const cudaError_t ce = moe::ffn_setup();
         if (ce != cudaSuccess)
-            st = cuda_error(ce, "the handle's kernels and memory");
+            st = cuda_error(ce, "the handle's kernels");
     }
     if (st != EP_OK) {
-        if (h->ids)
-            cudaFree(h->ids);
         h->flags.free();
-        if (h->few)
-            ep_experts_destroy(h->few);
         delete h;
         return st;
     }
@@ -367,7 +343,6 @@ ep_status ep_ffn_run(ep_ffn *h, const void *x, long long x_stride, int num_token
     if (num_tokens == 0)
         return set_error(EP_OK, "");
     const int T = num_tokens, H = h->cfg.hidden, I = h->cfg.intermediate;
-    const ep_ffn_call call = saved ? EP_FFN_FORWARD : EP_FFN_RUN;
     st = check_rows("x", x, x_stride, H, 16, 8);
     if (st == EP_OK)
         st = check_rows("out", out, out_stride, H, 2, 1);
@@ -377,7 +352,7 @@ ep_status ep_ffn_run(ep_ffn *h, const void *x, long long x_stride, int num_token
         MOE_FAIL("saved is not 16-byte aligned");
     const Span in = {"x", x, extent(T, x_stride, H, 2), x_stride}, y = {"out", out, extent(T, out_stride, H, 2), out_stride},
                keep = {"saved", saved, extent(T, 2 * I, 2 * I, 4), 2 * I};
-    const FfnLayout l(h->cfg, call, T);
+    const FfnLayout l(h->cfg, saved ? EP_FFN_FORWARD : EP_FFN_RUN, T);
     st = check_overlap(y, in, false);
     if (st == EP_OK)
         st = check_overlap(keep, in, false);
@@ -389,8 +364,6 @@ ep_status ep_ffn_run(ep_ffn *h, const void *x, long long x_stride, int num_token
         st = h->flags.take();
     if (st != EP_OK)
         return st;
-    if (few_rows(call, T))
-        return ep_experts_run(h->few, x, x_stride, h->ids, h->weights, T, out, out_stride, stream);
     unsigned long long *rec = epk::check_record();
     const epk::CheckCtx chk = epk::check_ctx(rec);
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
@@ -411,6 +384,7 @@ ep_status ep_ffn_run(ep_ffn *h, const void *x, long long x_stride, int num_token
     p.a.M = H;
     p.a.N = T;
     p.a.K = I;
+    p.a.early = moe::kFfnWeights;
     p.a.out = out;
     p.a.out_stride = out_stride;
     st = product(h, p, w2, mh, chk, s);
@@ -496,9 +470,12 @@ ep_status ep_ffn_backward(ep_ffn *h, const ep_ffn_grads *grads, int num_tokens, 
         p.a.dgu = dgu;
         st = product(h, p, w2, mdy, chk, s);
     }
+    int early = moe::kFfnWeights;
     if (st == EP_OK && g.dx) {
         moe::FfnProduct p = {};
         p.a_mn = true;
+        p.a.early = early;
+        early = moe::kFfnAll;  // for what comes next
         p.a.M = H;
         p.a.N = T;
         p.a.K = 2 * I;
@@ -509,6 +486,8 @@ ep_status ep_ffn_backward(ep_ffn *h, const ep_ffn_grads *grads, int num_tokens, 
     if (st == EP_OK && g.dgate_up) {
         moe::FfnProduct p = {};
         p.a_mn = p.b_mn = true;
+        p.a.early = early;
+        early = moe::kFfnAll;
         p.a.M = H;
         p.a.N = 2 * I;
         p.a.K = T;
@@ -521,6 +500,7 @@ ep_status ep_ffn_backward(ep_ffn *h, const ep_ffn_grads *grads, int num_tokens, 
     if (st == EP_OK && g.ddown) {
         moe::FfnProduct p = {};
         p.a_mn = p.b_mn = true;
+        p.a.early = early == moe::kFfnAll ? moe::kFfnAll : moe::kFfnNone;  // h is the last kernel's
         p.a.M = I;
         p.a.N = H;
         p.a.K = T;
@@ -537,8 +517,6 @@ ep_status ep_ffn_destroy(ep_ffn *h)
 {
     if (h) {
         wait_for_device(h->device);
-        ep_experts_destroy(h->few);
-        cudaFree(h->ids);
         h->flags.free();
         delete h;
     }

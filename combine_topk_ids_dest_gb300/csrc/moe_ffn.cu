@@ -24,6 +24,8 @@
 //  - splits: for few tiles. A block has 128 features, a cluster of 1 to 8 blocks
 //    shares a tile's K. Their sums meet in distributed shared memory, added in
 //    the order of K, a share of the rows in each block.
+#include <cmath>
+
 #include <cuda_bf16.h>
 
 #include "moe_sched.h"
@@ -32,12 +34,14 @@ namespace moe {
 
 namespace {
 
-constexpr int kThreads = 384;       // warp 0 copies, warp 1 multiplies, warps 4 to 11 store
-constexpr int kEpilogue = 256;
+// Threads that store results: of a pair's block 16 warps, which have the next tile's MMAs to hide under; of a split's 8.
+static __host__ __device__ constexpr int storers(bool pair) { return pair ? 512 : 256; }
+// Warp 0 copies, warp 1 multiplies, warps from the fourth on store.
+static __host__ __device__ constexpr int threads(bool pair) { return 128 + storers(pair); }
 constexpr int kMaxStages = 12;
 constexpr int kBlockA = 16384;      // 128 features x 64 k
 constexpr int kHalfTmem = 256;      // columns of one accumulator
-constexpr int kExchange = 4 * 2 * 2 * 1024;  // gate and up: [pair of warps][turn][which][8 rows][32 lanes] floats
+constexpr int kExchange = 16 * 16 * 32 * 4;  // [warps][rows][features] floats
 constexpr int kBand = 8;            // row tiles of a band of tiles
 
 struct Shared {
@@ -48,84 +52,109 @@ struct Shared {
     int abort, issued;
 };
 
-static __device__ __forceinline__ void tmem_ld8_wait(uint32_t addr, float (&v)[8])
+// Tensor memory is given out in powers of two from 32 columns on.
+static __host__ __device__ __forceinline__ uint32_t tmem_columns(int n)
 {
-    tmem_ld8(addr, v);
-    tmem_wait_ld();
+    return n <= 32 ? 32 : n <= 64 ? 64 : n <= 128 ? 128 : 256;
 }
 
-// silu and its derivative times what reaches them. e = exp(-g), bounded: sigma is then 1e-35 where it would be less.
+// silu of g and its derivative, to some 5e-6 of their values (the fast exponential and division; the results are rounded
+// to 2^-8). e = exp(-g), bounded for the derivative: sigma is then 1e-35 where it would be less.
+static __device__ __forceinline__ float silu(float g) { return __fdividef(g, 1.0f + __expf(-g)); }
+
 struct Gate {
     float silu, slope;
     __device__ __forceinline__ explicit Gate(float g)
     {
-        const float e = expf(fminf(-g, 80.0f)), s = 1.0f / (1.0f + e);
+        const float e = __expf(fminf(-g, 80.0f)), s = __fdividef(1.0f, 1.0f + e);
         silu = g * s;
         slope = s * fmaf(g, e * s, 1.0f);
     }
 };
 
-// What one thread does with the results of one feature for successive rows.
-template <int EPI> struct Sink {
+static __device__ __forceinline__ void add4(float4 &a, const float4 &b)
+{
+    a.x += b.x, a.y += b.y, a.z += b.z, a.w += b.w;
+}
+
+static __device__ __forceinline__ uint2 pack4(float a, float b, float c, float d)
+{
+    const __nv_bfloat162 lo = __floats2bfloat162_rn(a, b), hi = __floats2bfloat162_rn(c, d);
+    return make_uint2(*reinterpret_cast<const uint32_t *>(&lo), *reinterpret_cast<const uint32_t *>(&hi));
+}
+
+// What one thread does with the results of four features (col ..) of a row. Feature counts are multiples of 8: all four
+// are there, or none.
+// WEIGHT: of a weight's gradient, which may be fp32 and is aligned.
+template <int EPI, bool WEIGHT> struct Sink {
     const FfnArgs &a;
     const int col;
+
+    struct Kept {
+        float4 g, u;
+    };
+
     __device__ __forceinline__ Sink(const FfnArgs &a_, int col_) : a(a_), col(col_) {}
 
-    // n results v[0..n) (joined: of gate, with those of up in w) for rows t, t + step, ...
-    template <int R> __device__ __forceinline__ void put(int t, int step, const float (&v)[R], const float (&w)[R])
+    __device__ __forceinline__ bool live(int t) const { return col < a.M && t < a.N; }
+
+    // split: the kept g and u of row t, ahead of their use
+    __device__ __forceinline__ void fetch(int t, Kept &k) const
     {
-        if (col >= a.M)
-            return;
-        if (EPI == kFfnStore) {
-            if (a.fp32) {
-                float *p = static_cast<float *>(a.out) + static_cast<long long>(t) * a.out_stride + col;
-#pragma unroll
-                for (int i = 0; i < R; ++i, p += step * a.out_stride)
-                    if (t + i * step < a.N && inside(p, 4))
-                        *p = a.accumulate ? *p + v[i] : v[i];
-            } else {
-                __nv_bfloat16 *p = static_cast<__nv_bfloat16 *>(a.out) + static_cast<long long>(t) * a.out_stride + col;
-#pragma unroll
-                for (int i = 0; i < R; ++i, p += step * a.out_stride)
-                    if (t + i * step < a.N && inside(p, 2))
-                        *p = __float2bfloat16_rn(v[i]);
-            }
-        } else if (EPI == kFfnJoin) {
-            __nv_bfloat16 *p = static_cast<__nv_bfloat16 *>(a.out) + static_cast<long long>(t) * a.out_stride + col;
-            float *s = a.saved + 2LL * t * a.M + col;
-#pragma unroll
-            for (int i = 0; i < R; ++i, p += step * a.out_stride, s += 2LL * step * a.M)
-                if (t + i * step < a.N) {
-                    *p = __float2bfloat16_rn(swiglu(v[i], w[i]));
-                    if (a.saved) {
-                        s[0] = v[i];
-                        s[a.M] = w[i];
-                    }
-                }
-        } else {
-            __nv_bfloat16 *p = static_cast<__nv_bfloat16 *>(a.out) + static_cast<long long>(t) * a.out_stride + col;
-            __nv_bfloat16 *d = a.dgu + 2LL * t * a.M + col;
-            const float *s = a.saved + 2LL * t * a.M + col;
-            float g[R], u[R];
-#pragma unroll
-            for (int i = 0; i < R; ++i, s += 2LL * step * a.M) {
-                const bool live = t + i * step < a.N;
-                g[i] = live ? s[0] : 0.0f;
-                u[i] = live ? s[a.M] : 0.0f;
-            }
-#pragma unroll
-            for (int i = 0; i < R; ++i, p += step * a.out_stride, d += 2LL * step * a.M)
-                if (t + i * step < a.N) {
-                    const Gate gate(g[i]);
-                    d[0] = __float2bfloat16_rn(v[i] * u[i] * gate.slope);
-                    d[a.M] = __float2bfloat16_rn(v[i] * gate.silu);
-                    *p = __float2bfloat16_rn(swiglu(g[i], u[i]));
-                }
+        if (EPI == kFfnSplit && live(t)) {
+            const float *const s = a.saved + 2LL * t * a.M + col;
+            k.g = *reinterpret_cast<const float4 *>(s);
+            k.u = *reinterpret_cast<const float4 *>(s + a.M);
         }
     }
-    __device__ __forceinline__ bool inside(const void *p, int bytes) const
+
+    // v: the results; joined: of gate, those of up are in k.u
+    __device__ __forceinline__ void put(int t, const float4 &v, const Kept &k) const
     {
-        return EP_IN_BOUNDS(a.chk, epk::kSiteMoeOut, p, bytes, a.out, bytes * ((a.N - 1LL) * a.out_stride + a.M));
+        if (!live(t))
+            return;
+        const long long at = t * a.out_stride + col;
+        if (WEIGHT && a.fp32) {
+            float4 *const p = reinterpret_cast<float4 *>(static_cast<float *>(a.out) + at);
+            if (inside(p, 16, 4)) {
+                const float4 o = a.accumulate ? *p : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                *p = a.accumulate ? make_float4(o.x + v.x, o.y + v.y, o.z + v.z, o.w + v.w) : v;
+            }
+            return;
+        }
+        uint2 r;
+        if (EPI == kFfnStore) {
+            r = pack4(v.x, v.y, v.z, v.w);
+        } else if (EPI == kFfnJoin) {
+            r = pack4(silu(v.x) * k.u.x, silu(v.y) * k.u.y, silu(v.z) * k.u.z, silu(v.w) * k.u.w);
+            if (a.saved) {
+                float *const s = a.saved + 2LL * t * a.M + col;
+                *reinterpret_cast<float4 *>(s) = v;
+                *reinterpret_cast<float4 *>(s + a.M) = k.u;
+            }
+        } else {
+            const Gate x(k.g.x), y(k.g.y), z(k.g.z), w(k.g.w);
+            __nv_bfloat16 *const d = a.dgu + 2LL * t * a.M + col;
+            *reinterpret_cast<uint2 *>(d) = pack4(v.x * k.u.x * x.slope, v.y * k.u.y * y.slope, v.z * k.u.z * z.slope,
+                                                  v.w * k.u.w * w.slope);
+            *reinterpret_cast<uint2 *>(d + a.M) = pack4(v.x * x.silu, v.y * y.silu, v.z * z.silu, v.w * w.silu);
+            r = pack4(x.silu * k.u.x, y.silu * k.u.y, z.silu * k.u.z, w.silu * k.u.w);
+        }
+        __nv_bfloat16 *const p = static_cast<__nv_bfloat16 *>(a.out) + at;
+        if (!inside(p, 8, 2))
+            return;
+        if (EPI != kFfnStore || WEIGHT || a.aligned) {
+            *reinterpret_cast<uint2 *>(p) = r;
+        } else {
+            uint16_t *const e = reinterpret_cast<uint16_t *>(p);
+            e[0] = r.x & 0xFFFF, e[1] = r.x >> 16, e[2] = r.y & 0xFFFF, e[3] = r.y >> 16;
+        }
+    }
+
+    __device__ __forceinline__ bool inside(const void *p, int bytes, int size) const
+    {
+        return EPI != kFfnStore ||
+               EP_IN_BOUNDS(a.chk, epk::kSiteMoeOut, p, bytes, a.out, size * ((a.N - 1LL) * a.out_stride + a.M));
     }
 };
 
@@ -140,7 +169,7 @@ static __device__ __forceinline__ void tile_of(const FfnArgs &a, int i, int &m, 
 }
 
 template <int EPI, bool A_MN, bool B_MN, bool PAIR>
-__global__ void __launch_bounds__(kThreads, 1) ffn_kernel(const __grid_constant__ FfnArgs a)
+__global__ void __launch_bounds__(threads(PAIR), PAIR ? 1 : 2) ffn_kernel(const __grid_constant__ FfnArgs a)
 {
     extern __shared__ uint8_t dyn[];
     __shared__ Shared sh;
@@ -154,6 +183,8 @@ __global__ void __launch_bounds__(kThreads, 1) ffn_kernel(const __grid_constant_
     const int rows_b = PAIR ? a.tile_n / 2 : a.tile_n, blocks_b = (rows_b + 63) / 64;
     const int bytes = kBlockA + (B_MN ? blocks_b * 8192 : rows_b * 128);
     constexpr int kFeatures = EPI == kFfnJoin ? 64 : 128;  // of a block
+    constexpr int kEpilogue = storers(PAIR);
+    using To = Sink<EPI, A_MN && B_MN>;
     volatile int *const abort = &sh.abort;
 
     if (tid == 0) {
@@ -171,49 +202,71 @@ __global__ void __launch_bounds__(kThreads, 1) ffn_kernel(const __grid_constant_
         tma_prefetch_map(&a.ma);
         tma_prefetch_map(&a.mb);
     }
+    const uint32_t columns = PAIR ? 2 * kHalfTmem : tmem_columns(a.tile_n);
     if (warp == 1)
-        tmem_alloc<PAIR>(smem_u32(&sh.tmem), 2 * kHalfTmem);
+        tmem_alloc<PAIR>(smem_u32(&sh.tmem), columns);
     tc_fence_before();
     __syncthreads();
-    cluster_sync();  // no copy or arrival reaches a block before its barriers are set
+    if (PAIR)
+        cluster_sync();  // no copy or arrival reaches a block before its barriers are set
     tc_fence_after();
     const uint32_t tmem = sh.tmem;
 
     if (warp == 0 && elect_one()) {
         // ---- copies ----
+        auto load = [&](uint32_t dst, const CUtensorMap *map, uint32_t full, int x, int y) {
+            if (PAIR)
+                tma_load_2d_pair(dst, map, in_first_block(full), x, y);
+            else
+                tma_load_2d(dst, map, full, x, y);
+        };
+        auto expect = [&](uint32_t full) {
+            if (!PAIR || rank == 0)
+                mbar_expect(full, PAIR ? 2 * bytes : bytes);
+        };
+        auto load_a = [&](uint32_t dst, uint32_t full, int m, int k) {
+            const int m0 = (PAIR ? 2 * m + rank : m) * kFeatures;
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const int f = EPI == kFfnJoin ? m0 + j * a.M : m0 + j * 64;
+                load(dst + j * 8192, &a.ma, full, A_MN ? f : k, A_MN ? k : f);
+            }
+        };
+        auto load_b = [&](uint32_t dst, uint32_t full, int n, int k) {
+            const int n0 = n * a.tile_n + (PAIR ? rank * rows_b : 0);
+            if (B_MN) {
+                for (int j = 0; j < blocks_b; ++j)
+                    load(dst + kBlockA + j * 8192, &a.mb, full, n0 + j * 64, k);
+            } else {
+                load(dst + kBlockA, &a.mb, full, k, n0);
+            }
+        };
+        int m, n, ahead = 0;  // the ring's first round: weights that are copied before the rows are there
+        if (a.early == kFfnWeights && first < tiles) {
+            tile_of(a, first, m, n);
+            for (; ahead < a.stages && c0 + ahead < c1; ++ahead) {
+                expect(smem_u32(&sh.full[ahead]));
+                load_a(ring + ahead * bytes, smem_u32(&sh.full[ahead]), m, (c0 + ahead) * kChunk);
+            }
+        }
+        if (a.early != kFfnAll)
+            pdl_wait();
+        pdl_launch_next();
         Cursor at;
         int issued = 0;
         bool run = true;
         for (int i = first; run && i < tiles; i += next) {
-            int m, n;
             tile_of(a, i, m, n);
-            const int m0 = (PAIR ? 2 * m + rank : m) * kFeatures, n0 = n * a.tile_n + (PAIR ? rank * rows_b : 0);
             for (int c = c0; c < c1; ++c) {
-                run = mbar_wait(smem_u32(&sh.empty[at.s]), at.parity ^ 1, abort, kWaitEmptyA);
-                if (!run)
-                    break;
-                const uint32_t to = ring + at.s * bytes, mine = smem_u32(&sh.full[at.s]);
-                const uint32_t bar = PAIR ? in_first_block(mine) : mine;
-                if (!PAIR || rank == 0)
-                    mbar_expect(mine, PAIR ? 2 * bytes : bytes);
-                auto load = [&](uint32_t dst, const CUtensorMap *map, int x, int y) {
-                    if (PAIR)
-                        tma_load_2d_pair(dst, map, bar, x, y);
-                    else
-                        tma_load_2d(dst, map, bar, x, y);
-                };
-                const int k = c * kChunk;
-#pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    const int f = EPI == kFfnJoin ? m0 + j * a.M : m0 + j * 64;
-                    load(to + j * 8192, &a.ma, A_MN ? f : k, A_MN ? k : f);
+                const uint32_t to = ring + at.s * bytes, full = smem_u32(&sh.full[at.s]);
+                if (issued >= ahead) {
+                    run = mbar_wait(smem_u32(&sh.empty[at.s]), at.parity ^ 1, abort, kWaitEmptyA);
+                    if (!run)
+                        break;
+                    expect(full);
+                    load_a(to, full, m, c * kChunk);
                 }
-                if (B_MN) {
-                    for (int j = 0; j < blocks_b; ++j)
-                        load(to + kBlockA + j * 8192, &a.mb, n0 + j * 64, k);
-                } else {
-                    load(to + kBlockA, &a.mb, k, n0);
-                }
+                load_b(to, full, n, c * kChunk);
                 at.next(a.stages);
                 ++issued;
             }
@@ -269,50 +322,58 @@ __global__ void __launch_bounds__(kThreads, 1) ffn_kernel(const __grid_constant_
         mbar_wait(smem_u32(&sh.drain), 0, nullptr, kWaitOther);
     } else if (warp >= 4 && PAIR) {
         // ---- results, under the next tile's products ----
+        // 16 rows x 32 features of a warp at a time, through shared memory: then a lane has four features of a row. A
+        // quarter of the lanes (features) has four warps, which take its 16 rows in turn. Joined: a warp of quarters 0 and
+        // 1 has gate, the one two quarters on up of the same 32 features; each joins half of the 16 rows.
         Cursor at_d;
-        const int quarter = warp & 3, half = (warp - 4) >> 2, span = a.tile_n / 2;  // two warps share the lanes' rows
+        const int quarter = warp & 3, turn = (warp - 4) >> 2, steps = a.tile_n / 16;
+        const bool second = EPI == kFfnJoin && quarter >= 2;
+        constexpr int kRows = EPI == kFfnJoin ? 8 : 16;  // of a warp's 16
+        const int strip = EPI == kFfnJoin ? quarter & 1 : quarter, row0 = (second ? 8 : 0) + (lane >> 3);
         float *const exchange = reinterpret_cast<float *>(dyn + (ring - dyn0) + a.stages * bytes);
+        float *const tile = exchange + (EPI == kFfnJoin ? (turn * 2 + strip) * 1024 : (turn * 4 + quarter) * 512);
+        float *const mine = tile + (second ? 512 : 0) + lane;
+        const float4 *const from = reinterpret_cast<const float4 *>(tile + row0 * 32 + (lane & 7) * 4);
         for (int i = first; i < tiles; i += next) {
+            int m, n;
+            tile_of(a, i, m, n);
+            const To sink(a, (2 * m + rank) * kFeatures + strip * 32 + (lane & 7) * 4);
+            const int t0 = n * a.tile_n + row0;
+            typename To::Kept kept[kRows / 4];
+            auto fetch = [&](int step) {
+                if (EPI == kFfnSplit && step < steps)
+#pragma unroll
+                    for (int r = 0; r < kRows / 4; ++r)
+                        sink.fetch(t0 + step * 16 + 4 * r, kept[r]);
+            };
+            fetch(turn);
             const bool run = mbar_wait(smem_u32(&sh.full_d[at_d.s]), at_d.parity, abort, kWaitFullD);
             if (!named_all(1, kEpilogue, run))
                 break;
             tc_fence_after();
-            int m, n;
-            tile_of(a, i, m, n);
-            const uint32_t d = tmem + (static_cast<uint32_t>(quarter) << 21) + at_d.s * kHalfTmem + half * span;
-            const int t0 = n * a.tile_n + half * span, m0 = (2 * m + rank) * kFeatures;
-            if (EPI == kFfnJoin) {
-                // A warp has gate (quarters 0, 1) or up (2, 3) of 32 features for the same rows as another has the
-                // other: the first joins them for the even steps of 8 rows, the second for the odd ones.
-                const bool up = quarter >= 2;
-                const int pair = half * 2 + (quarter & 1);
-                Sink<EPI> sink(a, m0 + (quarter & 1) * 32 + lane);
-                for (int j = 0, turn = 0; j < span; j += 16, turn ^= 1) {
-                    float even[8], odd[8], got[8];
-                    tmem_ld8(d + j, even);
-                    if (j + 8 < span)
-                        tmem_ld8(d + j + 8, odd);
-                    tmem_wait_ld();
-                    float *const slot = exchange + ((pair * 2 + turn) * 2) * 256 + lane;
+            const uint32_t d = tmem + (static_cast<uint32_t>(quarter) << 21) + at_d.s * kHalfTmem;
+            for (int step = turn; step < steps; step += 4) {
+                float v[16];
+                tmem_ld16(d + step * 16, v);
+                tmem_wait_ld();
+                if (EPI == kFfnJoin)
+                    named_sync(2 + turn * 2 + strip, 64);  // the rows before are read
+                else
+                    __syncwarp();
 #pragma unroll
-                    for (int r = 0; r < 8; ++r)
-                        slot[(up ? 256 : 0) + r * 32] = up ? even[r] : odd[r];
-                    named_sync(2 + pair, 64);
+                for (int r = 0; r < 16; ++r)
+                    mine[r * 32] = v[r];
+                if (EPI == kFfnJoin)
+                    named_sync(2 + turn * 2 + strip, 64);
+                else
+                    __syncwarp();
 #pragma unroll
-                    for (int r = 0; r < 8; ++r)
-                        got[r] = slot[(up ? 0 : 256) + r * 32];
-                    if (!up)
-                        sink.put(t0 + j, 1, even, got);
-                    else if (j + 8 < span)
-                        sink.put(t0 + j + 8, 1, got, odd);
+                for (int r = 0; r < kRows / 4; ++r) {
+                    if (EPI == kFfnJoin)
+                        kept[r].u = from[128 + r * 32];
+                    sink.put(t0 + step * 16 + 4 * r, from[r * 32], kept[r]);
                 }
-            } else {
-                Sink<EPI> sink(a, m0 + quarter * 32 + lane);
-                for (int j = 0; j < span; j += 8) {
-                    float v[8];
-                    tmem_ld8_wait(d + j, v);
-                    sink.put(t0 + j, 1, v, v);
-                }
+                fetch(step + 4);
             }
             tc_fence_before();
             __syncwarp();
@@ -330,56 +391,70 @@ __global__ void __launch_bounds__(kThreads, 1) ffn_kernel(const __grid_constant_
             const bool run = mbar_wait(smem_u32(&sh.full_d[0]), 0, abort, kWaitFullD);
             if (named_all(1, kEpilogue, run)) {
                 tc_fence_after();
-                const int quarter = warp & 3, half = (warp - 4) >> 2, span = a.tile_n / 2;
-                const uint32_t d = tmem + (static_cast<uint32_t>(quarter) << 21) + half * span;
-                float *const to = sums + half * span * 128 + quarter * 32 + lane;
-                for (int j = 0; j < span; j += 8) {
-                    float v[8];
-                    tmem_ld8_wait(d + j, v);
+                const int quarter = warp & 3;
+                const uint32_t d = tmem + (static_cast<uint32_t>(quarter) << 21);
+                float *const to = sums + quarter * 32 + lane;
+                for (int j = (warp - 4) / 4 * 16; j < a.tile_n; j += 32) {
+                    float v[16];
+                    tmem_ld16(d + j, v);
+                    tmem_wait_ld();
 #pragma unroll
-                    for (int r = 0; r < 8; ++r)
+                    for (int r = 0; r < 16; ++r)
                         to[(j + r) * 128] = v[r];
                 }
                 tc_fence_before();
             }
         }
         __syncwarp();
-        cluster_sync();
+        if (a.split > 1)
+            cluster_sync();
+        else
+            __syncthreads();
         if (warp >= 4 && !sh.abort) {
-            constexpr int kWarps = kFeatures / 32, kStep = kEpilogue / 32 / kWarps;  // warps side by side; rows at a time
-            const int f = (warp - 4) % kWarps * 32 + lane;
+            constexpr int kLanes = kFeatures / 4, kStep = kEpilogue / kLanes, R = EPI == kFfnStore ? 2 : 1;  // lanes of a row, rows at a time
+            const int f = lane % kLanes * 4;
             const int lo = a.tile_n * rank / a.split, hi = a.tile_n * (rank + 1) / a.split;
             const uint32_t at = smem_u32(sums) + f * 4;
-            Sink<EPI> sink(a, m * kFeatures + f);
-            constexpr int R = 4;
-            for (int j = lo + (warp - 4) / kWarps; j < hi; j += kStep * R) {
-                float v[R], w[R];
+            const To sink(a, m * kFeatures + f);
+            for (int j = lo + (tid - 128) / kLanes; j < hi; j += kStep * R) {
+                float4 v[R];
+                typename To::Kept k[R];
+#pragma unroll
+                for (int r = 0; r < R; ++r) {
+                    v[r] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                    if (EPI == kFfnJoin)
+                        k[r].u = v[r];
+                    if (j + r * kStep < hi)
+                        sink.fetch(n * a.tile_n + j + r * kStep, k[r]);
+                }
+                for (int s0 = 0; s0 < a.split; s0 += 4) {
+                    float4 x[4][R], y[4][R];
+#pragma unroll
+                    for (int s = 0; s < 4; ++s)
+                        if (s0 + s < a.split) {
+                            const uint32_t from = in_block(at, s0 + s);
+#pragma unroll
+                            for (int r = 0; r < R; ++r)
+                                if (j + r * kStep < hi) {
+                                    x[s][r] = ld_cluster4(from + (j + r * kStep) * 512);
+                                    if (EPI == kFfnJoin)
+                                        y[s][r] = ld_cluster4(from + (j + r * kStep) * 512 + 256);
+                                }
+                        }
+#pragma unroll
+                    for (int s = 0; s < 4; ++s)
+                        if (s0 + s < a.split)
+#pragma unroll
+                            for (int r = 0; r < R; ++r) {
+                                add4(v[r], x[s][r]);
+                                if (EPI == kFfnJoin)
+                                    add4(k[r].u, y[s][r]);
+                            }
+                }
 #pragma unroll
                 for (int r = 0; r < R; ++r)
-                    v[r] = w[r] = 0.0f;
-                for (int s = 0; s < a.split; ++s) {
-                    const uint32_t from = in_block(at, s);
-#pragma unroll
-                    for (int r = 0; r < R; ++r) {
-                        const int row = j + r * kStep;
-                        if (row < hi) {
-                            v[r] += ld_cluster(from + row * 512);
-                            if (EPI == kFfnJoin)
-                                w[r] += ld_cluster(from + row * 512 + 256);
-                        }
-                    }
-                }
-                // rows of another block's share are not this one's to store
-                if (j + (R - 1) * kStep < hi) {
-                    sink.put(n * a.tile_n + j, kStep, v, w);
-                } else {
-#pragma unroll
-                    for (int r = 0; r < R; ++r)
-                        if (j + r * kStep < hi) {
-                            const float v1[1] = {v[r]}, w1[1] = {w[r]};
-                            sink.put(n * a.tile_n + j + r * kStep, kStep, v1, w1);
-                        }
-                }
+                    if (j + r * kStep < hi)  // the others are another block's
+                        sink.put(n * a.tile_n + j + r * kStep, v[r], k[r]);
             }
         }
     }
@@ -402,15 +477,18 @@ __global__ void __launch_bounds__(kThreads, 1) ffn_kernel(const __grid_constant_
         __syncthreads();
     }
     if (warp == 1)
-        tmem_free<PAIR>(tmem, 2 * kHalfTmem);
-    cluster_sync();  // the other blocks' copies, arrivals and reads have come
+        tmem_free<PAIR>(tmem, columns);
+    if (PAIR || a.split > 1)
+        cluster_sync();  // the other blocks' copies, arrivals and reads have come
+    if (a.early == kFfnAll && tid == 0)
+        pdl_wait();  // what follows this kernel follows the one before it too
 }
 
-// Gradients of no rows; the routing weights of a block that is one expert.
-__global__ void __launch_bounds__(256) fill_kernel(uint32_t *p, size_t words, uint32_t value)
+// Gradients of no rows.
+__global__ void __launch_bounds__(256) zero_kernel(uint32_t *p, size_t words)
 {
     for (size_t i = blockIdx.x * size_t(256) + threadIdx.x; i < words; i += size_t(gridDim.x) * 256)
-        p[i] = value;
+        p[i] = 0;
 }
 
 using Kernel = void (*)(FfnArgs);
@@ -434,16 +512,20 @@ int stage_bytes(const FfnProduct &p)
     return kBlockA + (p.b_mn ? div_up(rows, 64) * 8192 : rows * 128);
 }
 
-constexpr int kRoom = kSmemMax - 1024 - 64 - static_cast<int>(sizeof(Shared));
+// Dynamic shared memory of a block that has an SM for itself, and of one that shares it with another.
+constexpr int kRoom = kSmemMax - 64 - static_cast<int>(sizeof(Shared));
+constexpr int kHalfRoom = (228 * 1024) / 2 - 1024 - 64 - static_cast<int>(sizeof(Shared));
+constexpr int kShareRows = 128;  // up to so many rows a tile, a split's blocks can share an SM
 
 }  // namespace
 
-// Cycles of a tile's 64 k, as measured: the MMAs need 2 a row, the copies of a block's operands 64 bytes a cycle.
-// The plan with the smallest product of waves of blocks and cycles of a block.
+// The plan of least cost, in cycles. A tile's 64 k take 2 cycles a row in the MMAs or 64 bytes a cycle of the copies
+// of a block's operands, whichever is more; the weights, or all operands, have to come from DRAM once.
 void ffn_plan(FfnProduct *p, int sms)
 {
     FfnArgs &a = p->a;
     const int chunks = div_up(a.K, kChunk), features = p->epilogue == kFfnJoin ? 64 : 128;
+    const double dram = 2.0 * a.K * (static_cast<double>(a.M) * (p->epilogue == kFfnJoin ? 2 : 1) + a.N) / 3500.0;
     double best = 0.0;
     bool any = false;
     int best_n = 16, best_split = 1;
@@ -454,13 +536,20 @@ void ffn_plan(FfnProduct *p, int sms)
             if (n > 16 && div_up(a.N, n - 16) == n_tiles)
                 continue;  // the same tiles with more waste
             const double tiles = static_cast<double>(n_tiles) * div_up(a.M, features * (pair ? 2 : 1));
+            const double mma = 2.0 * n, copy = (kBlockA + 128.0 * (pair ? n / 2 : n)) / 64.0;
+            const double chunk = mma > copy ? mma : copy;
             for (int split = 1; split <= (pair ? 1 : 8) && split <= chunks; split *= 2) {
-                const double mma = 2.0 * n, copy = (kBlockA + 128.0 * (pair ? n / 2 : n)) / 64.0;
-                const double chunk = mma > copy ? mma : copy;
-                const double slots = pair ? sms / 2 : sms;
-                const double waves = static_cast<double>(static_cast<long long>((tiles * split + slots - 1) / slots));
-                const double block = div_up(chunks, split) * chunk;
-                const double cost = pair ? 3000 + waves * (block + 400) + 10 * n : waves * (3000 + block + 16 * n);
+                double cost;
+                if (pair) {
+                    const double waves = std::ceil(tiles / (sms / 2));
+                    cost = waves * (chunks * chunk + 400.0);
+                    cost = (cost > dram ? cost : dram) + 3000.0 + 10.0 * n;
+                } else {
+                    const int resident = n <= kShareRows ? 2 : 1;  // they share the SM's MMAs and copies
+                    const double blocks = tiles * split, mine = std::ceil(blocks / sms);
+                    cost = mine * div_up(chunks, split) * chunk;
+                    cost = (cost > dram ? cost : dram) + std::ceil(blocks / (resident * sms)) * (3000.0 + 16.0 * n);
+                }
                 if (!any || cost < best) {
                     any = true;
                     best = cost;
@@ -476,16 +565,18 @@ void ffn_plan(FfnProduct *p, int sms)
     a.m_tiles = div_up(a.M, features * (best_pair ? 2 : 1));
     a.n_tiles = div_up(a.N, best_n);
     p->box_b = best_pair ? best_n / 2 : best_n;
-    const int room = kRoom - (best_pair ? kExchange : 0), stage = stage_bytes(*p);
-    a.stages = room / stage < kMaxStages ? room / stage : kMaxStages;
+    // Two blocks of a split on an SM where there are more blocks than SMs
+    const bool share = !best_pair && best_n <= kShareRows && static_cast<long long>(a.m_tiles) * a.n_tiles * best_split > sms;
+    const int room = share ? kHalfRoom : kRoom - (best_pair ? kExchange : 0), stage = stage_bytes(*p);
+    a.stages = (room - 1024) / stage < kMaxStages ? (room - 1024) / stage : kMaxStages;
 }
 
 cudaError_t ffn_setup()
 {
     cudaError_t ce = cudaSuccess;
     for (const void *f : ffn_kernels())
-        if (ce == cudaSuccess && f != reinterpret_cast<const void *>(fill_kernel))
-            ce = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, kRoom + 1024);
+        if (ce == cudaSuccess && f != reinterpret_cast<const void *>(zero_kernel))
+            ce = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, kRoom);
     return ce;
 }
 
@@ -494,33 +585,29 @@ cudaError_t launch_ffn(const FfnProduct &p, int sms, cudaStream_t stream)
     const FfnArgs &a = p.a;
     const int tiles = a.m_tiles * a.n_tiles;
     size_t ring = static_cast<size_t>(a.stages) * stage_bytes(p);
-    const size_t sums = static_cast<size_t>(a.tile_n) * 512;
+    const size_t sums = static_cast<size_t>(a.tile_n) * 512;  // no more than a stage or two
     if (!p.pair && ring < sums)
         ring = sums;
     cudaLaunchConfig_t cfg = {};
     const int pairs = sms / 2;
     cfg.gridDim = dim3(p.pair ? 2 * (tiles < pairs ? tiles : pairs) : tiles * a.split);
-    cfg.blockDim = dim3(kThreads);
+    cfg.blockDim = dim3(threads(p.pair));
     cfg.dynamicSmemBytes = 1024 + ring + (p.pair ? kExchange : 0);
     cfg.stream = stream;
-    cudaLaunchAttribute at[1];
+    cudaLaunchAttribute at[2];
     at[0].id = cudaLaunchAttributeClusterDimension;
     at[0].val.clusterDim.x = p.pair ? 2 : a.split;
     at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+    at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = at;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = 2;
     return cudaLaunchKernelEx(&cfg, p.pair ? kernel_of<true>(p) : kernel_of<false>(p), a);
 }
 
 cudaError_t launch_ffn_zero(void *p, size_t bytes, cudaStream_t stream)
 {
-    fill_kernel<<<1024, 256, 0, stream>>>(static_cast<uint32_t *>(p), bytes / 4, 0u);
-    return cudaGetLastError();
-}
-
-cudaError_t launch_ffn_ones(float *p, int n, cudaStream_t stream)
-{
-    fill_kernel<<<1, 256, 0, stream>>>(reinterpret_cast<uint32_t *>(p), n, 0x3F800000u);
+    zero_kernel<<<1024, 256, 0, stream>>>(static_cast<uint32_t *>(p), bytes / 4);
     return cudaGetLastError();
 }
 
@@ -532,7 +619,7 @@ std::vector<const void *> ffn_kernels()
         reinterpret_cast<const void *>(ffn_kernel<kFfnStore, false, false, PAIR>),          \
         reinterpret_cast<const void *>(ffn_kernel<kFfnStore, true, false, PAIR>),           \
         reinterpret_cast<const void *>(ffn_kernel<kFfnStore, true, true, PAIR>)
-    return {FFN(true), FFN(false), reinterpret_cast<const void *>(fill_kernel)};
+    return {FFN(true), FFN(false), reinterpret_cast<const void *>(zero_kernel)};
 #undef FFN
 }
 

@@ -218,6 +218,10 @@ std::vector<const void *> norm_kernels();  // every kernel of the file
 // What a product's results become: stored as they are, gate and up joined, or the gradients of gate and up.
 enum FfnEpilogue { kFfnStore = 0, kFfnJoin, kFfnSplit };
 
+// What of a product's operands may be read before the kernel that was queued before it has ended: nothing; A, which
+// that kernel, of the same call, does not write; everything, where that kernel itself began after what wrote them.
+enum FfnEarly { kFfnNone = 0, kFfnWeights, kFfnAll };
+
 // One product D[M features, N rows] = A[M, K] B[N, K]^T; a tile is 128 features (joined: 64, with gate and up) of a
 // block by tile_n rows.
 struct FfnArgs {
@@ -229,6 +233,8 @@ struct FfnArgs {
     unsigned int *err;
     int M, N, K, tile_n, m_tiles, n_tiles, stages, split;
     int fp32, accumulate;  // of out
+    int early;             // FfnEarly
+    int aligned;           // out and its rows are 8-byte aligned
     epk::CheckCtx chk;
 };
 
@@ -244,7 +250,6 @@ void ffn_plan(FfnProduct *p, int sms);
 cudaError_t ffn_setup();
 cudaError_t launch_ffn(const FfnProduct &p, int sms, cudaStream_t stream);
 cudaError_t launch_ffn_zero(void *p, size_t bytes, cudaStream_t stream);
-cudaError_t launch_ffn_ones(float *p, int n, cudaStream_t stream);
 std::vector<const void *> ffn_kernels();  // every kernel of the file
 
 // Binary versions of this library's MoE kernels, as epk::kernel_binary_versions.

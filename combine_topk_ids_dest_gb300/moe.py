@@ -470,8 +470,6 @@ class EpFfn(_Handle):
 
     def _workspace(self, call: int, n: int) -> Tuple[Optional[torch.Tensor], int, int]:
         """A call's workspace: the tensor, its address and its bytes."""
-        if call == _lib.EP_FFN_RUN and n <= _lib.EP_MOE_MAX_TOKENS:
-            return None, 0, 0
         size = ctypes.c_size_t(0)
         check(self._L.ep_ffn_workspace_size(self._live(), call, n, ctypes.byref(size)))
         ws = torch.empty(size.value, dtype=torch.uint8, device=self.device)

@@ -264,10 +264,9 @@ ep_status ep_norm_backward(const ep_norm_config *cfg, const void *dy, long long 
 /* ---- feed-forward ------------------------------------------------------------------
  * The gated block of a dense layer, or of an expert that every token uses:
  *   g = x W1^T;  u = x W3^T;  h = silu(g) u;  y = h W2^T
- * for any number of rows, and its gradients. bf16, sums fp32. Up to
- * EP_MOE_MAX_TOKENS rows the intermediate row h keeps 16 bits of mantissa,
- * above it is rounded to bf16, as are the gradients of g and u before they are
- * multiplied; y and the gradients are rounded once. g and u are not rounded.
+ * for any number of rows, and its gradients. bf16, sums fp32. The rows of h,
+ * and the gradients of g and u, are rounded to bf16 before the product that
+ * takes them; y and the gradients are rounded once. g and u are not rounded.
  */
 typedef struct ep_ffn ep_ffn;
 
