@@ -272,11 +272,19 @@ ep_status product(const ep_ffn *h, moe::FfnProduct &p, const Matrix &ma, const M
     ep_status st = encode_map(&p.a.ma, ma.name, 0, ma.p, ma.cols, ma.rows, 0, ma.stride, 0, moe::kChunk, 64);
     if (st == EP_OK)
         st = encode_map(&p.a.mb, mb.name, 0, mb.p, mb.cols, mb.rows, 0, mb.stride, 0, moe::kChunk, p.b_mn ? 64 : p.box_b);
+    moe::FfnArgs &a = p.a;
+    const int size = a.fp32 ? 4 : 2, features = p.epilogue == moe::kFfnJoin ? 64 : 128;
+    a.aligned = aligned(a.out, 8) && a.out_stride % 4 == 0;
+    // The checked build tests the stores of y and dx one by one; all others are bounded by their maps.
+    a.boxes = aligned(a.out, 16) && a.out_stride * size % 16 == 0 && !(EP_CHECKED && p.epilogue == moe::kFfnStore && !p.b_mn);
+    if (st == EP_OK && p.pair && a.boxes)
+        st = encode_result(&a.mo, "result", a.fp32 != 0, a.out, a.M, a.N, 0, a.out_stride, 0, features, 16);
+    if (st == EP_OK && p.pair && a.dgu)
+        st = encode_result(&a.md, "gradients of gate and up", false, a.dgu, a.M, a.N, 2, 2LL * a.M, a.M, features, 16);
     if (st != EP_OK)
         return st;
-    p.a.err = h->flags.err;
-    p.a.aligned = aligned(p.a.out, 8) && p.a.out_stride % 4 == 0;
-    p.a.chk = chk;
+    a.err = h->flags.err;
+    a.chk = chk;
     const cudaError_t ce = moe::launch_ffn(p, h->sms, s);
     return ce == cudaSuccess ? EP_OK : cuda_error(ce, "launch");
 }

@@ -41,7 +41,10 @@ static __host__ __device__ constexpr int threads(bool pair) { return 128 + store
 constexpr int kMaxStages = 12;
 constexpr int kBlockA = 16384;      // 128 features x 64 k
 constexpr int kHalfTmem = 256;      // columns of one accumulator
-constexpr int kExchange = 16 * 16 * 32 * 4;  // [warps][rows][features] floats
+// Shared memory through which a pair's results leave: of four warps, two boxes of 16 rows, one of fp32 or of three results;
+// joined, also the halves of gate and up that 8 pairs of warps exchange.
+static __host__ __device__ constexpr int box_bytes(int epi) { return epi == kFfnStore ? 8192 : epi == kFfnJoin ? 4096 : 12288; }
+static __host__ __device__ constexpr int out_bytes(int epi) { return 4 * box_bytes(epi) + (epi == kFfnJoin ? 8 * 2048 : 0); }
 constexpr int kBand = 8;            // row tiles of a band of tiles
 
 struct Shared {
@@ -83,7 +86,14 @@ static __device__ __forceinline__ uint2 pack4(float a, float b, float c, float d
     return make_uint2(*reinterpret_cast<const uint32_t *>(&lo), *reinterpret_cast<const uint32_t *>(&hi));
 }
 
-// What one thread does with the results of four features (col ..) of a row. Feature counts are multiples of 8: all four
+// Whether a store is inside a call's result (of the checked build; h, saved and dgu are workspace).
+template <int EPI> static __device__ __forceinline__ bool inside(const FfnArgs &a, const void *p, int bytes, int size)
+{
+    return EPI != kFfnStore ||
+           EP_IN_BOUNDS(a.chk, epk::kSiteMoeOut, p, bytes, a.out, size * ((a.N - 1LL) * a.out_stride + a.M));
+}
+
+// Of a split: what one thread does with the results of four features (col ..) of a row. Feature counts are multiples of 8: all four
 // are there, or none.
 // WEIGHT: of a weight's gradient, which may be fp32 and is aligned.
 template <int EPI, bool WEIGHT> struct Sink {
@@ -116,7 +126,7 @@ template <int EPI, bool WEIGHT> struct Sink {
         const long long at = t * a.out_stride + col;
         if (WEIGHT && a.fp32) {
             float4 *const p = reinterpret_cast<float4 *>(static_cast<float *>(a.out) + at);
-            if (inside(p, 16, 4)) {
+            if (inside<EPI>(a, p, 16, 4)) {
                 const float4 o = a.accumulate ? *p : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
                 *p = a.accumulate ? make_float4(o.x + v.x, o.y + v.y, o.z + v.z, o.w + v.w) : v;
             }
@@ -141,7 +151,7 @@ template <int EPI, bool WEIGHT> struct Sink {
             r = pack4(x.silu * k.u.x, y.silu * k.u.y, z.silu * k.u.z, w.silu * k.u.w);
         }
         __nv_bfloat16 *const p = static_cast<__nv_bfloat16 *>(a.out) + at;
-        if (!inside(p, 8, 2))
+        if (!inside<EPI>(a, p, 8, 2))
             return;
         if (EPI != kFfnStore || WEIGHT || a.aligned) {
             *reinterpret_cast<uint2 *>(p) = r;
@@ -151,11 +161,6 @@ template <int EPI, bool WEIGHT> struct Sink {
         }
     }
 
-    __device__ __forceinline__ bool inside(const void *p, int bytes, int size) const
-    {
-        return EPI != kFfnStore ||
-               EP_IN_BOUNDS(a.chk, epk::kSiteMoeOut, p, bytes, a.out, size * ((a.N - 1LL) * a.out_stride + a.M));
-    }
 };
 
 // Tiles in bands of kBand row tiles, feature tiles one after the other within a band: tiles that run at a time share
@@ -249,8 +254,10 @@ __global__ void __launch_bounds__(threads(PAIR), PAIR ? 1 : 2) ffn_kernel(const 
                 load_a(ring + ahead * bytes, smem_u32(&sh.full[ahead]), m, (c0 + ahead) * kChunk);
             }
         }
-        if (a.early != kFfnAll)
+        if (a.early != kFfnAll) {
             pdl_wait();
+            fence_async_proxy();  // what the kernel before stored from registers is read by copies
+        }
         pdl_launch_next();
         Cursor at;
         int issued = 0;
@@ -322,29 +329,39 @@ __global__ void __launch_bounds__(threads(PAIR), PAIR ? 1 : 2) ffn_kernel(const 
         mbar_wait(smem_u32(&sh.drain), 0, nullptr, kWaitOther);
     } else if (warp >= 4 && PAIR) {
         // ---- results, under the next tile's products ----
-        // 16 rows x 32 features of a warp at a time, through shared memory: then a lane has four features of a row. A
-        // quarter of the lanes (features) has four warps, which take its 16 rows in turn. Joined: a warp of quarters 0 and
-        // 1 has gate, the one two quarters on up of the same 32 features; each joins half of the 16 rows.
+        // A step is 16 rows. Four warps with the four quarters of the features take every fourth step, give each row's
+        // features their place in shared memory, and one of them sends it off as a box (out of bounds is cut off by the
+        // map). Joined: a warp of quarters 0 and 1 has gate, the one two quarters on up of the same 32 features; they
+        // exchange halves, and each joins 8 of the 16 rows.
         Cursor at_d;
         const int quarter = warp & 3, turn = (warp - 4) >> 2, steps = a.tile_n / 16;
-        const bool second = EPI == kFfnJoin && quarter >= 2;
-        constexpr int kRows = EPI == kFfnJoin ? 8 : 16;  // of a warp's 16
-        const int strip = EPI == kFfnJoin ? quarter & 1 : quarter, row0 = (second ? 8 : 0) + (lane >> 3);
-        float *const exchange = reinterpret_cast<float *>(dyn + (ring - dyn0) + a.stages * bytes);
-        float *const tile = exchange + (EPI == kFfnJoin ? (turn * 2 + strip) * 1024 : (turn * 4 + quarter) * 512);
-        float *const mine = tile + (second ? 512 : 0) + lane;
-        const float4 *const from = reinterpret_cast<const float4 *>(tile + row0 * 32 + (lane & 7) * 4);
+        const bool second = EPI == kFfnJoin && quarter >= 2, sender = quarter == 0 && elect_one();
+        const int f = (EPI == kFfnJoin ? quarter & 1 : quarter) * 32 + lane;  // of the block's features
+        constexpr int kRows = EPI == kFfnJoin ? 8 : 16;                       // of a warp
+        const int row0 = second ? 8 : 0;
+        uint8_t *const stage = dyn + (ring - dyn0) + a.stages * bytes + turn * box_bytes(EPI);
+        float *const exchange = reinterpret_cast<float *>(dyn + (ring - dyn0) + a.stages * bytes + 4 * box_bytes(EPI)) +
+                                (turn * 2 + (quarter & 1)) * 512 + lane;  // [gate, up][8][32]
+        constexpr bool kWeight = A_MN && B_MN;
+        const bool boxes = a.boxes != 0;
+        int sent = 0;
         for (int i = first; i < tiles; i += next) {
             int m, n;
             tile_of(a, i, m, n);
-            const To sink(a, (2 * m + rank) * kFeatures + strip * 32 + (lane & 7) * 4);
-            const int t0 = n * a.tile_n + row0;
-            typename To::Kept kept[kRows / 4];
-            auto fetch = [&](int step) {
-                if (EPI == kFfnSplit && step < steps)
+            const int m0 = (2 * m + rank) * kFeatures, col = m0 + f, t0 = n * a.tile_n;
+            float g[16], u[16];
+            auto fetch = [&](int step) {  // the kept g and u, ahead of their use
+                if (EPI == kFfnSplit && step < steps) {
+                    const float *s = a.saved + 2LL * (t0 + step * 16) * a.M + col;
 #pragma unroll
-                    for (int r = 0; r < kRows / 4; ++r)
-                        sink.fetch(t0 + step * 16 + 4 * r, kept[r]);
+                    for (int r = 0; r < 16; ++r, s += 2LL * a.M)
+                        if (col < a.M && t0 + step * 16 + r < a.N) {
+                            g[r] = s[0];
+                            u[r] = s[a.M];
+                        } else {
+                            g[r] = u[r] = 0.0f;
+                        }
+                }
             };
             fetch(turn);
             const bool run = mbar_wait(smem_u32(&sh.full_d[at_d.s]), at_d.parity, abort, kWaitFullD);
@@ -353,25 +370,85 @@ __global__ void __launch_bounds__(threads(PAIR), PAIR ? 1 : 2) ffn_kernel(const 
             tc_fence_after();
             const uint32_t d = tmem + (static_cast<uint32_t>(quarter) << 21) + at_d.s * kHalfTmem;
             for (int step = turn; step < steps; step += 4) {
+                const int t = t0 + step * 16;
                 float v[16];
                 tmem_ld16(d + step * 16, v);
                 tmem_wait_ld();
-                if (EPI == kFfnJoin)
-                    named_sync(2 + turn * 2 + strip, 64);  // the rows before are read
-                else
-                    __syncwarp();
+                if (EPI == kFfnJoin) {
 #pragma unroll
-                for (int r = 0; r < 16; ++r)
-                    mine[r * 32] = v[r];
-                if (EPI == kFfnJoin)
-                    named_sync(2 + turn * 2 + strip, 64);
-                else
-                    __syncwarp();
+                    for (int r = 0; r < 8; ++r)
+                        exchange[(second ? 256 : 0) + r * 32] = v[second ? r : r + 8];
+                    named_sync(6 + turn * 2 + (quarter & 1), 64);
 #pragma unroll
-                for (int r = 0; r < kRows / 4; ++r) {
-                    if (EPI == kFfnJoin)
-                        kept[r].u = from[128 + r * 32];
-                    sink.put(t0 + step * 16 + 4 * r, from[r * 32], kept[r]);
+                    for (int r = 0; r < 8; ++r) {
+                        const float other = exchange[(second ? 0 : 256) + r * 32];
+                        g[r] = second ? other : v[r];
+                        u[r] = second ? v[r + 8] : other;
+                    }
+                    if (a.saved && col < a.M) {
+                        float *s = a.saved + 2LL * (t + row0) * a.M + col;
+#pragma unroll
+                        for (int r = 0; r < 8; ++r, s += 2LL * a.M)
+                            if (t + row0 + r < a.N) {
+                                s[0] = g[r];
+                                s[a.M] = u[r];
+                            }
+                    }
+                }
+                if (boxes) {
+                    // two boxes of bf16 in turn, of fp32 or of three results one
+                    const bool one = EPI == kFfnSplit || (kWeight && a.fp32);
+                    uint8_t *const box = stage + (one || (sent & 1) == 0 ? 0 : kFeatures * 32);
+                    ++sent;
+                    if (sender) {
+                        if (one)
+                            bulk_wait_read<0>();
+                        else
+                            bulk_wait_read<1>();
+                    }
+                    named_sync(2 + turn, 128);
+                    if (kWeight && a.fp32) {
+                        float *const to = reinterpret_cast<float *>(box) + f;
+#pragma unroll
+                        for (int r = 0; r < 16; ++r)
+                            to[r * 128] = v[r];
+                    } else {
+                        __nv_bfloat16 *const to = reinterpret_cast<__nv_bfloat16 *>(box) + row0 * kFeatures + f;
+#pragma unroll
+                        for (int r = 0; r < kRows; ++r) {
+                            if (EPI == kFfnStore) {
+                                to[r * 128] = __float2bfloat16_rn(v[r]);
+                            } else if (EPI == kFfnJoin) {
+                                to[r * 64] = __float2bfloat16_rn(silu(g[r]) * u[r]);
+                            } else {
+                                const Gate gate(g[r]);
+                                to[r * 128] = __float2bfloat16_rn(gate.silu * u[r]);
+                                to[r * 128 + 2048] = __float2bfloat16_rn(v[r] * u[r] * gate.slope);
+                                to[r * 128 + 4096] = __float2bfloat16_rn(v[r] * gate.silu);
+                            }
+                        }
+                    }
+                    fence_async_shared();
+                    named_sync(2 + turn, 128);
+                    if (sender && m0 < a.M && t < a.N) {
+                        const uint32_t from = smem_u32(box);
+                        if (kWeight && a.accumulate)
+                            tma_add_2d(&a.mo, from, m0, t);
+                        else
+                            tma_store_2d(&a.mo, from, m0, t);
+                        if (EPI == kFfnSplit) {
+                            tma_store_3d(&a.md, from + 4096, m0, t, 0);
+                            tma_store_3d(&a.md, from + 8192, m0, t, 1);
+                        }
+                    }
+                    if (sender)
+                        bulk_commit();
+                } else {  // y or dx with rows that a map does not take (or checked): one by one
+                    __nv_bfloat16 *p = static_cast<__nv_bfloat16 *>(a.out) + (t + row0) * a.out_stride + col;
+#pragma unroll
+                    for (int r = 0; r < kRows; ++r, p += a.out_stride)
+                        if (col < a.M && t + row0 + r < a.N && inside<EPI>(a, p, 2, 2))
+                            *p = __float2bfloat16_rn(v[r]);
                 }
                 fetch(step + 4);
             }
@@ -381,6 +458,8 @@ __global__ void __launch_bounds__(threads(PAIR), PAIR ? 1 : 2) ffn_kernel(const 
                 mbar_arrive_cluster(in_first_block(smem_u32(&sh.empty_d[at_d.s])));
             at_d.next(2);
         }
+        if (sender)
+            bulk_wait<0>();
     }
     if (!PAIR) {
         // ---- a split's sums into this block's memory, then a share of the rows from all of the cluster's ----
@@ -567,7 +646,7 @@ void ffn_plan(FfnProduct *p, int sms)
     p->box_b = best_pair ? best_n / 2 : best_n;
     // Two blocks of a split on an SM where there are more blocks than SMs
     const bool share = !best_pair && best_n <= kShareRows && static_cast<long long>(a.m_tiles) * a.n_tiles * best_split > sms;
-    const int room = share ? kHalfRoom : kRoom - (best_pair ? kExchange : 0), stage = stage_bytes(*p);
+    const int room = share ? kHalfRoom : kRoom - (best_pair ? out_bytes(p->epilogue) : 0), stage = stage_bytes(*p);
     a.stages = (room - 1024) / stage < kMaxStages ? (room - 1024) / stage : kMaxStages;
 }
 
@@ -592,7 +671,7 @@ cudaError_t launch_ffn(const FfnProduct &p, int sms, cudaStream_t stream)
     const int pairs = sms / 2;
     cfg.gridDim = dim3(p.pair ? 2 * (tiles < pairs ? tiles : pairs) : tiles * a.split);
     cfg.blockDim = dim3(threads(p.pair));
-    cfg.dynamicSmemBytes = 1024 + ring + (p.pair ? kExchange : 0);
+    cfg.dynamicSmemBytes = 1024 + ring + (p.pair ? out_bytes(p.epilogue) : 0);
     cfg.stream = stream;
     cudaLaunchAttribute at[2];
     at[0].id = cudaLaunchAttributeClusterDimension;

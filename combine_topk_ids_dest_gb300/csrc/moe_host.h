@@ -117,6 +117,25 @@ inline ep_status encode_map(CUtensorMap *m, const char *what, int fp16, const vo
     return EP_OK;
 }
 
+// A row-major result [.., rows, cols] of bf16 or fp32 that is written through boxes of box_cols x box_rows.
+inline ep_status encode_result(CUtensorMap *m, const char *what, bool fp32, void *base, long long cols, long long rows,
+                               long long mats, long long row_stride, long long mat_stride, int box_cols, int box_rows)
+{
+    EncodeTiled fn = encode_tiled();
+    if (!fn)
+        return set_error(EP_ERR_CUDA, "cuTensorMapEncodeTiled is not available");
+    const int size = fp32 ? 4 : 2;
+    const cuuint64_t dims[3] = {cuuint64_t(cols), cuuint64_t(rows), cuuint64_t(mats > 0 ? mats : 1)};
+    const cuuint64_t strides[2] = {cuuint64_t(row_stride) * size, cuuint64_t(mat_stride) * size};
+    const cuuint32_t box[3] = {cuuint32_t(box_cols), cuuint32_t(box_rows), 1}, step[3] = {1, 1, 1};
+    const CUresult r = fn(m, fp32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, mats > 0 ? 3 : 2,
+                          base, dims, strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE,
+                          CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (r != CUDA_SUCCESS)
+        return set_error(EP_ERR_CUDA, "cuTensorMapEncodeTiled of %s: error %d", what, static_cast<int>(r));
+    return EP_OK;
+}
+
 // A 16-bit tensor [rows, 32 n] as [n][rows][32]: boxes of all its inner 32
 // columns, box_rows rows and box_steps steps of 32, zeros outside.
 inline ep_status encode_steps(CUtensorMap *m, const char *what, int fp16, const void *base, long long steps, long long rows,

@@ -226,6 +226,7 @@ enum FfnEarly { kFfnNone = 0, kFfnWeights, kFfnAll };
 // block by tile_n rows.
 struct FfnArgs {
     CUtensorMap ma, mb;  // boxes of 64 x 64; mb with K contiguous: 64 x the rows of a block's tile
+    CUtensorMap mo, md;  // out, boxes of a block's features x 16; dgu as [2][N, M] (split), likewise
     void *out;           // [N, M], rows out_stride apart: y, dx, the weights' gradients (N and M both features), h
     long long out_stride;
     float *saved;           // [N, 2 M]: g and u, written (joined) or read (split); NULL: not wanted
@@ -235,6 +236,7 @@ struct FfnArgs {
     int fp32, accumulate;  // of out
     int early;             // FfnEarly
     int aligned;           // out and its rows are 8-byte aligned
+    int boxes;             // out can be written through mo
     epk::CheckCtx chk;
 };
 
