@@ -1,6 +1,8 @@
 // moe_block_host.cu -- the C ABI of include/ep_moe.h, second part: the norm and
 // the feed-forward block, their argument checks, tensor maps and launches.
+#include <atomic>
 #include <cmath>
+#include <cstring>
 
 #include "moe_host.h"
 
@@ -63,6 +65,22 @@ ep_status check_norm(const ep_norm_config *c, int num_tokens)
     return EP_OK;
 }
 
+// The current device for the norm's calls, whose kernels have no handle: set up when a device is first seen.
+ep_status norm_device(int *sms)
+{
+    static std::atomic<unsigned long long> seen{0};
+    int dev = 0;
+    ep_status st = current_device(&dev, sms);
+    const unsigned long long bit = 1ULL << (dev & 63);
+    if (st != EP_OK || (dev < 64 && (seen.load(std::memory_order_acquire) & bit)))
+        return st;
+    const cudaError_t ce = moe::norm_setup();
+    if (ce != cudaSuccess)
+        return cuda_error(ce, "the norm's kernels");
+    seen.fetch_or(bit, std::memory_order_release);
+    return EP_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -77,9 +95,8 @@ ep_status ep_norm_run(const ep_norm_config *cfg, const ep_norm_rows *rows, int n
         return st;
     if (!rows)
         MOE_FAIL("rows is NULL");
-    int dev = 0;
     moe::NormArgs a = {};
-    st = current_device(&dev, &a.sms);
+    st = norm_device(&a.sms);
     if (st != EP_OK)
         return st;
     if (num_tokens == 0)
@@ -142,8 +159,8 @@ ep_status ep_norm_backward_workspace_size(const ep_norm_config *cfg, int num_tok
     ep_status st = check_norm(cfg, num_tokens);
     if (st != EP_OK)
         return st;
-    int dev = 0, sms = 0;
-    st = current_device(&dev, &sms);
+    int sms = 0;
+    st = norm_device(&sms);
     if (st != EP_OK)
         return st;
     *bytes = align256(size_t(moe::norm_back_blocks(num_tokens, sms)) * cfg->hidden * 4);
@@ -158,9 +175,8 @@ ep_status ep_norm_backward(const ep_norm_config *cfg, const void *dy, long long 
     ep_status st = check_norm(cfg, num_tokens);
     if (st != EP_OK)
         return st;
-    int dev = 0;
     moe::NormBackArgs a = {};
-    st = current_device(&dev, &a.sms);
+    st = norm_device(&a.sms);
     if (st != EP_OK)
         return st;
     const int H = cfg->hidden, size = size_of(cfg->dtype);
@@ -215,10 +231,17 @@ ep_status ep_norm_backward(const ep_norm_config *cfg, const void *dy, long long 
 
 // ---- feed-forward ------------------------------------------------------------------------
 
+enum Kind { kJoin = 0, kDown, kSplit, kGradients, kPlans = kGradients + 8 };  // kGradients + which are asked for
+
 struct ep_ffn {
     ep_ffn_config cfg;
     int device, sms;
     Flags flags;
+    int *parts;  // device: which parts of shared tiles are written, 0 between launches
+    struct {
+        int T;
+        moe::FfnLaunch l;
+    } plan[kPlans];  // of the last call of each kind
 };
 
 namespace {
@@ -247,17 +270,6 @@ ep_status check_ffn_tokens(const ep_ffn *h, int num_tokens)
     return EP_OK;
 }
 
-// The intermediate rows; for the backward pass the gradients of gate and up too.
-struct FfnLayout {
-    size_t off_dgu, total;
-    FfnLayout(const ep_ffn_config &c, ep_ffn_call call, int num_tokens)
-    {
-        const size_t row = size_t(c.intermediate) * 2;
-        off_dgu = align256(num_tokens * row);
-        total = off_dgu + (call == EP_FFN_BACKWARD ? align256(num_tokens * 2 * row) : 0);
-    }
-};
-
 // A matrix operand as it lies in memory: `rows` rows of `cols` bf16, `stride` apart.
 struct Matrix {
     const char *name;
@@ -265,27 +277,175 @@ struct Matrix {
     long long rows, cols, stride;
 };
 
-// Plans and queues D[M, N] = A B^T. An operand is either [M or N, K], or [K, M or N] (mn).
-ep_status product(const ep_ffn *h, moe::FfnProduct &p, const Matrix &ma, const Matrix &mb, epk::CheckCtx chk, cudaStream_t s)
+// One launch: up to three products D[M, N] = A B^T, each operand either [M or N, K], or [K, M or N] (mn).
+struct Launch {
+    moe::FfnLaunch l = {};
+    int kind;
+    Matrix a[3], b[3];
+
+    Launch(int epilogue, int kind_) : kind(kind_) { l.epilogue = epilogue; }
+    moe::FfnArgs &add(int M, int N, int K, bool a_mn, bool b_mn, const Matrix &ma, const Matrix &mb)
+    {
+        const int g = l.q.count++;
+        a[g] = ma;
+        b[g] = mb;
+        moe::FfnArgs &p = l.q.p[g];
+        p.M = M;
+        p.N = N;
+        p.K = K;
+        p.a_mn = a_mn;
+        p.b_mn = b_mn;
+        return p;
+    }
+};
+
+// The products of a call; pointers that a plan does not need may be missing.
+Launch join_of(const ep_ffn_config &c, int T, const void *x, long long x_stride, void *h, float *saved)
 {
-    moe::ffn_plan(&p, h->sms);
-    ep_status st = encode_map(&p.a.ma, ma.name, 0, ma.p, ma.cols, ma.rows, 0, ma.stride, 0, moe::kChunk, 64);
-    if (st == EP_OK)
-        st = encode_map(&p.a.mb, mb.name, 0, mb.p, mb.cols, mb.rows, 0, mb.stride, 0, moe::kChunk, p.b_mn ? 64 : p.box_b);
-    moe::FfnArgs &a = p.a;
-    const int size = a.fp32 ? 4 : 2, features = p.epilogue == moe::kFfnJoin ? 64 : 128;
-    a.aligned = aligned(a.out, 8) && a.out_stride % 4 == 0;
-    // The checked build tests the stores of y and dx one by one; all others are bounded by their maps.
-    a.boxes = aligned(a.out, 16) && a.out_stride * size % 16 == 0 && !(EP_CHECKED && p.epilogue == moe::kFfnStore && !p.b_mn);
-    if (st == EP_OK && p.pair && a.boxes)
-        st = encode_result(&a.mo, "result", a.fp32 != 0, a.out, a.M, a.N, 0, a.out_stride, 0, features, 16);
-    if (st == EP_OK && p.pair && a.dgu)
-        st = encode_result(&a.md, "gradients of gate and up", false, a.dgu, a.M, a.N, 2, 2LL * a.M, a.M, features, 16);
-    if (st != EP_OK)
-        return st;
-    a.err = h->flags.err;
-    a.chk = chk;
-    const cudaError_t ce = moe::launch_ffn(p, h->sms, s);
+    const int H = c.hidden, I = c.intermediate;
+    Launch l(moe::kFfnJoin, kJoin);
+    moe::FfnArgs &p = l.add(I, T, H, false, false, {"gate_up", c.gate_up, 2 * I, H, H}, {"x", x, T, H, x_stride});
+    p.out = h;
+    p.out_stride = I;
+    p.saved = saved;
+    return l;
+}
+
+Launch down_of(const ep_ffn_config &c, int T, const void *h, void *out, long long out_stride)
+{
+    const int H = c.hidden, I = c.intermediate;
+    Launch l(moe::kFfnStore, kDown);
+    moe::FfnArgs &p = l.add(H, T, I, false, false, {"down", c.down, H, I, I}, {"h", h, T, I, I});
+    p.early = 1;
+    p.out = out;
+    p.out_stride = out_stride;
+    return l;
+}
+
+Launch split_of(const ep_ffn_config &c, int T, const ep_ffn_grads &g, void *h, __nv_bfloat16 *dgu)
+{
+    const int H = c.hidden, I = c.intermediate;
+    Launch l(moe::kFfnSplit, kSplit);
+    moe::FfnArgs &p = l.add(I, T, H, true, false, {"down", c.down, H, I, I}, {"dy", g.dy, T, H, g.dy_stride});
+    p.out = h;
+    p.out_stride = I;
+    p.saved = const_cast<float *>(g.saved);
+    p.dgu = dgu;
+    return l;
+}
+
+// dx and the weights' gradients, as far as they are asked for.
+Launch gradients_of(const ep_ffn_config &c, int T, const ep_ffn_grads &g, const void *h, const __nv_bfloat16 *dgu)
+{
+    const int H = c.hidden, I = c.intermediate;
+    const Matrix rows = {"gradients of gate and up", dgu, T, 2 * I, 2 * I}, x = {"x", g.x, T, H, g.x_stride};
+    Launch l(moe::kFfnStore, kGradients + (g.dx ? 1 : 0) + (g.dgate_up ? 2 : 0) + (g.ddown ? 4 : 0));
+    if (g.dx) {
+        moe::FfnArgs &p = l.add(H, T, 2 * I, true, false, {"gate_up", c.gate_up, 2 * I, H, H}, rows);
+        p.early = 1;
+        p.out = g.dx;
+        p.out_stride = g.dx_stride;
+    }
+    if (g.dgate_up) {
+        moe::FfnArgs &p = l.add(H, 2 * I, T, true, true, x, rows);
+        p.early = 1;
+        p.out = g.dgate_up;
+        p.out_stride = H;
+    }
+    if (g.ddown) {
+        moe::FfnArgs &p = l.add(I, H, T, true, true, {"h", h, T, I, I}, {"dy", g.dy, T, H, g.dy_stride});
+        p.out = g.ddown;
+        p.out_stride = I;
+    }
+    for (int i = 0; i < l.l.q.count; ++i)
+        if (l.l.q.p[i].b_mn) {
+            l.l.q.p[i].fp32 = g.grad_dtype == EP_DTYPE_FP32;
+            l.l.q.p[i].accumulate = g.accumulate != 0;
+        }
+    return l;
+}
+
+// The plan follows from the sizes alone: the last one of each kind is kept.
+void plan(ep_ffn *h, int num_tokens, Launch &w)
+{
+    auto &kept = h->plan[w.kind];
+    if (kept.T != num_tokens) {
+        moe::ffn_plan(&w.l, h->sms);
+        kept.l = w.l;
+        kept.T = num_tokens;
+        return;
+    }
+    moe::FfnGroup &q = w.l.q;
+    const moe::FfnGroup &k = kept.l.q;
+    for (int g = 0; g < q.count; ++g) {
+        moe::FfnArgs &a = q.p[g];
+        const moe::FfnArgs &b = k.p[g];
+        a.tile_n = b.tile_n;
+        a.m_tiles = b.m_tiles;
+        a.n_tiles = b.n_tiles;
+        a.chunks = b.chunks;
+        a.box_b = b.box_b;
+        a.whole = b.whole;
+    }
+    q.pairs = k.pairs;
+    q.stages = k.stages;
+    q.bytes = k.bytes;
+    q.whole = k.whole;
+    q.cut = k.cut;
+    memcpy(q.begin, k.begin, sizeof(q.begin));
+    w.l.split = kept.l.split;
+    w.l.parts = kept.l.parts;
+}
+
+// The intermediate rows, for the backward pass the gradients of gate and up too, and the parts of shared tiles.
+struct FfnLayout {
+    size_t off_dgu, off_parts, total;
+    FfnLayout(ep_ffn *h, ep_ffn_call call, int num_tokens)
+    {
+        const size_t row = size_t(h->cfg.intermediate) * 2;
+        off_dgu = align256(num_tokens * row);
+        off_parts = off_dgu + (call == EP_FFN_BACKWARD ? align256(num_tokens * 2 * row) : 0);
+        total = off_parts;
+        if (num_tokens == 0)
+            return;
+        size_t parts = size_t(2 * moe::kFfnMaxPairs) * 256 * 128 * sizeof(float);  // whichever gradients are asked for
+        if (call != EP_FFN_BACKWARD) {
+            Launch first = join_of(h->cfg, num_tokens, nullptr, 0, nullptr, nullptr), second = down_of(h->cfg, num_tokens, nullptr, nullptr, 0);
+            plan(h, num_tokens, first);
+            plan(h, num_tokens, second);
+            parts = first.l.parts > second.l.parts ? first.l.parts : second.l.parts;
+        }
+        total += align256(parts);
+    }
+};
+
+ep_status launch(ep_ffn *h, int num_tokens, Launch &w, void *parts, epk::CheckCtx chk, cudaStream_t s)
+{
+    moe::FfnGroup &q = w.l.q;
+    plan(h, num_tokens, w);
+    q.parts = static_cast<float *>(parts);
+    q.flags = h->parts;
+    q.err = h->flags.err;
+    const int features = w.l.epilogue == moe::kFfnJoin ? 64 : 128;
+    for (int g = 0; g < q.count; ++g) {
+        moe::FfnArgs &a = q.p[g];
+        const Matrix &ma = w.a[g], &mb = w.b[g];
+        ep_status st = encode_map(&a.ma, ma.name, 0, ma.p, ma.cols, ma.rows, 0, ma.stride, 0, moe::kChunk, 64);
+        if (st == EP_OK)
+            st = encode_map(&a.mb, mb.name, 0, mb.p, mb.cols, mb.rows, 0, mb.stride, 0, moe::kChunk, a.b_mn ? 64 : a.box_b);
+        const int size = a.fp32 ? 4 : 2;
+        a.aligned = aligned(a.out, 8) && a.out_stride % 4 == 0;
+        // The checked build tests the stores of y and dx one by one; all others are bounded by their maps.
+        a.boxes = aligned(a.out, 16) && a.out_stride * size % 16 == 0 && !(EP_CHECKED && w.l.epilogue == moe::kFfnStore && !a.b_mn);
+        if (st == EP_OK && !w.l.split && a.boxes)
+            st = encode_result(&a.mo, "result", a.fp32 != 0, a.out, a.M, a.N, 0, a.out_stride, 0, features, 16);
+        if (st == EP_OK && !w.l.split && a.dgu)
+            st = encode_result(&a.md, "gradients of gate and up", false, a.dgu, a.M, a.N, 2, 2LL * a.M, a.M, features, 16);
+        if (st != EP_OK)
+            return st;
+        a.chk = chk;
+    }
+    const cudaError_t ce = moe::launch_ffn(w.l, s);
     return ce == cudaSuccess ? EP_OK : cuda_error(ce, "launch");
 }
 
@@ -313,11 +473,20 @@ ep_status ep_ffn_create(const ep_ffn_config *cfg, ep_ffn **out)
     h->sms = sms;
     st = h->flags.make();
     if (st == EP_OK) {
-        const cudaError_t ce = moe::ffn_setup();
+        const size_t bytes = (2 * moe::kFfnMaxPairs + 1) * sizeof(int);
+        cudaError_t ce = moe::ffn_setup();
+        if (ce == cudaSuccess)
+            ce = cudaMalloc(reinterpret_cast<void **>(&h->parts), bytes);
+        if (ce == cudaSuccess)
+            ce = cudaMemset(h->parts, 0, bytes);
+        if (ce == cudaSuccess)
+            ce = cudaStreamSynchronize(nullptr);
         if (ce != cudaSuccess)
-            st = cuda_error(ce, "the handle's kernels");
+            st = cuda_error(ce, "the handle's kernels and flags");
     }
     if (st != EP_OK) {
+        if (h->parts)
+            cudaFree(h->parts);
         h->flags.free();
         delete h;
         return st;
@@ -326,7 +495,7 @@ ep_status ep_ffn_create(const ep_ffn_config *cfg, ep_ffn **out)
     return set_error(EP_OK, "");
 }
 
-ep_status ep_ffn_workspace_size(const ep_ffn *h, ep_ffn_call call, int num_tokens, size_t *bytes)
+ep_status ep_ffn_workspace_size(ep_ffn *h, ep_ffn_call call, int num_tokens, size_t *bytes)
 {
     const ep_status st = check_ffn_tokens(h, num_tokens);
     if (st != EP_OK)
@@ -335,7 +504,7 @@ ep_status ep_ffn_workspace_size(const ep_ffn *h, ep_ffn_call call, int num_token
         MOE_FAIL("bytes is NULL");
     if (call != EP_FFN_RUN && call != EP_FFN_FORWARD && call != EP_FFN_BACKWARD)
         MOE_FAIL("unknown call %d", static_cast<int>(call));
-    *bytes = FfnLayout(h->cfg, call, num_tokens).total;
+    *bytes = FfnLayout(h, call, num_tokens).total;
     return set_error(EP_OK, "");
 }
 
@@ -360,7 +529,7 @@ ep_status ep_ffn_run(ep_ffn *h, const void *x, long long x_stride, int num_token
         MOE_FAIL("saved is not 16-byte aligned");
     const Span in = {"x", x, extent(T, x_stride, H, 2), x_stride}, y = {"out", out, extent(T, out_stride, H, 2), out_stride},
                keep = {"saved", saved, extent(T, 2 * I, 2 * I, 4), 2 * I};
-    const FfnLayout l(h->cfg, saved ? EP_FFN_FORWARD : EP_FFN_RUN, T);
+    const FfnLayout l(h, saved ? EP_FFN_FORWARD : EP_FFN_RUN, T);
     st = check_overlap(y, in, false);
     if (st == EP_OK)
         st = check_overlap(keep, in, false);
@@ -375,27 +544,11 @@ ep_status ep_ffn_run(ep_ffn *h, const void *x, long long x_stride, int num_token
     unsigned long long *rec = epk::check_record();
     const epk::CheckCtx chk = epk::check_ctx(rec);
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
-    const Matrix mx = {"x", x, T, H, x_stride}, mh = {"h", workspace, T, I, I}, w1 = {"gate_up", h->cfg.gate_up, 2 * I, H, H},
-                 w2 = {"down", h->cfg.down, H, I, I};
-    moe::FfnProduct join = {};
-    join.epilogue = moe::kFfnJoin;
-    join.a.M = I;
-    join.a.N = T;
-    join.a.K = H;
-    join.a.out = workspace;
-    join.a.out_stride = I;
-    join.a.saved = saved;
-    st = product(h, join, w1, mx, chk, s);
-    if (st != EP_OK)
-        return st;
-    moe::FfnProduct p = {};
-    p.a.M = H;
-    p.a.N = T;
-    p.a.K = I;
-    p.a.early = moe::kFfnWeights;
-    p.a.out = out;
-    p.a.out_stride = out_stride;
-    st = product(h, p, w2, mh, chk, s);
+    void *const parts = static_cast<uint8_t *>(workspace) + l.off_parts;
+    Launch first = join_of(h->cfg, T, x, x_stride, workspace, saved), second = down_of(h->cfg, T, workspace, out, out_stride);
+    st = launch(h, T, first, parts, chk, s);
+    if (st == EP_OK)
+        st = launch(h, T, second, parts, chk, s);
     return st == EP_OK ? finish(cudaSuccess, "ep_ffn_run", rec, s) : st;
 }
 
@@ -450,7 +603,7 @@ ep_status ep_ffn_backward(ep_ffn *h, const ep_ffn_grads *grads, int num_tokens, 
         for (int i = 0; i < o && st == EP_OK; ++i)
             st = check_overlap(out[o], out[i], false);
     }
-    const FfnLayout l(h->cfg, EP_FFN_BACKWARD, T);
+    const FfnLayout l(h, EP_FFN_BACKWARD, T);
     if (st == EP_OK)
         st = check_workspace(workspace, workspace_bytes, l.total);
     if (st == EP_OK)
@@ -462,62 +615,11 @@ ep_status ep_ffn_backward(ep_ffn *h, const ep_ffn_grads *grads, int num_tokens, 
     unsigned long long *rec = epk::check_record();
     const epk::CheckCtx chk = epk::check_ctx(rec);
     __nv_bfloat16 *const dgu = reinterpret_cast<__nv_bfloat16 *>(static_cast<uint8_t *>(workspace) + l.off_dgu);
-    const Matrix mx = {"x", g.x, T, H, g.x_stride}, mdy = {"dy", g.dy, T, H, g.dy_stride}, mh = {"h", workspace, T, I, I},
-                 mdgu = {"dgate_up rows", dgu, T, 2 * I, 2 * I}, w1 = {"gate_up", h->cfg.gate_up, 2 * I, H, H},
-                 w2 = {"down", h->cfg.down, H, I, I};
-    {
-        moe::FfnProduct p = {};
-        p.epilogue = moe::kFfnSplit;
-        p.a_mn = true;
-        p.a.M = I;
-        p.a.N = T;
-        p.a.K = H;
-        p.a.out = workspace;
-        p.a.out_stride = I;
-        p.a.saved = const_cast<float *>(g.saved);
-        p.a.dgu = dgu;
-        st = product(h, p, w2, mdy, chk, s);
-    }
-    int early = moe::kFfnWeights;
-    if (st == EP_OK && g.dx) {
-        moe::FfnProduct p = {};
-        p.a_mn = true;
-        p.a.early = early;
-        early = moe::kFfnAll;  // for what comes next
-        p.a.M = H;
-        p.a.N = T;
-        p.a.K = 2 * I;
-        p.a.out = g.dx;
-        p.a.out_stride = g.dx_stride;
-        st = product(h, p, w1, mdgu, chk, s);
-    }
-    if (st == EP_OK && g.dgate_up) {
-        moe::FfnProduct p = {};
-        p.a_mn = p.b_mn = true;
-        p.a.early = early;
-        early = moe::kFfnAll;
-        p.a.M = H;
-        p.a.N = 2 * I;
-        p.a.K = T;
-        p.a.out = g.dgate_up;
-        p.a.out_stride = H;
-        p.a.fp32 = size == 4;
-        p.a.accumulate = g.accumulate != 0;
-        st = product(h, p, mx, mdgu, chk, s);
-    }
-    if (st == EP_OK && g.ddown) {
-        moe::FfnProduct p = {};
-        p.a_mn = p.b_mn = true;
-        p.a.early = early == moe::kFfnAll ? moe::kFfnAll : moe::kFfnNone;  // h is the last kernel's
-        p.a.M = I;
-        p.a.N = H;
-        p.a.K = T;
-        p.a.out = g.ddown;
-        p.a.out_stride = I;
-        p.a.fp32 = size == 4;
-        p.a.accumulate = g.accumulate != 0;
-        st = product(h, p, mh, mdy, chk, s);
-    }
+    void *const parts = static_cast<uint8_t *>(workspace) + l.off_parts;
+    Launch first = split_of(h->cfg, T, g, workspace, dgu), rest = gradients_of(h->cfg, T, g, workspace, dgu);
+    st = launch(h, T, first, parts, chk, s);
+    if (st == EP_OK)
+        st = launch(h, T, rest, parts, chk, s);
     return st == EP_OK ? finish(cudaSuccess, "ep_ffn_backward", rec, s) : st;
 }
 
@@ -525,6 +627,7 @@ ep_status ep_ffn_destroy(ep_ffn *h)
 {
     if (h) {
         wait_for_device(h->device);
+        cudaFree(h->parts);
         h->flags.free();
         delete h;
     }

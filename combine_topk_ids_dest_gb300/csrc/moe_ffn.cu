@@ -17,42 +17,50 @@
 // and up joined (a block's 128 MMA rows are 64 of gate and the same 64 of up),
 // or the gradient of h split into those of gate and up.
 //
-// Two shapes of one kernel:
+// Two kernels:
 //  - pairs: two neighbouring blocks multiply together (cta_group::2), 256
 //    features x up to 256 rows a tile, persistent, accumulators in two halves of
-//    tensor memory, so that one tile's epilogue runs under the next one's MMAs;
+//    tensor memory, so that one tile's epilogue runs under the next one's MMAs.
+//    A launch has up to three products (the three that follow the split). Whole
+//    tiles go round the pairs; the last one or two rounds are cut evenly along K
+//    over all of them, so that no round is left half empty. A tile that pairs
+//    share: all but the last one's sums go through memory, written first of all
+//    a pair does, and the last pair, which ends with it, adds them in the order of
+//    K. Waits go to lower pairs only;
 //  - splits: for few tiles. A block has 128 features, a cluster of 1 to 8 blocks
 //    shares a tile's K. Their sums meet in distributed shared memory, added in
 //    the order of K, a share of the rows in each block.
+// No sum depends on timing.
 #include <cmath>
 
 #include <cuda_bf16.h>
 
+#include "moe_ffn.h"
 #include "moe_sched.h"
 
 namespace moe {
 
 namespace {
 
-// Threads that store results: of a pair's block 16 warps, which have the next tile's MMAs to hide under; of a split's 8.
-static __host__ __device__ constexpr int storers(bool pair) { return pair ? 512 : 256; }
-// Warp 0 copies, warp 1 multiplies, warps from the fourth on store.
-static __host__ __device__ constexpr int threads(bool pair) { return 128 + storers(pair); }
 constexpr int kMaxStages = 12;
 constexpr int kBlockA = 16384;      // 128 features x 64 k
 constexpr int kHalfTmem = 256;      // columns of one accumulator
+constexpr int kPairStore = 512;     // threads that store a pair's results: 16 warps, under the next tile's MMAs
+constexpr int kSplitStore = 256;
+constexpr int kFirstStore = 4;      // warp 0 copies, warp 1 multiplies, warps from this one on store
+
 // Shared memory through which a pair's results leave: of four warps, two boxes of 16 rows, one of fp32 or of three results;
 // joined, also the halves of gate and up that 8 pairs of warps exchange.
 static __host__ __device__ constexpr int box_bytes(int epi) { return epi == kFfnStore ? 8192 : epi == kFfnJoin ? 4096 : 12288; }
 static __host__ __device__ constexpr int out_bytes(int epi) { return 4 * box_bytes(epi) + (epi == kFfnJoin ? 8 * 2048 : 0); }
-constexpr int kBand = 8;            // row tiles of a band of tiles
+static __host__ __device__ constexpr int features_of(int epi) { return epi == kFfnJoin ? 64 : 128; }  // of a block
 
 struct Shared {
     uint64_t full[kMaxStages], empty[kMaxStages];
     uint64_t full_d[2], empty_d[2];
     uint64_t drain;
     uint32_t tmem;
-    int abort, issued;
+    int abort, issued, reset;
 };
 
 // Tensor memory is given out in powers of two from 32 columns on.
@@ -95,8 +103,7 @@ template <int EPI> static __device__ __forceinline__ bool inside(const FfnArgs &
 
 // Of a split: what one thread does with the results of four features (col ..) of a row. Feature counts are multiples of 8: all four
 // are there, or none.
-// WEIGHT: of a weight's gradient, which may be fp32 and is aligned.
-template <int EPI, bool WEIGHT> struct Sink {
+template <int EPI> struct Sink {
     const FfnArgs &a;
     const int col;
 
@@ -124,14 +131,6 @@ template <int EPI, bool WEIGHT> struct Sink {
         if (!live(t))
             return;
         const long long at = t * a.out_stride + col;
-        if (WEIGHT && a.fp32) {
-            float4 *const p = reinterpret_cast<float4 *>(static_cast<float *>(a.out) + at);
-            if (inside<EPI>(a, p, 16, 4)) {
-                const float4 o = a.accumulate ? *p : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-                *p = a.accumulate ? make_float4(o.x + v.x, o.y + v.y, o.z + v.z, o.w + v.w) : v;
-            }
-            return;
-        }
         uint2 r;
         if (EPI == kFfnStore) {
             r = pack4(v.x, v.y, v.z, v.w);
@@ -153,201 +152,225 @@ template <int EPI, bool WEIGHT> struct Sink {
         __nv_bfloat16 *const p = static_cast<__nv_bfloat16 *>(a.out) + at;
         if (!inside<EPI>(a, p, 8, 2))
             return;
-        if (EPI != kFfnStore || WEIGHT || a.aligned) {
+        if (EPI != kFfnStore || a.aligned) {
             *reinterpret_cast<uint2 *>(p) = r;
         } else {
             uint16_t *const e = reinterpret_cast<uint16_t *>(p);
             e[0] = r.x & 0xFFFF, e[1] = r.x >> 16, e[2] = r.y & 0xFFFF, e[3] = r.y >> 16;
         }
     }
-
 };
 
-// Tiles in bands of kBand row tiles, feature tiles one after the other within a band: tiles that run at a time share
-// operands in L2.
-static __device__ __forceinline__ void tile_of(const FfnArgs &a, int i, int &m, int &n)
+// What both kernels do before their work, and after it.
+static __device__ __forceinline__ void set_barriers(Shared &sh, int storers)
 {
-    const int band = i / (kBand * a.m_tiles), first = band * kBand, wide = min(kBand, a.n_tiles - first);
-    const int in = i - first * a.m_tiles;
-    m = in / wide;
-    n = first + in - m * wide;
+    sh.abort = sh.issued = sh.reset = 0;
+    for (int i = 0; i < kMaxStages; ++i) {
+        mbar_init(smem_u32(&sh.full[i]), 1);
+        mbar_init(smem_u32(&sh.empty[i]), 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+        mbar_init(smem_u32(&sh.full_d[i]), 1);
+        mbar_init(smem_u32(&sh.empty_d[i]), storers);
+    }
+    mbar_init(smem_u32(&sh.drain), 1);
+    mbar_init_fence();
 }
 
-template <int EPI, bool A_MN, bool B_MN, bool PAIR>
-__global__ void __launch_bounds__(threads(PAIR), PAIR ? 1 : 2) ffn_kernel(const __grid_constant__ FfnArgs a)
+static __device__ __forceinline__ void report(const Shared &sh, unsigned int *err)
+{
+    atomicAdd_system(err + sh.abort, 1u);
+    __threadfence_system();
+    atomicAdd_system(err, 1u);
+}
+
+// Bytes of B in a stage: rows (k contiguous), or blocks of 64 rows.
+static __host__ __device__ __forceinline__ int bytes_b(int rows, bool mn) { return mn ? (rows + 63) / 64 * 8192 : rows * 128; }
+
+// The kernels' operands: A is MN-major in what follows the forward pass (GRAD), B in the weights' gradients only.
+template <int EPI, bool GRAD> constexpr bool kAmn = EPI == kFfnSplit || GRAD;
+
+// One chunk of 64 k: four instructions of 16, which are 32 bytes of a row apart, or 16 rows of 128 bytes.
+template <bool A_MN, bool B_MN, bool PAIR>
+static __device__ __forceinline__ void multiply(uint32_t d, uint32_t from, int tile_n, bool add)
+{
+    const uint32_t idesc =
+        idesc_f16(PAIR ? 256 : 128, tile_n, 1) | (A_MN ? kIdescAmn : 0u) | (B_MN ? kIdescBmn : 0u);
+    const uint64_t da = A_MN ? desc_mn(from) : desc_sw128(from);
+    const uint64_t db = B_MN ? desc_mn(from + kBlockA) : desc_sw128(from + kBlockA);
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {  // in 16-byte units
+        const uint64_t qa = da + q * (A_MN ? 128 : 2), qb = db + q * (B_MN ? 128 : 2);
+        if (PAIR)
+            mma_ss_pair(d, qa, qb, idesc, add || q > 0);
+        else
+            mma_ss(d, qa, qb, idesc, add || q > 0);
+    }
+}
+
+template <bool PAIR>
+static __device__ __forceinline__ void load_box(uint32_t dst, const CUtensorMap *map, uint32_t full, int x, int y)
+{
+    if (PAIR)
+        tma_load_2d_pair(dst, map, in_first_block(full), x, y);
+    else
+        tma_load_2d(dst, map, full, x, y);
+}
+
+// 128 features from m0 on (joined: 64 of gate, and of up), and `rows` rows from n0 on, of 64 k.
+template <int EPI, bool A_MN, bool PAIR>
+static __device__ __forceinline__ void load_a(const FfnArgs &a, uint32_t dst, uint32_t full, int m0, int k)
+{
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+        const int f = EPI == kFfnJoin ? m0 + j * a.M : m0 + j * 64;
+        load_box<PAIR>(dst + j * 8192, &a.ma, full, A_MN ? f : k, A_MN ? k : f);
+    }
+}
+template <bool PAIR>
+static __device__ __forceinline__ void load_b(const FfnArgs &a, bool mn, uint32_t dst, uint32_t full, int n0, int rows, int k)
+{
+    if (mn) {
+        for (int j = 0; j < rows; j += 64)
+            load_box<PAIR>(dst + kBlockA + j * 128, &a.mb, full, n0 + j, k);
+    } else {
+        load_box<PAIR>(dst + kBlockA, &a.mb, full, k, n0);
+    }
+}
+
+// ---- pairs -------------------------------------------------------------------------------
+
+// GRAD: dx and the weights' gradients, up to three products; else one product.
+template <int EPI, bool GRAD> __global__ void __launch_bounds__(128 + kPairStore, 1) pair_kernel(const __grid_constant__ FfnGroup q)
 {
     extern __shared__ uint8_t dyn[];
     __shared__ Shared sh;
     const uint32_t dyn0 = smem_u32(dyn), ring = (dyn0 + 1023u) & ~1023u;
     const int tid = threadIdx.x, warp = __shfl_sync(~0u, tid >> 5, 0), lane = tid & 31;
-    const int group = PAIR ? 2 : a.split;  // blocks of a cluster
-    const int rank = blockIdx.x % group, first = blockIdx.x / group, next = gridDim.x / group;
-    const int tiles = a.m_tiles * a.n_tiles, chunks = (a.K + kChunk - 1) / kChunk;
-    const int c0 = PAIR ? 0 : static_cast<int>(static_cast<long long>(chunks) * rank / a.split);
-    const int c1 = PAIR ? chunks : static_cast<int>(static_cast<long long>(chunks) * (rank + 1) / a.split);
-    const int rows_b = PAIR ? a.tile_n / 2 : a.tile_n, blocks_b = (rows_b + 63) / 64;
-    const int bytes = kBlockA + (B_MN ? blocks_b * 8192 : rows_b * 128);
-    constexpr int kFeatures = EPI == kFfnJoin ? 64 : 128;  // of a block
-    constexpr int kEpilogue = storers(PAIR);
-    using To = Sink<EPI, A_MN && B_MN>;
+    const int rank = blockIdx.x & 1, pair = blockIdx.x >> 1;
+    constexpr int kFeatures = features_of(EPI);
+    constexpr bool A_MN = kAmn<EPI, GRAD>;
     volatile int *const abort = &sh.abort;
 
-    if (tid == 0) {
-        sh.abort = sh.issued = 0;
-        for (int i = 0; i < kMaxStages; ++i) {
-            mbar_init(smem_u32(&sh.full[i]), 1);
-            mbar_init(smem_u32(&sh.empty[i]), 1);
-        }
-        for (int i = 0; i < 2; ++i) {
-            mbar_init(smem_u32(&sh.full_d[i]), 1);
-            mbar_init(smem_u32(&sh.empty_d[i]), (PAIR ? 2 : 1) * kEpilogue / 32);
-        }
-        mbar_init(smem_u32(&sh.drain), 1);
-        mbar_init_fence();
-        tma_prefetch_map(&a.ma);
-        tma_prefetch_map(&a.mb);
+    if (tid == 0)
+        set_barriers(sh, 2 * kPairStore / 32);
+    else if (tid >= 64 && tid < 64 + q.count) {
+        tma_prefetch_map(&q.p[tid - 64].ma);
+        tma_prefetch_map(&q.p[tid - 64].mb);
     }
-    const uint32_t columns = PAIR ? 2 * kHalfTmem : tmem_columns(a.tile_n);
     if (warp == 1)
-        tmem_alloc<PAIR>(smem_u32(&sh.tmem), columns);
+        tmem_alloc<true>(smem_u32(&sh.tmem), 2 * kHalfTmem);
     tc_fence_before();
     __syncthreads();
-    if (PAIR)
-        cluster_sync();  // no copy or arrival reaches a block before its barriers are set
+    cluster_sync();  // no copy or arrival reaches a block before its barriers are set
     tc_fence_after();
     const uint32_t tmem = sh.tmem;
 
     if (warp == 0 && elect_one()) {
         // ---- copies ----
-        auto load = [&](uint32_t dst, const CUtensorMap *map, uint32_t full, int x, int y) {
-            if (PAIR)
-                tma_load_2d_pair(dst, map, in_first_block(full), x, y);
-            else
-                tma_load_2d(dst, map, full, x, y);
+        auto expect = [&](uint32_t full, int bytes) {
+            if (rank == 0)
+                mbar_expect(full, 2 * bytes);
         };
-        auto expect = [&](uint32_t full) {
-            if (!PAIR || rank == 0)
-                mbar_expect(full, PAIR ? 2 * bytes : bytes);
-        };
-        auto load_a = [&](uint32_t dst, uint32_t full, int m, int k) {
-            const int m0 = (PAIR ? 2 * m + rank : m) * kFeatures;
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                const int f = EPI == kFfnJoin ? m0 + j * a.M : m0 + j * 64;
-                load(dst + j * 8192, &a.ma, full, A_MN ? f : k, A_MN ? k : f);
-            }
-        };
-        auto load_b = [&](uint32_t dst, uint32_t full, int n, int k) {
-            const int n0 = n * a.tile_n + (PAIR ? rank * rows_b : 0);
-            if (B_MN) {
-                for (int j = 0; j < blocks_b; ++j)
-                    load(dst + kBlockA + j * 8192, &a.mb, full, n0 + j * 64, k);
-            } else {
-                load(dst + kBlockA, &a.mb, full, k, n0);
-            }
-        };
-        int m, n, ahead = 0;  // the ring's first round: weights that are copied before the rows are there
-        if (a.early == kFfnWeights && first < tiles) {
-            tile_of(a, first, m, n);
-            for (; ahead < a.stages && c0 + ahead < c1; ++ahead) {
-                expect(smem_u32(&sh.full[ahead]));
-                load_a(ring + ahead * bytes, smem_u32(&sh.full[ahead]), m, (c0 + ahead) * kChunk);
+        Item it;
+        int ahead = 0;  // the ring's first round: weights that are copied before the rows are there
+        {
+            Items first(q, pair);
+            if (first.next(it) && q.p[GRAD ? it.g : 0].early) {
+                const FfnArgs &a = q.p[GRAD ? it.g : 0];
+                int m, n;
+                tile_of(a, it.tile, m, n);
+                for (; ahead < q.stages && it.c0 + ahead < it.c1; ++ahead) {
+                    expect(smem_u32(&sh.full[ahead]), kBlockA + bytes_b(a.tile_n / 2, GRAD && a.b_mn));
+                    load_a<EPI, A_MN, true>(a, ring + ahead * q.bytes, smem_u32(&sh.full[ahead]), (2 * m + rank) * kFeatures,
+                                      (it.c0 + ahead) * kChunk);
+                }
             }
         }
-        if (a.early != kFfnAll) {
-            pdl_wait();
-            fence_async_proxy();  // what the kernel before stored from registers is read by copies
-        }
+        pdl_wait();
+        fence_async_proxy();  // what the kernel before stored from registers is read by copies
         pdl_launch_next();
         Cursor at;
         int issued = 0;
         bool run = true;
-        for (int i = first; run && i < tiles; i += next) {
-            tile_of(a, i, m, n);
-            for (int c = c0; c < c1; ++c) {
-                const uint32_t to = ring + at.s * bytes, full = smem_u32(&sh.full[at.s]);
+        for (Items w(q, pair); run && w.next(it);) {
+            const FfnArgs &a = q.p[GRAD ? it.g : 0];
+            int m, n;
+            tile_of(a, it.tile, m, n);
+            const int m0 = (2 * m + rank) * kFeatures, rows = a.tile_n / 2, n0 = n * a.tile_n + rank * rows;
+            const int bytes = kBlockA + bytes_b(rows, GRAD && a.b_mn);
+            for (int c = it.c0; c < it.c1; ++c) {
+                const uint32_t to = ring + at.s * q.bytes, full = smem_u32(&sh.full[at.s]);
                 if (issued >= ahead) {
                     run = mbar_wait(smem_u32(&sh.empty[at.s]), at.parity ^ 1, abort, kWaitEmptyA);
                     if (!run)
                         break;
-                    expect(full);
-                    load_a(to, full, m, c * kChunk);
+                    expect(full, bytes);
+                    load_a<EPI, A_MN, true>(a, to, full, m0, c * kChunk);
                 }
-                load_b(to, full, n, c * kChunk);
-                at.next(a.stages);
+                load_b<true>(a, GRAD && a.b_mn, to, full, n0, rows, c * kChunk);
+                at.next(q.stages);
                 ++issued;
             }
         }
         sh.issued = issued;
     } else if (warp == 1) {
-        // ---- matrix instructions, of a pair in its first block ----
+        // ---- matrix instructions, in the first block ----
         Cursor at, at_d;
-        bool run = true;
-        const uint32_t idesc =
-            idesc_f16(PAIR ? 256 : 128, a.tile_n, 1) | (A_MN ? kIdescAmn : 0u) | (B_MN ? kIdescBmn : 0u);
-        for (int i = first; run && i < tiles && (!PAIR || rank == 0); i += next) {
+        bool run = rank == 0;
+        Item it;
+        for (Items w(q, pair); run && w.next(it);) {
+            const FfnArgs &a = q.p[GRAD ? it.g : 0];
+            // one value for all lanes, which the compiler then keeps in uniform registers
+            const int tile_n = __shfl_sync(~0u, a.tile_n, 0), b_mn = GRAD ? __shfl_sync(~0u, a.b_mn, 0) : 0;
             run = mbar_wait_warp(smem_u32(&sh.empty_d[at_d.s]), at_d.parity ^ 1, abort, kWaitEmptyD);
             const uint32_t d = tmem + at_d.s * kHalfTmem;
-            for (int c = c0; run && c < c1; ++c) {
+            for (int c = it.c0; run && c < it.c1; ++c) {
                 run = mbar_wait_warp(smem_u32(&sh.full[at.s]), at.parity, abort, kWaitFullA);
                 if (!run)
                     break;
                 tc_fence_after();
                 if (elect_one()) {
-                    const uint32_t from = ring + at.s * bytes;
-                    const uint64_t da = A_MN ? desc_mn(from) : desc_sw128(from);
-                    const uint64_t db = B_MN ? desc_mn(from + kBlockA) : desc_sw128(from + kBlockA);
-#pragma unroll
-                    for (int q = 0; q < 4; ++q) {  // 16 k each: 32 bytes of a row, or 16 rows of 128, in 16-byte units
-                        const uint64_t qa = da + q * (A_MN ? 128 : 2), qb = db + q * (B_MN ? 128 : 2);
-                        if (PAIR)
-                            mma_ss_pair(d, qa, qb, idesc, c > c0 || q > 0);
-                        else
-                            mma_ss(d, qa, qb, idesc, c > c0 || q > 0);
-                    }
-                    if (PAIR)
-                        tc_commit_pair(smem_u32(&sh.empty[at.s]));
+                    if (GRAD && b_mn)
+                        multiply<A_MN, true, true>(d, ring + at.s * q.bytes, tile_n, c > it.c0);
                     else
-                        tc_commit(smem_u32(&sh.empty[at.s]));
+                        multiply<A_MN, false, true>(d, ring + at.s * q.bytes, tile_n, c > it.c0);
+                    tc_commit_pair(smem_u32(&sh.empty[at.s]));
                 }
-                at.next(a.stages);
+                at.next(q.stages);
             }
-            if (elect_one()) {
-                if (PAIR)
-                    tc_commit_pair(smem_u32(&sh.full_d[at_d.s]));
-                else
-                    tc_commit(smem_u32(&sh.full_d[at_d.s]));
-            }
+            if (elect_one())
+                tc_commit_pair(smem_u32(&sh.full_d[at_d.s]));
             at_d.next(2);
         }
-        if ((!PAIR || rank == 0) && elect_one()) {
-            if (PAIR)
-                tc_commit_pair(smem_u32(&sh.drain));
-            else
-                tc_commit(smem_u32(&sh.drain));
-        }
+        if (rank == 0 && elect_one())
+            tc_commit_pair(smem_u32(&sh.drain));
         mbar_wait(smem_u32(&sh.drain), 0, nullptr, kWaitOther);
-    } else if (warp >= 4 && PAIR) {
+    } else if (warp >= kFirstStore) {
         // ---- results, under the next tile's products ----
         // A step is 16 rows. Four warps with the four quarters of the features take every fourth step, give each row's
         // features their place in shared memory, and one of them sends it off as a box (out of bounds is cut off by the
         // map). Joined: a warp of quarters 0 and 1 has gate, the one two quarters on up of the same 32 features; they
         // exchange halves, and each joins 8 of the 16 rows.
         Cursor at_d;
-        const int quarter = warp & 3, turn = (warp - 4) >> 2, steps = a.tile_n / 16;
+        const int quarter = warp & 3, turn = (warp - kFirstStore) >> 2;
         const bool second = EPI == kFfnJoin && quarter >= 2, sender = quarter == 0 && elect_one();
         const int f = (EPI == kFfnJoin ? quarter & 1 : quarter) * 32 + lane;  // of the block's features
         constexpr int kRows = EPI == kFfnJoin ? 8 : 16;                       // of a warp
         const int row0 = second ? 8 : 0;
-        uint8_t *const stage = dyn + (ring - dyn0) + a.stages * bytes + turn * box_bytes(EPI);
-        float *const exchange = reinterpret_cast<float *>(dyn + (ring - dyn0) + a.stages * bytes + 4 * box_bytes(EPI)) +
+        uint8_t *const stage = dyn + (ring - dyn0) + q.stages * q.bytes + turn * box_bytes(EPI);
+        float *const exchange = reinterpret_cast<float *>(dyn + (ring - dyn0) + q.stages * q.bytes + 4 * box_bytes(EPI)) +
                                 (turn * 2 + (quarter & 1)) * 512 + lane;  // [gate, up][8][32]
-        constexpr bool kWeight = A_MN && B_MN;
-        const bool boxes = a.boxes != 0;
+        // a block's part of a tile: [row][128 MMA rows]
+        const auto part_of = [&](int p) { return q.parts + (static_cast<size_t>(2 * p + rank) * 256) * 128 + quarter * 32 + lane; };
         int sent = 0;
-        for (int i = first; i < tiles; i += next) {
+        Item it;
+        for (Items w(q, pair); w.next(it);) {
+            const FfnArgs &a = q.p[GRAD ? it.g : 0];
+            const int steps = a.tile_n / 16;
+            const bool weight = GRAD && a.fp32, boxes = EPI != kFfnStore || a.boxes;
             int m, n;
-            tile_of(a, i, m, n);
+            tile_of(a, it.tile, m, n);
             const int m0 = (2 * m + rank) * kFeatures, col = m0 + f, t0 = n * a.tile_n;
             float g[16], u[16];
             auto fetch = [&](int step) {  // the kept g and u, ahead of their use
@@ -363,94 +386,141 @@ __global__ void __launch_bounds__(threads(PAIR), PAIR ? 1 : 2) ffn_kernel(const 
                         }
                 }
             };
-            fetch(turn);
-            const bool run = mbar_wait(smem_u32(&sh.full_d[at_d.s]), at_d.parity, abort, kWaitFullD);
-            if (!named_all(1, kEpilogue, run))
+            const int p0 = it.kind == kLast ? w.first_of_last() : pair;
+            float before[16];  // the sums of the tile's other parts
+            auto fetch_parts = [&](int step) {
+#pragma unroll
+                for (int r = 0; r < 16; ++r)
+                    before[r] = 0.0f;
+                if (step < steps)
+                    for (int p = p0; p < pair; ++p)
+                        if (q.begin[p] < q.begin[p + 1]) {
+                            const float *const part = part_of(p) + step * 16 * 128;
+#pragma unroll
+                            for (int r = 0; r < 16; ++r)
+                                before[r] += __ldcg(part + r * 128);
+                        }
+            };
+            bool run = true;
+            if (it.kind == kLast) {
+                if (tid == kFirstStore * 32)
+                    for (int p = p0; run && p < pair; ++p)
+                        if (q.begin[p] < q.begin[p + 1])
+                            run = wait_count(q.flags + 2 * p + rank, 1, abort, kWaitDone);
+                if (!named_all(1, kPairStore, run))
+                    break;
+                fetch_parts(turn);
+            }
+            if (it.kind != kPart)
+                fetch(turn);
+            run = mbar_wait(smem_u32(&sh.full_d[at_d.s]), at_d.parity, abort, kWaitFullD);
+            if (!named_all(1, kPairStore, run))
                 break;
             tc_fence_after();
             const uint32_t d = tmem + (static_cast<uint32_t>(quarter) << 21) + at_d.s * kHalfTmem;
-            for (int step = turn; step < steps; step += 4) {
-                const int t = t0 + step * 16;
-                float v[16];
-                tmem_ld16(d + step * 16, v);
-                tmem_wait_ld();
-                if (EPI == kFfnJoin) {
+            if (it.kind == kPart) {
+                float *const part = part_of(pair);
+                for (int step = turn; step < steps; step += 4) {
+                    float v[16];
+                    tmem_ld16(d + step * 16, v);
+                    tmem_wait_ld();
 #pragma unroll
-                    for (int r = 0; r < 8; ++r)
-                        exchange[(second ? 256 : 0) + r * 32] = v[second ? r : r + 8];
-                    named_sync(6 + turn * 2 + (quarter & 1), 64);
-#pragma unroll
-                    for (int r = 0; r < 8; ++r) {
-                        const float other = exchange[(second ? 0 : 256) + r * 32];
-                        g[r] = second ? other : v[r];
-                        u[r] = second ? v[r + 8] : other;
-                    }
-                    if (a.saved && col < a.M) {
-                        float *s = a.saved + 2LL * (t + row0) * a.M + col;
-#pragma unroll
-                        for (int r = 0; r < 8; ++r, s += 2LL * a.M)
-                            if (t + row0 + r < a.N) {
-                                s[0] = g[r];
-                                s[a.M] = u[r];
-                            }
-                    }
+                    for (int r = 0; r < 16; ++r)
+                        part[(step * 16 + r) * 128] = v[r];
                 }
-                if (boxes) {
-                    // two boxes of bf16 in turn, of fp32 or of three results one
-                    const bool one = EPI == kFfnSplit || (kWeight && a.fp32);
-                    uint8_t *const box = stage + (one || (sent & 1) == 0 ? 0 : kFeatures * 32);
-                    ++sent;
-                    if (sender) {
-                        if (one)
-                            bulk_wait_read<0>();
-                        else
-                            bulk_wait_read<1>();
-                    }
-                    named_sync(2 + turn, 128);
-                    if (kWeight && a.fp32) {
-                        float *const to = reinterpret_cast<float *>(box) + f;
+                named_sync(1, kPairStore);
+                if (tid == kFirstStore * 32)
+                    add_acq_rel(q.flags + 2 * pair + rank, 1);
+            } else {
+                for (int step = turn; step < steps; step += 4) {
+                    const int t = t0 + step * 16;
+                    float v[16];
+                    tmem_ld16(d + step * 16, v);
+                    tmem_wait_ld();
+                    if (it.kind == kLast) {
 #pragma unroll
                         for (int r = 0; r < 16; ++r)
-                            to[r * 128] = v[r];
-                    } else {
-                        __nv_bfloat16 *const to = reinterpret_cast<__nv_bfloat16 *>(box) + row0 * kFeatures + f;
+                            v[r] = before[r] + v[r];
+                        fetch_parts(step + 4);
+                    }
+                    if (EPI == kFfnJoin) {
 #pragma unroll
-                        for (int r = 0; r < kRows; ++r) {
-                            if (EPI == kFfnStore) {
-                                to[r * 128] = __float2bfloat16_rn(v[r]);
-                            } else if (EPI == kFfnJoin) {
-                                to[r * 64] = __float2bfloat16_rn(silu(g[r]) * u[r]);
-                            } else {
-                                const Gate gate(g[r]);
-                                to[r * 128] = __float2bfloat16_rn(gate.silu * u[r]);
-                                to[r * 128 + 2048] = __float2bfloat16_rn(v[r] * u[r] * gate.slope);
-                                to[r * 128 + 4096] = __float2bfloat16_rn(v[r] * gate.silu);
+                        for (int r = 0; r < 8; ++r)
+                            exchange[(second ? 256 : 0) + r * 32] = v[second ? r : r + 8];
+                        named_sync(6 + turn * 2 + (quarter & 1), 64);
+#pragma unroll
+                        for (int r = 0; r < 8; ++r) {
+                            const float other = exchange[(second ? 0 : 256) + r * 32];
+                            g[r] = second ? other : v[r];
+                            u[r] = second ? v[r + 8] : other;
+                        }
+                        if (a.saved && col < a.M) {
+                            float *s = a.saved + 2LL * (t + row0) * a.M + col;
+#pragma unroll
+                            for (int r = 0; r < 8; ++r, s += 2LL * a.M)
+                                if (t + row0 + r < a.N) {
+                                    s[0] = g[r];
+                                    s[a.M] = u[r];
+                                }
+                        }
+                    }
+                    if (boxes) {
+                        // two boxes of bf16 in turn, of fp32 or of three results one
+                        const bool one = EPI == kFfnSplit || weight;
+                        uint8_t *const box = stage + (one || (sent & 1) == 0 ? 0 : kFeatures * 32);
+                        ++sent;
+                        if (sender) {
+                            if (one || GRAD)  // boxes of several products may differ
+                                bulk_wait_read<0>();
+                            else
+                                bulk_wait_read<1>();
+                        }
+                        named_sync(2 + turn, 128);
+                        if (weight) {
+                            float *const to = reinterpret_cast<float *>(box) + f;
+#pragma unroll
+                            for (int r = 0; r < 16; ++r)
+                                to[r * 128] = v[r];
+                        } else {
+                            __nv_bfloat16 *const to = reinterpret_cast<__nv_bfloat16 *>(box) + row0 * kFeatures + f;
+#pragma unroll
+                            for (int r = 0; r < kRows; ++r) {
+                                if (EPI == kFfnStore) {
+                                    to[r * 128] = __float2bfloat16_rn(v[r]);
+                                } else if (EPI == kFfnJoin) {
+                                    to[r * 64] = __float2bfloat16_rn(silu(g[r]) * u[r]);
+                                } else {
+                                    const Gate gate(g[r]);
+                                    to[r * 128] = __float2bfloat16_rn(gate.silu * u[r]);
+                                    to[r * 128 + 2048] = __float2bfloat16_rn(v[r] * u[r] * gate.slope);
+                                    to[r * 128 + 4096] = __float2bfloat16_rn(v[r] * gate.silu);
+                                }
                             }
                         }
-                    }
-                    fence_async_shared();
-                    named_sync(2 + turn, 128);
-                    if (sender && m0 < a.M && t < a.N) {
-                        const uint32_t from = smem_u32(box);
-                        if (kWeight && a.accumulate)
-                            tma_add_2d(&a.mo, from, m0, t);
-                        else
-                            tma_store_2d(&a.mo, from, m0, t);
-                        if (EPI == kFfnSplit) {
-                            tma_store_3d(&a.md, from + 4096, m0, t, 0);
-                            tma_store_3d(&a.md, from + 8192, m0, t, 1);
+                        fence_async_shared();
+                        named_sync(2 + turn, 128);
+                        if (sender && m0 < a.M && t < a.N) {
+                            const uint32_t from = smem_u32(box);
+                            if (weight && a.accumulate)
+                                tma_add_2d(&a.mo, from, m0, t);
+                            else
+                                tma_store_2d(&a.mo, from, m0, t);
+                            if (EPI == kFfnSplit) {
+                                tma_store_3d(&a.md, from + 4096, m0, t, 0);
+                                tma_store_3d(&a.md, from + 8192, m0, t, 1);
+                            }
                         }
-                    }
-                    if (sender)
-                        bulk_commit();
-                } else {  // y or dx with rows that a map does not take (or checked): one by one
-                    __nv_bfloat16 *p = static_cast<__nv_bfloat16 *>(a.out) + (t + row0) * a.out_stride + col;
+                        if (sender)
+                            bulk_commit();
+                    } else {  // y or dx with rows that a map does not take (or checked): one by one
+                        __nv_bfloat16 *p = static_cast<__nv_bfloat16 *>(a.out) + (t + row0) * a.out_stride + col;
 #pragma unroll
-                    for (int r = 0; r < kRows; ++r, p += a.out_stride)
-                        if (col < a.M && t + row0 + r < a.N && inside<EPI>(a, p, 2, 2))
-                            *p = __float2bfloat16_rn(v[r]);
+                        for (int r = 0; r < kRows; ++r, p += a.out_stride)
+                            if (col < a.M && t + row0 + r < a.N && inside<EPI>(a, p, 2, 2))
+                                *p = __float2bfloat16_rn(v[r]);
+                    }
+                    fetch(step + 4);
                 }
-                fetch(step + 4);
             }
             tc_fence_before();
             __syncwarp();
@@ -461,80 +531,186 @@ __global__ void __launch_bounds__(threads(PAIR), PAIR ? 1 : 2) ffn_kernel(const 
         if (sender)
             bulk_wait<0>();
     }
-    if (!PAIR) {
-        // ---- a split's sums into this block's memory, then a share of the rows from all of the cluster's ----
-        float *const sums = reinterpret_cast<float *>(dyn + (ring - dyn0));  // [rows][128 features]
-        int m, n;
-        tile_of(a, first, m, n);
-        if (warp >= 4) {
-            const bool run = mbar_wait(smem_u32(&sh.full_d[0]), 0, abort, kWaitFullD);
-            if (named_all(1, kEpilogue, run)) {
-                tc_fence_after();
-                const int quarter = warp & 3;
-                const uint32_t d = tmem + (static_cast<uint32_t>(quarter) << 21);
-                float *const to = sums + quarter * 32 + lane;
-                for (int j = (warp - 4) / 4 * 16; j < a.tile_n; j += 32) {
-                    float v[16];
-                    tmem_ld16(d + j, v);
-                    tmem_wait_ld();
-#pragma unroll
-                    for (int r = 0; r < 16; ++r)
-                        to[(j + r) * 128] = v[r];
-                }
-                tc_fence_before();
+    __syncwarp();
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (sh.abort) {  // copies in flight land before the block's memory is given back
+        if (tid == 0) {
+            bool landed = true;
+            for (int i = max(0, sh.issued - q.stages); rank == 0 && landed && i < sh.issued; ++i)
+                landed = mbar_wait(smem_u32(&sh.full[i % q.stages]), (i / q.stages) & 1, nullptr, kWaitOther);
+            // copies that the first block no longer counts land meanwhile
+            for (const long long from = clock64(); clock64() - from < 1000000;) {
             }
+            report(sh, q.err);
         }
-        __syncwarp();
-        if (a.split > 1)
-            cluster_sync();
-        else
-            __syncthreads();
-        if (warp >= 4 && !sh.abort) {
-            constexpr int kLanes = kFeatures / 4, kStep = kEpilogue / kLanes, R = EPI == kFfnStore ? 2 : 1;  // lanes of a row, rows at a time
-            const int f = lane % kLanes * 4;
-            const int lo = a.tile_n * rank / a.split, hi = a.tile_n * (rank + 1) / a.split;
-            const uint32_t at = smem_u32(sums) + f * 4;
-            const To sink(a, m * kFeatures + f);
-            for (int j = lo + (tid - 128) / kLanes; j < hi; j += kStep * R) {
-                float4 v[R];
-                typename To::Kept k[R];
-#pragma unroll
-                for (int r = 0; r < R; ++r) {
-                    v[r] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-                    if (EPI == kFfnJoin)
-                        k[r].u = v[r];
-                    if (j + r * kStep < hi)
-                        sink.fetch(n * a.tile_n + j + r * kStep, k[r]);
-                }
-                for (int s0 = 0; s0 < a.split; s0 += 4) {
-                    float4 x[4][R], y[4][R];
-#pragma unroll
-                    for (int s = 0; s < 4; ++s)
-                        if (s0 + s < a.split) {
-                            const uint32_t from = in_block(at, s0 + s);
-#pragma unroll
-                            for (int r = 0; r < R; ++r)
-                                if (j + r * kStep < hi) {
-                                    x[s][r] = ld_cluster4(from + (j + r * kStep) * 512);
-                                    if (EPI == kFfnJoin)
-                                        y[s][r] = ld_cluster4(from + (j + r * kStep) * 512 + 256);
-                                }
-                        }
-#pragma unroll
-                    for (int s = 0; s < 4; ++s)
-                        if (s0 + s < a.split)
-#pragma unroll
-                            for (int r = 0; r < R; ++r) {
-                                add4(v[r], x[s][r]);
-                                if (EPI == kFfnJoin)
-                                    add4(k[r].u, y[s][r]);
-                            }
-                }
-#pragma unroll
-                for (int r = 0; r < R; ++r)
-                    if (j + r * kStep < hi)  // the others are another block's
-                        sink.put(n * a.tile_n + j + r * kStep, v[r], k[r]);
+        __syncthreads();
+    }
+    if (warp == 1)
+        tmem_free<true>(tmem, 2 * kHalfTmem);
+    cluster_sync();  // the other block's copies and arrivals have come
+    if (q.cut) {     // the last block to leave clears the flags for the next launch
+        if (tid == 0)
+            sh.reset = add_acq_rel(q.flags + 2 * kFfnMaxPairs, 1) == static_cast<int>(gridDim.x) - 1;
+        __syncthreads();
+        if (sh.reset) {
+            if (tid < 2 * kFfnMaxPairs)
+                q.flags[tid] = 0;
+            if (tid == 0)
+                q.flags[2 * kFfnMaxPairs] = 0;
+        }
+    }
+}
+
+// ---- splits --------------------------------------------------------------------------------
+
+template <int EPI> __global__ void __launch_bounds__(128 + kSplitStore, 2) split_kernel(const __grid_constant__ FfnSplit q)
+{
+    extern __shared__ uint8_t dyn[];
+    __shared__ Shared sh;
+    const FfnArgs &a = q.a;
+    const uint32_t dyn0 = smem_u32(dyn), ring = (dyn0 + 1023u) & ~1023u;
+    const int tid = threadIdx.x, warp = __shfl_sync(~0u, tid >> 5, 0), lane = tid & 31;
+    const int rank = blockIdx.x % q.split;
+    const int c0 = a.chunks * rank / q.split, c1 = a.chunks * (rank + 1) / q.split;
+    const int bytes = kBlockA + bytes_b(a.tile_n, false);
+    constexpr int kFeatures = features_of(EPI);
+    constexpr bool A_MN = kAmn<EPI, false>;
+    volatile int *const abort = &sh.abort;
+    int m, n;
+    tile_of(a, blockIdx.x / q.split, m, n);
+
+    if (tid == 0) {
+        set_barriers(sh, 1);
+    } else if (tid == 64) {
+        tma_prefetch_map(&a.ma);
+        tma_prefetch_map(&a.mb);
+    }
+    const uint32_t columns = tmem_columns(a.tile_n);
+    if (warp == 1)
+        tmem_alloc(smem_u32(&sh.tmem), columns);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = sh.tmem;
+
+    if (warp == 0 && elect_one()) {
+        // ---- copies ----
+        auto a_of = [&](int s, int c) {
+            mbar_expect(smem_u32(&sh.full[s]), bytes);
+            load_a<EPI, A_MN, false>(a, ring + s * bytes, smem_u32(&sh.full[s]), m * kFeatures, c * kChunk);
+        };
+        int ahead = 0;  // the ring's first round: weights that are copied before the rows are there
+        if (a.early)
+            for (; ahead < q.stages && c0 + ahead < c1; ++ahead)
+                a_of(ahead, c0 + ahead);
+        pdl_wait();
+        fence_async_proxy();  // what the kernel before stored from registers is read by copies
+        pdl_launch_next();
+        Cursor at;
+        int issued = 0;
+        for (int c = c0; c < c1; ++c) {
+            if (issued >= ahead) {
+                if (!mbar_wait(smem_u32(&sh.empty[at.s]), at.parity ^ 1, abort, kWaitEmptyA))
+                    break;
+                a_of(at.s, c);
             }
+            load_b<false>(a, false, ring + at.s * bytes, smem_u32(&sh.full[at.s]), n * a.tile_n, a.tile_n, c * kChunk);
+            at.next(q.stages);
+            ++issued;
+        }
+        sh.issued = issued;
+    } else if (warp == 1) {
+        // ---- matrix instructions ----
+        Cursor at;
+        for (int c = c0; c < c1; ++c) {
+            if (!mbar_wait_warp(smem_u32(&sh.full[at.s]), at.parity, abort, kWaitFullA))
+                break;
+            tc_fence_after();
+            if (elect_one()) {
+                multiply<A_MN, false, false>(tmem, ring + at.s * bytes, a.tile_n, c > c0);
+                tc_commit(smem_u32(&sh.empty[at.s]));
+            }
+            at.next(q.stages);
+        }
+        if (elect_one()) {
+            tc_commit(smem_u32(&sh.full_d[0]));
+            tc_commit(smem_u32(&sh.drain));
+        }
+        mbar_wait(smem_u32(&sh.drain), 0, nullptr, kWaitOther);
+    }
+    // ---- this block's sums into its memory, then a share of the rows from all of the cluster's ----
+    float *const sums = reinterpret_cast<float *>(dyn + (ring - dyn0));  // [rows][128 features]
+    if (warp >= kFirstStore) {
+        const bool run = mbar_wait(smem_u32(&sh.full_d[0]), 0, abort, kWaitFullD);
+        if (named_all(1, kSplitStore, run)) {
+            tc_fence_after();
+            const int quarter = warp & 3;
+            const uint32_t d = tmem + (static_cast<uint32_t>(quarter) << 21);
+            float *const to = sums + quarter * 32 + lane;
+            for (int j = (warp - kFirstStore) / 4 * 16; j < a.tile_n; j += 32) {
+                float v[16];
+                tmem_ld16(d + j, v);
+                tmem_wait_ld();
+#pragma unroll
+                for (int r = 0; r < 16; ++r)
+                    to[(j + r) * 128] = v[r];
+            }
+            tc_fence_before();
+        }
+    }
+    __syncwarp();
+    if (q.split > 1)
+        cluster_sync();
+    else
+        __syncthreads();
+    if (warp >= kFirstStore && !sh.abort) {
+        constexpr int kLanes = kFeatures / 4, kStep = kSplitStore / kLanes;  // lanes of a row, rows at a time
+        constexpr int R = EPI == kFfnStore ? 2 : 1;
+        const int f = lane % kLanes * 4;
+        const int lo = a.tile_n * rank / q.split, hi = a.tile_n * (rank + 1) / q.split;
+        const uint32_t at = smem_u32(sums) + f * 4;
+        const Sink<EPI> sink(a, m * kFeatures + f);
+        for (int j = lo + (tid - kFirstStore * 32) / kLanes; j < hi; j += kStep * R) {
+            float4 v[R];
+            typename Sink<EPI>::Kept k[R];
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+                v[r] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                if (EPI == kFfnJoin)
+                    k[r].u = v[r];
+                if (j + r * kStep < hi)
+                    sink.fetch(n * a.tile_n + j + r * kStep, k[r]);
+            }
+            for (int s0 = 0; s0 < q.split; s0 += 4) {
+                float4 x[4][R], y[4][R];
+#pragma unroll
+                for (int s = 0; s < 4; ++s)
+                    if (s0 + s < q.split) {
+                        const uint32_t from = in_block(at, s0 + s);
+#pragma unroll
+                        for (int r = 0; r < R; ++r)
+                            if (j + r * kStep < hi) {
+                                x[s][r] = ld_cluster4(from + (j + r * kStep) * 512);
+                                if (EPI == kFfnJoin)
+                                    y[s][r] = ld_cluster4(from + (j + r * kStep) * 512 + 256);
+                            }
+                    }
+#pragma unroll
+                for (int s = 0; s < 4; ++s)
+                    if (s0 + s < q.split)
+#pragma unroll
+                        for (int r = 0; r < R; ++r) {
+                            add4(v[r], x[s][r]);
+                            if (EPI == kFfnJoin)
+                                add4(k[r].u, y[s][r]);
+                        }
+            }
+#pragma unroll
+            for (int r = 0; r < R; ++r)
+                if (j + r * kStep < hi)  // the others are another block's
+                    sink.put(n * a.tile_n + j + r * kStep, v[r], k[r]);
         }
     }
     __syncwarp();
@@ -544,23 +720,16 @@ __global__ void __launch_bounds__(threads(PAIR), PAIR ? 1 : 2) ffn_kernel(const 
     if (sh.abort) {  // copies in flight land before the block's memory is given back
         if (tid == 0) {
             bool landed = true;
-            for (int i = max(0, sh.issued - a.stages); (!PAIR || rank == 0) && landed && i < sh.issued; ++i)
-                landed = mbar_wait(smem_u32(&sh.full[i % a.stages]), (i / a.stages) & 1, nullptr, kWaitOther);
-            if (PAIR)  // copies that the first block no longer counts land meanwhile
-                for (const long long from = clock64(); clock64() - from < 1000000;) {
-                }
-            atomicAdd_system(a.err + sh.abort, 1u);
-            __threadfence_system();
-            atomicAdd_system(a.err, 1u);
+            for (int i = max(0, sh.issued - q.stages); landed && i < sh.issued; ++i)
+                landed = mbar_wait(smem_u32(&sh.full[i % q.stages]), (i / q.stages) & 1, nullptr, kWaitOther);
+            report(sh, q.err);
         }
         __syncthreads();
     }
     if (warp == 1)
-        tmem_free<PAIR>(tmem, columns);
-    if (PAIR || a.split > 1)
-        cluster_sync();  // the other blocks' copies, arrivals and reads have come
-    if (a.early == kFfnAll && tid == 0)
-        pdl_wait();  // what follows this kernel follows the one before it too
+        tmem_free(tmem, columns);
+    if (q.split > 1)
+        cluster_sync();  // the other blocks have read this one's sums
 }
 
 // Gradients of no rows.
@@ -570,85 +739,209 @@ __global__ void __launch_bounds__(256) zero_kernel(uint32_t *p, size_t words)
         p[i] = 0;
 }
 
-using Kernel = void (*)(FfnArgs);
-
-template <bool PAIR> Kernel kernel_of(const FfnProduct &p)
-{
-    if (p.epilogue == kFfnJoin)
-        return ffn_kernel<kFfnJoin, false, false, PAIR>;
-    if (p.epilogue == kFfnSplit)
-        return ffn_kernel<kFfnSplit, true, false, PAIR>;
-    if (!p.a_mn)
-        return ffn_kernel<kFfnStore, false, false, PAIR>;
-    return p.b_mn ? ffn_kernel<kFfnStore, true, true, PAIR> : ffn_kernel<kFfnStore, true, false, PAIR>;
-}
-
-int div_up(int a, int b) { return (a + b - 1) / b; }
-
-int stage_bytes(const FfnProduct &p)
-{
-    const int rows = p.pair ? p.a.tile_n / 2 : p.a.tile_n;
-    return kBlockA + (p.b_mn ? div_up(rows, 64) * 8192 : rows * 128);
-}
+// ---- plans ---------------------------------------------------------------------------------
 
 // Dynamic shared memory of a block that has an SM for itself, and of one that shares it with another.
 constexpr int kRoom = kSmemMax - 64 - static_cast<int>(sizeof(Shared));
 constexpr int kHalfRoom = (228 * 1024) / 2 - 1024 - 64 - static_cast<int>(sizeof(Shared));
 constexpr int kShareRows = 128;  // up to so many rows a tile, a split's blocks can share an SM
 
+int div_up(int a, int b) { return (a + b - 1) / b; }
+
+// Cycles of a tile's 64 k: 2 a row in the MMAs, or 64 bytes a cycle of the copies of a block's operands.
+double chunk_cycles(int n, bool pair)
+{
+    const double mma = 2.0 * n, copy = (kBlockA + 128.0 * (pair ? n / 2 : n)) / 64.0;
+    return mma > copy ? mma : copy;
+}
+
+struct Choice {
+    double cost;
+    int n, split;  // split 0: pairs
+    bool cut;      // the last rounds of the pairs
+};
+
+// All operands come from DRAM once, whoever asks for them.
+double dram_cycles(const FfnArgs &a, int epilogue)
+{
+    return 2.0 * a.K * (static_cast<double>(a.M) * (epilogue == kFfnJoin ? 2 : 1) + a.N) / 3500.0;
+}
+
+// Cycles of a product's pairs with tiles of n rows: all rounds whole, or evenly cut (which costs the parts' way through
+// memory); a tile's epilogue is hidden if its products take as long.
+Choice pair_choice(const FfnArgs &a, int epilogue, int n, int sms)
+{
+    const double pairs = sms / 2, tiles = static_cast<double>(div_up(a.N, n)) * div_up(a.M, 2 * features_of(epilogue));
+    const double products = a.chunks * chunk_cycles(n, true) + 200, store = 20.0 * n;
+    const double tile = products > store ? products : store;
+    const double parts = pairs > tiles ? pairs / tiles : 1.0;
+    const double whole = std::ceil(tiles / pairs) * tile, even = tiles / pairs * tile + 3000 + 3000 * parts;
+    const double best = whole < even ? whole : even, dram = dram_cycles(a, epilogue);
+    return {(best > dram ? best : dram) + 5000 + 10.0 * n, n, 0, even < whole};
+}
+
+// A cluster's sums meet at a cost that grows with its blocks. A block alone on its SM leaves no room for the next kernel's
+// first copies.
+Choice split_choice(const FfnArgs &a, int epilogue, int n, int split, int sms)
+{
+    const double tiles = static_cast<double>(div_up(a.N, n)) * div_up(a.M, features_of(epilogue)), blocks = tiles * split;
+    const bool share = n <= kShareRows && blocks > sms;
+    const double copy = (kBlockA + 128.0 * n) / 45.0, chunk = copy > 2.0 * n ? copy : 2.0 * n;  // mostly from DRAM
+    const double cost = std::ceil(blocks / sms) * div_up(a.chunks, split) * chunk;
+    const double after = std::ceil(blocks / (share ? 2 * sms : sms)) * (3000.0 + n * (8.0 + 4.0 * split));
+    const double dram = dram_cycles(a, epilogue);
+    return {(cost > dram ? cost : dram) + after + (share ? 0.0 : 1500.0), n, split, false};
+}
+
+template <class F> Choice least(const FfnArgs &a, F &&cost)
+{
+    // Of rows that lie along memory a pair's halves are whole lines: 128 rows or 256. Other heights read up to twice as
+    // much (the gradients of 1999 rows, 2056 x 1400: 51 us instead of 33).
+    const int step = a.b_mn ? 128 : 16;
+    Choice best = {-1.0, step, 0, false};
+    for (int n = step; n <= 256; n += step) {
+        if (n > step && div_up(a.N, n - step) == div_up(a.N, n))
+            continue;  // the same tiles with more waste
+        const Choice c = cost(n);
+        if (best.cost < 0.0 || c.cost < best.cost)
+            best = c;
+    }
+    return best;
+}
+
+// Which tiles are whole and which are cut. Tiles of a product whose shares end within a few chunks of a tile's edge are
+// not cut there.
+void cut_rounds(FfnGroup *q, bool cut)
+{
+    const int pairs = q->pairs;
+    int tiles = 0;
+    for (int g = 0; g < q->count; ++g)
+        tiles += q->p[g].m_tiles * q->p[g].n_tiles;
+    // a last round of few tiles is cut together with the one before: a tile has few parts
+    const int rounds = tiles / pairs, rest_tiles = tiles % pairs;
+    q->whole = !cut ? tiles : (rest_tiles * 3 >= pairs || rounds == 0 ? rounds : rounds - 1) * pairs;
+    double units[kFfnMaxPairs] = {}, all = 0.0;
+    int left = q->whole, first = 0;
+    for (int g = 0; g < q->count; ++g) {
+        FfnArgs &a = q->p[g];
+        const int mine = a.m_tiles * a.n_tiles;
+        a.whole = left < mine ? left : mine;
+        left -= a.whole;
+        for (int p = 0; p < pairs; ++p) {  // whole tiles first + p, ... of this product
+            const int skip = ((p - first) % pairs + pairs) % pairs;
+            const int n = a.whole > skip ? (a.whole - skip + pairs - 1) / pairs : 0;
+            units[p] += static_cast<double>(n) * a.chunks * chunk_cycles(a.tile_n, true);
+        }
+        first = (first + a.whole) % pairs;
+        all += static_cast<double>(mine) * a.chunks * chunk_cycles(a.tile_n, true);
+    }
+    // shares of the cut rounds: what a pair's whole tiles leave of its part of everything
+    double want[kFfnMaxPairs], sum = 0.0, rest = all;
+    for (int p = 0; p < pairs; ++p) {
+        rest -= units[p];
+        want[p] = all / pairs - units[p] > 0.0 ? all / pairs - units[p] : 0.0;
+        sum += want[p];
+    }
+    double to = 0.0;
+    for (int p = 0; p <= kFfnMaxPairs; ++p)
+        q->begin[p] = 0;
+    int unit = 0;
+    for (int p = 0; p < pairs; ++p) {
+        q->begin[p] = unit;
+        to += sum > 0.0 ? want[p] * rest / sum : 0.0;
+        // the unit at `to` cycles
+        double at = 0.0;
+        unit = 0;
+        for (int g = 0; g < q->count; ++g) {
+            const FfnArgs &a = q->p[g];
+            const double one = chunk_cycles(a.tile_n, true);
+            const int have = (a.m_tiles * a.n_tiles - a.whole) * a.chunks;
+            if (p == pairs - 1 || at + have * one <= to) {
+                at += have * one;
+                unit += have;
+                continue;
+            }
+            int here = static_cast<int>((to - at) / one + 0.5);
+            const int edge = a.chunks / 16 > 2 ? a.chunks / 16 : 2, in = here % a.chunks;
+            if (in <= edge)
+                here -= in;
+            else if (a.chunks - in <= edge)
+                here += a.chunks - in;
+            unit += here;
+            break;
+        }
+        if (unit < q->begin[p])
+            unit = q->begin[p];
+    }
+    for (int p = pairs; p <= kFfnMaxPairs; ++p)
+        q->begin[p] = unit;
+}
+
 }  // namespace
 
-// The plan of least cost, in cycles. A tile's 64 k take 2 cycles a row in the MMAs or 64 bytes a cycle of the copies
-// of a block's operands, whichever is more; the weights, or all operands, have to come from DRAM once.
-void ffn_plan(FfnProduct *p, int sms)
+void ffn_plan(FfnLaunch *l, int sms)
 {
-    FfnArgs &a = p->a;
-    const int chunks = div_up(a.K, kChunk), features = p->epilogue == kFfnJoin ? 64 : 128;
-    const double dram = 2.0 * a.K * (static_cast<double>(a.M) * (p->epilogue == kFfnJoin ? 2 : 1) + a.N) / 3500.0;
-    double best = 0.0;
-    bool any = false;
-    int best_n = 16, best_split = 1;
-    bool best_pair = false;
-    for (int pair = 0; pair < 2; ++pair)
-        for (int n = 16; n <= 256; n += 16) {
-            const int n_tiles = div_up(a.N, n);
-            if (n > 16 && div_up(a.N, n - 16) == n_tiles)
-                continue;  // the same tiles with more waste
-            const double tiles = static_cast<double>(n_tiles) * div_up(a.M, features * (pair ? 2 : 1));
-            const double mma = 2.0 * n, copy = (kBlockA + 128.0 * (pair ? n / 2 : n)) / 64.0;
-            const double chunk = mma > copy ? mma : copy;
-            for (int split = 1; split <= (pair ? 1 : 8) && split <= chunks; split *= 2) {
-                double cost;
-                if (pair) {
-                    const double waves = std::ceil(tiles / (sms / 2));
-                    cost = waves * (chunks * chunk + 400.0);
-                    cost = (cost > dram ? cost : dram) + 3000.0 + 10.0 * n;
-                } else {
-                    const int resident = n <= kShareRows ? 2 : 1;  // they share the SM's MMAs and copies
-                    const double blocks = tiles * split, mine = std::ceil(blocks / sms);
-                    cost = mine * div_up(chunks, split) * chunk;
-                    cost = (cost > dram ? cost : dram) + std::ceil(blocks / (resident * sms)) * (3000.0 + 16.0 * n);
-                }
-                if (!any || cost < best) {
-                    any = true;
-                    best = cost;
-                    best_n = n;
-                    best_split = split;
-                    best_pair = pair != 0;
-                }
+    FfnGroup &q = l->q;
+    q.pairs = sms / 2 < kFfnMaxPairs ? sms / 2 : kFfnMaxPairs;
+    const bool grad = q.p[0].a_mn && l->epilogue == kFfnStore;  // dx, or the weights' gradients: pairs
+    bool cut = q.count > 1;
+    l->split = 0;
+    for (int g = 0; g < q.count; ++g) {
+        FfnArgs &a = q.p[g];
+        a.chunks = div_up(a.K, kChunk);
+        Choice c = least(a, [&](int n) { return pair_choice(a, l->epilogue, n, 2 * q.pairs); });
+        if (q.count == 1) {
+            cut = c.cut;
+            for (int split = 1; !grad && split <= 8 && split <= a.chunks; split *= 2) {
+                const Choice s = least(a, [&](int n) { return split_choice(a, l->epilogue, n, split, sms); });
+                if (s.cost < c.cost)
+                    c = s;
             }
+            l->split = c.split;
         }
-    a.tile_n = best_n;
-    a.split = best_split;
-    p->pair = best_pair;
-    a.m_tiles = div_up(a.M, features * (best_pair ? 2 : 1));
-    a.n_tiles = div_up(a.N, best_n);
-    p->box_b = best_pair ? best_n / 2 : best_n;
-    // Two blocks of a split on an SM where there are more blocks than SMs
-    const bool share = !best_pair && best_n <= kShareRows && static_cast<long long>(a.m_tiles) * a.n_tiles * best_split > sms;
-    const int room = share ? kHalfRoom : kRoom - (best_pair ? out_bytes(p->epilogue) : 0), stage = stage_bytes(*p);
-    a.stages = (room - 1024) / stage < kMaxStages ? (room - 1024) / stage : kMaxStages;
+        a.tile_n = c.n;
+        a.m_tiles = div_up(a.M, features_of(l->epilogue) * (c.split ? 1 : 2));
+        a.n_tiles = div_up(a.N, c.n);
+        a.box_b = c.split ? c.n : c.n / 2;
+    }
+    if (l->split) {
+        const FfnArgs &a = q.p[0];
+        // two blocks on an SM where there are more blocks than SMs
+        const bool share = a.tile_n <= kShareRows && static_cast<long long>(a.m_tiles) * a.n_tiles * l->split > sms;
+        q.bytes = kBlockA + bytes_b(a.tile_n, a.b_mn);
+        q.stages = ((share ? kHalfRoom : kRoom) - 1024) / q.bytes;
+    } else {
+        q.bytes = 0;
+        for (int g = 0; g < q.count; ++g) {
+            const int bytes = kBlockA + bytes_b(q.p[g].tile_n / 2, q.p[g].b_mn);
+            q.bytes = bytes > q.bytes ? bytes : q.bytes;
+        }
+        q.stages = (kRoom - 1024 - out_bytes(l->epilogue)) / q.bytes;
+        cut_rounds(&q, cut);
+        q.cut = q.begin[q.pairs] > 0;
+    }
+    q.stages = q.stages < kMaxStages ? q.stages : kMaxStages;
+    l->parts = !l->split && q.cut ? static_cast<size_t>(2 * q.pairs) * 256 * 128 * sizeof(float) : 0;
 }
+
+namespace {
+
+using PairKernel = void (*)(FfnGroup);
+using SplitKernel = void (*)(FfnSplit);
+
+PairKernel pair_of(int epilogue, bool grad)
+{
+    return epilogue == kFfnJoin    ? pair_kernel<kFfnJoin, false>
+           : epilogue == kFfnSplit ? pair_kernel<kFfnSplit, false>
+           : grad                  ? pair_kernel<kFfnStore, true>
+                                   : pair_kernel<kFfnStore, false>;
+}
+SplitKernel split_of(int epilogue)
+{
+    return epilogue == kFfnJoin ? split_kernel<kFfnJoin> : epilogue == kFfnSplit ? split_kernel<kFfnSplit> : split_kernel<kFfnStore>;
+}
+
+}  // namespace
 
 cudaError_t ffn_setup()
 {
@@ -659,29 +952,38 @@ cudaError_t ffn_setup()
     return ce;
 }
 
-cudaError_t launch_ffn(const FfnProduct &p, int sms, cudaStream_t stream)
+cudaError_t launch_ffn(const FfnLaunch &l, cudaStream_t stream)
 {
-    const FfnArgs &a = p.a;
-    const int tiles = a.m_tiles * a.n_tiles;
-    size_t ring = static_cast<size_t>(a.stages) * stage_bytes(p);
-    const size_t sums = static_cast<size_t>(a.tile_n) * 512;  // no more than a stage or two
-    if (!p.pair && ring < sums)
-        ring = sums;
+    const FfnGroup &q = l.q;
+    const FfnArgs &a = q.p[0];
     cudaLaunchConfig_t cfg = {};
-    const int pairs = sms / 2;
-    cfg.gridDim = dim3(p.pair ? 2 * (tiles < pairs ? tiles : pairs) : tiles * a.split);
-    cfg.blockDim = dim3(threads(p.pair));
-    cfg.dynamicSmemBytes = 1024 + ring + (p.pair ? out_bytes(p.epilogue) : 0);
     cfg.stream = stream;
     cudaLaunchAttribute at[2];
     at[0].id = cudaLaunchAttributeClusterDimension;
-    at[0].val.clusterDim.x = p.pair ? 2 : a.split;
+    at[0].val.clusterDim.x = l.split ? l.split : 2;
     at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
     at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     at[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = at;
     cfg.numAttrs = 2;
-    return cudaLaunchKernelEx(&cfg, p.pair ? kernel_of<true>(p) : kernel_of<false>(p), a);
+    size_t ring = static_cast<size_t>(q.stages) * q.bytes;
+    if (l.split) {
+        const size_t sums = static_cast<size_t>(a.tile_n) * 512;  // no more than a few stages
+        FfnSplit s;
+        s.a = a;
+        s.stages = q.stages;
+        s.split = l.split;
+        s.err = q.err;
+        cfg.gridDim = dim3(a.m_tiles * a.n_tiles * l.split);
+        cfg.blockDim = dim3(128 + kSplitStore);
+        cfg.dynamicSmemBytes = 1024 + (ring > sums ? ring : sums);
+        return cudaLaunchKernelEx(&cfg, split_of(l.epilogue), s);
+    }
+    int busy = q.cut ? q.pairs : q.whole < q.pairs ? q.whole : q.pairs;
+    cfg.gridDim = dim3(2 * busy);
+    cfg.blockDim = dim3(128 + kPairStore);
+    cfg.dynamicSmemBytes = 1024 + ring + out_bytes(l.epilogue);
+    return cudaLaunchKernelEx(&cfg, pair_of(l.epilogue, a.a_mn != 0), q);
 }
 
 cudaError_t launch_ffn_zero(void *p, size_t bytes, cudaStream_t stream)
@@ -692,14 +994,13 @@ cudaError_t launch_ffn_zero(void *p, size_t bytes, cudaStream_t stream)
 
 std::vector<const void *> ffn_kernels()
 {
-#define FFN(PAIR)                                                                           \
-    reinterpret_cast<const void *>(ffn_kernel<kFfnJoin, false, false, PAIR>),               \
-        reinterpret_cast<const void *>(ffn_kernel<kFfnSplit, true, false, PAIR>),           \
-        reinterpret_cast<const void *>(ffn_kernel<kFfnStore, false, false, PAIR>),          \
-        reinterpret_cast<const void *>(ffn_kernel<kFfnStore, true, false, PAIR>),           \
-        reinterpret_cast<const void *>(ffn_kernel<kFfnStore, true, true, PAIR>)
-    return {FFN(true), FFN(false), reinterpret_cast<const void *>(zero_kernel)};
-#undef FFN
+    std::vector<const void *> all = {reinterpret_cast<const void *>(zero_kernel)};
+    all.push_back(reinterpret_cast<const void *>(pair_of(kFfnStore, true)));
+    for (const int e : {kFfnStore, kFfnJoin, kFfnSplit}) {
+        all.push_back(reinterpret_cast<const void *>(pair_of(e, false)));
+        all.push_back(reinterpret_cast<const void *>(split_of(e)));
+    }
+    return all;
 }
 
 }  // namespace moe

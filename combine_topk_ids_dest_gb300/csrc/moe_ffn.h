@@ -1,0 +1,105 @@
+// moe_ffn.h -- the order of a feed-forward launch's work: tiles in bands, and
+// what each pair of blocks does (shared with the test of all plans).
+#pragma once
+
+#include "moe_internal.h"
+
+namespace moe {
+
+constexpr int kBand = 8;  // row tiles of a band of tiles
+
+// Tiles in bands of kBand row tiles, feature tiles one after the other within a band: tiles that run at a time share
+// operands in L2.
+static __host__ __device__ __forceinline__ void tile_of(const FfnArgs &a, int i, int &m, int &n)
+{
+    const int band = i / (kBand * a.m_tiles), first = band * kBand, wide = a.n_tiles - first < kBand ? a.n_tiles - first : kBand;
+    const int in = i - first * a.m_tiles;
+    m = in / wide;
+    n = first + in - m * wide;
+}
+
+// A pair's work: a tile of product g over chunks [c0, c1) of K.
+enum ItemKind { kWhole = 0, kPart, kLast };  // a part's sums go to memory; the last part of a tile adds the others'
+struct Item {
+    int g, tile, c0, c1, kind;
+};
+
+// In the order in which all roles go through it: whole tiles, every pairs-th, so that pairs that share operands read them
+// at the same time; the first part of a tile that later pairs end; tiles cut out of the last rounds in full; the last part
+// of a tile that earlier pairs began, whose parts are there by then.
+struct Items {
+    const FfnGroup &q;
+    const int pair;
+    int gb, tb, cb, ge, te, ce;  // the share of the cut rounds: from chunk cb of tile tb of product gb to ge, te, ce
+    bool any;
+    int phase, g, t;
+
+    __host__ __device__ __forceinline__ Items(const FfnGroup &q_, int pair_) : q(q_), pair(pair_), phase(0)
+    {
+        any = q.begin[pair] < q.begin[pair + 1];
+        locate(q.begin[pair], gb, tb, cb);
+        locate(q.begin[pair + 1], ge, te, ce);
+        g = 0;
+        t = pair;
+    }
+    __host__ __device__ __forceinline__ void locate(int u, int &at_g, int &at_t, int &at_c) const
+    {
+        for (at_g = 0; at_g < q.count - 1; ++at_g) {
+            const FfnArgs &a = q.p[at_g];
+            const int units = (a.m_tiles * a.n_tiles - a.whole) * a.chunks;
+            if (u < units)
+                break;
+            u -= units;
+        }
+        at_t = q.p[at_g].whole + u / q.p[at_g].chunks;
+        at_c = u % q.p[at_g].chunks;
+    }
+    __host__ __device__ __forceinline__ bool next(Item &it)
+    {
+        const bool one = gb == ge && tb == te;  // all of the share is in one tile
+        if (phase == 0) {
+            if (t < q.whole) {
+                int i = t;
+                for (g = 0; g < q.count - 1 && i >= q.p[g].whole; ++g)
+                    i -= q.p[g].whole;
+                t += q.pairs;
+                it = {g, i, 0, q.p[g].chunks, kWhole};
+                return true;
+            }
+            if (!any)
+                return false;
+            phase = 1;
+            g = gb;
+            t = tb + (cb > 0);
+            if (ce > 0) {
+                it = {ge, te, one ? cb : 0, ce, kPart};
+                return true;
+            }
+        }
+        if (phase == 1) {
+            while (g < ge && t >= q.p[g].m_tiles * q.p[g].n_tiles)
+                t = q.p[++g].whole;
+            if (g < ge || t < te) {
+                it = {g, t++, 0, q.p[g].chunks, kWhole};
+                return true;
+            }
+            phase = 2;
+            if (cb > 0 && !one) {
+                it = {gb, tb, cb, q.p[gb].chunks, kLast};
+                return true;
+            }
+        }
+        return false;
+    }
+    // The first of the pairs that have parts of the tile that this one ends.
+    __host__ __device__ __forceinline__ int first_of_last() const
+    {
+        const int start = q.begin[pair] - cb;
+        int p = pair - 1;
+        while (p > 0 && q.begin[p] > start)
+            --p;
+        return p;
+    }
+};
+
+}  // namespace moe

@@ -204,10 +204,12 @@ struct NormBackArgs {
     float *dweight;
     float *parts;  // [blocks, H], or NULL: no dweight
     int T, H, dtype, weight_fp32, sms;
+    int team, teams, rows, stage, stages;  // warps of a row, rows at a time; the ring's rows in a stage, bytes, stages
     float eps;
     epk::CheckCtx chk;
 };
 
+cudaError_t norm_setup();
 cudaError_t launch_norm(const NormArgs &a, cudaStream_t stream);
 cudaError_t launch_norm_back(const NormBackArgs &a, cudaStream_t stream);
 int norm_back_blocks(int T, int sms);  // parts of dweight
@@ -218,9 +220,7 @@ std::vector<const void *> norm_kernels();  // every kernel of the file
 // What a product's results become: stored as they are, gate and up joined, or the gradients of gate and up.
 enum FfnEpilogue { kFfnStore = 0, kFfnJoin, kFfnSplit };
 
-// What of a product's operands may be read before the kernel that was queued before it has ended: nothing; A, which
-// that kernel, of the same call, does not write; everything, where that kernel itself began after what wrote them.
-enum FfnEarly { kFfnNone = 0, kFfnWeights, kFfnAll };
+constexpr int kFfnMaxPairs = 80;  // pairs of blocks of one launch
 
 // One product D[M features, N rows] = A[M, K] B[N, K]^T; a tile is 128 features (joined: 64, with gate and up) of a
 // block by tile_n rows.
@@ -229,28 +229,47 @@ struct FfnArgs {
     CUtensorMap mo, md;  // out, boxes of a block's features x 16; dgu as [2][N, M] (split), likewise
     void *out;           // [N, M], rows out_stride apart: y, dx, the weights' gradients (N and M both features), h
     long long out_stride;
-    float *saved;           // [N, 2 M]: g and u, written (joined) or read (split); NULL: not wanted
-    __nv_bfloat16 *dgu;     // [N, 2 M], split
-    unsigned int *err;
-    int M, N, K, tile_n, m_tiles, n_tiles, stages, split;
-    int fp32, accumulate;  // of out
-    int early;             // FfnEarly
-    int aligned;           // out and its rows are 8-byte aligned
-    int boxes;             // out can be written through mo
+    float *saved;        // [N, 2 M]: g and u, written (joined) or read (split); NULL: not wanted
+    __nv_bfloat16 *dgu;  // [N, 2 M], split
+    int M, N, K;
+    int a_mn, b_mn;         // the operand's features or rows are contiguous, not K
+    int fp32, accumulate;   // of out
+    int early;              // A may be read before the kernel that was queued before has ended (it does not write it)
+    int aligned;            // out and its rows are 8-byte aligned
+    int boxes;              // out can be written through mo
+    int tile_n, m_tiles, n_tiles, chunks, box_b;  // of the plan; box_b: rows of mb's box where K is contiguous
+    int whole;              // tiles that are not in the cut rounds
     epk::CheckCtx chk;
 };
 
-// A product as the host asks for it; the plan fills in the rest of a.
-struct FfnProduct {
-    FfnArgs a;
-    int epilogue;
-    bool a_mn, b_mn;  // the operand's features or rows are contiguous, not K
-    bool pair;
-    int box_b;        // rows of mb's box where K is contiguous
+// Up to three products with the same epilogue, over pairs of blocks.
+struct FfnGroup {
+    FfnArgs p[3];
+    float *parts;  // [pair][block][256 rows][128]: sums of tiles that another pair ends
+    int *flags;    // [pair][block]: that part is written; then the number of blocks that have left. 0 between launches
+    unsigned int *err;
+    int count, pairs, stages, bytes;  // bytes of a stage
+    int whole, cut;                   // whole tiles of all products; whether there are cut rounds
+    int begin[kFfnMaxPairs + 1];      // each pair's share of the cut rounds, in chunks of their tiles
 };
-void ffn_plan(FfnProduct *p, int sms);
+
+// One product over clusters of `split` blocks that share a tile's K.
+struct FfnSplit {
+    FfnArgs a;
+    unsigned int *err;
+    int stages, split;
+};
+
+// A launch as the host asks for it (count, epilogue, the products' sizes and pointers); the plan fills in the rest.
+struct FfnLaunch {
+    FfnGroup q;
+    int epilogue;
+    int split;     // 0: pairs
+    size_t parts;  // bytes of q.parts
+};
+void ffn_plan(FfnLaunch *l, int sms);
 cudaError_t ffn_setup();
-cudaError_t launch_ffn(const FfnProduct &p, int sms, cudaStream_t stream);
+cudaError_t launch_ffn(const FfnLaunch &l, cudaStream_t stream);
 cudaError_t launch_ffn_zero(void *p, size_t bytes, cudaStream_t stream);
 std::vector<const void *> ffn_kernels();  // every kernel of the file
 

@@ -4,8 +4,9 @@
 //   s = x + residual;  r = 1 / sqrt(mean(s^2) + eps);  y = s r w
 //   backward:  n = h r;  g = dy w;  dx = r (g - n mean(g n)) + dh;  dw = sum_t dy n
 //
-// A row is read once and stays in registers, 8 columns to a unit; a block has
-// one row, or several short ones.
+// A row is read once and stays in registers, 8 columns to a unit. Forward, a
+// block has one row, or several short ones; backward, the blocks are persistent
+// and a row comes through a ring of shared memory.
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
 
@@ -17,6 +18,9 @@ namespace moe {
 namespace {
 
 constexpr int kUnit = 8;             // columns that a thread takes at a time
+constexpr int kBackThreads = 17 * 32;  // of the backward pass: 16 warps that compute, one that copies
+constexpr int kFewUnits = 2, kMostUnits = 4;  // units of a lane: the more up to 16384 columns in 16 warps
+constexpr int kBackStages = 32, kBackRing = 200 * 1024;
 constexpr float kScaled = 0x1p-80f;  // squares of rows whose sum exceeds fp32 are taken of s * this
 
 struct Raw16 {
@@ -124,9 +128,10 @@ template <class T> static __device__ __forceinline__ void load_weight(const void
     }
 }
 
-// Sums of N values over the `warps` warps of a row, in the same order in every thread. slots: [N][32] of this row. All
-// threads of the block call it.
-template <int N> static __device__ __forceinline__ void row_sums(float (&v)[N], float (*slots)[32], int warps, int warp, int lane)
+// Sums of N values over the `warps` warps of a row, in the same order in every thread. slots: [N][32] of this row.
+// Rows of several warps have a block for themselves (barriers by a register's number would cost a block all 16).
+template <int N>
+static __device__ __forceinline__ void row_sums(float (&v)[N], float (*slots)[32], int warps, int warp, int lane)
 {
 #pragma unroll
     for (int i = 0; i < N; ++i)
@@ -149,6 +154,28 @@ template <int N> static __device__ __forceinline__ void row_sums(float (&v)[N], 
     }
 }
 
+// Two sums over a team's warps, in the same order in all its threads.
+static __device__ __forceinline__ void team_sums(float (&v)[2], float (*slots)[16], int warps, int place, int team, int lane)
+{
+#pragma unroll
+    for (int d = 16; d; d >>= 1) {
+        v[0] += __shfl_xor_sync(~0u, v[0], d);
+        v[1] += __shfl_xor_sync(~0u, v[1], d);
+    }
+    if (warps == 1)
+        return;
+    if (lane < 2)
+        slots[lane][place] = lane ? v[1] : v[0];
+    named_sync(1 + team, warps * 32);
+    // lanes 0 to 15 have the first sum's parts, 16 to 31 the second's
+    float x = (lane & 15) < warps ? slots[lane >> 4][lane & 15] : 0.0f;
+#pragma unroll
+    for (int d = 8; d; d >>= 1)
+        x += __shfl_xor_sync(~0u, x, d);
+    v[0] = __shfl_sync(~0u, x, 0);
+    v[1] = __shfl_sync(~0u, x, 16);
+}
+
 // 1 / sqrt(sum / H + eps); for a sum of squares of finite values that exceeds fp32, from the sum of (s kScaled)^2,
 // next to which eps is nothing.
 static __device__ __forceinline__ float rstd_of(float sum, int H, float eps)
@@ -167,6 +194,8 @@ template <class T, int U> __global__ void __launch_bounds__(1024) norm_kernel(co
     const int units = a.H / kUnit, lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
     const long long t = static_cast<long long>(blockIdx.x) * blockDim.y + threadIdx.y;
     const bool live = t < a.T;
+    pdl_wait();
+    pdl_launch_next();
     float s[U][kUnit];
     float sum[1] = {0.0f};
     {
@@ -204,8 +233,7 @@ template <class T, int U> __global__ void __launch_bounds__(1024) norm_kernel(co
     }
     row_sums<1>(sum, slots[threadIdx.y][0], warps, warp, lane);
     float rstd = rstd_of(sum[0], a.H, a.eps);
-    // rare: squares that exceed fp32 (all rows of the block take part, for the barrier)
-    if (__syncthreads_or(isinf(sum[0]))) {
+    if (isinf(sum[0])) {  // rare: squares that exceed fp32; the same in all threads of the row
         float again[1] = {0.0f};
 #pragma unroll
         for (int i = 0; i < U; ++i)
@@ -213,8 +241,7 @@ template <class T, int U> __global__ void __launch_bounds__(1024) norm_kernel(co
             for (int j = 0; j < kUnit; ++j)
                 again[0] = fmaf(s[i][j] * kScaled, s[i][j] * kScaled, again[0]);
         row_sums<1>(again, slots[threadIdx.y][1], warps, warp, lane);
-        if (isinf(sum[0]))
-            rstd = rstd_scaled(again[0], a.H);
+        rstd = rstd_scaled(again[0], a.H);
     }
 #pragma unroll
     for (int i = 0; i < U; ++i) {
@@ -264,107 +291,236 @@ template <class T, int U> __global__ void __launch_bounds__(1024) norm_kernel(co
     }
 }
 
-// One block has rows blockIdx.x + i gridDim.x, and the sums of its rows' parts of dw, per column in one thread.
-template <class T, int U> __global__ void __launch_bounds__(1024) back_kernel(const __grid_constant__ NormBackArgs a)
+// Two fp32 numbers at a time (one instruction each; the kernel below is near the rate of instructions otherwise).
+static __device__ __forceinline__ uint64_t as64(float2 v) { return *reinterpret_cast<uint64_t *>(&v); }
+static __device__ __forceinline__ float2 as2(uint64_t v) { return *reinterpret_cast<float2 *>(&v); }
+static __device__ __forceinline__ float2 mul2(float2 a, float2 b)
 {
-    __shared__ float slots[2][2][32];
-    __shared__ float slots_again[2][2][32];
-    const int units = a.H / kUnit, lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
-    float acc[U][kUnit];
+    uint64_t d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(as64(a)), "l"(as64(b)));
+    return as2(d);
+}
+static __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c)
+{
+    uint64_t d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(as64(a)), "l"(as64(b)), "l"(as64(c)));
+    return as2(d);
+}
+constexpr int kPairs = kUnit / 2;
+
+template <class T> static __device__ __forceinline__ void widen_pairs(const Raw16 &u, float2 (&f)[kPairs])
+{
+    f[0] = widen<T>(u.v.x), f[1] = widen<T>(u.v.y), f[2] = widen<T>(u.v.z), f[3] = widen<T>(u.v.w);
+}
+template <class T> static __device__ __forceinline__ void widen_pairs(const Raw32 &u, float2 (&f)[kPairs])
+{
 #pragma unroll
-    for (int i = 0; i < U; ++i)
-#pragma unroll
-        for (int j = 0; j < kUnit; ++j)
-            acc[i][j] = 0.0f;
-    int turn = 0;
-    for (long long t = blockIdx.x; t < a.T; t += gridDim.x, turn ^= 1) {
-        Unit<T> rh[U], rdy[U], rdh[U];
-#pragma unroll
-        for (int i = 0; i < U; ++i) {
-            const int u = threadIdx.x + i * blockDim.x;
-            if (u < units) {
-                rh[i] = load(unit_at<T>(a.h, a.h_stride, t, u));
-                rdy[i] = load(unit_at<T>(a.dy, a.dy_stride, t, u));
-                if (a.dx && a.dh)
-                    rdh[i] = load(unit_at<T>(a.dh, a.dh_stride, t, u));
-            }
+    for (int i = 0; i < 2; ++i) {
+        f[2 * i] = make_float2(__uint_as_float(u.v[i].x), __uint_as_float(u.v[i].y));
+        f[2 * i + 1] = make_float2(__uint_as_float(u.v[i].z), __uint_as_float(u.v[i].w));
+    }
+}
+
+// The backward pass: one block an SM. Rows of h, dy and dh are copied into a ring of shared memory, as many as it holds
+// on their way at a time, and taken in turn by teams of warps (a.team warps; a lane has up to U units of a row).
+// A stage of the ring has a.rows rows that follow one another, block b's are b, b + gridDim.x, ...; team r takes the
+// stage's rows r, r + a.teams, ... Where rows are contiguous in memory a stage is one copy per operand. A lane keeps the sum of its columns' parts of
+// dw; at the end the teams' sums are added in their order.
+//   p = dy h;  dw += p r;  dx = dy w r - h (r^2 mean(g n)) + dh,  mean(g n) = r sum(p w) / H
+template <class T, int U> __global__ void __launch_bounds__(kBackThreads, 1) back_kernel(const __grid_constant__ NormBackArgs a)
+{
+    extern __shared__ uint8_t dyn[];
+    __shared__ uint64_t full[kBackStages], empty[kBackStages];
+    __shared__ float slots[16][2][2][16];  // [team][turn][sum][warp]
+    __shared__ int abort_, issued_;
+    uint8_t *const ring = dyn + (128 - (smem_u32(dyn) & 127)) % 128;
+    const int tid = threadIdx.x, warp = __shfl_sync(~0u, tid >> 5, 0), lane = tid & 31;
+    const int team = warp / a.team, place = warp - team * a.team, units = a.H / kUnit;
+    const int groups = static_cast<int>((a.T + a.rows - 1LL) / a.rows), mine = (groups - 1 - static_cast<int>(blockIdx.x)) / static_cast<int>(gridDim.x) + 1;
+    const uint32_t row_bytes = a.H * sizeof(T);
+    const bool has_dh = a.dx && a.dh;
+    volatile int *const abort = &abort_;
+
+    if (tid == 0) {
+        abort_ = issued_ = 0;
+        for (int i = 0; i < a.stages; ++i) {
+            mbar_init(smem_u32(&full[i]), 1);
+            mbar_init(smem_u32(&empty[i]), a.team * a.teams);
         }
-        float sums[2] = {0.0f, 0.0f};  // of h^2 and of dy w h
-#pragma unroll
-        for (int i = 0; i < U; ++i) {
-            const int u = threadIdx.x + i * blockDim.x;
-            if (u < units) {
-                float h[kUnit], dy[kUnit], w[kUnit];
-                widen_unit<T>(rh[i], h);
-                widen_unit<T>(rdy[i], dy);
-                load_weight<T>(a.weight, a.weight_fp32, u, w);
-#pragma unroll
-                for (int j = 0; j < kUnit; ++j) {
-                    sums[0] = fmaf(h[j], h[j], sums[0]);
-                    sums[1] = fmaf(dy[j] * w[j], h[j], sums[1]);
+        mbar_init_fence();
+    }
+    __syncthreads();
+    pdl_wait();
+    pdl_launch_next();
+
+    if (warp == kBackThreads / 32 - 1) {
+        // ---- copies ----
+        int s = 0, i = 0;
+        uint32_t parity = 0;
+        for (; i < mine; ++i) {
+            if (!mbar_wait_warp(smem_u32(&empty[s]), parity ^ 1, abort, kWaitEmptyB))
+                break;
+            const long long t = (blockIdx.x + static_cast<long long>(i) * gridDim.x) * a.rows;
+            const int rows = static_cast<int>(a.T - t < a.rows ? a.T - t : a.rows);
+            const uint32_t bar = smem_u32(&full[s]);
+            if (lane == 0)
+                mbar_expect(bar, row_bytes * rows * (has_dh ? 3 : 2));
+            __syncwarp();
+            for (int o = 0; o < (has_dh ? 3 : 2); ++o) {
+                const T *const from = static_cast<const T *>(o == 0 ? a.h : o == 1 ? a.dy : a.dh);
+                const long long stride = o == 0 ? a.h_stride : o == 1 ? a.dy_stride : a.dh_stride;
+                const uint32_t to = smem_u32(ring) + s * a.stage + o * a.rows * row_bytes;
+                if (stride == a.H) {
+                    if (lane == o)
+                        bulk_load_plain(to, from + t * stride, row_bytes * rows, bar);
+                } else {
+                    for (int r = lane; r < rows; r += 32)
+                        bulk_load_plain(to + r * row_bytes, from + (t + r) * stride, row_bytes, bar);
                 }
             }
+            if (++s == a.stages) {
+                s = 0;
+                parity ^= 1;
+            }
         }
-        row_sums<2>(sums, slots[turn], warps, warp, lane);
-        float rstd = rstd_of(sums[0], a.H, a.eps), mean = rstd * sums[1] / static_cast<float>(a.H);  // of g n
-        if (!isfinite(sums[0]) || !isfinite(sums[1])) {  // squares that exceed fp32; the same in all threads
-            float again[2] = {0.0f, 0.0f};
+        if (lane == 0)
+            issued_ = i;
+    } else if (team < a.teams) {
+        // ---- a team's rows ----
+        float2 acc[U][kPairs], w[U][kPairs];
 #pragma unroll
-            for (int i = 0; i < U; ++i) {
-                const int u = threadIdx.x + i * blockDim.x;
+        for (int k = 0; k < U; ++k) {
+            const int u = (k * a.team + place) * 32 + lane;
+#pragma unroll
+            for (int j = 0; j < kPairs; ++j)
+                acc[k][j] = w[k][j] = make_float2(0.0f, 0.0f);
+            if (u < units) {
+                float f[kUnit];
+                load_weight<T>(a.weight, a.weight_fp32, u, f);
+#pragma unroll
+                for (int j = 0; j < kPairs; ++j)
+                    w[k][j] = make_float2(f[2 * j], f[2 * j + 1]);
+            }
+        }
+        int turn = 0, s = 0;
+        uint32_t parity = 0;
+        bool run = true;
+        for (int i = 0; run && i < mine; ++i) {
+            run = mbar_wait(smem_u32(&full[s]), parity, abort, kWaitFullB);
+            run = a.team > 1 ? named_all(1 + team, a.team * 32, run) : __all_sync(~0u, run);
+            if (!run)
+                break;
+            const long long t0 = (blockIdx.x + static_cast<long long>(i) * gridDim.x) * a.rows;
+            const int rows = static_cast<int>(a.T - t0 < a.rows ? a.T - t0 : a.rows);
+            for (int row = team; row < rows; row += a.teams, turn ^= 1) {
+                const uint8_t *const at = ring + s * a.stage + row * row_bytes;
+                const uint32_t next = a.rows * row_bytes;  // operand
+                const Unit<T> *const h_at = reinterpret_cast<const Unit<T> *>(at) + place * 32 + lane;
+                const Unit<T> *const dy_at = reinterpret_cast<const Unit<T> *>(at + next) + place * 32 + lane;
+                const Unit<T> *const dh_at = reinterpret_cast<const Unit<T> *>(at + 2 * next) + place * 32 + lane;
+                Unit<T> rh[U], rdy[U];
+                float2 sums[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};  // of h^2 and of dy w h
+#pragma unroll
+                for (int k = 0; k < U; ++k)
+                    if ((k * a.team + place) * 32 + lane < units) {
+                        rh[k] = h_at[k * a.team * 32];
+                        rdy[k] = dy_at[k * a.team * 32];
+                        float2 h[kPairs], dy[kPairs];
+                        widen_pairs<T>(rh[k], h);
+                        widen_pairs<T>(rdy[k], dy);
+#pragma unroll
+                        for (int j = 0; j < kPairs; ++j) {
+                            sums[0] = fma2(h[j], h[j], sums[0]);
+                            sums[1] = fma2(mul2(dy[j], h[j]), w[k][j], sums[1]);
+                        }
+                    }
+                float sum[2] = {sums[0].x + sums[0].y, sums[1].x + sums[1].y};
+                team_sums(sum, slots[team][turn], a.team, place, team, lane);
+                float rstd = rstd_of(sum[0], a.H, a.eps), mean = rstd * sum[1] / static_cast<float>(a.H);  // of g n
+                if (!isfinite(sum[0]) || !isfinite(sum[1])) {  // squares that exceed fp32; the same in all threads of the team
+                    float again[2] = {0.0f, 0.0f};
+                    for (int u = place * 32 + lane; u < units; u += a.team * 32) {
+                        float h[kUnit], dy[kUnit], wu[kUnit];
+                        widen_unit<T>(h_at[u - place * 32 - lane], h);
+                        widen_unit<T>(dy_at[u - place * 32 - lane], dy);
+                        load_weight<T>(a.weight, a.weight_fp32, u, wu);
+#pragma unroll
+                        for (int j = 0; j < kUnit; ++j) {
+                            again[0] = fmaf(h[j] * kScaled, h[j] * kScaled, again[0]);
+                            again[1] = fmaf(dy[j] * wu[j], h[j] * kScaled, again[1]);
+                        }
+                    }
+                    const bool large = isinf(sum[0]);
+                    if (a.team > 1)
+                        named_sync(1 + team, a.team * 32);  // the slots are read
+                    team_sums(again, slots[team][turn], a.team, place, team, lane);
+                    if (large)
+                        rstd = rstd_scaled(again[0], a.H);
+                    mean = rstd / kScaled * again[1] / static_cast<float>(a.H);
+                }
+                const float2 r2 = make_float2(rstd, rstd);
+                // h r is n, which may be large where r^2 alone is too small for fp32
+                const float2 m2 = make_float2(-mean, -mean);
+                const long long t = t0 + row;
+                Unit<T> *const to = a.dx ? unit_at<T>(a.dx, a.dx_stride, t, place * 32 + lane) : nullptr;
+#pragma unroll
+                for (int k = 0; k < U; ++k)
+                    if ((k * a.team + place) * 32 + lane < units) {
+                        float2 h[kPairs], dy[kPairs], dx[kPairs];
+                        widen_pairs<T>(rh[k], h);
+                        widen_pairs<T>(rdy[k], dy);
+                        if (has_dh) {
+                            widen_pairs<T>(dh_at[k * a.team * 32], dx);
+                        } else {
+#pragma unroll
+                            for (int j = 0; j < kPairs; ++j)
+                                dx[j] = make_float2(0.0f, 0.0f);
+                        }
+#pragma unroll
+                        for (int j = 0; j < kPairs; ++j) {
+                            const float2 n = mul2(h[j], r2);
+                            acc[k][j] = fma2(dy[j], n, acc[k][j]);
+                            dx[j] = fma2(fma2(n, m2, mul2(dy[j], w[k][j])), r2, dx[j]);
+                        }
+                        if (to && EP_IN_BOUNDS(a.chk, epk::kSiteMoeOut, to + k * a.team * 32, sizeof(Unit<T>), a.dx, sizeof(T) * ((a.T - 1LL) * a.dx_stride + a.H))) {
+                            const float f[kUnit] = {dx[0].x, dx[0].y, dx[1].x, dx[1].y, dx[2].x, dx[2].y, dx[3].x, dx[3].y};
+                            store_unit<T>(to + k * a.team * 32, f);
+                        }
+                    }
+            }
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive(smem_u32(&empty[s]));
+            if (++s == a.stages) {
+                s = 0;
+                parity ^= 1;
+            }
+        }
+        if (a.parts) {  // the teams' sums, one after the other, where the ring was
+            float *const sums = reinterpret_cast<float *>(ring) + static_cast<size_t>(team) * a.H;
+            named_sync(15, a.teams * a.team * 32);  // all rows are read (or given up)
+#pragma unroll
+            for (int k = 0; k < U; ++k) {
+                const int u = (k * a.team + place) * 32 + lane;
                 if (u < units) {
-                    float h[kUnit], dy[kUnit], w[kUnit];
-                    widen_unit<T>(rh[i], h);
-                    widen_unit<T>(rdy[i], dy);
-                    load_weight<T>(a.weight, a.weight_fp32, u, w);
-#pragma unroll
-                    for (int j = 0; j < kUnit; ++j) {
-                        again[0] = fmaf(h[j] * kScaled, h[j] * kScaled, again[0]);
-                        again[1] = fmaf(dy[j] * w[j], h[j] * kScaled, again[1]);
-                    }
+                    const float f[kUnit] = {acc[k][0].x, acc[k][0].y, acc[k][1].x, acc[k][1].y,
+                                            acc[k][2].x, acc[k][2].y, acc[k][3].x, acc[k][3].y};
+                    store_unit<float>(reinterpret_cast<Raw32 *>(sums) + u, f);
                 }
             }
-            __syncthreads();
-            row_sums<2>(again, slots_again[turn], warps, warp, lane);
-            if (isinf(sums[0]))
-                rstd = rstd_scaled(again[0], a.H);
-            mean = rstd / kScaled * again[1] / static_cast<float>(a.H);
-        }
-#pragma unroll
-        for (int i = 0; i < U; ++i) {
-            const int u = threadIdx.x + i * blockDim.x;
-            if (u < units) {
-                float h[kUnit], dy[kUnit], w[kUnit], dx[kUnit];
-                widen_unit<T>(rh[i], h);
-                widen_unit<T>(rdy[i], dy);
-                load_weight<T>(a.weight, a.weight_fp32, u, w);
-#pragma unroll
-                for (int j = 0; j < kUnit; ++j) {
-                    const float n = h[j] * rstd;
-                    acc[i][j] = fmaf(dy[j], n, acc[i][j]);
-                    dx[j] = rstd * fmaf(-n, mean, dy[j] * w[j]);
-                }
-                if (a.dx) {
-                    if (a.dh) {
-                        float dh[kUnit];
-                        widen_unit<T>(rdh[i], dh);
-#pragma unroll
-                        for (int j = 0; j < kUnit; ++j)
-                            dx[j] += dh[j];
-                    }
-                    if (EP_IN_BOUNDS(a.chk, epk::kSiteMoeOut, unit_at<T>(a.dx, a.dx_stride, t, u), sizeof(Unit<T>), a.dx, sizeof(T) * ((a.T - 1LL) * a.dx_stride + a.H)))
-                        store_unit<T>(unit_at<T>(a.dx, a.dx_stride, t, u), dx);
-                }
+            named_sync(15, a.teams * a.team * 32);
+            for (int c = tid; c < a.H; c += a.teams * a.team * 32) {
+                float total = *abort ? __uint_as_float(0x7FC00000u) : 0.0f;
+                for (int r = 0; r < a.teams; ++r)
+                    total += reinterpret_cast<float *>(ring)[static_cast<size_t>(r) * a.H + c];
+                a.parts[static_cast<size_t>(blockIdx.x) * a.H + c] = total;
             }
         }
     }
-    if (!a.parts)
-        return;
-#pragma unroll
-    for (int i = 0; i < U; ++i) {
-        const int u = threadIdx.x + i * blockDim.x;
-        if (u < units)
-            store_unit<float>(reinterpret_cast<Raw32 *>(a.parts + static_cast<size_t>(blockIdx.x) * a.H) + u, acc[i]);
+    __syncthreads();
+    if (abort_ && tid == 0) {  // copies in flight land before the block's memory is given back
+        for (int i = max(0, issued_ - a.stages); i < issued_; ++i)
+            mbar_wait(smem_u32(&full[i % a.stages]), (i / a.stages) & 1, nullptr, kWaitOther);
     }
 }
 
@@ -373,6 +529,7 @@ __global__ void __launch_bounds__(1024) parts_kernel(const __grid_constant__ Nor
 {
     __shared__ float sums[32][33];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, col = blockIdx.x * 32 + lane;
+    pdl_wait();
     float s = 0.0f;
     if (col < a.H)
         for (int b = warp; b < blocks; b += 32)
@@ -392,45 +549,69 @@ struct Shape {
     int units, threads, rows;  // units of a thread, threads of a row, rows of a block
 };
 
-// Threads of a row: `u` units each, in whole warps. Short rows share a block.
-Shape shape_of(int H, int u, bool one_row)
+// Threads of a row: `u` units each, in whole warps. Rows of one warp share a block.
+Shape shape_of(int H, int u)
 {
     const int units = H / kUnit;
     Shape s;
     s.units = u;
     s.threads = ((units + u - 1) / u + 31) / 32 * 32;
-    s.rows = one_row || s.threads >= 128 ? 1 : 128 / s.threads;
+    s.rows = s.threads == 32 ? kNormRows : 1;
     return s;
+}
+
+// A launch whose blocks may start while the kernel before it ends; they wait for its end before they read anything.
+template <class... Args, class... Given>
+cudaError_t launch_early(void (*kernel)(Args...), dim3 grid, dim3 block, size_t smem, cudaStream_t stream, const Given &...args)
+{
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = block;
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
 template <class T> cudaError_t launch(const NormArgs &a, const Shape &s, cudaStream_t stream)
 {
     const dim3 grid(static_cast<unsigned>((a.T + static_cast<long long>(s.rows) - 1) / s.rows)), block(s.threads, s.rows);
-    if (s.units == 1)
-        norm_kernel<T, 1><<<grid, block, 0, stream>>>(a);
-    else if (s.units == 2)
-        norm_kernel<T, 2><<<grid, block, 0, stream>>>(a);
-    else
-        norm_kernel<T, 4><<<grid, block, 0, stream>>>(a);
-    return cudaGetLastError();
+    if constexpr (sizeof(T) == 2)
+        if (s.units == 4)
+            return launch_early(norm_kernel<T, 4>, grid, block, 0, stream, a);
+    return launch_early(s.units == 1 ? norm_kernel<T, 1> : norm_kernel<T, 2>, grid, block, 0, stream, a);
 }
 
-template <class T> cudaError_t launch_back(const NormBackArgs &a, const Shape &s, int blocks, cudaStream_t stream)
+template <class T> cudaError_t launch_back(NormBackArgs a, int *blocks, cudaStream_t stream)
 {
-    if (s.units == 1)
-        back_kernel<T, 1><<<blocks, s.threads, 0, stream>>>(a);
-    else
-        back_kernel<T, 2><<<blocks, s.threads, 0, stream>>>(a);
-    return cudaGetLastError();
+    const int row = a.H * static_cast<int>(sizeof(T)), copies = a.dx && a.dh ? 3 : 2;
+    const int lane_units = a.H > kFewUnits * 16 * 32 * kUnit ? kMostUnits : kFewUnits;
+    a.team = (a.H / kUnit + 32 * lane_units - 1) / (32 * lane_units);
+    a.teams = (kBackThreads / 32 - 1) / a.team;
+    // as many rows to a stage as there are teams, unless that leaves blocks without any
+    a.rows = (a.T - 1) / a.sms + 1 < a.teams ? (a.T - 1) / a.sms + 1 : a.teams;
+    a.stage = (copies * row * a.rows + 127) & ~127;
+    a.stages = kBackRing / a.stage < kBackStages ? kBackRing / a.stage : kBackStages;
+    const int groups = (a.T - 1) / a.rows + 1;
+    *blocks = groups < a.sms ? groups : a.sms;
+    const int ring = a.stages * a.stage, sums = a.teams * a.H * 4;  // sums: 64 KB at most
+    return launch_early(lane_units == kFewUnits ? back_kernel<T, kFewUnits> : back_kernel<T, kMostUnits>, dim3(*blocks), dim3(kBackThreads), 128 + (ring > sums ? ring : sums), stream, a);
 }
 
 }  // namespace
 
 cudaError_t launch_norm(const NormArgs &a, cudaStream_t stream)
 {
-    // Few rows: as many threads as there are units, for the shortest way through a row; many: 4 units a thread
-    const int least = (a.H / kUnit + 1023) / 1024, u = a.T <= 2 * a.sms ? (least > 1 ? 2 : 1) : 4;
-    const Shape s = shape_of(a.H, u, false);
+    // Few rows: as many threads as there are units, for the shortest way through a row. Many: units of a thread that
+    // keep a row's loads on their way at once and its warps few (bf16, 8-bit rows too: 16000 x 256 6.9, 8.3, 12.1 us
+    // with 1, 2, 4; 8000 x 2048 27.4, 24.6, 25.5; 16001 x 7168 290, 182, 152; fp32 with 4 does not fit the registers)
+    const int units = a.H / kUnit;
+    const int u = a.T <= 2 * a.sms ? (units > 1024 ? 2 : 1) : units <= 32 ? 1 : units <= 256 || a.dtype == EP_DTYPE_FP32 ? 2 : 4;
+    const Shape s = shape_of(a.H, u);
     switch (a.dtype) {
     case EP_DTYPE_BF16: return launch<__nv_bfloat16>(a, s, stream);
     case EP_DTYPE_FP16: return launch<__half>(a, s, stream);
@@ -438,32 +619,41 @@ cudaError_t launch_norm(const NormArgs &a, cudaStream_t stream)
     }
 }
 
-int norm_back_blocks(int T, int sms) { return T < 2 * sms ? T : 2 * sms; }
+int norm_back_blocks(int T, int sms) { return T < sms ? T : sms; }  // at most
 
 cudaError_t launch_norm_back(const NormBackArgs &a, cudaStream_t stream)
 {
-    const int blocks = norm_back_blocks(a.T, a.sms);
+    int blocks = norm_back_blocks(a.T, a.sms);
     cudaError_t ce = cudaSuccess;
     if (blocks > 0) {
-        const Shape s = shape_of(a.H, a.H / kUnit > 512 ? 2 : 1, true);
-        ce = a.dtype == EP_DTYPE_BF16   ? launch_back<__nv_bfloat16>(a, s, blocks, stream)
-             : a.dtype == EP_DTYPE_FP16 ? launch_back<__half>(a, s, blocks, stream)
-                                        : launch_back<float>(a, s, blocks, stream);
+        ce = a.dtype == EP_DTYPE_BF16   ? launch_back<__nv_bfloat16>(a, &blocks, stream)
+             : a.dtype == EP_DTYPE_FP16 ? launch_back<__half>(a, &blocks, stream)
+                                        : launch_back<float>(a, &blocks, stream);
     }
     if (ce == cudaSuccess && a.dweight) {
-        parts_kernel<<<(a.H + 31) / 32, 1024, 0, stream>>>(a, blocks);
-        ce = cudaGetLastError();
+        ce = launch_early(parts_kernel, dim3((a.H + 31) / 32), dim3(1024), 0, stream, a, blocks);
     }
+    return ce;
+}
+
+// The backward kernels' shared memory, on the current device.
+cudaError_t norm_setup()
+{
+    cudaError_t ce = cudaSuccess;
+    for (const auto k : {back_kernel<__nv_bfloat16, kFewUnits>, back_kernel<__half, kFewUnits>, back_kernel<float, kFewUnits>,
+                         back_kernel<__nv_bfloat16, kMostUnits>, back_kernel<__half, kMostUnits>, back_kernel<float, kMostUnits>})
+        if (ce == cudaSuccess)
+            ce = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kBackRing + 128);
     return ce;
 }
 
 std::vector<const void *> norm_kernels()
 {
-#define NORM(T)                                                                                             \
-    reinterpret_cast<const void *>(norm_kernel<T, 1>), reinterpret_cast<const void *>(norm_kernel<T, 2>),   \
-        reinterpret_cast<const void *>(norm_kernel<T, 4>), reinterpret_cast<const void *>(back_kernel<T, 1>), \
-        reinterpret_cast<const void *>(back_kernel<T, 2>)
-    return {NORM(__nv_bfloat16), NORM(__half), NORM(float), reinterpret_cast<const void *>(parts_kernel)};
+#define NORM(T)                                                                                           \
+    reinterpret_cast<const void *>(norm_kernel<T, 1>), reinterpret_cast<const void *>(norm_kernel<T, 2>), \
+        reinterpret_cast<const void *>(back_kernel<T, kFewUnits>), reinterpret_cast<const void *>(back_kernel<T, kMostUnits>)
+    return {NORM(__nv_bfloat16), NORM(__half), NORM(float), reinterpret_cast<const void *>(norm_kernel<__nv_bfloat16, 4>),
+            reinterpret_cast<const void *>(norm_kernel<__half, 4>), reinterpret_cast<const void *>(parts_kernel)};
 #undef NORM
 }
 

@@ -379,9 +379,11 @@ class EpNorm(_OnDevice):
         self._L = _lib.load()
         self._cfg = _lib.EpNormConfigC(self.hidden, _NORM_DTYPES[self.dtype], _NORM_DTYPES[weight.dtype], float(eps),
                                        weight.data_ptr())
-        need = ctypes.c_size_t(0)  # also checks the configuration
+        need = ctypes.c_size_t(0)  # of the largest call; this also checks the configuration
         with torch.cuda.device(self.device):
-            check(self._L.ep_norm_backward_workspace_size(ctypes.byref(self._cfg), 1, ctypes.byref(need)))
+            check(self._L.ep_norm_backward_workspace_size(self._cfg, 0x7FFFFFFF, ctypes.byref(need)))
+        self._back_bytes = need.value
+        self._groups = -(-self.hidden // _lib.EP_SCALE_GROUP)
 
     def __call__(self, x: torch.Tensor, residual: Optional[torch.Tensor] = None, plain: bool = True,
                  quantized: bool = False, out: Optional[torch.Tensor] = None,
@@ -391,28 +393,29 @@ class EpNorm(_OnDevice):
 
         ``out`` and ``residual_out``, if given, receive the results; both may be ``x`` or ``residual``."""
         n, stride = self._rows(x, self.hidden, self.dtype)
-        r = _lib.EpNormRowsC(x=x.data_ptr(), x_stride=stride)
+        r = r_stride = ro = ro_stride = o = o_stride = q_at = scales_at = 0
         if residual is not None:
-            m, r.residual_stride = self._rows(residual, self.hidden, self.dtype, "residual")
+            m, r_stride = self._rows(residual, self.hidden, self.dtype, "residual")
             if m != n:
                 raise ValueError(f"residual must have {n} rows, got {m}")
-            r.residual = residual.data_ptr()
-            residual_out, r.residual_out_stride = self._out(residual_out, n, self.hidden, self.dtype, "residual_out")
-            r.residual_out = residual_out.data_ptr()
+            r = residual.data_ptr()
+            residual_out, ro_stride = self._out(residual_out, n, self.hidden, self.dtype, "residual_out")
+            ro = residual_out.data_ptr()
         elif residual_out is not None:
             raise ValueError("residual_out without residual")
         if plain:
-            out, r.out_stride = self._out(out, n, self.hidden, self.dtype)
-            r.out = out.data_ptr()
+            out, o_stride = self._out(out, n, self.hidden, self.dtype)
+            o = out.data_ptr()
         elif out is not None:
             raise ValueError("out without plain")
         q = scales = None
         if quantized:
             q = torch.empty((n, self.hidden), dtype=torch.float8_e4m3fn, device=self.device)
-            scales = torch.empty((n, -(-self.hidden // _lib.EP_SCALE_GROUP)), dtype=torch.float32, device=self.device)
-            r.q, r.scales = q.data_ptr(), scales.data_ptr()
+            scales = torch.empty((n, self._groups), dtype=torch.float32, device=self.device)
+            q_at, scales_at = q.data_ptr(), scales.data_ptr()
         if n:
-            self._run_on(self._L.ep_norm_run, self._cfg, r, n)
+            rows = _lib.EpNormRowsC(x.data_ptr(), stride, r, r_stride, ro, ro_stride, o, o_stride, q_at, scales_at)
+            self._run_on(self._L.ep_norm_run, self._cfg, rows, n)
         return EpNormResult(out, residual_out, q, scales)
 
     def backward(self, dy: torch.Tensor, h: torch.Tensor, dh: Optional[torch.Tensor] = None,
@@ -434,12 +437,9 @@ class EpNorm(_OnDevice):
             args += [t.data_ptr(), stride]
         dx, stride = self._out(dx, n, self.hidden, self.dtype, "dx")
         dweight = torch.empty(self.hidden, dtype=torch.float32, device=self.device)
-        need = ctypes.c_size_t(0)
-        with torch.cuda.device(self._index):
-            check(self._L.ep_norm_backward_workspace_size(self._cfg, n, ctypes.byref(need)))
-        ws = torch.empty(need.value, dtype=torch.uint8, device=self.device)
+        ws = torch.empty(self._back_bytes, dtype=torch.uint8, device=self.device)
         self._run_on(self._L.ep_norm_backward, self._cfg, *args, n, dx.data_ptr(), stride, dweight.data_ptr(),
-                     ws.data_ptr(), need.value)
+                     ws.data_ptr(), self._back_bytes)
         return dx, dweight
 
 
@@ -463,6 +463,7 @@ class EpFfn(_Handle):
                    _weight("down", down, self.dtype, (self.hidden, self.intermediate), device))
         self._open(device)
         cfg = _lib.EpFfnConfigC(self.hidden, self.intermediate, gate_up.data_ptr(), down.data_ptr())
+        self._sized = -1, -1, 0  # call, tokens and bytes of the last workspace
         h = ctypes.c_void_p()
         with torch.cuda.device(device):
             check(self._L.ep_ffn_create(ctypes.byref(cfg), ctypes.byref(h)))
@@ -470,10 +471,13 @@ class EpFfn(_Handle):
 
     def _workspace(self, call: int, n: int) -> Tuple[Optional[torch.Tensor], int, int]:
         """A call's workspace: the tensor, its address and its bytes."""
-        size = ctypes.c_size_t(0)
-        check(self._L.ep_ffn_workspace_size(self._live(), call, n, ctypes.byref(size)))
-        ws = torch.empty(size.value, dtype=torch.uint8, device=self.device)
-        return ws, ws.data_ptr(), size.value
+        if self._sized[:2] != (call, n):
+            size = ctypes.c_size_t(0)
+            check(self._L.ep_ffn_workspace_size(self._live(), call, n, ctypes.byref(size)))
+            self._sized = call, n, size.value
+        size = self._sized[2]
+        ws = torch.empty(size, dtype=torch.uint8, device=self.device)
+        return ws, ws.data_ptr(), size
 
     def __call__(self, x: torch.Tensor, out: Optional[torch.Tensor] = None) -> torch.Tensor:
         """``x`` bf16 [tokens, hidden] -> bf16 [tokens, hidden] (``out`` if given)."""

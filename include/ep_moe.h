@@ -289,7 +289,7 @@ typedef enum {
 ep_status ep_ffn_create(const ep_ffn_config *cfg, ep_ffn **out);
 
 /* Bytes of device workspace such a call with num_tokens rows needs (may be 0). */
-ep_status ep_ffn_workspace_size(const ep_ffn *h, ep_ffn_call call, int num_tokens, size_t *bytes);
+ep_status ep_ffn_workspace_size(ep_ffn *h, ep_ffn_call call, int num_tokens, size_t *bytes);
 
 /* x, out: device bf16 [num_tokens, hidden], rows x_stride / out_stride
  * elements apart (x_stride a multiple of 8, both >= hidden), x 16-byte aligned. saved: NULL, or
