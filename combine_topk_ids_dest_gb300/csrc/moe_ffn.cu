@@ -365,6 +365,7 @@ template <int EPI, bool GRAD> __global__ void __launch_bounds__(128 + kPairStore
         const auto part_of = [&](int p) { return q.parts + (static_cast<size_t>(2 * p + rank) * 256) * 128 + quarter * 32 + lane; };
         int sent = 0;
         Item it;
+        pdl_wait();  // flags, and what is fetched ahead of the sums, are the kernel's before until then
         for (Items w(q, pair); w.next(it);) {
             const FfnArgs &a = q.p[GRAD ? it.g : 0];
             const int steps = a.tile_n / 16;

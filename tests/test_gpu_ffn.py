@@ -49,3 +49,45 @@ def test_training(cuda_device, T, H, I):
     for name, got, (g, e) in zip(("dx", "dgate_up", "ddown"), grads, block_ref.ffn_back(dy, state)):
         assert got.dtype is torch.bfloat16 and got.shape == g.shape
         block_ref.check(got, g, e, name)
+
+
+# sizes whose launches have rounds that are cut over the pairs: parts of 1 to 4 blocks a tile, several products at once
+CUT = [(515, 4096, 14336), (300, 7168, 2048), (1999, 2056, 1400), (700, 1024, 9000), (4100, 1032, 2504)]
+
+
+@pytest.mark.parametrize("T,H,I", CUT)
+def test_cut_rounds(cuda_device, T, H, I):
+    x, gate_up, down, dy = make(T, H, I, seed=T)
+    ffn = EpFfn(gate_up, down)
+    want, err, state = block_ref.ffn(x, gate_up, down)
+    y = ffn(x)
+    block_ref.check(y, want, err, "y")
+    y2, saved = ffn.forward(x)
+    assert torch.equal(y, y2)
+    grads = ffn.backward(dy, x, saved)
+    for name, got, (g, e) in zip(("dx", "dgate_up", "ddown"), grads, block_ref.ffn_back(dy, state)):
+        block_ref.check(got, g, e, name)
+
+
+@pytest.mark.parametrize("T,H,I", [(515, 4096, 14336), (300, 7168, 2048), (1999, 2056, 1400), (128, 7168, 2048), (1, 4096, 4096)])
+def test_calls_in_a_row_do_not_meet(cuda_device, T, H, I):
+    """Kernels of calls that follow one another overlap: every call's results are those of a call alone, bit for bit."""
+    a, b = make(T, H, I, seed=1), make(T, H, I, seed=2)
+    ffns = [EpFfn(t[1], t[2]) for t in (a, b)]
+    alone = []
+    for f, t in zip(ffns, (a, b)):
+        y, saved = f.forward(t[0])
+        torch.cuda.synchronize()
+        grads = f.backward(t[3], t[0], saved)
+        torch.cuda.synchronize()
+        alone.append((y, saved, *grads))
+    got = []
+    for i in (0, 0, 1, 0, 1, 1, 0, 1):  # nothing waits between
+        t = (a, b)[i]
+        y = ffns[i](t[0])
+        y2, saved = ffns[i].forward(t[0])
+        got.append((i, y, y2, saved, *ffns[i].backward(t[3], t[0], saved)))
+    for i, y, *rest in got:
+        assert torch.equal(y, alone[i][0])
+        for x, want in zip(rest, alone[i]):
+            assert torch.equal(x, want)
