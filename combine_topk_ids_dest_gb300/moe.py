@@ -383,6 +383,7 @@ class EpNorm(_OnDevice):
         with torch.cuda.device(self.device):
             check(self._L.ep_norm_backward_workspace_size(self._cfg, 0x7FFFFFFF, ctypes.byref(need)))
         self._back_bytes = need.value
+        self._run, self._run_back = self._L.ep_norm_run, self._L.ep_norm_backward
         self._groups = -(-self.hidden // _lib.EP_SCALE_GROUP)
 
     def __call__(self, x: torch.Tensor, residual: Optional[torch.Tensor] = None, plain: bool = True,
@@ -392,30 +393,38 @@ class EpNorm(_OnDevice):
         what ``EpComm.dispatch`` takes as 8-bit rows), and with ``residual`` the sum ``x + residual``.
 
         ``out`` and ``residual_out``, if given, receive the results; both may be ``x`` or ``residual``."""
-        n, stride = self._rows(x, self.hidden, self.dtype)
+        hidden, dtype = self.hidden, self.dtype
+        n, stride = self._rows(x, hidden, dtype)
+        like = x if stride == hidden else None  # what new rows look like
         r = r_stride = ro = ro_stride = o = o_stride = q_at = scales_at = 0
         if residual is not None:
-            m, r_stride = self._rows(residual, self.hidden, self.dtype, "residual")
+            m, r_stride = self._rows(residual, hidden, dtype, "residual")
             if m != n:
                 raise ValueError(f"residual must have {n} rows, got {m}")
             r = residual.data_ptr()
-            residual_out, ro_stride = self._out(residual_out, n, self.hidden, self.dtype, "residual_out")
+            if residual_out is None and like is not None:
+                residual_out, ro_stride = torch.empty_like(like), hidden
+            else:
+                residual_out, ro_stride = self._out(residual_out, n, hidden, dtype, "residual_out")
             ro = residual_out.data_ptr()
         elif residual_out is not None:
             raise ValueError("residual_out without residual")
         if plain:
-            out, o_stride = self._out(out, n, self.hidden, self.dtype)
+            if out is None and like is not None:
+                out, o_stride = torch.empty_like(like), hidden
+            else:
+                out, o_stride = self._out(out, n, hidden, dtype)
             o = out.data_ptr()
         elif out is not None:
             raise ValueError("out without plain")
         q = scales = None
         if quantized:
-            q = torch.empty((n, self.hidden), dtype=torch.float8_e4m3fn, device=self.device)
+            q = torch.empty((n, hidden), dtype=torch.float8_e4m3fn, device=self.device)
             scales = torch.empty((n, self._groups), dtype=torch.float32, device=self.device)
             q_at, scales_at = q.data_ptr(), scales.data_ptr()
         if n:
-            rows = _lib.EpNormRowsC(x.data_ptr(), stride, r, r_stride, ro, ro_stride, o, o_stride, q_at, scales_at)
-            self._run_on(self._L.ep_norm_run, self._cfg, rows, n)
+            self._run_on(self._run, self._cfg, _lib.EpNormRowsC(x.data_ptr(), stride, r, r_stride, ro, ro_stride, o, o_stride,
+                                                                q_at, scales_at), n)
         return EpNormResult(out, residual_out, q, scales)
 
     def backward(self, dy: torch.Tensor, h: torch.Tensor, dh: Optional[torch.Tensor] = None,
@@ -438,7 +447,7 @@ class EpNorm(_OnDevice):
         dx, stride = self._out(dx, n, self.hidden, self.dtype, "dx")
         dweight = torch.empty(self.hidden, dtype=torch.float32, device=self.device)
         ws = torch.empty(self._back_bytes, dtype=torch.uint8, device=self.device)
-        self._run_on(self._L.ep_norm_backward, self._cfg, *args, n, dx.data_ptr(), stride, dweight.data_ptr(),
+        self._run_on(self._run_back, self._cfg, *args, n, dx.data_ptr(), stride, dweight.data_ptr(),
                      ws.data_ptr(), self._back_bytes)
         return dx, dweight
 
