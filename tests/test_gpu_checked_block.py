@@ -11,8 +11,8 @@ import sys
 import pytest
 import torch
 
-from combine_topk_ids_dest_gb300 import EpFfn, EpNorm, _lib
-from test_gpu_checked import in_checked_child
+from combine_topk_ids_dest_gb300 import EpError, EpFfn, EpNorm, _lib
+from test_gpu_checked import _trim, in_checked_child
 from test_gpu_checked_moe import ROOT, _reported
 from test_gpu_ffn import make as make_ffn
 from test_gpu_norm import make as make_norm
@@ -52,14 +52,20 @@ def test_trimmed_norm_results_are_reported_and_skipped(cuda_device):
 
 
 @in_checked_child
-@pytest.mark.parametrize("T,each", [(5, 4), (1100, 1)])
-def test_trimmed_ffn_results_are_reported_and_skipped(cuda_device, T, each):
-    """Few rows: four columns a store; many: one by one."""
+@pytest.mark.parametrize("T", [5, 1100, 4000])
+def test_trimmed_ffn_results_are_reported_and_skipped(cuda_device, T):
     x, gate_up, down, dy = make_ffn(T, 520, 1032)
     ffn = EpFfn(gate_up, down)
     want = ffn(x)
     out = torch.full_like(want, 7.0)
-    _reported("moe_out", 520 * 2, 520 // each, "moe: output row", lambda: ffn(x, out=out))
+    _trim("moe_out", 520 * 2)
+    try:
+        with pytest.raises(EpError) as e:
+            ffn(x, out=out)
+    finally:
+        _trim("", 0)
+    # four columns a store of a split's blocks, one of a pair's
+    assert re.search(r"\b(130|520) device accesses", str(e.value)) and "moe: output row" in str(e.value), str(e.value)
     assert torch.equal(out[:-1], want[:-1]) and bool((out[-1] == 7.0).all())
     _, saved = ffn.forward(x)
     dx = ffn.backward(dy, x, saved)[0]
