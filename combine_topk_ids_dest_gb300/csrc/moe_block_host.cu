@@ -392,6 +392,7 @@ void plan(ep_ffn *h, int num_tokens, Launch &w)
     q.bytes = k.bytes;
     q.whole = k.whole;
     q.cut = k.cut;
+    q.late = k.late;
     memcpy(q.begin, k.begin, sizeof(q.begin));
     w.l.split = kept.l.split;
     w.l.parts = kept.l.parts;

@@ -21,12 +21,11 @@
 //  - pairs: two neighbouring blocks multiply together (cta_group::2), 256
 //    features x up to 256 rows a tile, persistent, accumulators in two halves of
 //    tensor memory, so that one tile's epilogue runs under the next one's MMAs.
-//    A launch has up to three products (the three that follow the split). Whole
-//    tiles go round the pairs; the last one or two rounds are cut evenly along K
-//    over all of them, so that no round is left half empty. A tile that pairs
-//    share: all but the last one's sums go through memory, written first of all
-//    a pair does, and the last pair, which ends with it, adds them in the order of
-//    K. Waits go to lower pairs only;
+//    The three products that follow the split are one launch: whole tiles go
+//    round the pairs, the last one or two rounds are cut evenly along K over all of
+//    them. A tile that pairs share: all but the last one's sums go through memory;
+//    the last pair, which ends with it, puts them into tensor memory and adds its
+//    own there, in the order of K. Waits go to lower pairs only;
 //  - splits: for few tiles. A block has 128 features, a cluster of 1 to 8 blocks
 //    shares a tile's K. Their sums meet in distributed shared memory, added in
 //    the order of K, a share of the rows in each block.
@@ -58,7 +57,7 @@ static __host__ __device__ constexpr int features_of(int epi) { return epi == kF
 struct Shared {
     uint64_t full[kMaxStages], empty[kMaxStages];
     uint64_t full_d[2], empty_d[2];
-    uint64_t drain;
+    uint64_t drain, loaded;
     uint32_t tmem;
     int abort, issued, reset;
 };
@@ -174,6 +173,7 @@ static __device__ __forceinline__ void set_barriers(Shared &sh, int storers)
         mbar_init(smem_u32(&sh.empty_d[i]), storers);
     }
     mbar_init(smem_u32(&sh.drain), 1);
+    mbar_init(smem_u32(&sh.loaded), storers);
     mbar_init_fence();
 }
 
@@ -325,6 +325,9 @@ template <int EPI, bool GRAD> __global__ void __launch_bounds__(128 + kPairStore
             const int tile_n = __shfl_sync(~0u, a.tile_n, 0), b_mn = GRAD ? __shfl_sync(~0u, a.b_mn, 0) : 0;
             run = mbar_wait_warp(smem_u32(&sh.empty_d[at_d.s]), at_d.parity ^ 1, abort, kWaitEmptyD);
             const uint32_t d = tmem + at_d.s * kHalfTmem;
+            const bool add = GRAD && it.kind == kLast;  // to the sums of the tile's other parts
+            if (run && add)
+                run = mbar_wait_warp(smem_u32(&sh.loaded), 0, abort, kWaitDone);
             for (int c = it.c0; run && c < it.c1; ++c) {
                 run = mbar_wait_warp(smem_u32(&sh.full[at.s]), at.parity, abort, kWaitFullA);
                 if (!run)
@@ -332,9 +335,9 @@ template <int EPI, bool GRAD> __global__ void __launch_bounds__(128 + kPairStore
                 tc_fence_after();
                 if (elect_one()) {
                     if (GRAD && b_mn)
-                        multiply<A_MN, true, true>(d, ring + at.s * q.bytes, tile_n, c > it.c0);
+                        multiply<A_MN, true, true>(d, ring + at.s * q.bytes, tile_n, add || c > it.c0);
                     else
-                        multiply<A_MN, false, true>(d, ring + at.s * q.bytes, tile_n, c > it.c0);
+                        multiply<A_MN, false, true>(d, ring + at.s * q.bytes, tile_n, add || c > it.c0);
                     tc_commit_pair(smem_u32(&sh.empty[at.s]));
                 }
                 at.next(q.stages);
@@ -363,8 +366,49 @@ template <int EPI, bool GRAD> __global__ void __launch_bounds__(128 + kPairStore
                                 (turn * 2 + (quarter & 1)) * 512 + lane;  // [gate, up][8][32]
         // a block's part of a tile: [row][128 MMA rows]
         const auto part_of = [&](int p) { return q.parts + (static_cast<size_t>(2 * p + rank) * 256) * 128 + quarter * 32 + lane; };
-        int sent = 0;
-        Item it;
+        // The sums of the other parts of the tile that this pair ends go into tensor memory, where its own are added:
+        // under the item before, unless that is this pair's part, for which others may be waiting.
+        Item it, last;
+        int left = -1;  // items before they are loaded
+        if (Items w(q, pair); GRAD && w.last(last)) {
+            int before = kPart, at = 0;
+            while (w.next(it) && it.kind != kLast) {
+                before = it.kind;
+                ++at;
+            }
+            left = before == kPart ? at : at - 1;
+        }
+        auto load_parts = [&](uint32_t d) {
+            Items w(q, pair);
+            bool run = true;
+            if (tid == kFirstStore * 32)
+                for (int p = w.first_of_last(); run && p < pair; ++p)
+                    if (q.begin[p] < q.begin[p + 1])
+                        run = wait_count(q.flags + 2 * p + rank, 1, abort, kWaitDone);
+            if (!named_all(1, kPairStore, run))
+                return false;
+            for (int step = turn; step < q.p[GRAD ? last.g : 0].tile_n / 16; step += 4) {
+                float v[16];
+#pragma unroll
+                for (int r = 0; r < 16; ++r)
+                    v[r] = 0.0f;
+                for (int p = w.first_of_last(); p < pair; ++p)
+                    if (q.begin[p] < q.begin[p + 1]) {
+                        const float *const part = part_of(p) + step * 16 * 128;
+#pragma unroll
+                        for (int r = 0; r < 16; ++r)
+                            v[r] += __ldcg(part + r * 128);
+                    }
+                tmem_st16(d + step * 16, v);
+            }
+            tmem_wait_st();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive_cluster(in_first_block(smem_u32(&sh.loaded)));
+            return true;
+        };
+        int sent = 0, items = 0;
         pdl_wait();  // flags, and what is fetched ahead of the sums, are the kernel's before until then
         for (Items w(q, pair); w.next(it);) {
             const FfnArgs &a = q.p[GRAD ? it.g : 0];
@@ -387,39 +431,20 @@ template <int EPI, bool GRAD> __global__ void __launch_bounds__(128 + kPairStore
                         }
                 }
             };
-            const int p0 = it.kind == kLast ? w.first_of_last() : pair;
-            float before[16];  // the sums of the tile's other parts
-            auto fetch_parts = [&](int step) {
-#pragma unroll
-                for (int r = 0; r < 16; ++r)
-                    before[r] = 0.0f;
-                if (step < steps)
-                    for (int p = p0; p < pair; ++p)
-                        if (q.begin[p] < q.begin[p + 1]) {
-                            const float *const part = part_of(p) + step * 16 * 128;
-#pragma unroll
-                            for (int r = 0; r < 16; ++r)
-                                before[r] += __ldcg(part + r * 128);
-                        }
-            };
             bool run = true;
-            if (it.kind == kLast) {
-                if (tid == kFirstStore * 32)
-                    for (int p = p0; run && p < pair; ++p)
-                        if (q.begin[p] < q.begin[p + 1])
-                            run = wait_count(q.flags + 2 * p + rank, 1, abort, kWaitDone);
-                if (!named_all(1, kPairStore, run))
+            if (GRAD && items++ == left) {  // the last item's half of tensor memory is this one's, or the other
+                const int half = at_d.s ^ (it.kind == kLast ? 0 : 1);
+                run = load_parts(tmem + (static_cast<uint32_t>(quarter) << 21) + half * kHalfTmem);
+                if (!run)
                     break;
-                fetch_parts(turn);
             }
-            if (it.kind != kPart)
-                fetch(turn);
+            fetch(turn);
             run = mbar_wait(smem_u32(&sh.full_d[at_d.s]), at_d.parity, abort, kWaitFullD);
             if (!named_all(1, kPairStore, run))
                 break;
             tc_fence_after();
             const uint32_t d = tmem + (static_cast<uint32_t>(quarter) << 21) + at_d.s * kHalfTmem;
-            if (it.kind == kPart) {
+            if (GRAD && it.kind == kPart) {
                 float *const part = part_of(pair);
                 for (int step = turn; step < steps; step += 4) {
                     float v[16];
@@ -438,12 +463,6 @@ template <int EPI, bool GRAD> __global__ void __launch_bounds__(128 + kPairStore
                     float v[16];
                     tmem_ld16(d + step * 16, v);
                     tmem_wait_ld();
-                    if (it.kind == kLast) {
-#pragma unroll
-                        for (int r = 0; r < 16; ++r)
-                            v[r] = before[r] + v[r];
-                        fetch_parts(step + 4);
-                    }
                     if (EPI == kFfnJoin) {
 #pragma unroll
                         for (int r = 0; r < 8; ++r)
@@ -551,7 +570,7 @@ template <int EPI, bool GRAD> __global__ void __launch_bounds__(128 + kPairStore
     if (warp == 1)
         tmem_free<true>(tmem, 2 * kHalfTmem);
     cluster_sync();  // the other block's copies and arrivals have come
-    if (q.cut) {     // the last block to leave clears the flags for the next launch
+    if (GRAD && q.cut) {  // the last block to leave clears the flags for the next launch
         if (tid == 0)
             sh.reset = add_acq_rel(q.flags + 2 * kFfnMaxPairs, 1) == static_cast<int>(gridDim.x) - 1;
         __syncthreads();
@@ -759,7 +778,6 @@ double chunk_cycles(int n, bool pair)
 struct Choice {
     double cost;
     int n, split;  // split 0: pairs
-    bool cut;      // the last rounds of the pairs
 };
 
 // All operands come from DRAM once, whoever asks for them.
@@ -768,17 +786,14 @@ double dram_cycles(const FfnArgs &a, int epilogue)
     return 2.0 * a.K * (static_cast<double>(a.M) * (epilogue == kFfnJoin ? 2 : 1) + a.N) / 3500.0;
 }
 
-// Cycles of a product's pairs with tiles of n rows: all rounds whole, or evenly cut (which costs the parts' way through
-// memory); a tile's epilogue is hidden if its products take as long.
+// Cycles of a product's pairs with tiles of n rows: rounds of whole tiles, whose epilogue is hidden if their products
+// take as long.
 Choice pair_choice(const FfnArgs &a, int epilogue, int n, int sms)
 {
-    const double pairs = sms / 2, tiles = static_cast<double>(div_up(a.N, n)) * div_up(a.M, 2 * features_of(epilogue));
-    const double products = a.chunks * chunk_cycles(n, true) + 200, store = 20.0 * n;
-    const double tile = products > store ? products : store;
-    const double parts = pairs > tiles ? pairs / tiles : 1.0;
-    const double whole = std::ceil(tiles / pairs) * tile, even = tiles / pairs * tile + 3000 + 3000 * parts;
-    const double best = whole < even ? whole : even, dram = dram_cycles(a, epilogue);
-    return {(best > dram ? best : dram) + 5000 + 10.0 * n, n, 0, even < whole};
+    const double tiles = static_cast<double>(div_up(a.N, n)) * div_up(a.M, 2 * features_of(epilogue));
+    const double products = a.chunks * chunk_cycles(n, true) + 200, store = 20.0 * n, dram = dram_cycles(a, epilogue);
+    const double cost = std::ceil(tiles / (sms / 2)) * (products > store ? products : store);
+    return {(cost > dram ? cost : dram) + 7000 + 10.0 * n, n, 0};
 }
 
 // A cluster's sums meet at a cost that grows with its blocks. A block alone on its SM leaves no room for the next kernel's
@@ -791,7 +806,7 @@ Choice split_choice(const FfnArgs &a, int epilogue, int n, int split, int sms)
     const double cost = std::ceil(blocks / sms) * div_up(a.chunks, split) * chunk;
     const double after = std::ceil(blocks / (share ? 2 * sms : sms)) * (3000.0 + n * (8.0 + 4.0 * split));
     const double dram = dram_cycles(a, epilogue);
-    return {(cost > dram ? cost : dram) + after + (share ? 0.0 : 1500.0), n, split, false};
+    return {(cost > dram ? cost : dram) + after + (share ? 0.0 : 800.0), n, split};
 }
 
 template <class F> Choice least(const FfnArgs &a, F &&cost)
@@ -799,7 +814,7 @@ template <class F> Choice least(const FfnArgs &a, F &&cost)
     // Of rows that lie along memory a pair's halves are whole lines: 128 rows or 256. Other heights read up to twice as
     // much (the gradients of 1999 rows, 2056 x 1400: 51 us instead of 33).
     const int step = a.b_mn ? 128 : 16;
-    Choice best = {-1.0, step, 0, false};
+    Choice best = {-1.0, step, 0};
     for (int n = step; n <= 256; n += step) {
         if (n > step && div_up(a.N, n - step) == div_up(a.N, n))
             continue;  // the same tiles with more waste
@@ -820,6 +835,7 @@ void cut_rounds(FfnGroup *q, bool cut)
         tiles += q->p[g].m_tiles * q->p[g].n_tiles;
     // a last round of few tiles is cut together with the one before: a tile has few parts
     const int rounds = tiles / pairs, rest_tiles = tiles % pairs;
+    q->late = rounds > 8;  // with many rounds, tiles that run side by side share what they read
     q->whole = !cut ? tiles : (rest_tiles * 3 >= pairs || rounds == 0 ? rounds : rounds - 1) * pairs;
     double units[kFfnMaxPairs] = {}, all = 0.0;
     int left = q->whole, first = 0;
@@ -885,14 +901,15 @@ void ffn_plan(FfnLaunch *l, int sms)
     FfnGroup &q = l->q;
     q.pairs = sms / 2 < kFfnMaxPairs ? sms / 2 : kFfnMaxPairs;
     const bool grad = q.p[0].a_mn && l->epilogue == kFfnStore;  // dx, or the weights' gradients: pairs
-    bool cut = q.count > 1;
+    // Several products of different K are balanced by cutting. One is not: pairs that go through K out of step read the
+    // weights once for each tile of rows (y of 515 rows, 4096 x 14336: 50 us over all pairs, 45 over 64 of 76 in step).
+    const bool cut = q.count > 1;
     l->split = 0;
     for (int g = 0; g < q.count; ++g) {
         FfnArgs &a = q.p[g];
         a.chunks = div_up(a.K, kChunk);
         Choice c = least(a, [&](int n) { return pair_choice(a, l->epilogue, n, 2 * q.pairs); });
         if (q.count == 1) {
-            cut = c.cut;
             for (int split = 1; !grad && split <= 8 && split <= a.chunks; split *= 2) {
                 const Choice s = least(a, [&](int n) { return split_choice(a, l->epilogue, n, split, sms); });
                 if (s.cost < c.cost)

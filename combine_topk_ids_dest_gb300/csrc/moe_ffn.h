@@ -24,9 +24,9 @@ struct Item {
     int g, tile, c0, c1, kind;
 };
 
-// In the order in which all roles go through it: whole tiles, every pairs-th, so that pairs that share operands read them
-// at the same time; the first part of a tile that later pairs end; tiles cut out of the last rounds in full; the last part
-// of a tile that earlier pairs began, whose parts are there by then.
+// In the order in which all roles go through it: whole tiles, every pairs-th; the first part of a tile that later pairs end
+// (before the whole ones unless q.late); tiles cut out of the last rounds in full; the last part of a tile that earlier
+// pairs began.
 struct Items {
     const FfnGroup &q;
     const int pair;
@@ -54,10 +54,28 @@ struct Items {
         at_t = q.p[at_g].whole + u / q.p[at_g].chunks;
         at_c = u % q.p[at_g].chunks;
     }
+    __host__ __device__ __forceinline__ bool part(Item &it) const
+    {
+        if (!any || ce == 0)
+            return false;
+        it = {ge, te, gb == ge && tb == te ? cb : 0, ce, kPart};
+        return true;
+    }
+    __host__ __device__ __forceinline__ bool last(Item &it) const
+    {
+        if (!any || cb == 0 || (gb == ge && tb == te))  // all of the share is in one tile
+            return false;
+        it = {gb, tb, cb, q.p[gb].chunks, kLast};
+        return true;
+    }
     __host__ __device__ __forceinline__ bool next(Item &it)
     {
-        const bool one = gb == ge && tb == te;  // all of the share is in one tile
         if (phase == 0) {
+            phase = 1;
+            if (!q.late && part(it))
+                return true;
+        }
+        if (phase == 1) {
             if (t < q.whole) {
                 int i = t;
                 for (g = 0; g < q.count - 1 && i >= q.p[g].whole; ++g)
@@ -66,28 +84,21 @@ struct Items {
                 it = {g, i, 0, q.p[g].chunks, kWhole};
                 return true;
             }
-            if (!any)
-                return false;
-            phase = 1;
+            phase = 2;
             g = gb;
             t = tb + (cb > 0);
-            if (ce > 0) {
-                it = {ge, te, one ? cb : 0, ce, kPart};
+            if (q.late && part(it))
                 return true;
-            }
         }
-        if (phase == 1) {
-            while (g < ge && t >= q.p[g].m_tiles * q.p[g].n_tiles)
+        if (phase == 2) {
+            while (any && g < ge && t >= q.p[g].m_tiles * q.p[g].n_tiles)
                 t = q.p[++g].whole;
-            if (g < ge || t < te) {
+            if (any && (g < ge || t < te)) {
                 it = {g, t++, 0, q.p[g].chunks, kWhole};
                 return true;
             }
-            phase = 2;
-            if (cb > 0 && !one) {
-                it = {gb, tb, cb, q.p[gb].chunks, kLast};
-                return true;
-            }
+            phase = 3;
+            return last(it);
         }
         return false;
     }

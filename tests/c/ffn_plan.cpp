@@ -12,6 +12,9 @@ struct Product {
     int M, N, K, a_mn, b_mn;
 };
 
+// Of one chunk of a pair's tile: its MMAs, or the copies.
+int cycles(int n) { return 2 * n > 256 + n ? 2 * n : 256 + n; }
+
 // 0, or what is wrong with the plan of one launch.
 int look(int epilogue, const Product *products, int count, int sms, long long *most)
 {
@@ -43,6 +46,9 @@ int look(int epilogue, const Product *products, int count, int sms, long long *m
         if (16384 + (a.b_mn ? (rows + 63) / 64 * 8192 : rows * 128) > q.bytes)
             return 5;
     }
+    most[4] = 0;
+    for (int g = 0; g < count; ++g)
+        most[4] += static_cast<long long>(q.p[g].m_tiles) * q.p[g].n_tiles * q.p[g].chunks * cycles(q.p[g].tile_n);
     if (l.split) {
         if (count != 1 || l.split > 8 || l.split > q.p[0].chunks || q.p[0].b_mn)
             return 6;
@@ -70,8 +76,11 @@ int look(int epilogue, const Product *products, int count, int sms, long long *m
             tile_of(a, it.tile, m, n);
             if (m < 0 || m >= a.m_tiles || n < 0 || n >= a.n_tiles)
                 return 9;
+            Item end;
             if (last)
                 return 10;  // what waits for others comes last
+            if (w.last(end) != (it.kind == kLast) && it.kind == kLast)
+                return 17;
             if (it.kind == kWhole && (it.c0 != 0 || it.c1 != a.chunks))
                 return 11;
             if (it.kind == kPart && written[p]++)
@@ -84,7 +93,7 @@ int look(int epilogue, const Product *products, int count, int sms, long long *m
                     if (q.begin[o] < q.begin[o + 1])
                         ++awaited[o];
             }
-            units += it.c1 - it.c0;
+            units += static_cast<long long>(it.c1 - it.c0) * cycles(a.tile_n);
             auto &list = done[it.g][it.tile];
             for (int c = it.c0; c < it.c1; ++c)
                 list.push_back(c);
@@ -110,12 +119,14 @@ int look(int epilogue, const Product *products, int count, int sms, long long *m
 
 extern "C" {
 
-// The launches of every call of a block: 0, or 100 * the launch + what is wrong. v: the chunks of the busiest pair of each.
+// The launches of every call of a block: 0, or 100 * the launch + what is wrong. v: the busiest pair's
+// cycles of each, and all cycles of each.
 int ffn_look(int T, int H, int I, int sms, int wanted, long long *v)
 {
     const Product join = {I, T, H, 0, 0}, down = {H, T, I, 0, 0}, split = {I, T, H, 1, 0};
     const Product all[3] = {{H, T, 2 * I, 1, 0}, {H, 2 * I, T, 1, 1}, {I, H, T, 1, 1}};
-    v[0] = v[1] = v[2] = v[3] = 0;
+    for (int i = 0; i < 8; ++i)
+        v[i] = 0;
     if (const int bad = look(moe::kFfnJoin, &join, 1, sms, v))
         return 100 + bad;
     if (const int bad = look(moe::kFfnStore, &down, 1, sms, v + 1))
