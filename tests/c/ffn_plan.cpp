@@ -124,7 +124,8 @@ extern "C" {
 int ffn_look(int T, int H, int I, int sms, int wanted, long long *v)
 {
     const Product join = {I, T, H, 0, 0}, down = {H, T, I, 0, 0}, split = {I, T, H, 1, 0};
-    const Product all[3] = {{H, T, 2 * I, 1, 0}, {H, 2 * I, T, 1, 1}, {I, H, T, 1, 1}};
+    const Product dx = {H, T, 2 * I, 1, 0}, up = {H, 2 * I, T, 1, 1}, low = {I, H, T, 1, 1};
+    const Product all[3] = {2 * I > 16 * T ? up : dx, 2 * I > 16 * T ? low : up, 2 * I > 16 * T ? dx : low};  // as the calls order them
     for (int i = 0; i < 8; ++i)
         v[i] = 0;
     if (const int bad = look(moe::kFfnJoin, &join, 1, sms, v))
