@@ -14,16 +14,16 @@ using epk::set_error;
 
 #define MOE_FAIL(...) return set_error(EP_ERR_INVALID_ARG, __VA_ARGS__)
 
-inline size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
+static inline size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 
-inline bool aligned(const void *p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
+static inline bool aligned(const void *p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
 struct Range {
     explicit Range(const char *name) { nvtxRangePushA(name); }
     ~Range() { nvtxRangePop(); }
 };
 
-inline ep_status cuda_error(cudaError_t ce, const char *what)
+static inline ep_status cuda_error(cudaError_t ce, const char *what)
 {
     cudaGetLastError();
     return set_error(ce == cudaErrorMemoryAllocation ? EP_ERR_OOM : EP_ERR_CUDA, "%s: %s", what,
@@ -31,7 +31,7 @@ inline ep_status cuda_error(cudaError_t ce, const char *what)
 }
 
 // The current device, which must be able to run the library.
-inline ep_status current_device(int *dev, int *sms)
+static inline ep_status current_device(int *dev, int *sms)
 {
     cudaError_t ce = cudaGetDevice(dev);
     if (ce != cudaSuccess)
@@ -50,7 +50,7 @@ inline ep_status current_device(int *dev, int *sms)
     return EP_OK;
 }
 
-inline ep_status same_device(int want)
+static inline ep_status same_device(int want)
 {
     int dev = -1;
     const cudaError_t ce = cudaGetDevice(&dev);
@@ -62,7 +62,7 @@ inline ep_status same_device(int want)
 }
 
 // Waits for all work of a device: before a handle's memory is freed, or is its owner's again.
-inline void wait_for_device(int device)
+static inline void wait_for_device(int device)
 {
     int now = device;
     cudaGetDevice(&now);
@@ -79,7 +79,7 @@ using EncodeTiled = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t,
                                  const cuuint64_t *, const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave,
                                  CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
 
-inline EncodeTiled encode_tiled()
+static inline EncodeTiled encode_tiled()
 {
     static EncodeTiled fn = [] {
         void *p = nullptr;
@@ -97,7 +97,7 @@ inline EncodeTiled encode_tiled()
 
 // A 16-bit tensor [.., rows, cols]: row stride and matrix stride in elements,
 // box_cols x box_rows boxes (of 64 columns: in 128-byte swizzled rows), zeros outside.
-inline ep_status encode_map(CUtensorMap *m, const char *what, int fp16, const void *base, long long cols, long long rows,
+static inline ep_status encode_map(CUtensorMap *m, const char *what, int fp16, const void *base, long long cols, long long rows,
                      long long mats, long long row_stride, long long mat_stride, int box_cols, int box_rows)
 {
     EncodeTiled fn = encode_tiled();
@@ -118,7 +118,7 @@ inline ep_status encode_map(CUtensorMap *m, const char *what, int fp16, const vo
 }
 
 // A row-major result [.., rows, cols] of bf16 or fp32 that is written through boxes of box_cols x box_rows.
-inline ep_status encode_result(CUtensorMap *m, const char *what, bool fp32, void *base, long long cols, long long rows,
+static inline ep_status encode_result(CUtensorMap *m, const char *what, bool fp32, void *base, long long cols, long long rows,
                                long long mats, long long row_stride, long long mat_stride, int box_cols, int box_rows)
 {
     EncodeTiled fn = encode_tiled();
@@ -138,7 +138,7 @@ inline ep_status encode_result(CUtensorMap *m, const char *what, bool fp32, void
 
 // A 16-bit tensor [rows, 32 n] as [n][rows][32]: boxes of all its inner 32
 // columns, box_rows rows and box_steps steps of 32, zeros outside.
-inline ep_status encode_steps(CUtensorMap *m, const char *what, int fp16, const void *base, long long steps, long long rows,
+static inline ep_status encode_steps(CUtensorMap *m, const char *what, int fp16, const void *base, long long steps, long long rows,
                        long long row_stride, int box_rows, int box_steps)
 {
     EncodeTiled fn = encode_tiled();
@@ -193,7 +193,7 @@ struct Flags {
     }
 };
 
-inline ep_status finish(cudaError_t ce, const char *what, unsigned long long *rec, cudaStream_t stream)
+static inline ep_status finish(cudaError_t ce, const char *what, unsigned long long *rec, cudaStream_t stream)
 {
     if (ce != cudaSuccess)
         return cuda_error(ce, what);
@@ -201,9 +201,9 @@ inline ep_status finish(cudaError_t ce, const char *what, unsigned long long *re
     return st == EP_OK ? set_error(EP_OK, "") : st;
 }
 
-inline int div_up(int a, int b) { return (a + b - 1) / b; }
+static inline int div_up(int a, int b) { return (a + b - 1) / b; }
 
-inline ep_status check_rows(const char *name, const void *p, long long stride, int cols, int align, int step)
+static inline ep_status check_rows(const char *name, const void *p, long long stride, int cols, int align, int step)
 {
     if (!p || !aligned(p, align))
         MOE_FAIL("%s is NULL or not %d-byte aligned", name, align);
