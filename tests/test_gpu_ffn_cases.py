@@ -62,9 +62,9 @@ def test_rows_that_are_not_finite_stay_in_their_rows(cuda_device, T, H, I):
 
 
 @pytest.mark.parametrize("T", [6, 400])
-@pytest.mark.parametrize("spread", [50.0, 1e4])
+@pytest.mark.parametrize("spread", [50.0, 1e4, 1e12])
 def test_gates_far_from_zero(cuda_device, T, spread):
-    """Gates up to some 10^5: silu is then the gate, or nothing, and its slope 1 or 0."""
+    """Gates up to some 10^13: silu is then the gate, or nothing, and its slope 1 or 0."""
     x, gate_up, down, dy = make(T, 256, 200, seed=4, spread=spread)
     ffn = EpFfn(gate_up, down)
     want, err, state = block_ref.ffn(x, gate_up, down)
