@@ -810,12 +810,20 @@ Choice pair_choice(const FfnArgs &a, int epilogue, int n, bool cut, int sms)
     return {(cost > dram ? cost : dram) + 7000 + 10.0 * n, n, 0};
 }
 
+// Whether a split's blocks take half of an SM's memory: where there are more blocks than SMs, or half holds all that a block
+// copies. The next kernel's blocks then start beside them (1 row, 1024 x 1024: 7.9 us, alone on the SMs 11.5; 128 rows,
+// 7168 x 2048, whose copies need the room: 24.7, alone 22.0).
+bool shares_sm(const FfnArgs &a, double blocks, int n, int split, int sms)
+{
+    return n <= kShareRows && (blocks > sms || div_up(a.chunks, split) <= (kHalfRoom - 1024) / (kBlockA + 128 * n));
+}
+
 // A cluster's sums meet at a cost that grows with its blocks. A block alone on its SM leaves no room for the next kernel's
 // first copies.
 Choice split_choice(const FfnArgs &a, int epilogue, int n, int split, int sms)
 {
     const double tiles = static_cast<double>(div_up(a.N, n)) * div_up(a.M, features_of(epilogue)), blocks = tiles * split;
-    const bool share = n <= kShareRows && blocks > sms;
+    const bool share = shares_sm(a, blocks, n, split, sms);
     const double copy = (kBlockA + 128.0 * n) / 45.0, chunk = copy > 2.0 * n ? copy : 2.0 * n;  // mostly from DRAM
     const double cost = std::ceil(blocks / sms) * div_up(a.chunks, split) * chunk;
     const double after = std::ceil(blocks / (share ? 2 * sms : sms)) * (3000.0 + n * (8.0 + 4.0 * split));
@@ -940,8 +948,7 @@ void ffn_plan(FfnLaunch *l, int sms)
     }
     if (l->split) {
         const FfnArgs &a = q.p[0];
-        // two blocks on an SM where there are more blocks than SMs
-        const bool share = a.tile_n <= kShareRows && static_cast<long long>(a.m_tiles) * a.n_tiles * l->split > sms;
+        const bool share = shares_sm(a, static_cast<double>(a.m_tiles) * a.n_tiles * l->split, a.tile_n, l->split, sms);
         q.bytes = kBlockA + bytes_b(a.tile_n, a.b_mn);
         q.stages = ((share ? kHalfRoom : kRoom) - 1024) / q.bytes;
     } else {
