@@ -392,6 +392,8 @@ void plan(ep_ffn *h, int num_tokens, Launch &w)
         a.chunks = b.chunks;
         a.box_b = b.box_b;
         a.whole = b.whole;
+        a.band_inverse = b.band_inverse;
+        a.rest_inverse = b.rest_inverse;
     }
     q.pairs = k.pairs;
     q.stages = k.stages;

@@ -422,6 +422,9 @@ template <int EPI, bool GRAD> __global__ void __launch_bounds__(128 + kPairStore
                 mbar_arrive_cluster(in_first_block(smem_u32(&sh.loaded)));
             return true;
         };
+        bool one = EPI == kFfnSplit;
+        for (int i = 0; GRAD && i < q.count; ++i)
+            one = one || q.p[i].fp32;
         int sent = 0, items = 0;
         pdl_wait();  // flags, and what is fetched ahead of the sums, are the kernel's before until then
         for (Items w(q, pair); w.next(it);) {
@@ -499,12 +502,11 @@ template <int EPI, bool GRAD> __global__ void __launch_bounds__(128 + kPairStore
                         }
                     }
                     if (boxes) {
-                        // two boxes of bf16 in turn, of fp32 or of three results one
-                        const bool one = EPI == kFfnSplit || weight;
+                        // two boxes of bf16 in turn; one of fp32 (in the whole launch then) or of three results
                         uint8_t *const box = stage + (one || (sent & 1) == 0 ? 0 : kFeatures * 32);
                         ++sent;
                         if (sender) {
-                            if (one || GRAD)  // boxes of several products may differ
+                            if (one)
                                 bulk_wait_read<0>();
                             else
                                 bulk_wait_read<1>();
@@ -805,7 +807,7 @@ double dram_cycles(const FfnArgs &a, int epilogue)
 Choice pair_choice(const FfnArgs &a, int epilogue, int n, bool cut, int sms)
 {
     const double tiles = static_cast<double>(div_up(a.N, n)) * div_up(a.M, 2 * features_of(epilogue));
-    const double products = a.chunks * chunk_cycles(n, true) + 200, store = 20.0 * n, dram = dram_cycles(a, epilogue);
+    const double products = a.chunks * chunk_cycles(n, true) + 200, store = 1500 + 18.0 * n, dram = dram_cycles(a, epilogue);
     const double rounds = tiles / (sms / 2), cost = (cut ? rounds : std::ceil(rounds)) * (products > store ? products : store);
     return {(cost > dram ? cost : dram) + 7000 + 10.0 * n, n, 0};
 }
@@ -945,6 +947,8 @@ void ffn_plan(FfnLaunch *l, int sms)
         a.m_tiles = div_up(a.M, features_of(l->epilogue) * (c.split ? 1 : 2));
         a.n_tiles = div_up(a.N, c.n);
         a.box_b = c.split ? c.n : c.n / 2;
+        a.band_inverse = 1.0f / static_cast<float>(kBand * a.m_tiles);
+        a.rest_inverse = 1.0f / static_cast<float>(a.n_tiles % kBand ? a.n_tiles % kBand : kBand);
     }
     if (l->split) {
         const FfnArgs &a = q.p[0];

@@ -239,6 +239,7 @@ struct FfnArgs {
     int boxes;              // out can be written through mo
     int tile_n, m_tiles, n_tiles, chunks, box_b;  // of the plan; box_b: rows of mb's box where K is contiguous
     int whole;              // tiles that are not in the cut rounds
+    float band_inverse, rest_inverse;  // of the tiles of a band, and of the row tiles of the last one
     epk::CheckCtx chk;
 };
 
