@@ -406,13 +406,20 @@ template <int EPI, bool GRAD> __global__ void __launch_bounds__(128 + kPairStore
 #pragma unroll
                 for (int r = 0; r < 16; ++r)
                     v[r] = 0.0f;
-                for (int p = w.first_of_last(); p < pair; ++p)
-                    if (q.begin[p] < q.begin[p + 1]) {
-                        const float *const part = part_of(p) + step * 16 * 128;
+                for (int p = w.first_of_last(); p < pair; p += 2) {  // two parts' loads in flight
+                    float x[16], y[16];
+                    const bool has_x = q.begin[p] < q.begin[p + 1], has_y = p + 1 < pair && q.begin[p + 1] < q.begin[p + 2];
+                    const float *const at_x = part_of(p) + step * 16 * 128, *const at_y = part_of(p + 1) + step * 16 * 128;
 #pragma unroll
-                        for (int r = 0; r < 16; ++r)
-                            v[r] += __ldcg(part + r * 128);
-                    }
+                    for (int r = 0; r < 16; ++r)
+                        x[r] = has_x ? __ldcg(at_x + r * 128) : 0.0f;
+#pragma unroll
+                    for (int r = 0; r < 16; ++r)
+                        y[r] = has_y ? __ldcg(at_y + r * 128) : 0.0f;
+#pragma unroll
+                    for (int r = 0; r < 16; ++r)
+                        v[r] = v[r] + x[r] + y[r];
+                }
                 tmem_st16(d + step * 16, v);
             }
             tmem_wait_st();
@@ -791,9 +798,17 @@ double chunk_cycles(int n, bool pair)
     return mma > copy ? mma : copy;
 }
 
+// Of a pair's tile of n rows: its products, under which its epilogue is hidden, or that.
+double tile_cycles(const FfnArgs &a, int n)
+{
+    const double products = a.chunks * chunk_cycles(n, true) + 200, store = 1500 + 18.0 * n;
+    return products > store ? products : store;
+}
+
 struct Choice {
     double cost;
     int n, split;  // split 0: pairs
+    bool cut;
 };
 
 // All operands come from DRAM once, whoever asks for them.
@@ -802,14 +817,24 @@ double dram_cycles(const FfnArgs &a, int epilogue)
     return 2.0 * a.K * (static_cast<double>(a.M) * (epilogue == kFfnJoin ? 2 : 1) + a.N) / 3500.0;
 }
 
-// Cycles of a product's pairs with tiles of n rows: rounds of whole tiles (or an even share of them, cut), whose epilogue
-// is hidden if their products take as long.
-Choice pair_choice(const FfnArgs &a, int epilogue, int n, bool cut, int sms)
+// A part costs a trip of its sums through memory, on both sides. So rounds whose whole tiles leave little to gain are not
+// cut, and pairs that have nearly their share in whole tiles get no more (gradients of 700 rows, 2048 x 768: 22 us, with
+// cuts wherever they even the pairs out 37; 1500 rows, 4096 x 1536: 80 and 85; others within 1 %).
+constexpr double kCutGain = 8000, kLeastShare = 4000;  // cycles
+
+// Cycles of a product's pairs with tiles of n rows: rounds of whole tiles, or an even share of them, cut. Gradients of different K in one launch are balanced by cutting. One product
+// is not, unless its tiles are few: pairs that go through K out of step read the weights once for each tile of rows (y of
+// 515 rows, 4096 x 14336: 50 us over all pairs, 45 over 64 of 76 in step), and a pair with nothing but a tile's last part
+// waits for the others' before it begins. (dx and what it needs, 64 rows, 4096 x 4096: 33 us cut, 43 whole; 512 rows: 68
+// and 55.)
+Choice pair_choice(const FfnArgs &a, int epilogue, int n, int count, bool grad, int sms)
 {
     const double tiles = static_cast<double>(div_up(a.N, n)) * div_up(a.M, 2 * features_of(epilogue));
-    const double products = a.chunks * chunk_cycles(n, true) + 200, store = 1500 + 18.0 * n, dram = dram_cycles(a, epilogue);
-    const double rounds = tiles / (sms / 2), cost = (cut ? rounds : std::ceil(rounds)) * (products > store ? products : store);
-    return {(cost > dram ? cost : dram) + 7000 + 10.0 * n, n, 0};
+    const double rounds = tiles / (sms / 2), tile = tile_cycles(a, n), dram = dram_cycles(a, epilogue);
+    const double whole = std::ceil(rounds) * tile;
+    const double even = count > 1 ? rounds * tile : 2.0 * rounds * tile + 10.0 * n / rounds + kCutGain;
+    const bool cut = grad && (count > 1 || (rounds < 0.5 && even < whole));
+    return {std::fmax(cut ? even : whole, dram) + 7000 + 10.0 * n, n, 0, cut};
 }
 
 // Whether a split's blocks take half of an SM's memory: where there are more blocks than SMs, or half holds all that a block
@@ -830,7 +855,7 @@ Choice split_choice(const FfnArgs &a, int epilogue, int n, int split, int sms)
     const double cost = std::ceil(blocks / sms) * div_up(a.chunks, split) * chunk;
     const double after = std::ceil(blocks / (share ? 2 * sms : sms)) * (3000.0 + n * (8.0 + 4.0 * split));
     const double dram = dram_cycles(a, epilogue);
-    return {(cost > dram ? cost : dram) + after + (share ? 0.0 : 800.0), n, split};
+    return {(cost > dram ? cost : dram) + after + (share ? 0.0 : 800.0), n, split, false};
 }
 
 template <class F> Choice least(const FfnArgs &a, F &&cost)
@@ -838,7 +863,7 @@ template <class F> Choice least(const FfnArgs &a, F &&cost)
     // Of rows that lie along memory a pair's halves are whole lines: 128 rows or 256. Other heights read up to twice as
     // much (the gradients of 1999 rows, 2056 x 1400: 51 us instead of 33).
     const int step = a.b_mn ? 128 : 16;
-    Choice best = {-1.0, step, 0};
+    Choice best = {-1.0, step, 0, false};
     for (int n = step; n <= 256; n += step) {
         if (n > step && div_up(a.N, n - step) == div_up(a.N, n))
             continue;  // the same tiles with more waste
@@ -849,40 +874,59 @@ template <class F> Choice least(const FfnArgs &a, F &&cost)
     return best;
 }
 
+// Cycles of a pair's whole tiles: every pairs-th of those of all products.
+double whole_cycles(const FfnGroup &q, int pair)
+{
+    double sum = 0.0;
+    int first = 0;  // the pair that has the product's first one
+    for (int g = 0; g < q.count; ++g) {
+        const FfnArgs &a = q.p[g];
+        const int skip = ((pair - first) % q.pairs + q.pairs) % q.pairs;
+        const int n = a.whole > skip ? (a.whole - skip + q.pairs - 1) / q.pairs : 0;
+        sum += n * tile_cycles(a, a.tile_n);
+        first = (first + a.whole) % q.pairs;
+    }
+    return sum;
+}
+
 // Which tiles are whole and which are cut. Tiles of a product whose shares end within a few chunks of a tile's edge are
 // not cut there.
 void cut_rounds(FfnGroup *q, bool cut)
 {
     const int pairs = q->pairs;
     int tiles = 0;
-    for (int g = 0; g < q->count; ++g)
-        tiles += q->p[g].m_tiles * q->p[g].n_tiles;
+    double all = 0.0, most = 0.0;
+    for (int g = 0; g < q->count; ++g) {
+        FfnArgs &a = q->p[g];
+        a.whole = a.m_tiles * a.n_tiles;
+        tiles += a.whole;
+        all += a.whole * tile_cycles(a, a.tile_n);
+    }
+    for (int p = 0; p < pairs; ++p)
+        most = std::fmax(most, whole_cycles(*q, p));
+    cut = cut && most > all / pairs + kCutGain;
     // a last round of few tiles is cut together with the one before: a tile has few parts
     const int rounds = tiles / pairs, rest_tiles = tiles % pairs;
     // Parts first: their readers find them. With many rounds, parts after the whole tiles, which then stay in step and share
     // what they read (4096 rows, 4096 x 14336: 2.8 ms with parts first, 2.65; 1999 rows, 2056 x 1400: 114 us, after 120).
     q->late = rounds > 8;
     q->whole = !cut ? tiles : (rest_tiles * 3 >= pairs || rounds == 0 ? rounds : rounds - 1) * pairs;
-    double units[kFfnMaxPairs] = {}, all = 0.0;
-    int left = q->whole, first = 0;
-    for (int g = 0; g < q->count; ++g) {
+    for (int g = 0, left = q->whole; g < q->count; ++g) {
         FfnArgs &a = q->p[g];
-        const int mine = a.m_tiles * a.n_tiles;
-        a.whole = left < mine ? left : mine;
+        a.whole = a.whole < left ? a.whole : left;
         left -= a.whole;
-        for (int p = 0; p < pairs; ++p) {  // whole tiles first + p, ... of this product
-            const int skip = ((p - first) % pairs + pairs) % pairs;
-            const int n = a.whole > skip ? (a.whole - skip + pairs - 1) / pairs : 0;
-            units[p] += static_cast<double>(n) * a.chunks * chunk_cycles(a.tile_n, true);
-        }
-        first = (first + a.whole) % pairs;
-        all += static_cast<double>(mine) * a.chunks * chunk_cycles(a.tile_n, true);
     }
     // shares of the cut rounds: what a pair's whole tiles leave of its part of everything
-    double want[kFfnMaxPairs], sum = 0.0, rest = all;
+    double want[kFfnMaxPairs], sum = 0.0, rest = all, largest = 0.0;
     for (int p = 0; p < pairs; ++p) {
-        rest -= units[p];
-        want[p] = all / pairs - units[p] > 0.0 ? all / pairs - units[p] : 0.0;
+        const double whole = whole_cycles(*q, p);
+        rest -= whole;
+        want[p] = std::fmax(all / pairs - whole, 0.0);
+        largest = std::fmax(largest, want[p]);
+    }
+    const int apart = largest > 0.0 && largest < kLeastShare ? static_cast<int>(std::ceil(kLeastShare / largest)) : 1;
+    for (int p = 0; p < pairs; ++p) {  // shares that would be too small go to the others
+        want[p] = apart > 1 ? (p % apart == 0 ? largest : 0.0) : want[p] < kLeastShare ? 0.0 : want[p];
         sum += want[p];
     }
     double to = 0.0;
@@ -897,7 +941,7 @@ void cut_rounds(FfnGroup *q, bool cut)
         unit = 0;
         for (int g = 0; g < q->count; ++g) {
             const FfnArgs &a = q->p[g];
-            const double one = chunk_cycles(a.tile_n, true);
+            const double one = tile_cycles(a, a.tile_n) / a.chunks;
             const int have = (a.m_tiles * a.n_tiles - a.whole) * a.chunks;
             if (p == pairs - 1 || at + have * one <= to) {
                 at += have * one;
@@ -927,14 +971,12 @@ void ffn_plan(FfnLaunch *l, int sms)
     FfnGroup &q = l->q;
     q.pairs = sms / 2 < kFfnMaxPairs ? sms / 2 : kFfnMaxPairs;
     const bool grad = q.p[0].a_mn && l->epilogue == kFfnStore;  // dx, or the weights' gradients: pairs
-    // Several products of different K are balanced by cutting. One is not: pairs that go through K out of step read the
-    // weights once for each tile of rows (y of 515 rows, 4096 x 14336: 50 us over all pairs, 45 over 64 of 76 in step).
-    const bool cut = q.count > 1;
     l->split = 0;
+    bool cut = false;
     for (int g = 0; g < q.count; ++g) {
         FfnArgs &a = q.p[g];
         a.chunks = div_up(a.K, kChunk);
-        Choice c = least(a, [&](int n) { return pair_choice(a, l->epilogue, n, cut, 2 * q.pairs); });
+        Choice c = least(a, [&](int n) { return pair_choice(a, l->epilogue, n, q.count, grad, 2 * q.pairs); });
         if (q.count == 1) {
             for (int split = 1; !grad && split <= 8 && split <= a.chunks; split *= 2) {
                 const Choice s = least(a, [&](int n) { return split_choice(a, l->epilogue, n, split, sms); });
@@ -944,6 +986,7 @@ void ffn_plan(FfnLaunch *l, int sms)
             l->split = c.split;
         }
         a.tile_n = c.n;
+        cut = c.cut;
         a.m_tiles = div_up(a.M, features_of(l->epilogue) * (c.split ? 1 : 2));
         a.n_tiles = div_up(a.N, c.n);
         a.box_b = c.split ? c.n : c.n / 2;
