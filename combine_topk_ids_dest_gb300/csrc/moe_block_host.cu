@@ -341,8 +341,8 @@ Launch gradients_of(const ep_ffn_config &c, int T, const ep_ffn_grads &g, const 
     const Matrix rows = {"gradients of gate and up", dgu, T, 2 * I, 2 * I}, x = {"x", g.x, T, H, g.x_stride};
     Launch l(moe::kFfnStore, kGradients + (g.dx ? 1 : 0) + (g.dgate_up ? 2 : 0) + (g.ddown ? 4 : 0));
     // Only the last rounds are cut over all pairs. A tile of dx goes through 2 I, one of the weights' gradients through T: where
-    // that is so much more that few tiles of dx would fill a pair's share, dx comes last (700 rows, 1024 x 9000: 148 us,
-    // first 173; 300 rows, 2048 x 768: 44, first 37).
+    // that is so much more that few tiles of dx would fill a pair's share, dx comes last (all gradients of 700 rows, 1024 x
+    // 9000: 90 us, first 120; 8192 rows, 2048 x 1000: 150, first 141).
     const bool dx_last = 2 * I > 16 * T;
     for (int turn = 0; turn < 2; ++turn) {
         if (g.dx && turn == dx_last) {
@@ -400,7 +400,6 @@ void plan(ep_ffn *h, int num_tokens, Launch &w)
     q.bytes = k.bytes;
     q.whole = k.whole;
     q.cut = k.cut;
-    q.late = k.late;
     memcpy(q.begin, k.begin, sizeof(q.begin));
     w.l.split = kept.l.split;
     w.l.parts = kept.l.parts;

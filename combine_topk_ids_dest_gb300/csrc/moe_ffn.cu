@@ -21,8 +21,8 @@
 //    features x up to 256 rows a tile, persistent, accumulators in two halves of
 //    tensor memory, so that one tile's epilogue runs under the next one's MMAs.
 //    The three products that follow the split are one launch: whole tiles go
-//    round the pairs, the last one or two rounds are cut evenly along K over all of
-//    them. A tile that pairs share: all but the last one's sums go through memory;
+//    round the pairs, the last one or two rounds are cut along K where that evens the
+//    pairs out. A tile that pairs share: all but the last one's sums go through memory;
 //    the last pair, which ends with it, puts them into tensor memory and adds its
 //    own there, in the order of K. Waits go to lower pairs only;
 //  - splits: for few tiles. A block has 128 features, a cluster of 1 to 8 blocks
@@ -35,14 +35,15 @@
 // What bounds them: for many rows the MMAs, then the power limit (a step of
 // 4096 rows, 4096 x 14336, 4.3 TFLOP: 2.57 to 2.7 ms in captured calls, 1.6 to
 // 1.68 PFLOP/s where cuBLAS sustains 1.72 and reaches 1.89 for a moment; 8191 rows,
-// 7168 x 2048, forward 419 us, 1.72 PFLOP/s; tensor pipe active 82 % in the three
+// 7168 x 2048, forward 408 to 425 us, 1.7 PFLOP/s; tensor pipe active 82 % in the three
 // gradients of 2048 x 4096 x 4096). Below 256 rows a tile the copies: 57 bytes a
 // cycle come into an SM, a chunk of 64 k takes 0.23 us with 176 rows, 0.31 with
 // 256 (515 rows, 4096 x 14336: 121 to 142 us as the clock is, floor 96). For few
 // rows DRAM and a fixed part of some 4 us a kernel, of which the wait for the kernel
 // before, the first copy and the results are one each: one row, 7168 x 2048, 19.4
 // us, 14 of them at 6.6 TB/s; 128 rows 24.7. Rows whose length is no multiple of 128
-// bytes cost up to a quarter more (2056 x 1400 against 2048 x 1408: 115 and 95 us).
+// bytes cost up to a quarter more (2056 x 1400 against 2048 x 1408: 109 and 88 us):
+// each of a tile's rows lies in two lines.
 #include <cmath>
 
 #include <cuda_bf16.h>
@@ -822,11 +823,11 @@ double dram_cycles(const FfnArgs &a, int epilogue)
 // cuts wherever they even the pairs out 37; 1500 rows, 4096 x 1536: 80 and 85; others within 1 %).
 constexpr double kCutGain = 8000, kLeastShare = 4000;  // cycles
 
-// Cycles of a product's pairs with tiles of n rows: rounds of whole tiles, or an even share of them, cut. Gradients of different K in one launch are balanced by cutting. One product
-// is not, unless its tiles are few: pairs that go through K out of step read the weights once for each tile of rows (y of
-// 515 rows, 4096 x 14336: 50 us over all pairs, 45 over 64 of 76 in step), and a pair with nothing but a tile's last part
-// waits for the others' before it begins. (dx and what it needs, 64 rows, 4096 x 4096: 33 us cut, 43 whole; 512 rows: 68
-// and 55.)
+// Cycles of a product's pairs with tiles of n rows: rounds of whole tiles, or an even share of them, cut. Gradients of
+// different K in one launch are balanced by cutting. One product is not, unless its tiles are few: pairs that go through K
+// out of step read the weights once for each tile of rows (y of 515 rows, 4096 x 14336: 50 us over all pairs, 45 over 64 of
+// 76 in step), and a pair with nothing but a tile's last part waits for the others' before it begins. (dx and what it needs,
+// 64 rows, 4096 x 4096: 33 us cut, 43 whole; 512 rows: 68 and 55.)
 Choice pair_choice(const FfnArgs &a, int epilogue, int n, int count, bool grad, int sms)
 {
     const double tiles = static_cast<double>(div_up(a.N, n)) * div_up(a.M, 2 * features_of(epilogue));
@@ -907,9 +908,6 @@ void cut_rounds(FfnGroup *q, bool cut)
     cut = cut && most > all / pairs + kCutGain;
     // a last round of few tiles is cut together with the one before: a tile has few parts
     const int rounds = tiles / pairs, rest_tiles = tiles % pairs;
-    // Parts first: their readers find them. With many rounds, parts after the whole tiles, which then stay in step and share
-    // what they read (4096 rows, 4096 x 14336: 2.8 ms with parts first, 2.65; 1999 rows, 2056 x 1400: 114 us, after 120).
-    q->late = rounds > 8;
     q->whole = !cut ? tiles : (rest_tiles * 3 >= pairs || rounds == 0 ? rounds : rounds - 1) * pairs;
     for (int g = 0, left = q->whole; g < q->count; ++g) {
         FfnArgs &a = q->p[g];

@@ -250,7 +250,7 @@ struct FfnGroup {
     int *flags;    // [pair][block]: that part is written; then the number of blocks that have left. 0 between launches
     unsigned int *err;
     int count, pairs, stages, bytes;  // bytes of a stage
-    int whole, cut, late;             // whole tiles of all products; whether there are cut rounds; whether parts come after
+    int whole, cut;                   // whole tiles of all products; whether there are cut rounds
     int begin[kFfnMaxPairs + 1];      // each pair's share of the cut rounds, in chunks of their tiles
 };
 
