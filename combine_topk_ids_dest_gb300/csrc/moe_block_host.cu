@@ -65,6 +65,8 @@ ep_status check_norm(const ep_norm_config *c, int num_tokens)
     return EP_OK;
 }
 
+Span weight_span(const ep_norm_config &c) { return {"weight", c.weight, size_t(c.hidden) * size_of(c.weight_dtype), c.hidden}; }
+
 // The current device for the norm's calls, whose kernels have no handle: set up when a device is first seen.
 ep_status norm_device(int *sms)
 {
@@ -117,10 +119,13 @@ ep_status ep_norm_run(const ep_norm_config *cfg, const ep_norm_rows *rows, int n
                 return st;
     if (!aligned(r.q, 8) || !aligned(r.scales, 4))
         MOE_FAIL("q is not 8-byte or scales not 4-byte aligned");
+    const Span w = weight_span(*cfg);
     const Span eight[2] = {{"q", r.q, extent(num_tokens, H, H, 1), H}, {"scales", r.scales, extent(num_tokens, groups, groups, 4), groups}};
     for (int o = 2; o < 4 && st == EP_OK; ++o)
         for (int i = 0; i < o && st == EP_OK; ++i)
             st = check_overlap(all[o], all[i], i < 2);
+    for (int o = 0; o < 4 && st == EP_OK; ++o)
+        st = check_overlap(o < 2 ? all[2 + o] : eight[o - 2], w, false);
     for (int o = 0; o < 2 && st == EP_OK; ++o) {
         for (int i = 0; i < 4 && st == EP_OK; ++i)
             st = check_overlap(eight[o], all[i], false);
@@ -185,9 +190,10 @@ ep_status ep_norm_backward(const ep_norm_config *cfg, const void *dy, long long 
     if ((!dx && !dweight) || (num_tokens == 0 && !dweight))
         return set_error(EP_OK, "");
     if (num_tokens > 0) {
-        const Span in[3] = {{"dy", dy, extent(num_tokens, dy_stride, H, size), dy_stride},
+        const Span in[4] = {{"dy", dy, extent(num_tokens, dy_stride, H, size), dy_stride},
                             {"h", h, extent(num_tokens, h_stride, H, size), h_stride},
-                            {"dh", dh, extent(num_tokens, dh_stride, H, size), dh_stride}};
+                            {"dh", dh, extent(num_tokens, dh_stride, H, size), dh_stride},
+                            weight_span(*cfg)};
         const Span out[2] = {{"dx", dx, extent(num_tokens, dx_stride, H, size), dx_stride}, {"dweight", dweight, size_t(H) * 4, H}};
         for (int i = 0; i < 3 && st == EP_OK; ++i)
             if (i < 2 || dh)
@@ -195,8 +201,8 @@ ep_status ep_norm_backward(const ep_norm_config *cfg, const void *dy, long long 
         if (st == EP_OK && dx)
             st = check_rows("dx", dx, dx_stride, H, 16, 8);
         for (int o = 0; o < 2 && st == EP_OK; ++o)
-            for (int i = 0; i < 3 && st == EP_OK; ++i)
-                st = check_overlap(out[o], in[i], o == 0);
+            for (int i = 0; i < 4 && st == EP_OK; ++i)
+                st = check_overlap(out[o], in[i], o == 0 && i < 3);
         if (st == EP_OK)
             st = check_overlap(out[0], out[1], false);
     }
@@ -405,6 +411,14 @@ void plan(ep_ffn *h, int num_tokens, Launch &w)
     w.l.parts = kept.l.parts;
 }
 
+// An output that overlaps the weights.
+ep_status check_weights(const Span &out, const ep_ffn_config &c)
+{
+    const size_t bytes = size_t(c.hidden) * c.intermediate * 2;
+    const ep_status st = check_overlap(out, {"gate_up", c.gate_up, 2 * bytes, c.hidden}, false);
+    return st == EP_OK ? check_overlap(out, {"down", c.down, bytes, c.intermediate}, false) : st;
+}
+
 // The intermediate rows, for the backward pass the gradients of gate and up too, and the parts of shared tiles.
 struct FfnLayout {
     size_t off_dgu, off_parts, total;
@@ -544,6 +558,10 @@ ep_status ep_ffn_run(ep_ffn *h, const void *x, long long x_stride, int num_token
     if (st == EP_OK)
         st = check_overlap(keep, y, false);
     if (st == EP_OK)
+        st = check_weights(y, h->cfg);
+    if (st == EP_OK)
+        st = check_weights(keep, h->cfg);
+    if (st == EP_OK)
         st = check_workspace(workspace, workspace_bytes, l.total);
     if (st == EP_OK)
         st = h->flags.take();
@@ -610,6 +628,8 @@ ep_status ep_ffn_backward(ep_ffn *h, const ep_ffn_grads *grads, int num_tokens, 
             st = check_overlap(out[o], in[i], false);
         for (int i = 0; i < o && st == EP_OK; ++i)
             st = check_overlap(out[o], out[i], false);
+        if (st == EP_OK)
+            st = check_weights(out[o], h->cfg);
     }
     const FfnLayout l(h, EP_FFN_BACKWARD, T);
     if (st == EP_OK)

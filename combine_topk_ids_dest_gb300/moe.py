@@ -480,11 +480,12 @@ class EpFfn(_Handle):
 
     def _workspace(self, call: int, n: int) -> Tuple[Optional[torch.Tensor], int, int]:
         """A call's workspace: the tensor, its address and its bytes."""
-        if self._sized[:2] != (call, n):
-            size = ctypes.c_size_t(0)
-            check(self._L.ep_ffn_workspace_size(self._live(), call, n, ctypes.byref(size)))
-            self._sized = call, n, size.value
-        size = self._sized[2]
+        sized = self._sized
+        if sized[:2] != (call, n):
+            need = ctypes.c_size_t(0)
+            check(self._L.ep_ffn_workspace_size(self._live(), call, n, ctypes.byref(need)))
+            self._sized = sized = call, n, need.value
+        size = sized[2]
         ws = torch.empty(size, dtype=torch.uint8, device=self.device)
         return ws, ws.data_ptr(), size
 

@@ -228,7 +228,7 @@ typedef struct {
  * then residual_out is too (s is x). Each of residual_out, out and the pair
  * q [num_tokens, hidden], scales [num_tokens, ceil(hidden / 128)] (contiguous;
  * q 8-byte, scales 4-byte aligned) may be NULL. residual_out and out may be x or residual themselves
- * (same address and stride); no other overlap. */
+ * (same address and stride); no other overlap, with weight neither. */
 typedef struct {
     const void *x;
     long long x_stride;
@@ -251,7 +251,7 @@ ep_status ep_norm_run(const ep_norm_config *cfg, const ep_norm_rows *rows, int n
  * dx is the gradient of x and of residual alike, rounded once to dtype;
  * dweight is fp32 [hidden], summed in an order that does not depend on timing.
  * Either may be NULL. Rows as above, strides a multiple of 8; dx may be dy, h or
- * dh itself. workspace: device, 256-byte aligned, of at least
+ * dh itself, no other overlap. workspace: device, 256-byte aligned, of at least
  * ep_norm_backward_workspace_size bytes (used by this call alone). Without
  * rows dweight is 0. */
 ep_status ep_norm_backward_workspace_size(const ep_norm_config *cfg, int num_tokens, size_t *bytes);
@@ -295,7 +295,8 @@ ep_status ep_ffn_workspace_size(ep_ffn *h, ep_ffn_call call, int num_tokens, siz
  * elements apart (x_stride a multiple of 8, both >= hidden), x 16-byte aligned. saved: NULL, or
  * device fp32 [num_tokens, 2 * intermediate], contiguous, 16-byte aligned: receives g and u of
  * each row, for ep_ffn_backward. workspace: device, 256-byte aligned (used by this call
- * alone). 0 <= num_tokens <= EP_FFN_MAX_TOKENS; 0 does nothing. out may not overlap the inputs. */
+ * alone). 0 <= num_tokens <= EP_FFN_MAX_TOKENS; 0 does nothing. out and saved
+ * overlap neither x nor the weights. */
 ep_status ep_ffn_run(ep_ffn *h, const void *x, long long x_stride, int num_tokens, float *saved, void *out,
                      long long out_stride, void *workspace, size_t workspace_bytes, void *stream);
 
@@ -304,8 +305,8 @@ ep_status ep_ffn_run(ep_ffn *h, const void *x, long long x_stride, int num_token
  *   dx = dg W1 + du W3;  dW1 = dg^T x;  dW3 = du^T x;  dW2 = dy^T h
  * dy, x, dx: rows as above (dy as x). dgate_up and ddown: device, contiguous, shaped
  * like the weights, 16-byte aligned, of type grad_dtype: EP_DTYPE_BF16, or EP_DTYPE_FP32; with
- * accumulate (fp32 only) they are added to. Each of dx, dgate_up and ddown may be NULL.
- * Without rows weight gradients are 0 (with accumulate: unchanged). */
+ * accumulate (fp32 only) they are added to. Each of dx, dgate_up and ddown may be NULL;
+ * none overlaps an input or a weight. Without rows weight gradients are 0 (with accumulate: unchanged). */
 typedef struct {
     const void *dy;
     long long dy_stride;

@@ -67,6 +67,12 @@ def test_norm_rows_refused(fake, kw, frag):
     assert fake.launches() == []
 
 
+@pytest.mark.parametrize("kw", [dict(out=AT[0]), dict(residual_out=AT[0] + 16), dict(q=AT[0] + 2 * H - 8), dict(scales=AT[0])])
+def test_norm_results_on_the_weight_refused(fake, kw):
+    assert _norm(fake, **kw) == INVALID and "overlaps weight" in fake.message(), fake.message()
+    assert fake.launches() == []
+
+
 def test_norm_in_place_and_without_rows(fake):
     for kw in (dict(), dict(out=AT[1]), dict(residual_out=AT[2]), dict(residual_out=AT[1], out=AT[2]),
                dict(residual=0, residual_out=0), dict(q=0, scales=0), dict(out=0)):
@@ -107,6 +113,12 @@ def _back(fake, cfg=None, n=T, workspace=AT[8], bytes=1 << 30, **kw):
 ])
 def test_norm_backward_refused(fake, kw, frag):
     assert _back(fake, **kw) == INVALID and frag in fake.message(), fake.message()
+    assert fake.launches() == []
+
+
+@pytest.mark.parametrize("kw", [dict(dx=AT[0]), dict(dweight=AT[0])])
+def test_norm_gradients_on_the_weight_refused(fake, kw):
+    assert _back(fake, **kw) == INVALID and "overlaps weight" in fake.message(), fake.message()
     assert fake.launches() == []
 
 
@@ -207,6 +219,24 @@ def _backward(fake, h, n=T, workspace=AT[8], bytes=1 << 36, **kw):
     (dict(n=-3), "num_tokens"),
 ])
 def test_ffn_backward_refused(fake, ffn, kw, frag):
+    assert _backward(fake, ffn, **kw) == INVALID and frag in fake.message(), fake.message()
+    assert fake.launches() == []
+
+
+@pytest.mark.parametrize("kw,frag", [
+    (dict(out=AT[0]), "out overlaps gate_up"), (dict(out=AT[1] + 2), "out overlaps down"),
+    (dict(saved=AT[0] + 4 * H * I - 16), "saved overlaps gate_up"), (dict(saved=AT[1]), "saved overlaps down"),
+])
+def test_ffn_results_on_the_weights_refused(fake, ffn, kw, frag):
+    assert _run(fake, ffn, **kw) == INVALID and frag in fake.message(), fake.message()
+    assert fake.launches() == []
+
+
+@pytest.mark.parametrize("kw,frag", [
+    (dict(dx=AT[1]), "dx overlaps down"), (dict(dgate_up=AT[0]), "dgate_up overlaps gate_up"),
+    (dict(ddown=AT[1]), "ddown overlaps down"), (dict(ddown=AT[0] + 4 * H * I - 16), "ddown overlaps gate_up"),
+])
+def test_ffn_gradients_on_the_weights_refused(fake, ffn, kw, frag):
     assert _backward(fake, ffn, **kw) == INVALID and frag in fake.message(), fake.message()
     assert fake.launches() == []
 

@@ -91,6 +91,24 @@ def test_what_is_not_asked_for(cuda_device, T, H, I):
         assert bool((off <= 2.0 ** -7 * want.double().abs() + 2.0 ** -12 * want.double().abs().mean()).all())
 
 
+@pytest.mark.parametrize("T,H,I", [(100, 256, 4096), (16, 1024, 5000), (3, 72, 16384), (300, 520, 8192), (9001, 264, 256), (700, 2048, 768)])
+def test_few_tiles_shared_by_many_blocks(cuda_device, T, H, I):
+    """dx alone, the weights' gradients alone and all: tiles whose K goes over many blocks, and shares that some blocks lack."""
+    x, gate_up, down, dy = make(T, H, I, seed=11)
+    ffn = EpFfn(gate_up, down)
+    _, _, state = block_ref.ffn(x, gate_up, down)
+    want = block_ref.ffn_back(dy, state)
+    _, saved = ffn.forward(x)
+    calls = [ffn.backward(dy, x, saved, **kw) for kw in (dict(), dict(need_weights=False), dict(need_dx=False))]
+    for got in calls:
+        for name, t, (g, e) in zip(("dx", "dgate_up", "ddown"), got, want):
+            if t is not None:
+                block_ref.check(t, g, e, name)
+    for kw, first in zip((dict(), dict(need_weights=False), dict(need_dx=False)), calls):
+        for t, again in zip(first, ffn.backward(dy, x, saved, **kw)):
+            assert t is None and again is None or torch.equal(t, again)
+
+
 @pytest.mark.parametrize("T,H,I", [(1, 72, 40), (70, 264, 136), (1100, 520, 1032)])
 def test_gradients_in_fp32_and_added_up(cuda_device, T, H, I):
     x, gate_up, down, dy = make(T, H, I, seed=6)
