@@ -35,7 +35,7 @@
 // What bounds them: for many rows the MMAs, then the power limit (a step of
 // 4096 rows, 4096 x 14336, 4.3 TFLOP: 2.54 to 2.7 ms in captured calls, 1.6 to
 // 1.7 PFLOP/s where cuBLAS sustains 1.72 and reaches 1.89 for a moment; 8191 rows,
-// 7168 x 2048, forward 408 to 425 us, 1.7 PFLOP/s; tensor pipe active 82 % in the three
+// 7168 x 2048, forward 408 to 425 us, 1.7 PFLOP/s; tensor pipe active 86 % in the three
 // gradients of 2048 x 4096 x 4096). Below 256 rows a tile the copies: 57 bytes a
 // cycle come into an SM, a chunk of 64 k takes 0.23 us with 176 rows, 0.31 with
 // 256 (515 rows, 4096 x 14336: 121 to 142 us as the clock is, floor 96). For few
