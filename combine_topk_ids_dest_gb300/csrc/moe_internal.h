@@ -124,7 +124,7 @@ struct Int4Args {
     epk::CheckCtx chk;
 };
 
-constexpr int kInt4StagesA = 12, kInt4StagesB = 16;  // most stages of the rings of weights and tokens
+constexpr int kInt4StagesA = 12, kInt4StagesB = 16;  // most stages of the rings of weights and tokens, even
 constexpr int kInt4SumStride = kTileRows + 4;        // column stride of the groups' sums: fragments' stores hit all banks
 constexpr int kInt4Groups = 4;                       // groups of four warps that multiply
 
@@ -155,10 +155,10 @@ static __host__ __device__ __forceinline__ Int4Layout int4_layout(bool linear, i
     l.sums = (fixed_bytes + 127) & ~127;
     l.ring_b = l.sums + kInt4Groups * l.cols * kInt4SumStride * 4;
     const int room = smem - l.ring_b, both = least(kInt4StagesB, room / (stage_a + l.stage_b[1]));
-    l.stages_b[1] = both < 2 ? 2 : both;
-    l.stages_b[0] = least(kInt4StagesB, l.stages_b[1] * l.stage_b[1] / l.stage_b[0]);
+    l.stages_b[1] = both < 2 ? 2 : both & ~1;
+    l.stages_b[0] = least(kInt4StagesB, (l.stages_b[1] * l.stage_b[1] / l.stage_b[0]) & ~1);
     l.ring_a = l.ring_b + l.stages_b[1] * l.stage_b[1];
-    l.stages = least(kInt4StagesA, (smem - l.ring_a) / stage_a);
+    l.stages = least(kInt4StagesA, ((smem - l.ring_a) / stage_a) & ~1);
     return l;
 }
 
