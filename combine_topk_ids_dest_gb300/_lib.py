@@ -26,7 +26,7 @@ STATUS_NAMES = {0: "EP_OK", 1: "EP_ERR_INVALID_ARG", 2: "EP_ERR_STATE", 3: "EP_E
 CHECK_SITES = ("src_hidden", "src_ids", "src_scale", "src_weights", "recv_hidden", "recv_ids",
                "recv_scale", "recv_weights", "route_write", "eplb_src", "eplb_dst", "route_read",
                "combine_in", "combine_out", "noalloc_ids", "noalloc_route", "dev_counts", "live_counts",
-               "moe_ids", "moe_weights", "moe_out")
+               "moe_ids", "moe_weights", "moe_out", "moe_rows")
 
 EP_DTYPE_BF16 = 0
 EP_DTYPE_FP8_E4M3 = 1

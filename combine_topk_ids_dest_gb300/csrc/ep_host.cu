@@ -392,7 +392,7 @@ const char *epk::check_site_name(int site)
         "dispatch: eplb_local_stats", "dispatch: gathered eplb stats", "combine: routing state",
         "combine: expert output row", "combine: output row", "ep_combine_noalloc: id row",
         "ep_combine_noalloc: routing scratch", "dispatch: device token counts", "live token counts",
-        "moe: ids", "moe: routing weights", "moe: output row"};
+        "moe: ids", "moe: routing weights", "moe: output row", "moe: input row"};
     return (site >= 0 && site < kNumSites) ? names[site] : "unknown site";
 }
 

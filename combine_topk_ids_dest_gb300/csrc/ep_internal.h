@@ -29,7 +29,7 @@ enum CheckSite {
     kSiteRouteWrite, kSiteEplbSrc, kSiteEplbDst,
     kSiteRouteRead, kSiteCombineIn, kSiteCombineOut,
     kSiteNoallocIds, kSiteNoallocRoute, kSiteDevCounts, kSiteLiveCounts,
-    kSiteMoeIds, kSiteMoeWeights, kSiteMoeOut,
+    kSiteMoeIds, kSiteMoeWeights, kSiteMoeOut, kSiteMoeRows,
     kNumSites
 };
 

@@ -342,7 +342,7 @@ template <class T, int U> __global__ void __launch_bounds__(kBackThreads, 1) bac
     extern __shared__ uint8_t dyn[];
     __shared__ uint64_t full[kBackStages], empty[kBackStages];
     __shared__ float slots[16][2][2][16];  // [team][turn][sum][warp]
-    __shared__ int abort_, issued_;
+    __shared__ int abort_, issued_, stopped[16];  // stopped: the stage from which on a team gave up
     uint8_t *const ring = dyn + (128 - (smem_u32(dyn) & 127)) % 128;
     const int tid = threadIdx.x, warp = __shfl_sync(~0u, tid >> 5, 0), lane = tid & 31;
     const int team = warp / a.team, place = warp - team * a.team, units = a.H / kUnit;
@@ -358,6 +358,8 @@ template <class T, int U> __global__ void __launch_bounds__(kBackThreads, 1) bac
             mbar_init(smem_u32(&empty[i]), a.team * a.teams);
         }
         mbar_init_fence();
+    } else if (tid >= 32 && tid < 48) {
+        stopped[tid - 32] = mine;
     }
     __syncthreads();
     pdl_wait();
@@ -380,12 +382,17 @@ template <class T, int U> __global__ void __launch_bounds__(kBackThreads, 1) bac
                 const T *const from = static_cast<const T *>(o == 0 ? a.h : o == 1 ? a.dy : a.dh);
                 const long long stride = o == 0 ? a.h_stride : o == 1 ? a.dy_stride : a.dh_stride;
                 const uint32_t to = smem_u32(ring) + s * a.stage + o * a.rows * row_bytes;
+                // Of the checked build: rows outside are not copied, and the wait for them runs out.
+                const auto there = [&](const T *p, int n) {
+                    return EP_IN_BOUNDS(a.chk, epk::kSiteMoeRows, p, row_bytes * n, from, sizeof(T) * ((a.T - 1LL) * stride + a.H));
+                };
                 if (stride == a.H) {
-                    if (lane == o)
+                    if (lane == o && there(from + t * stride, rows))
                         bulk_load_plain(to, from + t * stride, row_bytes * rows, bar);
                 } else {
                     for (int r = lane; r < rows; r += 32)
-                        bulk_load_plain(to + r * row_bytes, from + (t + r) * stride, row_bytes, bar);
+                        if (there(from + (t + r) * stride, 1))
+                            bulk_load_plain(to + r * row_bytes, from + (t + r) * stride, row_bytes, bar);
                 }
             }
             if (++s == a.stages) {
@@ -414,12 +421,13 @@ template <class T, int U> __global__ void __launch_bounds__(kBackThreads, 1) bac
         }
         int turn = 0, s = 0;
         uint32_t parity = 0;
-        bool run = true;
-        for (int i = 0; run && i < mine; ++i) {
-            run = mbar_wait(smem_u32(&full[s]), parity, abort, kWaitFullB);
+        for (int i = 0; i < mine; ++i) {
+            bool run = mbar_wait(smem_u32(&full[s]), parity, abort, kWaitFullB);
             run = a.team > 1 ? named_all(1 + team, a.team * 32, run) : __all_sync(~0u, run);
-            if (!run)
+            if (!run) {
+                stopped[team] = i;
                 break;
+            }
             const long long t0 = (blockIdx.x + static_cast<long long>(i) * gridDim.x) * a.rows;
             const int rows = static_cast<int>(a.T - t0 < a.rows ? a.T - t0 : a.rows);
             for (int row = team; row < rows; row += a.teams, turn ^= 1) {
@@ -528,9 +536,22 @@ template <class T, int U> __global__ void __launch_bounds__(kBackThreads, 1) bac
         }
     }
     __syncthreads();
-    if (abort_ && tid == 0) {  // copies in flight land before the block's memory is given back
-        for (int i = max(0, issued_ - a.stages); i < issued_; ++i)
-            mbar_wait(smem_u32(&full[i % a.stages]), (i / a.stages) & 1, nullptr, kWaitOther);
+    if (abort_) {
+        // rows of dx that were given up are NaN: there is no handle that could report it
+        for (int r = 0; a.dx && r < a.teams; ++r)
+            for (int i = stopped[r]; i < mine; ++i) {
+                const long long t0 = (blockIdx.x + static_cast<long long>(i) * gridDim.x) * a.rows;
+                for (long long t = t0 + r; t < t0 + a.rows && t < a.T; t += a.teams)
+                    for (int u = tid; u < units; u += kBackThreads) {
+                        const float f[kUnit] = {NAN, NAN, NAN, NAN, NAN, NAN, NAN, NAN};
+                        Unit<T> *const to = unit_at<T>(a.dx, a.dx_stride, t, u);
+                        if (EP_IN_BOUNDS(a.chk, epk::kSiteMoeOut, to, sizeof(Unit<T>), a.dx, sizeof(T) * ((a.T - 1LL) * a.dx_stride + a.H)))
+                            store_unit<T>(to, f);
+                    }
+            }
+        if (tid == 0)  // copies in flight land before the block's memory is given back
+            for (int i = max(0, issued_ - a.stages); i < issued_; ++i)
+                mbar_wait(smem_u32(&full[i % a.stages]), (i / a.stages) & 1, nullptr, kWaitOther);
     }
 }
 

@@ -16,9 +16,10 @@
  * Statuses, ep_last_error, streams, devices and threads are as in ep.h: every
  * call checks its arguments on the host before it launches anything, queues its
  * work on the given stream and returns. The checked build reports as there, but
- * tests fewer accesses here: the experts' reads of ids and weights, and all
- * stores of ids, weights and results. Reads of x, weights and biases, packed
- * weights and workspaces are not tested.
+ * tests fewer accesses here: the experts' reads of ids and weights, the rows
+ * that the norm's gradients are made of, and all stores of ids, weights and
+ * results. Other reads of x, weights and biases, packed weights and workspaces
+ * are not tested.
  * Calls on one handle must be ordered on the device too (one stream, or
  * streams with events between them): a handle's workspace holds one call's
  * intermediate results. Handles are created and destroyed outside stream
@@ -253,7 +254,9 @@ ep_status ep_norm_run(const ep_norm_config *cfg, const ep_norm_rows *rows, int n
  * Either may be NULL. Rows as above, strides a multiple of 8; dx may be dy, h or
  * dh itself, no other overlap. workspace: device, 256-byte aligned, of at least
  * ep_norm_backward_workspace_size bytes (used by this call alone). Without
- * rows dweight is 0. */
+ * rows dweight is 0. There is no handle that could report a wait that ran out
+ * (about 2 s, for a copy of rows): dweight and the rows of dx that were given
+ * up are then NaN. */
 ep_status ep_norm_backward_workspace_size(const ep_norm_config *cfg, int num_tokens, size_t *bytes);
 
 ep_status ep_norm_backward(const ep_norm_config *cfg, const void *dy, long long dy_stride, const void *h,
