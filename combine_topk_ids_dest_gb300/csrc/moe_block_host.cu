@@ -189,23 +189,23 @@ ep_status ep_norm_backward(const ep_norm_config *cfg, const void *dy, long long 
         MOE_FAIL("dweight is not 4-byte aligned");
     if ((!dx && !dweight) || (num_tokens == 0 && !dweight))
         return set_error(EP_OK, "");
-    if (num_tokens > 0) {
-        const Span in[4] = {{"dy", dy, extent(num_tokens, dy_stride, H, size), dy_stride},
-                            {"h", h, extent(num_tokens, h_stride, H, size), h_stride},
-                            {"dh", dh, extent(num_tokens, dh_stride, H, size), dh_stride},
-                            weight_span(*cfg)};
-        const Span out[2] = {{"dx", dx, extent(num_tokens, dx_stride, H, size), dx_stride}, {"dweight", dweight, size_t(H) * 4, H}};
-        for (int i = 0; i < 3 && st == EP_OK; ++i)
-            if (i < 2 || dh)
-                st = check_rows(in[i].name, in[i].p, in[i].stride, H, 16, 8);
-        if (st == EP_OK && dx)
-            st = check_rows("dx", dx, dx_stride, H, 16, 8);
-        for (int o = 0; o < 2 && st == EP_OK; ++o)
-            for (int i = 0; i < 4 && st == EP_OK; ++i)
-                st = check_overlap(out[o], in[i], o == 0 && i < 3);
-        if (st == EP_OK)
-            st = check_overlap(out[0], out[1], false);
-    }
+    if (num_tokens == 0)  // dweight is written all the same
+        dy = h = dh = dx = nullptr;
+    const Span in[4] = {{"dy", dy, extent(num_tokens, dy_stride, H, size), dy_stride},
+                        {"h", h, extent(num_tokens, h_stride, H, size), h_stride},
+                        {"dh", dh, extent(num_tokens, dh_stride, H, size), dh_stride},
+                        weight_span(*cfg)};
+    const Span out[2] = {{"dx", dx, extent(num_tokens, dx_stride, H, size), dx_stride}, {"dweight", dweight, size_t(H) * 4, H}};
+    for (int i = 0; i < 3 && st == EP_OK && num_tokens > 0; ++i)
+        if (i < 2 || dh)
+            st = check_rows(in[i].name, in[i].p, in[i].stride, H, 16, 8);
+    if (st == EP_OK && dx)
+        st = check_rows("dx", dx, dx_stride, H, 16, 8);
+    for (int o = 0; o < 2 && st == EP_OK; ++o)
+        for (int i = 0; i < 4 && st == EP_OK; ++i)
+            st = check_overlap(out[o], in[i], o == 0 && i < 3);
+    if (st == EP_OK)
+        st = check_overlap(out[0], out[1], false);
     const size_t need = dweight ? align256(size_t(moe::norm_back_blocks(num_tokens, a.sms)) * H * 4) : 0;
     if (st == EP_OK)
         st = check_workspace(workspace, workspace_bytes, need);
@@ -600,7 +600,23 @@ ep_status ep_ffn_backward(ep_ffn *h, const ep_ffn_grads *grads, int num_tokens, 
     const int size = size_of(g.grad_dtype);
     const size_t weight = size_t(H) * I * size;
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
+    const Span out[3] = {{"dx", T ? g.dx : nullptr, extent(T, g.dx_stride, H, 2), g.dx_stride},
+                         {"dgate_up", g.dgate_up, 2 * weight, H},
+                         {"ddown", g.ddown, weight, I}};
+    const auto check_results = [&] {
+        ep_status bad = EP_OK;
+        for (int o = 0; o < 3 && bad == EP_OK; ++o) {
+            for (int i = 0; i < o && bad == EP_OK; ++i)
+                bad = check_overlap(out[o], out[i], false);
+            if (bad == EP_OK)
+                bad = check_weights(out[o], h->cfg);
+        }
+        return bad;
+    };
     if (T == 0) {
+        st = check_results();
+        if (st != EP_OK)
+            return st;
         cudaError_t ce = cudaSuccess;
         if (g.dgate_up && !g.accumulate)
             ce = moe::launch_ffn_zero(g.dgate_up, 2 * weight, s);
@@ -620,17 +636,11 @@ ep_status ep_ffn_backward(ep_ffn *h, const ep_ffn_grads *grads, int num_tokens, 
     const Span in[3] = {{"dy", g.dy, extent(T, g.dy_stride, H, 2), g.dy_stride},
                         {"x", g.x, extent(T, g.x_stride, H, 2), g.x_stride},
                         {"saved", g.saved, extent(T, 2 * I, 2 * I, 4), 2 * I}};
-    const Span out[3] = {{"dx", g.dx, extent(T, g.dx_stride, H, 2), g.dx_stride},
-                         {"dgate_up", g.dgate_up, 2 * weight, H},
-                         {"ddown", g.ddown, weight, I}};
-    for (int o = 0; o < 3 && st == EP_OK; ++o) {
+    for (int o = 0; o < 3 && st == EP_OK; ++o)
         for (int i = 0; i < 3 && st == EP_OK; ++i)
             st = check_overlap(out[o], in[i], false);
-        for (int i = 0; i < o && st == EP_OK; ++i)
-            st = check_overlap(out[o], out[i], false);
-        if (st == EP_OK)
-            st = check_weights(out[o], h->cfg);
-    }
+    if (st == EP_OK)
+        st = check_results();
     const FfnLayout l(h, EP_FFN_BACKWARD, T);
     if (st == EP_OK)
         st = check_workspace(workspace, workspace_bytes, l.total);
