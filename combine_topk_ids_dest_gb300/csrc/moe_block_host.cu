@@ -12,29 +12,39 @@ namespace {
 
 int size_of(ep_dtype t) { return t == EP_DTYPE_FP32 ? 4 : 2; }
 
-// Bytes from the first to the last element of `rows` rows of `cols` elements, `stride` elements apart.
-size_t extent(long long rows, long long stride, long long cols, int size)
-{
-    return static_cast<size_t>((rows - 1) * stride + cols) * size;
-}
-
+// An operand's memory: `rows` rows of `row` bytes, `pitch` bytes apart; p NULL: not there, nor without rows.
 struct Span {
     const char *name;
-    const void *p;  // NULL: not there
-    size_t bytes;
-    long long stride;
+    const void *p;
+    long long rows;
+    size_t row, pitch;
 };
+
+// Rows of `cols` elements of `size` bytes, `stride` elements apart.
+Span rows_of(const char *name, const void *p, long long rows, long long cols, long long stride, int size)
+{
+    return {name, rows > 0 ? p : nullptr, rows, static_cast<size_t>(cols) * size, static_cast<size_t>(stride) * size};
+}
+Span whole(const char *name, const void *p, size_t bytes) { return {name, p, 1, bytes, bytes}; }
 
 bool overlap(const Span &a, const Span &b)
 {
+    if (!a.p || !b.p)
+        return false;
     const uintptr_t x = reinterpret_cast<uintptr_t>(a.p), y = reinterpret_cast<uintptr_t>(b.p);
-    return a.p && b.p && x < y + b.bytes && y < x + a.bytes;
+    if (x >= y + (b.rows - 1) * b.pitch + b.row || y >= x + (a.rows - 1) * a.pitch + a.row)
+        return false;
+    if (a.pitch != b.pitch)
+        return true;
+    // columns of the same rows: b's begin where a's have ended, and end before a's begin again
+    const size_t d = (y >= x ? y - x : a.pitch - (x - y) % a.pitch) % a.pitch;
+    return d < a.row || d + b.row > a.pitch;
 }
 
 // An output that overlaps an input; in_place: other than as the very same rows.
 ep_status check_overlap(const Span &out, const Span &in, bool in_place)
 {
-    if (overlap(out, in) && !(in_place && out.p == in.p && out.stride == in.stride))
+    if (overlap(out, in) && !(in_place && out.p == in.p && out.pitch == in.pitch))
         MOE_FAIL("%s overlaps %s", out.name, in.name);
     return EP_OK;
 }
@@ -65,7 +75,7 @@ ep_status check_norm(const ep_norm_config *c, int num_tokens)
     return EP_OK;
 }
 
-Span weight_span(const ep_norm_config &c) { return {"weight", c.weight, size_t(c.hidden) * size_of(c.weight_dtype), c.hidden}; }
+Span weight_span(const ep_norm_config &c) { return whole("weight", c.weight, size_t(c.hidden) * size_of(c.weight_dtype)); }
 
 // The current device for the norm's calls, whose kernels have no handle: set up when a device is first seen.
 ep_status norm_device(int *sms)
@@ -109,18 +119,19 @@ ep_status ep_norm_run(const ep_norm_config *cfg, const ep_norm_rows *rows, int n
         MOE_FAIL("residual_out without residual");
     if ((r.q == nullptr) != (r.scales == nullptr))
         MOE_FAIL("q and scales must be given together");
-    const Span all[4] = {{"x", r.x, extent(num_tokens, r.x_stride, H, size), r.x_stride},
-                         {"residual", r.residual, extent(num_tokens, r.residual_stride, H, size), r.residual_stride},
-                         {"residual_out", r.residual_out, extent(num_tokens, r.residual_out_stride, H, size), r.residual_out_stride},
-                         {"out", r.out, extent(num_tokens, r.out_stride, H, size), r.out_stride}};
-    for (const Span &s : all)
-        if (s.p || &s == all)
-            if ((st = check_rows(s.name, s.p, s.stride, H, 16, 8)) != EP_OK)
+    const long long strides[4] = {r.x_stride, r.residual_stride, r.residual_out_stride, r.out_stride};
+    const Span all[4] = {rows_of("x", r.x, num_tokens, H, r.x_stride, size),
+                         rows_of("residual", r.residual, num_tokens, H, r.residual_stride, size),
+                         rows_of("residual_out", r.residual_out, num_tokens, H, r.residual_out_stride, size),
+                         rows_of("out", r.out, num_tokens, H, r.out_stride, size)};
+    for (int i = 0; i < 4; ++i)
+        if (all[i].p || i == 0)
+            if ((st = check_rows(all[i].name, all[i].p, strides[i], H, 16, 8)) != EP_OK)
                 return st;
     if (!aligned(r.q, 8) || !aligned(r.scales, 4))
         MOE_FAIL("q is not 8-byte or scales not 4-byte aligned");
     const Span w = weight_span(*cfg);
-    const Span eight[2] = {{"q", r.q, extent(num_tokens, H, H, 1), H}, {"scales", r.scales, extent(num_tokens, groups, groups, 4), groups}};
+    const Span eight[2] = {whole("q", r.q, size_t(num_tokens) * H), whole("scales", r.scales, size_t(num_tokens) * groups * 4)};
     for (int o = 2; o < 4 && st == EP_OK; ++o)
         for (int i = 0; i < o && st == EP_OK; ++i)
             st = check_overlap(all[o], all[i], i < 2);
@@ -189,17 +200,15 @@ ep_status ep_norm_backward(const ep_norm_config *cfg, const void *dy, long long 
         MOE_FAIL("dweight is not 4-byte aligned");
     if ((!dx && !dweight) || (num_tokens == 0 && !dweight))
         return set_error(EP_OK, "");
-    if (num_tokens == 0)  // dweight is written all the same
-        dy = h = dh = dx = nullptr;
-    const Span in[4] = {{"dy", dy, extent(num_tokens, dy_stride, H, size), dy_stride},
-                        {"h", h, extent(num_tokens, h_stride, H, size), h_stride},
-                        {"dh", dh, extent(num_tokens, dh_stride, H, size), dh_stride},
-                        weight_span(*cfg)};
-    const Span out[2] = {{"dx", dx, extent(num_tokens, dx_stride, H, size), dx_stride}, {"dweight", dweight, size_t(H) * 4, H}};
-    for (int i = 0; i < 3 && st == EP_OK && num_tokens > 0; ++i)
+    const bool any = num_tokens > 0;  // dweight is written without rows too
+    const long long strides[3] = {dy_stride, h_stride, dh_stride};
+    const Span in[4] = {rows_of("dy", dy, num_tokens, H, dy_stride, size), rows_of("h", h, num_tokens, H, h_stride, size),
+                        rows_of("dh", dh, num_tokens, H, dh_stride, size), weight_span(*cfg)};
+    const Span out[2] = {rows_of("dx", dx, num_tokens, H, dx_stride, size), whole("dweight", dweight, size_t(H) * 4)};
+    for (int i = 0; i < 3 && st == EP_OK && any; ++i)
         if (i < 2 || dh)
-            st = check_rows(in[i].name, in[i].p, in[i].stride, H, 16, 8);
-    if (st == EP_OK && dx)
+            st = check_rows(in[i].name, in[i].p, strides[i], H, 16, 8);
+    if (st == EP_OK && dx && any)
         st = check_rows("dx", dx, dx_stride, H, 16, 8);
     for (int o = 0; o < 2 && st == EP_OK; ++o)
         for (int i = 0; i < 4 && st == EP_OK; ++i)
@@ -415,8 +424,8 @@ void plan(ep_ffn *h, int num_tokens, Launch &w)
 ep_status check_weights(const Span &out, const ep_ffn_config &c)
 {
     const size_t bytes = size_t(c.hidden) * c.intermediate * 2;
-    const ep_status st = check_overlap(out, {"gate_up", c.gate_up, 2 * bytes, c.hidden}, false);
-    return st == EP_OK ? check_overlap(out, {"down", c.down, bytes, c.intermediate}, false) : st;
+    const ep_status st = check_overlap(out, whole("gate_up", c.gate_up, 2 * bytes), false);
+    return st == EP_OK ? check_overlap(out, whole("down", c.down, bytes), false) : st;
 }
 
 // The intermediate rows, for the backward pass the gradients of gate and up too, and the parts of shared tiles.
@@ -549,8 +558,8 @@ ep_status ep_ffn_run(ep_ffn *h, const void *x, long long x_stride, int num_token
         return st;
     if (!aligned(saved, 16))
         MOE_FAIL("saved is not 16-byte aligned");
-    const Span in = {"x", x, extent(T, x_stride, H, 2), x_stride}, y = {"out", out, extent(T, out_stride, H, 2), out_stride},
-               keep = {"saved", saved, extent(T, 2 * I, 2 * I, 4), 2 * I};
+    const Span in = rows_of("x", x, T, H, x_stride, 2), y = rows_of("out", out, T, H, out_stride, 2),
+               keep = whole("saved", saved, size_t(T) * 2 * I * 4);
     const FfnLayout l(h, saved ? EP_FFN_FORWARD : EP_FFN_RUN, T);
     st = check_overlap(y, in, false);
     if (st == EP_OK)
@@ -600,9 +609,8 @@ ep_status ep_ffn_backward(ep_ffn *h, const ep_ffn_grads *grads, int num_tokens, 
     const int size = size_of(g.grad_dtype);
     const size_t weight = size_t(H) * I * size;
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
-    const Span out[3] = {{"dx", T ? g.dx : nullptr, extent(T, g.dx_stride, H, 2), g.dx_stride},
-                         {"dgate_up", g.dgate_up, 2 * weight, H},
-                         {"ddown", g.ddown, weight, I}};
+    const Span out[3] = {rows_of("dx", g.dx, T, H, g.dx_stride, 2), whole("dgate_up", g.dgate_up, 2 * weight),
+                         whole("ddown", g.ddown, weight)};
     const auto check_results = [&] {
         ep_status bad = EP_OK;
         for (int o = 0; o < 3 && bad == EP_OK; ++o) {
@@ -633,9 +641,8 @@ ep_status ep_ffn_backward(ep_ffn *h, const ep_ffn_grads *grads, int num_tokens, 
         return st;
     if (!g.saved || !aligned(g.saved, 16))
         MOE_FAIL("saved is NULL or not 16-byte aligned");
-    const Span in[3] = {{"dy", g.dy, extent(T, g.dy_stride, H, 2), g.dy_stride},
-                        {"x", g.x, extent(T, g.x_stride, H, 2), g.x_stride},
-                        {"saved", g.saved, extent(T, 2 * I, 2 * I, 4), 2 * I}};
+    const Span in[3] = {rows_of("dy", g.dy, T, H, g.dy_stride, 2), rows_of("x", g.x, T, H, g.x_stride, 2),
+                        whole("saved", g.saved, size_t(T) * 2 * I * 4)};
     for (int o = 0; o < 3 && st == EP_OK; ++o)
         for (int i = 0; i < 3 && st == EP_OK; ++i)
             st = check_overlap(out[o], in[i], false);

@@ -229,7 +229,8 @@ typedef struct {
  * then residual_out is too (s is x). Each of residual_out, out and the pair
  * q [num_tokens, hidden], scales [num_tokens, ceil(hidden / 128)] (contiguous;
  * q 8-byte, scales 4-byte aligned) may be NULL. residual_out and out may be x or residual themselves
- * (same address and stride); no other overlap, with weight neither. */
+ * (same address and stride); no other overlap, with weight neither. (Here and below: different
+ * columns of the rows of one buffer, of the same stride, do not overlap.) */
 typedef struct {
     const void *x;
     long long x_stride;

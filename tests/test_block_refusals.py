@@ -20,3 +20,29 @@ def test_gradients_of_no_rows_on_the_weights_refused(fake, ffn):
     # operands that have no rows may be anything
     assert _back(fake, n=0, dy=0, h=0, dh=0, dx=0) == OK, fake.message()
     assert _backward(fake, ffn, n=0, dy=0, x=0, saved=0, dx=0, workspace=None) == OK, fake.message()
+
+
+def test_columns_of_one_buffer_do_not_overlap(fake, ffn):
+    """x and its results as columns of a wider buffer's rows: no element is both."""
+    wide, at = 2 * H, AT[1]
+    rows = dict(x=at, x_stride=wide, residual=AT[2], residual_stride=wide, residual_out=at + 2 * H, residual_out_stride=wide,
+                out=AT[2] + 2 * H, out_stride=wide)
+    assert _norm(fake, **rows) == OK, fake.message()
+    for kw in (dict(residual_out=at + 2 * H - 16), dict(residual_out=at + 16), dict(residual_out=at + 4 * H - 16),
+               dict(residual_out=at + 2 * H, residual_out_stride=wide + 8), dict(residual_out=at + 2 * H, residual_out_stride=H)):
+        assert _norm(fake, **dict(rows, **kw)) == INVALID and "overlaps" in fake.message(), (kw, fake.message())
+    # a row further on, the columns beside still, or not
+    assert _norm(fake, **dict(rows, residual_out=at + 2 * wide + 2 * H)) == OK, fake.message()
+    assert _norm(fake, **dict(rows, residual_out=at + 2 * wide)) == INVALID
+    assert _norm(fake, **dict(rows, residual_out=at - 2 * wide + 2 * H)) == OK, fake.message()
+    assert _norm(fake, **dict(rows, residual_out=at - 2 * wide)) == INVALID
+    back = dict(dy=at, dy_stride=wide, dx=at + 2 * H, dx_stride=wide)
+    assert _back(fake, **back) == OK, fake.message()
+    assert _back(fake, **dict(back, dx=at + 16)) == INVALID
+    at = AT[9]  # AT[0] and AT[1] are the block's weights
+    assert _run(fake, ffn, x=at, x_stride=wide, out=at + 2 * H, out_stride=wide) == OK, fake.message()
+    at = AT[9]  # AT[0] and AT[1] are the block's weights
+    assert _run(fake, ffn, x=at, x_stride=wide, out=at + 2 * H - 2, out_stride=wide) == INVALID
+    assert _backward(fake, ffn, dy=at, dy_stride=wide, dx=at + 2 * H, dx_stride=wide) == OK, fake.message()
+    # rows of another kind may lie between, too: a row of the weights' gradients is no row of x
+    assert _backward(fake, ffn, dy=at, dy_stride=wide, dgate_up=at + 2 * H) == INVALID
