@@ -31,7 +31,8 @@ constexpr int kUnit = 8;             // columns that a thread takes at a time
 constexpr int kBackThreads = 17 * 32;  // of the backward pass: 16 warps that compute, one that copies
 constexpr int kFewUnits = 2, kMostUnits = 4;  // units of a lane: the more up to 16384 columns in 16 warps
 constexpr int kBackStages = 32, kBackRing = 200 * 1024;
-constexpr float kScaled = 0x1p-80f;  // squares of rows whose sum exceeds fp32 are taken of s * this
+constexpr float kScaled = 0x1p-80f;  // squares of rows whose sum exceeds fp32 are taken of s * this, of small rows of s / this
+constexpr float kLeastMean = 0x1p-80f;  // of squares, with eps: what is below fp32's 2^-149 is nothing next to it
 
 struct Raw16 {
     uint4 v;
@@ -186,16 +187,20 @@ static __device__ __forceinline__ void team_sums(float (&v)[2], float (*slots)[1
     v[1] = __shfl_sync(~0u, x, 16);
 }
 
-// 1 / sqrt(sum / H + eps); for a sum of squares of finite values that exceeds fp32, from the sum of (s kScaled)^2,
-// next to which eps is nothing.
-static __device__ __forceinline__ float rstd_of(float sum, int H, float eps)
-{
-    return 1.0f / sqrtf(sum / static_cast<float>(H) + eps);
-}
-static __device__ __forceinline__ float rstd_scaled(float sum, int H)
-{
-    return kScaled / sqrtf(sum / static_cast<float>(H));
-}
+// r = 1 / sqrt(sum / H + eps) of a sum of squares. Where that leaves fp32 (an infinite sum of finite values, or so little
+// that squares may have vanished), the sum is taken again of (s f)^2, f a power of two: r = f / sqrt(sum / H + eps f^2).
+struct Root {
+    float mean, rstd;
+    __device__ __forceinline__ Root(float sum, int H, float eps) : mean(sum / static_cast<float>(H) + eps), rstd(1.0f / sqrtf(mean)) {}
+    // with eps above the one no square counts that vanished; NaN stays NaN
+    __device__ __forceinline__ bool left() const { return mean < kLeastMean || isinf(mean); }
+    __device__ __forceinline__ float factor() const { return mean < kLeastMean ? 1.0f / kScaled : kScaled; }
+    __device__ __forceinline__ void again(float sum, int H, float eps)
+    {
+        const float f = factor();
+        rstd = f / sqrtf(sum / static_cast<float>(H) + eps * f * f);
+    }
+};
 
 // blockDim (threads of a row, rows of a block); thread i of a row has its units i, i + blockDim.x, ...: U of them.
 template <class T, int U> __global__ void __launch_bounds__(1024) norm_kernel(const __grid_constant__ NormArgs a)
@@ -242,17 +247,19 @@ template <class T, int U> __global__ void __launch_bounds__(1024) norm_kernel(co
         }
     }
     row_sums<1>(sum, slots[threadIdx.y][0], warps, warp, lane);
-    float rstd = rstd_of(sum[0], a.H, a.eps);
-    if (isinf(sum[0])) {  // rare: squares that exceed fp32; the same in all threads of the row
+    Root root(sum[0], a.H, a.eps);
+    if (root.left()) {  // rare; the same in all threads of the row
+        const float f = root.factor();
         float again[1] = {0.0f};
 #pragma unroll
         for (int i = 0; i < U; ++i)
 #pragma unroll
             for (int j = 0; j < kUnit; ++j)
-                again[0] = fmaf(s[i][j] * kScaled, s[i][j] * kScaled, again[0]);
+                again[0] = fmaf(s[i][j] * f, s[i][j] * f, again[0]);
         row_sums<1>(again, slots[threadIdx.y][1], warps, warp, lane);
-        rstd = rstd_scaled(again[0], a.H);
+        root.again(again[0], a.H, a.eps);
     }
+    const float rstd = root.rstd;
 #pragma unroll
     for (int i = 0; i < U; ++i) {
         const int u = threadIdx.x + i * blockDim.x;
@@ -454,8 +461,10 @@ template <class T, int U> __global__ void __launch_bounds__(kBackThreads, 1) bac
                     }
                 float sum[2] = {sums[0].x + sums[0].y, sums[1].x + sums[1].y};
                 team_sums(sum, slots[team][turn], a.team, place, team, lane);
-                float rstd = rstd_of(sum[0], a.H, a.eps), mean = rstd * sum[1] / static_cast<float>(a.H);  // of g n
-                if (!isfinite(sum[0]) || !isfinite(sum[1])) {  // squares that exceed fp32; the same in all threads of the team
+                Root root(sum[0], a.H, a.eps);
+                float mean = root.rstd * sum[1] / static_cast<float>(a.H);  // of g n
+                if (root.left() || !isfinite(sum[1])) {  // rare; the same in all threads of the team
+                    const float f = root.factor();
                     float again[2] = {0.0f, 0.0f};
                     for (int u = place * 32 + lane; u < units; u += a.team * 32) {
                         float h[kUnit], dy[kUnit], wu[kUnit];
@@ -464,19 +473,18 @@ template <class T, int U> __global__ void __launch_bounds__(kBackThreads, 1) bac
                         load_weight<T>(a.weight, a.weight_fp32, u, wu);
 #pragma unroll
                         for (int j = 0; j < kUnit; ++j) {
-                            again[0] = fmaf(h[j] * kScaled, h[j] * kScaled, again[0]);
-                            again[1] = fmaf(dy[j] * wu[j], h[j] * kScaled, again[1]);
+                            again[0] = fmaf(h[j] * f, h[j] * f, again[0]);
+                            again[1] = fmaf(dy[j] * wu[j], h[j] * f, again[1]);
                         }
                     }
-                    const bool large = isinf(sum[0]);
                     if (a.team > 1)
                         named_sync(1 + team, a.team * 32);  // the slots are read
                     team_sums(again, slots[team][turn], a.team, place, team, lane);
-                    if (large)
-                        rstd = rstd_scaled(again[0], a.H);
-                    mean = rstd / kScaled * again[1] / static_cast<float>(a.H);
+                    if (root.left())
+                        root.again(again[0], a.H, a.eps);
+                    mean = root.rstd / f * again[1] / static_cast<float>(a.H);
                 }
-                const float2 r2 = make_float2(rstd, rstd);
+                const float2 r2 = make_float2(root.rstd, root.rstd);
                 // h r is n, which may be large where r^2 alone is too small for fp32
                 const float2 m2 = make_float2(-mean, -mean);
                 const long long t = t0 + row;

@@ -210,8 +210,8 @@ ep_status ep_layer_run(ep_router *r, ep_experts *h, const void *x, long long x_s
  * as ep_dispatch carries them: for each EP_SCALE_GROUP columns (the last
  * group may have fewer) scale = max(max |y| / 448, 2^-126), q = y / scale
  * rounded to e4m3, from the unrounded y; a group with an infinite or NaN y has
- * a NaN scale and NaN codes. Rows whose sum of squares exceeds fp32 keep their
- * value (the sum is taken again, scaled).
+ * a NaN scale and NaN codes. Rows whose squares leave fp32, above or next to a
+ * tiny eps below, keep their value (the sum is taken again, scaled).
  */
 #define EP_NORM_MAX_HIDDEN 16384
 #define EP_NORM_MAX_TOKENS 2147483647 /* rows of one call */
