@@ -202,6 +202,14 @@ struct Root {
     }
 };
 
+// Four values in e4m3.
+static __device__ __forceinline__ uint32_t codes(float a, float b, float c, float d)
+{
+    const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
+    const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(c, d), __NV_SATFINITE, __NV_E4M3);
+    return lo | (hi << 16);
+}
+
 // blockDim (threads of a row, rows of a block); thread i of a row has its units i, i + blockDim.x, ...: U of them.
 template <class T, int U> __global__ void __launch_bounds__(1024) norm_kernel(const __grid_constant__ NormArgs a)
 {
@@ -285,16 +293,18 @@ template <class T, int U> __global__ void __launch_bounds__(1024) norm_kernel(co
                 most = max(most, __shfl_xor_sync(~0u, most, d));
             const float scale = most >= 0x7F800000u ? __uint_as_float(0x7FC00000u)
                                                     : fmaxf(__uint_as_float(most) / 448.0f, 0x1p-126f);
-            const float inverse = 1.0f / scale;
             if (mine) {
+                // Codes of y / scale. A division for each y takes 16001 x 7168 from 155 to 167 us: where the products with a
+                // little less and a little more than 1 / scale have the same code, so has the quotient. (1 / scale, what is
+                // more or less, the product and the quotient itself are each off by 2^-24 at most, together 2^-22.)
+                const float inverse = 1.0f / scale, less = inverse * (1.0f - 0x1p-21f), more = inverse * (1.0f + 0x1p-21f);
                 uint32_t w[2];
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
-                    const uint32_t lo = __nv_cvt_float2_to_fp8x2(
-                        make_float2(y[4 * j] * inverse, y[4 * j + 1] * inverse), __NV_SATFINITE, __NV_E4M3);
-                    const uint32_t hi = __nv_cvt_float2_to_fp8x2(
-                        make_float2(y[4 * j + 2] * inverse, y[4 * j + 3] * inverse), __NV_SATFINITE, __NV_E4M3);
-                    w[j] = lo | (hi << 16);
+                    const float *const v = y + 4 * j;
+                    w[j] = codes(v[0] * less, v[1] * less, v[2] * less, v[3] * less);
+                    if (w[j] != codes(v[0] * more, v[1] * more, v[2] * more, v[3] * more))
+                        w[j] = codes(v[0] / scale, v[1] / scale, v[2] / scale, v[3] / scale);
                 }
                 uint2 *const q = reinterpret_cast<uint2 *>(a.q + t * a.H) + u;
                 if (EP_IN_BOUNDS(a.chk, epk::kSiteMoeOut, q, 8, a.q, a.T * static_cast<long long>(a.H)))
