@@ -82,18 +82,27 @@ static __host__ __device__ __forceinline__ uint32_t tmem_columns(int n)
     return n <= 32 ? 32 : n <= 64 ? 64 : n <= 128 ? 128 : 256;
 }
 
-// silu of g and its derivative, to some 5e-6 of their values (the fast exponential and division; the results are rounded
-// to 2^-8). Far below zero exp(-g) is infinite and sigma 0; from 17 on sigma is 1 and 1 - sigma 0, which in between is
-// 6e-8 off at most, g times that in the derivative.
-static __device__ __forceinline__ float silu(float g) { return __fdividef(g, 1.0f + __expf(-g)); }
+// silu of g and its derivative, to some 1e-5 of their values (the fast exponential and division; the results are rounded
+// to 2^-8). From exp(-|g|), so that the divisor lies in [1, 2] and sigma and 1 - sigma keep their value down to fp32's
+// smallest numbers (1 / (1 + exp(-g)) is 0 from g = -87.4 on).
+struct Sigma {
+    float s, rest;  // sigma and 1 - sigma
+    __device__ __forceinline__ explicit Sigma(float g)
+    {
+        const float x = __expf(-fabsf(g)), large = __fdividef(1.0f, 1.0f + x), small = x * large;
+        s = g < 0.0f ? small : large;
+        rest = g < 0.0f ? large : small;
+    }
+};
+static __device__ __forceinline__ float silu(float g) { return g * Sigma(g).s; }
 
 struct Gate {
     float silu, slope;
     __device__ __forceinline__ explicit Gate(float g)
     {
-        const float s = __fdividef(1.0f, 1.0f + __expf(-g));
-        silu = g * s;
-        slope = s * fmaf(g, 1.0f - s, 1.0f);
+        const Sigma sigma(g);
+        silu = g * sigma.s;
+        slope = sigma.s * fmaf(g, sigma.rest, 1.0f);
     }
 };
 
