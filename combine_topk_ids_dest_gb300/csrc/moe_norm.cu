@@ -384,6 +384,7 @@ template <class T, int U> __global__ void __launch_bounds__(kBackThreads, 1) bac
 
     if (warp == kBackThreads / 32 - 1) {
         // ---- copies ----
+        fence_async_proxy();  // what the kernel before stored from registers is read by copies
         int s = 0, i = 0;
         uint32_t parity = 0;
         for (; i < mine; ++i) {
