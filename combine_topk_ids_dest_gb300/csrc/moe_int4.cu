@@ -442,6 +442,8 @@ __global__ void __launch_bounds__(kThreads, 1) int4_kernel(const __grid_constant
     } else if (warp > kCopyWarp && elect_one()) {
         // ---- token tiles ----
         const int half = warp - kCopyWarp - 1;
+        if (LINEAR)
+            fence_async_global();  // what the kernel before stored from registers is read by copies
         Cursor at;
         int issued = 0;
         bool run = true;
