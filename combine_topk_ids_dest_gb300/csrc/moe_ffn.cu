@@ -340,6 +340,7 @@ template <int EPI, bool GRAD> __global__ void __launch_bounds__(128 + kPairStore
         sh.issued = issued;
     } else if (warp == 1) {
         // ---- matrix instructions, in the first block ----
+        pdl_wait();  // waits are for this kernel's copies: the kernel before may take longer than their limit
         Cursor at, at_d;
         bool run = rank == 0;
         Item it;
@@ -676,6 +677,7 @@ template <int EPI> __global__ void __launch_bounds__(128 + kSplitStore, 2) split
         sh.issued = issued;
     } else if (warp == 1) {
         // ---- matrix instructions ----
+        pdl_wait();  // waits are for this kernel's copies: the kernel before may take longer than their limit
         Cursor at;
         for (int c = c0; c < c1; ++c) {
             if (!mbar_wait_warp(smem_u32(&sh.full[at.s]), at.parity, abort, kWaitFullA))
@@ -696,6 +698,7 @@ template <int EPI> __global__ void __launch_bounds__(128 + kSplitStore, 2) split
     // ---- this block's sums into its memory, then a share of the rows from all of the cluster's ----
     float *const sums = reinterpret_cast<float *>(dyn + (ring - dyn0));  // [rows][128 features]
     if (warp >= kFirstStore) {
+        pdl_wait();
         const bool run = mbar_wait(smem_u32(&sh.full_d[0]), 0, abort, kWaitFullD);
         if (named_all(1, kSplitStore, run)) {
             tc_fence_after();
