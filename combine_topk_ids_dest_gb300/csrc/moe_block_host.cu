@@ -428,27 +428,26 @@ ep_status check_weights(const Span &out, const ep_ffn_config &c)
     return st == EP_OK ? check_overlap(out, whole("down", c.down, bytes), false) : st;
 }
 
-// The intermediate rows, for the backward pass the gradients of gate and up too, and the parts of shared tiles.
+// The intermediate rows, for the backward pass the gradients of gate and up too, then the parts of shared tiles.
 struct FfnLayout {
-    size_t off_dgu, off_parts, total;
-    FfnLayout(ep_ffn *h, ep_ffn_call call, int num_tokens)
+    size_t off_dgu, off_parts;
+    FfnLayout(const ep_ffn_config &c, bool backward, int num_tokens)
     {
-        const size_t row = size_t(h->cfg.intermediate) * 2;
+        const size_t row = size_t(c.intermediate) * 2;
         off_dgu = align256(num_tokens * row);
-        off_parts = off_dgu + (call == EP_FFN_BACKWARD ? align256(num_tokens * 2 * row) : 0);
-        total = off_parts;
-        if (num_tokens == 0)
-            return;
-        size_t parts = size_t(2 * moe::kFfnMaxPairs) * 256 * 128 * sizeof(float);  // whichever gradients are asked for
-        if (call != EP_FFN_BACKWARD) {
-            Launch first = join_of(h->cfg, num_tokens, nullptr, 0, nullptr, nullptr), second = down_of(h->cfg, num_tokens, nullptr, nullptr, 0);
-            plan(h, num_tokens, first);
-            plan(h, num_tokens, second);
-            parts = first.l.parts > second.l.parts ? first.l.parts : second.l.parts;
-        }
-        total += align256(parts);
+        off_parts = off_dgu + (backward ? align256(num_tokens * 2 * row) : 0);
     }
 };
+
+// Bytes of shared tiles' parts: only products that make gradients have such tiles, and only where their plan cuts rounds.
+size_t parts_of(ep_ffn *h, int num_tokens, const ep_ffn_grads &g)
+{
+    Launch w = gradients_of(h->cfg, num_tokens, g, nullptr, nullptr);
+    if (num_tokens == 0 || w.l.q.count == 0)
+        return 0;
+    plan(h, num_tokens, w);
+    return align256(w.l.parts);
+}
 
 ep_status launch(ep_ffn *h, int num_tokens, Launch &w, void *parts, epk::CheckCtx chk, cudaStream_t s)
 {
@@ -535,7 +534,17 @@ ep_status ep_ffn_workspace_size(ep_ffn *h, ep_ffn_call call, int num_tokens, siz
         MOE_FAIL("bytes is NULL");
     if (call != EP_FFN_RUN && call != EP_FFN_FORWARD && call != EP_FFN_BACKWARD)
         MOE_FAIL("unknown call %d", static_cast<int>(call));
-    *bytes = FfnLayout(h, call, num_tokens).total;
+    *bytes = FfnLayout(h->cfg, call == EP_FFN_BACKWARD, num_tokens).off_parts;
+    size_t parts = 0;
+    for (int asked = 1; asked < 8 && call == EP_FFN_BACKWARD; ++asked) {  // whichever gradients a call wants
+        ep_ffn_grads g = {};
+        g.dx = asked & 1 ? h : nullptr;
+        g.dgate_up = asked & 2 ? h : nullptr;
+        g.ddown = asked & 4 ? h : nullptr;
+        const size_t here = parts_of(h, num_tokens, g);
+        parts = here > parts ? here : parts;
+    }
+    *bytes += parts;
     return set_error(EP_OK, "");
 }
 
@@ -560,7 +569,6 @@ ep_status ep_ffn_run(ep_ffn *h, const void *x, long long x_stride, int num_token
         MOE_FAIL("saved is not 16-byte aligned");
     const Span in = rows_of("x", x, T, H, x_stride, 2), y = rows_of("out", out, T, H, out_stride, 2),
                keep = whole("saved", saved, size_t(T) * 2 * I * 4);
-    const FfnLayout l(h, saved ? EP_FFN_FORWARD : EP_FFN_RUN, T);
     st = check_overlap(y, in, false);
     if (st == EP_OK)
         st = check_overlap(keep, in, false);
@@ -571,7 +579,7 @@ ep_status ep_ffn_run(ep_ffn *h, const void *x, long long x_stride, int num_token
     if (st == EP_OK)
         st = check_weights(keep, h->cfg);
     if (st == EP_OK)
-        st = check_workspace(workspace, workspace_bytes, l.total);
+        st = check_workspace(workspace, workspace_bytes, FfnLayout(h->cfg, false, T).off_parts);
     if (st == EP_OK)
         st = h->flags.take();
     if (st != EP_OK)
@@ -579,11 +587,10 @@ ep_status ep_ffn_run(ep_ffn *h, const void *x, long long x_stride, int num_token
     unsigned long long *rec = epk::check_record();
     const epk::CheckCtx chk = epk::check_ctx(rec);
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
-    void *const parts = static_cast<uint8_t *>(workspace) + l.off_parts;
     Launch first = join_of(h->cfg, T, x, x_stride, workspace, saved), second = down_of(h->cfg, T, workspace, out, out_stride);
-    st = launch(h, T, first, parts, chk, s);
+    st = launch(h, T, first, nullptr, chk, s);
     if (st == EP_OK)
-        st = launch(h, T, second, parts, chk, s);
+        st = launch(h, T, second, nullptr, chk, s);
     return st == EP_OK ? finish(cudaSuccess, "ep_ffn_run", rec, s) : st;
 }
 
@@ -648,9 +655,9 @@ ep_status ep_ffn_backward(ep_ffn *h, const ep_ffn_grads *grads, int num_tokens, 
             st = check_overlap(out[o], in[i], false);
     if (st == EP_OK)
         st = check_results();
-    const FfnLayout l(h, EP_FFN_BACKWARD, T);
+    const FfnLayout l(h->cfg, true, T);
     if (st == EP_OK)
-        st = check_workspace(workspace, workspace_bytes, l.total);
+        st = check_workspace(workspace, workspace_bytes, l.off_parts + parts_of(h, T, g));
     if (st == EP_OK)
         st = h->flags.take();
     if (st != EP_OK)

@@ -46,3 +46,45 @@ def test_columns_of_one_buffer_do_not_overlap(fake, ffn):
     assert _backward(fake, ffn, dy=at, dy_stride=wide, dx=at + 2 * H, dx_stride=wide) == OK, fake.message()
     # rows of another kind may lie between, too: a row of the weights' gradients is no row of x
     assert _backward(fake, ffn, dy=at, dy_stride=wide, dgate_up=at + 2 * H) == INVALID
+
+
+def _size(fake, h, call, n):
+    size = ctypes.c_size_t(0)
+    assert fake.L.ep_ffn_workspace_size(h, call, n, ctypes.byref(size)) == OK
+    return size.value
+
+
+def test_ffn_workspaces_are_what_the_calls_use(fake):
+    """h's rows; for the gradients those of gate and up, and parts of tiles only where pairs share them."""
+    up = lambda n: (n + 255) // 256 * 256  # noqa: E731
+    shared = 0
+    for hidden, intermediate in ((8, 8), (2056, 1400), (512, 8192), (4096, 14336)):
+        st, h = _ffn(fake, hidden=hidden, intermediate=intermediate, gate_up=AT[9], down=AT[10])
+        assert st == OK
+        for n in (1, 64, 300, 700, 1999, 4096):
+            rows = up(n * intermediate * 2)
+            assert _size(fake, h, 0, n) == _size(fake, h, 1, n) == rows
+            both = rows + up(n * intermediate * 4)
+            size = _size(fake, h, 2, n)
+            assert size == both or size == both + 2 * 76 * 256 * 128 * 4
+            shared += size > both
+            # it is enough for any of the gradients, one byte less is refused where a call uses all
+            far = dict(zip(("dy", "x", "saved", "dx", "dgate_up", "ddown"), (k << 48 for k in range(1, 7))))
+            strides = dict(dy_stride=hidden, x_stride=hidden, dx_stride=hidden)
+            for skip in ((), ("dx",), ("dgate_up",), ("ddown",), ("dx", "ddown"), ("dgate_up", "ddown"), ("dx", "dgate_up")):
+                ops = dict(far, **{k: 0 for k in skip})
+                assert _backward(fake, h, n, bytes=size, **strides, **ops) == OK, fake.message()
+            refused = [_backward(fake, h, n, bytes=size - 1, **strides, **dict(far, **{k: 0 for k in skip})) == INVALID
+                       for skip in ((), ("dx",), ("dgate_up",), ("ddown",), ("dx", "ddown"), ("dgate_up", "ddown"), ("dx", "dgate_up"))]
+            assert any(refused)
+        assert _size(fake, h, 2, 0) == _size(fake, h, 0, 0) == 0
+        assert fake.L.ep_ffn_destroy(h) == OK
+    assert 0 < shared < 24
+
+
+def test_ffn_backward_reports_a_wait_that_ran_out_once(fake, ffn):
+    words = fake.L.fake_error_words()
+    fake.L.fake_clear()
+    words[0] = words[4] = 1
+    assert _backward(fake, ffn) == _lib.EP_ERR_CUDA and "ran out" in fake.message() and fake.launches() == []
+    assert _backward(fake, ffn) == OK and len(fake.launches()) == 2
