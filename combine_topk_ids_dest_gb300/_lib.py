@@ -53,8 +53,6 @@ MOE_EXPORTS = ("ep_router_create", "ep_router_workspace_size", "ep_router_run", 
                "ep_linear_run", "ep_linear_destroy", "ep_layer_run",
                "ep_norm_run", "ep_norm_backward_workspace_size", "ep_norm_backward",
                "ep_ffn_create", "ep_ffn_workspace_size", "ep_ffn_run", "ep_ffn_backward", "ep_ffn_destroy")
-EP_NORM_MAX_HIDDEN = 16384
-EP_FFN_MAX_TOKENS = 16777216
 EP_FFN_RUN = 0
 EP_FFN_FORWARD = 1
 EP_FFN_BACKWARD = 2

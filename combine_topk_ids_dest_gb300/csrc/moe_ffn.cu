@@ -16,6 +16,12 @@
 // and up joined (a block's 128 MMA rows are 64 of gate and the same 64 of up),
 // or the gradient of h split into those of gate and up.
 //
+// Roundings: sums, g and u are fp32, y and the gradients are rounded once. h, and
+// the gradients of g and u, are rounded to bf16 before the product that takes
+// them: a result's error is then 1.41 times its own rounding's. In two bf16 parts,
+// as the experts' kernels keep h for a few rows, that product would take twice the
+// MMAs, which bound it for many rows.
+//
 // Two kernels:
 //  - pairs: two neighbouring blocks multiply together (cta_group::2), 256
 //    features x up to 256 rows a tile, persistent, accumulators in two halves of

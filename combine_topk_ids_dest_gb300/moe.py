@@ -10,6 +10,9 @@ with their gradients. All work runs in the CUDA library on
 torch's current stream of the tensors' device; torch supplies device memory
 and streams only. Weights are kept by reference, not copied.
 
+Gradients are calls of their own (``backward``): a result has no autograd graph,
+whatever ``requires_grad`` its inputs and weights have.
+
 Calls on one object must be ordered on the device (one stream, or streams
 with events between them): it holds one call's intermediate results. Create
 objects, and let them go, outside CUDA graph captures; calls can be captured.
@@ -365,7 +368,7 @@ class EpNorm(_OnDevice):
     ``y = s / sqrt(mean(s * s) + eps) * weight``, in fp32.
 
     ``weight`` [hidden] is of the rows' type or float32; ``dtype``, the rows' type (bfloat16, float16 or
-    float32), is the weight's unless given.
+    float32), is the weight's unless given. Results have no autograd graph: gradients come from :meth:`backward`.
     """
 
     def __init__(self, weight: torch.Tensor, eps: float = 1e-6, dtype: Optional[torch.dtype] = None):
@@ -457,7 +460,9 @@ class EpFfn(_Handle):
     ``y = (silu(x @ W1.T) * (x @ W3.T)) @ W2.T``, for any number of tokens, and its gradients.
 
     ``gate_up`` bf16 [2*intermediate, hidden] (W1's rows, then W3's) and ``down`` bf16 [hidden, intermediate]
-    are kept by reference; each call reads their present values.
+    are kept by reference; each call reads their present values. The intermediate rows are rounded to bf16 once
+    (:class:`EpExperts` keeps them in two parts: the same weights give its result within one rounding, this one's
+    with 1.41 times that error). Results have no autograd graph: gradients come from :meth:`backward`.
     """
 
     _destroy = "ep_ffn_destroy"
