@@ -48,7 +48,7 @@
 // rows DRAM and a fixed part of some 4 us a kernel, of which the wait for the kernel
 // before, the first copy and the results are one each: one row, 7168 x 2048, 19.4
 // us, 14 of them at 6.6 TB/s; 128 rows 24.7. Rows whose length is no multiple of 128
-// bytes cost up to a quarter more (2056 x 1400 against 2048 x 1408: 109 and 88 us):
+// bytes cost up to a quarter more (2056 x 1400 against 2048 x 1408: 110 and 88 us):
 // each of a tile's rows lies in two lines.
 #include <cmath>
 

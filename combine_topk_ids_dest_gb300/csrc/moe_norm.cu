@@ -8,15 +8,15 @@
 // unit; a block has one row, or several of one warp. Backward, one persistent
 // block an SM takes rows from a ring of shared memory that bulk copies fill:
 // with the loads in registers too few were on their way, and the sums of dw need
-// the registers (8192 x 4096 60 us, now 45). Its arithmetic is two numbers an
+// the registers (8192 x 4096 60 us, now 47). Its arithmetic is two numbers an
 // instruction: near the rate of instructions otherwise (69 us).
 //
 // What bounds them: DRAM. bf16 rows with residual and 8-bit rows, 16001 x 7168
-// (1.04 GB) 151 us, 6.8 TB/s, the rate of a copy; backward with dh, 8192 x 4096
-// (268 MB) 46 us, 5.8 TB/s, 3 of them the sum of the blocks' parts of dw. Narrow
-// rows reach 5.4 to 6 TB/s (16000 x 256 6.9 us). A few rows are launch and one
-// trip to memory: one row of 4096 2.0 us, 128 of 7168 3.3 us in a graph. Rows of
-// more than 8192 columns spill registers backward (4000 x 16384 150 us, 3.5 TB/s).
+// (1.04 GB) 153 us, 6.8 TB/s, the rate of a copy (fp32 316, 6.2 TB/s); backward with dh, 8192 x 4096
+// (268 MB) 46 to 48 us, 5.7 TB/s, 3 of them the sum of the blocks' parts of dw. Narrow
+// rows reach 5.3 to 6 TB/s (16000 x 256 7.0 us). A few rows are launch and one
+// trip to memory: one row of 4096 2.0 us, 128 of 7168 3.4 us in a graph. Rows of
+// more than 8192 columns spill registers backward (4000 x 16384 142 us, 3.7 TB/s).
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
 
@@ -202,11 +202,28 @@ struct Root {
     }
 };
 
-// Four values in e4m3.
-static __device__ __forceinline__ uint32_t codes(float a, float b, float c, float d)
+// Two fp32 numbers at a time (one instruction each; both kernels would be near the rate of instructions otherwise).
+static __device__ __forceinline__ uint64_t as64(float2 v) { return *reinterpret_cast<uint64_t *>(&v); }
+static __device__ __forceinline__ float2 as2(uint64_t v) { return *reinterpret_cast<float2 *>(&v); }
+static __device__ __forceinline__ float2 mul2(float2 a, float2 b)
 {
-    const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
-    const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(c, d), __NV_SATFINITE, __NV_E4M3);
+    uint64_t d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(as64(a)), "l"(as64(b)));
+    return as2(d);
+}
+static __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c)
+{
+    uint64_t d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(as64(a)), "l"(as64(b)), "l"(as64(c)));
+    return as2(d);
+}
+constexpr int kPairs = kUnit / 2;
+
+// Four values in e4m3.
+static __device__ __forceinline__ uint32_t codes(float2 a, float2 b)
+{
+    const uint32_t lo = __nv_cvt_float2_to_fp8x2(a, __NV_SATFINITE, __NV_E4M3);
+    const uint32_t hi = __nv_cvt_float2_to_fp8x2(b, __NV_SATFINITE, __NV_E4M3);
     return lo | (hi << 16);
 }
 
@@ -280,9 +297,11 @@ template <class T, int U> __global__ void __launch_bounds__(1024) norm_kernel(co
             float w[kUnit];
             load_weight<T>(a.weight, a.weight_fp32, u, w);
 #pragma unroll
-            for (int j = 0; j < kUnit; ++j) {
-                y[j] = s[i][j] * rstd * w[j];
-                most = max(most, __float_as_uint(fabsf(y[j])));
+            for (int j = 0; j < kUnit; j += 2) {
+                const float2 v = mul2(mul2(make_float2(s[i][j], s[i][j + 1]), make_float2(rstd, rstd)), make_float2(w[j], w[j + 1]));
+                y[j] = v.x;
+                y[j + 1] = v.y;
+                most = max(most, max(__float_as_uint(fabsf(v.x)), __float_as_uint(fabsf(v.y))));
             }
             if (a.out && EP_IN_BOUNDS(a.chk, epk::kSiteMoeOut, unit_at<T>(a.out, a.out_stride, t, u), sizeof(Unit<T>), a.out, sizeof(T) * ((a.T - 1LL) * a.out_stride + a.H)))
                 store_unit<T>(unit_at<T>(a.out, a.out_stride, t, u), y);
@@ -294,17 +313,18 @@ template <class T, int U> __global__ void __launch_bounds__(1024) norm_kernel(co
             const float scale = most >= 0x7F800000u ? __uint_as_float(0x7FC00000u)
                                                     : fmaxf(__uint_as_float(most) / 448.0f, 0x1p-126f);
             if (mine) {
-                // Codes of y / scale. A division for each y takes 16001 x 7168 from 155 to 167 us: where the products with a
+                // Codes of y / scale. A division for each y takes 16001 x 7168 from 153 to some 165 us: where the products with a
                 // little less and a little more than 1 / scale have the same code, so has the quotient. (1 / scale, what is
                 // more or less, the product and the quotient itself are each off by 2^-24 at most, together 2^-22.)
-                const float inverse = 1.0f / scale, less = inverse * (1.0f - 0x1p-21f), more = inverse * (1.0f + 0x1p-21f);
+                const float inverse = 1.0f / scale, l = inverse * (1.0f - 0x1p-21f), m = inverse * (1.0f + 0x1p-21f);
+                const float2 less = make_float2(l, l), more = make_float2(m, m);
                 uint32_t w[2];
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
-                    const float *const v = y + 4 * j;
-                    w[j] = codes(v[0] * less, v[1] * less, v[2] * less, v[3] * less);
-                    if (w[j] != codes(v[0] * more, v[1] * more, v[2] * more, v[3] * more))
-                        w[j] = codes(v[0] / scale, v[1] / scale, v[2] / scale, v[3] / scale);
+                    const float2 a2 = make_float2(y[4 * j], y[4 * j + 1]), b2 = make_float2(y[4 * j + 2], y[4 * j + 3]);
+                    w[j] = codes(mul2(a2, less), mul2(b2, less));
+                    if (w[j] != codes(mul2(a2, more), mul2(b2, more)))
+                        w[j] = codes(make_float2(a2.x / scale, a2.y / scale), make_float2(b2.x / scale, b2.y / scale));
                 }
                 uint2 *const q = reinterpret_cast<uint2 *>(a.q + t * a.H) + u;
                 if (EP_IN_BOUNDS(a.chk, epk::kSiteMoeOut, q, 8, a.q, a.T * static_cast<long long>(a.H)))
@@ -317,23 +337,6 @@ template <class T, int U> __global__ void __launch_bounds__(1024) norm_kernel(co
         }
     }
 }
-
-// Two fp32 numbers at a time (one instruction each; the kernel below is near the rate of instructions otherwise).
-static __device__ __forceinline__ uint64_t as64(float2 v) { return *reinterpret_cast<uint64_t *>(&v); }
-static __device__ __forceinline__ float2 as2(uint64_t v) { return *reinterpret_cast<float2 *>(&v); }
-static __device__ __forceinline__ float2 mul2(float2 a, float2 b)
-{
-    uint64_t d;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(as64(a)), "l"(as64(b)));
-    return as2(d);
-}
-static __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c)
-{
-    uint64_t d;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(as64(a)), "l"(as64(b)), "l"(as64(c)));
-    return as2(d);
-}
-constexpr int kPairs = kUnit / 2;
 
 template <class T> static __device__ __forceinline__ void widen_pairs(const Raw16 &u, float2 (&f)[kPairs])
 {
@@ -658,7 +661,7 @@ cudaError_t launch_norm(const NormArgs &a, cudaStream_t stream)
 {
     // Few rows: as many threads as there are units, for the shortest way through a row. Many: units of a thread that
     // keep a row's loads on their way at once and its warps few (bf16, 8-bit rows too: 16000 x 256 6.9, 8.3, 12.1 us
-    // with 1, 2, 4; 8000 x 2048 27.4, 24.6, 25.5; 16001 x 7168 290, 182, 152; fp32 with 4 does not fit the registers)
+    // with 1, 2, 4; 8000 x 2048 27.4, 24.6, 25.5; 16001 x 7168 290, 182, 153; fp32 with 4 does not fit the registers)
     const int units = a.H / kUnit;
     const int u = a.T <= 2 * a.sms ? (units > 1024 ? 2 : 1) : units <= 32 ? 1 : units <= 256 || a.dtype == EP_DTYPE_FP32 ? 2 : 4;
     const Shape s = shape_of(a.H, u);
