@@ -366,7 +366,7 @@ template <class T, int U> __global__ void __launch_bounds__(kBackThreads, 1) bac
     uint8_t *const ring = dyn + (128 - (smem_u32(dyn) & 127)) % 128;
     const int tid = threadIdx.x, warp = __shfl_sync(~0u, tid >> 5, 0), lane = tid & 31;
     const int team = warp / a.team, place = warp - team * a.team, units = a.H / kUnit;
-    const int groups = static_cast<int>((a.T + a.rows - 1LL) / a.rows), mine = (groups - 1 - static_cast<int>(blockIdx.x)) / static_cast<int>(gridDim.x) + 1;
+    const int groups = (a.T - 1) / a.rows + 1, mine = (groups - 1 - static_cast<int>(blockIdx.x)) / static_cast<int>(gridDim.x) + 1;
     const uint32_t row_bytes = a.H * sizeof(T);
     const bool has_dh = a.dx && a.dh;
     volatile int *const abort = &abort_;
