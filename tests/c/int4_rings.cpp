@@ -17,7 +17,7 @@ int main()
                         for (int nmax = 8; nmax <= 32 && nmax <= ((T + 7) & ~7); nmax += 8) {
                             // the lists' bytes as the kernel counts them; any shared memory that it may have besides its rings
                             const int fixed = (linear ? 0 : T * moe::kTileRows * 4) + E * 22 + P * 5 + 4;
-                            for (int own = 1024; own <= 3072; own += 512) {
+                            for (int own = 1024; own <= 2816; own += 256) {
                                 const moe::Int4Layout l = moe::int4_layout(linear, moe::kSmemMax - own, fixed, 2 * tile, nmax);
                                 seen.insert(std::make_tuple(l.stages, l.stages_b[0], l.stages_b[1]));
                             }
